@@ -348,6 +348,135 @@ selscan_status_t selscan_conv1d(const selscan_conv_shape_t* shape, const void* x
                                 const float* weight, const float* bias, int silu,
                                 void* out, void* stream);
 
+/*
+ * Gated delta rule: the recurrence next to the Mamba-2 scan whose heads erase
+ * along the current key before they write.  Tensors and state are laid out as
+ * for the Mamba-2 scan, with selscan_m2_shape_t's dstate N the size of a key
+ * and headdim P the size of a value.  For every batch element and head, with
+ * S [P, N] and S_{-1} = h0 (zero when NULL):
+ *
+ *     S_t = exp(g_t) (S_{t-1} - beta_t (S_{t-1} k_t) k_t^T) + beta_t v_t k_t^T
+ *     y_t = scale S_t q_t
+ *
+ *   q, k       [B, L, G, N]  in_dtype   shared by the heads of a group: head h
+ *                                       reads group h / (H / G); taken as
+ *                                       given (normalise k before the call)
+ *   v          [B, L, H, P]  in_dtype
+ *   g          [B, L, H]     fp32       log decay, normally <= 0; minus infinity
+ *                                       (or -200 and less) is a decay of zero
+ *   beta       [B, L, H]     fp32       write strength, normally in (0, 1)
+ *   lengths    [B]           int32      tokens of each batch element, device
+ *                                       memory, clamped to 0..L; NULL = L.
+ *                                       Tokens past the end are not read,
+ *                                       their y is zero, and last_state is
+ *                                       the state after the last token inside
+ *   h0         [B, H, P, N]  fp32       NULL = zero
+ *   y          [B, L, H, P]  out_dtype  (written)
+ *   last_state [B, H, P, N]  fp32       (written; NULL = skip); may not alias h0
+ *
+ * 1 <= N <= 128 (UNSUPPORTED above), any P and L.  Workspace as for the other
+ * entry points, sized by selscan_delta_workspace_bytes.  State, decays and
+ * sums are fp32.
+ */
+size_t selscan_delta_workspace_bytes(const selscan_m2_shape_t* shape);
+
+selscan_status_t selscan_delta_fwd(const selscan_m2_shape_t* shape,
+                                   const void* q, const void* k, const void* v,
+                                   const float* g, const float* beta, float scale,
+                                   const int32_t* lengths, const float* h0,
+                                   void* y, float* last_state, void* stream);
+
+/*
+ * Gated delta rule, one token: shape as for selscan_delta_fwd (seqlen and
+ * workspace ignored); q, k [B, G, N], v [B, H, P] in_dtype, g, beta [B, H]
+ * fp32, y [B, H, P] out_dtype.  state [B, H, P, N] fp32 is updated in place
+ * (16-byte aligned when N is a multiple of 4).
+ */
+selscan_status_t selscan_delta_step(const selscan_m2_shape_t* shape, float* state,
+                                    const void* q, const void* k, const void* v,
+                                    const float* g, const float* beta, float scale,
+                                    void* y, void* stream);
+
+/*
+ * Dropout whose mask is a function of (seed, offset, element index) and is
+ * never stored: element i is kept when word i % 4 of Philox4x32-10 (Salmon,
+ * Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2, 3", 2011)
+ * at counter (i / 4, offset) -- i / 4 in words 0 and 1, offset in words 2 and
+ * 3, low halves first -- and key `seed` is at least floor(p 2^32).  Kept
+ * elements are multiplied by 1 / (1 - p), the others are zero whatever they
+ * were.  The gradient is the same call on the output's gradient.
+ *   x, y  [n]  dtype   y may be x; n >= 1, 0 <= p <= 1
+ */
+typedef struct {
+    int64_t n;
+    int32_t dtype;
+    double p;
+    uint64_t seed, offset;
+} selscan_dropout_shape_t;
+
+selscan_status_t selscan_dropout(const selscan_dropout_shape_t* shape, const void* x, void* y, void* stream);
+
+/*
+ * Layer norm between two blocks, with the dropout and the residual sum that
+ * come before it:
+ *
+ *     s    = dropout(x) + residual            (element r * dim + d of the mask)
+ *     mean = sum_d s / dim;  rstd = 1 / sqrt(sum_d (s - mean)^2 / dim + eps)
+ *     y    = (s - mean) rstd weight + bias
+ *
+ *   x            [rows, dim]  in_dtype
+ *   residual     [rows, dim]  res_dtype   NULL = 0
+ *   weight, bias [dim]        fp32        NULL = 1 and 0
+ *   y            [rows, dim]  out_dtype   (written)
+ *   residual_out [rows, dim]  res_dtype   s (written; NULL = skip); may be residual
+ *   mean, rstd   [rows]       fp32        (written; NULL = skip)
+ * p, seed, offset as for selscan_dropout; p = 0 leaves x as it is.  The sums
+ * are fp32 over s before it is rounded to res_dtype.  rows, dim >= 1;
+ * workspace is used by the gradients only.
+ */
+typedef struct {
+    int64_t rows, dim;
+    int32_t in_dtype, res_dtype, out_dtype;
+    float eps;
+    double p;
+    uint64_t seed, offset;
+    void* workspace;
+    size_t workspace_bytes;
+} selscan_norm_shape_t;
+
+selscan_status_t selscan_layer_norm_fwd(const selscan_norm_shape_t* shape, const void* x, const void* residual,
+                                        const float* weight, const float* bias, void* y, void* residual_out,
+                                        float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace selscan_layer_norm_bwd needs (0 on a bad shape). */
+size_t selscan_layer_norm_bwd_workspace_bytes(const selscan_norm_shape_t* shape);
+
+/*
+ * Gradients of selscan_layer_norm_fwd from what it kept (s as written to
+ * residual_out -- or x itself when there was neither dropout nor residual --
+ * mean and rstd):
+ *
+ *     xhat = (s - mean) rstd;  w = dy weight
+ *     ds   = rstd (w - sum_d w / dim - xhat sum_d (w xhat) / dim) + dresidual_out
+ *     dx   = dropout's gradient of ds;  dresidual = ds
+ *     dweight = sum_r dy xhat;  dbias = sum_r dy
+ *
+ *   dy            [rows, dim]  out_dtype
+ *   s             [rows, dim]  res_dtype
+ *   weight        [dim]        fp32        NULL = 1
+ *   mean, rstd    [rows]       fp32
+ *   dresidual_out [rows, dim]  res_dtype   gradient of s from its other uses; NULL = 0
+ *   dx            [rows, dim]  in_dtype    (written; NULL = skip)
+ *   dresidual     [rows, dim]  res_dtype   (written; NULL = skip); may be dresidual_out
+ *   dweight, dbias [dim]       fp32        (written; NULL = skip)
+ * Sums over rows run in a fixed order: results are reproducible bit for bit.
+ * Workspace as for the other entry points.
+ */
+selscan_status_t selscan_layer_norm_bwd(const selscan_norm_shape_t* shape, const void* dy, const void* s,
+                                        const float* weight, const float* mean, const float* rstd,
+                                        const void* dresidual_out, void* dx, void* dresidual,
+                                        float* dweight, float* dbias, void* stream);
+
 /* Message for the last failed call on this thread ("" after a success).
  * The string stays valid until the next call on the same thread. */
 const char* selscan_last_error(void);

@@ -50,12 +50,29 @@ EXPORTED = ("selscan_fwd", "selscan_mamba2_fwd", "selscan_workspace_bytes", "sel
             "selscan_fwd_h0", "selscan_mamba2_fwd_h0", "selscan_step", "selscan_mamba2_step", "selscan_conv1d",
             "selscan_bwd", "selscan_bwd_workspace_bytes", "selscan_fwd_noalloc",
             "selscan_mamba2_bwd", "selscan_mamba2_bwd_workspace_bytes",
+            "selscan_delta_fwd", "selscan_delta_workspace_bytes", "selscan_delta_step",
+            "selscan_dropout", "selscan_layer_norm_fwd", "selscan_layer_norm_bwd",
+            "selscan_layer_norm_bwd_workspace_bytes",
             "selscan_last_error", "selscan_version", "selscan_timing_enable", "selscan_timing_collect")
 
 
 class ConvShape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("dim", ctypes.c_int64), ("seqlen", ctypes.c_int64),
                 ("width", ctypes.c_int64), ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class NormShape(ctypes.Structure):
+    """selscan_norm_shape_t."""
+    _fields_ = [("rows", ctypes.c_int64), ("dim", ctypes.c_int64), ("in_dtype", ctypes.c_int32),
+                ("res_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class DropoutShape(ctypes.Structure):
+    """selscan_dropout_shape_t."""
+    _fields_ = [("n", ctypes.c_int64), ("dtype", ctypes.c_int32), ("p", ctypes.c_double),
+                ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
 
 
 class KernelTime(ctypes.Structure):
@@ -103,6 +120,21 @@ def lib() -> ctypes.CDLL:
         L.selscan_workspace_bytes.restype = ctypes.c_size_t
         L.selscan_mamba2_workspace_bytes.argtypes = [ctypes.POINTER(M2Shape)]
         L.selscan_mamba2_workspace_bytes.restype = ctypes.c_size_t
+        f32 = ctypes.c_float
+        L.selscan_delta_workspace_bytes.argtypes = [ctypes.POINTER(M2Shape)]
+        L.selscan_delta_workspace_bytes.restype = ctypes.c_size_t
+        L.selscan_delta_fwd.argtypes = [ctypes.POINTER(M2Shape), vp, vp, vp, fp, fp, f32, vp, fp, vp, fp, vp]
+        L.selscan_delta_fwd.restype = i32
+        L.selscan_delta_step.argtypes = [ctypes.POINTER(M2Shape), fp, vp, vp, vp, fp, fp, f32, vp, vp]
+        L.selscan_delta_step.restype = i32
+        L.selscan_dropout.argtypes = [ctypes.POINTER(DropoutShape), vp, vp, vp]
+        L.selscan_dropout.restype = i32
+        L.selscan_layer_norm_fwd.argtypes = [ctypes.POINTER(NormShape), vp, vp, fp, fp, vp, vp, fp, fp, vp]
+        L.selscan_layer_norm_fwd.restype = i32
+        L.selscan_layer_norm_bwd.argtypes = [ctypes.POINTER(NormShape), vp, vp, fp, fp, fp, vp, vp, vp, fp, fp, vp]
+        L.selscan_layer_norm_bwd.restype = i32
+        L.selscan_layer_norm_bwd_workspace_bytes.argtypes = [ctypes.POINTER(NormShape)]
+        L.selscan_layer_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.selscan_last_error.restype = ctypes.c_char_p
         L.selscan_version.restype = ctypes.c_char_p
         L.selscan_timing_enable.argtypes = [i32]
@@ -498,6 +530,182 @@ def conv1d(x, weight, bias=None, silu=True, out=None, out_dtype=None):
     return out
 
 
+def _ws_arg(workspace, need, device):
+    """(pointer, bytes, keep-alive) of a caller's workspace or of one from
+    torch's allocator, which is ordered on the current stream."""
+    if workspace is None:
+        if need == 0:
+            return None, 0, None
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def delta_workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, in_dtype=BF16, out_dtype=None) -> int:
+    s = M2Shape(batch, seqlen, nheads, headdim, ngroups, dstate, in_dtype, in_dtype if out_dtype is None else out_dtype,
+                None, 0)
+    return int(lib().selscan_delta_workspace_bytes(ctypes.byref(s)))
+
+
+def delta_fwd(q, k, v, g, beta, scale=None, lengths=None, h0=None, out=None, last_state=None, return_last_state=True,
+              workspace=None, out_dtype=None):
+    """Gated delta rule over a sequence.
+
+    q, k: [batch, L, G, N]; v: [batch, L, H, P] (float32 or bfloat16, one
+    dtype), H a multiple of G; g (log decay) and beta (write strength):
+    [batch, L, H] float32; scale multiplies the read-out (None: N ** -0.5).
+    lengths: [batch] int32 on the GPU, tokens of each row (None: all L);
+    h0: [batch, H, P, N] float32 initial state (None: zero).
+    Returns (y [batch, L, H, P] float32 unless out_dtype says otherwise,
+    last_state [batch, H, P, N] float32 or None).
+    """
+    torch = _torch()
+    f32 = torch.float32
+    dev, dt = q.device, q.dtype
+    batch, L, G, N = q.shape
+    H, P = v.shape[2], v.shape[3]
+    odt = (out.dtype if out is not None else f32) if out_dtype is None else out_dtype
+    if dev.type != "cuda":
+        raise ValueError("selscan.delta_fwd needs tensors on a GPU device")
+    if out is None:
+        out = torch.empty((batch, L, H, P), dtype=odt, device=dev)
+    if last_state is None and return_last_state:
+        last_state = torch.empty((batch, H, P, N), dtype=f32, device=dev)
+    s = M2Shape(batch, L, H, P, G, N, _dtype_code(q), _dtype_code(out), None, 0)
+    args = (_ptr(q, "q", (batch, L, G, N), dt, dev), _ptr(k, "k", (batch, L, G, N), dt, dev),
+            _ptr(v, "v", (batch, L, H, P), dt, dev), _ptr(g, "g", (batch, L, H), f32, dev),
+            _ptr(beta, "beta", (batch, L, H), f32, dev), N ** -0.5 if scale is None else float(scale),
+            _ptr(lengths, "lengths", (batch,), torch.int32, dev), _ptr(h0, "h0", (batch, H, P, N), f32, dev),
+            _ptr(out, "out", (batch, L, H, P), odt, dev), _ptr(last_state, "last_state", (batch, H, P, N), f32, dev),
+            _stream_handle(dev))
+    L_ = lib()
+    s.workspace, s.workspace_bytes, ws = _ws_arg(workspace, L_.selscan_delta_workspace_bytes(ctypes.byref(s)), dev)
+    _check(L_.selscan_delta_fwd(ctypes.byref(s), *args))
+    return out, last_state
+
+
+def _delta_step_args(state, q, k, v, g, beta, scale, out, out_dtype):
+    torch = _torch()
+    f32 = torch.float32
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("selscan.delta_step needs tensors on a GPU device")
+    batch, G, N = q.shape
+    H, P = v.shape[1], v.shape[2]
+    odt = (out.dtype if out is not None else f32) if out_dtype is None else out_dtype
+    if out is None:
+        out = torch.empty((batch, H, P), dtype=odt, device=dev)
+    s = M2Shape(batch, 1, H, P, G, N, _dtype_code(q), _dtype_code(out), None, 0)
+    return s, (_ptr(state, "state", (batch, H, P, N), f32, dev), _ptr(q, "q", (batch, G, N), dt, dev),
+               _ptr(k, "k", (batch, G, N), dt, dev), _ptr(v, "v", (batch, H, P), dt, dev),
+               _ptr(g, "g", (batch, H), f32, dev), _ptr(beta, "beta", (batch, H), f32, dev),
+               N ** -0.5 if scale is None else float(scale), _ptr(out, "out", (batch, H, P), odt, dev),
+               _stream_handle(dev)), out
+
+
+def delta_step(state, q, k, v, g, beta, scale=None, out=None, out_dtype=None):
+    """One token of the gated delta rule (decoding).  state [batch, H, P, N]
+    float32 is updated in place; q, k [batch, G, N]; v [batch, H, P] (float32
+    or bfloat16); g, beta [batch, H] float32.  Returns y [batch, H, P]
+    (float32 unless out_dtype or out says otherwise)."""
+    s, args, out = _delta_step_args(state, q, k, v, g, beta, scale, out, out_dtype)
+    _check(lib().selscan_delta_step(ctypes.byref(s), *args))
+    return out
+
+
+def bind_delta_step(state, q, k, v, g, beta, scale=None, out=None, out_dtype=None):
+    """selscan_delta_step with its arguments checked and marshalled once:
+    returns (call, y); see bind_step."""
+    s, args, out = _delta_step_args(state, q, k, v, g, beta, scale, out, out_dtype)
+    return _BoundCall(lib().selscan_delta_step, s, args), out
+
+
+def dropout(x, p, seed, offset=0, out=None):
+    """Dropout with a mask that is a function of (seed, offset, element index)
+    and is never stored: kept elements times 1 / (1 - p), the others zero.
+    The gradient is the same call on the output's gradient.  x: any shape,
+    float32 or bfloat16; out: the result (may be x).  seed, offset: integers
+    in [0, 2^64)."""
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("selscan.dropout needs tensors on a GPU device")
+    if out is None:
+        out = _torch().empty_like(x)
+    s = DropoutShape(x.numel(), _dtype_code(x), p, seed, offset)
+    _check(lib().selscan_dropout(ctypes.byref(s), _ptr(x, "x"), _ptr(out, "out", x.shape, x.dtype, dev),
+                                 _stream_handle(dev)))
+    return out
+
+
+def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, p=0.0, seed=0, offset=0, out=None,
+                   out_dtype=None, res_dtype=None):
+    """Layer norm of s = dropout(x) + residual over the last dimension.
+
+    x: [..., dim] float32 or bfloat16; residual: the same shape, float32 or
+    bfloat16, or None; weight, bias: [dim] float32 or None (1 and 0); p, seed,
+    offset: the dropout of x (see dropout).
+    Returns (y, s, mean, rstd): y in x's dtype unless out_dtype or out says
+    otherwise; s in residual's dtype (x's, or res_dtype, without one; x itself
+    when there is neither dropout nor residual); mean and rstd [...] float32.
+    """
+    torch = _torch()
+    f32 = torch.float32
+    dev, shape = x.device, x.shape
+    if dev.type != "cuda":
+        raise ValueError("selscan.layer_norm_fwd needs tensors on a GPU device")
+    dim = shape[-1]
+    odt = (out.dtype if out is not None else x.dtype) if out_dtype is None else out_dtype
+    rdt = residual.dtype if residual is not None else (x.dtype if res_dtype is None else res_dtype)
+    if out is None:
+        out = torch.empty(shape, dtype=odt, device=dev)
+    s = x if residual is None and p == 0.0 and rdt == x.dtype else torch.empty(shape, dtype=rdt, device=dev)
+    mean = torch.empty(shape[:-1], dtype=f32, device=dev)
+    rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
+    sh = NormShape(x.numel() // max(dim, 1), dim, _dtype_code(x), _dtype_code(s), _dtype_code(out), eps, p, seed,
+                   offset, None, 0)
+    _check(lib().selscan_layer_norm_fwd(
+        ctypes.byref(sh), _ptr(x, "x"), _ptr(residual, "residual", shape, rdt, dev),
+        _ptr(weight, "weight", (dim,), f32, dev), _ptr(bias, "bias", (dim,), f32, dev),
+        _ptr(out, "out", shape, odt, dev), None if s is x else s.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+        _stream_handle(dev)))
+    return out, s, mean, rstd
+
+
+def layer_norm_bwd(dy, s, weight=None, mean=None, rstd=None, dresidual=None, p=0.0, seed=0, offset=0, x_dtype=None,
+                   workspace=None):
+    """Gradients of layer_norm_fwd from the s, mean and rstd that it returned.
+
+    dy: [..., dim] gradient of y; dresidual: gradient of s from its other
+    uses, in s's dtype, or None; p, seed, offset as in the forward call.
+    Returns a dict: dx in x_dtype (None: s's dtype), dresidual (the gradient
+    of residual; the same tensor as dx when there is no dropout and the dtypes
+    agree) in s's dtype, dweight and dbias [dim] float32.
+    """
+    torch = _torch()
+    f32 = torch.float32
+    dev, shape = dy.device, dy.shape
+    if dev.type != "cuda":
+        raise ValueError("selscan.layer_norm_bwd needs tensors on a GPU device")
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd are required")
+    dim = shape[-1]
+    xdt = s.dtype if x_dtype is None else x_dtype
+    ds = torch.empty(shape, dtype=s.dtype, device=dev)
+    dx = ds if p == 0.0 and xdt == s.dtype else torch.empty(shape, dtype=xdt, device=dev)
+    dw = torch.empty((dim,), dtype=f32, device=dev)
+    db = torch.empty((dim,), dtype=f32, device=dev)
+    sh = NormShape(dy.numel() // max(dim, 1), dim, _dtype_code(dx), _dtype_code(s), _dtype_code(dy), 0.0, p, seed,
+                   offset, None, 0)
+    L_ = lib()
+    sh.workspace, sh.workspace_bytes, ws = _ws_arg(
+        workspace, L_.selscan_layer_norm_bwd_workspace_bytes(ctypes.byref(sh)), dev)
+    _check(L_.selscan_layer_norm_bwd(
+        ctypes.byref(sh), _ptr(dy, "dy"), _ptr(s, "s", shape, None, dev), _ptr(weight, "weight", (dim,), f32, dev),
+        _ptr(mean, "mean", shape[:-1], f32, dev), _ptr(rstd, "rstd", shape[:-1], f32, dev),
+        _ptr(dresidual, "dresidual", shape, s.dtype, dev), None if dx is ds else dx.data_ptr(), ds.data_ptr(),
+        dw.data_ptr(), db.data_ptr(), _stream_handle(dev)))
+    return {"dx": dx, "dresidual": ds, "dweight": dw, "dbias": db}
+
+
 def timing_enable(on: bool) -> None:
     """Bracket every later kernel launch with HIP events on its own stream."""
     _check(lib().selscan_timing_enable(int(bool(on))))
@@ -518,5 +726,6 @@ def timing_collect() -> dict:
     return res
 
 
-__all__ = ["bind_step", "bind_mamba2_step", "bwd", "bwd_workspace_bytes", "conv1d", "ConvShape", "step", "mamba2_step", "timing_enable", "timing_collect", "KernelTime", "fwd", "mamba2_fwd", "workspace_bytes", "mamba2_workspace_bytes", "version", "last_error", "lib",
+__all__ = ["delta_fwd", "delta_step", "bind_delta_step", "delta_workspace_bytes", "dropout", "layer_norm_fwd",
+           "layer_norm_bwd", "NormShape", "DropoutShape", "bind_step", "bind_mamba2_step", "bwd", "bwd_workspace_bytes", "conv1d", "ConvShape", "step", "mamba2_step", "timing_enable", "timing_collect", "KernelTime", "fwd", "mamba2_fwd", "workspace_bytes", "mamba2_workspace_bytes", "version", "last_error", "lib",
            "SelscanError", "Shape", "M2Shape", "m1_shape", "EXPORTED", "LIB_PATH"]

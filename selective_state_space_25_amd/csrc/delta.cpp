@@ -1,0 +1,107 @@
+// delta.cpp -- host side of the gated delta rule: argument checks, plans and
+// workspace behind the entry points declared in selscan.h.
+#include <hip/hip_runtime.h>
+
+#include <cstdio>
+#include <string>
+
+#include "host.hpp"
+#include "kernels.hpp"
+#include "selscan.h"
+
+using namespace selscan::host;
+using selscan::set_error;
+
+namespace {
+
+selscan_status_t check_shape(const selscan_m2_shape_t* s) {
+    if (!s) return set_error(SELSCAN_ERR_INVALID_ARG, "shape is NULL");
+    if (s->batch < 1 || s->seqlen < 1 || s->nheads < 1 || s->headdim < 1 || s->ngroups < 1 || s->dstate < 1)
+        return set_error(SELSCAN_ERR_INVALID_ARG, "batch, seqlen, nheads, headdim, ngroups, dstate must be >= 1");
+    if (s->nheads % s->ngroups != 0)
+        return set_error(SELSCAN_ERR_INVALID_ARG, "nheads must be a multiple of ngroups");
+    if (s->dstate > 128) return set_error(SELSCAN_ERR_UNSUPPORTED, "the gated delta rule supports dstate <= 128");
+    if ((s->in_dtype != SELSCAN_F32 && s->in_dtype != SELSCAN_BF16) ||
+        (s->out_dtype != SELSCAN_F32 && s->out_dtype != SELSCAN_BF16))
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "dtypes must be SELSCAN_F32 or SELSCAN_BF16");
+    if (mul_checked({s->batch, s->seqlen, s->nheads, s->headdim, 4}) < 0 ||
+        mul_checked({s->batch, s->seqlen, s->ngroups, s->dstate, 4}) < 0 ||
+        mul_checked({s->batch, s->nheads, s->headdim, s->dstate, 4}) < 0)
+        return set_error(SELSCAN_ERR_INVALID_ARG, "tensor sizes overflow 64-bit byte counts");
+    // 16 rows of a state per workgroup of the token-by-token kernel
+    if (mul_checked({s->batch, s->nheads, s->headdim}) / 16 >= 0x7fffffff)
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "too many (batch, head, channel) rows for one launch");
+    return SELSCAN_OK;
+}
+
+bool vec4(const selscan_m2_shape_t* s, const void* q, const void* k) {
+    const uintptr_t m = s->in_dtype == SELSCAN_BF16 ? 7 : 15;
+    return s->dstate % 4 == 0 && (reinterpret_cast<uintptr_t>(q) & m) == 0 && (reinterpret_cast<uintptr_t>(k) & m) == 0;
+}
+
+selscan_status_t launched(hipError_t e) {
+    if (e != hipSuccess)
+        return set_error(SELSCAN_ERR_LAUNCH, std::string("kernel launch failed: ") + hipGetErrorString(e));
+    return set_error(SELSCAN_OK, "");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t selscan_delta_workspace_bytes(const selscan_m2_shape_t* s) {
+    if (check_shape(s) != SELSCAN_OK) return 0;
+    return 0;
+}
+
+selscan_status_t selscan_delta_fwd(const selscan_m2_shape_t* s, const void* q, const void* k, const void* v,
+                                   const float* g, const float* beta, float scale, const int32_t* lengths,
+                                   const float* h0, void* y, float* last_state, void* stream) {
+    try {
+        selscan_status_t st = check_shape(s);
+        if (st != SELSCAN_OK) return st;
+        if (!q || !k || !v || !g || !beta || !y)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "q, k, v, g, beta and y must be non-NULL");
+        if (h0 && h0 == last_state) return set_error(SELSCAN_ERR_INVALID_ARG, "h0 and last_state must not alias");
+        st = device_check();
+        if (st != SELSCAN_OK) return st;
+        selscan::DeltaArgs a{};
+        a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths; a.h0 = h0; a.y = y; a.last = last_state;
+        a.batch = s->batch; a.L = s->seqlen; a.H = s->nheads; a.P = s->headdim; a.G = s->ngroups;
+        a.N = (int)s->dstate; a.scale = scale;
+        a.vec = vec4(s, q, k) && aligned16(h0) && aligned16(last_state);
+        return launched(selscan::launch_delta_rec(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16,
+                                                  reinterpret_cast<hipStream_t>(stream)));
+    } catch (...) {
+        return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
+    }
+}
+
+selscan_status_t selscan_delta_step(const selscan_m2_shape_t* s, float* state, const void* q, const void* k,
+                                    const void* v, const float* g, const float* beta, float scale, void* y,
+                                    void* stream) {
+    try {
+        if (!s) return set_error(SELSCAN_ERR_INVALID_ARG, "shape is NULL");
+        selscan_m2_shape_t one = *s;
+        one.seqlen = 1;
+        selscan_status_t st = check_shape(&one);
+        if (st != SELSCAN_OK) return st;
+        if (!state || !q || !k || !v || !g || !beta || !y)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "state, q, k, v, g, beta and y must be non-NULL");
+        if (s->dstate % 4 == 0 && !aligned16(state))
+            return set_error(SELSCAN_ERR_INVALID_ARG, "state must be 16-byte aligned");
+        st = device_check();
+        if (st != SELSCAN_OK) return st;
+        selscan::DeltaArgs a{};
+        a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.h0 = state; a.y = y; a.last = state;
+        a.batch = s->batch; a.L = 1; a.H = s->nheads; a.P = s->headdim; a.G = s->ngroups;
+        a.N = (int)s->dstate; a.scale = scale;
+        a.vec = vec4(s, q, k);
+        return launched(selscan::launch_delta_rec(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16,
+                                                  reinterpret_cast<hipStream_t>(stream)));
+    } catch (...) {
+        return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
+    }
+}
+
+}  // extern "C"

@@ -199,4 +199,62 @@ bool m2_ssd_supported(const M2Args& a, int in_bf16);
 // ws: 1 = warp-specialised kernel (state waves and chunk waves), 0 = every wave in every phase
 hipError_t launch_m2_ssd(const M2Args& a, int out_bf16, int ws, hipStream_t stream);
 
+// Gated delta rule (q, k [batch, L, G, N]; v, y [batch, L, H, P]; g, beta
+// [batch, L, H]; states [batch, H, P, N]).
+struct DeltaArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const float* g;
+    const float* beta;
+    const int32_t* lengths;   // tokens of each batch element, or NULL
+    const float* h0;          // NULL = zero; the one-token update: last (in place)
+    void* y;
+    float* last;
+    int64_t batch, L, H, P, G;
+    int N;
+    float scale;
+    int vec;                  // rows of q, k and the states allow vector access
+};
+hipError_t launch_delta_rec(const DeltaArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
+
+// Layer norm with dropout and residual sum in front.
+struct NormArgs {
+    const void* x;            // forward: x; gradients: dy
+    const void* res;          // forward: residual; gradients: s
+    const float* weight;
+    const float* bias;
+    const float* mean_in;     // gradients
+    const float* rstd_in;
+    const void* dres_in;
+    void* y;                  // forward: y; gradients: dx
+    void* res_out;            // forward: s; gradients: dresidual
+    float* mean;
+    float* rstd;
+    float* dweight;
+    float* dbias;
+    float* part;              // gradients: [blocks, 2, dim] partial sums of dweight, dbias
+    int64_t rows, dim;
+    int blocks;
+    float eps, inv_dim;
+    uint64_t seed, offset;
+    uint64_t keep_from;       // a word below this drops its element (2^32: all are dropped)
+    float keep_scale;
+    int drop;                 // dropout is on
+    int vec;                  // rows start on 16-byte boundaries, dim % 8 == 0
+};
+int norm_bwd_blocks(int64_t rows, int64_t dim);
+hipError_t launch_norm_fwd(const NormArgs& a, int in_bf16, int res_bf16, int out_bf16, hipStream_t stream);
+hipError_t launch_norm_bwd(const NormArgs& a, int in_bf16, int res_bf16, int out_bf16, hipStream_t stream);
+
+struct DropArgs {
+    const void* x;
+    void* y;
+    int64_t n;
+    uint64_t seed, offset, keep_from;
+    float keep_scale;
+    int vec;                  // x and y on 16-byte boundaries
+};
+hipError_t launch_dropout(const DropArgs& a, int bf16, hipStream_t stream);
+
 }  // namespace selscan

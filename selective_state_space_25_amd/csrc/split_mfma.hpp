@@ -1,0 +1,131 @@
+// split_mfma.hpp -- fp32-grade matrix products on the bf16 matrix cores.
+//
+// An fp32 value is held as the sum of up to three bfloat16 values, each the
+// rounding of what the ones before it leave (8 significant bits a plane, 24
+// in all), so a product of two such sums is a handful of bf16 MFMAs that
+// accumulate in fp32.  Keeping the plane pairs (a, b) with a + b < 3 leaves
+// out terms near 2^-25 of the product: the result is as exact as an fp32
+// product, at 6 (both sides fp32) or 3 (one side bf16, which is one plane)
+// of the 16 MFMAs that the same product takes at the fp32 rate.  bf16 planes
+// keep fp32's range; an infinity leaves NaN in its lower planes.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "device_math.hpp"
+
+namespace selscan {
+namespace smm {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
+
+// v_mfma_f32_16x16x32_bf16.  Lane l = 16 g + i: operand A holds row i,
+// operand B column i, k = 8 g .. 8 g + 7 of either; C holds rows
+// 4 g .. 4 g + 3 of column i.
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// c += A B over one k-step of 32, the sides split in NA and NB planes, plane
+// pairs with a + b < LIM, small terms first.
+template <int LIM, int NA, int NB>
+__device__ __forceinline__ f32x4 mm(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4 c) {
+#pragma unroll
+    for (int s = LIM - 1; s >= 0; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB) c = mfma(a[i], b[s - i], c);
+    return c;
+}
+
+// One value into element e of NP planes.
+template <int NP>
+__device__ __forceinline__ void split(float v, bf16x8 (&p)[NP], int e) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        const __bf16 h = (__bf16)v;
+        p[i][e] = h;
+        if (i + 1 < NP) v -= (float)h;
+    }
+}
+
+// Two C tiles (rows r0 .. r0 + 15 and r0 + 16 .. r0 + 31 of one column
+// block) as the B operand of a product over those 32 rows, k in the order in
+// which the lanes hold them: lane group g has rows r0 + 4 g + q, then
+// r0 + 16 + 4 g + q.  The A operand has to be read in that order (kperm).
+template <int NP>
+__device__ __forceinline__ void split_tiles(f32x4 t0, f32x4 t1, bf16x8 (&p)[NP]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        split<NP>(t0[q], p, q);
+        split<NP>(t1[q], p, 4 + q);
+    }
+}
+
+// Position of column n in a row whose 4-element pieces are permuted inside
+// each group of 32 so that one 16-byte read gives a lane group the k order of
+// split_tiles: pieces 0 .. 7 at positions 0, 2, 4, 6, 1, 3, 5, 7.
+__device__ __forceinline__ int kperm(int n) {
+    const int pc = (n & 31) >> 2;
+    return (n & ~31) + 4 * (pc < 4 ? 2 * pc : 2 * pc - 7) + (n & 3);
+}
+
+__device__ __forceinline__ bf16x8 ld8(const uint16_t* p) {
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(p));
+}
+
+__device__ __forceinline__ bf16x8 cat(s16x4 a, s16x4 b) {
+    const s16x8 r = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_bit_cast(bf16x8, r);
+}
+
+// Transposing LDS load: within 16 lanes, lane a passes the address of 4
+// consecutive elements of row r0 + a / 4 (columns c0 + 4 (a % 4) ..); lane i
+// receives rows r0 .. r0 + 3 of column c0 + i.
+__device__ __forceinline__ s16x4 ld_tr(const uint16_t* p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p));
+}
+
+// Operand with k running down the rows of m (row stride rs), columns
+// c0 .. c0 + 15: k = rows r0 .. r0 + 31 in split_tiles' order.  PERM: m's
+// columns are stored through kperm.
+template <bool PERM>
+__device__ __forceinline__ bf16x8 ld_down(const uint16_t* m, int rs, int r0, int c0, int lane) {
+    const int g = lane >> 4, a = lane & 15;
+    const int c = c0 + 4 * (a & 3);
+    const uint16_t* p = m + (r0 + 4 * g + (a >> 2)) * rs + (PERM ? kperm(c) : c);
+    return cat(ld_tr(p), ld_tr(p + 16 * rs));
+}
+
+// As ld_down with k in natural order (rows r0 + 8 g .. + 7 for lane group g).
+template <bool PERM>
+__device__ __forceinline__ bf16x8 ld_down8(const uint16_t* m, int rs, int r0, int c0, int lane) {
+    const int g = lane >> 4, a = lane & 15;
+    const int c = c0 + 4 * (a & 3);
+    const uint16_t* p = m + (r0 + 8 * g + (a >> 2)) * rs + (PERM ? kperm(c) : c);
+    return cat(ld_tr(p), ld_tr(p + 4 * rs));
+}
+
+// Four consecutive values into NP planes of 4 bf16 each.
+template <int NP>
+__device__ __forceinline__ void split4(const float (&v)[4], uint2 (&p)[NP]) {
+    float r[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+        p[i] = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
+        if (i + 1 < NP) {
+            r[0] -= bf16lo(p[i].x);
+            r[1] -= bf16hi(p[i].x);
+            r[2] -= bf16lo(p[i].y);
+            r[3] -= bf16hi(p[i].y);
+        }
+    }
+}
+
+}  // namespace smm
+}  // namespace selscan

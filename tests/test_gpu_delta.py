@@ -1,0 +1,200 @@
+"""The gated delta rule on the GPU against the fp64 oracle."""
+import numpy as np
+import pytest
+import torch
+
+import selective_state_space_25_amd as ss
+from oracle import block_ops as ref
+from parity import check_close, host
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+F32, BF16 = torch.float32, torch.bfloat16
+
+# Products and sums are fp32-grade: 2^-22 of the sum of magnitudes, which for
+# up to ~1000 random-signed terms is ~32 times the result, over about six
+# chained stages: 32 x 6 x 2^-22 ~ 5e-5 of the output's scale.
+TOL = 5e-5
+
+
+def close(got, want, what, tol=TOL):
+    want = np.asarray(want)
+    rms = float(np.sqrt(np.mean(np.square(want[np.isfinite(want)])))) if want.size else 0.0
+    half = 2.0 ** -8 if got.dtype == BF16 else 0.0
+    check_close(host(got).double().numpy(), want, (tol * max(rms, 1e-6), tol + half), what)
+
+
+def inputs(B, L, H, G, P, N, dtype, seed, h0=False, strong=False):
+    g = torch.Generator().manual_seed(seed)
+    rnd = lambda *s: torch.randn(s, generator=g)
+    unit = lambda x: x / x.norm(dim=-1, keepdim=True)
+    i = dict(q=unit(rnd(B, L, G, N)).to(dtype), k=unit(rnd(B, L, G, N)).to(dtype), v=rnd(B, L, H, P).to(dtype),
+             g=-torch.rand((B, L, H), generator=g) * (20.0 if strong else 0.3), beta=torch.sigmoid(rnd(B, L, H)))
+    if h0:
+        i["h0"] = rnd(B, H, P, N)
+    return {n: x.to(DEV) for n, x in i.items()}
+
+
+SHAPES = [  # B, L, H, G, P, N
+    (1, 1, 1, 1, 1, 1), (2, 1, 2, 1, 64, 128), (1, 2, 2, 2, 16, 16), (1, 63, 1, 1, 64, 64), (1, 64, 2, 1, 64, 128),
+    (2, 65, 2, 2, 33, 27), (1, 130, 3, 1, 80, 96), (1, 200, 2, 2, 128, 128), (2, 129, 4, 2, 48, 40),
+    (1, 257, 2, 1, 130, 100), (1, 77, 6, 3, 7, 3)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("h0", [False, True])
+def test_fwd_matches_oracle(gpu, shape, dtype, h0):
+    i = inputs(*shape, dtype, seed=sum(shape), h0=h0)
+    y, last = ss.delta_fwd(**i)
+    yb, none = ss.delta_fwd(**i, out_dtype=BF16, return_last_state=False)
+    torch.cuda.synchronize()
+    yr, lr = ref.delta(**i)
+    close(y, yr, "y")
+    close(last, lr, "last_state")
+    close(yb, yr, "bf16 y")
+    assert none is None
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_fwd_lengths(gpu, dtype):
+    """Rows of every length, none and past-the-end among them; what lies past
+    a row's end is never read (NaN there changes nothing)."""
+    L, lengths = 150, [150, 0, 1, 64, 65, 149, 999, -3]
+    i = inputs(8, L, 2, 1, 40, 48, dtype, seed=5, h0=True)
+    n = torch.tensor(lengths, dtype=torch.int32, device=DEV)
+    for b, m in enumerate(lengths):
+        for name in ("q", "k", "v", "g", "beta"):
+            i[name][b, max(m, 0):] = float("nan")
+    y, last = ss.delta_fwd(**i, lengths=n)
+    torch.cuda.synchronize()
+    yr, lr = ref.delta(**i, lengths=lengths)
+    close(y, yr, "y")
+    close(last, lr, "last_state")
+    assert torch.equal(host(last[1]), host(i["h0"][1])) and torch.equal(host(last[7]), host(i["h0"][7]))
+    for b, m in enumerate(lengths):
+        assert not host(y[b, min(max(m, 0), L):]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(F32).min, -1e4, -200.0])
+def test_fwd_decay_of_zero(gpu, dtype, low):
+    """A log decay of minus infinity, the type's lowest value or any large
+    negative number resets the state; strong decays around it lose nothing."""
+    i = inputs(2, 140, 2, 2, 32, 64, dtype, seed=6, h0=True, strong=True)
+    i["g"][0, 70] = low
+    i["g"][1, [0, 63, 64, 100, 101]] = low
+    y, last = ss.delta_fwd(**i)
+    torch.cuda.synchronize()
+    yr, lr = ref.delta(**i)
+    close(y, yr, "y")
+    close(last, lr, "last_state")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_fwd_hard_keys(gpu, dtype):
+    """Equal keys, write strengths 0, 1 and 2 and no decay: the chunk's
+    triangular system is as far from the identity as it gets."""
+    i = inputs(1, 192, 1, 1, 32, 64, dtype, seed=7)
+    i["k"][:] = i["k"][:, :1]
+    i["q"][:] = i["k"]
+    i["g"].zero_()
+    i["beta"][:, :64] = 1.0
+    i["beta"][:, 64:128] = 2.0
+    i["beta"][:, 128:] = 0.0
+    # with beta 2 the state's component along the key flips each token and the
+    # rounding of |k|^2 (bf16 keys: up to 2^-8 off 1) grows with it: the fp64
+    # recurrence does the same on the same inputs
+    y, last = ss.delta_fwd(**i)
+    torch.cuda.synchronize()
+    yr, lr = ref.delta(**i)
+    close(y, yr, "y")
+    close(last, lr, "last_state")
+
+
+def test_fwd_unaligned_and_split(gpu):
+    """Tensors off 16-byte boundaries; a sequence in two calls equals one."""
+    i = inputs(2, 100, 2, 1, 64, 128, BF16, seed=8)
+
+    def shifted(t):
+        buf = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)
+        v = buf[1:].view(t.shape)
+        v.copy_(t)
+        return v
+
+    y, last = ss.delta_fwd(**i)
+    ys, ls = ss.delta_fwd(**{n: shifted(x) for n, x in i.items()})
+    close(ys, host(y).double().numpy(), "unaligned y")
+    close(ls, host(last).double().numpy(), "unaligned last_state")
+    a = {n: x[:, :37].contiguous() for n, x in i.items()}
+    b = {n: x[:, 37:].contiguous() for n, x in i.items()}
+    _, l1 = ss.delta_fwd(**a)
+    y2, l2 = ss.delta_fwd(**b, h0=l1)
+    close(y2, host(y[:, 37:]).double().numpy(), "second part")
+    close(l2, host(last).double().numpy(), "state after the second part")
+
+
+def test_fwd_scale_stream_and_reproducible(gpu):
+    i = inputs(1, 300, 2, 2, 64, 64, BF16, seed=9)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        y, last = ss.delta_fwd(**i, scale=0.75)
+    torch.cuda.synchronize()
+    yr, _ = ref.delta(**i, scale=0.75)
+    close(y, yr, "y")
+    y2, last2 = ss.delta_fwd(**i, scale=0.75)
+    assert torch.equal(y, y2) and torch.equal(last, last2)
+
+
+@pytest.mark.parametrize("shape", [(1, 1, 1, 1, 1), (3, 2, 1, 64, 128), (2, 4, 2, 33, 27), (5, 3, 3, 16, 16),
+                                   (2, 6, 3, 40, 100), (1, 2, 2, 128, 64), (70, 2, 1, 8, 32)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_step_matches_oracle(gpu, shape, dtype):
+    """Tokens one at a time, in place; the rows after the state are not written."""
+    B, H, G, P, N = shape
+    T = 5
+    i = inputs(B, T, H, G, P, N, dtype, seed=sum(shape), h0=True)
+    h0 = i.pop("h0")
+    buf = torch.full((h0.numel() + 512,), 7.0, device=DEV)
+    state = buf[:h0.numel()].view(h0.shape)
+    state.copy_(h0)
+    ys = [ss.delta_step(state, **{n: x[:, t].contiguous() for n, x in i.items()}) for t in range(T)]
+    torch.cuda.synchronize()
+    yr, lr = ref.delta(**i, h0=h0)
+    close(torch.stack(ys, 1), yr, "y over the steps")
+    close(state, lr, "state after the steps")
+    assert torch.equal(host(buf[h0.numel():]), torch.full((512,), 7.0))
+
+
+def test_bound_step_continues_a_prompt(gpu):
+    T, Lp = 6, 90
+    i = inputs(2, Lp + T, 4, 2, 64, 128, BF16, seed=11)
+    _, state = ss.delta_fwd(**{n: x[:, :Lp].contiguous() for n, x in i.items()})
+    cur = {n: x[:, Lp].clone() for n, x in i.items()}
+    call, y = ss.bind_delta_step(state, **cur)
+    ys = []
+    for t in range(T):
+        for n in cur:
+            cur[n].copy_(i[n][:, Lp + t])
+        call()
+        ys.append(y.clone())
+    torch.cuda.synchronize()
+    yr, lr = ref.delta(**i)
+    close(torch.stack(ys, 1), yr[:, Lp:], "decoded y")
+    close(state, lr, "state")
+
+
+def test_python_refusals(gpu):
+    i = inputs(1, 8, 2, 1, 16, 16, BF16, seed=12)
+    with pytest.raises(TypeError):
+        ss.delta_fwd(**{**i, "g": i["g"].bfloat16()})
+    with pytest.raises(ValueError):
+        ss.delta_fwd(**{**i, "k": i["k"][..., :8]})
+    with pytest.raises(ValueError):
+        ss.delta_fwd(**{**i, "v": i["v"].transpose(1, 2)})
+    with pytest.raises(TypeError):
+        ss.delta_fwd(**i, lengths=torch.tensor([8], device=DEV))
+    with pytest.raises(ValueError):
+        ss.delta_fwd(**{n: x.cpu() for n, x in i.items()})
