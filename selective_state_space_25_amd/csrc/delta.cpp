@@ -28,15 +28,24 @@ selscan_status_t check_shape(const selscan_m2_shape_t* s) {
         mul_checked({s->batch, s->seqlen, s->ngroups, s->dstate, 4}) < 0 ||
         mul_checked({s->batch, s->nheads, s->headdim, s->dstate, 4}) < 0)
         return set_error(SELSCAN_ERR_INVALID_ARG, "tensor sizes overflow 64-bit byte counts");
-    // 16 rows of a state per workgroup of the token-by-token kernel
-    if (mul_checked({s->batch, s->nheads, s->headdim}) / 16 >= 0x7fffffff)
-        return set_error(SELSCAN_ERR_UNSUPPORTED, "too many (batch, head, channel) rows for one launch");
+    // 16 rows of a state per workgroup of the token-by-token kernel, a chunk per workgroup of the chunked form
+    if (mul_checked({s->batch, s->nheads, s->headdim}) / 16 >= 0x7fffff00 ||
+        mul_checked({s->batch, s->nheads, selscan::delta_chunks(s->seqlen)}) >= 0x7fffff00)
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "too many (batch, head, channel) rows or chunks for one launch");
     return SELSCAN_OK;
 }
 
 bool vec4(const selscan_m2_shape_t* s, const void* q, const void* k) {
     const uintptr_t m = s->in_dtype == SELSCAN_BF16 ? 7 : 15;
     return s->dstate % 4 == 0 && (reinterpret_cast<uintptr_t>(q) & m) == 0 && (reinterpret_cast<uintptr_t>(k) & m) == 0;
+}
+
+// Sequences longer than this take the chunked form.
+constexpr int64_t kRecTokens = 16;
+
+size_t fwd_bytes(const selscan_m2_shape_t* s) {
+    if (s->seqlen <= kRecTokens) return 0;
+    return align256((size_t)(s->batch * s->nheads * selscan::delta_chunks(s->seqlen)) * selscan::delta_record_bytes());
 }
 
 selscan_status_t launched(hipError_t e) {
@@ -51,7 +60,7 @@ extern "C" {
 
 size_t selscan_delta_workspace_bytes(const selscan_m2_shape_t* s) {
     if (check_shape(s) != SELSCAN_OK) return 0;
-    return 0;
+    return fwd_bytes(s);
 }
 
 selscan_status_t selscan_delta_fwd(const selscan_m2_shape_t* s, const void* q, const void* k, const void* v,
@@ -69,9 +78,21 @@ selscan_status_t selscan_delta_fwd(const selscan_m2_shape_t* s, const void* q, c
         a.q = q; a.k = k; a.v = v; a.g = g; a.beta = beta; a.lengths = lengths; a.h0 = h0; a.y = y; a.last = last_state;
         a.batch = s->batch; a.L = s->seqlen; a.H = s->nheads; a.P = s->headdim; a.G = s->ngroups;
         a.N = (int)s->dstate; a.scale = scale;
-        a.vec = vec4(s, q, k) && aligned16(h0) && aligned16(last_state);
-        return launched(selscan::launch_delta_rec(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16,
-                                                  reinterpret_cast<hipStream_t>(stream)));
+        const int in_bf16 = s->in_dtype == SELSCAN_BF16, out_bf16 = s->out_dtype == SELSCAN_BF16;
+        hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+        if (s->seqlen <= kRecTokens) {
+            a.vec = vec4(s, q, k) && aligned16(h0) && aligned16(last_state);
+            return launched(selscan::launch_delta_rec(a, in_bf16, out_bf16, hs));
+        }
+        Scratch ws;
+        st = ws.get(s->workspace, s->workspace_bytes, fwd_bytes(s), hs);
+        if (st != SELSCAN_OK) return st;
+        a.vec = s->dstate % 8 == 0 && aligned16(q) && aligned16(k);
+        float* recs = static_cast<float*>(ws.ptr);
+        hipError_t e = selscan::launch_delta_prep(a, in_bf16, recs, hs);
+        if (e == hipSuccess) e = selscan::launch_delta_scan(a, in_bf16, out_bf16, recs, hs);
+        ws.release();
+        return launched(e);
     } catch (...) {
         return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
     }

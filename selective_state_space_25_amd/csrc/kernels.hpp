@@ -217,6 +217,13 @@ struct DeltaArgs {
     int vec;                  // rows of q, k and the states allow vector access
 };
 hipError_t launch_delta_rec(const DeltaArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
+// The chunked form: records of delta_record_bytes() for each of the
+// batch x H x delta_chunks(L) chunks (vec: rows of q and k on 16-byte
+// boundaries, N % 8 == 0), then the scan over them.
+int64_t delta_chunks(int64_t L);
+size_t delta_record_bytes();
+hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, float* recs, hipStream_t stream);
+hipError_t launch_delta_scan(const DeltaArgs& a, int in_bf16, int out_bf16, const float* recs, hipStream_t stream);
 
 // Layer norm with dropout and residual sum in front.
 struct NormArgs {
