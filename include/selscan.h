@@ -386,6 +386,38 @@ selscan_status_t selscan_delta_fwd(const selscan_m2_shape_t* shape,
                                    const int32_t* lengths, const float* h0,
                                    void* y, float* last_state, void* stream);
 
+/* Bytes of workspace selscan_delta_bwd needs for `shape` (0 on a bad shape).
+ * It grows with batch x heads x L: per head and 64 tokens two states, two
+ * P-wide rows per token and 21 KiB (213 KiB at N = P = 128; 436 MB for batch
+ * 4, L 2048, 16 heads), and 2 N fp32 per token and head where heads share q
+ * and k. */
+size_t selscan_delta_bwd_workspace_bytes(const selscan_m2_shape_t* shape);
+
+/*
+ * Gradients of the gated delta rule (training; reverse mode through the
+ * recurrence, the states recomputed from the inputs).
+ *   q .. lengths, h0  as for selscan_delta_fwd
+ *   dout         [B, L, H, P]  out_dtype  gradient of y (not read past a
+ *                                         sequence's end)
+ *   dlast_state  [B, H, P, N]  fp32       gradient of last_state; NULL = 0
+ *   dq, dk       [B, L, G, N]  in_dtype   (written; summed over the heads of a
+ *                                         group in fp32, then rounded once)
+ *   dv           [B, L, H, P]  in_dtype   (written)
+ *   dg, dbeta    [B, L, H]     fp32       (written)
+ *   dh0          [B, H, P, N]  fp32       (written; NULL = skip)
+ * Gradients of tokens past a sequence's end are zero.  Gradients must not
+ * alias inputs or each other.  Sums run in a fixed order: results are
+ * reproducible bit for bit.  Unlike the scans' gradients, dq, dk and dv come
+ * in the inputs' type: they are read next by the backward of a projection.
+ */
+selscan_status_t selscan_delta_bwd(const selscan_m2_shape_t* shape,
+                                   const void* q, const void* k, const void* v,
+                                   const float* g, const float* beta, float scale,
+                                   const int32_t* lengths, const float* h0,
+                                   const void* dout, const float* dlast_state,
+                                   void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                                   float* dh0, void* stream);
+
 /*
  * Gated delta rule, one token: shape as for selscan_delta_fwd (seqlen and
  * workspace ignored); q, k [B, G, N], v [B, H, P] in_dtype, g, beta [B, H]

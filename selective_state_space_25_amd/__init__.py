@@ -51,6 +51,7 @@ EXPORTED = ("selscan_fwd", "selscan_mamba2_fwd", "selscan_workspace_bytes", "sel
             "selscan_bwd", "selscan_bwd_workspace_bytes", "selscan_fwd_noalloc",
             "selscan_mamba2_bwd", "selscan_mamba2_bwd_workspace_bytes",
             "selscan_delta_fwd", "selscan_delta_workspace_bytes", "selscan_delta_step",
+            "selscan_delta_bwd", "selscan_delta_bwd_workspace_bytes",
             "selscan_dropout", "selscan_layer_norm_fwd", "selscan_layer_norm_bwd",
             "selscan_layer_norm_bwd_workspace_bytes",
             "selscan_last_error", "selscan_version", "selscan_timing_enable", "selscan_timing_collect")
@@ -125,6 +126,11 @@ def lib() -> ctypes.CDLL:
         L.selscan_delta_workspace_bytes.restype = ctypes.c_size_t
         L.selscan_delta_fwd.argtypes = [ctypes.POINTER(M2Shape), vp, vp, vp, fp, fp, f32, vp, fp, vp, fp, vp]
         L.selscan_delta_fwd.restype = i32
+        L.selscan_delta_bwd.argtypes = [ctypes.POINTER(M2Shape), vp, vp, vp, fp, fp, f32, vp, fp, vp, fp, vp, vp, vp] + \
+            [fp] * 3 + [vp]
+        L.selscan_delta_bwd.restype = i32
+        L.selscan_delta_bwd_workspace_bytes.argtypes = [ctypes.POINTER(M2Shape)]
+        L.selscan_delta_bwd_workspace_bytes.restype = ctypes.c_size_t
         L.selscan_delta_step.argtypes = [ctypes.POINTER(M2Shape), fp, vp, vp, vp, fp, fp, f32, vp, vp]
         L.selscan_delta_step.restype = i32
         L.selscan_dropout.argtypes = [ctypes.POINTER(DropoutShape), vp, vp, vp]
@@ -583,6 +589,50 @@ def delta_fwd(q, k, v, g, beta, scale=None, lengths=None, h0=None, out=None, las
     return out, last_state
 
 
+def delta_bwd_workspace_bytes(batch, seqlen, nheads, headdim, ngroups, dstate, in_dtype=BF16, out_dtype=None) -> int:
+    s = M2Shape(batch, seqlen, nheads, headdim, ngroups, dstate, in_dtype, in_dtype if out_dtype is None else out_dtype,
+                None, 0)
+    return int(lib().selscan_delta_bwd_workspace_bytes(ctypes.byref(s)))
+
+
+def delta_bwd(q, k, v, g, beta, dout, scale=None, lengths=None, h0=None, dlast_state=None, want_dh0=False,
+              workspace=None):
+    """Gradients of the gated delta rule.
+
+    Inputs as for delta_fwd; dout [batch, L, H, P] (float32 or bfloat16) is
+    the gradient of the loss with respect to y, dlast_state [batch, H, P, N]
+    float32 that with respect to last_state (None: zero).  Returns a dict: dq,
+    dk [batch, L, G, N] and dv [batch, L, H, P] in the inputs' dtype; dg,
+    dbeta [batch, L, H] float32; dh0 [batch, H, P, N] float32 (when h0 is
+    given or want_dh0).
+    """
+    torch = _torch()
+    f32 = torch.float32
+    dev, dt = q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("selscan.delta_bwd needs tensors on a GPU device")
+    batch, L, G, N = q.shape
+    H, P = v.shape[2], v.shape[3]
+    new = lambda shape, dtype: torch.empty(shape, dtype=dtype, device=dev)
+    r = {"dq": new((batch, L, G, N), dt), "dk": new((batch, L, G, N), dt), "dv": new((batch, L, H, P), dt),
+         "dg": new((batch, L, H), f32), "dbeta": new((batch, L, H), f32)}
+    if h0 is not None or want_dh0:
+        r["dh0"] = new((batch, H, P, N), f32)
+    s = M2Shape(batch, L, H, P, G, N, _dtype_code(q), _dtype_code(dout), None, 0)
+    args = (_ptr(q, "q", (batch, L, G, N), dt, dev), _ptr(k, "k", (batch, L, G, N), dt, dev),
+            _ptr(v, "v", (batch, L, H, P), dt, dev), _ptr(g, "g", (batch, L, H), f32, dev),
+            _ptr(beta, "beta", (batch, L, H), f32, dev), N ** -0.5 if scale is None else float(scale),
+            _ptr(lengths, "lengths", (batch,), torch.int32, dev), _ptr(h0, "h0", (batch, H, P, N), f32, dev),
+            _ptr(dout, "dout", (batch, L, H, P), None, dev),
+            _ptr(dlast_state, "dlast_state", (batch, H, P, N), f32, dev),
+            *(r[n].data_ptr() if n in r else None for n in ("dq", "dk", "dv", "dg", "dbeta", "dh0")),
+            _stream_handle(dev))
+    L_ = lib()
+    s.workspace, s.workspace_bytes, ws = _ws_arg(workspace, L_.selscan_delta_bwd_workspace_bytes(ctypes.byref(s)), dev)
+    _check(L_.selscan_delta_bwd(ctypes.byref(s), *args))
+    return r
+
+
 def _delta_step_args(state, q, k, v, g, beta, scale, out, out_dtype):
     torch = _torch()
     f32 = torch.float32
@@ -726,6 +776,6 @@ def timing_collect() -> dict:
     return res
 
 
-__all__ = ["delta_fwd", "delta_step", "bind_delta_step", "delta_workspace_bytes", "dropout", "layer_norm_fwd",
+__all__ = ["delta_fwd", "delta_bwd", "delta_bwd_workspace_bytes", "delta_step", "bind_delta_step", "delta_workspace_bytes", "dropout", "layer_norm_fwd",
            "layer_norm_bwd", "NormShape", "DropoutShape", "bind_step", "bind_mamba2_step", "bwd", "bwd_workspace_bytes", "conv1d", "ConvShape", "step", "mamba2_step", "timing_enable", "timing_collect", "KernelTime", "fwd", "mamba2_fwd", "workspace_bytes", "mamba2_workspace_bytes", "version", "last_error", "lib",
            "SelscanError", "Shape", "M2Shape", "m1_shape", "EXPORTED", "LIB_PATH"]

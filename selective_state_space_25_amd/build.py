@@ -28,7 +28,8 @@ LIB = os.path.join(HERE, "libselscan.so")
 ABI_BENCH = os.path.join(HERE, "abi_bench")   # host cost of the decode entry points, timed from C++
 BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["selscan.cpp", "timing.cpp", "m1_scan.hip", "m2_scan.hip", "m2_ssd.hip", "step.hip", "conv1d.hip", "m1_bwd.hip", "m2_bwd.hip", "noalloc.hip",
-           "delta.cpp", "delta_rec.hip", "delta_prep.hip", "delta_scan.hip", "block_ops.cpp", "norm.hip", "dropout.hip"]
+           "delta.cpp", "delta_rec.hip", "delta_prep.hip", "delta_scan.hip", "delta_bwd.hip",
+           "block_ops.cpp", "norm.hip", "dropout.hip"]
 ARCH = os.environ.get("SELSCAN_ARCH", "gfx950")
 
 

@@ -48,6 +48,24 @@ size_t fwd_bytes(const selscan_m2_shape_t* s) {
     return align256((size_t)(s->batch * s->nheads * selscan::delta_chunks(s->seqlen)) * selscan::delta_record_bytes());
 }
 
+selscan_status_t check_bwd_shape(const selscan_m2_shape_t* s) {
+    selscan_status_t st = check_shape(s);
+    if (st != SELSCAN_OK) return st;
+    // the kept states and columns are sized by 64-token chunks and P rounded up to 32
+    if (s->headdim > (int64_t(1) << 20))
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "gradients of the gated delta rule support headdim <= 2^20");
+    if (mul_checked({s->batch, s->nheads, selscan::delta_chunks(s->seqlen), (s->headdim + 31) / 32 * 32, 128, 16}) < 0 ||
+        mul_checked({s->batch, s->seqlen, s->nheads, s->dstate, 16}) < 0)
+        return set_error(SELSCAN_ERR_INVALID_ARG, "workspace size overflows 64-bit byte counts");
+    if (s->batch * s->seqlen * s->ngroups * s->dstate / 256 >= 0x7fffff00)
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "too many dq/dk elements for one launch");
+    return SELSCAN_OK;
+}
+
+size_t bwd_bytes(const selscan_m2_shape_t* s) {
+    return selscan::delta_bwd_bytes(s->batch, s->seqlen, s->nheads, s->ngroups, s->headdim, s->dstate);
+}
+
 selscan_status_t launched(hipError_t e) {
     if (e != hipSuccess)
         return set_error(SELSCAN_ERR_LAUNCH, std::string("kernel launch failed: ") + hipGetErrorString(e));
@@ -91,6 +109,44 @@ selscan_status_t selscan_delta_fwd(const selscan_m2_shape_t* s, const void* q, c
         float* recs = static_cast<float*>(ws.ptr);
         hipError_t e = selscan::launch_delta_prep(a, in_bf16, recs, hs);
         if (e == hipSuccess) e = selscan::launch_delta_scan(a, in_bf16, out_bf16, recs, hs);
+        ws.release();
+        return launched(e);
+    } catch (...) {
+        return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
+    }
+}
+
+size_t selscan_delta_bwd_workspace_bytes(const selscan_m2_shape_t* s) {
+    if (check_bwd_shape(s) != SELSCAN_OK) return 0;
+    return bwd_bytes(s);
+}
+
+selscan_status_t selscan_delta_bwd(const selscan_m2_shape_t* s, const void* q, const void* k, const void* v,
+                                   const float* g, const float* beta, float scale, const int32_t* lengths,
+                                   const float* h0, const void* dout, const float* dlast_state, void* dq, void* dk,
+                                   void* dv, float* dg, float* dbeta, float* dh0, void* stream) {
+    try {
+        selscan_status_t st = check_bwd_shape(s);
+        if (st != SELSCAN_OK) return st;
+        if (!q || !k || !v || !g || !beta || !dout)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "q, k, v, g, beta and dout must be non-NULL");
+        if (!dq || !dk || !dv || !dg || !dbeta)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "dq, dk, dv, dg and dbeta must be non-NULL");
+        st = device_check();
+        if (st != SELSCAN_OK) return st;
+        hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+        Scratch ws;
+        st = ws.get(s->workspace, s->workspace_bytes, bwd_bytes(s), hs);
+        if (st != SELSCAN_OK) return st;
+        selscan::DeltaBwdArgs a{};
+        a.f.q = q; a.f.k = k; a.f.v = v; a.f.g = g; a.f.beta = beta; a.f.lengths = lengths; a.f.h0 = h0;
+        a.f.batch = s->batch; a.f.L = s->seqlen; a.f.H = s->nheads; a.f.P = s->headdim; a.f.G = s->ngroups;
+        a.f.N = (int)s->dstate; a.f.scale = scale;
+        a.f.vec = s->dstate % 8 == 0 && aligned16(q) && aligned16(k);
+        a.vec_p = s->headdim % 8 == 0 && aligned16(v) && aligned16(dout);
+        a.dout = dout; a.dlast = dlast_state; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0;
+        selscan::delta_bwd_carve(a, ws.ptr);
+        const hipError_t e = selscan::launch_delta_bwd(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16, hs);
         ws.release();
         return launched(e);
     } catch (...) {

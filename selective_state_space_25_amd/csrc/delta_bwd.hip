@@ -1,0 +1,720 @@
+// delta_bwd.hip -- gradients of the gated delta rule over 64-token chunks.
+//
+// With the names of delta_scan.hip, dO = scale dout, D the adjoint of the
+// state S' that leaves a chunk, G[t, s] = e^(cum_t - cum_s):
+//
+//   dU = A^T dO + e^(last - cum) (K D);   dR = T^T dU;   dV = beta dR
+//   D_in = e^last D + Q^T (e^cum dO) - K^T (beta e^cum dR)
+//
+//   X  = (dO U^T) G on and below the diagonal;  E = -beta (dR U^T) G below it
+//   dQ = e^cum dO S^T + X K
+//   dK = e^(last - cum) U D^T - beta e^cum dR S^T + X^T Q + E K + E^T K
+//   beta dbeta = beta (dR.V - e^cum k.(S dR)) + rowsum(E KK^T)
+//
+// and for the decays, where Z = X QK^T + E KK^T (pairs of different tokens),
+// a_t = e^cum (q.(S dO) - beta k.(S dR)), b_t = e^(last - cum) k.(D U):
+//
+//   dg_t = sum_{i >= t} (rowsum Z - colsum Z + a)_i + sum_{i < t} b_i + e^last <S, D>
+//
+// Row and column sums are taken of the same Z and, like the dots, in fp64:
+// where a key is written over, dg is a small difference of these sums.  Five kernels: the records (delta_prep.hip), the
+// scan that keeps every S and U (delta_scan.hip), the scan back over the
+// chunks that makes D, dR and dV (a wave per 16 value columns, as forward),
+// the gradients that are local to a chunk (all chunks at once), and, where
+// heads share q and k, their sum over the heads in a fixed order.  All
+// products are fp32-grade except those that go into a bf16 dq or dk alone.
+#include "delta_chunk.hpp"
+
+namespace selscan {
+
+namespace {
+
+using namespace dchunk;
+
+// ------------------------------------------------------------ the scan back
+template <typename Tin, int NP>
+struct BackSmem {
+    static constexpr int kRow = NP + 8;
+    float gam[kC], tail[kC], beta[kC];
+    uint16_t K[kPlanes<Tin>][kC][kRow];   // columns through kperm
+    uint16_t Q[kPlanes<Tin>][kC][kRow];
+    Frags<3> T, A;                        // transposed
+};
+
+template <typename Tin, typename Tdo, int NP, int W>
+__global__ __launch_bounds__(64 * W) void delta_back_kernel(DeltaBwdArgs ba, int64_t nch, int npb) {
+    constexpr int NK = kPlanes<Tin>, NO = kPlanes<Tdo>;
+    constexpr int kRow = BackSmem<Tin, NP>::kRow;
+    constexpr int NB = NP / 16, KS = NP / 32;
+    constexpr int kT = 64 * W;
+    constexpr int NPC = kC * (NP / 8) / kT;
+    constexpr int NTR = (kBlocks * 64 + kT - 1) / kT;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
+    auto& sm = *reinterpret_cast<BackSmem<Tin, NP>*>(smem_raw);
+    const DeltaArgs& a = ba.f;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    const int64_t j = blockIdx.x / 8;
+    const int64_t bh = (j / npb) * 8 + blockIdx.x % 8;
+    if (bh >= a.batch * a.H) return;
+    const int64_t b = bh / a.H, h = bh - b * a.H, grp = h / (a.H / a.G);
+    const int64_t len = seq_len(a, b);
+    const int64_t mine = (len + kC - 1) / kC;
+    const int64_t p0 = (int64_t)(j % npb) * 16 * W + 16 * wave;
+    const int64_t p = p0 + li;
+    const int pad = ba.pad;
+    const bool active = p0 < pad, pok = p < a.P;
+    const int N = a.N;
+    const Tin* Kg = reinterpret_cast<const Tin*>(a.k);
+    const Tin* Qg = reinterpret_cast<const Tin*>(a.q);
+    const Tdo* Og = reinterpret_cast<const Tdo*>(ba.dout);
+    Tin* dVg = reinterpret_cast<Tin*>(ba.dv);
+
+    f32x4 D[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int n = 16 * i + 4 * lg + q;
+            D[i][q] = ba.dlast && pok && n < N ? ba.dlast[(bh * a.P + p) * N + n] : 0.0f;
+        }
+
+    struct Stage {
+        Raw8<Tin> k[NPC], q[NPC];
+        float t[NTR][4], am[NTR][4];
+        float4 gate;
+        Tdo o[16];
+    } st;
+    auto fetch = [&](int64_t c) {
+        const int64_t t0 = c * kC;
+        const int live = (int)min((int64_t)kC, len - t0);
+        const float* rec = ba.recs + (bh * nch + c) * kRec;
+#pragma unroll
+        for (int i = 0; i < NPC; ++i) {
+            const int id = tid + i * kT, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+            if (r < live) {
+                const int64_t row = ((b * a.L + t0 + r) * a.G + grp) * N;
+                fetch8(Kg + row, n0, N, a.vec, st.k[i]);
+                fetch8(Qg + row, n0, N, a.vec, st.q[i]);
+            } else {
+                zero(st.k[i]);
+                zero(st.q[i]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NTR; ++i) {
+            const int id = tid + i * kT;
+            if (id < kBlocks * 64) {   // lane li is a column of the block, four rows down from 4 lg
+                const int o = (id >> 6) * 256 + ((id >> 4) & 3) * 64 + (id & 15);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    st.t[i][q] = rec[kRecT + o + 16 * q];
+                    st.am[i][q] = rec[kRecA + o + 16 * q];
+                }
+            }
+        }
+        if (tid < 48) st.gate = *reinterpret_cast<const float4*>(rec + kRecGam + 4 * tid);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int r = 16 * (i >> 2) + 4 * lg + (i & 3);
+            st.o[i] = pok && r < live ? Og[((b * a.L + t0 + r) * a.H + h) * a.P + p] : Tdo(0);
+        }
+    };
+    auto stage = [&]() {
+#pragma unroll
+        for (int i = 0; i < NPC; ++i) {
+            const int id = tid + i * kT, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+            stage8<true>(sm.K[0][r], kC * kRow, n0, st.k[i]);
+            stage8<true>(sm.Q[0][r], kC * kRow, n0, st.q[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < NTR; ++i) {
+            const int id = tid + i * kT;
+            if (id < kBlocks * 64) {
+                int tb, sb;
+                lower_tile(id >> 6, tb, sb);
+                const int f = frag_t(sb, tb >> 1), e = 4 * (tb & 1);
+                uint2 tp[3], ap[3];
+                split4<3>(st.t[i], tp);
+                split4<3>(st.am[i], ap);
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    *reinterpret_cast<uint2*>(&sm.T.p[x][f][id & 63][e]) = tp[x];
+                    *reinterpret_cast<uint2*>(&sm.A.p[x][f][id & 63][e]) = ap[x];
+                }
+            }
+        }
+        if (tid < 48) *reinterpret_cast<float4*>(&sm.gam[4 * tid]) = st.gate;
+    };
+    // the zero blocks inside fragments 2 and 5 (row blocks 1 and 3), written once
+    for (int i = tid; i < 128; i += kT) {
+        const int f = i < 64 ? 2 : 5;
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            *reinterpret_cast<uint2*>(&sm.T.p[x][f][i & 63][0]) = make_uint2(0, 0);
+            *reinterpret_cast<uint2*>(&sm.A.p[x][f][i & 63][0]) = make_uint2(0, 0);
+        }
+    }
+    if (mine > 0) {
+        fetch(mine - 1);
+        stage();
+    }
+    __syncthreads();
+    for (int64_t c = mine - 1; c >= 0; --c) {
+        const int64_t t0 = c * kC;
+        float o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = io::ld(&st.o[i]);
+        // (fp32 inputs: the pieces would not fit beside the tiles, so they
+        // are fetched when the tiles are done with)
+        if (NK == 1 && c > 0) fetch(c - 1);
+        if (active) {
+            float* kd = ba.D + ((bh * nch + c) * pad + p) * NP + 4 * lg;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) *reinterpret_cast<f32x4*>(kd + 16 * i) = D[i];
+            bf16x8 Dp[KS][3], Op[2][NO], Bp[2][3];
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) split_tiles<3>(D[2 * ks], D[2 * ks + 1], Dp[ks]);
+            f32x4 O[4], R[4];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) O[i >> 2][i & 3] = o[i];
+            split_tiles<NO>(O[0], O[1], Op[0]);
+            split_tiles<NO>(O[2], O[3], Op[1]);
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
+                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, au = acc;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    bf16x8 k[NK];
+#pragma unroll
+                    for (int x = 0; x < NK; ++x) k[x] = ld8(&sm.K[x][16 * tb + li][32 * ks + 8 * lg]);
+                    acc = mm<3>(k, Dp[ks], acc);
+                }
+#pragma unroll
+                for (int ks = tb / 2; ks < 2; ++ks) {
+                    bf16x8 x[3];
+                    ld_frag(sm.A, frag_t(tb, ks), lane, x);
+                    au = mm<3>(x, Op[ks], au);
+                }
+                const f32x4 tail = *reinterpret_cast<const f32x4*>(&sm.tail[16 * tb + 4 * lg]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) R[tb][q] = __builtin_fmaf(tail[q], acc[q], a.scale * au[q]);   // dU
+            }
+            split_tiles<3>(R[0], R[1], Bp[0]);
+            split_tiles<3>(R[2], R[3], Bp[1]);
+            float* kr = ba.dR + (bh * nch + c) * kC * pad + p;
+#pragma unroll
+            for (int tb = 0; tb < 4; ++tb) {
+                R[tb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int ks = tb / 2; ks < 2; ++ks) {
+                    bf16x8 x[3];
+                    ld_frag(sm.T, frag_t(tb, ks), lane, x);
+                    R[tb] = mm<3>(x, Bp[ks], R[tb]);
+                }
+                const f32x4 gam = *reinterpret_cast<const f32x4*>(&sm.gam[16 * tb + 4 * lg]);
+                const f32x4 beta = *reinterpret_cast<const f32x4*>(&sm.beta[16 * tb + 4 * lg]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int r = 16 * tb + 4 * lg + q;
+                    kr[r * pad] = R[tb][q];
+                    R[tb][q] *= beta[q];
+                    if (pok && t0 + r < a.L) io::st(dVg + ((b * a.L + t0 + r) * a.H + h) * a.P + p, R[tb][q]);
+                    R[tb][q] *= -gam[q];
+                    O[tb][q] *= a.scale * gam[q];
+                }
+            }
+            const float gl = sm.gam[kC - 1];
+            auto down = [&](const uint16_t* m) {   // D += m^T (the tiles in Bp)
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) {
+                        bf16x8 x[NK];
+#pragma unroll
+                        for (int l = 0; l < NK; ++l) x[l] = ld_down<true>(m + l * kC * kRow, kRow, 32 * ks, 16 * i, lane);
+                        D[i] = mm<3>(x, Bp[ks], D[i]);
+                    }
+            };
+#pragma unroll
+            for (int i = 0; i < NB; ++i) D[i] *= gl;
+            split_tiles<3>(R[0], R[1], Bp[0]);
+            split_tiles<3>(R[2], R[3], Bp[1]);
+            down(&sm.K[0][0][0]);
+            split_tiles<3>(O[0], O[1], Bp[0]);
+            split_tiles<3>(O[2], O[3], Bp[1]);
+            down(&sm.Q[0][0][0]);
+        }
+        if (NK == 3 && c > 0) fetch(c - 1);
+        __syncthreads();
+        if (c > 0) stage();
+        __syncthreads();
+    }
+    if (pok) {
+        for (int64_t t = mine * kC + lg; t < a.L; t += 4) io::st(dVg + ((b * a.L + t) * a.H + h) * a.P + p, 0.0f);
+        if (ba.dh0) {
+#pragma unroll
+            for (int i = 0; i < NB; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int n = 16 * i + 4 * lg + q;
+                    if (n < N) ba.dh0[(bh * a.P + p) * N + n] = D[i][q];
+                }
+        }
+    }
+}
+
+// ------------------------------------------------- gradients inside a chunk
+constexpr int kPb = 32;            // value columns per step of the sums over p
+constexpr int kRowP = kPb + 8;
+constexpr int kRowX = kC + 8;
+
+template <typename Tin, typename Tdo, int NP, int LB>
+struct GradSmem {
+    static constexpr int kRow = NP + 8;
+    double cum[kC];
+    double col[4][kC];             // per row block: column sums of Z
+    double up[kC], down[kC];       // rowsum Z + a; b
+    double sd[4];
+    float rv[kC];
+    union {
+        struct {                   // a step over 32 value columns
+            uint16_t S[3][kPb][kRow], D[3][kPb][kRow];
+            uint16_t U[3][kC][kRowP], R[3][kC][kRowP];
+            uint16_t O[kPlanes<Tdo>][kC][kRowP];
+        } s;
+        struct {                   // the chunk's pairs
+            uint16_t K[kPlanes<Tin>][kC][kRow], Q[kPlanes<Tin>][kC][kRow];
+            uint16_t X[LB][kC][kRowX], E[LB][kC][kRowX];
+        } m;
+    };
+};
+
+__device__ __forceinline__ double sum16(double v) {
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+template <typename Tin, typename Tdo, int NP>
+__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_t nch) {
+    constexpr int NK = kPlanes<Tin>, NO = kPlanes<Tdo>;
+    constexpr int LB = NK == 1 ? 2 : 3;      // plane pairs of what goes into dq and dk alone
+    using Smem = GradSmem<Tin, Tdo, NP, LB>;
+    constexpr int kRow = Smem::kRow;
+    constexpr int NB = NP / 16;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
+    auto& sm = *reinterpret_cast<Smem*>(smem_raw);
+    const DeltaArgs& a = ba.f;
+    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    const int tb = wave;                     // the wave's 16 tokens
+    const int64_t bh = blockIdx.x / nch, c = blockIdx.x - bh * nch;
+    const int64_t b = bh / a.H, h = bh - b * a.H, grp = h / (a.H / a.G);
+    const int64_t t0 = c * kC;
+    const int64_t len = seq_len(a, b);
+    const int live = (int)max((int64_t)0, min((int64_t)kC, len - t0));
+    const int inside = (int)min((int64_t)kC, a.L - t0);   // tokens of the chunk that exist
+    const int N = a.N;
+    const int pad = ba.pad;
+    // dq and dk: one row per head where they are summed over a group later
+    const bool shared_qk = ba.pq != nullptr;
+    auto put = [&](void* out, float* part, int r, int n, float v) {
+        if (shared_qk) part[((b * a.L + t0 + r) * a.H + h) * N + n] = v;
+        else io::st(reinterpret_cast<Tin*>(out) + ((b * a.L + t0 + r) * a.G + grp) * N + n, v);
+    };
+    if (live == 0) {
+        for (int i = tid; i < inside * N; i += 256) {
+            put(ba.dq, ba.pq, i / N, i % N, 0.0f);
+            put(ba.dk, ba.pk, i / N, i % N, 0.0f);
+        }
+        if (tid < inside) {
+            ba.dg[(b * a.L + t0 + tid) * a.H + h] = 0.0f;
+            ba.dbeta[(b * a.L + t0 + tid) * a.H + h] = 0.0f;
+        }
+        return;
+    }
+    const float* rec = ba.recs + (int64_t)blockIdx.x * kRec;
+    if (tid < kC) sm.cum[tid] = reinterpret_cast<const double*>(rec + kRecCum)[tid];
+
+    // ---- sums over the value columns: dO S^T, dR S^T, U D^T for the wave's
+    // tokens, dO U^T and dR U^T for its row block, <S, D>, dR.V
+    const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 q1[NB], k2[NB], k3[NB], x1[4], x2[4];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) q1[i] = k2[i] = k3[i] = z4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x1[i] = x2[i] = z4;
+    double sd = 0.0;
+    float rv[2] = {0.0f, 0.0f};
+    const float* Sg = ba.S + (int64_t)blockIdx.x * pad * NP;
+    const float* Dg = ba.D + (int64_t)blockIdx.x * pad * NP;
+    const float* Ug = ba.U + (int64_t)blockIdx.x * kC * pad;
+    const float* Rg = ba.dR + (int64_t)blockIdx.x * kC * pad;
+    const Tdo* Og = reinterpret_cast<const Tdo*>(ba.dout);
+    const Tin* Vg = reinterpret_cast<const Tin*>(a.v);
+    for (int pb = 0; pb < pad; pb += kPb) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < NP / 32; ++i) {      // S and D: 32 rows of NP
+            const int id = tid + 256 * i, r = id / (NP / 4), n = 4 * (id % (NP / 4));
+            float s[4], d[4];
+            io::ld4(Sg + (int64_t)(pb + r) * NP + n, s);
+            io::ld4(Dg + (int64_t)(pb + r) * NP + n, d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sd = __builtin_fma((double)s[e], (double)d[e], sd);
+            uint2 sp[3], dp[3];
+            split4<3>(s, sp);
+            split4<3>(d, dp);
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+                *reinterpret_cast<uint2*>(&sm.s.S[x][r][n]) = sp[x];
+                *reinterpret_cast<uint2*>(&sm.s.D[x][r][n]) = dp[x];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {            // U and dR: 64 rows of 32
+            const int id = tid + 256 * i, r = id >> 3, e0 = 4 * (id & 7);
+            float u[4], d[4];
+            io::ld4(Ug + (int64_t)r * pad + pb + e0, u);
+            io::ld4(Rg + (int64_t)r * pad + pb + e0, d);
+            if (r < live) {
+                const Tin* vr = Vg + ((b * a.L + t0 + r) * a.H + h) * a.P;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (pb + e0 + e < a.P) rv[i] = __builtin_fmaf(d[e], io::ld(vr + pb + e0 + e), rv[i]);
+            }
+            uint2 up[3], dp[3];
+            split4<3>(u, up);
+            split4<3>(d, dp);
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+                *reinterpret_cast<uint2*>(&sm.s.U[x][r][e0]) = up[x];
+                *reinterpret_cast<uint2*>(&sm.s.R[x][r][e0]) = dp[x];
+            }
+        }
+        {                                        // dout: 64 rows of 32
+            const int r = tid >> 2, e0 = 8 * (tid & 3);
+            Raw8<Tdo> o;
+            if (r < live) fetch8(Og + ((b * a.L + t0 + r) * a.H + h) * a.P + pb, e0, (int)min(a.P - pb, (int64_t)kPb), ba.vec_p, o);
+            else zero(o);
+            stage8<false>(sm.s.O[0][r], kC * kRowP, e0, o);
+        }
+        __syncthreads();
+        bf16x8 o[NO], r[3], u[3];
+#pragma unroll
+        for (int x = 0; x < NO; ++x) o[x] = ld8(&sm.s.O[x][16 * tb + li][8 * lg]);
+#pragma unroll
+        for (int x = 0; x < 3; ++x) {
+            r[x] = ld8(&sm.s.R[x][16 * tb + li][8 * lg]);
+            u[x] = ld8(&sm.s.U[x][16 * tb + li][8 * lg]);
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            bf16x8 s[3], d[3];
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+                s[x] = ld_down8<false>(&sm.s.S[x][0][0], kRow, 0, 16 * i, lane);
+                d[x] = ld_down8<false>(&sm.s.D[x][0][0], kRow, 0, 16 * i, lane);
+            }
+            q1[i] = mm<3>(o, s, q1[i]);
+            k2[i] = mm<3>(r, s, k2[i]);
+            k3[i] = mm<3>(u, d, k3[i]);
+        }
+#pragma unroll
+        for (int sb = 0; sb < 4; ++sb) {
+            if (sb > tb) continue;
+            bf16x8 w[3];
+#pragma unroll
+            for (int x = 0; x < 3; ++x) w[x] = ld8(&sm.s.U[x][16 * sb + li][8 * lg]);
+            x1[sb] = mm<3>(o, w, x1[sb]);
+            x2[sb] = mm<3>(r, w, x2[sb]);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) sd += __shfl_xor(sd, o, 64);
+    if (lane == 0) sm.sd[wave] = sd;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) rv[i] += __shfl_xor(rv[i], o, 64);
+        if ((tid & 7) == 0) sm.rv[(tid >> 3) + 32 * i] = rv[i];
+    }
+    // K and Q over what the steps used
+#pragma unroll
+    for (int i = 0; i < NP / 32; ++i) {
+        const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+        Raw8<Tin> k, q;
+        if (r < live) {
+            const int64_t row = ((b * a.L + t0 + r) * a.G + grp) * N;
+            fetch8(reinterpret_cast<const Tin*>(a.k) + row, n0, N, a.vec, k);
+            fetch8(reinterpret_cast<const Tin*>(a.q) + row, n0, N, a.vec, q);
+        } else {
+            zero(k);
+            zero(q);
+        }
+        stage8<false>(sm.m.K[0][r], kC * kRow, n0, k);
+        stage8<false>(sm.m.Q[0][r], kC * kRow, n0, q);
+    }
+    __syncthreads();
+
+    // ---- the dots with q and k; dQ and dK from the states
+    const f32x4 gam = *reinterpret_cast<const f32x4*>(rec + kRecGam + 16 * tb + 4 * lg);
+    const f32x4 tail = *reinterpret_cast<const f32x4*>(rec + kRecTail + 16 * tb + 4 * lg);
+    const f32x4 beta = *reinterpret_cast<const f32x4*>(rec + kRecBeta + 16 * tb + 4 * lg);
+    double aq[4] = {}, ak[4] = {}, bk[4] = {};
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = 16 * tb + 4 * lg + q, n = 16 * i + li;
+            float kv = 0.0f, qv = 0.0f;
+#pragma unroll
+            for (int x = NK - 1; x >= 0; --x) {
+                kv += bf16_to_f32(sm.m.K[x][r][n]);
+                qv += bf16_to_f32(sm.m.Q[x][r][n]);
+            }
+            aq[q] = __builtin_fma((double)qv, (double)q1[i][q], aq[q]);
+            ak[q] = __builtin_fma((double)kv, (double)k2[i][q], ak[q]);
+            bk[q] = __builtin_fma((double)kv, (double)k3[i][q], bk[q]);
+            q1[i][q] *= a.scale * gam[q];
+            k3[i][q] = __builtin_fmaf(tail[q], k3[i][q], -beta[q] * gam[q] * k2[i][q]);
+        }
+    // ---- pairs: X, E and the sums of Z
+    double row[4] = {}, rb[4] = {};
+#pragma unroll
+    for (int sb = 0; sb < 4; ++sb) {
+        float xv[4] = {}, ev[4] = {};
+        const int s = 16 * sb + li;
+        if (sb <= tb) {
+            f32x4 kk = z4;
+#pragma unroll
+            for (int ks = 0; ks < NP / 32; ++ks) {
+                bf16x8 x[NK], y[NK];
+#pragma unroll
+                for (int p = 0; p < NK; ++p) {
+                    x[p] = ld8(&sm.m.K[p][16 * tb + li][32 * ks + 8 * lg]);
+                    y[p] = ld8(&sm.m.K[p][s][32 * ks + 8 * lg]);
+                }
+                kk = mm<3>(x, y, kk);
+            }
+            const float* ab = rec + kRecA + (tb * (tb + 1) / 2 + sb) * 256 + li;
+            const double cs = sm.cum[s];
+            double cz = 0.0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int t = 16 * tb + 4 * lg + q;
+                const float g = s <= t ? exp_f32((float)(sm.cum[t] - cs)) : 0.0f;
+                const float gl = s < t ? g : 0.0f;
+                const float e0 = -x2[sb][q] * gl;             // E without beta
+                xv[q] = a.scale * x1[sb][q] * g;
+                ev[q] = beta[q] * e0;
+                const float ekk = e0 * kk[q];
+                const float zv = (s < t ? a.scale * x1[sb][q] * ab[(4 * lg + q) * 16] : 0.0f) + beta[q] * ekk;
+                rb[q] += ekk;
+                row[q] += zv;
+                cz += zv;
+            }
+            cz += __shfl_xor(cz, 16, 64);
+            cz += __shfl_xor(cz, 32, 64);
+            if (lg == 0) sm.col[tb][s] = cz;
+        }
+        // (block tb + 1 of an even row block shares its k-step: zero)
+        if (sb <= (tb | 1)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int t = 16 * tb + 4 * lg + q;
+                float x = xv[q], e = ev[q];
+#pragma unroll
+                for (int l = 0; l < LB; ++l) {
+                    const uint16_t xh = f32_to_bf16(x), eh = f32_to_bf16(e);
+                    sm.m.X[l][t][s] = xh;
+                    sm.m.E[l][t][s] = eh;
+                    x -= bf16_to_f32(xh);
+                    e -= bf16_to_f32(eh);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int t = 16 * tb + 4 * lg + q;
+        aq[q] = sum16(aq[q]);
+        ak[q] = sum16(ak[q]);
+        bk[q] = sum16(bk[q]);
+        row[q] = sum16(row[q]);
+        rb[q] = sum16(rb[q]);
+        if (li == 0) {
+            sm.up[t] = row[q] + gam[q] * (a.scale * aq[q] - beta[q] * ak[q]);
+            sm.down[t] = tail[q] * bk[q];
+            if (t < inside)
+                ba.dbeta[(b * a.L + t0 + t) * a.H + h] = t < live ? (float)(sm.rv[t] - gam[q] * ak[q] + rb[q]) : 0.0f;
+        }
+    }
+    __syncthreads();
+    if (wave == 0) {   // dg: lane = token
+        double up = sm.up[lane], down = sm.down[lane];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i >= lane / 16) up -= sm.col[i][lane];
+        const double own = down;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double u = __shfl_down(up, o, 64), d = __shfl_up(down, o, 64);
+            if (lane + o < 64) up += u;
+            if (lane >= o) down += d;
+        }
+        const double last = rec[kRecGam + kC - 1] * ((sm.sd[0] + sm.sd[1]) + (sm.sd[2] + sm.sd[3]));
+        if (lane < inside) {
+            // a decay that is zero has no gradient; the sums would leave their rounding
+            const int64_t gi = (b * a.L + t0 + lane) * a.H + h;
+            ba.dg[gi] = lane < live && exp_f32(a.g[gi]) != 0.0f ? (float)(up + (down - own) + last) : 0.0f;
+        }
+    }
+    // ---- dQ += X K;  dK += X^T Q + E K + E^T K
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) {
+        const bool lo = ks <= tb / 2, hi = ks >= tb / 2;   // rows of X and E; their columns
+        bf16x8 x[LB], e[LB], xt[LB], et[LB];
+#pragma unroll
+        for (int l = 0; l < LB; ++l) {
+            if (lo) {
+                x[l] = ld8(&sm.m.X[l][16 * tb + li][32 * ks + 8 * lg]);
+                e[l] = ld8(&sm.m.E[l][16 * tb + li][32 * ks + 8 * lg]);
+            }
+            if (hi) {
+                xt[l] = ld_down8<false>(&sm.m.X[l][0][0], kRowX, 32 * ks, 16 * tb, lane);
+                et[l] = ld_down8<false>(&sm.m.E[l][0][0], kRowX, 32 * ks, 16 * tb, lane);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+            bf16x8 k[NK], q[NK];
+#pragma unroll
+            for (int p = 0; p < NK; ++p) k[p] = ld_down8<false>(&sm.m.K[p][0][0], kRow, 32 * ks, 16 * i, lane);
+            if (lo) {
+                q1[i] = mm<LB>(x, k, q1[i]);
+                k3[i] = mm<LB>(e, k, k3[i]);
+            }
+            if (hi) {
+#pragma unroll
+                for (int p = 0; p < NK; ++p) q[p] = ld_down8<false>(&sm.m.Q[p][0][0], kRow, 32 * ks, 16 * i, lane);
+                k3[i] = mm<LB>(et, k, k3[i]);
+                k3[i] = mm<LB>(xt, q, k3[i]);
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int r = 16 * tb + 4 * lg + q, n = 16 * i + li;
+            if (r < inside && n < N) {
+                put(ba.dq, ba.pq, r, n, q1[i][q]);
+                put(ba.dk, ba.pk, r, n, k3[i][q]);
+            }
+        }
+}
+
+// dq and dk of a group: the sum over its heads, in their order.
+template <typename Tin>
+__global__ __launch_bounds__(256) void delta_group_kernel(DeltaBwdArgs ba) {
+    const DeltaArgs& a = ba.f;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // [batch * L, G, N]
+    const int64_t n = i % a.N, tg = i / a.N;
+    if (tg >= a.batch * a.L * a.G) return;
+    const int64_t r = a.H / a.G;
+    float q = 0.0f, k = 0.0f;
+    for (int64_t j = 0; j < r; ++j) {   // head g r + j of token t is row t H + g r + j = tg r + j
+        q += ba.pq[(tg * r + j) * a.N + n];
+        k += ba.pk[(tg * r + j) * a.N + n];
+    }
+    io::st(reinterpret_cast<Tin*>(ba.dq) + i, q);
+    io::st(reinterpret_cast<Tin*>(ba.dk) + i, k);
+}
+
+template <typename K>
+hipError_t lds(K* kern, int bytes) {
+    return hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <typename Tin, typename Tdo, int NP>
+hipError_t launch(const DeltaBwdArgs& a, hipStream_t stream) {
+    constexpr int W = 4;
+    const DeltaArgs& f = a.f;
+    const int64_t nch = delta_chunks(f.L);
+    hipError_t e = launch_delta_prep(f, sizeof(Tin) == 2, a.recs, stream);
+    if (e != hipSuccess) return e;
+    e = launch_delta_keep(f, sizeof(Tin) == 2, a.recs, a.S, a.U, a.pad, stream);
+    if (e != hipSuccess) return e;
+    {
+        const auto kern = &delta_back_kernel<Tin, Tdo, NP, W>;
+        constexpr int bytes = (int)sizeof(BackSmem<Tin, NP>);
+        if ((e = lds(kern, bytes)) != hipSuccess) return e;
+        const int npb = (a.pad + 16 * W - 1) / (16 * W);
+        const int64_t units = (f.batch * f.H + 7) / 8 * 8;
+        KTime kt("delta_back", stream);
+        hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(64 * W), bytes, stream, a, nch, npb);
+    }
+    {
+        const auto kern = &delta_grad_kernel<Tin, Tdo, NP>;
+        constexpr int bytes = (int)sizeof(GradSmem<Tin, Tdo, NP, kPlanes<Tin> == 1 ? 2 : 3>);
+        static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
+        if ((e = lds(kern, bytes)) != hipSuccess) return e;
+        KTime kt("delta_grad", stream);
+        hipLaunchKernelGGL(kern, dim3((unsigned)(f.batch * f.H * nch)), dim3(256), bytes, stream, a, nch);
+    }
+    if (a.pq) {
+        KTime kt("delta_group", stream);
+        const int64_t n = f.batch * f.L * f.G * f.N;
+        hipLaunchKernelGGL((delta_group_kernel<Tin>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, a);
+    }
+    return hipGetLastError();
+}
+
+template <typename Tin, typename Tdo>
+hipError_t by_n(const DeltaBwdArgs& a, hipStream_t stream) {
+    return a.f.N <= 64 ? launch<Tin, Tdo, 64>(a, stream) : launch<Tin, Tdo, 128>(a, stream);
+}
+
+struct Sizes {
+    size_t recs, state, rows, part;
+};
+
+Sizes sizes(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N) {
+    const size_t chunks = (size_t)(batch * H * delta_chunks(L)), pad = (size_t)(P + 31) / 32 * 32;
+    auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+    return {up(chunks * delta_record_bytes()), up(chunks * pad * (N <= 64 ? 64 : 128) * 4), up(chunks * kC * pad * 4),
+            H > G ? up((size_t)(batch * L * H * N) * 4) : 0};
+}
+
+}  // namespace
+
+size_t delta_bwd_bytes(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N) {
+    const Sizes s = sizes(batch, L, H, G, P, N);
+    return s.recs + 2 * s.state + 2 * s.rows + 2 * s.part;
+}
+
+void delta_bwd_carve(DeltaBwdArgs& a, void* ws) {
+    const Sizes s = sizes(a.f.batch, a.f.L, a.f.H, a.f.G, a.f.P, a.f.N);
+    char* p = static_cast<char*>(ws);
+    auto take = [&](size_t n) {
+        float* r = reinterpret_cast<float*>(p);
+        p += n;
+        return r;
+    };
+    a.recs = take(s.recs);
+    a.S = take(s.state);
+    a.D = take(s.state);
+    a.U = take(s.rows);
+    a.dR = take(s.rows);
+    a.pq = s.part ? take(s.part) : nullptr;
+    a.pk = s.part ? take(s.part) : nullptr;
+    a.pad = (int)((a.f.P + 31) / 32 * 32);
+}
+
+hipError_t launch_delta_bwd(const DeltaBwdArgs& a, int in_bf16, int out_bf16, hipStream_t stream) {
+    if (in_bf16) return out_bf16 ? by_n<uint16_t, uint16_t>(a, stream) : by_n<uint16_t, float>(a, stream);
+    return out_bf16 ? by_n<float, uint16_t>(a, stream) : by_n<float, float>(a, stream);
+}
+
+}  // namespace selscan

@@ -26,20 +26,25 @@ namespace {
 
 using namespace dchunk;
 
-// OL: plane pairs a + b < OL in the products of y.
+// OL: plane pairs a + b < OL in the products of y; without y (OL = 0) Q and
+// A stay out.
 template <typename Tin, int NP, int OL>
 struct ScanSmem {
     static constexpr int kRow = NP + 8;
-    uint16_t K[kPlanes<Tin>][kC][kRow];   // columns through kperm
-    uint16_t Q[kPlanes<Tin>][kC][kRow];
-    Frags<3> T;
-    Frags<OL> A;
     float gam[kC], tail[kC], beta[kC];
+    uint16_t K[kPlanes<Tin>][kC][kRow];   // columns through kperm
+    Frags<3> T;
+    uint16_t Q[OL ? kPlanes<Tin> : 1][OL ? kC : 1][kRow];
+    Frags<OL ? OL : 1> A;
 };
 
-template <typename Tin, typename Tout, int NP, int W>
-__global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const float* recs, int64_t nch, int npb) {
-    constexpr int OL = sizeof(Tout) == 2 ? 2 : 3;
+// KEEP: instead of y, the state entering each chunk [chunk, pad, NP] and U
+// [chunk, 64, pad], which the gradients read (pad: P rounded up to 32, the
+// columns past P zero).
+template <typename Tin, typename Tout, int NP, int W, bool KEEP>
+__global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const float* recs, int64_t nch, int npb,
+                                                            float* keep_s, float* keep_u, int pad) {
+    constexpr int OL = KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3;
     constexpr int NK = kPlanes<Tin>;
     constexpr int kRow = ScanSmem<Tin, NP, OL>::kRow;
     constexpr int NB = NP / 16;              // state tiles
@@ -60,7 +65,7 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const f
     const int64_t mine = (len + kC - 1) / kC;
     const int64_t p0 = (int64_t)(j % npb) * 16 * W + 16 * wave;
     const int64_t p = p0 + li;
-    const bool active = p0 < a.P, pok = p < a.P;
+    const bool active = p0 < (KEEP ? (int64_t)pad : a.P), pok = p < a.P;
     const int N = a.N;
     const Tin* Kg = reinterpret_cast<const Tin*>(a.k);
     const Tin* Qg = reinterpret_cast<const Tin*>(a.q);
@@ -76,11 +81,9 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const f
             S[i][q] = a.h0 && pok && n < N ? a.h0[(bh * a.P + p) * N + n] : 0.0f;
         }
 
-    struct Stage {
-        Raw8<Tin> k[NPC], q[NPC];
-        float4 t[NTR], am[NTR], gate;
-        Tin v[16];
-    } st;
+    Raw8<Tin> sk[NPC], sq[NPC];   // the next chunk's pieces, on their way to LDS
+    float4 stt[NTR], sa[NTR], sgate;
+    Tin sv[16];
     auto fetch = [&](int64_t c) {
         const int64_t t0 = c * kC;
         const int live = (int)min((int64_t)kC, len - t0);
@@ -90,11 +93,11 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const f
             const int id = tid + i * kT, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
             if (r < live) {
                 const int64_t row = ((b * a.L + t0 + r) * a.G + grp) * N;
-                fetch8(Kg + row, n0, N, a.vec, st.k[i]);
-                fetch8(Qg + row, n0, N, a.vec, st.q[i]);
+                fetch8(Kg + row, n0, N, a.vec, sk[i]);
+                if constexpr (!KEEP) fetch8(Qg + row, n0, N, a.vec, sq[i]);
             } else {
-                zero(st.k[i]);
-                zero(st.q[i]);
+                zero(sk[i]);
+                if constexpr (!KEEP) zero(sq[i]);
             }
         }
 #pragma unroll
@@ -102,23 +105,23 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const f
             const int id = tid + i * kT;
             if (id < kBlocks * 64) {
                 const int o = (id >> 6) * 256 + (id & 15) * 16 + ((id >> 4) & 3) * 4;
-                st.t[i] = *reinterpret_cast<const float4*>(rec + kRecT + o);
-                st.am[i] = *reinterpret_cast<const float4*>(rec + kRecA + o);
+                stt[i] = *reinterpret_cast<const float4*>(rec + kRecT + o);
+                if constexpr (!KEEP) sa[i] = *reinterpret_cast<const float4*>(rec + kRecA + o);
             }
         }
-        if (tid < 48) st.gate = *reinterpret_cast<const float4*>(rec + kRecGam + 4 * tid);
+        if (tid < 48) sgate = *reinterpret_cast<const float4*>(rec + kRecGam + 4 * tid);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             const int r = 16 * (i >> 2) + 4 * lg + (i & 3);
-            st.v[i] = pok && r < live ? Vg[((b * a.L + t0 + r) * a.H + h) * a.P + p] : Tin(0);
+            sv[i] = pok && r < live ? Vg[((b * a.L + t0 + r) * a.H + h) * a.P + p] : Tin(0);
         }
     };
     auto stage = [&]() {
 #pragma unroll
         for (int i = 0; i < NPC; ++i) {
             const int id = tid + i * kT, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-            stage8<true>(sm.K[0][r], kC * kRow, n0, st.k[i]);
-            stage8<true>(sm.Q[0][r], kC * kRow, n0, st.q[i]);
+            stage8<true>(sm.K[0][r], kC * kRow, n0, sk[i]);
+            if constexpr (!KEEP) stage8<true>(sm.Q[0][r], kC * kRow, n0, sq[i]);
         }
 #pragma unroll
         for (int i = 0; i < NTR; ++i) {
@@ -127,18 +130,21 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const f
                 int tb, sb;
                 lower_tile(id >> 6, tb, sb);
                 const int f = frag(tb, sb >> 1), e = 4 * (sb & 1);
-                const float tv[4] = {st.t[i].x, st.t[i].y, st.t[i].z, st.t[i].w};
-                const float av[4] = {st.am[i].x, st.am[i].y, st.am[i].z, st.am[i].w};
-                uint2 tp[3], ap[OL];
+                const float tv[4] = {stt[i].x, stt[i].y, stt[i].z, stt[i].w};
+                uint2 tp[3];
                 split4<3>(tv, tp);
-                split4<OL>(av, ap);
 #pragma unroll
                 for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2*>(&sm.T.p[x][f][id & 63][e]) = tp[x];
+                if constexpr (!KEEP) {
+                    const float av[4] = {sa[i].x, sa[i].y, sa[i].z, sa[i].w};
+                    uint2 ap[OL];
+                    split4<OL>(av, ap);
 #pragma unroll
-                for (int x = 0; x < OL; ++x) *reinterpret_cast<uint2*>(&sm.A.p[x][f][id & 63][e]) = ap[x];
+                    for (int x = 0; x < OL; ++x) *reinterpret_cast<uint2*>(&sm.A.p[x][f][id & 63][e]) = ap[x];
+                }
             }
         }
-        if (tid < 48) *reinterpret_cast<float4*>(&sm.gam[4 * tid]) = st.gate;   // gam, tail, beta in a row
+        if (tid < 48) *reinterpret_cast<float4*>(&sm.gam[4 * tid]) = sgate;   // gam, tail, beta in a row
     };
     // the zero blocks above the diagonal inside fragments 0 and 3, written once
     for (int i = tid; i < 128; i += kT) {
@@ -146,8 +152,10 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const f
         const uint2 z = make_uint2(0, 0);
 #pragma unroll
         for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2*>(&sm.T.p[x][f][i & 63][4]) = z;
+        if constexpr (!KEEP) {
 #pragma unroll
-        for (int x = 0; x < OL; ++x) *reinterpret_cast<uint2*>(&sm.A.p[x][f][i & 63][4]) = z;
+            for (int x = 0; x < OL; ++x) *reinterpret_cast<uint2*>(&sm.A.p[x][f][i & 63][4]) = z;
+        }
     }
     if (mine > 0) {
         fetch(0);
@@ -158,7 +166,7 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const f
         const int64_t t0 = c * kC;
         float v[16];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = io::ld(&st.v[i]);
+        for (int i = 0; i < 16; ++i) v[i] = io::ld(&sv[i]);
         if (c + 1 < mine) fetch(c + 1);
         if (active) {
             bf16x8 Sp[KS][3];
@@ -193,30 +201,39 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const f
                     U[tb] = mm<3>(t, Bp[ks], U[tb]);
                 }
             }
-            // y
-            split_tiles<3>(U[0], U[1], Bp[0]);
-            split_tiles<3>(U[2], U[3], Bp[1]);
+            if constexpr (KEEP) {
+                float* ku = keep_u + (bh * nch + c) * kC * pad + p;
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {
-                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+                for (int i = 0; i < 16; ++i) ku[(16 * (i >> 2) + 4 * lg + (i & 3)) * pad] = U[i >> 2][i & 3];
+                float* ks = keep_s + ((bh * nch + c) * pad + p) * NP + 4 * lg;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    bf16x8 x[NK];
+                for (int i = 0; i < NB; ++i) *reinterpret_cast<f32x4*>(ks + 16 * i) = S[i];
+            } else {
+                // y
+                split_tiles<3>(U[0], U[1], Bp[0]);
+                split_tiles<3>(U[2], U[3], Bp[1]);
 #pragma unroll
-                    for (int i = 0; i < NK; ++i) x[i] = ld8(&sm.Q[i][16 * tb + li][32 * ks + 8 * lg]);
-                    acc = mm<OL>(x, Sp[ks], acc);
-                }
-                acc *= *reinterpret_cast<const f32x4*>(&sm.gam[16 * tb + 4 * lg]);
+                for (int tb = 0; tb < 4; ++tb) {
+                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int ks = 0; ks <= tb / 2; ++ks) {
-                    bf16x8 x[OL];
-                    ld_frag(sm.A, frag(tb, ks), lane, x);
-                    acc = mm<OL>(x, Bp[ks], acc);
-                }
+                    for (int ks = 0; ks < KS; ++ks) {
+                        bf16x8 x[NK];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int64_t t = t0 + 16 * tb + 4 * lg + q;
-                    if (pok && t < a.L) io::st(Yg + ((b * a.L + t) * a.H + h) * a.P + p, a.scale * acc[q]);
+                        for (int i = 0; i < NK; ++i) x[i] = ld8(&sm.Q[i][16 * tb + li][32 * ks + 8 * lg]);
+                        acc = mm<OL>(x, Sp[ks], acc);
+                    }
+                    acc *= *reinterpret_cast<const f32x4*>(&sm.gam[16 * tb + 4 * lg]);
+#pragma unroll
+                    for (int ks = 0; ks <= tb / 2; ++ks) {
+                        bf16x8 x[OL];
+                        ld_frag(sm.A, frag(tb, ks), lane, x);
+                        acc = mm<OL>(x, Bp[ks], acc);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int64_t t = t0 + 16 * tb + 4 * lg + q;
+                        if (pok && t < a.L) io::st(Yg + ((b * a.L + t) * a.H + h) * a.P + p, a.scale * acc[q]);
+                    }
                 }
             }
             // the next state
@@ -241,7 +258,7 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const f
         if (c + 1 < mine) stage();
         __syncthreads();
     }
-    if (pok) {
+    if (!KEEP && pok) {
         for (int64_t t = mine * kC + lg; t < a.L; t += 4) io::st(Yg + ((b * a.L + t) * a.H + h) * a.P + p, 0.0f);
         if (a.last) {
 #pragma unroll
@@ -255,22 +272,25 @@ __global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const f
     }
 }
 
-template <typename Tin, typename Tout, int NP, int W>
-hipError_t launch(const DeltaArgs& a, const float* recs, hipStream_t stream) {
-    constexpr int bytes = (int)sizeof(ScanSmem<Tin, NP, sizeof(Tout) == 2 ? 2 : 3>);
-    const auto kern = &delta_scan_kernel<Tin, Tout, NP, W>;
+template <typename Tin, typename Tout, int NP, bool KEEP>
+hipError_t launch(const DeltaArgs& a, const float* recs, float* keep_s, float* keep_u, int pad, hipStream_t stream) {
+    constexpr int W = 4;
+    constexpr int bytes = (int)sizeof(ScanSmem<Tin, NP, KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3>);
+    const auto kern = &delta_scan_kernel<Tin, Tout, NP, W, KEEP>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     const int npb = (int)((a.P + 16 * W - 1) / (16 * W));
     const int64_t units = (a.batch * a.H + 7) / 8 * 8;
-    KTime kt("delta_scan", stream);
-    hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(64 * W), bytes, stream, a, recs, delta_chunks(a.L), npb);
+    KTime kt(KEEP ? "delta_keep" : "delta_scan", stream);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(64 * W), bytes, stream, a, recs, delta_chunks(a.L), npb,
+                       keep_s, keep_u, pad);
     return hipGetLastError();
 }
 
 template <typename Tin, typename Tout>
 hipError_t by_n(const DeltaArgs& a, const float* recs, hipStream_t stream) {
-    return a.N <= 64 ? launch<Tin, Tout, 64, 4>(a, recs, stream) : launch<Tin, Tout, 128, 4>(a, recs, stream);
+    return a.N <= 64 ? launch<Tin, Tout, 64, false>(a, recs, nullptr, nullptr, 0, stream)
+                     : launch<Tin, Tout, 128, false>(a, recs, nullptr, nullptr, 0, stream);
 }
 
 }  // namespace
@@ -278,6 +298,14 @@ hipError_t by_n(const DeltaArgs& a, const float* recs, hipStream_t stream) {
 hipError_t launch_delta_scan(const DeltaArgs& a, int in_bf16, int out_bf16, const float* recs, hipStream_t stream) {
     if (in_bf16) return out_bf16 ? by_n<uint16_t, uint16_t>(a, recs, stream) : by_n<uint16_t, float>(a, recs, stream);
     return out_bf16 ? by_n<float, uint16_t>(a, recs, stream) : by_n<float, float>(a, recs, stream);
+}
+
+hipError_t launch_delta_keep(const DeltaArgs& a, int in_bf16, const float* recs, float* keep_s, float* keep_u, int pad,
+                             hipStream_t stream) {
+    if (in_bf16) return a.N <= 64 ? launch<uint16_t, float, 64, true>(a, recs, keep_s, keep_u, pad, stream)
+                                  : launch<uint16_t, float, 128, true>(a, recs, keep_s, keep_u, pad, stream);
+    return a.N <= 64 ? launch<float, float, 64, true>(a, recs, keep_s, keep_u, pad, stream)
+                     : launch<float, float, 128, true>(a, recs, keep_s, keep_u, pad, stream);
 }
 
 }  // namespace selscan

@@ -225,6 +225,29 @@ size_t delta_record_bytes();
 hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, float* recs, hipStream_t stream);
 hipError_t launch_delta_scan(const DeltaArgs& a, int in_bf16, int out_bf16, const float* recs, hipStream_t stream);
 
+// Gradients of the gated delta rule; the arrays below dh0 are workspace
+// (delta_bwd_carve).  f.y and f.last are unused.
+struct DeltaBwdArgs {
+    DeltaArgs f;
+    const void* dout;
+    const float* dlast;       // NULL = zero
+    void *dq, *dk, *dv;
+    float *dg, *dbeta, *dh0;
+    float* recs;
+    float* S;                 // [chunks, pad, NP] state entering each chunk (NP: N rounded up to 64 or 128)
+    float* D;                 // [chunks, pad, NP] adjoint of the state leaving it
+    float* U;                 // [chunks, 64, pad]
+    float* dR;                // [chunks, 64, pad]
+    float *pq, *pk;           // [batch, L, H, N] per-head dq and dk when heads share q and k, else NULL
+    int pad;                  // P rounded up to 32
+    int vec_p;                // rows of v and dout on 16-byte boundaries, P % 8 == 0
+};
+size_t delta_bwd_bytes(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N);
+void delta_bwd_carve(DeltaBwdArgs& a, void* ws);
+hipError_t launch_delta_keep(const DeltaArgs& a, int in_bf16, const float* recs, float* keep_s, float* keep_u, int pad,
+                             hipStream_t stream);
+hipError_t launch_delta_bwd(const DeltaBwdArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
+
 // Layer norm with dropout and residual sum in front.
 struct NormArgs {
     const void* x;            // forward: x; gradients: dy

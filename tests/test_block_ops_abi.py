@@ -97,3 +97,21 @@ def test_norm_null():
                                     None) == ss.ERR_INVALID_ARG
     assert L.selscan_layer_norm_bwd(ctypes.byref(s), FAKE, FAKE, None, FAKE, FAKE, None, None, None, None, None,
                                     None) == ss.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("field,value,status", BAD_DELTA + [("seqlen", 0, ss.ERR_INVALID_ARG),
+                                                            ("headdim", 1 << 21, ss.ERR_UNSUPPORTED)])
+def test_delta_bwd_bad_shape(field, value, status):
+    s = _delta(**{field: value})
+    r = ss.lib().selscan_delta_bwd(ctypes.byref(s), FAKE, FAKE, FAKE, FAKE, FAKE, 1.0, None, None, FAKE, None, FAKE,
+                                   FAKE, FAKE, FAKE, FAKE, None, None)
+    assert r == status and ss.last_error()
+    assert ss.lib().selscan_delta_bwd_workspace_bytes(ctypes.byref(s)) == 0
+
+
+@pytest.mark.parametrize("missing", [0, 4, 8, 10, 14])
+def test_delta_bwd_null(missing):
+    s = _delta()
+    a = [FAKE] * 5 + [1.0, None, None, FAKE, None] + [FAKE] * 5 + [None, None]
+    a[missing] = None
+    assert ss.lib().selscan_delta_bwd(ctypes.byref(s), *a) == ss.ERR_INVALID_ARG

@@ -198,3 +198,126 @@ def test_python_refusals(gpu):
         ss.delta_fwd(**i, lengths=torch.tensor([8], device=DEV))
     with pytest.raises(ValueError):
         ss.delta_fwd(**{n: x.cpu() for n, x in i.items()})
+
+
+def grads(i, dout, dlast=None, **kw):
+    want = ref.delta_bwd(**i, dout=dout, dlast=dlast, scale=kw.get("scale"),
+                         lengths=None if kw.get("lengths") is None else host(kw["lengths"]).tolist())
+    got = ss.delta_bwd(**i, dout=dout, dlast_state=dlast, want_dh0=True, **kw)
+    torch.cuda.synchronize()
+    return got, want
+
+
+def check_grads(got, want):
+    assert set(got) == set(want)
+    for n in got:
+        # (a gradient that is zero everywhere is exactly zero)
+        close(got[n], want[n], n)
+
+
+def douts(B, L, H, P, N, dtype, seed):
+    g = torch.Generator().manual_seed(1000 + seed)
+    return torch.randn((B, L, H, P), generator=g).to(dtype).to(DEV), torch.randn((B, H, P, N), generator=g).to(DEV)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, BF16), (BF16, F32), (F32, BF16)])
+def test_bwd_matches_oracle(gpu, shape, types):
+    B, L, H, G, P, N = shape
+    i = inputs(*shape, types[0], seed=sum(shape), h0=True)
+    dout, dlast = douts(B, L, H, P, N, types[1], sum(shape))
+    got, want = grads(i, dout, dlast)
+    for n in ("dq", "dk", "dv"):
+        assert got[n].dtype == types[0]
+    check_grads(got, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_bwd_from_zero_without_dlast(gpu, dtype):
+    i = inputs(1, 1, 2, 1, 24, 40, dtype, seed=31)
+    dout, _ = douts(1, 1, 2, 24, 40, dtype, 31)
+    got, want = grads(i, dout)
+    assert not host(got["dg"]).any()   # one token from a zero state: nothing decays
+    check_grads(got, want)
+    i = inputs(2, 70, 2, 1, 24, 40, dtype, seed=32)
+    dout, _ = douts(2, 70, 2, 24, 40, dtype, 32)
+    got = ss.delta_bwd(**i, dout=dout, scale=0.5)
+    assert "dh0" not in got
+    want = ref.delta_bwd(**i, dout=dout, scale=0.5)
+    check_grads(got, {n: want[n] for n in got})
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_bwd_lengths(gpu, dtype):
+    L, lengths = 150, [150, 0, 1, 64, 65, 149, 999, -3]
+    i = inputs(8, L, 4, 2, 40, 48, dtype, seed=33, h0=True)
+    dout, dlast = douts(8, L, 4, 40, 48, dtype, 33)
+    for b, m in enumerate(lengths):
+        dout[b, max(m, 0):] = float("nan")
+        for name in ("q", "k", "v", "g", "beta"):
+            i[name][b, max(m, 0):] = float("nan")
+    got, want = grads(i, dout, dlast, lengths=torch.tensor(lengths, dtype=torch.int32, device=DEV))
+    check_grads(got, want)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("low", [float("-inf"), torch.finfo(F32).min, -200.0])
+def test_bwd_decay_of_zero(gpu, dtype, low):
+    i = inputs(2, 140, 2, 2, 32, 64, dtype, seed=34, h0=True, strong=True)
+    i["g"][0, 70] = low
+    i["g"][1, [0, 63, 64, 100, 101]] = low
+    dout, dlast = douts(2, 140, 2, 32, 64, dtype, 34)
+    got, want = grads(i, dout, dlast)
+    check_grads(got, want)
+    assert not host(got["dg"])[0, 70].any() and not host(got["dh0"])[1].any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_bwd_hard_keys(gpu, dtype):
+    """Write strengths of exactly 0 and 1 on equal keys."""
+    i = inputs(1, 130, 1, 1, 32, 64, dtype, seed=35)
+    i["k"][:] = i["k"][:, :1]
+    i["g"].zero_()
+    i["beta"][:, :50] = 1.0
+    i["beta"][:, 50:80] = 0.0
+    dout, dlast = douts(1, 130, 1, 32, 64, dtype, 35)
+    check_grads(*grads(i, dout, dlast))
+
+
+def test_bwd_matches_differences(gpu):
+    """The gradient along random directions against central differences of
+    the fp32 forward call."""
+    i = inputs(1, 100, 2, 1, 32, 40, F32, seed=36, h0=True)
+    dout, dlast = douts(1, 100, 2, 32, 40, F32, 36)
+    got = ss.delta_bwd(**i, dout=dout, dlast_state=dlast)
+
+    def loss(x):
+        y, s = ss.delta_fwd(**x)
+        return float((y.double() * dout).sum() + (s.double() * dlast).sum())
+
+    g = torch.Generator().manual_seed(3)
+    e = 1e-2
+    for n in i:
+        d = torch.randn(i[n].shape, generator=g).to(DEV) * i[n].square().mean().sqrt()
+        num = (loss({**i, n: i[n] + e * d}) - loss({**i, n: i[n] - e * d})) / (2 * e)
+        ana = float((got["d" + n].double() * d).sum())
+        # e^2 of the third derivative and fp32 rounding of the loss over 2 e
+        scale = float(got["d" + n].double().norm() * d.double().norm()) / d.numel() ** 0.5
+        assert abs(num - ana) <= 2e-2 * abs(ana) + 2e-2 * scale * 3, n
+
+
+def test_bwd_reproducible_stream_workspace(gpu):
+    i = inputs(2, 200, 4, 2, 64, 128, BF16, seed=37)
+    dout, dlast = douts(2, 200, 4, 64, 128, BF16, 37)
+    a = ss.delta_bwd(**i, dout=dout, dlast_state=dlast)
+    need = ss.delta_bwd_workspace_bytes(2, 200, 4, 64, 2, 128)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)   # (NaN where it is read before it is written)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b = ss.delta_bwd(**i, dout=dout, dlast_state=dlast, workspace=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a[n], b[n]) for n in a)
+    with pytest.raises(ss.SelscanError) as err:
+        ss.delta_bwd(**i, dout=dout, workspace=ws[:need - 256])
+    assert err.value.status == ss.ERR_WORKSPACE
