@@ -28,6 +28,9 @@ selscan_status_t check_shape(const selscan_m2_shape_t* s) {
         mul_checked({s->batch, s->seqlen, s->ngroups, s->dstate, 4}) < 0 ||
         mul_checked({s->batch, s->nheads, s->headdim, s->dstate, 4}) < 0)
         return set_error(SELSCAN_ERR_INVALID_ARG, "tensor sizes overflow 64-bit byte counts");
+    // the chunked form's offsets inside 64 tokens are 32-bit
+    if (s->nheads * s->headdim > (int64_t(1) << 22) || s->ngroups > (int64_t(1) << 15))
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "the gated delta rule supports nheads headdim <= 2^22 and ngroups <= 2^15");
     // 16 rows of a state per workgroup of the token-by-token kernel, a chunk per workgroup of the chunked form
     if (mul_checked({s->batch, s->nheads, s->headdim}) / 16 >= 0x7fffff00 ||
         mul_checked({s->batch, s->nheads, selscan::delta_chunks(s->seqlen)}) >= 0x7fffff00)
@@ -43,17 +46,41 @@ bool vec4(const selscan_m2_shape_t* s, const void* q, const void* k) {
 // Sequences longer than this take the chunked form.
 constexpr int64_t kRecTokens = 16;
 
+// Padded copies of q and k, which rows that are not made of 16-byte pieces take.
+size_t pad_bytes(const selscan_m2_shape_t* s) {
+    return align256((size_t)(s->batch * s->seqlen * s->ngroups) * 2 * (s->dstate <= 64 ? 64 : 128) *
+                    (s->in_dtype == SELSCAN_BF16 ? 2 : 4));
+}
+
+size_t record_bytes(const selscan_m2_shape_t* s) {
+    return align256((size_t)(s->batch * s->nheads * selscan::delta_chunks(s->seqlen)) * selscan::delta_record_bytes(false));
+}
+
 size_t fwd_bytes(const selscan_m2_shape_t* s) {
     if (s->seqlen <= kRecTokens) return 0;
-    return align256((size_t)(s->batch * s->nheads * selscan::delta_chunks(s->seqlen)) * selscan::delta_record_bytes());
+    return record_bytes(s) + (s->dstate % 8 ? pad_bytes(s) : 0);
+}
+
+// The copies' place: after the call's other workspace when N asks for them
+// whatever the addresses, else (q or k off a 16-byte boundary) their own.
+selscan_status_t pad_rows(selscan::DeltaArgs& a, const selscan_m2_shape_t* s, char* after, Scratch& own, hipStream_t hs) {
+    a.NL = a.N;
+    a.qk_row = a.N;
+    if (a.N % 8 == 0) {
+        if (aligned16(a.q) && aligned16(a.k)) return SELSCAN_OK;
+        const selscan_status_t st = own.get(nullptr, 0, pad_bytes(s), hs);
+        if (st != SELSCAN_OK) return st;
+        after = static_cast<char*>(own.ptr);
+    }
+    const hipError_t e = selscan::launch_delta_pad(a, s->in_dtype == SELSCAN_BF16, after, hs);
+    if (e != hipSuccess)
+        return set_error(SELSCAN_ERR_LAUNCH, std::string("kernel launch failed: ") + hipGetErrorString(e));
+    return SELSCAN_OK;
 }
 
 selscan_status_t check_bwd_shape(const selscan_m2_shape_t* s) {
     selscan_status_t st = check_shape(s);
     if (st != SELSCAN_OK) return st;
-    // the kept states and columns are sized by 64-token chunks and P rounded up to 32
-    if (s->headdim > (int64_t(1) << 20))
-        return set_error(SELSCAN_ERR_UNSUPPORTED, "gradients of the gated delta rule support headdim <= 2^20");
     if (mul_checked({s->batch, s->nheads, selscan::delta_chunks(s->seqlen), (s->headdim + 31) / 32 * 32, 128, 16}) < 0 ||
         mul_checked({s->batch, s->seqlen, s->nheads, s->dstate, 16}) < 0)
         return set_error(SELSCAN_ERR_INVALID_ARG, "workspace size overflows 64-bit byte counts");
@@ -62,9 +89,11 @@ selscan_status_t check_bwd_shape(const selscan_m2_shape_t* s) {
     return SELSCAN_OK;
 }
 
-size_t bwd_bytes(const selscan_m2_shape_t* s) {
+size_t bwd_main_bytes(const selscan_m2_shape_t* s) {
     return selscan::delta_bwd_bytes(s->batch, s->seqlen, s->nheads, s->ngroups, s->headdim, s->dstate);
 }
+
+size_t bwd_bytes(const selscan_m2_shape_t* s) { return bwd_main_bytes(s) + (s->dstate % 8 ? pad_bytes(s) : 0); }
 
 selscan_status_t launched(hipError_t e) {
     if (e != hipSuccess)
@@ -105,12 +134,15 @@ selscan_status_t selscan_delta_fwd(const selscan_m2_shape_t* s, const void* q, c
         Scratch ws;
         st = ws.get(s->workspace, s->workspace_bytes, fwd_bytes(s), hs);
         if (st != SELSCAN_OK) return st;
-        a.vec = s->dstate % 8 == 0 && aligned16(q) && aligned16(k);
+        Scratch pad;
         float* recs = static_cast<float*>(ws.ptr);
-        hipError_t e = selscan::launch_delta_prep(a, in_bf16, recs, hs);
-        if (e == hipSuccess) e = selscan::launch_delta_scan(a, in_bf16, out_bf16, recs, hs);
+        st = pad_rows(a, s, static_cast<char*>(ws.ptr) + record_bytes(s), pad, hs);
+        hipError_t e = hipSuccess;
+        if (st == SELSCAN_OK) e = selscan::launch_delta_prep(a, in_bf16, false, recs, hs);
+        if (st == SELSCAN_OK && e == hipSuccess) e = selscan::launch_delta_scan(a, in_bf16, out_bf16, recs, hs);
+        pad.release();
         ws.release();
-        return launched(e);
+        return st != SELSCAN_OK ? st : launched(e);
     } catch (...) {
         return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
     }
@@ -142,13 +174,17 @@ selscan_status_t selscan_delta_bwd(const selscan_m2_shape_t* s, const void* q, c
         a.f.q = q; a.f.k = k; a.f.v = v; a.f.g = g; a.f.beta = beta; a.f.lengths = lengths; a.f.h0 = h0;
         a.f.batch = s->batch; a.f.L = s->seqlen; a.f.H = s->nheads; a.f.P = s->headdim; a.f.G = s->ngroups;
         a.f.N = (int)s->dstate; a.f.scale = scale;
-        a.f.vec = s->dstate % 8 == 0 && aligned16(q) && aligned16(k);
-        a.vec_p = s->headdim % 8 == 0 && aligned16(v) && aligned16(dout);
+        a.vec_p = s->headdim % 8 == 0 && aligned16(dout);
         a.dout = dout; a.dlast = dlast_state; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0;
         selscan::delta_bwd_carve(a, ws.ptr);
-        const hipError_t e = selscan::launch_delta_bwd(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16, hs);
+        Scratch pad;
+        st = pad_rows(a.f, s, static_cast<char*>(ws.ptr) + bwd_main_bytes(s), pad, hs);
+        hipError_t e = hipSuccess;
+        if (st == SELSCAN_OK)
+            e = selscan::launch_delta_bwd(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16, hs);
+        pad.release();
         ws.release();
-        return launched(e);
+        return st != SELSCAN_OK ? st : launched(e);
     } catch (...) {
         return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
     }

@@ -19,7 +19,7 @@
 // Row and column sums are taken of the same Z and, like the dots, in fp64:
 // where a key is written over, dg is a small difference of these sums.  Five kernels: the records (delta_prep.hip), the
 // scan that keeps every S and U (delta_scan.hip), the scan back over the
-// chunks that makes D, dR and dV (a wave per 16 value columns, as forward),
+// chunks that makes D, dR and dV (16 value columns a workgroup, as forward),
 // the gradients that are local to a chunk (all chunks at once), and, where
 // heads share q and k, their sum over the heads in a fixed order.  All
 // products are fp32-grade except those that go into a bf16 dq or dk alone.
@@ -32,232 +32,245 @@ namespace {
 using namespace dchunk;
 
 // ------------------------------------------------------------ the scan back
-template <typename Tin, int NP>
+// Waves share the work as in delta_scan.hip: wave w has dU, dR and dV of the
+// tokens 16 w .. 16 w + 15 and a quarter of D's rows.
+template <typename Tin, typename Tdo, int NP, int CT>
 struct BackSmem {
     static constexpr int kRow = NP + 8;
-    float gam[kC], tail[kC], beta[kC];
-    uint16_t K[kPlanes<Tin>][kC][kRow];   // columns through kperm
+    uint16_t K[kPlanes<Tin>][kC][kRow];
     uint16_t Q[kPlanes<Tin>][kC][kRow];
-    Frags<3> T, A;                        // transposed
+    Operands<NP / 32, 3> D[CT];
+    Operands<2, kPlanes<Tdo>> O[CT];         // dout
+    Operands<2, 3> U[CT], R[CT], G[CT];      // dU; -beta e^cum dR; e^cum dO
 };
 
-template <typename Tin, typename Tdo, int NP, int W>
-__global__ __launch_bounds__(64 * W) void delta_back_kernel(DeltaBwdArgs ba, int64_t nch, int npb) {
+template <typename Tin, typename Tdo, int NP, int CT>
+__global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_t nch, int npb) {
     constexpr int NK = kPlanes<Tin>, NO = kPlanes<Tdo>;
-    constexpr int kRow = BackSmem<Tin, NP>::kRow;
-    constexpr int NB = NP / 16, KS = NP / 32;
-    constexpr int kT = 64 * W;
-    constexpr int NPC = kC * (NP / 8) / kT;
-    constexpr int NTR = (kBlocks * 64 + kT - 1) / kT;
+    constexpr int ES = (int)sizeof(Tin), EO = (int)sizeof(Tdo);
+    constexpr int kRow = BackSmem<Tin, Tdo, NP, CT>::kRow;
+    constexpr int KS = NP / 32, NT = NP / 64, NPC = NP / 32;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
-    auto& sm = *reinterpret_cast<BackSmem<Tin, NP>*>(smem_raw);
+    auto& sm = *reinterpret_cast<BackSmem<Tin, Tdo, NP, CT>*>(smem_raw);
     const DeltaArgs& a = ba.f;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
-    const int64_t j = blockIdx.x / 8;
-    const int64_t bh = (j / npb) * 8 + blockIdx.x % 8;
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int jx = blockIdx.x / 8;
+    const int64_t bh = (int64_t)(jx / npb) * 8 + blockIdx.x % 8;
     if (bh >= a.batch * a.H) return;
     const int64_t b = bh / a.H, h = bh - b * a.H, grp = h / (a.H / a.G);
     const int64_t len = seq_len(a, b);
-    const int64_t mine = (len + kC - 1) / kC;
-    const int64_t p0 = (int64_t)(j % npb) * 16 * W + 16 * wave;
-    const int64_t p = p0 + li;
-    const int pad = ba.pad;
-    const bool active = p0 < pad, pok = p < a.P;
-    const int N = a.N;
-    const Tin* Kg = reinterpret_cast<const Tin*>(a.k);
-    const Tin* Qg = reinterpret_cast<const Tin*>(a.q);
-    const Tdo* Og = reinterpret_cast<const Tdo*>(ba.dout);
-    Tin* dVg = reinterpret_cast<Tin*>(ba.dv);
+    const int mine = (int)((len + kC - 1) / kC);
+    const int N = a.N, P = (int)a.P, pad = ba.pad;
+    const int p0 = (jx % npb) * 16 * CT + li;
+    const int64_t sk = a.G * a.qk_row * ES, sv = a.H * P * ES, so = a.H * P * EO;
+    const char* Kg = static_cast<const char*>(a.k) + b * a.L * sk + grp * a.qk_row * ES;
+    const char* Qg = static_cast<const char*>(a.q) + b * a.L * sk + grp * a.qk_row * ES;
+    const char* Og = static_cast<const char*>(ba.dout) + b * a.L * so + h * P * EO;
+    char* dVg = static_cast<char*>(ba.dv) + b * a.L * sv + h * P * ES;
 
-    f32x4 D[NB];
+    f32x4 D[NT][CT];
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int n = 16 * i + 4 * lg + q;
-            D[i][q] = ba.dlast && pok && n < N ? ba.dlast[(bh * a.P + p) * N + n] : 0.0f;
-        }
-
-    struct Stage {
-        Raw8<Tin> k[NPC], q[NPC];
-        float t[NTR][4], am[NTR][4];
-        float4 gate;
-        Tdo o[16];
-    } st;
-    auto fetch = [&](int64_t c) {
-        const int64_t t0 = c * kC;
-        const int live = (int)min((int64_t)kC, len - t0);
-        const float* rec = ba.recs + (bh * nch + c) * kRec;
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int i = 0; i < NPC; ++i) {
-            const int id = tid + i * kT, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-            if (r < live) {
-                const int64_t row = ((b * a.L + t0 + r) * a.G + grp) * N;
-                fetch8(Kg + row, n0, N, a.vec, st.k[i]);
-                fetch8(Qg + row, n0, N, a.vec, st.q[i]);
-            } else {
-                zero(st.k[i]);
-                zero(st.q[i]);
+            for (int q = 0; q < 4; ++q) {
+                const int n = 16 * (NT * w + i) + 4 * lg + q, p = p0 + 16 * ct;
+                D[i][ct][q] = ba.dlast && p < P && n < N ? ba.dlast[(bh * P + p) * N + n] : 0.0f;
             }
-        }
+    auto put_state = [&]() {
 #pragma unroll
-        for (int i = 0; i < NTR; ++i) {
-            const int id = tid + i * kT;
-            if (id < kBlocks * 64) {   // lane li is a column of the block, four rows down from 4 lg
-                const int o = (id >> 6) * 256 + ((id >> 4) & 3) * 64 + (id & 15);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    st.t[i][q] = rec[kRecT + o + 16 * q];
-                    st.am[i][q] = rec[kRecA + o + 16 * q];
-                }
-            }
-        }
-        if (tid < 48) st.gate = *reinterpret_cast<const float4*>(rec + kRecGam + 4 * tid);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = 16 * (i >> 2) + 4 * lg + (i & 3);
-            st.o[i] = pok && r < live ? Og[((b * a.L + t0 + r) * a.H + h) * a.P + p] : Tdo(0);
+        for (int ct = 0; ct < CT; ++ct) {
+            if constexpr (NT == 2) sm.D[ct].put(w, D[0][ct], D[1][ct], lane);
+            else sm.D[ct].put_tile(w, D[0][ct], lane);
         }
     };
-    auto stage = [&]() {
+    int koff[NPC], roff, voff[CT], ooff[CT];
 #pragma unroll
-        for (int i = 0; i < NPC; ++i) {
-            const int id = tid + i * kT, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-            stage8<true>(sm.K[0][r], kC * kRow, n0, st.k[i]);
-            stage8<true>(sm.Q[0][r], kC * kRow, n0, st.q[i]);
-        }
-#pragma unroll
-        for (int i = 0; i < NTR; ++i) {
-            const int id = tid + i * kT;
-            if (id < kBlocks * 64) {
-                int tb, sb;
-                lower_tile(id >> 6, tb, sb);
-                const int f = frag_t(sb, tb >> 1), e = 4 * (tb & 1);
-                uint2 tp[3], ap[3];
-                split4<3>(st.t[i], tp);
-                split4<3>(st.am[i], ap);
-#pragma unroll
-                for (int x = 0; x < 3; ++x) {
-                    *reinterpret_cast<uint2*>(&sm.T.p[x][f][id & 63][e]) = tp[x];
-                    *reinterpret_cast<uint2*>(&sm.A.p[x][f][id & 63][e]) = ap[x];
-                }
-            }
-        }
-        if (tid < 48) *reinterpret_cast<float4*>(&sm.gam[4 * tid]) = st.gate;
-    };
-    // the zero blocks inside fragments 2 and 5 (row blocks 1 and 3), written once
-    for (int i = tid; i < 128; i += kT) {
-        const int f = i < 64 ? 2 : 5;
-#pragma unroll
-        for (int x = 0; x < 3; ++x) {
-            *reinterpret_cast<uint2*>(&sm.T.p[x][f][i & 63][0]) = make_uint2(0, 0);
-            *reinterpret_cast<uint2*>(&sm.A.p[x][f][i & 63][0]) = make_uint2(0, 0);
-        }
+    for (int i = 0; i < NPC; ++i) {
+        const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+        koff[i] = n0 < a.NL ? r * (int)sk + n0 * ES : kOut;
     }
+    roff = (16 * w + li) * (int)sk + 4 * lg * ES;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        const int p = p0 + 16 * ct;
+        voff[ct] = p < P ? (16 * w + 4 * lg) * (int)sv + p * ES : kOut;
+        ooff[ct] = p < P ? (16 * w + 4 * lg) * (int)so + p * EO : kOut;
+    }
+
+    int toff[4];   // rows 16 w .. of the transposed matrices: blocks (t, w); above the diagonal none, zeros
+#pragma unroll
+    for (int t = 0; t < 4; ++t) toff[t] = t >= w ? (block_at(t, w) + li * 16 + 4 * lg) * 4 : kOut;
+
+    Raw8<Tin> fk[NPC], fq[NPC], fr[KS];
+    f32x4 ft[4], fa[4], fgate[3];
+    float fgl;
+    Tdo fo[CT][4];
+    auto fetch = [&](int c) {
+        const int64_t t0 = (int64_t)c * kC;
+        const int live = (int)min((int64_t)kC, len - t0);
+        const auto kb = rows_buf(Kg + t0 * sk, live, sk, a.NL * ES);
+        const auto qb = rows_buf(Qg + t0 * sk, live, sk, a.NL * ES);
+        const auto ob = rows_buf(Og + t0 * so, live, so, P * EO);
+        const auto rb = rows_buf(ba.recs + (bh * nch + c) * kRecGrad, 1, 0, kRecGrad * 4);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) fo[ct][q] = buf_raw<Tdo>(ob, ooff[ct] + q * (int)so);
+#pragma unroll
+        for (int i = 0; i < 3; ++i) fgate[i] = buf_ld4(rb, (kRecGam + i * kC + 16 * w + 4 * lg) * 4);
+        fgl = buf_raw<float>(rb, (kRecGam + kC - 1) * 4);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) fetch_row(kb, roff + 32 * ks * ES, fr[ks]);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+            fa[t] = buf_ld4(rb, toff[t] + kRecAt * 4);
+            ft[t] = buf_ld4(rb, toff[t] + kRecTt * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < NPC; ++i) {
+            fetch8(kb, koff[i], fk[i]);
+            fetch8(qb, koff[i], fq[i]);
+        }
+    };
+    bf16x8 Kr[KS][NK], T[2][3], A[2][3];
+    f32x4 gam, tail, beta, o[CT];
+    float gl;
+    auto ready = [&]() {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            if (a.NL < NP) {
+                const int n = 32 * ks + 4 * lg;
+                keep_row(fr[ks], n < a.NL, n + 16 < a.NL);
+            }
+            to_operand(fr[ks], Kr[ks]);
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            split8<3>(ft[2 * ks], ft[2 * ks + 1], T[ks]);
+            split8<3>(fa[2 * ks], fa[2 * ks + 1], A[ks]);
+        }
+        gam = fgate[0];
+        tail = fgate[1];
+        beta = fgate[2];
+        gl = fgl;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            o[ct] = widen(fo[ct]);
+            sm.O[ct].put_tile(w, o[ct], lane);
+        }
+    };
+
+    put_state();
     if (mine > 0) {
         fetch(mine - 1);
-        stage();
+        ready();
     }
-    __syncthreads();
-    for (int64_t c = mine - 1; c >= 0; --c) {
-        const int64_t t0 = c * kC;
-        float o[16];
+    lds_barrier();
+    for (int c = mine - 1; c >= 0; --c) {
+        const int64_t t0 = (int64_t)c * kC;
+        const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = io::ld(&st.o[i]);
-        // (fp32 inputs: the pieces would not fit beside the tiles, so they
-        // are fetched when the tiles are done with)
-        if (NK == 1 && c > 0) fetch(c - 1);
-        if (active) {
-            float* kd = ba.D + ((bh * nch + c) * pad + p) * NP + 4 * lg;
-#pragma unroll
-            for (int i = 0; i < NB; ++i) *reinterpret_cast<f32x4*>(kd + 16 * i) = D[i];
-            bf16x8 Dp[KS][3], Op[2][NO], Bp[2][3];
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) split_tiles<3>(D[2 * ks], D[2 * ks + 1], Dp[ks]);
-            f32x4 O[4], R[4];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) O[i >> 2][i & 3] = o[i];
-            split_tiles<NO>(O[0], O[1], Op[0]);
-            split_tiles<NO>(O[2], O[3], Op[1]);
-#pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {
-                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f}, au = acc;
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    bf16x8 k[NK];
-#pragma unroll
-                    for (int x = 0; x < NK; ++x) k[x] = ld8(&sm.K[x][16 * tb + li][32 * ks + 8 * lg]);
-                    acc = mm<3>(k, Dp[ks], acc);
-                }
-#pragma unroll
-                for (int ks = tb / 2; ks < 2; ++ks) {
-                    bf16x8 x[3];
-                    ld_frag(sm.A, frag_t(tb, ks), lane, x);
-                    au = mm<3>(x, Op[ks], au);
-                }
-                const f32x4 tail = *reinterpret_cast<const f32x4*>(&sm.tail[16 * tb + 4 * lg]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) R[tb][q] = __builtin_fmaf(tail[q], acc[q], a.scale * au[q]);   // dU
-            }
-            split_tiles<3>(R[0], R[1], Bp[0]);
-            split_tiles<3>(R[2], R[3], Bp[1]);
-            float* kr = ba.dR + (bh * nch + c) * kC * pad + p;
-#pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {
-                R[tb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                for (int ks = tb / 2; ks < 2; ++ks) {
-                    bf16x8 x[3];
-                    ld_frag(sm.T, frag_t(tb, ks), lane, x);
-                    R[tb] = mm<3>(x, Bp[ks], R[tb]);
-                }
-                const f32x4 gam = *reinterpret_cast<const f32x4*>(&sm.gam[16 * tb + 4 * lg]);
-                const f32x4 beta = *reinterpret_cast<const f32x4*>(&sm.beta[16 * tb + 4 * lg]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int r = 16 * tb + 4 * lg + q;
-                    kr[r * pad] = R[tb][q];
-                    R[tb][q] *= beta[q];
-                    if (pok && t0 + r < a.L) io::st(dVg + ((b * a.L + t0 + r) * a.H + h) * a.P + p, R[tb][q]);
-                    R[tb][q] *= -gam[q];
-                    O[tb][q] *= a.scale * gam[q];
-                }
-            }
-            const float gl = sm.gam[kC - 1];
-            auto down = [&](const uint16_t* m) {   // D += m^T (the tiles in Bp)
-#pragma unroll
-                for (int i = 0; i < NB; ++i)
-#pragma unroll
-                    for (int ks = 0; ks < 2; ++ks) {
-                        bf16x8 x[NK];
-#pragma unroll
-                        for (int l = 0; l < NK; ++l) x[l] = ld_down<true>(m + l * kC * kRow, kRow, 32 * ks, 16 * i, lane);
-                        D[i] = mm<3>(x, Bp[ks], D[i]);
-                    }
-            };
-#pragma unroll
-            for (int i = 0; i < NB; ++i) D[i] *= gl;
-            split_tiles<3>(R[0], R[1], Bp[0]);
-            split_tiles<3>(R[2], R[3], Bp[1]);
-            down(&sm.K[0][0][0]);
-            split_tiles<3>(O[0], O[1], Bp[0]);
-            split_tiles<3>(O[2], O[3], Bp[1]);
-            down(&sm.Q[0][0][0]);
+        for (int i = 0; i < NPC; ++i) {
+            const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+            stage8<false>(sm.K[0][r], kC * kRow, n0, fk[i]);
+            stage8<false>(sm.Q[0][r], kC * kRow, n0, fq[i]);
         }
-        if (NK == 3 && c > 0) fetch(c - 1);
-        __syncthreads();
-        if (c > 0) stage();
-        __syncthreads();
+        fetch(max(c - 1, 0));
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) sm.G[ct].put_tile(w, o[ct] * gam * a.scale, lane);
+        // dU for the wave's tokens
+        f32x4 u[CT], x[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) u[ct] = x[ct] = z4;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                bf16x8 d[3];
+                sm.D[ct].get(ks, lane, d);
+                u[ct] = mm<3>(Kr[ks], d, u[ct]);
+            }
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8 d[NO];
+                sm.O[ct].get(ks, lane, d);
+                x[ct] = mm<3>(A[ks], d, x[ct]);
+            }
+            sm.U[ct].put_tile(w, u[ct] * tail + x[ct] * a.scale, lane);
+            float* kd = ba.D + ((bh * nch + c) * pad + p0 + 16 * ct) * NP + 4 * lg;
+#pragma unroll
+            for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(kd + 16 * (NT * w + i)) = D[i][ct];
+        }
+        lds_barrier();
+        // dR and dV for the wave's tokens
+        const auto vb = rows_buf(dVg + t0 * sv, (int)min((int64_t)kC, a.L - t0), sv, P * ES);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            f32x4 r = z4;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8 y[3];
+                sm.U[ct].get(ks, lane, y);
+                r = mm<3>(T[ks], y, r);
+            }
+            const f32x4 dv = r * beta;
+            sm.R[ct].put_tile(w, -(dv * gam), lane);
+            float* kr = ba.dR + (bh * nch + c) * kC * pad + p0 + 16 * ct;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) kr[(16 * w + 4 * lg + q) * pad] = r[q];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) buf_st(vb, voff[ct] + q * (int)sv, dv[q], Tin(0));
+        }
+        lds_barrier();
+        // the wave's rows of the adjoint before the chunk
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) D[i][ct] *= gl;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 k[NT][NK], q[NT][NK];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int l = 0; l < NK; ++l) {
+                    k[i][l] = ld_down<false>(&sm.K[l][0][0], kRow, 32 * ks, 16 * (NT * w + i), lane);
+                    q[i][l] = ld_down<false>(&sm.Q[l][0][0], kRow, 32 * ks, 16 * (NT * w + i), lane);
+                }
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                bf16x8 r[3], g[3];
+                sm.R[ct].get(ks, lane, r);
+                sm.G[ct].get(ks, lane, g);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) {
+                    D[i][ct] = mm<3>(k[i], r, D[i][ct]);
+                    D[i][ct] = mm<3>(q[i], g, D[i][ct]);
+                }
+            }
+        }
+        put_state();
+        ready();
+        lds_barrier();
     }
-    if (pok) {
-        for (int64_t t = mine * kC + lg; t < a.L; t += 4) io::st(dVg + ((b * a.L + t) * a.H + h) * a.P + p, 0.0f);
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        const int p = p0 + 16 * ct;
+        if (p >= P) continue;
+        for (int64_t t = (int64_t)mine * kC + 4 * w + lg; t < a.L; t += 16)
+            io::st(reinterpret_cast<Tin*>(dVg + t * sv) + p, 0.0f);
         if (ba.dh0) {
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const int n = 16 * i + 4 * lg + q;
-                    if (n < N) ba.dh0[(bh * a.P + p) * N + n] = D[i][q];
+                    const int n = 16 * (NT * w + i) + 4 * lg + q;
+                    if (n < N) ba.dh0[(bh * P + p) * N + n] = D[i][ct][q];
                 }
         }
     }
@@ -288,6 +301,15 @@ struct GradSmem {
         } m;
     };
 };
+
+__device__ __forceinline__ void from_floats(const float (&e)[8], Raw8<uint16_t>& r) {   // (values that are bf16)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
+}
+__device__ __forceinline__ void from_floats(const float (&e)[8], Raw8<float>& r) {
+    r.lo = f32x4{e[0], e[1], e[2], e[3]};
+    r.hi = f32x4{e[4], e[5], e[6], e[7]};
+}
 
 __device__ __forceinline__ double sum16(double v) {
 #pragma unroll
@@ -332,7 +354,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
         }
         return;
     }
-    const float* rec = ba.recs + (int64_t)blockIdx.x * kRec;
+    const float* rec = ba.recs + (int64_t)blockIdx.x * kRecGrad;
     if (tid < kC) sm.cum[tid] = reinterpret_cast<const double*>(rec + kRecCum)[tid];
 
     // ---- sums over the value columns: dO S^T, dR S^T, U D^T for the wave's
@@ -349,16 +371,19 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     const float* Dg = ba.D + (int64_t)blockIdx.x * pad * NP;
     const float* Ug = ba.U + (int64_t)blockIdx.x * kC * pad;
     const float* Rg = ba.dR + (int64_t)blockIdx.x * kC * pad;
-    const Tdo* Og = reinterpret_cast<const Tdo*>(ba.dout);
-    const Tin* Vg = reinterpret_cast<const Tin*>(a.v);
+    constexpr int ES = (int)sizeof(Tin), EO = (int)sizeof(Tdo);
+    const int P = (int)a.P;
+    const int64_t sk = a.G * a.qk_row * ES, sv = a.H * P * ES, so = a.H * P * EO;
+    const int64_t row0 = b * a.L + t0;
+    const auto ob = rows_buf(static_cast<const char*>(ba.dout) + row0 * so + h * P * EO, live, so, P * EO);
+    const auto vb = rows_buf(static_cast<const char*>(a.v) + row0 * sv + h * P * ES, live, sv, P * ES);
     for (int pb = 0; pb < pad; pb += kPb) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NP / 32; ++i) {      // S and D: 32 rows of NP
             const int id = tid + 256 * i, r = id / (NP / 4), n = 4 * (id % (NP / 4));
-            float s[4], d[4];
-            io::ld4(Sg + (int64_t)(pb + r) * NP + n, s);
-            io::ld4(Dg + (int64_t)(pb + r) * NP + n, d);
+            const f32x4 s = *reinterpret_cast<const f32x4*>(Sg + (int64_t)(pb + r) * NP + n);
+            const f32x4 d = *reinterpret_cast<const f32x4*>(Dg + (int64_t)(pb + r) * NP + n);
 #pragma unroll
             for (int e = 0; e < 4; ++e) sd = __builtin_fma((double)s[e], (double)d[e], sd);
             uint2 sp[3], dp[3];
@@ -373,15 +398,11 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
 #pragma unroll
         for (int i = 0; i < 2; ++i) {            // U and dR: 64 rows of 32
             const int id = tid + 256 * i, r = id >> 3, e0 = 4 * (id & 7);
-            float u[4], d[4];
-            io::ld4(Ug + (int64_t)r * pad + pb + e0, u);
-            io::ld4(Rg + (int64_t)r * pad + pb + e0, d);
-            if (r < live) {
-                const Tin* vr = Vg + ((b * a.L + t0 + r) * a.H + h) * a.P;
+            const f32x4 u = *reinterpret_cast<const f32x4*>(Ug + (int64_t)r * pad + pb + e0);
+            const f32x4 d = *reinterpret_cast<const f32x4*>(Rg + (int64_t)r * pad + pb + e0);
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (pb + e0 + e < a.P) rv[i] = __builtin_fmaf(d[e], io::ld(vr + pb + e0 + e), rv[i]);
-            }
+            for (int e = 0; e < 4; ++e)
+                rv[i] = __builtin_fmaf(d[e], buf_ld<Tin>(vb, pb + e0 + e < P ? r * (int)sv + (pb + e0 + e) * ES : kOut), rv[i]);
             uint2 up[3], dp[3];
             split4<3>(u, up);
             split4<3>(d, dp);
@@ -393,9 +414,16 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
         }
         {                                        // dout: 64 rows of 32
             const int r = tid >> 2, e0 = 8 * (tid & 3);
+            const int off = r * (int)so + (pb + e0) * EO;
             Raw8<Tdo> o;
-            if (r < live) fetch8(Og + ((b * a.L + t0 + r) * a.H + h) * a.P + pb, e0, (int)min(a.P - pb, (int64_t)kPb), ba.vec_p, o);
-            else zero(o);
+            if (ba.vec_p) {
+                fetch8(ob, pb + e0 < P ? off : kOut, o);
+            } else {
+                float e[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) e[i] = buf_ld<Tdo>(ob, pb + e0 + i < P ? off + i * EO : kOut);
+                from_floats(e, o);
+            }
             stage8<false>(sm.s.O[0][r], kC * kRowP, e0, o);
         }
         __syncthreads();
@@ -440,20 +468,20 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
         if ((tid & 7) == 0) sm.rv[(tid >> 3) + 32 * i] = rv[i];
     }
     // K and Q over what the steps used
+    {
+        const int64_t at = row0 * sk + grp * a.qk_row * ES;
+        const auto kb = rows_buf(static_cast<const char*>(a.k) + at, live, sk, a.NL * ES);
+        const auto qb = rows_buf(static_cast<const char*>(a.q) + at, live, sk, a.NL * ES);
 #pragma unroll
-    for (int i = 0; i < NP / 32; ++i) {
-        const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-        Raw8<Tin> k, q;
-        if (r < live) {
-            const int64_t row = ((b * a.L + t0 + r) * a.G + grp) * N;
-            fetch8(reinterpret_cast<const Tin*>(a.k) + row, n0, N, a.vec, k);
-            fetch8(reinterpret_cast<const Tin*>(a.q) + row, n0, N, a.vec, q);
-        } else {
-            zero(k);
-            zero(q);
+        for (int i = 0; i < NP / 32; ++i) {
+            const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+            const int off = n0 < a.NL ? r * (int)sk + n0 * ES : kOut;
+            Raw8<Tin> k, q;
+            fetch8(kb, off, k);
+            fetch8(qb, off, q);
+            stage8<false>(sm.m.K[0][r], kC * kRow, n0, k);
+            stage8<false>(sm.m.Q[0][r], kC * kRow, n0, q);
         }
-        stage8<false>(sm.m.K[0][r], kC * kRow, n0, k);
-        stage8<false>(sm.m.Q[0][r], kC * kRow, n0, q);
     }
     __syncthreads();
 
@@ -639,21 +667,22 @@ hipError_t lds(K* kern, int bytes) {
 
 template <typename Tin, typename Tdo, int NP>
 hipError_t launch(const DeltaBwdArgs& a, hipStream_t stream) {
-    constexpr int W = 4;
+    constexpr int CT = 1;
     const DeltaArgs& f = a.f;
     const int64_t nch = delta_chunks(f.L);
-    hipError_t e = launch_delta_prep(f, sizeof(Tin) == 2, a.recs, stream);
+    hipError_t e = launch_delta_prep(f, sizeof(Tin) == 2, true, a.recs, stream);
     if (e != hipSuccess) return e;
     e = launch_delta_keep(f, sizeof(Tin) == 2, a.recs, a.S, a.U, a.pad, stream);
     if (e != hipSuccess) return e;
     {
-        const auto kern = &delta_back_kernel<Tin, Tdo, NP, W>;
-        constexpr int bytes = (int)sizeof(BackSmem<Tin, NP>);
+        const auto kern = &delta_back_kernel<Tin, Tdo, NP, CT>;
+        constexpr int bytes = (int)sizeof(BackSmem<Tin, Tdo, NP, CT>);
+        static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
         if ((e = lds(kern, bytes)) != hipSuccess) return e;
-        const int npb = (a.pad + 16 * W - 1) / (16 * W);
+        const int npb = a.pad / (16 * CT);
         const int64_t units = (f.batch * f.H + 7) / 8 * 8;
         KTime kt("delta_back", stream);
-        hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(64 * W), bytes, stream, a, nch, npb);
+        hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(256), bytes, stream, a, nch, npb);
     }
     {
         const auto kern = &delta_grad_kernel<Tin, Tdo, NP>;
@@ -683,7 +712,7 @@ struct Sizes {
 Sizes sizes(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N) {
     const size_t chunks = (size_t)(batch * H * delta_chunks(L)), pad = (size_t)(P + 31) / 32 * 32;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-    return {up(chunks * delta_record_bytes()), up(chunks * pad * (N <= 64 ? 64 : 128) * 4), up(chunks * kC * pad * 4),
+    return {up(chunks * delta_record_bytes(true)), up(chunks * pad * (N <= 64 ? 64 : 128) * 4), up(chunks * kC * pad * 4),
             H > G ? up((size_t)(batch * L * H * N) * 4) : 0};
 }
 

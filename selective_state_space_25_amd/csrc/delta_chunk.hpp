@@ -1,6 +1,5 @@
 // delta_chunk.hpp -- what the chunked gated delta rule's kernels share: the
-// per-chunk record, 64-token staging, and the fragments of triangular
-// matrices in LDS.
+// per-chunk record, bounded loads of 64-token pieces, operands in LDS.
 #pragma once
 
 #include "io.hpp"
@@ -18,7 +17,7 @@ constexpr int kBlocks = 10;        // 16 x 16 blocks on and below a chunk matrix
 // Record of one (batch, head, chunk), in floats: T and A as 10 row-major
 // 16 x 16 blocks (block (t, s) at t (t + 1) / 2 + s), then per token
 // e^cum, e^(last - cum), beta (zero past the sequence's end), and cum itself
-// as doubles.
+// as doubles; for the gradients T's and A's blocks again, each transposed.
 constexpr int kRecT = 0;
 constexpr int kRecA = kBlocks * 256;
 constexpr int kRecGam = 2 * kBlocks * 256;
@@ -26,6 +25,11 @@ constexpr int kRecTail = kRecGam + kC;
 constexpr int kRecBeta = kRecTail + kC;
 constexpr int kRecCum = kRecBeta + kC;
 constexpr int kRec = kRecCum + 2 * kC;
+constexpr int kRecTt = kRec;
+constexpr int kRecAt = kRecTt + kBlocks * 256;
+constexpr int kRecGrad = kRecAt + kBlocks * 256;
+
+__device__ __forceinline__ int block_at(int t, int s) { return (t * (t + 1) / 2 + s) * 256; }
 
 __device__ __forceinline__ int64_t seq_len(const DeltaArgs& a, int64_t b) {
     return a.lengths ? min((int64_t)max(a.lengths[b], 0), a.L) : a.L;
@@ -36,61 +40,81 @@ __device__ __forceinline__ float exp_f32(float x) { return fast_exp2(x * kLog2e)
 // Planes that an input of type T takes.
 template <typename T> constexpr int kPlanes = sizeof(T) == 2 ? 1 : 3;
 
-// Eight elements of a row as loaded.
+// Workgroup barrier for LDS traffic only: global loads and stores in flight
+// keep running across it.
+__device__ __forceinline__ void lds_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// A buffer over `rows` rows spaced `stride` bytes apart, of which `bytes`
+// belong to it: loads past its end give zero, stores there are dropped.
+// Offsets are 32-bit: 64 rows stay within 2^30 bytes (checked on the host).
+constexpr int kOut = 1 << 30;   // an offset past every buffer, with room for a few rows more
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buf(const void* p, int rows, int64_t stride, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, rows > 0 ? (rows - 1) * (int)stride + bytes : 0,
+                                             0x00020000);
+}
+
+template <typename T> __device__ __forceinline__ float buf_ld(__amdgpu_buffer_rsrc_t r, int off);
+template <> __device__ __forceinline__ float buf_ld<float>(__amdgpu_buffer_rsrc_t r, int off) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+template <> __device__ __forceinline__ float buf_ld<uint16_t>(__amdgpu_buffer_rsrc_t r, int off) {
+    return bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
+}
+// One element as loaded; widen it when it is used, not before: widening
+// waits for the load.
+template <typename T> __device__ __forceinline__ T buf_raw(__amdgpu_buffer_rsrc_t r, int off);
+template <> __device__ __forceinline__ float buf_raw<float>(__amdgpu_buffer_rsrc_t r, int off) {
+    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+}
+template <> __device__ __forceinline__ uint16_t buf_raw<uint16_t>(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+}
+__device__ __forceinline__ f32x4 widen(const float (&v)[4]) { return f32x4{v[0], v[1], v[2], v[3]}; }
+__device__ __forceinline__ f32x4 widen(const uint16_t (&v)[4]) {
+    return f32x4{bf16_to_f32(v[0]), bf16_to_f32(v[1]), bf16_to_f32(v[2]), bf16_to_f32(v[3])};
+}
+__device__ __forceinline__ f32x4 buf_ld4(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ void buf_st(__amdgpu_buffer_rsrc_t r, int off, float v, float) {
+    __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), r, off, 0, 0);
+}
+__device__ __forceinline__ void buf_st(__amdgpu_buffer_rsrc_t r, int off, float v, uint16_t) {
+    __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v), r, off, 0, 0);
+}
+
+// Eight consecutive elements of a row as loaded, and into the planes of a
+// staged row (plane stride ps elements; PERM: columns through kperm).
 template <typename T> struct Raw8;
-template <> struct Raw8<uint16_t> { uint4 w; };
-template <> struct Raw8<float> { float4 lo, hi; };
+template <> struct Raw8<uint16_t> { u32x4 w; };
+template <> struct Raw8<float> { f32x4 lo, hi; };
 
-__device__ __forceinline__ void zero(Raw8<uint16_t>& r) { r.w = make_uint4(0, 0, 0, 0); }
-__device__ __forceinline__ void zero(Raw8<float>& r) { r.lo = r.hi = make_float4(0, 0, 0, 0); }
-
-// Elements n0 .. n0 + 7 of a row of N (zeros past it); vec: 16-byte loads
-// are aligned and N % 8 == 0.
-__device__ __forceinline__ void fetch8(const uint16_t* row, int n0, int N, int vec, Raw8<uint16_t>& r) {
-    if (vec) {
-        if (n0 < N) r.w = *reinterpret_cast<const uint4*>(row + n0);
-        else zero(r);
-    } else {
-        uint32_t e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = n0 + i < N ? row[n0 + i] : 0u;
-        r.w = make_uint4(e[0] | e[1] << 16, e[2] | e[3] << 16, e[4] | e[5] << 16, e[6] | e[7] << 16);
-    }
+__device__ __forceinline__ void fetch8(__amdgpu_buffer_rsrc_t b, int off, Raw8<uint16_t>& r) {
+    r.w = __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0);
 }
-__device__ __forceinline__ void fetch8(const float* row, int n0, int N, int vec, Raw8<float>& r) {
-    if (vec) {
-        if (n0 < N) {
-            r.lo = *reinterpret_cast<const float4*>(row + n0);
-            r.hi = *reinterpret_cast<const float4*>(row + n0 + 4);
-        } else {
-            zero(r);
-        }
-    } else {
-        float e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = n0 + i < N ? row[n0 + i] : 0.0f;
-        r.lo = make_float4(e[0], e[1], e[2], e[3]);
-        r.hi = make_float4(e[4], e[5], e[6], e[7]);
-    }
+__device__ __forceinline__ void fetch8(__amdgpu_buffer_rsrc_t b, int off, Raw8<float>& r) {
+    r.lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+    r.hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 16, 0));
 }
-
-// Eight elements into the planes of a staged row (plane stride ps elements),
-// columns n0 .. n0 + 7, through kperm when PERM.
 template <bool PERM>
 __device__ __forceinline__ void stage8(uint16_t* row, int ps, int n0, const Raw8<uint16_t>& r) {
     if constexpr (PERM) {
-        *reinterpret_cast<uint2*>(row + kperm(n0)) = make_uint2(r.w.x, r.w.y);
-        *reinterpret_cast<uint2*>(row + kperm(n0 + 4)) = make_uint2(r.w.z, r.w.w);
+        *reinterpret_cast<uint2*>(row + kperm(n0)) = make_uint2(r.w[0], r.w[1]);
+        *reinterpret_cast<uint2*>(row + kperm(n0 + 4)) = make_uint2(r.w[2], r.w[3]);
     } else {
-        *reinterpret_cast<uint4*>(row + n0) = r.w;
+        *reinterpret_cast<u32x4*>(row + n0) = r.w;
     }
 }
 template <bool PERM>
 __device__ __forceinline__ void stage8(uint16_t* row, int ps, int n0, const Raw8<float>& r) {
-    const float a[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w}, b[4] = {r.hi.x, r.hi.y, r.hi.z, r.hi.w};
     uint2 pa[3], pb[3];
-    split4<3>(a, pa);
-    split4<3>(b, pb);
+    split4<3>(r.lo, pa);
+    split4<3>(r.hi, pb);
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
         *reinterpret_cast<uint2*>(row + p * ps + (PERM ? kperm(n0) : n0)) = pa[p];
@@ -98,31 +122,61 @@ __device__ __forceinline__ void stage8(uint16_t* row, int ps, int n0, const Raw8
     }
 }
 
+// An A operand row straight from memory in tile order: k-step at column n0
+// of the lane's row takes columns n0 + 4 g .. and n0 + 16 + 4 g ...
+__device__ __forceinline__ void fetch_row(__amdgpu_buffer_rsrc_t b, int off, Raw8<uint16_t>& r) {
+    const auto lo = __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0);
+    const auto hi = __builtin_amdgcn_raw_buffer_load_b64(b, off, 32, 0);
+    r.w = u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+__device__ __forceinline__ void fetch_row(__amdgpu_buffer_rsrc_t b, int off, Raw8<float>& r) {
+    r.lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
+    r.hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 64, 0));
+}
+// ... its two groups of four columns zero unless lo, hi
+__device__ __forceinline__ void keep_row(Raw8<uint16_t>& r, bool lo, bool hi) {
+    r.w = u32x4{lo ? r.w[0] : 0u, lo ? r.w[1] : 0u, hi ? r.w[2] : 0u, hi ? r.w[3] : 0u};
+}
+__device__ __forceinline__ void keep_row(Raw8<float>& r, bool lo, bool hi) {
+    const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+    r.lo = lo ? r.lo : z;
+    r.hi = hi ? r.hi : z;
+}
+__device__ __forceinline__ void to_operand(const Raw8<uint16_t>& r, bf16x8 (&p)[1]) {
+    p[0] = __builtin_bit_cast(bf16x8, r.w);
+}
+__device__ __forceinline__ void to_operand(const Raw8<float>& r, bf16x8 (&p)[3]) { split8<3>(r.lo, r.hi, p); }
+
 // Tile k of the 10 lower tiles: row block tb, column block sb.
 __device__ __forceinline__ void lower_tile(int k, int& tb, int& sb) {
     tb = k >= 6 ? 3 : k >= 3 ? 2 : k >= 1 ? 1 : 0;
     sb = k - tb * (tb + 1) / 2;
 }
 
-// A lower triangular chunk matrix as MFMA operands: fragment (row block tb,
-// k-step ks <= tb / 2) holds column blocks 2 ks and 2 ks + 1 in
-// split_tiles' k order.
-__device__ __forceinline__ int frag(int tb, int ks) { return tb < 2 ? tb : 2 * tb - 2 + ks; }
-
-// Its transpose: fragment (row block jb, k-step ks >= jb / 2).
-__device__ __forceinline__ int frag_t(int jb, int ks) { return jb < 2 ? 2 * jb + ks : jb + 2; }
-
-// NPL planes of a chunk matrix's six fragments.
-template <int NPL>
-struct Frags {
-    uint16_t p[NPL][6][64][8];
-};
-
-template <int NPL>
-__device__ __forceinline__ void ld_frag(const Frags<NPL>& f, int i, int lane, bf16x8 (&a)[NPL]) {
+// B operands that waves hand to each other through LDS: NPL planes of KS
+// k-steps in tile order, each lane's 16 bytes in its own slot.
+template <int KS, int NPL>
+struct Operands {
+    uint16_t p[KS][NPL][64][8];
+    // C tile t of the operand's rows (half t % 2 of k-step t / 2), split
+    __device__ __forceinline__ void put_tile(int t, f32x4 v, int lane) {
+        uint2 w[NPL];
+        split4<NPL>(v, w);
 #pragma unroll
-    for (int p = 0; p < NPL; ++p) a[p] = ld8(f.p[p][i][lane]);
-}
+        for (int i = 0; i < NPL; ++i) *reinterpret_cast<uint2*>(&p[t >> 1][i][lane][4 * (t & 1)]) = w[i];
+    }
+    // both tiles of k-step ks
+    __device__ __forceinline__ void put(int ks, f32x4 lo, f32x4 hi, int lane) {
+        bf16x8 w[NPL];
+        split8<NPL>(lo, hi, w);
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) *reinterpret_cast<bf16x8*>(p[ks][i][lane]) = w[i];
+    }
+    __device__ __forceinline__ void get(int ks, int lane, bf16x8 (&w)[NPL]) const {
+#pragma unroll
+        for (int i = 0; i < NPL; ++i) w[i] = ld8(p[ks][i][lane]);
+    }
+};
 
 }  // namespace dchunk
 }  // namespace selscan

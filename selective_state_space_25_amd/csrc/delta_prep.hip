@@ -18,6 +18,8 @@
 // strong decay cum is large and its fp32 steps would be errors of the
 // decays between the tokens that follow.  g below -200 counts as -200, whose
 // exponential is zero in fp32 either way, so that a reset (-inf) stays finite.
+#include <algorithm>
+
 #include "delta_chunk.hpp"
 
 namespace selscan {
@@ -60,7 +62,8 @@ __device__ __forceinline__ f32x4 ld_block(const float* Y, int li, int lg) {
     return v;
 }
 
-template <typename Tin, int NP>
+// GRAD: the transposed blocks too.
+template <typename Tin, int NP, bool GRAD>
 __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, float* recs, int64_t nch) {
     constexpr int NK = kPlanes<Tin>;
     constexpr int kRow = PrepSmem<Tin, NP>::kRow;
@@ -73,28 +76,24 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, float* rec
     const int64_t len = seq_len(a, b);
     if (t0 >= len) return;
     const int live = (int)min((int64_t)kC, len - t0);
-    float* rec = recs + (int64_t)blockIdx.x * kRec;
+    float* rec = recs + (int64_t)blockIdx.x * (GRAD ? kRecGrad : kRec);
 
-    {   // K and Q rows: a thread takes every fourth 8-element piece of a token
-        const int r = tid >> 2;
-        const int64_t row = ((b * a.L + t0 + r) * a.G + grp) * a.N;
-        const Tin* kr = reinterpret_cast<const Tin*>(a.k) + row;
-        const Tin* qr = reinterpret_cast<const Tin*>(a.q) + row;
+    {   // K and Q rows
+        constexpr int ES = (int)sizeof(Tin);
+        const int64_t sk = a.G * a.qk_row * ES, at = (b * a.L + t0) * sk + grp * a.qk_row * ES;
+        const auto kb = rows_buf(static_cast<const char*>(a.k) + at, live, sk, a.NL * ES);
+        const auto qb = rows_buf(static_cast<const char*>(a.q) + at, live, sk, a.NL * ES);
         Raw8<Tin> x[NP / 32], y[NP / 32];
 #pragma unroll
         for (int i = 0; i < NP / 32; ++i) {
-            const int n0 = 8 * ((tid & 3) + 4 * i);
-            if (r < live) {
-                fetch8(kr, n0, a.N, a.vec, x[i]);
-                fetch8(qr, n0, a.N, a.vec, y[i]);
-            } else {
-                zero(x[i]);
-                zero(y[i]);
-            }
+            const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+            const int off = n0 < a.NL ? r * (int)sk + n0 * ES : kOut;
+            fetch8(kb, off, x[i]);
+            fetch8(qb, off, y[i]);
         }
 #pragma unroll
         for (int i = 0; i < NP / 32; ++i) {
-            const int n0 = 8 * ((tid & 3) + 4 * i);
+            const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
             stage8<false>(sm.K[0][r], kC * kRow, n0, x[i]);
             stage8<false>(sm.Q[0][r], kC * kRow, n0, y[i]);
         }
@@ -143,9 +142,11 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, float* rec
         for (int q = 0; q < 4; ++q) {
             const int t = 16 * tb + 4 * lg + q;
             const float v = acc[q] * exp_f32((float)(sm.cum[t] - cs));
-            if (isq) rec[kRecA + blk * 256 + (4 * lg + q) * 16 + li] = s <= t ? v : 0.0f;
+            acc[q] = s <= t ? v : 0.0f;
+            if (isq) rec[kRecA + blk * 256 + (4 * lg + q) * 16 + li] = acc[q];
             else sm.M[t][s] = s < t ? sm.beta[t] * v : 0.0f;
         }
+        if (GRAD && isq) *reinterpret_cast<f32x4*>(rec + kRecAt + blk * 256 + li * 16 + 4 * lg) = acc;
     }
     __syncthreads();
 
@@ -196,12 +197,16 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, float* rec
         const int r = (i & 63) >> 2, q4 = 4 * (i & 3);
         *reinterpret_cast<float4*>(rec + kRecT + 4 * i) =
             *reinterpret_cast<const float4*>(&sm.T[16 * tb + r][16 * sb + q4]);
+        if constexpr (GRAD) {
+            const float* x = &sm.T[16 * tb + q4][16 * sb + r];
+            *reinterpret_cast<float4*>(rec + kRecTt + 4 * i) = make_float4(x[0], x[kRowM], x[2 * kRowM], x[3 * kRowM]);
+        }
     }
 }
 
-template <typename Tin, int NP>
+template <typename Tin, int NP, bool GRAD>
 hipError_t launch(const DeltaArgs& a, float* recs, int64_t nch, hipStream_t stream) {
-    const auto kern = &delta_prep_kernel<Tin, NP>;
+    const auto kern = &delta_prep_kernel<Tin, NP, GRAD>;
     constexpr int bytes = (int)sizeof(PrepSmem<Tin, NP>);
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
@@ -210,15 +215,51 @@ hipError_t launch(const DeltaArgs& a, float* recs, int64_t nch, hipStream_t stre
     return hipGetLastError();
 }
 
+template <typename Tin, bool GRAD>
+hipError_t by_n(const DeltaArgs& a, float* recs, hipStream_t stream) {
+    const int64_t nch = delta_chunks(a.L);
+    return a.N <= 64 ? launch<Tin, 64, GRAD>(a, recs, nch, stream) : launch<Tin, 128, GRAD>(a, recs, nch, stream);
+}
+
+// Rows of N elements, one after the other, to rows of `to`, zeros past N.
+template <typename T>
+__global__ __launch_bounds__(256) void delta_pad_kernel(const T* q, const T* k, T* qo, T* ko, int N, int to, int64_t n) {
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+        const int64_t r = i / to;
+        const int c = (int)(i - r * to);
+        qo[i] = c < N ? q[r * N + c] : T(0);
+        ko[i] = c < N ? k[r * N + c] : T(0);
+    }
+}
+
 }  // namespace
 
 int64_t delta_chunks(int64_t L) { return (L + dchunk::kC - 1) / dchunk::kC; }
-size_t delta_record_bytes() { return sizeof(float) * dchunk::kRec; }
+size_t delta_record_bytes(bool grad) { return sizeof(float) * (grad ? dchunk::kRecGrad : dchunk::kRec); }
 
-hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, float* recs, hipStream_t stream) {
-    const int64_t nch = delta_chunks(a.L);
-    if (in_bf16) return a.N <= 64 ? launch<uint16_t, 64>(a, recs, nch, stream) : launch<uint16_t, 128>(a, recs, nch, stream);
-    return a.N <= 64 ? launch<float, 64>(a, recs, nch, stream) : launch<float, 128>(a, recs, nch, stream);
+hipError_t launch_delta_pad(DeltaArgs& a, int in_bf16, void* rows, hipStream_t stream) {
+    const int to = a.N <= 64 ? 64 : 128;
+    const int64_t n = a.batch * a.L * a.G * to;
+    const unsigned blocks = (unsigned)std::min<int64_t>((n + 255) / 256, 1 << 16);
+    KTime kt("delta_pad", stream);
+    void* k = static_cast<char*>(rows) + n * (in_bf16 ? 2 : 4);
+    if (in_bf16)
+        hipLaunchKernelGGL((delta_pad_kernel<uint16_t>), dim3(blocks), dim3(256), 0, stream,
+                           static_cast<const uint16_t*>(a.q), static_cast<const uint16_t*>(a.k),
+                           static_cast<uint16_t*>(rows), static_cast<uint16_t*>(k), a.N, to, n);
+    else
+        hipLaunchKernelGGL((delta_pad_kernel<float>), dim3(blocks), dim3(256), 0, stream, static_cast<const float*>(a.q),
+                           static_cast<const float*>(a.k), static_cast<float*>(rows), static_cast<float*>(k), a.N, to, n);
+    a.q = rows;
+    a.k = k;
+    a.NL = to;
+    a.qk_row = to;
+    return hipGetLastError();
+}
+
+hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, bool grad, float* recs, hipStream_t stream) {
+    if (in_bf16) return grad ? by_n<uint16_t, true>(a, recs, stream) : by_n<uint16_t, false>(a, recs, stream);
+    return grad ? by_n<float, true>(a, recs, stream) : by_n<float, false>(a, recs, stream);
 }
 
 }  // namespace selscan

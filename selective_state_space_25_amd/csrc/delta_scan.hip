@@ -9,11 +9,16 @@
 //   S' = e^last S + K^T (e^(last - cum) U)
 //
 // which is the token recurrence regrouped: U's rows are the u_t of
-// S_t = e^g_t S_{t-1} + k_t u_t^T.  Value columns are independent, so a wave
-// owns 16 columns of one head and walks its chunks in order with nothing to
-// exchange: S, R and U stay in its registers as C tiles, and a C tile pair is
-// the B operand of the next product (split_tiles).  A workgroup's waves share
-// the chunk's K, Q, T and A in LDS, fetched a chunk ahead.
+// S_t = e^g_t S_{t-1} + k_t u_t^T.  Value columns are independent: a
+// workgroup owns 16 CT columns of one head and walks its chunks in order.
+// The walk is a chain of three products a chunk, so what bounds it is their
+// latency, and the four waves split each of them: wave w has the tokens
+// 16 w .. 16 w + 15 of R, U and Y and a quarter of the state's rows.  What a
+// wave makes the others need as a B operand, which a C tile pair is (see
+// split_mfma.hpp): split into planes it goes through LDS, three barriers a
+// chunk.  A wave's rows of Q, T and A are nobody else's and come from memory
+// straight into its registers; only K, needed both ways up, is staged.  All
+// of a chunk's inputs are fetched a chunk ahead.
 //
 // Products are fp32-grade (split_mfma.hpp) where they reach the state.  What
 // goes into a bf16 y alone (Q S, A U) keeps plane pairs a + b < 2, an error
@@ -26,263 +31,301 @@ namespace {
 
 using namespace dchunk;
 
-// OL: plane pairs a + b < OL in the products of y; without y (OL = 0) Q and
-// A stay out.
-template <typename Tin, int NP, int OL>
+// OL: plane pairs a + b < OL in the products of y; 0 = no y.
+template <typename Tin, int NP, int CT, int OL>
 struct ScanSmem {
     static constexpr int kRow = NP + 8;
-    float gam[kC], tail[kC], beta[kC];
-    uint16_t K[kPlanes<Tin>][kC][kRow];   // columns through kperm
-    Frags<3> T;
-    uint16_t Q[OL ? kPlanes<Tin> : 1][OL ? kC : 1][kRow];
-    Frags<OL ? OL : 1> A;
+    uint16_t K[2][kPlanes<Tin>][kC][kRow];   // by chunk parity; columns through kperm
+    Operands<NP / 32, 3> S[CT];
+    Operands<2, 3> R[CT], W[CT];             // R; e^(last - cum) U
+    Operands<2, OL ? OL : 1> U[CT];
 };
 
 // KEEP: instead of y, the state entering each chunk [chunk, pad, NP] and U
 // [chunk, 64, pad], which the gradients read (pad: P rounded up to 32, the
 // columns past P zero).
-template <typename Tin, typename Tout, int NP, int W, bool KEEP>
-__global__ __launch_bounds__(64 * W) void delta_scan_kernel(DeltaArgs a, const float* recs, int64_t nch, int npb,
-                                                            float* keep_s, float* keep_u, int pad) {
+template <typename Tin, typename Tout, int NP, int CT, bool KEEP>
+__global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const float* recs, int64_t nch, int npb,
+                                                         float* keep_s, float* keep_u, int pad) {
     constexpr int OL = KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3;
+    constexpr int OA = OL ? OL : 1;
     constexpr int NK = kPlanes<Tin>;
-    constexpr int kRow = ScanSmem<Tin, NP, OL>::kRow;
-    constexpr int NB = NP / 16;              // state tiles
+    constexpr int ES = (int)sizeof(Tin), EO = (int)sizeof(Tout);
+    constexpr int kRow = ScanSmem<Tin, NP, CT, OL>::kRow;
     constexpr int KS = NP / 32;              // k-steps over the key dimension
-    constexpr int kT = 64 * W;
-    constexpr int NPC = kC * (NP / 8) / kT;  // 8-element pieces of K (or Q) per thread
-    constexpr int NTR = (kBlocks * 64 + kT - 1) / kT;   // float4 pieces of T (or A) per thread
+    constexpr int NT = NP / 64;              // state tiles per wave
+    constexpr int NPC = NP / 32;             // 8-element pieces of K per thread
+    constexpr int kRecS = KEEP ? kRecGrad : kRec;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
-    auto& sm = *reinterpret_cast<ScanSmem<Tin, NP, OL>*>(smem_raw);
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    auto& sm = *reinterpret_cast<ScanSmem<Tin, NP, CT, OL>*>(smem_raw);
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     // the column blocks of a head on one XCD (workgroups go round the eight),
     // whose L2 then serves its K, Q and records once from memory
-    const int64_t j = blockIdx.x / 8;
-    const int64_t bh = (j / npb) * 8 + blockIdx.x % 8;
+    const int jx = blockIdx.x / 8;
+    const int64_t bh = (int64_t)(jx / npb) * 8 + blockIdx.x % 8;
     if (bh >= a.batch * a.H) return;
     const int64_t b = bh / a.H, h = bh - b * a.H, grp = h / (a.H / a.G);
     const int64_t len = seq_len(a, b);
-    const int64_t mine = (len + kC - 1) / kC;
-    const int64_t p0 = (int64_t)(j % npb) * 16 * W + 16 * wave;
-    const int64_t p = p0 + li;
-    const bool active = p0 < (KEEP ? (int64_t)pad : a.P), pok = p < a.P;
-    const int N = a.N;
-    const Tin* Kg = reinterpret_cast<const Tin*>(a.k);
-    const Tin* Qg = reinterpret_cast<const Tin*>(a.q);
-    const Tin* Vg = reinterpret_cast<const Tin*>(a.v);
-    Tout* Yg = reinterpret_cast<Tout*>(a.y);
+    const int mine = (int)((len + kC - 1) / kC);
+    const int N = a.N, P = (int)a.P;
+    const int p0 = (jx % npb) * 16 * CT + li;   // the lane's first column
+    // strides of a token in bytes; chunk 0's rows
+    const int64_t sk = a.G * a.qk_row * ES, sv = a.H * P * ES, sy = a.H * P * EO;
+    const char* Kg = static_cast<const char*>(a.k) + b * a.L * sk + grp * a.qk_row * ES;
+    const char* Qg = static_cast<const char*>(a.q) + b * a.L * sk + grp * a.qk_row * ES;
+    const char* Vg = static_cast<const char*>(a.v) + b * a.L * sv + h * P * ES;
+    char* Yg = static_cast<char*>(a.y) + b * a.L * sy + h * P * EO;
 
-    f32x4 S[NB];   // tile i: rows n = 16 i + 4 lg + q, column p
+    f32x4 S[NT][CT];   // tile i: rows n = 16 (NT w + i) + 4 lg + q, column p0 + 16 ct
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NT; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int n = 16 * i + 4 * lg + q;
-            S[i][q] = a.h0 && pok && n < N ? a.h0[(bh * a.P + p) * N + n] : 0.0f;
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = 16 * (NT * w + i) + 4 * lg + q, p = p0 + 16 * ct;
+                S[i][ct][q] = a.h0 && p < P && n < N ? a.h0[(bh * P + p) * N + n] : 0.0f;
+            }
+    auto put_state = [&]() {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            if constexpr (NT == 2) sm.S[ct].put(w, S[0][ct], S[1][ct], lane);
+            else sm.S[ct].put_tile(w, S[0][ct], lane);
         }
+    };
 
-    Raw8<Tin> sk[NPC], sq[NPC];   // the next chunk's pieces, on their way to LDS
-    float4 stt[NTR], sa[NTR], sgate;
-    Tin sv[16];
-    auto fetch = [&](int64_t c) {
-        const int64_t t0 = c * kC;
+    int koff[NPC], qoff, voff[CT], yoff[CT];
+#pragma unroll
+    for (int i = 0; i < NPC; ++i) {
+        const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+        koff[i] = n0 < a.NL ? r * (int)sk + n0 * ES : kOut;
+    }
+    qoff = (16 * w + li) * (int)sk + 4 * lg * ES;
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        const int p = p0 + 16 * ct;
+        voff[ct] = p < P ? (16 * w + 4 * lg) * (int)sv + p * ES : kOut;
+        yoff[ct] = p < P ? (16 * w + 4 * lg) * (int)sy + p * EO : kOut;
+    }
+
+    int toff[4];                             // blocks (w, s) of T; above the diagonal: none, zeros
+#pragma unroll
+    for (int s = 0; s < 4; ++s) toff[s] = s <= w ? (block_at(w, s) + li * 16 + 4 * lg) * 4 : kOut;
+
+    // A chunk's inputs as fetched.  Loads complete in order with the stores
+    // after them, so they are turned into operands before the chunk's stores
+    // are issued and the wait for them never includes those.
+    Raw8<Tin> fk[NPC], fq[KS];
+    f32x4 ft[4], fa[4], fgate[3];
+    float fgl;
+    Tin fv[CT][4];
+    auto fetch = [&](int c) {
+        const int64_t t0 = (int64_t)c * kC;
         const int live = (int)min((int64_t)kC, len - t0);
-        const float* rec = recs + (bh * nch + c) * kRec;
+        const auto kb = rows_buf(Kg + t0 * sk, live, sk, a.NL * ES);
+        const auto qb = rows_buf(Qg + t0 * sk, live, sk, a.NL * ES);
+        const auto vb = rows_buf(Vg + t0 * sv, live, sv, P * ES);
+        const auto rb = rows_buf(recs + (bh * nch + c) * kRecS, 1, 0, kRecS * 4);
 #pragma unroll
-        for (int i = 0; i < NPC; ++i) {
-            const int id = tid + i * kT, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-            if (r < live) {
-                const int64_t row = ((b * a.L + t0 + r) * a.G + grp) * N;
-                fetch8(Kg + row, n0, N, a.vec, sk[i]);
-                if constexpr (!KEEP) fetch8(Qg + row, n0, N, a.vec, sq[i]);
-            } else {
-                zero(sk[i]);
-                if constexpr (!KEEP) zero(sq[i]);
-            }
-        }
+        for (int i = 0; i < NPC; ++i) fetch8(kb, koff[i], fk[i]);
 #pragma unroll
-        for (int i = 0; i < NTR; ++i) {
-            const int id = tid + i * kT;
-            if (id < kBlocks * 64) {
-                const int o = (id >> 6) * 256 + (id & 15) * 16 + ((id >> 4) & 3) * 4;
-                stt[i] = *reinterpret_cast<const float4*>(rec + kRecT + o);
-                if constexpr (!KEEP) sa[i] = *reinterpret_cast<const float4*>(rec + kRecA + o);
-            }
-        }
-        if (tid < 48) sgate = *reinterpret_cast<const float4*>(rec + kRecGam + 4 * tid);
+        for (int i = 0; i < 3; ++i) fgate[i] = buf_ld4(rb, (kRecGam + i * kC + 16 * w + 4 * lg) * 4);
+        fgl = buf_raw<float>(rb, (kRecGam + kC - 1) * 4);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int r = 16 * (i >> 2) + 4 * lg + (i & 3);
-            sv[i] = pok && r < live ? Vg[((b * a.L + t0 + r) * a.H + h) * a.P + p] : Tin(0);
-        }
-    };
-    auto stage = [&]() {
+        for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-        for (int i = 0; i < NPC; ++i) {
-            const int id = tid + i * kT, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-            stage8<true>(sm.K[0][r], kC * kRow, n0, sk[i]);
-            if constexpr (!KEEP) stage8<true>(sm.Q[0][r], kC * kRow, n0, sq[i]);
-        }
+            for (int q = 0; q < 4; ++q) fv[ct][q] = buf_raw<Tin>(vb, voff[ct] + q * (int)sv);
 #pragma unroll
-        for (int i = 0; i < NTR; ++i) {
-            const int id = tid + i * kT;
-            if (id < kBlocks * 64) {
-                int tb, sb;
-                lower_tile(id >> 6, tb, sb);
-                const int f = frag(tb, sb >> 1), e = 4 * (sb & 1);
-                const float tv[4] = {stt[i].x, stt[i].y, stt[i].z, stt[i].w};
-                uint2 tp[3];
-                split4<3>(tv, tp);
-#pragma unroll
-                for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2*>(&sm.T.p[x][f][id & 63][e]) = tp[x];
-                if constexpr (!KEEP) {
-                    const float av[4] = {sa[i].x, sa[i].y, sa[i].z, sa[i].w};
-                    uint2 ap[OL];
-                    split4<OL>(av, ap);
-#pragma unroll
-                    for (int x = 0; x < OL; ++x) *reinterpret_cast<uint2*>(&sm.A.p[x][f][id & 63][e]) = ap[x];
-                }
-            }
-        }
-        if (tid < 48) *reinterpret_cast<float4*>(&sm.gam[4 * tid]) = sgate;   // gam, tail, beta in a row
-    };
-    // the zero blocks above the diagonal inside fragments 0 and 3, written once
-    for (int i = tid; i < 128; i += kT) {
-        const int f = i < 64 ? 0 : 3;
-        const uint2 z = make_uint2(0, 0);
-#pragma unroll
-        for (int x = 0; x < 3; ++x) *reinterpret_cast<uint2*>(&sm.T.p[x][f][i & 63][4]) = z;
+        for (int s = 0; s < 4; ++s) ft[s] = buf_ld4(rb, toff[s]);
         if constexpr (!KEEP) {
 #pragma unroll
-            for (int x = 0; x < OL; ++x) *reinterpret_cast<uint2*>(&sm.A.p[x][f][i & 63][4]) = z;
+            for (int ks = 0; ks < KS; ++ks) fetch_row(qb, qoff + 32 * ks * ES, fq[ks]);
+#pragma unroll
+            for (int s = 0; s < 4; ++s) fa[s] = buf_ld4(rb, toff[s] + kRecA * 4);
         }
-    }
+    };
+    bf16x8 Q[KS][NK], T[2][3], A[2][OA];
+    f32x4 gam, tail, beta, v[CT];
+    float gl;
+    auto ready = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < NPC; ++i) {
+            const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+            stage8<true>(sm.K[c & 1][0][r], kC * kRow, n0, fk[i]);
+        }
+        if constexpr (!KEEP) {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                if (a.NL < NP) {   // past NL a row goes on with the next group's
+                    const int n = 32 * ks + 4 * lg;
+                    keep_row(fq[ks], n < a.NL, n + 16 < a.NL);
+                }
+                to_operand(fq[ks], Q[ks]);
+            }
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            split8<3>(ft[2 * ks], ft[2 * ks + 1], T[ks]);
+            if constexpr (!KEEP) split8<OA>(fa[2 * ks], fa[2 * ks + 1], A[ks]);
+        }
+        gam = fgate[0];
+        tail = fgate[1];
+        beta = fgate[2];
+        gl = fgl;
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) v[ct] = widen(fv[ct]);
+    };
+
+    f32x4 y[CT];
+    auto put_y = [&](int c) {   // (chunk -1: none, a buffer of no rows)
+        if constexpr (!KEEP) {
+            const int64_t t0 = (int64_t)max(c, 0) * kC;
+            const auto yb = rows_buf(Yg + t0 * sy, c < 0 ? 0 : (int)min((int64_t)kC, a.L - t0), sy, P * EO);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) buf_st(yb, yoff[ct] + q * (int)sy, a.scale * y[ct][q], Tout(0));
+        }
+    };
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) y[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    put_state();
     if (mine > 0) {
         fetch(0);
-        stage();
+        ready(0);
     }
-    __syncthreads();
-    for (int64_t c = 0; c < mine; ++c) {
-        const int64_t t0 = c * kC;
-        float v[16];
+    lds_barrier();
+    for (int c = 0; c < mine; ++c) {
+        const uint16_t* K = &sm.K[c & 1][0][0][0];
+        const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
+        // The next chunk's loads go out ahead of the last one's stores: the
+        // wait for them then finds only stores a chunk older.
+        fetch(min(c + 1, mine - 1));
+        put_y(c - 1);
+        // R for the wave's tokens; Q S
+        f32x4 u[CT];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = io::ld(&sv[i]);
-        if (c + 1 < mine) fetch(c + 1);
-        if (active) {
-            bf16x8 Sp[KS][3];
+        for (int ct = 0; ct < CT; ++ct) u[ct] = y[ct] = z4;
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) split_tiles<3>(S[2 * ks], S[2 * ks + 1], Sp[ks]);
-            f32x4 R[4], U[4];
-            bf16x8 Bp[2][3];
+        for (int ks = 0; ks < KS; ++ks) {
+            bf16x8 k[NK];
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {
-                f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int x = 0; x < NK; ++x) k[x] = ld8(K + (x * kC + 16 * w + li) * kRow + 32 * ks + 8 * lg);
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    bf16x8 k[NK];
-#pragma unroll
-                    for (int x = 0; x < NK; ++x) k[x] = ld8(&sm.K[x][16 * tb + li][32 * ks + 8 * lg]);
-                    acc = mm<3>(k, Sp[ks], acc);
-                }
-                const f32x4 gam = *reinterpret_cast<const f32x4*>(&sm.gam[16 * tb + 4 * lg]);
-                const f32x4 beta = *reinterpret_cast<const f32x4*>(&sm.beta[16 * tb + 4 * lg]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) R[tb][q] = beta[q] * __builtin_fmaf(-gam[q], acc[q], v[4 * tb + q]);
+            for (int ct = 0; ct < CT; ++ct) {
+                bf16x8 s[3];
+                sm.S[ct].get(ks, lane, s);
+                u[ct] = mm<3>(k, s, u[ct]);
+                if constexpr (!KEEP) y[ct] = mm<OA>(Q[ks], s, y[ct]);
             }
-            split_tiles<3>(R[0], R[1], Bp[0]);
-            split_tiles<3>(R[2], R[3], Bp[1]);
+        }
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) {
-                U[tb] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int ct = 0; ct < CT; ++ct) {
+            f32x4 r;
 #pragma unroll
-                for (int ks = 0; ks <= tb / 2; ++ks) {
-                    bf16x8 t[3];
-                    ld_frag(sm.T, frag(tb, ks), lane, t);
-                    U[tb] = mm<3>(t, Bp[ks], U[tb]);
-                }
+            for (int q = 0; q < 4; ++q) r[q] = beta[q] * __builtin_fmaf(-gam[q], u[ct][q], v[ct][q]);
+            sm.R[ct].put_tile(w, r, lane);
+        }
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                float* ks = keep_s + ((bh * nch + c) * pad + p0 + 16 * ct) * NP + 4 * lg;
+#pragma unroll
+                for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(ks + 16 * (NT * w + i)) = S[i][ct];
             }
+        }
+        lds_barrier();
+        // U for the wave's tokens
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            u[ct] = z4;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8 r[3];
+                sm.R[ct].get(ks, lane, r);
+                u[ct] = mm<3>(T[ks], r, u[ct]);
+            }
+            sm.W[ct].put_tile(w, u[ct] * tail, lane);
+            if constexpr (!KEEP) sm.U[ct].put_tile(w, u[ct], lane);
             if constexpr (KEEP) {
-                float* ku = keep_u + (bh * nch + c) * kC * pad + p;
+                float* ku = keep_u + (bh * nch + c) * kC * pad + p0 + 16 * ct;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) ku[(16 * (i >> 2) + 4 * lg + (i & 3)) * pad] = U[i >> 2][i & 3];
-                float* ks = keep_s + ((bh * nch + c) * pad + p) * NP + 4 * lg;
-#pragma unroll
-                for (int i = 0; i < NB; ++i) *reinterpret_cast<f32x4*>(ks + 16 * i) = S[i];
-            } else {
-                // y
-                split_tiles<3>(U[0], U[1], Bp[0]);
-                split_tiles<3>(U[2], U[3], Bp[1]);
-#pragma unroll
-                for (int tb = 0; tb < 4; ++tb) {
-                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int ks = 0; ks < KS; ++ks) {
-                        bf16x8 x[NK];
-#pragma unroll
-                        for (int i = 0; i < NK; ++i) x[i] = ld8(&sm.Q[i][16 * tb + li][32 * ks + 8 * lg]);
-                        acc = mm<OL>(x, Sp[ks], acc);
-                    }
-                    acc *= *reinterpret_cast<const f32x4*>(&sm.gam[16 * tb + 4 * lg]);
-#pragma unroll
-                    for (int ks = 0; ks <= tb / 2; ++ks) {
-                        bf16x8 x[OL];
-                        ld_frag(sm.A, frag(tb, ks), lane, x);
-                        acc = mm<OL>(x, Bp[ks], acc);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int64_t t = t0 + 16 * tb + 4 * lg + q;
-                        if (pok && t < a.L) io::st(Yg + ((b * a.L + t) * a.H + h) * a.P + p, a.scale * acc[q]);
-                    }
-                }
+                for (int q = 0; q < 4; ++q) ku[(16 * w + 4 * lg + q) * pad] = u[ct][q];
             }
-            // the next state
-            const float gl = sm.gam[kC - 1];
+        }
+        lds_barrier();
+        // the wave's rows of the next state
 #pragma unroll
-            for (int tb = 0; tb < 4; ++tb) U[tb] *= *reinterpret_cast<const f32x4*>(&sm.tail[16 * tb + 4 * lg]);
-            split_tiles<3>(U[0], U[1], Bp[0]);
-            split_tiles<3>(U[2], U[3], Bp[1]);
+        for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int i = 0; i < NB; ++i) {
-                S[i] *= gl;
+            for (int ct = 0; ct < CT; ++ct) S[i][ct] *= gl;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            bf16x8 k[NT][NK];
+#pragma unroll
+            for (int i = 0; i < NT; ++i)
+#pragma unroll
+                for (int x = 0; x < NK; ++x)
+                    k[i][x] = ld_down<true>(K + x * kC * kRow, kRow, 32 * ks, 16 * (NT * w + i), lane);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                bf16x8 x[3];
+                sm.W[ct].get(ks, lane, x);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) S[i][ct] = mm<3>(k[i], x, S[i][ct]);
+            }
+        }
+        put_state();
+        if constexpr (!KEEP) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                y[ct] *= gam;
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
-                    bf16x8 k[NK];
-#pragma unroll
-                    for (int x = 0; x < NK; ++x) k[x] = ld_down<true>(&sm.K[x][0][0], kRow, 32 * ks, 16 * i, lane);
-                    S[i] = mm<3>(k, Bp[ks], S[i]);
+                    bf16x8 x[OA];
+                    sm.U[ct].get(ks, lane, x);
+                    y[ct] = mm<OA>(A[ks], x, y[ct]);
                 }
             }
         }
-        __syncthreads();
-        if (c + 1 < mine) stage();
-        __syncthreads();
+        ready(c + 1);
+        lds_barrier();
     }
-    if (!KEEP && pok) {
-        for (int64_t t = mine * kC + lg; t < a.L; t += 4) io::st(Yg + ((b * a.L + t) * a.H + h) * a.P + p, 0.0f);
-        if (a.last) {
+    put_y(mine - 1);
 #pragma unroll
-            for (int i = 0; i < NB; ++i)
+    for (int ct = 0; ct < CT; ++ct) {
+        const int p = p0 + 16 * ct;
+        if (p >= P) continue;
+        if constexpr (!KEEP) {
+            for (int64_t t = (int64_t)mine * kC + 4 * w + lg; t < a.L; t += 16)
+                io::st(reinterpret_cast<Tout*>(Yg + t * sy) + p, 0.0f);
+            if (a.last) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = 16 * i + 4 * lg + q;
-                    if (n < N) a.last[(bh * a.P + p) * N + n] = S[i][q];
-                }
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int n = 16 * (NT * w + i) + 4 * lg + q;
+                        if (n < N) a.last[(bh * P + p) * N + n] = S[i][ct][q];
+                    }
+            }
         }
     }
 }
 
 template <typename Tin, typename Tout, int NP, bool KEEP>
 hipError_t launch(const DeltaArgs& a, const float* recs, float* keep_s, float* keep_u, int pad, hipStream_t stream) {
-    constexpr int W = 4;
-    constexpr int bytes = (int)sizeof(ScanSmem<Tin, NP, KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3>);
-    const auto kern = &delta_scan_kernel<Tin, Tout, NP, W, KEEP>;
+    constexpr int CT = 1;
+    constexpr int bytes = (int)sizeof(ScanSmem<Tin, NP, CT, KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3>);
+    static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
+    const auto kern = &delta_scan_kernel<Tin, Tout, NP, CT, KEEP>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
-    const int npb = (int)((a.P + 16 * W - 1) / (16 * W));
+    const int npb = (int)(((KEEP ? pad : a.P) + 16 * CT - 1) / (16 * CT));
     const int64_t units = (a.batch * a.H + 7) / 8 * 8;
     KTime kt(KEEP ? "delta_keep" : "delta_scan", stream);
-    hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(64 * W), bytes, stream, a, recs, delta_chunks(a.L), npb,
+    hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(256), bytes, stream, a, recs, delta_chunks(a.L), npb,
                        keep_s, keep_u, pad);
     return hipGetLastError();
 }

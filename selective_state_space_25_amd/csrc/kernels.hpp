@@ -213,16 +213,20 @@ struct DeltaArgs {
     float* last;
     int64_t batch, L, H, P, G;
     int N;
+    int NL;                   // chunked form: elements of a q or k row that are read (a multiple of 8),
+    int64_t qk_row;           // and from one group's row to the next
     float scale;
-    int vec;                  // rows of q, k and the states allow vector access
+    int vec;                  // token by token: rows of q, k and the states allow vector access
 };
 hipError_t launch_delta_rec(const DeltaArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
 // The chunked form: records of delta_record_bytes() for each of the
-// batch x H x delta_chunks(L) chunks (vec: rows of q and k on 16-byte
-// boundaries, N % 8 == 0), then the scan over them.
+// batch x H x delta_chunks(L) chunks, then the scan over them.  Rows of q and
+// k that are not made of aligned 16-byte pieces are copied first, padded to
+// 64 or 128 elements (2 batch L G of them in `rows`; a is set to the copies).
 int64_t delta_chunks(int64_t L);
-size_t delta_record_bytes();
-hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, float* recs, hipStream_t stream);
+size_t delta_record_bytes(bool grad);
+hipError_t launch_delta_pad(DeltaArgs& a, int in_bf16, void* rows, hipStream_t stream);
+hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, bool grad, float* recs, hipStream_t stream);
 hipError_t launch_delta_scan(const DeltaArgs& a, int in_bf16, int out_bf16, const float* recs, hipStream_t stream);
 
 // Gradients of the gated delta rule; the arrays below dh0 are workspace
@@ -240,7 +244,7 @@ struct DeltaBwdArgs {
     float* dR;                // [chunks, 64, pad]
     float *pq, *pk;           // [batch, L, H, N] per-head dq and dk when heads share q and k, else NULL
     int pad;                  // P rounded up to 32
-    int vec_p;                // rows of v and dout on 16-byte boundaries, P % 8 == 0
+    int vec_p;                // rows of dout on 16-byte boundaries, P % 8 == 0
 };
 size_t delta_bwd_bytes(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N);
 void delta_bwd_carve(DeltaBwdArgs& a, void* ws);

@@ -22,6 +22,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4* lds_s16x4;
 
 // v_mfma_f32_16x16x32_bf16.  Lane l = 16 g + i: operand A holds row i,
@@ -43,33 +44,47 @@ __device__ __forceinline__ f32x4 mm(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB]
     return c;
 }
 
-// One value into element e of NP planes.
+// Pairs e, e + 1 of two values into word `e` of NP planes (a plane is one
+// operand, four words of two bf16 each).
 template <int NP>
-__device__ __forceinline__ void split(float v, bf16x8 (&p)[NP], int e) {
+__device__ __forceinline__ void split2(float a, float b, u32x4 (&p)[NP], int e) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-        const __bf16 h = (__bf16)v;
-        p[i][e] = h;
-        if (i + 1 < NP) v -= (float)h;
+        const uint32_t w = pack_bf16x2(a, b);
+        p[i][e] = w;
+        if (i + 1 < NP) {
+            a -= bf16lo(w);
+            b -= bf16hi(w);
+        }
     }
+}
+
+template <int NP>
+__device__ __forceinline__ void as_operand(const u32x4 (&w)[NP], bf16x8 (&p)[NP]) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) p[i] = __builtin_bit_cast(bf16x8, w[i]);
+}
+
+// Eight values (two groups of four) into NP planes.
+template <int NP>
+__device__ __forceinline__ void split8(f32x4 lo, f32x4 hi, bf16x8 (&p)[NP]) {
+    u32x4 w[NP];
+    split2<NP>(lo[0], lo[1], w, 0);
+    split2<NP>(lo[2], lo[3], w, 1);
+    split2<NP>(hi[0], hi[1], w, 2);
+    split2<NP>(hi[2], hi[3], w, 3);
+    as_operand(w, p);
 }
 
 // Two C tiles (rows r0 .. r0 + 15 and r0 + 16 .. r0 + 31 of one column
-// block) as the B operand of a product over those 32 rows, k in the order in
-// which the lanes hold them: lane group g has rows r0 + 4 g + q, then
-// r0 + 16 + 4 g + q.  The A operand has to be read in that order (kperm).
-template <int NP>
-__device__ __forceinline__ void split_tiles(f32x4 t0, f32x4 t1, bf16x8 (&p)[NP]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        split<NP>(t0[q], p, q);
-        split<NP>(t1[q], p, 4 + q);
-    }
-}
+// block) make the B operand of a product over those 32 rows with k in the
+// order in which the lanes hold them: lane group g has rows r0 + 4 g + q,
+// then r0 + 16 + 4 g + q ("tile order").  The A operand has to be read in
+// that order: kperm, ld_down.
 
 // Position of column n in a row whose 4-element pieces are permuted inside
-// each group of 32 so that one 16-byte read gives a lane group the k order of
-// split_tiles: pieces 0 .. 7 at positions 0, 2, 4, 6, 1, 3, 5, 7.
+// each group of 32 so that one 16-byte read gives a lane group the tile
+// order: pieces 0 .. 7 at positions 0, 2, 4, 6, 1, 3, 5, 7.
 __device__ __forceinline__ int kperm(int n) {
     const int pc = (n & 31) >> 2;
     return (n & ~31) + 4 * (pc < 4 ? 2 * pc : 2 * pc - 7) + (n & 3);
@@ -92,7 +107,7 @@ __device__ __forceinline__ s16x4 ld_tr(const uint16_t* p) {
 }
 
 // Operand with k running down the rows of m (row stride rs), columns
-// c0 .. c0 + 15: k = rows r0 .. r0 + 31 in split_tiles' order.  PERM: m's
+// c0 .. c0 + 15: k = rows r0 .. r0 + 31 in tile order.  PERM: m's
 // columns are stored through kperm.
 template <bool PERM>
 __device__ __forceinline__ bf16x8 ld_down(const uint16_t* m, int rs, int r0, int c0, int lane) {
@@ -113,8 +128,7 @@ __device__ __forceinline__ bf16x8 ld_down8(const uint16_t* m, int rs, int r0, in
 
 // Four consecutive values into NP planes of 4 bf16 each.
 template <int NP>
-__device__ __forceinline__ void split4(const float (&v)[4], uint2 (&p)[NP]) {
-    float r[4] = {v[0], v[1], v[2], v[3]};
+__device__ __forceinline__ void split4(f32x4 r, uint2 (&p)[NP]) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
         p[i] = make_uint2(pack_bf16x2(r[0], r[1]), pack_bf16x2(r[2], r[3]));
