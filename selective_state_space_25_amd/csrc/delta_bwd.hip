@@ -81,18 +81,23 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
             }
     auto put_state = [&]() {
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            if constexpr (NT == 2) sm.D[ct].put(w, D[0][ct], D[1][ct], lane);
-            else sm.D[ct].put_tile(w, D[0][ct], lane);
-        }
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) sm.D[ct].put_tile(NT * w + i, D[i][ct], lane);
     };
-    int koff[NPC], roff, voff[CT], ooff[CT];
+    int koff[NPC], roff[KS], toff[2], voff[CT], ooff[CT];
 #pragma unroll
     for (int i = 0; i < NPC; ++i) {
         const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
         koff[i] = n0 < a.NL ? r * (int)sk + n0 * ES : kOut;
     }
-    roff = (16 * w + li) * (int)sk + 4 * lg * ES;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+        const int n = 32 * ks + 8 * lg;
+        roff[ks] = n < a.NL ? (16 * w + li) * (int)sk + n * ES : kOut;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) toff[ks] = row_of_t(w, ks, lane);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         const int p = p0 + 16 * ct;
@@ -100,62 +105,57 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
         ooff[ct] = p < P ? (16 * w + 4 * lg) * (int)so + p * EO : kOut;
     }
 
-    int toff[4];   // rows 16 w .. of the transposed matrices: blocks (t, w); above the diagonal none, zeros
-#pragma unroll
-    for (int t = 0; t < 4; ++t) toff[t] = t >= w ? (block_at(t, w) + li * 16 + 4 * lg) * 4 : kOut;
-
+    // inputs on their way, as in delta_scan.hip (before the first chunk the
+    // first one is read again)
     Raw8<Tin> fk[NPC], fq[NPC], fr[KS];
-    f32x4 ft[4], fa[4], fgate[3];
+    f32x4 ft[2][2], fa[2][2], fgate[3];
     float fgl;
     Tdo fo[CT][4];
-    auto fetch = [&](int c) {
-        const int64_t t0 = (int64_t)c * kC;
-        const int live = (int)min((int64_t)kC, len - t0);
-        const auto kb = rows_buf(Kg + t0 * sk, live, sk, a.NL * ES);
-        const auto qb = rows_buf(Qg + t0 * sk, live, sk, a.NL * ES);
-        const auto ob = rows_buf(Og + t0 * so, live, so, P * EO);
-        const auto rb = rows_buf(ba.recs + (bh * nch + c) * kRecGrad, 1, 0, kRecGrad * 4);
+    auto rows = [&](const char* base, int64_t stride, int c, int bytes) {
+        const int64_t t0 = (int64_t)max(c, 0) * kC;
+        return rows_buf(base + t0 * stride, (int)min((int64_t)kC, len - t0), stride, bytes);
+    };
+    auto record = [&](int c) { return rows_buf(ba.recs + (bh * nch + max(c, 0)) * kRecGrad, 1, 0, kRecGrad * 4); };
+    auto fetch_p = [&](const char* base, int c, Raw8<Tin> (&f)[NPC]) {
+        const auto kb = rows(base, sk, c, a.NL * ES);
+#pragma unroll
+        for (int i = 0; i < NPC; ++i) fetch8(kb, koff[i], f[i]);
+    };
+    auto fetch_r = [&](int c) {
+        const auto kb = rows(Kg, sk, c, a.NL * ES);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) fetch8(kb, roff[ks], fr[ks]);
+    };
+    auto fetch_o = [&](int c) {
+        const auto ob = rows(Og, so, c, P * EO);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int q = 0; q < 4; ++q) fo[ct][q] = buf_raw<Tdo>(ob, ooff[ct] + q * (int)so);
+    };
+    auto fetch_g = [&](int c) {
+        const auto rb = record(c);
 #pragma unroll
         for (int i = 0; i < 3; ++i) fgate[i] = buf_ld4(rb, (kRecGam + i * kC + 16 * w + 4 * lg) * 4);
         fgl = buf_raw<float>(rb, (kRecGam + kC - 1) * 4);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) fetch_row(kb, roff + 32 * ks * ES, fr[ks]);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-            fa[t] = buf_ld4(rb, toff[t] + kRecAt * 4);
-            ft[t] = buf_ld4(rb, toff[t] + kRecTt * 4);
-        }
-#pragma unroll
-        for (int i = 0; i < NPC; ++i) {
-            fetch8(kb, koff[i], fk[i]);
-            fetch8(qb, koff[i], fq[i]);
-        }
     };
-    bf16x8 Kr[KS][NK], T[2][3], A[2][3];
-    f32x4 gam, tail, beta, o[CT];
-    float gl;
-    auto ready = [&]() {
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            if (a.NL < NP) {
-                const int n = 32 * ks + 4 * lg;
-                keep_row(fr[ks], n < a.NL, n + 16 < a.NL);
-            }
-            to_operand(fr[ks], Kr[ks]);
-        }
+    auto fetch_m = [&](int c, int at, f32x4 (&f)[2][2]) {
+        const auto rb = record(c);
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-            split8<3>(ft[2 * ks], ft[2 * ks + 1], T[ks]);
-            split8<3>(fa[2 * ks], fa[2 * ks + 1], A[ks]);
+            f[ks][0] = buf_ld4(rb, toff[ks] + at * 4);
+            f[ks][1] = buf_ld4(rb, toff[ks] + at * 4 + 16);
         }
-        gam = fgate[0];
-        tail = fgate[1];
-        beta = fgate[2];
-        gl = fgl;
+    };
+    auto stage_p = [&](uint16_t (*m)[kC][kRow], const Raw8<Tin> (&f)[NPC]) {
+#pragma unroll
+        for (int i = 0; i < NPC; ++i) {
+            const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+            stage8(m[0][r], kC * kRow, n0, f[i]);
+        }
+    };
+    f32x4 o[CT];
+    auto put_o = [&]() {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
             o[ct] = widen(fo[ct]);
@@ -165,66 +165,95 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
 
     put_state();
     if (mine > 0) {
-        fetch(mine - 1);
-        ready();
+        const int c = mine - 1;
+        fetch_o(c);
+        fetch_r(c);
+        fetch_m(c, kRecAt, fa);
+        fetch_g(c);
+        fetch_p(Kg, c, fk);
+        fetch_m(c, kRecTt, ft);
+        fetch_p(Qg, c, fq);
+        put_o();
+        fetch_o(c - 1);
     }
     lds_barrier();
     for (int c = mine - 1; c >= 0; --c) {
         const int64_t t0 = (int64_t)c * kC;
         const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < NPC; ++i) {
-            const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-            stage8<false>(sm.K[0][r], kC * kRow, n0, fk[i]);
-            stage8<false>(sm.Q[0][r], kC * kRow, n0, fq[i]);
-        }
-        fetch(max(c - 1, 0));
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) sm.G[ct].put_tile(w, o[ct] * gam * a.scale, lane);
         // dU for the wave's tokens
         f32x4 u[CT], x[CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) u[ct] = x[ct] = z4;
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
+        for (int ks = 0; ks < KS; ++ks) {
+            bf16x8 k[NK];
+            to_operand(fr[ks], k);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 bf16x8 d[3];
                 sm.D[ct].get(ks, lane, d);
-                u[ct] = mm<3>(Kr[ks], d, u[ct]);
+                u[ct] = mm<3>(k, d, u[ct]);
             }
+        }
+        fetch_r(c - 1);
+        {
+            bf16x8 A[2][3];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) split8<3>(fa[ks][0], fa[ks][1], A[ks]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    bf16x8 d[NO];
+                    sm.O[ct].get(ks, lane, d);
+                    x[ct] = mm<3>(A[ks], d, x[ct]);
+                }
+        }
+        fetch_m(c - 1, kRecAt, fa);
+        const f32x4 gam = fgate[0], tail = fgate[1], beta = fgate[2];
+        const float gl = fgl;
+        fetch_g(c - 1);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 d[NO];
-                sm.O[ct].get(ks, lane, d);
-                x[ct] = mm<3>(A[ks], d, x[ct]);
-            }
             sm.U[ct].put_tile(w, u[ct] * tail + x[ct] * a.scale, lane);
+            sm.G[ct].put_tile(w, o[ct] * gam * a.scale, lane);
             float* kd = ba.D + ((bh * nch + c) * pad + p0 + 16 * ct) * NP + 4 * lg;
 #pragma unroll
             for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(kd + 16 * (NT * w + i)) = D[i][ct];
         }
+        stage_p(sm.K, fk);
+        fetch_p(Kg, c - 1, fk);
         lds_barrier();
         // dR and dV for the wave's tokens
+        f32x4 r[CT];
+        {
+            bf16x8 T[2][3];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) split8<3>(ft[ks][0], ft[ks][1], T[ks]);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                r[ct] = z4;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    bf16x8 y[3];
+                    sm.U[ct].get(ks, lane, y);
+                    r[ct] = mm<3>(T[ks], y, r[ct]);
+                }
+                sm.R[ct].put_tile(w, -(r[ct] * beta * gam), lane);
+            }
+        }
+        fetch_m(c - 1, kRecTt, ft);
+        stage_p(sm.Q, fq);
+        fetch_p(Qg, c - 1, fq);
         const auto vb = rows_buf(dVg + t0 * sv, (int)min((int64_t)kC, a.L - t0), sv, P * ES);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            f32x4 r = z4;
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 y[3];
-                sm.U[ct].get(ks, lane, y);
-                r = mm<3>(T[ks], y, r);
-            }
-            const f32x4 dv = r * beta;
-            sm.R[ct].put_tile(w, -(dv * gam), lane);
             float* kr = ba.dR + (bh * nch + c) * kC * pad + p0 + 16 * ct;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) kr[(16 * w + 4 * lg + q) * pad] = r[q];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) buf_st(vb, voff[ct] + q * (int)sv, dv[q], Tin(0));
+            for (int q = 0; q < 4; ++q) {
+                kr[(16 * w + 4 * lg + q) * pad] = r[ct][q];
+                buf_st(vb, voff[ct] + q * (int)sv, beta[q] * r[ct][q], Tin(0));
+            }
         }
         lds_barrier();
         // the wave's rows of the adjoint before the chunk
@@ -239,23 +268,24 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
             for (int i = 0; i < NT; ++i)
 #pragma unroll
                 for (int l = 0; l < NK; ++l) {
-                    k[i][l] = ld_down<false>(&sm.K[l][0][0], kRow, 32 * ks, 16 * (NT * w + i), lane);
-                    q[i][l] = ld_down<false>(&sm.Q[l][0][0], kRow, 32 * ks, 16 * (NT * w + i), lane);
+                    k[i][l] = ld_down(&sm.K[l][0][0], kRow, 32 * ks, 16 * (NT * w + i), lane);
+                    q[i][l] = ld_down(&sm.Q[l][0][0], kRow, 32 * ks, 16 * (NT * w + i), lane);
                 }
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                bf16x8 r[3], g[3];
-                sm.R[ct].get(ks, lane, r);
+                bf16x8 y[3], g[3];
+                sm.R[ct].get(ks, lane, y);
                 sm.G[ct].get(ks, lane, g);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) {
-                    D[i][ct] = mm<3>(k[i], r, D[i][ct]);
+                    D[i][ct] = mm<3>(k[i], y, D[i][ct]);
                     D[i][ct] = mm<3>(q[i], g, D[i][ct]);
                 }
             }
         }
         put_state();
-        ready();
+        put_o();
+        fetch_o(c - 2);
         lds_barrier();
     }
 #pragma unroll
@@ -360,9 +390,10 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     // ---- sums over the value columns: dO S^T, dR S^T, U D^T for the wave's
     // tokens, dO U^T and dR U^T for its row block, <S, D>, dR.V
     const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
-    f32x4 q1[NB], k2[NB], k3[NB], x1[4], x2[4];
+    // (U D^T in two sums: D may be far larger than what of it reaches dg)
+    f32x4 q1[NB], k2[NB], k3[NB], k3r[NB], x1[4], x2[4];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) q1[i] = k2[i] = k3[i] = z4;
+    for (int i = 0; i < NB; ++i) q1[i] = k2[i] = k3[i] = k3r[i] = z4;
 #pragma unroll
     for (int i = 0; i < 4; ++i) x1[i] = x2[i] = z4;
     double sd = 0.0;
@@ -424,7 +455,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 for (int i = 0; i < 8; ++i) e[i] = buf_ld<Tdo>(ob, pb + e0 + i < P ? off + i * EO : kOut);
                 from_floats(e, o);
             }
-            stage8<false>(sm.s.O[0][r], kC * kRowP, e0, o);
+            stage8(sm.s.O[0][r], kC * kRowP, e0, o);
         }
         __syncthreads();
         bf16x8 o[NO], r[3], u[3];
@@ -440,12 +471,12 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             bf16x8 s[3], d[3];
 #pragma unroll
             for (int x = 0; x < 3; ++x) {
-                s[x] = ld_down8<false>(&sm.s.S[x][0][0], kRow, 0, 16 * i, lane);
-                d[x] = ld_down8<false>(&sm.s.D[x][0][0], kRow, 0, 16 * i, lane);
+                s[x] = ld_down(&sm.s.S[x][0][0], kRow, 0, 16 * i, lane);
+                d[x] = ld_down(&sm.s.D[x][0][0], kRow, 0, 16 * i, lane);
             }
             q1[i] = mm<3>(o, s, q1[i]);
             k2[i] = mm<3>(r, s, k2[i]);
-            k3[i] = mm<3>(u, d, k3[i]);
+            mm2<3>(u, d, k3[i], k3r[i]);
         }
 #pragma unroll
         for (int sb = 0; sb < 4; ++sb) {
@@ -479,8 +510,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             Raw8<Tin> k, q;
             fetch8(kb, off, k);
             fetch8(qb, off, q);
-            stage8<false>(sm.m.K[0][r], kC * kRow, n0, k);
-            stage8<false>(sm.m.Q[0][r], kC * kRow, n0, q);
+            stage8(sm.m.K[0][r], kC * kRow, n0, k);
+            stage8(sm.m.Q[0][r], kC * kRow, n0, q);
         }
     }
     __syncthreads();
@@ -503,7 +534,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             }
             aq[q] = __builtin_fma((double)qv, (double)q1[i][q], aq[q]);
             ak[q] = __builtin_fma((double)kv, (double)k2[i][q], ak[q]);
-            bk[q] = __builtin_fma((double)kv, (double)k3[i][q], bk[q]);
+            bk[q] = __builtin_fma((double)kv, (double)k3[i][q] + (double)k3r[i][q], bk[q]);
+            k3[i][q] += k3r[i][q];
             q1[i][q] *= a.scale * gam[q];
             k3[i][q] = __builtin_fmaf(tail[q], k3[i][q], -beta[q] * gam[q] * k2[i][q]);
         }
@@ -536,8 +568,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 const float e0 = -x2[sb][q] * gl;             // E without beta
                 xv[q] = a.scale * x1[sb][q] * g;
                 ev[q] = beta[q] * e0;
-                const float ekk = e0 * kk[q];
-                const float zv = (s < t ? a.scale * x1[sb][q] * ab[(4 * lg + q) * 16] : 0.0f) + beta[q] * ekk;
+                const double ekk = (double)e0 * kk[q];
+                const double zv = (s < t ? (double)a.scale * x1[sb][q] * ab[(4 * lg + q) * 16] : 0.0) + beta[q] * ekk;
                 rb[q] += ekk;
                 row[q] += zv;
                 cz += zv;
@@ -610,22 +642,22 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 e[l] = ld8(&sm.m.E[l][16 * tb + li][32 * ks + 8 * lg]);
             }
             if (hi) {
-                xt[l] = ld_down8<false>(&sm.m.X[l][0][0], kRowX, 32 * ks, 16 * tb, lane);
-                et[l] = ld_down8<false>(&sm.m.E[l][0][0], kRowX, 32 * ks, 16 * tb, lane);
+                xt[l] = ld_down(&sm.m.X[l][0][0], kRowX, 32 * ks, 16 * tb, lane);
+                et[l] = ld_down(&sm.m.E[l][0][0], kRowX, 32 * ks, 16 * tb, lane);
             }
         }
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
             bf16x8 k[NK], q[NK];
 #pragma unroll
-            for (int p = 0; p < NK; ++p) k[p] = ld_down8<false>(&sm.m.K[p][0][0], kRow, 32 * ks, 16 * i, lane);
+            for (int p = 0; p < NK; ++p) k[p] = ld_down(&sm.m.K[p][0][0], kRow, 32 * ks, 16 * i, lane);
             if (lo) {
                 q1[i] = mm<LB>(x, k, q1[i]);
                 k3[i] = mm<LB>(e, k, k3[i]);
             }
             if (hi) {
 #pragma unroll
-                for (int p = 0; p < NK; ++p) q[p] = ld_down8<false>(&sm.m.Q[p][0][0], kRow, 32 * ks, 16 * i, lane);
+                for (int p = 0; p < NK; ++p) q[p] = ld_down(&sm.m.Q[p][0][0], kRow, 32 * ks, 16 * i, lane);
                 k3[i] = mm<LB>(et, k, k3[i]);
                 k3[i] = mm<LB>(xt, q, k3[i]);
             }

@@ -88,8 +88,8 @@ __device__ __forceinline__ void buf_st(__amdgpu_buffer_rsrc_t r, int off, float 
     __builtin_amdgcn_raw_buffer_store_b16(f32_to_bf16(v), r, off, 0, 0);
 }
 
-// Eight consecutive elements of a row as loaded, and into the planes of a
-// staged row (plane stride ps elements; PERM: columns through kperm).
+// Eight consecutive elements of a row as loaded, into the planes of a staged
+// row (plane stride ps elements), and as an operand.
 template <typename T> struct Raw8;
 template <> struct Raw8<uint16_t> { u32x4 w; };
 template <> struct Raw8<float> { f32x4 lo, hi; };
@@ -101,46 +101,14 @@ __device__ __forceinline__ void fetch8(__amdgpu_buffer_rsrc_t b, int off, Raw8<f
     r.lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
     r.hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 16, 0));
 }
-template <bool PERM>
 __device__ __forceinline__ void stage8(uint16_t* row, int ps, int n0, const Raw8<uint16_t>& r) {
-    if constexpr (PERM) {
-        *reinterpret_cast<uint2*>(row + kperm(n0)) = make_uint2(r.w[0], r.w[1]);
-        *reinterpret_cast<uint2*>(row + kperm(n0 + 4)) = make_uint2(r.w[2], r.w[3]);
-    } else {
-        *reinterpret_cast<u32x4*>(row + n0) = r.w;
-    }
+    *reinterpret_cast<u32x4*>(row + n0) = r.w;
 }
-template <bool PERM>
 __device__ __forceinline__ void stage8(uint16_t* row, int ps, int n0, const Raw8<float>& r) {
-    uint2 pa[3], pb[3];
-    split4<3>(r.lo, pa);
-    split4<3>(r.hi, pb);
+    bf16x8 p[3];
+    split8<3>(r.lo, r.hi, p);
 #pragma unroll
-    for (int p = 0; p < 3; ++p) {
-        *reinterpret_cast<uint2*>(row + p * ps + (PERM ? kperm(n0) : n0)) = pa[p];
-        *reinterpret_cast<uint2*>(row + p * ps + (PERM ? kperm(n0 + 4) : n0 + 4)) = pb[p];
-    }
-}
-
-// An A operand row straight from memory in tile order: k-step at column n0
-// of the lane's row takes columns n0 + 4 g .. and n0 + 16 + 4 g ...
-__device__ __forceinline__ void fetch_row(__amdgpu_buffer_rsrc_t b, int off, Raw8<uint16_t>& r) {
-    const auto lo = __builtin_amdgcn_raw_buffer_load_b64(b, off, 0, 0);
-    const auto hi = __builtin_amdgcn_raw_buffer_load_b64(b, off, 32, 0);
-    r.w = u32x4{lo[0], lo[1], hi[0], hi[1]};
-}
-__device__ __forceinline__ void fetch_row(__amdgpu_buffer_rsrc_t b, int off, Raw8<float>& r) {
-    r.lo = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 0, 0));
-    r.hi = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(b, off, 64, 0));
-}
-// ... its two groups of four columns zero unless lo, hi
-__device__ __forceinline__ void keep_row(Raw8<uint16_t>& r, bool lo, bool hi) {
-    r.w = u32x4{lo ? r.w[0] : 0u, lo ? r.w[1] : 0u, hi ? r.w[2] : 0u, hi ? r.w[3] : 0u};
-}
-__device__ __forceinline__ void keep_row(Raw8<float>& r, bool lo, bool hi) {
-    const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-    r.lo = lo ? r.lo : z;
-    r.hi = hi ? r.hi : z;
+    for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8*>(row + i * ps + n0) = p[i];
 }
 __device__ __forceinline__ void to_operand(const Raw8<uint16_t>& r, bf16x8 (&p)[1]) {
     p[0] = __builtin_bit_cast(bf16x8, r.w);
@@ -154,29 +122,36 @@ __device__ __forceinline__ void lower_tile(int k, int& tb, int& sb) {
 }
 
 // B operands that waves hand to each other through LDS: NPL planes of KS
-// k-steps in tile order, each lane's 16 bytes in its own slot.
+// k-steps, k in natural order, each lane's 16 bytes in its own slot.
 template <int KS, int NPL>
 struct Operands {
     uint16_t p[KS][NPL][64][8];
-    // C tile t of the operand's rows (half t % 2 of k-step t / 2), split
+    // C tile t of the operand's rows, split.  Its lane group g holds rows
+    // 16 t + 4 g ..: half g % 2 of what lane group 2 (t % 2) + g / 2 reads.
     __device__ __forceinline__ void put_tile(int t, f32x4 v, int lane) {
         uint2 w[NPL];
         split4<NPL>(v, w);
+        const int at = 16 * (2 * (t & 1) + (lane >> 5)) + (lane & 15), e = 4 * ((lane >> 4) & 1);
 #pragma unroll
-        for (int i = 0; i < NPL; ++i) *reinterpret_cast<uint2*>(&p[t >> 1][i][lane][4 * (t & 1)]) = w[i];
-    }
-    // both tiles of k-step ks
-    __device__ __forceinline__ void put(int ks, f32x4 lo, f32x4 hi, int lane) {
-        bf16x8 w[NPL];
-        split8<NPL>(lo, hi, w);
-#pragma unroll
-        for (int i = 0; i < NPL; ++i) *reinterpret_cast<bf16x8*>(p[ks][i][lane]) = w[i];
+        for (int i = 0; i < NPL; ++i) *reinterpret_cast<uint2*>(&p[t >> 1][i][at][e]) = w[i];
     }
     __device__ __forceinline__ void get(int ks, int lane, bf16x8 (&w)[NPL]) const {
 #pragma unroll
         for (int i = 0; i < NPL; ++i) w[i] = ld8(p[ks][i][lane]);
     }
 };
+
+// Byte offset in a record of the lane's eight floats of row block tb of T
+// (columns 32 ks + 8 g ..; kOut above the diagonal, where it is zero), and
+// of row block jb of T's transpose.
+__device__ __forceinline__ int row_of(int tb, int ks, int lane) {
+    const int s = 2 * ks + (lane >> 5);
+    return s <= tb ? (block_at(tb, s) + (lane & 15) * 16 + 8 * ((lane >> 4) & 1)) * 4 : kOut;
+}
+__device__ __forceinline__ int row_of_t(int jb, int ks, int lane) {
+    const int t = 2 * ks + (lane >> 5);
+    return t >= jb ? (block_at(t, jb) + (lane & 15) * 16 + 8 * ((lane >> 4) & 1)) * 4 : kOut;
+}
 
 }  // namespace dchunk
 }  // namespace selscan

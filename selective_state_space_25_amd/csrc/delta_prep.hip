@@ -94,8 +94,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, float* rec
 #pragma unroll
         for (int i = 0; i < NP / 32; ++i) {
             const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-            stage8<false>(sm.K[0][r], kC * kRow, n0, x[i]);
-            stage8<false>(sm.Q[0][r], kC * kRow, n0, y[i]);
+            stage8(sm.K[0][r], kC * kRow, n0, x[i]);
+            stage8(sm.Q[0][r], kC * kRow, n0, y[i]);
         }
     }
     if (wave == 0) {

@@ -35,7 +35,7 @@ using namespace dchunk;
 template <typename Tin, int NP, int CT, int OL>
 struct ScanSmem {
     static constexpr int kRow = NP + 8;
-    uint16_t K[2][kPlanes<Tin>][kC][kRow];   // by chunk parity; columns through kperm
+    uint16_t K[2][kPlanes<Tin>][kC][kRow];   // by chunk parity
     Operands<NP / 32, 3> S[CT];
     Operands<2, 3> R[CT], W[CT];             // R; e^(last - cum) U
     Operands<2, OL ? OL : 1> U[CT];
@@ -89,19 +89,17 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const floa
             }
     auto put_state = [&]() {
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            if constexpr (NT == 2) sm.S[ct].put(w, S[0][ct], S[1][ct], lane);
-            else sm.S[ct].put_tile(w, S[0][ct], lane);
-        }
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int i = 0; i < NT; ++i) sm.S[ct].put_tile(NT * w + i, S[i][ct], lane);
     };
 
-    int koff[NPC], qoff, voff[CT], yoff[CT];
+    int koff[NPC], qoff[KS], toff[2], voff[CT], yoff[CT];
 #pragma unroll
     for (int i = 0; i < NPC; ++i) {
         const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
         koff[i] = n0 < a.NL ? r * (int)sk + n0 * ES : kOut;
     }
-    qoff = (16 * w + li) * (int)sk + 4 * lg * ES;
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         const int p = p0 + 16 * ct;
@@ -109,26 +107,42 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const floa
         yoff[ct] = p < P ? (16 * w + 4 * lg) * (int)sy + p * EO : kOut;
     }
 
-    int toff[4];                             // blocks (w, s) of T; above the diagonal: none, zeros
 #pragma unroll
-    for (int s = 0; s < 4; ++s) toff[s] = s <= w ? (block_at(w, s) + li * 16 + 4 * lg) * 4 : kOut;
+    for (int ks = 0; ks < KS; ++ks) {
+        const int n = 32 * ks + 8 * lg;
+        qoff[ks] = n < a.NL ? (16 * w + li) * (int)sk + n * ES : kOut;
+    }
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) toff[ks] = row_of(w, ks, lane);
 
-    // A chunk's inputs as fetched.  Loads complete in order with the stores
-    // after them, so they are turned into operands before the chunk's stores
-    // are issued and the wait for them never includes those.
+    // A chunk's inputs on their way: each is asked for as soon as the chunk
+    // before has used its registers, so that a whole chunk's work covers
+    // memory's latency and no phase is held up issuing them all.  (Past the
+    // end the last chunk is read again.)  Loads and stores complete in order:
+    // y is stored after its phase's loads, so that the waits for those find
+    // only stores a chunk older.
     Raw8<Tin> fk[NPC], fq[KS];
-    f32x4 ft[4], fa[4], fgate[3];
+    f32x4 ft[2][2], fa[2][2], fgate[3];
     float fgl;
     Tin fv[CT][4];
-    auto fetch = [&](int c) {
-        const int64_t t0 = (int64_t)c * kC;
-        const int live = (int)min((int64_t)kC, len - t0);
-        const auto kb = rows_buf(Kg + t0 * sk, live, sk, a.NL * ES);
-        const auto qb = rows_buf(Qg + t0 * sk, live, sk, a.NL * ES);
-        const auto vb = rows_buf(Vg + t0 * sv, live, sv, P * ES);
-        const auto rb = rows_buf(recs + (bh * nch + c) * kRecS, 1, 0, kRecS * 4);
+    auto rows = [&](const char* base, int64_t stride, int c, int bytes) {
+        const int64_t t0 = (int64_t)min(c, mine - 1) * kC;
+        return rows_buf(base + t0 * stride, (int)min((int64_t)kC, len - t0), stride, bytes);
+    };
+    auto record = [&](int c) { return rows_buf(recs + (bh * nch + min(c, mine - 1)) * kRecS, 1, 0, kRecS * 4); };
+    auto fetch_k = [&](int c) {
+        const auto kb = rows(Kg, sk, c, a.NL * ES);
 #pragma unroll
         for (int i = 0; i < NPC; ++i) fetch8(kb, koff[i], fk[i]);
+    };
+    auto fetch_q = [&](int c) {
+        const auto qb = rows(Qg, sk, c, a.NL * ES);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) fetch8(qb, qoff[ks], fq[ks]);
+    };
+    auto fetch_v = [&](int c) {
+        const auto vb = rows(Vg, sv, c, P * ES);
+        const auto rb = record(c);
 #pragma unroll
         for (int i = 0; i < 3; ++i) fgate[i] = buf_ld4(rb, (kRecGam + i * kC + 16 * w + 4 * lg) * 4);
         fgl = buf_raw<float>(rb, (kRecGam + kC - 1) * 4);
@@ -136,76 +150,42 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const floa
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int q = 0; q < 4; ++q) fv[ct][q] = buf_raw<Tin>(vb, voff[ct] + q * (int)sv);
+    };
+    auto fetch_m = [&](int c, int at, f32x4 (&f)[2][2]) {
+        const auto rb = record(c);
 #pragma unroll
-        for (int s = 0; s < 4; ++s) ft[s] = buf_ld4(rb, toff[s]);
-        if constexpr (!KEEP) {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) fetch_row(qb, qoff + 32 * ks * ES, fq[ks]);
-#pragma unroll
-            for (int s = 0; s < 4; ++s) fa[s] = buf_ld4(rb, toff[s] + kRecA * 4);
+        for (int ks = 0; ks < 2; ++ks) {
+            f[ks][0] = buf_ld4(rb, toff[ks] + at * 4);
+            f[ks][1] = buf_ld4(rb, toff[ks] + at * 4 + 16);
         }
     };
-    bf16x8 Q[KS][NK], T[2][3], A[2][OA];
-    f32x4 gam, tail, beta, v[CT];
-    float gl;
-    auto ready = [&](int c) {
+    auto stage_k = [&](int c) {
 #pragma unroll
         for (int i = 0; i < NPC; ++i) {
             const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-            stage8<true>(sm.K[c & 1][0][r], kC * kRow, n0, fk[i]);
-        }
-        if constexpr (!KEEP) {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                if (a.NL < NP) {   // past NL a row goes on with the next group's
-                    const int n = 32 * ks + 4 * lg;
-                    keep_row(fq[ks], n < a.NL, n + 16 < a.NL);
-                }
-                to_operand(fq[ks], Q[ks]);
-            }
-        }
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            split8<3>(ft[2 * ks], ft[2 * ks + 1], T[ks]);
-            if constexpr (!KEEP) split8<OA>(fa[2 * ks], fa[2 * ks + 1], A[ks]);
-        }
-        gam = fgate[0];
-        tail = fgate[1];
-        beta = fgate[2];
-        gl = fgl;
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) v[ct] = widen(fv[ct]);
-    };
-
-    f32x4 y[CT];
-    auto put_y = [&](int c) {   // (chunk -1: none, a buffer of no rows)
-        if constexpr (!KEEP) {
-            const int64_t t0 = (int64_t)max(c, 0) * kC;
-            const auto yb = rows_buf(Yg + t0 * sy, c < 0 ? 0 : (int)min((int64_t)kC, a.L - t0), sy, P * EO);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) buf_st(yb, yoff[ct] + q * (int)sy, a.scale * y[ct][q], Tout(0));
+            stage8(sm.K[c & 1][0][r], kC * kRow, n0, fk[i]);
         }
     };
-#pragma unroll
-    for (int ct = 0; ct < CT; ++ct) y[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
     put_state();
     if (mine > 0) {
-        fetch(0);
-        ready(0);
+        fetch_k(0);
+        fetch_v(0);
+        fetch_m(0, kRecT, ft);
+        if constexpr (!KEEP) {
+            fetch_q(0);
+            fetch_m(0, kRecA, fa);
+        }
+        stage_k(0);
+        fetch_k(1);
     }
     lds_barrier();
     for (int c = 0; c < mine; ++c) {
+        const int64_t t0 = (int64_t)c * kC;
         const uint16_t* K = &sm.K[c & 1][0][0][0];
         const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
-        // The next chunk's loads go out ahead of the last one's stores: the
-        // wait for them then finds only stores a chunk older.
-        fetch(min(c + 1, mine - 1));
-        put_y(c - 1);
-        // R for the wave's tokens; Q S
-        f32x4 u[CT];
+        // R for the wave's tokens
+        f32x4 y[CT], u[CT];
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) u[ct] = y[ct] = z4;
 #pragma unroll
@@ -218,16 +198,19 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const floa
                 bf16x8 s[3];
                 sm.S[ct].get(ks, lane, s);
                 u[ct] = mm<3>(k, s, u[ct]);
-                if constexpr (!KEEP) y[ct] = mm<OA>(Q[ks], s, y[ct]);
             }
         }
+        const f32x4 gam = fgate[0], tail = fgate[1], beta = fgate[2];
+        const float gl = fgl;
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
+            const f32x4 v = widen(fv[ct]);
             f32x4 r;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) r[q] = beta[q] * __builtin_fmaf(-gam[q], u[ct][q], v[ct][q]);
+            for (int q = 0; q < 4; ++q) r[q] = beta[q] * __builtin_fmaf(-gam[q], u[ct][q], v[q]);
             sm.R[ct].put_tile(w, r, lane);
         }
+        fetch_v(c + 1);
         if constexpr (KEEP) {
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
@@ -237,26 +220,48 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const floa
             }
         }
         lds_barrier();
-        // U for the wave's tokens
+        // U for the wave's tokens; Q S
+        {
+            bf16x8 T[2][3];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            u[ct] = z4;
+            for (int ks = 0; ks < 2; ++ks) split8<3>(ft[ks][0], ft[ks][1], T[ks]);
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 r[3];
-                sm.R[ct].get(ks, lane, r);
-                u[ct] = mm<3>(T[ks], r, u[ct]);
+            for (int ct = 0; ct < CT; ++ct) {
+                u[ct] = z4;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    bf16x8 r[3];
+                    sm.R[ct].get(ks, lane, r);
+                    u[ct] = mm<3>(T[ks], r, u[ct]);
+                }
+                sm.W[ct].put_tile(w, u[ct] * tail, lane);
+                if constexpr (!KEEP) sm.U[ct].put_tile(w, u[ct], lane);
             }
-            sm.W[ct].put_tile(w, u[ct] * tail, lane);
-            if constexpr (!KEEP) sm.U[ct].put_tile(w, u[ct], lane);
-            if constexpr (KEEP) {
+        }
+        fetch_m(c + 1, kRecT, ft);
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
                 float* ku = keep_u + (bh * nch + c) * kC * pad + p0 + 16 * ct;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) ku[(16 * w + 4 * lg + q) * pad] = u[ct][q];
             }
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                bf16x8 x[NK];
+                to_operand(fq[ks], x);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    bf16x8 s[3];
+                    sm.S[ct].get(ks, lane, s);
+                    y[ct] = mm<OA>(x, s, y[ct]);
+                }
+            }
+            fetch_q(c + 1);
         }
         lds_barrier();
-        // the wave's rows of the next state
+        // the wave's rows of the next state; Y
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
@@ -267,8 +272,7 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const floa
 #pragma unroll
             for (int i = 0; i < NT; ++i)
 #pragma unroll
-                for (int x = 0; x < NK; ++x)
-                    k[i][x] = ld_down<true>(K + x * kC * kRow, kRow, 32 * ks, 16 * (NT * w + i), lane);
+                for (int x = 0; x < NK; ++x) k[i][x] = ld_down(K + x * kC * kRow, kRow, 32 * ks, 16 * (NT * w + i), lane);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 bf16x8 x[3];
@@ -278,7 +282,14 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const floa
             }
         }
         put_state();
+        stage_k(c + 1);
+        fetch_k(c + 2);
         if constexpr (!KEEP) {
+            bf16x8 A[2][OA];
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) split8<OA>(fa[ks][0], fa[ks][1], A[ks]);
+            fetch_m(c + 1, kRecA, fa);
+            const auto yb = rows_buf(Yg + t0 * sy, (int)min((int64_t)kC, a.L - t0), sy, P * EO);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 y[ct] *= gam;
@@ -288,12 +299,12 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const floa
                     sm.U[ct].get(ks, lane, x);
                     y[ct] = mm<OA>(A[ks], x, y[ct]);
                 }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) buf_st(yb, yoff[ct] + q * (int)sy, a.scale * y[ct][q], Tout(0));
             }
         }
-        ready(c + 1);
         lds_barrier();
     }
-    put_y(mine - 1);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         const int p = p0 + 16 * ct;

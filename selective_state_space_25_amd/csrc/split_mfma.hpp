@@ -44,6 +44,18 @@ __device__ __forceinline__ f32x4 mm(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB]
     return c;
 }
 
+// As mm, the product of the first planes and the rest in sums of their own:
+// the rest's additions then round at the rest's size.
+template <int LIM, int NA, int NB>
+__device__ __forceinline__ void mm2(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4& c, f32x4& rest) {
+#pragma unroll
+    for (int s = LIM - 1; s >= 1; --s)
+#pragma unroll
+        for (int i = 0; i < NA; ++i)
+            if (s - i >= 0 && s - i < NB) rest = mfma(a[i], b[s - i], rest);
+    c = mfma(a[0], b[0], c);
+}
+
 // Pairs e, e + 1 of two values into word `e` of NP planes (a plane is one
 // operand, four words of two bf16 each).
 template <int NP>
@@ -76,20 +88,6 @@ __device__ __forceinline__ void split8(f32x4 lo, f32x4 hi, bf16x8 (&p)[NP]) {
     as_operand(w, p);
 }
 
-// Two C tiles (rows r0 .. r0 + 15 and r0 + 16 .. r0 + 31 of one column
-// block) make the B operand of a product over those 32 rows with k in the
-// order in which the lanes hold them: lane group g has rows r0 + 4 g + q,
-// then r0 + 16 + 4 g + q ("tile order").  The A operand has to be read in
-// that order: kperm, ld_down.
-
-// Position of column n in a row whose 4-element pieces are permuted inside
-// each group of 32 so that one 16-byte read gives a lane group the tile
-// order: pieces 0 .. 7 at positions 0, 2, 4, 6, 1, 3, 5, 7.
-__device__ __forceinline__ int kperm(int n) {
-    const int pc = (n & 31) >> 2;
-    return (n & ~31) + 4 * (pc < 4 ? 2 * pc : 2 * pc - 7) + (n & 3);
-}
-
 __device__ __forceinline__ bf16x8 ld8(const uint16_t* p) {
     return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(p));
 }
@@ -106,23 +104,11 @@ __device__ __forceinline__ s16x4 ld_tr(const uint16_t* p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4)(p));
 }
 
-// Operand with k running down the rows of m (row stride rs), columns
-// c0 .. c0 + 15: k = rows r0 .. r0 + 31 in tile order.  PERM: m's
-// columns are stored through kperm.
-template <bool PERM>
+// Operand with k running down the rows of m (row stride rs): rows
+// r0 .. r0 + 31, columns c0 .. c0 + 15.
 __device__ __forceinline__ bf16x8 ld_down(const uint16_t* m, int rs, int r0, int c0, int lane) {
     const int g = lane >> 4, a = lane & 15;
-    const int c = c0 + 4 * (a & 3);
-    const uint16_t* p = m + (r0 + 4 * g + (a >> 2)) * rs + (PERM ? kperm(c) : c);
-    return cat(ld_tr(p), ld_tr(p + 16 * rs));
-}
-
-// As ld_down with k in natural order (rows r0 + 8 g .. + 7 for lane group g).
-template <bool PERM>
-__device__ __forceinline__ bf16x8 ld_down8(const uint16_t* m, int rs, int r0, int c0, int lane) {
-    const int g = lane >> 4, a = lane & 15;
-    const int c = c0 + 4 * (a & 3);
-    const uint16_t* p = m + (r0 + 8 * g + (a >> 2)) * rs + (PERM ? kperm(c) : c);
+    const uint16_t* p = m + (r0 + 8 * g + (a >> 2)) * rs + c0 + 4 * (a & 3);
     return cat(ld_tr(p), ld_tr(p + 4 * rs));
 }
 
