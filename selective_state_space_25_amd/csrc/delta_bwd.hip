@@ -108,14 +108,15 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
     // inputs on their way, as in delta_scan.hip (before the first chunk the
     // first one is read again)
     Raw8<Tin> fk[NPC], fq[NPC], fr[KS];
-    f32x4 ft[2][2], fa[2][2], fgate[3];
+    bf16x8 ft[2][3], fa[2][3];
+    f32x4 fgate[3];
     float fgl;
     Tdo fo[CT][4];
     auto rows = [&](const char* base, int64_t stride, int c, int bytes) {
         const int64_t t0 = (int64_t)max(c, 0) * kC;
         return rows_buf(base + t0 * stride, (int)min((int64_t)kC, len - t0), stride, bytes);
     };
-    auto record = [&](int c) { return rows_buf(ba.recs + (bh * nch + max(c, 0)) * kRecGrad, 1, 0, kRecGrad * 4); };
+    auto record = [&](int c) { return rows_buf(ba.recs + (bh * nch + max(c, 0)) * GradRec::bytes, 1, 0, GradRec::bytes); };
     auto fetch_p = [&](const char* base, int c, Raw8<Tin> (&f)[NPC]) {
         const auto kb = rows(base, sk, c, a.NL * ES);
 #pragma unroll
@@ -136,16 +137,15 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
     auto fetch_g = [&](int c) {
         const auto rb = record(c);
 #pragma unroll
-        for (int i = 0; i < 3; ++i) fgate[i] = buf_ld4(rb, (kRecGam + i * kC + 16 * w + 4 * lg) * 4);
-        fgl = buf_raw<float>(rb, (kRecGam + kC - 1) * 4);
+        for (int i = 0; i < 3; ++i) fgate[i] = buf_ld4(rb, GradRec::gam + (i * kC + 16 * w + 4 * lg) * 4);
+        fgl = buf_raw<float>(rb, GradRec::gam + (kC - 1) * 4);
     };
-    auto fetch_m = [&](int c, int at, f32x4 (&f)[2][2]) {
+    auto fetch_m = [&](int c, int at, bf16x8 (&f)[2][3]) {
         const auto rb = record(c);
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            f[ks][0] = buf_ld4(rb, toff[ks] + at * 4);
-            f[ks][1] = buf_ld4(rb, toff[ks] + at * 4 + 16);
-        }
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int x = 0; x < 3; ++x) f[ks][x] = buf_op(rb, toff[ks] + at + x * kPlane);
     };
     auto stage_p = [&](uint16_t (*m)[kC][kRow], const Raw8<Tin> (&f)[NPC]) {
 #pragma unroll
@@ -168,10 +168,10 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
         const int c = mine - 1;
         fetch_o(c);
         fetch_r(c);
-        fetch_m(c, kRecAt, fa);
+        fetch_m(c, GradRec::At, fa);
         fetch_g(c);
         fetch_p(Kg, c, fk);
-        fetch_m(c, kRecTt, ft);
+        fetch_m(c, GradRec::Tt, ft);
         fetch_p(Qg, c, fq);
         put_o();
         fetch_o(c - 1);
@@ -182,34 +182,36 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
         const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
         // dU for the wave's tokens
         f32x4 u[CT], x[CT];
+        {
+            bf16x8 k[KS][NK];
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) u[ct] = x[ct] = z4;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-            bf16x8 k[NK];
-            to_operand(fr[ks], k);
+            for (int ks = 0; ks < KS; ++ks) to_operand(fr[ks], k[ks]);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                bf16x8 d[3];
-                sm.D[ct].get(ks, lane, d);
-                u[ct] = mm<3>(k, d, u[ct]);
+                bf16x8 d[KS][3];
+                f32x4 acc[KS];
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    sm.D[ct].get(ks, lane, d[ks]);
+                    acc[ks] = z4;
+                }
+                mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return d[m]; }, acc);
+                u[ct] = sum_of(acc);
             }
         }
         fetch_r(c - 1);
         {
-            bf16x8 A[2][3];
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) split8<3>(fa[ks][0], fa[ks][1], A[ks]);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    bf16x8 d[NO];
-                    sm.O[ct].get(ks, lane, d);
-                    x[ct] = mm<3>(A[ks], d, x[ct]);
-                }
+            for (int ct = 0; ct < CT; ++ct) {
+                bf16x8 d[2][NO];
+                sm.O[ct].get(0, lane, d[0]);
+                sm.O[ct].get(1, lane, d[1]);
+                f32x4 acc[2] = {z4, z4};
+                mm_turns<3, 3, NO>([&](int m) { return fa[m]; }, [&](int m) { return d[m]; }, acc);
+                x[ct] = sum_of(acc);
+            }
         }
-        fetch_m(c - 1, kRecAt, fa);
+        fetch_m(c - 1, GradRec::At, fa);
         const f32x4 gam = fgate[0], tail = fgate[1], beta = fgate[2];
         const float gl = fgl;
         fetch_g(c - 1);
@@ -227,22 +229,18 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
         // dR and dV for the wave's tokens
         f32x4 r[CT];
         {
-            bf16x8 T[2][3];
-#pragma unroll
-            for (int ks = 0; ks < 2; ++ks) split8<3>(ft[ks][0], ft[ks][1], T[ks]);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                r[ct] = z4;
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    bf16x8 y[3];
-                    sm.U[ct].get(ks, lane, y);
-                    r[ct] = mm<3>(T[ks], y, r[ct]);
-                }
+                bf16x8 y[2][3];
+                sm.U[ct].get(0, lane, y[0]);
+                sm.U[ct].get(1, lane, y[1]);
+                f32x4 acc[2] = {z4, z4};
+                mm_turns<3, 3, 3>([&](int m) { return ft[m]; }, [&](int m) { return y[m]; }, acc);
+                r[ct] = sum_of(acc);
                 sm.R[ct].put_tile(w, -(r[ct] * beta * gam), lane);
             }
         }
-        fetch_m(c - 1, kRecTt, ft);
+        fetch_m(c - 1, GradRec::Tt, ft);
         stage_p(sm.Q, fq);
         fetch_p(Qg, c - 1, fq);
         const auto vb = rows_buf(dVg + t0 * sv, (int)min((int64_t)kC, a.L - t0), sv, P * ES);
@@ -257,30 +255,30 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
         }
         lds_barrier();
         // the wave's rows of the adjoint before the chunk
+        {
+            bf16x8 k[NT * 2][NK], q[NT * 2][NK];
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) D[i][ct] *= gl;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            bf16x8 k[NT][NK], q[NT][NK];
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT * 2; ++i)
 #pragma unroll
                 for (int l = 0; l < NK; ++l) {
-                    k[i][l] = ld_down(&sm.K[l][0][0], kRow, 32 * ks, 16 * (NT * w + i), lane);
-                    q[i][l] = ld_down(&sm.Q[l][0][0], kRow, 32 * ks, 16 * (NT * w + i), lane);
+                    k[i][l] = ld_down(&sm.K[l][0][0], kRow, 32 * (i & 1), 16 * (NT * w + i / 2), lane);
+                    q[i][l] = ld_down(&sm.Q[l][0][0], kRow, 32 * (i & 1), 16 * (NT * w + i / 2), lane);
                 }
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                bf16x8 y[3], g[3];
-                sm.R[ct].get(ks, lane, y);
-                sm.G[ct].get(ks, lane, g);
+                bf16x8 y[2][3], g[2][3];
 #pragma unroll
-                for (int i = 0; i < NT; ++i) {
-                    D[i][ct] = mm<3>(k[i], y, D[i][ct]);
-                    D[i][ct] = mm<3>(q[i], g, D[i][ct]);
+                for (int ks = 0; ks < 2; ++ks) {
+                    sm.R[ct].get(ks, lane, y[ks]);
+                    sm.G[ct].get(ks, lane, g[ks]);
                 }
+                f32x4 acc[NT * 2];
+#pragma unroll
+                for (int i = 0; i < NT * 2; ++i) acc[i] = i & 1 ? z4 : D[i / 2][ct] * gl;
+                mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return y[m & 1]; }, acc);
+                mm_turns<3, NK, 3>([&](int m) { return q[m]; }, [&](int m) { return g[m & 1]; }, acc);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) D[i][ct] = acc[2 * i] + acc[2 * i + 1];
             }
         }
         put_state();
@@ -384,8 +382,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
         }
         return;
     }
-    const float* rec = ba.recs + (int64_t)blockIdx.x * kRecGrad;
-    if (tid < kC) sm.cum[tid] = reinterpret_cast<const double*>(rec + kRecCum)[tid];
+    const char* rec = ba.recs + (int64_t)blockIdx.x * GradRec::bytes;
+    if (tid < kC) sm.cum[tid] = reinterpret_cast<const double*>(rec + GradRec::cum)[tid];
 
     // ---- sums over the value columns: dO S^T, dR S^T, U D^T for the wave's
     // tokens, dO U^T and dR U^T for its row block, <S, D>, dR.V
@@ -474,9 +472,16 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 s[x] = ld_down(&sm.s.S[x][0][0], kRow, 0, 16 * i, lane);
                 d[x] = ld_down(&sm.s.D[x][0][0], kRow, 0, 16 * i, lane);
             }
-            q1[i] = mm<3>(o, s, q1[i]);
-            k2[i] = mm<3>(r, s, k2[i]);
-            mm2<3>(u, d, k3[i], k3r[i]);
+            // the planes' products in turn over the sums
+#pragma unroll
+            for (int x = 2; x >= 0; --x)
+#pragma unroll
+                for (int y = 0; y <= x; ++y) {
+                    k2[i] = mfma(r[y], s[x - y], k2[i]);
+                    if (x > 0) k3r[i] = mfma(u[y], d[x - y], k3r[i]);
+                    else k3[i] = mfma(u[0], d[0], k3[i]);
+                    if (y < NO) q1[i] = mfma(o[y], s[x - y], q1[i]);
+                }
         }
 #pragma unroll
         for (int sb = 0; sb < 4; ++sb) {
@@ -484,8 +489,13 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             bf16x8 w[3];
 #pragma unroll
             for (int x = 0; x < 3; ++x) w[x] = ld8(&sm.s.U[x][16 * sb + li][8 * lg]);
-            x1[sb] = mm<3>(o, w, x1[sb]);
-            x2[sb] = mm<3>(r, w, x2[sb]);
+#pragma unroll
+            for (int x = 2; x >= 0; --x)
+#pragma unroll
+                for (int y = 0; y <= x; ++y) {
+                    x2[sb] = mfma(r[y], w[x - y], x2[sb]);
+                    if (y < NO) x1[sb] = mfma(o[y], w[x - y], x1[sb]);
+                }
         }
     }
     __syncthreads();
@@ -517,9 +527,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     __syncthreads();
 
     // ---- the dots with q and k; dQ and dK from the states
-    const f32x4 gam = *reinterpret_cast<const f32x4*>(rec + kRecGam + 16 * tb + 4 * lg);
-    const f32x4 tail = *reinterpret_cast<const f32x4*>(rec + kRecTail + 16 * tb + 4 * lg);
-    const f32x4 beta = *reinterpret_cast<const f32x4*>(rec + kRecBeta + 16 * tb + 4 * lg);
+    const f32x4 gam = *reinterpret_cast<const f32x4*>(rec + GradRec::gam + 4 * (16 * tb + 4 * lg));
+    const f32x4 tail = *reinterpret_cast<const f32x4*>(rec + GradRec::tail + 4 * (16 * tb + 4 * lg));
+    const f32x4 beta = *reinterpret_cast<const f32x4*>(rec + GradRec::beta + 4 * (16 * tb + 4 * lg));
     double aq[4] = {}, ak[4] = {}, bk[4] = {};
 #pragma unroll
     for (int i = 0; i < NB; ++i)
@@ -557,7 +567,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 }
                 kk = mm<3>(x, y, kk);
             }
-            const float* ab = rec + kRecA + (tb * (tb + 1) / 2 + sb) * 256 + li;
+            const float* ab = reinterpret_cast<const float*>(rec + GradRec::A) + block_at(tb, sb) * 256 + li;
             const double cs = sm.cum[s];
             double cz = 0.0;
 #pragma unroll
@@ -623,7 +633,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             if (lane + o < 64) up += u;
             if (lane >= o) down += d;
         }
-        const double last = rec[kRecGam + kC - 1] * ((sm.sd[0] + sm.sd[1]) + (sm.sd[2] + sm.sd[3]));
+        const double last = reinterpret_cast<const float*>(rec + GradRec::gam)[kC - 1] * ((sm.sd[0] + sm.sd[1]) + (sm.sd[2] + sm.sd[3]));
         if (lane < inside) {
             // a decay that is zero has no gradient; the sums would leave their rounding
             const int64_t gi = (b * a.L + t0 + lane) * a.H + h;
@@ -702,7 +712,7 @@ hipError_t launch(const DeltaBwdArgs& a, hipStream_t stream) {
     constexpr int CT = 1;
     const DeltaArgs& f = a.f;
     const int64_t nch = delta_chunks(f.L);
-    hipError_t e = launch_delta_prep(f, sizeof(Tin) == 2, true, a.recs, stream);
+    hipError_t e = launch_delta_prep(f, sizeof(Tin) == 2, 3, true, a.recs, stream);
     if (e != hipSuccess) return e;
     e = launch_delta_keep(f, sizeof(Tin) == 2, a.recs, a.S, a.U, a.pad, stream);
     if (e != hipSuccess) return e;
@@ -744,7 +754,7 @@ struct Sizes {
 Sizes sizes(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N) {
     const size_t chunks = (size_t)(batch * H * delta_chunks(L)), pad = (size_t)(P + 31) / 32 * 32;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-    return {up(chunks * delta_record_bytes(true)), up(chunks * pad * (N <= 64 ? 64 : 128) * 4), up(chunks * kC * pad * 4),
+    return {up(chunks * delta_record_bytes(3, true)), up(chunks * pad * (N <= 64 ? 64 : 128) * 4), up(chunks * kC * pad * 4),
             H > G ? up((size_t)(batch * L * H * N) * 4) : 0};
 }
 
@@ -763,7 +773,7 @@ void delta_bwd_carve(DeltaBwdArgs& a, void* ws) {
         p += n;
         return r;
     };
-    a.recs = take(s.recs);
+    a.recs = reinterpret_cast<char*>(take(s.recs));
     a.S = take(s.state);
     a.D = take(s.state);
     a.U = take(s.rows);

@@ -14,22 +14,27 @@ using namespace smm;
 constexpr int kC = 64;             // tokens per chunk
 constexpr int kBlocks = 10;        // 16 x 16 blocks on and below a chunk matrix's diagonal
 
-// Record of one (batch, head, chunk), in floats: T and A as 10 row-major
-// 16 x 16 blocks (block (t, s) at t (t + 1) / 2 + s), then per token
-// e^cum, e^(last - cum), beta (zero past the sequence's end), and cum itself
-// as doubles; for the gradients T's and A's blocks again, each transposed.
-constexpr int kRecT = 0;
-constexpr int kRecA = kBlocks * 256;
-constexpr int kRecGam = 2 * kBlocks * 256;
-constexpr int kRecTail = kRecGam + kC;
-constexpr int kRecBeta = kRecTail + kC;
-constexpr int kRecCum = kRecBeta + kC;
-constexpr int kRec = kRecCum + 2 * kC;
-constexpr int kRecTt = kRec;
-constexpr int kRecAt = kRecTt + kBlocks * 256;
-constexpr int kRecGrad = kRecAt + kBlocks * 256;
+// Record of one (batch, head, chunk), byte offsets.  T in three bf16 planes,
+// each 10 row-major 16 x 16 blocks (block (t, s) at t (t + 1) / 2 + s); A in
+// OL planes; then per token e^cum, e^(last - cum), beta (zero past the
+// sequence's end) and cum itself as doubles.  For the gradients A is fp32,
+// and T's and A's blocks follow in three planes, each block transposed.
+constexpr int kPlane = kBlocks * 512;
+template <int OL, bool GRAD>
+struct Rec {
+    static constexpr int T = 0;
+    static constexpr int A = 3 * kPlane;
+    static constexpr int gam = A + (GRAD ? 2 : OL) * kPlane;   // (fp32 takes the place of two planes)
+    static constexpr int tail = gam + 4 * kC;
+    static constexpr int beta = tail + 4 * kC;
+    static constexpr int cum = beta + 4 * kC;
+    static constexpr int Tt = cum + 8 * kC;
+    static constexpr int At = Tt + 3 * kPlane;
+    static constexpr int bytes = GRAD ? At + 3 * kPlane : Tt;
+};
+using GradRec = Rec<3, true>;
 
-__device__ __forceinline__ int block_at(int t, int s) { return (t * (t + 1) / 2 + s) * 256; }
+__device__ __forceinline__ int block_at(int t, int s) { return t * (t + 1) / 2 + s; }
 
 __device__ __forceinline__ int64_t seq_len(const DeltaArgs& a, int64_t b) {
     return a.lengths ? min((int64_t)max(a.lengths[b], 0), a.L) : a.L;
@@ -110,6 +115,21 @@ __device__ __forceinline__ void stage8(uint16_t* row, int ps, int n0, const Raw8
 #pragma unroll
     for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8*>(row + i * ps + n0) = p[i];
 }
+// The same with the row's columns through kperm.
+__device__ __forceinline__ void stage8_perm(uint16_t* row, int ps, int n0, const Raw8<uint16_t>& r) {
+    *reinterpret_cast<uint2*>(row + kperm(n0)) = make_uint2(r.w[0], r.w[1]);
+    *reinterpret_cast<uint2*>(row + kperm(n0 + 4)) = make_uint2(r.w[2], r.w[3]);
+}
+__device__ __forceinline__ void stage8_perm(uint16_t* row, int ps, int n0, const Raw8<float>& r) {
+    uint2 pa[3], pb[3];
+    split4<3>(r.lo, pa);
+    split4<3>(r.hi, pb);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        *reinterpret_cast<uint2*>(row + i * ps + kperm(n0)) = pa[i];
+        *reinterpret_cast<uint2*>(row + i * ps + kperm(n0 + 4)) = pb[i];
+    }
+}
 __device__ __forceinline__ void to_operand(const Raw8<uint16_t>& r, bf16x8 (&p)[1]) {
     p[0] = __builtin_bit_cast(bf16x8, r.w);
 }
@@ -120,6 +140,39 @@ __device__ __forceinline__ void lower_tile(int k, int& tb, int& sb) {
     tb = k >= 6 ? 3 : k >= 3 ? 2 : k >= 1 ? 1 : 0;
     sb = k - tb * (tb + 1) / 2;
 }
+
+__device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[2]) { return v[0] + v[1]; }
+__device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); }
+
+// A lower triangular chunk matrix (or, TR, its transpose) as A operands in
+// LDS: fragment (row block t, k-step ks <= t / 2; transposed: ks >= t / 2)
+// holds two 16-wide blocks in tile order, a lane's 16 bytes in its own slot.
+template <int NPL, bool TR>
+struct Frags {
+    uint16_t p[NPL][6][64][8];
+    static __device__ __forceinline__ int at(int t, int ks) {
+        return TR ? (t < 2 ? 2 * t + ks : t + 2) : (t < 2 ? t : 2 * t - 2 + ks);
+    }
+    // columns 8 c .. 8 c + 7 of row r of block i of a record's plane
+    __device__ __forceinline__ void put(int plane, int i, int r, int c, u32x4 v) {
+        int tb, sb;
+        lower_tile(i, tb, sb);
+        const int f = TR ? at(sb, tb >> 1) : at(tb, sb >> 1), e = 4 * ((TR ? tb : sb) & 1);
+        *reinterpret_cast<uint2*>(&p[plane][f][16 * (2 * c) + r][e]) = make_uint2(v[0], v[1]);
+        *reinterpret_cast<uint2*>(&p[plane][f][16 * (2 * c + 1) + r][e]) = make_uint2(v[2], v[3]);
+    }
+    // the blocks beyond the diagonal that share a fragment with one on it
+    __device__ __forceinline__ void clear(int tid, int threads) {
+        for (int i = tid; i < 128; i += threads)
+#pragma unroll
+            for (int x = 0; x < NPL; ++x)
+                *reinterpret_cast<uint2*>(&p[x][TR ? (i < 64 ? 2 : 5) : (i < 64 ? 0 : 3)][i & 63][TR ? 0 : 4]) = make_uint2(0, 0);
+    }
+    __device__ __forceinline__ void get(int t, int ks, int lane, bf16x8 (&a)[NPL]) const {
+#pragma unroll
+        for (int x = 0; x < NPL; ++x) a[x] = ld8(p[x][at(t, ks)][lane]);
+    }
+};
 
 // B operands that waves hand to each other through LDS: NPL planes of KS
 // k-steps, k in natural order, each lane's 16 bytes in its own slot.
@@ -141,16 +194,19 @@ struct Operands {
     }
 };
 
-// Byte offset in a record of the lane's eight floats of row block tb of T
-// (columns 32 ks + 8 g ..; kOut above the diagonal, where it is zero), and
-// of row block jb of T's transpose.
+// Byte offset in a plane of the lane's part of row block tb of T, an A
+// operand: columns 32 ks + 8 g .. (kOut above the diagonal, where it is
+// zero); and of row block jb of T's transpose.
 __device__ __forceinline__ int row_of(int tb, int ks, int lane) {
     const int s = 2 * ks + (lane >> 5);
-    return s <= tb ? (block_at(tb, s) + (lane & 15) * 16 + 8 * ((lane >> 4) & 1)) * 4 : kOut;
+    return s <= tb ? block_at(tb, s) * 512 + (lane & 15) * 32 + ((lane >> 4) & 1) * 16 : kOut;
 }
 __device__ __forceinline__ int row_of_t(int jb, int ks, int lane) {
     const int t = 2 * ks + (lane >> 5);
-    return t >= jb ? (block_at(t, jb) + (lane & 15) * 16 + 8 * ((lane >> 4) & 1)) * 4 : kOut;
+    return t >= jb ? block_at(t, jb) * 512 + (lane & 15) * 32 + ((lane >> 4) & 1) * 16 : kOut;
+}
+__device__ __forceinline__ bf16x8 buf_op(__amdgpu_buffer_rsrc_t r, int off) {
+    return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
 }
 
 }  // namespace dchunk

@@ -224,10 +224,10 @@ hipError_t launch_delta_rec(const DeltaArgs& a, int in_bf16, int out_bf16, hipSt
 // k that are not made of aligned 16-byte pieces are copied first, padded to
 // 64 or 128 elements (2 batch L G of them in `rows`; a is set to the copies).
 int64_t delta_chunks(int64_t L);
-size_t delta_record_bytes(bool grad);
+size_t delta_record_bytes(int planes, bool grad);   // planes of A: 2 for a bf16 y, 3 for fp32
 hipError_t launch_delta_pad(DeltaArgs& a, int in_bf16, void* rows, hipStream_t stream);
-hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, bool grad, float* recs, hipStream_t stream);
-hipError_t launch_delta_scan(const DeltaArgs& a, int in_bf16, int out_bf16, const float* recs, hipStream_t stream);
+hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, int planes, bool grad, char* recs, hipStream_t stream);
+hipError_t launch_delta_scan(const DeltaArgs& a, int in_bf16, int out_bf16, const char* recs, hipStream_t stream);
 
 // Gradients of the gated delta rule; the arrays below dh0 are workspace
 // (delta_bwd_carve).  f.y and f.last are unused.
@@ -237,7 +237,7 @@ struct DeltaBwdArgs {
     const float* dlast;       // NULL = zero
     void *dq, *dk, *dv;
     float *dg, *dbeta, *dh0;
-    float* recs;
+    char* recs;
     float* S;                 // [chunks, pad, NP] state entering each chunk (NP: N rounded up to 64 or 128)
     float* D;                 // [chunks, pad, NP] adjoint of the state leaving it
     float* U;                 // [chunks, 64, pad]
@@ -248,7 +248,7 @@ struct DeltaBwdArgs {
 };
 size_t delta_bwd_bytes(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N);
 void delta_bwd_carve(DeltaBwdArgs& a, void* ws);
-hipError_t launch_delta_keep(const DeltaArgs& a, int in_bf16, const float* recs, float* keep_s, float* keep_u, int pad,
+hipError_t launch_delta_keep(const DeltaArgs& a, int in_bf16, const char* recs, float* keep_s, float* keep_u, int pad,
                              hipStream_t stream);
 hipError_t launch_delta_bwd(const DeltaBwdArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
 

@@ -44,16 +44,19 @@ __device__ __forceinline__ f32x4 mm(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB]
     return c;
 }
 
-// As mm, the product of the first planes and the rest in sums of their own:
-// the rest's additions then round at the rest's size.
-template <int LIM, int NA, int NB>
-__device__ __forceinline__ void mm2(const bf16x8 (&a)[NA], const bf16x8 (&b)[NB], f32x4& c, f32x4& rest) {
+// M such products step by step: an MFMA that adds to the sum of the one
+// before waits out its latency (several times its issue slot), so products
+// that are independent take turns.  a(m), b(m): planes of product m.
+template <int LIM, int NA, int NB, int M, typename FA, typename FB>
+__device__ __forceinline__ void mm_turns(FA a, FB b, f32x4 (&c)[M]) {
 #pragma unroll
-    for (int s = LIM - 1; s >= 1; --s)
+    for (int s = LIM - 1; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i < NA; ++i)
-            if (s - i >= 0 && s - i < NB) rest = mfma(a[i], b[s - i], rest);
-    c = mfma(a[0], b[0], c);
+            if (s - i >= 0 && s - i < NB) {
+#pragma unroll
+                for (int m = 0; m < M; ++m) c[m] = mfma(a(m)[i], b(m)[s - i], c[m]);
+            }
 }
 
 // Pairs e, e + 1 of two values into word `e` of NP planes (a plane is one
@@ -88,6 +91,19 @@ __device__ __forceinline__ void split8(f32x4 lo, f32x4 hi, bf16x8 (&p)[NP]) {
     as_operand(w, p);
 }
 
+// Two C tiles (rows r0 .. r0 + 15 and r0 + 16 .. r0 + 31 of one column
+// block) split with split8 are the B operand of a product over those 32 rows
+// without leaving the lanes, k in the order in which the lanes hold them:
+// lane group g has rows r0 + 4 g + q, then r0 + 16 + 4 g + q ("tile order").
+// The A operand has to be read in that order.  kperm: position of column n
+// in a row whose 4-element pieces are permuted inside each group of 32 so
+// that one 16-byte read gives a lane group the tile order (pieces 0 .. 7 at
+// positions 0, 2, 4, 6, 1, 3, 5, 7).
+__device__ __forceinline__ int kperm(int n) {
+    const int pc = (n & 31) >> 2;
+    return (n & ~31) + 4 * (pc < 4 ? 2 * pc : 2 * pc - 7) + (n & 3);
+}
+
 __device__ __forceinline__ bf16x8 ld8(const uint16_t* p) {
     return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(p));
 }
@@ -110,6 +126,13 @@ __device__ __forceinline__ bf16x8 ld_down(const uint16_t* m, int rs, int r0, int
     const int g = lane >> 4, a = lane & 15;
     const uint16_t* p = m + (r0 + 8 * g + (a >> 2)) * rs + c0 + 4 * (a & 3);
     return cat(ld_tr(p), ld_tr(p + 4 * rs));
+}
+
+// The same in tile order, of an m whose columns are stored through kperm.
+__device__ __forceinline__ bf16x8 ld_down_tile(const uint16_t* m, int rs, int r0, int c0, int lane) {
+    const int g = lane >> 4, a = lane & 15;
+    const uint16_t* p = m + (r0 + 4 * g + (a >> 2)) * rs + kperm(c0 + 4 * (a & 3));
+    return cat(ld_tr(p), ld_tr(p + 16 * rs));
 }
 
 // Four consecutive values into NP planes of 4 bf16 each.
