@@ -164,9 +164,15 @@ def _check(status: int) -> None:
         raise SelscanError(status, last_error())
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -182,10 +188,13 @@ def _ptr(t, name, shape=None, dtype=None, device=None):
     """Device pointer of a dense tensor after checking shape/dtype/device."""
     if t is None:
         return None
-    torch = _torch()
+    if type(t) is _torch().Tensor and (shape is None or t.shape == shape) and (dtype is None or t.dtype is dtype) \
+            and t.is_contiguous() and (device is None or t.device == device):
+        return t.data_ptr()
+    torch = _torch()   # what is wrong with it, if anything
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -197,7 +206,12 @@ def _ptr(t, name, shape=None, dtype=None, device=None):
 
 
 def _stream_handle(device):
+    """The device's current stream as an integer (torch's raw query where it
+    has one: the Stream object costs more than the rest of a small call)."""
     torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None and device.index is not None:
+        return raw(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
 

@@ -5,8 +5,15 @@
 //   ds = rstd (w - mean_d w - xhat mean_d (w xhat)) + dresidual,  w = dy weight
 //   dweight = sum_r dy xhat;  dbias = sum_r dy
 //
-// One workgroup per row; the variance is summed over (s - mean)^2, not taken
-// as a difference of moments.
+// Both directions are streams bound by memory.  A row stays in registers
+// between its sums and its output: 8-element pieces over the 64 lanes of one
+// wave (rows to 2560 elements, sums without a barrier) or the 256 of a
+// workgroup (to 8192); longer rows, and rows that are not made of aligned
+// 16-byte pieces, are read again for each step instead.  The variance is
+// summed over (s - mean)^2, not taken as a difference of moments.  The
+// gradients' waves walk rows a fixed distance apart and keep their sums for
+// dweight and dbias in registers, one partial row a workgroup, which a second
+// kernel adds in a fixed order.
 #include "io.hpp"
 #include "kernels.hpp"
 #include "philox.hpp"
@@ -25,6 +32,163 @@ __device__ __forceinline__ float block_sum(float v, float* sm) {
     if ((threadIdx.x & 63) == 0) sm[threadIdx.x >> 6] = v;
     __syncthreads();
     return (sm[0] + sm[1]) + (sm[2] + sm[3]);
+}
+
+// The pieces' values after dropout: base: index of the first element.
+__device__ __forceinline__ void drop8(const NormArgs& a, int64_t base, float* v) {
+    uint32_t w[8];
+    philox4((uint64_t)base >> 2, a.offset, a.seed, w);
+    philox4(((uint64_t)base >> 2) + 1, a.offset, a.seed, w + 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = w[i] >= a.keep_from ? v[i] * a.keep_scale : 0.0f;
+}
+
+// Sum over the row's W waves, the same value in every lane.
+template <int W>
+__device__ __forceinline__ float row_sum(float v, float* sm) {
+    if constexpr (W == 4) return block_sum(v, sm);
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+    return v;
+}
+
+// W waves per row (a workgroup has 4 / W rows), NV pieces per lane.
+template <typename Tin, typename Tres, typename Tout, int W, int NV>
+__global__ __launch_bounds__(kT) void norm_fwd_reg_kernel(NormArgs a) {
+    __shared__ float sm[4];
+    const int at = threadIdx.x % (64 * W);
+    const int64_t row = (int64_t)blockIdx.x * (4 / W) + threadIdx.x / (64 * W);
+    if (row >= a.rows) return;   // (a wave's row is its own when W is 1; W = 4 has no such rows)
+    const int64_t base = row * a.dim;
+    const Tin* X = reinterpret_cast<const Tin*>(a.x) + base;
+    const Tres* R = a.res ? reinterpret_cast<const Tres*>(a.res) + base : nullptr;
+    const int np = (int)(a.dim / 8);
+    float s[NV][8];
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int d = 8 * (at + 64 * W * j);
+        if (at + 64 * W * j < np) {
+            float r[8];
+            io::ld8(X + d, s[j]);
+            if (R) io::ld8(R + d, r);
+            if (a.drop) drop8(a, base + d, s[j]);
+            if (R) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[j][i] += r[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += s[j][i];
+        }
+    }
+    const float mean = row_sum<W>(sum, sm) * a.inv_dim;
+    float sq = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+        if (at + 64 * W * j < np) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sq = __builtin_fmaf(s[j][i] - mean, s[j][i] - mean, sq);
+        }
+    const float rstd = 1.0f / sqrtf(row_sum<W>(sq, sm) * a.inv_dim + a.eps);
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+        const int d = 8 * (at + 64 * W * j);
+        if (at + 64 * W * j >= np) continue;
+        if (a.res_out) io::st8(reinterpret_cast<Tres*>(a.res_out) + base + d, s[j]);
+        float w[8], b[8];
+        if (a.weight) io::ld8(a.weight + d, w);
+        if (a.bias) io::ld8(a.bias + d, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float y = (s[j][i] - mean) * rstd;
+            if (a.weight) y *= w[i];
+            if (a.bias) y += b[i];
+            s[j][i] = y;
+        }
+        io::st8(reinterpret_cast<Tout*>(a.y) + base + d, s[j]);
+    }
+    if (at == 0) {
+        if (a.mean) a.mean[row] = mean;
+        if (a.rstd) a.rstd[row] = rstd;
+    }
+}
+
+template <typename Tin, typename Tres, typename Tout, int W, int NV>
+__global__ __launch_bounds__(kT) void norm_bwd_reg_kernel(NormArgs a) {
+    __shared__ float sm[4];
+    __shared__ float part[W == 1 ? 4 * 512 : 1];
+    const int at = threadIdx.x % (64 * W), np = (int)(a.dim / 8);
+    float gw[NV][8], gb[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) gw[j][i] = gb[j][i] = 0.0f;
+    for (int64_t row = (int64_t)blockIdx.x * (4 / W) + threadIdx.x / (64 * W); row < a.rows; row += (int64_t)gridDim.x * (4 / W)) {
+        const int64_t base = row * a.dim;
+        const Tout* DY = reinterpret_cast<const Tout*>(a.x) + base;
+        const Tres* S = reinterpret_cast<const Tres*>(a.res) + base;
+        const Tres* DR = a.dres_in ? reinterpret_cast<const Tres*>(a.dres_in) + base : nullptr;
+        const float mean = a.mean_in[row], rstd = a.rstd_in[row];
+        float y[NV][8], x[NV][8];
+        float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int d = 8 * (at + 64 * W * j);
+            if (at + 64 * W * j >= np) continue;
+            io::ld8(DY + d, y[j]);
+            io::ld8(S + d, x[j]);
+            float w[8];
+            if (a.weight) io::ld8(a.weight + d, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[j][i] = (x[j][i] - mean) * rstd;
+                gw[j][i] = __builtin_fmaf(y[j][i], x[j][i], gw[j][i]);
+                gb[j][i] += y[j][i];
+                if (a.weight) y[j][i] *= w[i];
+                c1 += y[j][i];
+                c2 = __builtin_fmaf(y[j][i], x[j][i], c2);
+            }
+        }
+        if (!a.y && !a.res_out) continue;
+        c1 = row_sum<W>(c1, sm) * a.inv_dim;
+        c2 = row_sum<W>(c2, sm) * a.inv_dim;
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int d = 8 * (at + 64 * W * j);
+            if (at + 64 * W * j >= np) continue;
+            float r[8];
+            if (DR) io::ld8(DR + d, r);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                y[j][i] = (y[j][i] - c1 - x[j][i] * c2) * rstd;
+                if (DR) y[j][i] += r[i];
+            }
+            if (a.res_out) io::st8(reinterpret_cast<Tres*>(a.res_out) + base + d, y[j]);
+            if (a.y) {
+                if (a.drop) drop8(a, base + d, y[j]);
+                io::st8(reinterpret_cast<Tin*>(a.y) + base + d, y[j]);
+            }
+        }
+    }
+    if (!a.dweight && !a.dbias) return;
+    float* out = a.part + 2 * (int64_t)blockIdx.x * a.dim;
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            float (&v)[8] = g ? gb[j] : gw[j];
+            const int d = 8 * (at + 64 * W * j);
+            if constexpr (W == 4) {
+                if (at + 64 * W * j < np) io::st8(out + g * a.dim + d, v);
+            } else {   // the four waves' sums of the same columns, in their order
+                __syncthreads();
+                io::st8(part + (threadIdx.x >> 6) * 512 + 8 * at, v);
+                __syncthreads();
+                for (int e = threadIdx.x; e < 512 && 512 * j + e < a.dim; e += kT)
+                    out[g * a.dim + 512 * j + e] = ((part[e] + part[512 + e]) + part[1024 + e]) + part[1536 + e];
+            }
+        }
+    }
 }
 
 __device__ __forceinline__ float dropped(const NormArgs& a, int64_t i, float v) {
@@ -113,20 +277,69 @@ __global__ __launch_bounds__(kT) void norm_wgrad_kernel(NormArgs a) {
     a.part[(2 * (int64_t)blockIdx.y + 1) * a.dim + d] = gb;
 }
 
-__global__ __launch_bounds__(kT) void norm_wsum_kernel(NormArgs a) {
-    const int64_t d = (int64_t)blockIdx.x * kT + threadIdx.x;
-    if (d >= a.dim) return;
+// Sums of the partial rows: 64 columns and 16 slices of the rows a workgroup.
+__global__ __launch_bounds__(1024) void norm_wsum_kernel(NormArgs a) {
+    __shared__ float sm[2][16][64];
+    const int col = threadIdx.x & 63, sl = threadIdx.x >> 6;
+    const int64_t d = (int64_t)blockIdx.x * 64 + col;
     float gw = 0.0f, gb = 0.0f;
-    for (int b = 0; b < a.blocks; ++b) {
-        gw += a.part[(2 * (int64_t)b) * a.dim + d];
-        gb += a.part[(2 * (int64_t)b + 1) * a.dim + d];
+    if (d < a.dim) {
+#pragma unroll 4
+        for (int b = sl; b < a.blocks; b += 16) {
+            gw += a.part[2 * (int64_t)b * a.dim + d];
+            gb += a.part[(2 * (int64_t)b + 1) * a.dim + d];
+        }
     }
-    if (a.dweight) a.dweight[d] = gw;
-    if (a.dbias) a.dbias[d] = gb;
+    sm[0][sl][col] = gw;
+    sm[1][sl][col] = gb;
+    __syncthreads();
+    if (sl < 2 && d < a.dim) {
+        float v = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v += sm[sl][i][col];
+        float* out = sl ? a.dbias : a.dweight;
+        if (out) out[d] = v;
+    }
+}
+
+// Waves per row and pieces per lane of the register kernels; 0: neither fits.
+int reg_pieces(const NormArgs& a, int& waves) {
+    if (!a.vec || a.dim > 8192) return 0;
+    const int np = (int)(a.dim / 8);
+    waves = np <= 5 * 64 ? 1 : 4;
+    return (np + 64 * waves - 1) / (64 * waves);
+}
+
+template <bool FWD, typename Tin, typename Tres, typename Tout, int W, int NV>
+hipError_t reg(const NormArgs& a, hipStream_t stream) {
+    KTime kt(FWD ? "norm_fwd" : "norm_bwd", stream);
+    if constexpr (FWD)
+        hipLaunchKernelGGL((norm_fwd_reg_kernel<Tin, Tres, Tout, W, NV>), dim3((unsigned)((a.rows + 4 / W - 1) / (4 / W))),
+                           dim3(kT), 0, stream, a);
+    else
+        hipLaunchKernelGGL((norm_bwd_reg_kernel<Tin, Tres, Tout, W, NV>), dim3(a.blocks), dim3(kT), 0, stream, a);
+    return hipGetLastError();
+}
+
+template <bool FWD, typename Tin, typename Tres, typename Tout>
+hipError_t by_size(const NormArgs& a, int waves, int pieces, hipStream_t stream) {
+    if (waves == 4) {
+        if (pieces == 2) return reg<FWD, Tin, Tres, Tout, 4, 2>(a, stream);
+        return pieces == 3 ? reg<FWD, Tin, Tres, Tout, 4, 3>(a, stream) : reg<FWD, Tin, Tres, Tout, 4, 4>(a, stream);
+    }
+    switch (pieces) {
+        case 1: return reg<FWD, Tin, Tres, Tout, 1, 1>(a, stream);
+        case 2: return reg<FWD, Tin, Tres, Tout, 1, 2>(a, stream);
+        case 3: return reg<FWD, Tin, Tres, Tout, 1, 3>(a, stream);
+        case 4: return reg<FWD, Tin, Tres, Tout, 1, 4>(a, stream);
+        default: return reg<FWD, Tin, Tres, Tout, 1, 5>(a, stream);
+    }
 }
 
 template <typename Tin, typename Tres, typename Tout>
 hipError_t fwd(const NormArgs& a, hipStream_t stream) {
+    int waves = 0;
+    if (const int pieces = reg_pieces(a, waves)) return by_size<true, Tin, Tres, Tout>(a, waves, pieces, stream);
     KTime kt("norm_fwd", stream);
     hipLaunchKernelGGL((norm_fwd_kernel<Tin, Tres, Tout>), dim3((unsigned)a.rows), dim3(kT), 0, stream, a);
     return hipGetLastError();
@@ -134,19 +347,23 @@ hipError_t fwd(const NormArgs& a, hipStream_t stream) {
 
 template <typename Tin, typename Tres, typename Tout>
 hipError_t bwd(const NormArgs& a, hipStream_t stream) {
-    if (a.y || a.res_out) {
-        KTime kt("norm_bwd", stream);
-        hipLaunchKernelGGL((norm_bwd_kernel<Tin, Tres, Tout>), dim3((unsigned)a.rows), dim3(kT), 0, stream, a);
-    }
-    if (a.dweight || a.dbias) {
-        const unsigned cols = (unsigned)((a.dim + kT - 1) / kT);
-        {
-            KTime kt("norm_wgrad", stream);
-            hipLaunchKernelGGL((norm_wgrad_kernel<Tres, Tout>), dim3(cols, a.blocks), dim3(kT), 0, stream, a);
+    int waves = 0;
+    const bool sums = a.dweight || a.dbias;
+    if (const int pieces = reg_pieces(a, waves)) {
+        const hipError_t e = by_size<false, Tin, Tres, Tout>(a, waves, pieces, stream);
+        if (e != hipSuccess || !sums) return e;
+    } else {
+        if (a.y || a.res_out) {
+            KTime kt("norm_bwd", stream);
+            hipLaunchKernelGGL((norm_bwd_kernel<Tin, Tres, Tout>), dim3((unsigned)a.rows), dim3(kT), 0, stream, a);
         }
-        KTime kt("norm_wsum", stream);
-        hipLaunchKernelGGL(norm_wsum_kernel, dim3(cols), dim3(kT), 0, stream, a);
+        if (!sums) return hipGetLastError();
+        KTime kt("norm_wgrad", stream);
+        hipLaunchKernelGGL((norm_wgrad_kernel<Tres, Tout>), dim3((unsigned)((a.dim + kT - 1) / kT), a.blocks), dim3(kT), 0,
+                           stream, a);
     }
+    KTime kt("norm_wsum", stream);
+    hipLaunchKernelGGL(norm_wsum_kernel, dim3((unsigned)((a.dim + 63) / 64)), dim3(1024), 0, stream, a);
     return hipGetLastError();
 }
 
@@ -164,12 +381,14 @@ hipError_t by_type(const NormArgs& a, int in_bf16, int res_bf16, int out_bf16, h
 
 }  // namespace
 
-// Row slices that the weight gradients are summed in.
+// Partial rows of dweight and dbias: enough workgroups for the whole GPU
+// (2 per unit for the register kernel, whose workgroup takes the row whole),
+// no more than there are rows.
 int norm_bwd_blocks(int64_t rows, int64_t dim) {
-    const int64_t cols = (dim + kT - 1) / kT;
-    int64_t n = (2048 + cols - 1) / cols;
-    if (n > rows) n = rows;
-    return (int)n;
+    int64_t n = 512;
+    if (dim > 8192) n = (2048 * kT + dim - 1) / dim;
+    if (n > (rows + 3) / 4) n = (rows + 3) / 4;
+    return (int)(n < 1 ? 1 : n);
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, int in_bf16, int res_bf16, int out_bf16, hipStream_t stream) {

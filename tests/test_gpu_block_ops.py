@@ -148,3 +148,23 @@ def test_workspace_too_small_is_refused(gpu):
     with pytest.raises(ss.SelscanError) as e:
         ss.layer_norm_bwd(x, s, None, mean, rstd, workspace=torch.empty(256, dtype=torch.uint8, device=DEV))
     assert e.value.status == ss.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("rows,dim", [(3, 3200), (2, 4096), (3, 5120), (2, 7000), (5000, 64), (2100, 3208)])
+def test_layer_norm_longer_rows_and_many_rows(gpu, rows, dim):
+    """Rows spread over a workgroup; more rows than one pass of the
+    gradients' workgroups."""
+    x, r = _normal((rows, dim), 21, BF16), _normal((rows, dim), 22)
+    w = _normal((dim,), 23, shift=1.0, scale=0.1)
+    y, s, mean, rstd = ss.layer_norm_fwd(x, w, None, residual=r, out_dtype=F32)
+    yr, sr, _, rr = ref.layer_norm(x, w, None, r)
+    amp = float(np.max(rr)) * 2.0 ** -21 * float(np.max(np.abs(sr)))
+    ay, ry = _tol(F32, yr)
+    check_close(host(y).double().numpy(), yr, (ay + amp, ry), "y")
+    dy = _normal((rows, dim), 24)
+    g = ss.layer_norm_bwd(dy, s, w, mean, rstd, x_dtype=BF16)
+    gr = ref.layer_norm_bwd(dy, s, w, mean, rstd)
+    for name, t in (("dx", BF16), ("dresidual", F32), ("dweight", F32), ("dbias", F32)):
+        atol, rtol = _tol(t, gr[name])
+        # (sums over the rows: their magnitudes add up where the result does not)
+        check_close(host(g[name]).double().numpy(), gr[name], (atol * max(1.0, float(np.max(rr))), rtol), name)
