@@ -204,11 +204,16 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 bf16x8 d[2][NO];
-                sm.O[ct].get(0, lane, d[0]);
+                // (the last two waves' rows of A^T begin in the second k-step)
                 sm.O[ct].get(1, lane, d[1]);
-                f32x4 acc[2] = {z4, z4};
-                mm_turns<3, 3, NO>([&](int m) { return fa[m]; }, [&](int m) { return d[m]; }, acc);
-                x[ct] = sum_of(acc);
+                if (w >= 2) {
+                    x[ct] = mm<3>(fa[1], d[1], z4);
+                } else {
+                    sm.O[ct].get(0, lane, d[0]);
+                    f32x4 acc[2] = {z4, z4};
+                    mm_turns<3, 3, NO>([&](int m) { return fa[m]; }, [&](int m) { return d[m]; }, acc);
+                    x[ct] = sum_of(acc);
+                }
             }
         }
         fetch_m(c - 1, GradRec::At, fa);
@@ -219,9 +224,9 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
         for (int ct = 0; ct < CT; ++ct) {
             sm.U[ct].put_tile(w, u[ct] * tail + x[ct] * a.scale, lane);
             sm.G[ct].put_tile(w, o[ct] * gam * a.scale, lane);
-            float* kd = ba.D + ((bh * nch + c) * pad + p0 + 16 * ct) * NP + 4 * lg;
+            float* kd = ba.D + (bh * nch + c) * pad * NP + kept_tile<NP>(p0 - li + 16 * ct, NT * w, lane);
 #pragma unroll
-            for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(kd + 16 * (NT * w + i)) = D[i][ct];
+            for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(kd + 256 * i) = D[i][ct];
         }
         stage_p(sm.K, fk);
         fetch_p(Kg, c - 1, fk);
@@ -232,11 +237,15 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 bf16x8 y[2][3];
-                sm.U[ct].get(0, lane, y[0]);
                 sm.U[ct].get(1, lane, y[1]);
-                f32x4 acc[2] = {z4, z4};
-                mm_turns<3, 3, 3>([&](int m) { return ft[m]; }, [&](int m) { return y[m]; }, acc);
-                r[ct] = sum_of(acc);
+                if (w >= 2) {
+                    r[ct] = mm<3>(ft[1], y[1], z4);
+                } else {
+                    sm.U[ct].get(0, lane, y[0]);
+                    f32x4 acc[2] = {z4, z4};
+                    mm_turns<3, 3, 3>([&](int m) { return ft[m]; }, [&](int m) { return y[m]; }, acc);
+                    r[ct] = sum_of(acc);
+                }
                 sm.R[ct].put_tile(w, -(r[ct] * beta * gam), lane);
             }
         }
@@ -410,9 +419,10 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < NP / 32; ++i) {      // S and D: 32 rows of NP
-            const int id = tid + 256 * i, r = id / (NP / 4), n = 4 * (id % (NP / 4));
-            const f32x4 s = *reinterpret_cast<const f32x4*>(Sg + (int64_t)(pb + r) * NP + n);
-            const f32x4 d = *reinterpret_cast<const f32x4*>(Dg + (int64_t)(pb + r) * NP + n);
+            const int id = wave + 4 * i, p16 = 16 * (id / NB), tile = id % NB;   // two column blocks' tiles in turn
+            const int r = p16 + li, n = 16 * tile + 4 * lg;
+            const f32x4 s = *reinterpret_cast<const f32x4*>(Sg + kept_tile<NP>(pb + p16, tile, lane));
+            const f32x4 d = *reinterpret_cast<const f32x4*>(Dg + kept_tile<NP>(pb + p16, tile, lane));
 #pragma unroll
             for (int e = 0; e < 4; ++e) sd = __builtin_fma((double)s[e], (double)d[e], sd);
             uint2 sp[3], dp[3];

@@ -34,6 +34,14 @@ struct Rec {
 };
 using GradRec = Rec<3, true>;
 
+// A state kept for the gradients: the C tiles of its 16-column blocks one
+// after the other, as the lanes hold them (1 KB a tile).  Floats from the
+// chunk's first to the lane's four of tile i of the columns from p0.
+template <int NP>
+__device__ __forceinline__ int64_t kept_tile(int64_t p0, int i, int lane) {
+    return p0 * NP + i * 256 + lane * 4;
+}
+
 __device__ __forceinline__ int block_at(int t, int s) { return t * (t + 1) / 2 + s; }
 
 __device__ __forceinline__ int64_t seq_len(const DeltaArgs& a, int64_t b) {

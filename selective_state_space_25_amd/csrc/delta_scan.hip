@@ -43,7 +43,7 @@ struct ScanSmem {
     Operands<2, OL ? OL : 1> U[CT];
 };
 
-// KEEP: instead of y, the state entering each chunk [chunk, pad, NP] and U
+// KEEP: instead of y, the state entering each chunk (kept_tile) and U
 // [chunk, 64, pad], which the gradients read (pad: P rounded up to 32, the
 // columns past P zero).
 template <typename Tin, typename Tout, int NP, int CT, bool KEEP>
@@ -193,7 +193,7 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const char
         const int64_t t0 = (int64_t)c * kC;
         const uint16_t* K = &sm.K[c & 1][0][0][0];
         const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
-        // R for the wave's tokens
+        // R for the wave's tokens; Q S
         f32x4 y[CT], u[CT];
         {
             bf16x8 k[KS][NK];
@@ -212,6 +212,16 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const char
                 }
                 mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return s[m]; }, acc);
                 u[ct] = sum_of(acc);
+                if constexpr (!KEEP) {
+                    bf16x8 x[KS][NK];
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        to_operand(fq[ks], x[ks]);
+                        acc[ks] = z4;
+                    }
+                    mm_turns<OA, NK, 3>([&](int m) { return x[m]; }, [&](int m) { return s[m]; }, acc);
+                    y[ct] = sum_of(acc);
+                }
             }
         }
         const f32x4 gam = fgate[0], tail = fgate[1], beta = fgate[2];
@@ -228,22 +238,26 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const char
         if constexpr (KEEP) {
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                float* ks = keep_s + ((bh * nch + c) * pad + p0 + 16 * ct) * NP + 4 * lg;
+                float* ks = keep_s + (bh * nch + c) * pad * NP + kept_tile<NP>(p0 - li + 16 * ct, NT * w, lane);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(ks + 16 * (NT * w + i)) = S[i][ct];
+                for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(ks + 256 * i) = S[i][ct];
             }
         }
         lds_barrier();
-        // U for the wave's tokens; Q S
+        // U for the wave's tokens (the first two waves' T ends in the first k-step)
         {
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 bf16x8 r[2][3];
                 sm.R[ct].get(0, lane, r[0]);
-                sm.R[ct].get(1, lane, r[1]);
-                f32x4 acc[2] = {z4, z4};
-                mm_turns<3, 3, 3>([&](int m) { return ft[m]; }, [&](int m) { return r[m]; }, acc);
-                u[ct] = sum_of(acc);
+                if (w < 2) {
+                    u[ct] = mm<3>(ft[0], r[0], z4);
+                } else {
+                    sm.R[ct].get(1, lane, r[1]);
+                    f32x4 acc[2] = {z4, z4};
+                    mm_turns<3, 3, 3>([&](int m) { return ft[m]; }, [&](int m) { return r[m]; }, acc);
+                    u[ct] = sum_of(acc);
+                }
                 sm.W[ct].put_tile(w, u[ct] * tail, lane);
                 if constexpr (!KEEP) sm.U[ct].put_tile(w, u[ct], lane);
             }
@@ -257,21 +271,6 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const char
                 for (int q = 0; q < 4; ++q) ku[(16 * w + 4 * lg + q) * pad] = u[ct][q];
             }
         } else {
-            bf16x8 x[KS][NK];
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) to_operand(fq[ks], x[ks]);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                bf16x8 s[KS][3];
-                f32x4 acc[KS];
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    sm.S[ct].get(ks, lane, s[ks]);
-                    acc[ks] = z4;
-                }
-                mm_turns<OA, NK, 3>([&](int m) { return x[m]; }, [&](int m) { return s[m]; }, acc);
-                y[ct] = sum_of(acc) * gam;
-            }
             fetch_q(c + 1);
         }
         lds_barrier();
@@ -305,10 +304,15 @@ __global__ __launch_bounds__(256) void delta_scan_kernel(DeltaArgs a, const char
             for (int ct = 0; ct < CT; ++ct) {
                 bf16x8 x[2][OA];
                 sm.U[ct].get(0, lane, x[0]);
-                sm.U[ct].get(1, lane, x[1]);
-                f32x4 acc[2] = {y[ct], z4};
-                mm_turns<OA, OA, OA>([&](int m) { return fa[m]; }, [&](int m) { return x[m]; }, acc);
-                y[ct] = sum_of(acc);
+                y[ct] *= gam;
+                if (w < 2) {
+                    y[ct] = mm<OA>(fa[0], x[0], y[ct]);
+                } else {
+                    sm.U[ct].get(1, lane, x[1]);
+                    f32x4 acc[2] = {y[ct], z4};
+                    mm_turns<OA, OA, OA>([&](int m) { return fa[m]; }, [&](int m) { return x[m]; }, acc);
+                    y[ct] = sum_of(acc);
+                }
             }
             fetch_a(c + 1);
 #pragma unroll
@@ -465,9 +469,9 @@ __global__ __launch_bounds__(256) void delta_wide_kernel(DeltaArgs a, const char
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) split8<3>(S[2 * ks], S[2 * ks + 1], Sp[ks]);
             if constexpr (KEEP) {
-                float* ks = keep_s + ((bh * nch + c) * pad + p) * NP + 4 * lg;
+                float* ks = keep_s + (bh * nch + c) * pad * NP + kept_tile<NP>(p - li, 0, lane);
 #pragma unroll
-                for (int i = 0; i < NB; ++i) *reinterpret_cast<f32x4*>(ks + 16 * i) = S[i];
+                for (int i = 0; i < NB; ++i) *reinterpret_cast<f32x4*>(ks + 256 * i) = S[i];
             }
             f32x4 E[4], U[4];
 #pragma unroll

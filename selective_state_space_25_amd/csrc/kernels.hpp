@@ -238,8 +238,9 @@ struct DeltaBwdArgs {
     void *dq, *dk, *dv;
     float *dg, *dbeta, *dh0;
     char* recs;
-    float* S;                 // [chunks, pad, NP] state entering each chunk (NP: N rounded up to 64 or 128)
-    float* D;                 // [chunks, pad, NP] adjoint of the state leaving it
+    float* S;                 // [chunks, pad / 16, NP / 16, 64, 4] C tiles of the state entering each chunk
+                              // (NP: N rounded up to 64 or 128)
+    float* D;                 // the same of the adjoint of the state leaving it
     float* U;                 // [chunks, 64, pad]
     float* dR;                // [chunks, 64, pad]
     float *pq, *pk;           // [batch, L, H, N] per-head dq and dk when heads share q and k, else NULL
