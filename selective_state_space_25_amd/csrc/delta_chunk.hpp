@@ -44,8 +44,9 @@ __device__ __forceinline__ int64_t kept_tile(int64_t p0, int i, int lane) {
 
 __device__ __forceinline__ int block_at(int t, int s) { return t * (t + 1) / 2 + s; }
 
+// Tokens of batch element b.
 __device__ __forceinline__ int64_t seq_len(const DeltaArgs& a, int64_t b) {
-    return a.lengths ? min((int64_t)max(a.lengths[b], 0), a.L) : a.L;
+    return a.lengths ? min((int64_t)max(__builtin_amdgcn_readfirstlane(a.lengths[b]), 0), a.L) : a.L;
 }
 
 __device__ __forceinline__ float exp_f32(float x) { return fast_exp2(x * kLog2e); }
@@ -65,10 +66,17 @@ __device__ __forceinline__ void lds_barrier() {
 // A buffer over `rows` rows spaced `stride` bytes apart, of which `bytes`
 // belong to it: loads past its end give zero, stores there are dropped.
 // Offsets are 32-bit: 64 rows stay within 2^30 bytes (checked on the host).
+// The descriptor is put in scalar registers by force: 64-bit comparisons run
+// on the vector unit, and a descriptor in vector registers, equal in every
+// lane or not, is accessed in a loop over its values (1.5 us a chunk here).
 constexpr int kOut = 1 << 30;   // an offset past every buffer, with room for a few rows more
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buf(const void* p, int rows, int64_t stride, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, rows > 0 ? (rows - 1) * (int)stride + bytes : 0,
-                                             0x00020000);
+    const uint64_t v = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);   // (the builtin returns an int: its sign
+    const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));   // must not reach the other half)
+    const uint64_t u = (uint64_t)hi << 32 | lo;
+    const int n = __builtin_amdgcn_readfirstlane(rows > 0 ? (rows - 1) * (int)stride + bytes : 0);
+    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), 0, n, 0x00020000);
 }
 
 template <typename T> __device__ __forceinline__ float buf_ld(__amdgpu_buffer_rsrc_t r, int off);
