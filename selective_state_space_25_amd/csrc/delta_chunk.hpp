@@ -157,6 +157,7 @@ __device__ __forceinline__ void lower_tile(int k, int& tb, int& sb) {
     sb = k - tb * (tb + 1) / 2;
 }
 
+__device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[1]) { return v[0]; }
 __device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[2]) { return v[0] + v[1]; }
 __device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); }
 
@@ -207,6 +208,19 @@ struct Operands {
     __device__ __forceinline__ void get(int ks, int lane, bf16x8 (&w)[NPL]) const {
 #pragma unroll
         for (int i = 0; i < NPL; ++i) w[i] = ld8(p[ks][i][lane]);
+    }
+};
+
+// C tiles handed through LDS as they are: a lane's four values in its slot.
+struct Tiles {
+    float p[4][64][4];
+    __device__ __forceinline__ void put(int t, f32x4 v, int lane) { *reinterpret_cast<f32x4*>(p[t][lane]) = v; }
+    __device__ __forceinline__ f32x4 get(int t, int lane) const { return *reinterpret_cast<const f32x4*>(p[t][lane]); }
+    // k-step ks of them as a B operand, split here
+    template <int NPL>
+    __device__ __forceinline__ void operand(int ks, int lane, bf16x8 (&w)[NPL]) const {
+        const int t = 2 * ks + (lane >> 5), at = 32 * ((lane >> 4) & 1) + (lane & 15);
+        split8<NPL>(get(t, at), get(t, at + 16), w);
     }
 };
 

@@ -37,6 +37,8 @@ constexpr int kThreads = 512;
 template <typename Tin, int NP, int OL>
 struct ScanSmem {
     static constexpr int kRow = NP + 8;
+    float gam[kC], tail[kC], beta[kC];
+    Tiles V;
     uint16_t K[2][kPlanes<Tin>][kC][kRow];   // by chunk parity
     Operands<NP / 32, 3> S;
     Operands<2, 3> R, W;                     // R; e^(last - cum) U
@@ -47,7 +49,7 @@ struct ScanSmem {
 // [chunk, 64, pad], which the gradients read (pad: P rounded up to 32, the
 // columns past P zero).
 template <typename Tin, typename Tout, int NP, bool KEEP>
-__global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb,
+__global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout) == 2) ? 4 : 2) void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb,
                                                               float* keep_s, float* keep_u, int pad) {
     constexpr int OL = KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3;
     constexpr int OA = OL ? OL : 1;
@@ -105,21 +107,7 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a, const
 #pragma unroll
             for (int i = 0; i < NT; ++i) sm.S.put_tile(NT * w + i, S[i], lane);
         };
-        const char* Vg = static_cast<const char*>(a.v) + b * a.L * sv + h * P * ES;
-        const int voff = p < P ? (16 * w + 4 * lg) * (int)sv + p * ES : kOut;
         bf16x8 ft[2][3];
-        f32x4 fgate[3];
-        float fgl;
-        Tin fv[4];
-        auto fetch_v = [&](int c) {
-            const auto vb = chunk_rows(Vg, sv, c, P * ES);
-            const auto rb = record(c);
-#pragma unroll
-            for (int i = 0; i < 3; ++i) fgate[i] = buf_ld4(rb, Rc::gam + (i * kC + 16 * w + 4 * lg) * 4);
-            fgl = buf_raw<float>(rb, Rc::gam + (kC - 1) * 4);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) fv[q] = buf_raw<Tin>(vb, voff + q * (int)sv);
-        };
         auto fetch_t = [&](int c) {
             const auto rb = record(c);
 #pragma unroll
@@ -128,7 +116,6 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a, const
                 for (int x = 0; x < 3; ++x) ft[ks][x] = buf_op(rb, toff[ks] + Rc::T + x * kPlane);
         };
         put_state();
-        fetch_v(0);
         fetch_t(0);
         __builtin_amdgcn_s_setprio(3);       // the chain goes first on the SIMD
         lds_barrier();
@@ -149,13 +136,13 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a, const
                 mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return s[m]; }, acc);
                 u = sum_of(acc);
             }
-            const f32x4 gam = fgate[0], tail = fgate[1], beta = fgate[2], v = widen(fv);
-            const float gl = fgl;
+            auto gate = [&](const float* g) { return *reinterpret_cast<const f32x4*>(g + 16 * w + 4 * lg); };
+            const f32x4 gam = gate(sm.gam), tail = gate(sm.tail), beta = gate(sm.beta), v = sm.V.get(w, lane);
+            const float gl = sm.gam[kC - 1];
             f32x4 r;
 #pragma unroll
             for (int q = 0; q < 4; ++q) r[q] = beta[q] * __builtin_fmaf(-gam[q], u[q], v[q]);
             sm.R.put_tile(w, r, lane);
-            fetch_v(c + 1);
             if constexpr (KEEP) {
                 float* ks = keep_s + (bh * nch + c) * pad * NP + kept_tile<NP>(p - li, NT * w, lane);
 #pragma unroll
@@ -170,14 +157,22 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a, const
                     u = mm<3>(ft[0], x[0], z4);
                 } else {
                     sm.R.get(1, lane, x[1]);
-                    f32x4 acc[2] = {z4, z4};
-                    mm_turns<3, 3, 3>([&](int m) { return ft[m]; }, [&](int m) { return x[m]; }, acc);
-                    u = sum_of(acc);
+                    u = mm_pair(ft, x);
                 }
                 sm.W.put_tile(w, u * tail, lane);
                 if constexpr (!KEEP) sm.U.put_tile(w, u, lane);
             }
             fetch_t(c + 1);
+            bf16x8 k[NT * 2][NK];
+            auto load_kt = [&]() {
+#pragma unroll
+                for (int i = 0; i < NT * 2; ++i)
+#pragma unroll
+                    for (int l = 0; l < NK; ++l)
+                        k[i][l] = ld_down(K + l * kC * kRow, kRow, 32 * (i & 1), 16 * (NT * w + i / 2), lane);
+            };
+            // before the barrier that it does not need, where registers allow
+            if constexpr (OL != 3) load_kt();
             if constexpr (KEEP) {
                 float* ku = keep_u + (bh * nch + c) * kC * pad + p;
 #pragma unroll
@@ -186,17 +181,13 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a, const
             lds_barrier();
             // the wave's rows of the next state
             {
-                bf16x8 k[NT * 2][NK], x[2][3];
+                if constexpr (OL == 3) load_kt();
+                bf16x8 x[2][3];
                 sm.W.get(0, lane, x[0]);
                 sm.W.get(1, lane, x[1]);
                 f32x4 acc[NT * 2];
 #pragma unroll
-                for (int i = 0; i < NT * 2; ++i) {
-#pragma unroll
-                    for (int l = 0; l < NK; ++l)
-                        k[i][l] = ld_down(K + l * kC * kRow, kRow, 32 * (i & 1), 16 * (NT * w + i / 2), lane);
-                    acc[i] = i & 1 ? z4 : S[i / 2] * gl;
-                }
+                for (int i = 0; i < NT * 2; ++i) acc[i] = i & 1 ? z4 : S[i / 2] * gl;
                 mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return x[m & 1]; }, acc);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) S[i] = acc[2 * i] + acc[2 * i + 1];
@@ -253,6 +244,20 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a, const
 #pragma unroll
             for (int x = 0; x < OA; ++x) fa[ks][x] = buf_op(rb, toff[ks] + Rc::A + x * kPlane);
     };
+    const char* Vg = static_cast<const char*>(a.v) + b * a.L * sv + h * P * ES;
+    const int voff = p < P ? (16 * w + 4 * lg) * (int)sv + p * ES : kOut;
+    f32x4 fgate;
+    Tin fv[4];
+    auto fetch_v = [&](int c) {
+        const auto vb = chunk_rows(Vg, sv, c, P * ES);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) fv[q] = buf_raw<Tin>(vb, voff + q * (int)sv);
+        fgate = buf_ld4(record(c), tid < 48 ? Rc::gam + 16 * tid : kOut);
+    };
+    auto stage_v = [&]() {
+        sm.V.put(w, widen(fv), lane);
+        if (tid < 48) *reinterpret_cast<f32x4*>(&sm.gam[4 * tid]) = fgate;   // gam, tail, beta in a row
+    };
     auto stage_k = [&](int c) {
 #pragma unroll
         for (int i = 0; i < NPC; ++i) {
@@ -279,12 +284,15 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a, const
         for (int q = 0; q < 4; ++q) buf_st(yb, yoff + q * (int)sy, a.scale * y[q], Tout(0));
     };
     fetch_k(0);
+    fetch_v(0);
     if constexpr (!KEEP) {
         fetch_q(0);
         fetch_a(0);
     }
     stage_k(0);
+    stage_v();
     fetch_k(1);
+    fetch_v(1);
     f32x4 y = z4;
     lds_barrier();
     for (int c = 0; c < mine; ++c) {
@@ -293,21 +301,28 @@ __global__ __launch_bounds__(kThreads) void delta_scan_kernel(DeltaArgs a, const
         }
         lds_barrier();
         if constexpr (!KEEP) {
-            f32x4 acc[KS];
-            bf16x8 x[KS][NK], s[KS][3];
+            constexpr int M = 2;   // k-steps at a time, as registers allow
+            f32x4 acc[M];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                sm.S.get(ks, lane, s[ks]);
-                to_operand(fq[ks], x[ks]);
-                acc[ks] = z4;
+            for (int i = 0; i < M; ++i) acc[i] = z4;
+#pragma unroll
+            for (int k0 = 0; k0 < KS; k0 += M) {
+                bf16x8 x[M][NK], s[M][3];
+#pragma unroll
+                for (int i = 0; i < M; ++i) {
+                    sm.S.get(k0 + i, lane, s[i]);
+                    to_operand(fq[k0 + i], x[i]);
+                }
+                mm_turns<OA, NK, 3>([&](int m) { return x[m]; }, [&](int m) { return s[m]; }, acc);
             }
-            mm_turns<OA, NK, 3>([&](int m) { return x[m]; }, [&](int m) { return s[m]; }, acc);
             y = sum_of(acc) * fgam;
             fetch_q(c + 1);
         }
         lds_barrier();
         stage_k(c + 1);
+        stage_v();
         fetch_k(c + 2);
+        fetch_v(c + 2);
         lds_barrier();
     }
     if constexpr (!KEEP) {

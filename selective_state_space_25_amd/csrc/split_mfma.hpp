@@ -59,6 +59,26 @@ __device__ __forceinline__ void mm_turns(FA a, FB b, f32x4 (&c)[M]) {
             }
 }
 
+// The 12 plane products of two k-steps of fp32 by fp32, four chains of three.
+__device__ __forceinline__ f32x4 mm_pair(const bf16x8 (&a)[2][3], const bf16x8 (&b)[2][3]) {
+    f32x4 c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < 2; ++k) c[k] = mfma(a[k][1], b[k][1], c[k]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) c[2 + k] = mfma(a[k][0], b[k][2], c[2 + k]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) c[k] = mfma(a[k][2], b[k][0], c[k]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) c[2 + k] = mfma(a[k][0], b[k][1], c[2 + k]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) c[k] = mfma(a[k][1], b[k][0], c[k]);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) c[2 + k] = mfma(a[k][0], b[k][0], c[2 + k]);
+    return (c[0] + c[1]) + (c[2] + c[3]);
+}
+
 // Pairs e, e + 1 of two values into word `e` of NP planes (a plane is one
 // operand, four words of two bf16 each).
 template <int NP>
