@@ -60,14 +60,17 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
     if (bh >= a.batch * a.H) return;
     const int64_t b = bh / a.H, h = bh - b * a.H, grp = h / (a.H / a.G);
     const int64_t len = seq_len(a, b);
-    const int mine = (int)((len + kC - 1) / kC);
+    const Chunks seq(len), all(a.L);
+    const int mine = seq.n;
     const int N = a.N, P = (int)a.P, pad = ba.pad;
     const int p0 = (jx % npb) * 16 * CT + li;
-    const int64_t sk = a.G * a.qk_row * ES, sv = a.H * P * ES, so = a.H * P * EO;
-    const char* Kg = static_cast<const char*>(a.k) + b * a.L * sk + grp * a.qk_row * ES;
-    const char* Qg = static_cast<const char*>(a.q) + b * a.L * sk + grp * a.qk_row * ES;
-    const char* Og = static_cast<const char*>(ba.dout) + b * a.L * so + h * P * EO;
-    char* dVg = static_cast<char*>(ba.dv) + b * a.L * sv + h * P * ES;
+    const int sk = scalar((int)(a.G * a.qk_row * ES)), sv = scalar((int)(a.H * P * ES)), so = scalar((int)(a.H * P * EO));
+    const int64_t krow = b * a.L * sk + grp * a.qk_row * ES;
+    const char* Kg = scalar(static_cast<const char*>(a.k) + krow);
+    const char* Qg = scalar(static_cast<const char*>(a.q) + krow);
+    const char* Og = scalar(static_cast<const char*>(ba.dout) + b * a.L * so + h * P * EO);
+    char* dVg = scalar(static_cast<char*>(ba.dv) + b * a.L * sv + h * P * ES);
+    const char* Rg = scalar(ba.recs + bh * nch * GradRec::bytes);
 
     f32x4 D[NT][CT];
 #pragma unroll
@@ -89,34 +92,34 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
 #pragma unroll
     for (int i = 0; i < NPC; ++i) {
         const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-        koff[i] = n0 < a.NL ? r * (int)sk + n0 * ES : kOut;
+        koff[i] = n0 < a.NL ? r * sk + n0 * ES : kOut;
     }
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         const int n = 32 * ks + 8 * lg;
-        roff[ks] = n < a.NL ? (16 * w + li) * (int)sk + n * ES : kOut;
+        roff[ks] = n < a.NL ? (16 * w + li) * sk + n * ES : kOut;
     }
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) toff[ks] = row_of_t(w, ks, lane);
 #pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         const int p = p0 + 16 * ct;
-        voff[ct] = p < P ? (16 * w + 4 * lg) * (int)sv + p * ES : kOut;
-        ooff[ct] = p < P ? (16 * w + 4 * lg) * (int)so + p * EO : kOut;
+        voff[ct] = p < P ? (16 * w + 4 * lg) * sv + p * ES : kOut;
+        ooff[ct] = p < P ? (16 * w + 4 * lg) * so + p * EO : kOut;
     }
 
-    // inputs on their way, as in delta_scan.hip (before the first chunk the
-    // first one is read again)
+    // Inputs are asked for as soon as the chunk before has used their
+    // registers, a chunk's work ahead (before the first chunk: buffers of no
+    // rows)
     Raw8<Tin> fk[NPC], fq[NPC], fr[KS];
     bf16x8 ft[2][3], fa[2][3];
     f32x4 fgate[3];
     float fgl;
     Tdo fo[CT][4];
-    auto rows = [&](const char* base, int64_t stride, int c, int bytes) {
-        const int64_t t0 = (int64_t)max(c, 0) * kC;
-        return rows_buf(base + t0 * stride, (int)min((int64_t)kC, len - t0), stride, bytes);
+    auto rows = [&](const char* base, int stride, int c, int bytes) {
+        return rows_buf(base + (int64_t)c * kC * stride, c < 0 ? 0 : seq.rows(c), stride, bytes);
     };
-    auto record = [&](int c) { return rows_buf(ba.recs + (bh * nch + max(c, 0)) * GradRec::bytes, 1, 0, GradRec::bytes); };
+    auto record = [&](int c) { return rows_buf(Rg + (int64_t)c * GradRec::bytes, c < 0 ? 0 : 1, 0, GradRec::bytes); };
     auto fetch_p = [&](const char* base, int c, Raw8<Tin> (&f)[NPC]) {
         const auto kb = rows(base, sk, c, a.NL * ES);
 #pragma unroll
@@ -132,7 +135,7 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) fo[ct][q] = buf_raw<Tdo>(ob, ooff[ct] + q * (int)so);
+            for (int q = 0; q < 4; ++q) fo[ct][q] = buf_raw<Tdo>(ob, ooff[ct] + q * so);
     };
     auto fetch_g = [&](int c) {
         const auto rb = record(c);
@@ -178,7 +181,6 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
     }
     lds_barrier();
     for (int c = mine - 1; c >= 0; --c) {
-        const int64_t t0 = (int64_t)c * kC;
         const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
         // dU for the wave's tokens
         f32x4 u[CT], x[CT];
@@ -252,14 +254,14 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
         fetch_m(c - 1, GradRec::Tt, ft);
         stage_p(sm.Q, fq);
         fetch_p(Qg, c - 1, fq);
-        const auto vb = rows_buf(dVg + t0 * sv, (int)min((int64_t)kC, a.L - t0), sv, P * ES);
+        const auto vb = rows_buf(scalar(dVg + (int64_t)c * kC * sv), scalar(all.rows(c)), sv, P * ES);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
             float* kr = ba.dR + (bh * nch + c) * kC * pad + p0 + 16 * ct;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 kr[(16 * w + 4 * lg + q) * pad] = r[ct][q];
-                buf_st(vb, voff[ct] + q * (int)sv, beta[q] * r[ct][q], Tin(0));
+                buf_st(vb, voff[ct] + q * sv, beta[q] * r[ct][q], Tin(0));
             }
         }
         lds_barrier();
@@ -411,10 +413,10 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     const float* Rg = ba.dR + (int64_t)blockIdx.x * kC * pad;
     constexpr int ES = (int)sizeof(Tin), EO = (int)sizeof(Tdo);
     const int P = (int)a.P;
-    const int64_t sk = a.G * a.qk_row * ES, sv = a.H * P * ES, so = a.H * P * EO;
+    const int sk = scalar((int)(a.G * a.qk_row * ES)), sv = scalar((int)(a.H * P * ES)), so = scalar((int)(a.H * P * EO));
     const int64_t row0 = b * a.L + t0;
-    const auto ob = rows_buf(static_cast<const char*>(ba.dout) + row0 * so + h * P * EO, live, so, P * EO);
-    const auto vb = rows_buf(static_cast<const char*>(a.v) + row0 * sv + h * P * ES, live, sv, P * ES);
+    const auto ob = rows_buf(scalar(static_cast<const char*>(ba.dout) + row0 * so + h * P * EO), scalar(live), so, P * EO);
+    const auto vb = rows_buf(scalar(static_cast<const char*>(a.v) + row0 * sv + h * P * ES), scalar(live), sv, P * ES);
     for (int pb = 0; pb < pad; pb += kPb) {
         __syncthreads();
 #pragma unroll
@@ -441,7 +443,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             const f32x4 d = *reinterpret_cast<const f32x4*>(Rg + (int64_t)r * pad + pb + e0);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                rv[i] = __builtin_fmaf(d[e], buf_ld<Tin>(vb, pb + e0 + e < P ? r * (int)sv + (pb + e0 + e) * ES : kOut), rv[i]);
+                rv[i] = __builtin_fmaf(d[e], buf_ld<Tin>(vb, pb + e0 + e < P ? r * sv + (pb + e0 + e) * ES : kOut), rv[i]);
             uint2 up[3], dp[3];
             split4<3>(u, up);
             split4<3>(d, dp);
@@ -453,7 +455,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
         }
         {                                        // dout: 64 rows of 32
             const int r = tid >> 2, e0 = 8 * (tid & 3);
-            const int off = r * (int)so + (pb + e0) * EO;
+            const int off = r * so + (pb + e0) * EO;
             Raw8<Tdo> o;
             if (ba.vec_p) {
                 fetch8(ob, pb + e0 < P ? off : kOut, o);
@@ -521,12 +523,12 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     // K and Q over what the steps used
     {
         const int64_t at = row0 * sk + grp * a.qk_row * ES;
-        const auto kb = rows_buf(static_cast<const char*>(a.k) + at, live, sk, a.NL * ES);
-        const auto qb = rows_buf(static_cast<const char*>(a.q) + at, live, sk, a.NL * ES);
+        const auto kb = rows_buf(scalar(static_cast<const char*>(a.k) + at), scalar(live), sk, a.NL * ES);
+        const auto qb = rows_buf(scalar(static_cast<const char*>(a.q) + at), scalar(live), sk, a.NL * ES);
 #pragma unroll
         for (int i = 0; i < NP / 32; ++i) {
             const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-            const int off = n0 < a.NL ? r * (int)sk + n0 * ES : kOut;
+            const int off = n0 < a.NL ? r * sk + n0 * ES : kOut;
             Raw8<Tin> k, q;
             fetch8(kb, off, k);
             fetch8(qb, off, q);

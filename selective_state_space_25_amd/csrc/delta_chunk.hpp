@@ -66,18 +66,31 @@ __device__ __forceinline__ void lds_barrier() {
 // A buffer over `rows` rows spaced `stride` bytes apart, of which `bytes`
 // belong to it: loads past its end give zero, stores there are dropped.
 // Offsets are 32-bit: 64 rows stay within 2^30 bytes (checked on the host).
-// The descriptor is put in scalar registers by force: 64-bit comparisons run
-// on the vector unit, and a descriptor in vector registers, equal in every
-// lane or not, is accessed in a loop over its values (1.5 us a chunk here).
 constexpr int kOut = 1 << 30;   // an offset past every buffer, with room for a few rows more
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buf(const void* p, int rows, int64_t stride, int bytes) {
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buf(const void* p, int rows, int stride, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, rows > 0 ? (rows - 1) * stride + bytes : 0, 0x00020000);
+}
+
+// A value that is the same in every lane, in a scalar register.  Descriptors
+// have to be made of such: one in vector registers, equal in every lane or
+// not, is accessed in a loop over its values (1.5 us a chunk in the scan).
+__device__ __forceinline__ int scalar(int v) { return __builtin_amdgcn_readfirstlane(v); }
+template <typename T>
+__device__ __forceinline__ T* scalar(T* p) {
     const uint64_t v = reinterpret_cast<uint64_t>(p);
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);   // (the builtin returns an int: its sign
     const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));   // must not reach the other half)
-    const uint64_t u = (uint64_t)hi << 32 | lo;
-    const int n = __builtin_amdgcn_readfirstlane(rows > 0 ? (rows - 1) * (int)stride + bytes : 0);
-    return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(u), 0, n, 0x00020000);
+    return reinterpret_cast<T*>((uint64_t)hi << 32 | lo);
 }
+
+// Chunks of n tokens, and the tokens in chunk c of them (32-bit comparisons,
+// which scalar registers allow).
+struct Chunks {
+    int n, last;
+    __device__ __forceinline__ explicit Chunks(int64_t tokens)
+        : n(scalar((int)((tokens + kC - 1) / kC))), last(scalar((int)(tokens - (tokens + kC - 1) / kC * kC + kC))) {}
+    __device__ __forceinline__ int rows(int c) const { return c + 1 < n ? kC : c + 1 == n ? last : 0; }
+};
 
 template <typename T> __device__ __forceinline__ float buf_ld(__amdgpu_buffer_rsrc_t r, int off);
 template <> __device__ __forceinline__ float buf_ld<float>(__amdgpu_buffer_rsrc_t r, int off) {

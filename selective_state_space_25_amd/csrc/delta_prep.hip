@@ -100,16 +100,17 @@ __global__ __launch_bounds__(64 * kUnits) void delta_prep_kernel(DeltaArgs a, ch
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) kk[i] = qk[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     {
-        const int64_t sk = a.G * a.qk_row * ES, at = (b * a.L + t0) * sk + grp * a.qk_row * ES;
-        const auto kb = rows_buf(static_cast<const char*>(a.k) + at, live, sk, a.NL * ES);
-        const auto qb = rows_buf(static_cast<const char*>(a.q) + at, live, sk, a.NL * ES);
+        const int sk = scalar((int)(a.G * a.qk_row * ES));
+        const int64_t at = (b * a.L + t0) * sk + grp * a.qk_row * ES;
+        const auto kb = rows_buf(scalar(static_cast<const char*>(a.k) + at), scalar(live), sk, a.NL * ES);
+        const auto qb = rows_buf(scalar(static_cast<const char*>(a.q) + at), scalar(live), sk, a.NL * ES);
 #pragma unroll
         for (int ks = 0; ks < NP / 32; ++ks) {
             const int n = 32 * ks + 8 * lg;
             bf16x8 k[4][NK], q[4][NK];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
-                const int off = n < a.NL ? (16 * t + li) * (int)sk + n * ES : kOut;
+                const int off = n < a.NL ? (16 * t + li) * sk + n * ES : kOut;
                 Raw8<Tin> x, y;
                 fetch8(kb, off, x);
                 fetch8(qb, off, y);

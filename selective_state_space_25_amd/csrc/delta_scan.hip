@@ -72,24 +72,28 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
     if (bh >= a.batch * a.H) return;
     const int64_t b = bh / a.H, h = bh - b * a.H, grp = h / (a.H / a.G);
     const int64_t len = seq_len(a, b);
-    const int mine = (int)((len + kC - 1) / kC);
+    const Chunks seq(len), all(a.L);         // of the sequence; of the tensors
+    const int mine = seq.n;
     const int N = a.N, P = (int)a.P;
     const int p = (jx % npb) * 16 + li;      // the lane's column
     // strides of a token in bytes
-    const int64_t sk = a.G * a.qk_row * ES, sv = a.H * P * ES, sy = a.H * P * EO;
+    const int sk = scalar((int)(a.G * a.qk_row * ES)), sv = scalar((int)(a.H * P * ES)), sy = scalar((int)(a.H * P * EO));
     const int64_t krow = b * a.L * sk + grp * a.qk_row * ES;
-    char* Yg = static_cast<char*>(a.y) + b * a.L * sy + h * P * EO;
+    const char* Kg = scalar(static_cast<const char*>(a.k) + krow);
+    const char* Qg = scalar(static_cast<const char*>(a.q) + krow);
+    const char* Vg = scalar(static_cast<const char*>(a.v) + b * a.L * sv + h * P * ES);
+    char* Yg = scalar(static_cast<char*>(a.y) + b * a.L * sy + h * P * EO);
+    const char* Rg = scalar(recs + bh * nch * Rc::bytes);
     const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
 
     // Inputs are asked for as soon as the chunk before has used their
     // registers, a chunk's work ahead.  (Past the end: buffers of no rows.)
     // Loads and stores complete in order: stores go out after a phase's
     // loads, so that the waits for those find only stores a chunk older.
-    auto chunk_rows = [&](const char* base, int64_t stride, int c, int bytes) {
-        const int64_t t0 = (int64_t)c * kC;
-        return rows_buf(base + t0 * stride, (int)min((int64_t)kC, len - t0), stride, bytes);
+    auto chunk_rows = [&](const char* base, int stride, int c, int bytes) {
+        return rows_buf(base + (int64_t)c * kC * stride, seq.rows(c), stride, bytes);
     };
-    auto record = [&](int c) { return rows_buf(recs + (bh * nch + c) * Rc::bytes, c < mine ? 1 : 0, 0, Rc::bytes); };
+    auto record = [&](int c) { return rows_buf(Rg + (int64_t)c * Rc::bytes, c < mine ? 1 : 0, 0, Rc::bytes); };
     int toff[2];
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) toff[ks] = row_of(w, ks, lane);
@@ -117,7 +121,6 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
         };
         put_state();
         fetch_t(0);
-        __builtin_amdgcn_s_setprio(3);       // the chain goes first on the SIMD
         lds_barrier();
         for (int c = 0; c < mine; ++c) {
             const uint16_t* K = &sm.K[c & 1][0][0][0];
@@ -195,7 +198,6 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
             put_state();
             lds_barrier();
         }
-        __builtin_amdgcn_s_setprio(0);
         if (!KEEP && a.last && p < P) {
 #pragma unroll
             for (int i = 0; i < NT; ++i)
@@ -209,20 +211,18 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
     }
 
     // ---- helper waves
-    const char* Kg = static_cast<const char*>(a.k) + krow;
-    const char* Qg = static_cast<const char*>(a.q) + krow;
     int koff[NPC], qoff[KS];
 #pragma unroll
     for (int i = 0; i < NPC; ++i) {
         const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-        koff[i] = n0 < a.NL ? r * (int)sk + n0 * ES : kOut;
+        koff[i] = n0 < a.NL ? r * sk + n0 * ES : kOut;
     }
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
         const int n = 32 * ks + 8 * lg;
-        qoff[ks] = n < a.NL ? (16 * w + li) * (int)sk + n * ES : kOut;
+        qoff[ks] = n < a.NL ? (16 * w + li) * sk + n * ES : kOut;
     }
-    const int yoff = p < P ? (16 * w + 4 * lg) * (int)sy + p * EO : kOut;
+    const int yoff = p < P ? (16 * w + 4 * lg) * sy + p * EO : kOut;
     Raw8<Tin> fk[NPC], fq[KS];
     bf16x8 fa[2][OA];
     f32x4 fgam;
@@ -244,14 +244,13 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
 #pragma unroll
             for (int x = 0; x < OA; ++x) fa[ks][x] = buf_op(rb, toff[ks] + Rc::A + x * kPlane);
     };
-    const char* Vg = static_cast<const char*>(a.v) + b * a.L * sv + h * P * ES;
-    const int voff = p < P ? (16 * w + 4 * lg) * (int)sv + p * ES : kOut;
+    const int voff = p < P ? (16 * w + 4 * lg) * sv + p * ES : kOut;
     f32x4 fgate;
     Tin fv[4];
     auto fetch_v = [&](int c) {
         const auto vb = chunk_rows(Vg, sv, c, P * ES);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) fv[q] = buf_raw<Tin>(vb, voff + q * (int)sv);
+        for (int q = 0; q < 4; ++q) fv[q] = buf_raw<Tin>(vb, voff + q * sv);
         fgate = buf_ld4(record(c), tid < 48 ? Rc::gam + 16 * tid : kOut);
     };
     auto stage_v = [&]() {
@@ -278,10 +277,9 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
             y = sum_of(acc);
         }
         fetch_a(c + 1);
-        const int64_t t0 = (int64_t)c * kC;
-        const auto yb = rows_buf(Yg + t0 * sy, (int)min((int64_t)kC, a.L - t0), sy, P * EO);
+        const auto yb = rows_buf(Yg + (int64_t)c * kC * sy, all.rows(c), sy, P * EO);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) buf_st(yb, yoff + q * (int)sy, a.scale * y[q], Tout(0));
+        for (int q = 0; q < 4; ++q) buf_st(yb, yoff + q * sy, a.scale * y[q], Tout(0));
     };
     fetch_k(0);
     fetch_v(0);
