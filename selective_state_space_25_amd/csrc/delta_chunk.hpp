@@ -63,14 +63,6 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
-// A buffer over `rows` rows spaced `stride` bytes apart, of which `bytes`
-// belong to it: loads past its end give zero, stores there are dropped.
-// Offsets are 32-bit: 64 rows stay within 2^30 bytes (checked on the host).
-constexpr int kOut = 1 << 30;   // an offset past every buffer, with room for a few rows more
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buf(const void* p, int rows, int stride, int bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, rows > 0 ? (rows - 1) * stride + bytes : 0, 0x00020000);
-}
-
 // A value that is the same in every lane, in a scalar register.  Descriptors
 // have to be made of such: one in vector registers, equal in every lane or
 // not, is accessed in a loop over its values (1.5 us a chunk in the scan).
@@ -81,6 +73,14 @@ __device__ __forceinline__ T* scalar(T* p) {
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v);   // (the builtin returns an int: its sign
     const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));   // must not reach the other half)
     return reinterpret_cast<T*>((uint64_t)hi << 32 | lo);
+}
+
+// A buffer over `rows` rows spaced `stride` bytes apart, of which `bytes`
+// belong to it: loads past its end give zero, stores there are dropped.
+// Offsets are 32-bit: 64 rows stay within 2^30 bytes (checked on the host).
+constexpr int kOut = 1 << 30;   // an offset past every buffer, with room for a few rows more
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buf(const void* p, int rows, int stride, int bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), 0, scalar(rows > 0 ? (rows - 1) * stride + bytes : 0), 0x00020000);
 }
 
 // Chunks of n tokens, and the tokens in chunk c of them (32-bit comparisons,
