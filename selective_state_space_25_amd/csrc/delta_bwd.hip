@@ -341,6 +341,36 @@ struct GradSmem {
     };
 };
 
+// Four elements of a row as loaded, those past n zero (vec: in one piece).
+template <typename T> struct Raw4;
+template <> struct Raw4<uint16_t> { unsigned w[2]; };
+template <> struct Raw4<float> { f32x4 v; };
+__device__ __forceinline__ void fetch4(__amdgpu_buffer_rsrc_t b, int off, int n, int vec, Raw4<uint16_t>& r) {
+    if (vec) {
+        const auto w = __builtin_amdgcn_raw_buffer_load_b64(b, n > 0 ? off : kOut, 0, 0);
+        r.w[0] = w[0];
+        r.w[1] = w[1];
+    } else {
+        unsigned e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) e[i] = __builtin_amdgcn_raw_buffer_load_b16(b, i < n ? off + 2 * i : kOut, 0, 0);
+        r.w[0] = e[0] | e[1] << 16;
+        r.w[1] = e[2] | e[3] << 16;
+    }
+}
+__device__ __forceinline__ void fetch4(__amdgpu_buffer_rsrc_t b, int off, int n, int vec, Raw4<float>& r) {
+    if (vec) {
+        r.v = buf_ld4(b, n > 0 ? off : kOut);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.v[i] = buf_raw<float>(b, i < n ? off + 4 * i : kOut);
+    }
+}
+__device__ __forceinline__ f32x4 widen(const Raw4<uint16_t>& r) {
+    return f32x4{bf16lo(r.w[0]), bf16hi(r.w[0]), bf16lo(r.w[1]), bf16hi(r.w[1])};
+}
+__device__ __forceinline__ f32x4 widen(const Raw4<float>& r) { return r.v; }
+
 __device__ __forceinline__ void from_floats(const float (&e)[8], Raw8<uint16_t>& r) {   // (values that are bf16)
 #pragma unroll
     for (int i = 0; i < 4; ++i) r.w[i] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
@@ -417,19 +447,59 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     const int64_t row0 = b * a.L + t0;
     const auto ob = rows_buf(scalar(static_cast<const char*>(ba.dout) + row0 * so + h * P * EO), scalar(live), so, P * EO);
     const auto vb = rows_buf(scalar(static_cast<const char*>(a.v) + row0 * sv + h * P * ES), scalar(live), sv, P * ES);
+    // A step's inputs are fetched while the step before computes.
+    f32x4 fs[NP / 32], fd[NP / 32], fu[2], fr[2];
+    Raw4<Tin> fv[2];
+    Raw8<Tdo> fo;
+    auto fetch = [&](int pb) {
+#pragma unroll
+        for (int i = 0; i < NP / 32; ++i) {      // S and D: two column blocks' tiles in turn
+            const int id = wave + 4 * i;
+            fs[i] = *reinterpret_cast<const f32x4*>(Sg + kept_tile<NP>(pb + 16 * (id / NB), id % NB, lane));
+            fd[i] = *reinterpret_cast<const f32x4*>(Dg + kept_tile<NP>(pb + 16 * (id / NB), id % NB, lane));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {            // U, dR and V: 64 rows of 32
+            const int id = tid + 256 * i, r = id >> 3, e0 = pb + 4 * (id & 7);
+            fu[i] = *reinterpret_cast<const f32x4*>(Ug + (int64_t)r * pad + e0);
+            fr[i] = *reinterpret_cast<const f32x4*>(Rg + (int64_t)r * pad + e0);
+            fetch4(vb, r * sv + e0 * ES, P - e0, ba.vec_p, fv[i]);
+        }
+        const int r = tid >> 2, e0 = pb + 8 * (tid & 3);
+        if (ba.vec_p) {
+            fetch8(ob, e0 < P ? r * so + e0 * EO : kOut, fo);
+        } else {
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e[i] = buf_ld<Tdo>(ob, e0 + i < P ? r * so + (e0 + i) * EO : kOut);
+            from_floats(e, fo);
+        }
+    };
+    // what follows the steps: K and Q
+    Raw8<Tin> fk[NP / 32], fq[NP / 32];
+    auto fetch_kq = [&]() {
+        const int64_t at = row0 * sk + grp * a.qk_row * ES;
+        const auto kb = rows_buf(scalar(static_cast<const char*>(a.k) + at), scalar(live), sk, a.NL * ES);
+        const auto qb = rows_buf(scalar(static_cast<const char*>(a.q) + at), scalar(live), sk, a.NL * ES);
+#pragma unroll
+        for (int i = 0; i < NP / 32; ++i) {
+            const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+            const int off = n0 < a.NL ? r * sk + n0 * ES : kOut;
+            fetch8(kb, off, fk[i]);
+            fetch8(qb, off, fq[i]);
+        }
+    };
+    fetch(0);
     for (int pb = 0; pb < pad; pb += kPb) {
-        __syncthreads();
+        lds_barrier();
 #pragma unroll
-        for (int i = 0; i < NP / 32; ++i) {      // S and D: 32 rows of NP
-            const int id = wave + 4 * i, p16 = 16 * (id / NB), tile = id % NB;   // two column blocks' tiles in turn
-            const int r = p16 + li, n = 16 * tile + 4 * lg;
-            const f32x4 s = *reinterpret_cast<const f32x4*>(Sg + kept_tile<NP>(pb + p16, tile, lane));
-            const f32x4 d = *reinterpret_cast<const f32x4*>(Dg + kept_tile<NP>(pb + p16, tile, lane));
+        for (int i = 0; i < NP / 32; ++i) {
+            const int id = wave + 4 * i, r = 16 * (id / NB) + li, n = 16 * (id % NB) + 4 * lg;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sd = __builtin_fma((double)s[e], (double)d[e], sd);
+            for (int e = 0; e < 4; ++e) sd = __builtin_fma((double)fs[i][e], (double)fd[i][e], sd);
             uint2 sp[3], dp[3];
-            split4<3>(s, sp);
-            split4<3>(d, dp);
+            split4<3>(fs[i], sp);
+            split4<3>(fd[i], dp);
 #pragma unroll
             for (int x = 0; x < 3; ++x) {
                 *reinterpret_cast<uint2*>(&sm.s.S[x][r][n]) = sp[x];
@@ -437,37 +507,24 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             }
         }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {            // U and dR: 64 rows of 32
+        for (int i = 0; i < 2; ++i) {
             const int id = tid + 256 * i, r = id >> 3, e0 = 4 * (id & 7);
-            const f32x4 u = *reinterpret_cast<const f32x4*>(Ug + (int64_t)r * pad + pb + e0);
-            const f32x4 d = *reinterpret_cast<const f32x4*>(Rg + (int64_t)r * pad + pb + e0);
+            const f32x4 v = widen(fv[i]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                rv[i] = __builtin_fmaf(d[e], buf_ld<Tin>(vb, pb + e0 + e < P ? r * sv + (pb + e0 + e) * ES : kOut), rv[i]);
+            for (int e = 0; e < 4; ++e) rv[i] = __builtin_fmaf(fr[i][e], v[e], rv[i]);
             uint2 up[3], dp[3];
-            split4<3>(u, up);
-            split4<3>(d, dp);
+            split4<3>(fu[i], up);
+            split4<3>(fr[i], dp);
 #pragma unroll
             for (int x = 0; x < 3; ++x) {
                 *reinterpret_cast<uint2*>(&sm.s.U[x][r][e0]) = up[x];
                 *reinterpret_cast<uint2*>(&sm.s.R[x][r][e0]) = dp[x];
             }
         }
-        {                                        // dout: 64 rows of 32
-            const int r = tid >> 2, e0 = 8 * (tid & 3);
-            const int off = r * so + (pb + e0) * EO;
-            Raw8<Tdo> o;
-            if (ba.vec_p) {
-                fetch8(ob, pb + e0 < P ? off : kOut, o);
-            } else {
-                float e[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) e[i] = buf_ld<Tdo>(ob, pb + e0 + i < P ? off + i * EO : kOut);
-                from_floats(e, o);
-            }
-            stage8(sm.s.O[0][r], kC * kRowP, e0, o);
-        }
-        __syncthreads();
+        stage8(sm.s.O[0][tid >> 2], kC * kRowP, 8 * (tid & 3), fo);
+        lds_barrier();
+        if (pb + kPb < pad) fetch(pb + kPb);
+        else fetch_kq();
         bf16x8 o[NO], r[3], u[3];
 #pragma unroll
         for (int x = 0; x < NO; ++x) o[x] = ld8(&sm.s.O[x][16 * tb + li][8 * lg]);
@@ -510,7 +567,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 }
         }
     }
-    __syncthreads();
+    lds_barrier();
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) sd += __shfl_xor(sd, o, 64);
     if (lane == 0) sm.sd[wave] = sd;
@@ -521,20 +578,11 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
         if ((tid & 7) == 0) sm.rv[(tid >> 3) + 32 * i] = rv[i];
     }
     // K and Q over what the steps used
-    {
-        const int64_t at = row0 * sk + grp * a.qk_row * ES;
-        const auto kb = rows_buf(scalar(static_cast<const char*>(a.k) + at), scalar(live), sk, a.NL * ES);
-        const auto qb = rows_buf(scalar(static_cast<const char*>(a.q) + at), scalar(live), sk, a.NL * ES);
 #pragma unroll
-        for (int i = 0; i < NP / 32; ++i) {
-            const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
-            const int off = n0 < a.NL ? r * sk + n0 * ES : kOut;
-            Raw8<Tin> k, q;
-            fetch8(kb, off, k);
-            fetch8(qb, off, q);
-            stage8(sm.m.K[0][r], kC * kRow, n0, k);
-            stage8(sm.m.Q[0][r], kC * kRow, n0, q);
-        }
+    for (int i = 0; i < NP / 32; ++i) {
+        const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+        stage8(sm.m.K[0][r], kC * kRow, n0, fk[i]);
+        stage8(sm.m.Q[0][r], kC * kRow, n0, fq[i]);
     }
     __syncthreads();
 
