@@ -174,6 +174,7 @@ selscan_status_t selscan_delta_bwd(const selscan_m2_shape_t* s, const void* q, c
         a.f.q = q; a.f.k = k; a.f.v = v; a.f.g = g; a.f.beta = beta; a.f.lengths = lengths; a.f.h0 = h0;
         a.f.batch = s->batch; a.f.L = s->seqlen; a.f.H = s->nheads; a.f.P = s->headdim; a.f.G = s->ngroups;
         a.f.N = (int)s->dstate; a.f.scale = scale;
+        a.vec_g = s->dstate % 8 == 0 && aligned16(dq) && aligned16(dk);
         a.vec_p = s->headdim % 8 == 0 && aligned16(dout) && aligned16(v);
         a.dout = dout; a.dlast = dlast_state; a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta; a.dh0 = dh0;
         selscan::delta_bwd_carve(a, ws.ptr);

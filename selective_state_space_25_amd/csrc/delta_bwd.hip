@@ -475,9 +475,16 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             from_floats(e, fo);
         }
     };
-    // what follows the steps: K and Q
+    // what follows the steps: K, Q, and A's rows of the wave's tokens
     Raw8<Tin> fk[NP / 32], fq[NP / 32];
+    float am[4][4];
     auto fetch_kq = [&]() {
+        const auto rb = rows_buf(scalar(rec), 1, 0, GradRec::bytes);
+#pragma unroll
+        for (int sb = 0; sb < 4; ++sb)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                am[sb][q] = buf_raw<float>(rb, sb <= tb ? GradRec::A + (block_at(tb, sb) * 256 + (4 * lg + q) * 16 + li) * 4 : kOut);
         const int64_t at = row0 * sk + grp * a.qk_row * ES;
         const auto kb = rows_buf(scalar(static_cast<const char*>(a.k) + at), scalar(live), sk, a.NL * ES);
         const auto qb = rows_buf(scalar(static_cast<const char*>(a.q) + at), scalar(live), sk, a.NL * ES);
@@ -627,7 +634,6 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 }
                 kk = mm<3>(x, y, kk);
             }
-            const float* ab = reinterpret_cast<const float*>(rec + GradRec::A) + block_at(tb, sb) * 256 + li;
             const double cs = sm.cum[s];
             double cz = 0.0;
 #pragma unroll
@@ -639,7 +645,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 xv[q] = a.scale * x1[sb][q] * g;
                 ev[q] = beta[q] * e0;
                 const double ekk = (double)e0 * kk[q];
-                const double zv = (s < t ? (double)a.scale * x1[sb][q] * ab[(4 * lg + q) * 16] : 0.0) + beta[q] * ekk;
+                const double zv = (s < t ? (double)a.scale * x1[sb][q] * am[sb][q] : 0.0) + beta[q] * ekk;
                 rb[q] += ekk;
                 row[q] += zv;
                 cz += zv;
@@ -733,16 +739,38 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             }
         }
     }
+    // rows through LDS (over K and Q), out 32 bytes or more a lane
+    lds_barrier();
+    float (&out)[16][NP + 4] = *reinterpret_cast<float (*)[16][NP + 4]>(&sm.m.K[0][0][0] + wave * (2 * 16 * (NP + 4)));
+    static_assert(4 * 16 * (NP + 4) * 4 <= (int)sizeof(sm.m.K) + (int)sizeof(sm.m.Q), "the waves' rows fit over K and Q");
+    auto put_rows = [&](const f32x4 (&v)[NB], void* to, float* part) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < NB; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const int r = 16 * tb + 4 * lg + q, n = 16 * i + li;
-            if (r < inside && n < N) {
-                put(ba.dq, ba.pq, r, n, q1[i][q]);
-                put(ba.dk, ba.pk, r, n, k3[i][q]);
+            for (int q = 0; q < 4; ++q) out[4 * lg + q][16 * i + li] = v[i][q];
+        wave_sync();
+        const int rows = min(16, inside - 16 * tb);
+        const bool wide = shared_qk ? N % 8 == 0 : ba.vec_g;
+        auto each = [&](auto* first, int64_t stride) {   // row r at first + r stride
+            if (wide) {
+                for (int id = lane; id < 2 * NP; id += 64) {
+                    const int r = id / (NP / 8), n = 8 * (id % (NP / 8));
+                    if (r < rows && n < N) io::st8(first + r * stride + n, &out[r][n]);
+                }
+            } else {
+                for (int id = lane; id < 16 * NP; id += 64) {
+                    const int r = id / NP, n = id % NP;
+                    if (r < rows && n < N) io::st(first + r * stride + n, out[r][n]);
+                }
             }
-        }
+        };
+        const int64_t t = row0 + 16 * tb;
+        if (shared_qk) each(part + (t * a.H + h) * N, a.H * N);
+        else each(reinterpret_cast<Tin*>(to) + (t * a.G + grp) * N, a.G * N);
+        wave_sync();
+    };
+    put_rows(q1, ba.dq, ba.pq);
+    put_rows(k3, ba.dk, ba.pk);
 }
 
 // dq and dk of a group: the sum over its heads, in their order.

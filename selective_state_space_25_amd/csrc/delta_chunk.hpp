@@ -63,6 +63,13 @@ __device__ __forceinline__ void lds_barrier() {
     asm volatile("" ::: "memory");
 }
 
+// What the wave's lanes wrote to LDS is there for its other lanes: LDS works
+// a wave's instructions off in order, so only the compiler has to keep them.
+__device__ __forceinline__ void wave_sync() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // A value that is the same in every lane, in a scalar register.  Descriptors
 // have to be made of such: one in vector registers, equal in every lane or
 // not, is accessed in a loop over its values (1.5 us a chunk in the scan).

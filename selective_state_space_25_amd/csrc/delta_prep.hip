@@ -45,13 +45,6 @@ struct PrepUnit {
     float beta[kC];
 };
 
-// What the wave's lanes wrote to LDS is there for its other lanes: LDS works
-// a wave's instructions off in order, so only the compiler has to keep them.
-__device__ __forceinline__ void wave_sync() {
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // c + X Y: X a block in LDS, Y a block held as a C tile (rows 4 g + q); step
 // q contracts rows 4 g + q, so X is read at columns 4 g + q.
 __device__ __forceinline__ f32x4 mul_block(const float (&X)[16][kRowB], f32x4 y, f32x4 c, int li, int lg) {

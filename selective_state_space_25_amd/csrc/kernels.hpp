@@ -245,6 +245,7 @@ struct DeltaBwdArgs {
     float* dR;                // [chunks, 64, pad]
     float *pq, *pk;           // [batch, L, H, N] per-head dq and dk when heads share q and k, else NULL
     int pad;                  // P rounded up to 32
+    int vec_g;                // rows of dq and dk on 16-byte boundaries, N % 8 == 0
     int vec_p;                // rows of v and dout on 16-byte boundaries, P % 8 == 0
 };
 size_t delta_bwd_bytes(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N);
