@@ -17,13 +17,16 @@
 //   dg_t = sum_{i >= t} (rowsum Z - colsum Z + a)_i + sum_{i < t} b_i + e^last <S, D>
 //
 // Row and column sums are taken of the same Z and, like the dots, in fp64:
-// where a key is written over, dg is a small difference of these sums.  Five kernels: the records (delta_prep.hip), the
-// scan that keeps every S and U (delta_scan.hip), the scan back over the
-// chunks that makes D, dR and dV (16 value columns a workgroup, as forward),
-// the gradients that are local to a chunk (all chunks at once), and, where
-// heads share q and k, their sum over the heads in a fixed order.  All
-// products are fp32-grade except those that go into a bf16 dq or dk alone.
+// where a key is written over, dg is a small difference of these sums.
+//
+// Five kernels: the records (delta_prep.hip), the scan that keeps every S
+// and U (delta_scan.hip), the scan back over the chunks that makes D, dR and
+// dV (16 or 32 value columns a workgroup), the gradients that are local to a
+// chunk (all chunks at once), and, where heads share q and k, their sum over
+// the heads in a fixed order.  All products are fp32-grade except those that
+// go into a bf16 dq or dk alone.
 #include "delta_chunk.hpp"
+#include "host.hpp"
 
 namespace selscan {
 
@@ -795,25 +798,39 @@ hipError_t lds(K* kern, int bytes) {
     return hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
+template <typename Tin, typename Tdo, int NP, int CT>
+hipError_t launch_back(const DeltaBwdArgs& a, hipStream_t stream) {
+    const DeltaArgs& f = a.f;
+    const auto kern = &delta_back_kernel<Tin, Tdo, NP, CT>;
+    constexpr int bytes = (int)sizeof(BackSmem<Tin, Tdo, NP, CT>);
+    static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
+    const hipError_t e = lds(kern, bytes);
+    if (e != hipSuccess) return e;
+    const int npb = a.pad / (16 * CT);
+    const int64_t units = (f.batch * f.H + 7) / 8 * 8;
+    KTime kt("delta_back", stream);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(256), bytes, stream, a, delta_chunks(f.L), npb);
+    return hipGetLastError();
+}
+
 template <typename Tin, typename Tdo, int NP>
 hipError_t launch(const DeltaBwdArgs& a, hipStream_t stream) {
-    constexpr int CT = 1;
     const DeltaArgs& f = a.f;
     const int64_t nch = delta_chunks(f.L);
     hipError_t e = launch_delta_prep(f, sizeof(Tin) == 2, 3, true, a.recs, stream);
     if (e != hipSuccess) return e;
     e = launch_delta_keep(f, sizeof(Tin) == 2, a.recs, a.S, a.U, a.pad, stream);
     if (e != hipSuccess) return e;
-    {
-        const auto kern = &delta_back_kernel<Tin, Tdo, NP, CT>;
-        constexpr int bytes = (int)sizeof(BackSmem<Tin, Tdo, NP, CT>);
-        static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
-        if ((e = lds(kern, bytes)) != hipSuccess) return e;
-        const int npb = a.pad / (16 * CT);
-        const int64_t units = (f.batch * f.H + 7) / 8 * 8;
-        KTime kt("delta_back", stream);
-        hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(256), bytes, stream, a, nch, npb);
+    // Two column blocks to a workgroup where half as many still give each CU
+    // one, as in the scan (batch 4, 16 heads of 128 x 128, L 2048: 171 us
+    // against 194).  float32 inputs: one block takes all registers.
+    bool two = false;
+    if constexpr (sizeof(Tin) == 2) {
+        two = f.batch * f.H * (a.pad / 32) >= host::device_cus();
+        if (two) e = launch_back<Tin, Tdo, NP, 2>(a, stream);
     }
+    if (!two) e = launch_back<Tin, Tdo, NP, 1>(a, stream);
+    if (e != hipSuccess) return e;
     {
         const auto kern = &delta_grad_kernel<Tin, Tdo, NP>;
         constexpr int bytes = (int)sizeof(GradSmem<Tin, Tdo, NP, kPlanes<Tin> == 1 ? 2 : 3>);

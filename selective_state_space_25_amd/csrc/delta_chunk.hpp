@@ -151,21 +151,6 @@ __device__ __forceinline__ void stage8(uint16_t* row, int ps, int n0, const Raw8
 #pragma unroll
     for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x8*>(row + i * ps + n0) = p[i];
 }
-// The same with the row's columns through kperm.
-__device__ __forceinline__ void stage8_perm(uint16_t* row, int ps, int n0, const Raw8<uint16_t>& r) {
-    *reinterpret_cast<uint2*>(row + kperm(n0)) = make_uint2(r.w[0], r.w[1]);
-    *reinterpret_cast<uint2*>(row + kperm(n0 + 4)) = make_uint2(r.w[2], r.w[3]);
-}
-__device__ __forceinline__ void stage8_perm(uint16_t* row, int ps, int n0, const Raw8<float>& r) {
-    uint2 pa[3], pb[3];
-    split4<3>(r.lo, pa);
-    split4<3>(r.hi, pb);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        *reinterpret_cast<uint2*>(row + i * ps + kperm(n0)) = pa[i];
-        *reinterpret_cast<uint2*>(row + i * ps + kperm(n0 + 4)) = pb[i];
-    }
-}
 __device__ __forceinline__ void to_operand(const Raw8<uint16_t>& r, bf16x8 (&p)[1]) {
     p[0] = __builtin_bit_cast(bf16x8, r.w);
 }
@@ -180,36 +165,6 @@ __device__ __forceinline__ void lower_tile(int k, int& tb, int& sb) {
 __device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[1]) { return v[0]; }
 __device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[2]) { return v[0] + v[1]; }
 __device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); }
-
-// A lower triangular chunk matrix (or, TR, its transpose) as A operands in
-// LDS: fragment (row block t, k-step ks <= t / 2; transposed: ks >= t / 2)
-// holds two 16-wide blocks in tile order, a lane's 16 bytes in its own slot.
-template <int NPL, bool TR>
-struct Frags {
-    uint16_t p[NPL][6][64][8];
-    static __device__ __forceinline__ int at(int t, int ks) {
-        return TR ? (t < 2 ? 2 * t + ks : t + 2) : (t < 2 ? t : 2 * t - 2 + ks);
-    }
-    // columns 8 c .. 8 c + 7 of row r of block i of a record's plane
-    __device__ __forceinline__ void put(int plane, int i, int r, int c, u32x4 v) {
-        int tb, sb;
-        lower_tile(i, tb, sb);
-        const int f = TR ? at(sb, tb >> 1) : at(tb, sb >> 1), e = 4 * ((TR ? tb : sb) & 1);
-        *reinterpret_cast<uint2*>(&p[plane][f][16 * (2 * c) + r][e]) = make_uint2(v[0], v[1]);
-        *reinterpret_cast<uint2*>(&p[plane][f][16 * (2 * c + 1) + r][e]) = make_uint2(v[2], v[3]);
-    }
-    // the blocks beyond the diagonal that share a fragment with one on it
-    __device__ __forceinline__ void clear(int tid, int threads) {
-        for (int i = tid; i < 128; i += threads)
-#pragma unroll
-            for (int x = 0; x < NPL; ++x)
-                *reinterpret_cast<uint2*>(&p[x][TR ? (i < 64 ? 2 : 5) : (i < 64 ? 0 : 3)][i & 63][TR ? 0 : 4]) = make_uint2(0, 0);
-    }
-    __device__ __forceinline__ void get(int t, int ks, int lane, bf16x8 (&a)[NPL]) const {
-#pragma unroll
-        for (int x = 0; x < NPL; ++x) a[x] = ld8(p[x][at(t, ks)][lane]);
-    }
-};
 
 // B operands that waves hand to each other through LDS: NPL planes of KS
 // k-steps, k in natural order, each lane's 16 bytes in its own slot.
@@ -236,12 +191,6 @@ struct Tiles {
     float p[4][64][4];
     __device__ __forceinline__ void put(int t, f32x4 v, int lane) { *reinterpret_cast<f32x4*>(p[t][lane]) = v; }
     __device__ __forceinline__ f32x4 get(int t, int lane) const { return *reinterpret_cast<const f32x4*>(p[t][lane]); }
-    // k-step ks of them as a B operand, split here
-    template <int NPL>
-    __device__ __forceinline__ void operand(int ks, int lane, bf16x8 (&w)[NPL]) const {
-        const int t = 2 * ks + (lane >> 5), at = 32 * ((lane >> 4) & 1) + (lane & 15);
-        split8<NPL>(get(t, at), get(t, at + 16), w);
-    }
 };
 
 // Byte offset in a plane of the lane's part of row block tb of T, an A

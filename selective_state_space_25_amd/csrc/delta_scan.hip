@@ -10,7 +10,7 @@
 //
 // which is the token recurrence regrouped: U's rows are the u_t of
 // S_t = e^g_t S_{t-1} + k_t u_t^T.  Value columns are independent: a
-// workgroup owns 16 columns of one head and walks its chunks in order.  The
+// workgroup owns 16 or 32 columns of one head and walks its chunks in order.  The
 // walk is a chain of three products a chunk, so what bounds it is their
 // latency, and eight waves share each chunk.  Four state waves split the
 // chain: wave w has the tokens 16 w .. 16 w + 15 of R and U and a quarter of
@@ -24,6 +24,7 @@
 // goes into a bf16 y alone (Q S, A U) keeps plane pairs a + b < 2, an error
 // near 2^-16 under the 2^-9 of y's own rounding.
 #include "delta_chunk.hpp"
+#include "host.hpp"
 
 namespace selscan {
 
@@ -34,34 +35,34 @@ using namespace dchunk;
 constexpr int kThreads = 512;
 
 // OL: plane pairs a + b < OL in the products of y; 0 = no y.
-template <typename Tin, int NP, int OL>
+template <typename Tin, int NP, int CT, int OL>
 struct ScanSmem {
     static constexpr int kRow = NP + 8;
     float gam[kC], tail[kC], beta[kC];
-    Tiles V;
+    Tiles V[CT];
     uint16_t K[2][kPlanes<Tin>][kC][kRow];   // by chunk parity
-    Operands<NP / 32, 3> S;
-    Operands<2, 3> R, W;                     // R; e^(last - cum) U
-    Operands<2, OL ? OL : 1> U;
+    Operands<NP / 32, 3> S[CT];
+    Operands<2, 3> R[CT], W[CT];             // R; e^(last - cum) U
+    Operands<2, OL ? OL : 1> U[CT];
 };
 
 // KEEP: instead of y, the state entering each chunk (kept_tile) and U
 // [chunk, 64, pad], which the gradients read (pad: P rounded up to 32, the
 // columns past P zero).
-template <typename Tin, typename Tout, int NP, bool KEEP>
-__global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout) == 2) ? 4 : 2) void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb,
-                                                              float* keep_s, float* keep_u, int pad) {
+template <typename Tin, typename Tout, int NP, int CT, bool KEEP>
+__global__ __launch_bounds__(kThreads, CT == 1 && sizeof(Tin) == 2 && (KEEP || sizeof(Tout) == 2) ? 4 : 2)
+void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, float* keep_s, float* keep_u, int pad) {
     constexpr int OL = KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3;
     constexpr int OA = OL ? OL : 1;
     constexpr int NK = kPlanes<Tin>;
     constexpr int ES = (int)sizeof(Tin), EO = (int)sizeof(Tout);
-    constexpr int kRow = ScanSmem<Tin, NP, OL>::kRow;
+    constexpr int kRow = ScanSmem<Tin, NP, CT, OL>::kRow;
     constexpr int KS = NP / 32;              // k-steps over the key dimension
     constexpr int NT = NP / 64;              // state tiles per state wave
     constexpr int NPC = NP / 32;             // 8-element pieces of K per helper thread
     using Rc = Rec<KEEP ? 3 : OA, KEEP>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
-    auto& sm = *reinterpret_cast<ScanSmem<Tin, NP, OL>*>(smem_raw);
+    auto& sm = *reinterpret_cast<ScanSmem<Tin, NP, CT, OL>*>(smem_raw);
     const int tid = threadIdx.x & 255, lane = tid & 63, li = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool helper = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
@@ -75,7 +76,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
     const Chunks seq(len), all(a.L);         // of the sequence; of the tensors
     const int mine = seq.n;
     const int N = a.N, P = (int)a.P;
-    const int p = (jx % npb) * 16 + li;      // the lane's column
+    const int p0 = (jx % npb) * 16 * CT + li;   // the lane's first column; the others 16 apart
     // strides of a token in bytes
     const int sk = scalar((int)(a.G * a.qk_row * ES)), sv = scalar((int)(a.H * P * ES)), sy = scalar((int)(a.H * P * EO));
     const int64_t krow = b * a.L * sk + grp * a.qk_row * ES;
@@ -99,17 +100,21 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
     for (int ks = 0; ks < 2; ++ks) toff[ks] = row_of(w, ks, lane);
 
     if (!helper) {
-        f32x4 S[NT];   // tile i: rows n = 16 (NT w + i) + 4 lg + q, column p
+        f32x4 S[NT][CT];   // tile i: rows n = 16 (NT w + i) + 4 lg + q, column p0 + 16 ct
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = 16 * (NT * w + i) + 4 * lg + q;
-                S[i][q] = a.h0 && p < P && n < N ? a.h0[(bh * P + p) * N + n] : 0.0f;
-            }
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int n = 16 * (NT * w + i) + 4 * lg + q, p = p0 + 16 * ct;
+                    S[i][ct][q] = a.h0 && p < P && n < N ? a.h0[(bh * P + p) * N + n] : 0.0f;
+                }
         auto put_state = [&]() {
 #pragma unroll
-            for (int i = 0; i < NT; ++i) sm.S.put_tile(NT * w + i, S[i], lane);
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) sm.S[ct].put_tile(NT * w + i, S[i][ct], lane);
         };
         bf16x8 ft[2][3];
         auto fetch_t = [&](int c) {
@@ -125,45 +130,56 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
         for (int c = 0; c < mine; ++c) {
             const uint16_t* K = &sm.K[c & 1][0][0][0];
             // R for the wave's tokens
-            f32x4 u;
+            f32x4 u[CT];
             {
-                bf16x8 k[KS][NK], s[KS][3];
-                f32x4 acc[KS];
+                bf16x8 k[KS][NK];
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    sm.S.get(ks, lane, s[ks]);
+                for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
                     for (int x = 0; x < NK; ++x) k[ks][x] = ld8(K + (x * kC + 16 * w + li) * kRow + 32 * ks + 8 * lg);
-                    acc[ks] = z4;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    bf16x8 s[KS][3];
+                    f32x4 acc[KS];
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        sm.S[ct].get(ks, lane, s[ks]);
+                        acc[ks] = z4;
+                    }
+                    mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return s[m]; }, acc);
+                    u[ct] = sum_of(acc);
                 }
-                mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return s[m]; }, acc);
-                u = sum_of(acc);
             }
             auto gate = [&](const float* g) { return *reinterpret_cast<const f32x4*>(g + 16 * w + 4 * lg); };
-            const f32x4 gam = gate(sm.gam), tail = gate(sm.tail), beta = gate(sm.beta), v = sm.V.get(w, lane);
+            const f32x4 gam = gate(sm.gam), tail = gate(sm.tail), beta = gate(sm.beta);
             const float gl = sm.gam[kC - 1];
-            f32x4 r;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) r[q] = beta[q] * __builtin_fmaf(-gam[q], u[q], v[q]);
-            sm.R.put_tile(w, r, lane);
-            if constexpr (KEEP) {
-                float* ks = keep_s + (bh * nch + c) * pad * NP + kept_tile<NP>(p - li, NT * w, lane);
+            for (int ct = 0; ct < CT; ++ct) {
+                const f32x4 v = sm.V[ct].get(w, lane);
+                f32x4 r;
 #pragma unroll
-                for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(ks + 256 * i) = S[i];
+                for (int q = 0; q < 4; ++q) r[q] = beta[q] * __builtin_fmaf(-gam[q], u[ct][q], v[q]);
+                sm.R[ct].put_tile(w, r, lane);
+                if constexpr (KEEP) {
+                    float* ks = keep_s + (bh * nch + c) * pad * NP + kept_tile<NP>(p0 - li + 16 * ct, NT * w, lane);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(ks + 256 * i) = S[i][ct];
+                }
             }
             lds_barrier();
             // U for the wave's tokens (the first two waves' T ends in the first k-step)
-            {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
                 bf16x8 x[2][3];
-                sm.R.get(0, lane, x[0]);
+                sm.R[ct].get(0, lane, x[0]);
                 if (w < 2) {
-                    u = mm<3>(ft[0], x[0], z4);
+                    u[ct] = mm<3>(ft[0], x[0], z4);
                 } else {
-                    sm.R.get(1, lane, x[1]);
-                    u = mm_pair(ft, x);
+                    sm.R[ct].get(1, lane, x[1]);
+                    u[ct] = mm_pair(ft, x);
                 }
-                sm.W.put_tile(w, u * tail, lane);
-                if constexpr (!KEEP) sm.U.put_tile(w, u, lane);
+                sm.W[ct].put_tile(w, u[ct] * tail, lane);
+                if constexpr (!KEEP) sm.U[ct].put_tile(w, u[ct], lane);
             }
             fetch_t(c + 1);
             bf16x8 k[NT * 2][NK];
@@ -177,35 +193,41 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
             // before the barrier that it does not need, where registers allow
             if constexpr (OL != 3) load_kt();
             if constexpr (KEEP) {
-                float* ku = keep_u + (bh * nch + c) * kC * pad + p;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) ku[(16 * w + 4 * lg + q) * pad] = u[q];
+                for (int ct = 0; ct < CT; ++ct) {
+                    float* ku = keep_u + (bh * nch + c) * kC * pad + p0 + 16 * ct;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) ku[(16 * w + 4 * lg + q) * pad] = u[ct][q];
+                }
             }
             lds_barrier();
             // the wave's rows of the next state
-            {
-                if constexpr (OL == 3) load_kt();
+            if constexpr (OL == 3) load_kt();
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
                 bf16x8 x[2][3];
-                sm.W.get(0, lane, x[0]);
-                sm.W.get(1, lane, x[1]);
+                sm.W[ct].get(0, lane, x[0]);
+                sm.W[ct].get(1, lane, x[1]);
                 f32x4 acc[NT * 2];
 #pragma unroll
-                for (int i = 0; i < NT * 2; ++i) acc[i] = i & 1 ? z4 : S[i / 2] * gl;
+                for (int i = 0; i < NT * 2; ++i) acc[i] = i & 1 ? z4 : S[i / 2][ct] * gl;
                 mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return x[m & 1]; }, acc);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) S[i] = acc[2 * i] + acc[2 * i + 1];
+                for (int i = 0; i < NT; ++i) S[i][ct] = acc[2 * i] + acc[2 * i + 1];
             }
             put_state();
             lds_barrier();
         }
-        if (!KEEP && a.last && p < P) {
+        if (!KEEP && a.last) {
 #pragma unroll
-            for (int i = 0; i < NT; ++i)
+            for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = 16 * (NT * w + i) + 4 * lg + q;
-                    if (n < N) a.last[(bh * P + p) * N + n] = S[i][q];
-                }
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int n = 16 * (NT * w + i) + 4 * lg + q, p = p0 + 16 * ct;
+                        if (p < P && n < N) a.last[(bh * P + p) * N + n] = S[i][ct][q];
+                    }
         }
         return;
     }
@@ -222,7 +244,13 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
         const int n = 32 * ks + 8 * lg;
         qoff[ks] = n < a.NL ? (16 * w + li) * sk + n * ES : kOut;
     }
-    const int yoff = p < P ? (16 * w + 4 * lg) * sy + p * EO : kOut;
+    int yoff[CT], voff[CT];
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+        const int p = p0 + 16 * ct;
+        yoff[ct] = p < P ? (16 * w + 4 * lg) * sy + p * EO : kOut;
+        voff[ct] = p < P ? (16 * w + 4 * lg) * sv + p * ES : kOut;
+    }
     Raw8<Tin> fk[NPC], fq[KS];
     bf16x8 fa[2][OA];
     f32x4 fgam;
@@ -244,17 +272,19 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
 #pragma unroll
             for (int x = 0; x < OA; ++x) fa[ks][x] = buf_op(rb, toff[ks] + Rc::A + x * kPlane);
     };
-    const int voff = p < P ? (16 * w + 4 * lg) * sv + p * ES : kOut;
     f32x4 fgate;
-    Tin fv[4];
+    Tin fv[CT][4];
     auto fetch_v = [&](int c) {
         const auto vb = chunk_rows(Vg, sv, c, P * ES);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) fv[q] = buf_raw<Tin>(vb, voff + q * sv);
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) fv[ct][q] = buf_raw<Tin>(vb, voff[ct] + q * sv);
         fgate = buf_ld4(record(c), tid < 48 ? Rc::gam + 16 * tid : kOut);
     };
     auto stage_v = [&]() {
-        sm.V.put(w, widen(fv), lane);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) sm.V[ct].put(w, widen(fv[ct]), lane);
         if (tid < 48) *reinterpret_cast<f32x4*>(&sm.gam[4 * tid]) = fgate;   // gam, tail, beta in a row
     };
     auto stage_k = [&](int c) {
@@ -265,21 +295,26 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
         }
     };
     // Y of chunk c from y = e^cum Q S, its A in fa and its U in LDS
-    auto finish_y = [&](int c, f32x4 y) {
-        bf16x8 x[2][OA];
-        sm.U.get(0, lane, x[0]);
-        if (w < 2) {
-            y = mm<OA>(fa[0], x[0], y);
-        } else {
-            sm.U.get(1, lane, x[1]);
-            f32x4 acc[2] = {y, z4};
-            mm_turns<OA, OA, OA>([&](int m) { return fa[m]; }, [&](int m) { return x[m]; }, acc);
-            y = sum_of(acc);
+    auto finish_y = [&](int c, f32x4 (&y)[CT]) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            bf16x8 x[2][OA];
+            sm.U[ct].get(0, lane, x[0]);
+            if (w < 2) {
+                y[ct] = mm<OA>(fa[0], x[0], y[ct]);
+            } else {
+                sm.U[ct].get(1, lane, x[1]);
+                f32x4 acc[2] = {y[ct], z4};
+                mm_turns<OA, OA, OA>([&](int m) { return fa[m]; }, [&](int m) { return x[m]; }, acc);
+                y[ct] = sum_of(acc);
+            }
         }
         fetch_a(c + 1);
         const auto yb = rows_buf(Yg + (int64_t)c * kC * sy, all.rows(c), sy, P * EO);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) buf_st(yb, yoff + q * sy, a.scale * y[q], Tout(0));
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) buf_st(yb, yoff[ct] + q * sy, a.scale * y[ct][q], Tout(0));
     };
     fetch_k(0);
     fetch_v(0);
@@ -291,7 +326,7 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
     stage_v();
     fetch_k(1);
     fetch_v(1);
-    f32x4 y = z4;
+    f32x4 y[CT];
     lds_barrier();
     for (int c = 0; c < mine; ++c) {
         if constexpr (!KEEP) {
@@ -300,20 +335,26 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
         lds_barrier();
         if constexpr (!KEEP) {
             constexpr int M = 2;   // k-steps at a time, as registers allow
-            f32x4 acc[M];
+            f32x4 acc[CT][M];
 #pragma unroll
-            for (int i = 0; i < M; ++i) acc[i] = z4;
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < M; ++i) acc[ct][i] = z4;
 #pragma unroll
             for (int k0 = 0; k0 < KS; k0 += M) {
-                bf16x8 x[M][NK], s[M][3];
+                bf16x8 x[M][NK];
 #pragma unroll
-                for (int i = 0; i < M; ++i) {
-                    sm.S.get(k0 + i, lane, s[i]);
-                    to_operand(fq[k0 + i], x[i]);
+                for (int i = 0; i < M; ++i) to_operand(fq[k0 + i], x[i]);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    bf16x8 s[M][3];
+#pragma unroll
+                    for (int i = 0; i < M; ++i) sm.S[ct].get(k0 + i, lane, s[i]);
+                    mm_turns<OA, NK, 3>([&](int m) { return x[m]; }, [&](int m) { return s[m]; }, acc[ct]);
                 }
-                mm_turns<OA, NK, 3>([&](int m) { return x[m]; }, [&](int m) { return s[m]; }, acc);
             }
-            y = sum_of(acc) * fgam;
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) y[ct] = sum_of(acc[ct]) * fgam;
             fetch_q(c + 1);
         }
         lds_barrier();
@@ -325,25 +366,44 @@ __global__ __launch_bounds__(kThreads, sizeof(Tin) == 2 && (KEEP || sizeof(Tout)
     }
     if constexpr (!KEEP) {
         if (mine > 0) finish_y(mine - 1, y);
-        if (p < P)
-            for (int64_t t = (int64_t)mine * kC + 4 * w + lg; t < a.L; t += 16)
-                io::st(reinterpret_cast<Tout*>(Yg + t * sy) + p, 0.0f);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            if (p0 + 16 * ct < P)
+                for (int64_t t = (int64_t)mine * kC + 4 * w + lg; t < a.L; t += 16)
+                    io::st(reinterpret_cast<Tout*>(Yg + t * sy) + p0 + 16 * ct, 0.0f);
     }
 }
 
-template <typename Tin, typename Tout, int NP, bool KEEP>
-hipError_t launch(const DeltaArgs& a, const char* recs, float* keep_s, float* keep_u, int pad, hipStream_t stream) {
-    constexpr int bytes = (int)sizeof(ScanSmem<Tin, NP, KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3>);
+template <typename Tin, typename Tout, int NP, int CT, bool KEEP>
+hipError_t launch_ct(const DeltaArgs& a, const char* recs, float* keep_s, float* keep_u, int pad, hipStream_t stream) {
+    constexpr int bytes = (int)sizeof(ScanSmem<Tin, NP, CT, KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3>);
     static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
-    const int npb = (int)(((KEEP ? pad : a.P) + 15) / 16);
+    const int npb = (int)(((KEEP ? pad : a.P) + 16 * CT - 1) / (16 * CT));
     const int64_t units = (a.batch * a.H + 7) / 8 * 8;
-    const auto kern = &delta_scan_kernel<Tin, Tout, NP, KEEP>;
+    const auto kern = &delta_scan_kernel<Tin, Tout, NP, CT, KEEP>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     KTime kt(KEEP ? "delta_keep" : "delta_scan", stream);
     hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(kThreads), bytes, stream, a, recs, delta_chunks(a.L), npb,
                        keep_s, keep_u, pad);
     return hipGetLastError();
+}
+
+template <typename Tin, typename Tout, int NP, bool KEEP>
+hipError_t launch(const DeltaArgs& a, const char* recs, float* keep_s, float* keep_u, int pad, hipStream_t stream) {
+    // Two column blocks to a workgroup share K's staging, its operands and
+    // the barriers, but a chunk takes longer: worth it where half as many
+    // workgroups still give each CU one (batch 8, 32 heads of 64 x 128, L
+    // 4096, f32 y: 423 us against 531; the scan of the gradients at batch 4,
+    // 16 heads of 128 x 128, L 2048: 94 against 107), not where CUs would
+    // idle (batch 1, 16 heads of 128 x 128, L 16384: 579 us against 397).
+    // float32 inputs: two blocks' LDS would leave room for one workgroup.
+    if constexpr (sizeof(Tin) == 2) {
+        const int64_t blocks = ((KEEP ? pad : a.P) + 31) / 32;
+        if (a.P > 16 && a.batch * a.H * blocks >= host::device_cus())
+            return launch_ct<Tin, Tout, NP, 2, KEEP>(a, recs, keep_s, keep_u, pad, stream);
+    }
+    return launch_ct<Tin, Tout, NP, 1, KEEP>(a, recs, keep_s, keep_u, pad, stream);
 }
 
 template <typename Tin, typename Tout>

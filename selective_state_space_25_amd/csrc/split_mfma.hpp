@@ -111,19 +111,6 @@ __device__ __forceinline__ void split8(f32x4 lo, f32x4 hi, bf16x8 (&p)[NP]) {
     as_operand(w, p);
 }
 
-// Two C tiles (rows r0 .. r0 + 15 and r0 + 16 .. r0 + 31 of one column
-// block) split with split8 are the B operand of a product over those 32 rows
-// without leaving the lanes, k in the order in which the lanes hold them:
-// lane group g has rows r0 + 4 g + q, then r0 + 16 + 4 g + q ("tile order").
-// The A operand has to be read in that order.  kperm: position of column n
-// in a row whose 4-element pieces are permuted inside each group of 32 so
-// that one 16-byte read gives a lane group the tile order (pieces 0 .. 7 at
-// positions 0, 2, 4, 6, 1, 3, 5, 7).
-__device__ __forceinline__ int kperm(int n) {
-    const int pc = (n & 31) >> 2;
-    return (n & ~31) + 4 * (pc < 4 ? 2 * pc : 2 * pc - 7) + (n & 3);
-}
-
 __device__ __forceinline__ bf16x8 ld8(const uint16_t* p) {
     return __builtin_bit_cast(bf16x8, *reinterpret_cast<const uint4*>(p));
 }
@@ -146,13 +133,6 @@ __device__ __forceinline__ bf16x8 ld_down(const uint16_t* m, int rs, int r0, int
     const int g = lane >> 4, a = lane & 15;
     const uint16_t* p = m + (r0 + 8 * g + (a >> 2)) * rs + c0 + 4 * (a & 3);
     return cat(ld_tr(p), ld_tr(p + 4 * rs));
-}
-
-// The same in tile order, of an m whose columns are stored through kperm.
-__device__ __forceinline__ bf16x8 ld_down_tile(const uint16_t* m, int rs, int r0, int c0, int lane) {
-    const int g = lane >> 4, a = lane & 15;
-    const uint16_t* p = m + (r0 + 4 * g + (a >> 2)) * rs + kperm(c0 + 4 * (a & 3));
-    return cat(ld_tr(p), ld_tr(p + 16 * rs));
 }
 
 // Four consecutive values into NP planes of 4 bf16 each.
