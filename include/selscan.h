@@ -374,9 +374,16 @@ selscan_status_t selscan_conv1d(const selscan_conv_shape_t* shape, const void* x
  *   y          [B, L, H, P]  out_dtype  (written)
  *   last_state [B, H, P, N]  fp32       (written; NULL = skip); may not alias h0
  *
- * 1 <= N <= 128 (UNSUPPORTED above), any P and L.  Workspace as for the other
- * entry points, sized by selscan_delta_workspace_bytes.  State, decays and
- * sums are fp32.
+ * 1 <= N <= 128, H P <= 2^22, G <= 2^15 (UNSUPPORTED above), any L.  State,
+ * decays and sums are fp32.  Past 16 tokens the sequence is worked on in
+ * chunks of 64, as matrix products: a NaN or infinity in a token reaches every
+ * y of its chunk and head, and what follows.
+ *
+ * Workspace as for the other entry points, sized by
+ * selscan_delta_workspace_bytes: per head and 64 tokens 27 KB (32 KB for fp32
+ * y), and where N is no multiple of 8 padded copies of q and k (which are
+ * allocated on `stream` by the call itself where only their addresses are off
+ * a 16-byte boundary).
  */
 size_t selscan_delta_workspace_bytes(const selscan_m2_shape_t* shape);
 
@@ -388,9 +395,9 @@ selscan_status_t selscan_delta_fwd(const selscan_m2_shape_t* shape,
 
 /* Bytes of workspace selscan_delta_bwd needs for `shape` (0 on a bad shape).
  * It grows with batch x heads x L: per head and 64 tokens two states, two
- * P-wide rows per token and 21 KiB (213 KiB at N = P = 128; 436 MB for batch
- * 4, L 2048, 16 heads), and 2 N fp32 per token and head where heads share q
- * and k. */
+ * P-wide rows per token and 57.6 KB (254 KB in all at N = P = 128; 521 MB for
+ * batch 4, L 2048, 16 heads), and 2 N fp32 per token and head where heads
+ * share q and k. */
 size_t selscan_delta_bwd_workspace_bytes(const selscan_m2_shape_t* shape);
 
 /*

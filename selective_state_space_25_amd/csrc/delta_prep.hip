@@ -277,7 +277,9 @@ hipError_t by_n(const DeltaArgs& a, char* recs, hipStream_t stream) {
 template <typename Tin>
 hipError_t by_use(const DeltaArgs& a, int planes, bool grad, char* recs, hipStream_t stream) {
     if (grad) return by_n<Tin, 3, true>(a, recs, stream);
-    return planes == 2 ? by_n<Tin, 2, false>(a, recs, stream) : by_n<Tin, 3, false>(a, recs, stream);
+    if constexpr (sizeof(Tin) == 2)
+        if (planes == 2) return by_n<Tin, 2, false>(a, recs, stream);
+    return by_n<Tin, 3, false>(a, recs, stream);
 }
 
 // Rows of N elements, one after the other, to rows of `to`, zeros past N.

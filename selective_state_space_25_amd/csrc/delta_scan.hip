@@ -20,9 +20,9 @@
 // chain: Y (Q S while the state waves make U, A U a chunk later), staging K,
 // needed both ways up, in LDS, and most of the loads, a chunk ahead.
 //
-// Products are fp32-grade (split_mfma.hpp) where they reach the state.  What
-// goes into a bf16 y alone (Q S, A U) keeps plane pairs a + b < 2, an error
-// near 2^-16 under the 2^-9 of y's own rounding.
+// Products are fp32-grade (split_mfma.hpp).  Where inputs and y are bf16, A
+// and U take two planes in A U, an error near 2^-17 of that term under the
+// 2^-9 of y's own rounding.
 #include "delta_chunk.hpp"
 #include "host.hpp"
 
@@ -34,7 +34,7 @@ using namespace dchunk;
 
 constexpr int kThreads = 512;
 
-// OL: plane pairs a + b < OL in the products of y; 0 = no y.
+// OL: planes of A and U in y; 0 = no y.
 template <typename Tin, int NP, int CT, int OL>
 struct ScanSmem {
     static constexpr int kRow = NP + 8;
@@ -52,7 +52,7 @@ struct ScanSmem {
 template <typename Tin, typename Tout, int NP, int CT, bool KEEP>
 __global__ __launch_bounds__(kThreads, CT == 1 && sizeof(Tin) == 2 && (KEEP || sizeof(Tout) == 2) ? 4 : 2)
 void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, float* keep_s, float* keep_u, int pad) {
-    constexpr int OL = KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3;
+    constexpr int OL = KEEP ? 0 : delta_a_planes(sizeof(Tin) == 2, sizeof(Tout) == 2);
     constexpr int OA = OL ? OL : 1;
     constexpr int NK = kPlanes<Tin>;
     constexpr int ES = (int)sizeof(Tin), EO = (int)sizeof(Tout);
@@ -301,11 +301,11 @@ void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, floa
             bf16x8 x[2][OA];
             sm.U[ct].get(0, lane, x[0]);
             if (w < 2) {
-                y[ct] = mm<OA>(fa[0], x[0], y[ct]);
+                y[ct] = mm<3>(fa[0], x[0], y[ct]);
             } else {
                 sm.U[ct].get(1, lane, x[1]);
                 f32x4 acc[2] = {y[ct], z4};
-                mm_turns<OA, OA, OA>([&](int m) { return fa[m]; }, [&](int m) { return x[m]; }, acc);
+                mm_turns<3, OA, OA>([&](int m) { return fa[m]; }, [&](int m) { return x[m]; }, acc);
                 y[ct] = sum_of(acc);
             }
         }
@@ -350,7 +350,7 @@ void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, floa
                     bf16x8 s[M][3];
 #pragma unroll
                     for (int i = 0; i < M; ++i) sm.S[ct].get(k0 + i, lane, s[i]);
-                    mm_turns<OA, NK, 3>([&](int m) { return x[m]; }, [&](int m) { return s[m]; }, acc[ct]);
+                    mm_turns<3, NK, 3>([&](int m) { return x[m]; }, [&](int m) { return s[m]; }, acc[ct]);
                 }
             }
 #pragma unroll
@@ -376,7 +376,7 @@ void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, floa
 
 template <typename Tin, typename Tout, int NP, int CT, bool KEEP>
 hipError_t launch_ct(const DeltaArgs& a, const char* recs, float* keep_s, float* keep_u, int pad, hipStream_t stream) {
-    constexpr int bytes = (int)sizeof(ScanSmem<Tin, NP, CT, KEEP ? 0 : sizeof(Tout) == 2 ? 2 : 3>);
+    constexpr int bytes = (int)sizeof(ScanSmem<Tin, NP, CT, KEEP ? 0 : delta_a_planes(sizeof(Tin) == 2, sizeof(Tout) == 2)>);
     static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
     const int npb = (int)(((KEEP ? pad : a.P) + 16 * CT - 1) / (16 * CT));
     const int64_t units = (a.batch * a.H + 7) / 8 * 8;

@@ -321,3 +321,130 @@ def test_bwd_reproducible_stream_workspace(gpu):
     with pytest.raises(ss.SelscanError) as err:
         ss.delta_bwd(**i, dout=dout, workspace=ws[:need - 256])
     assert err.value.status == ss.ERR_WORKSPACE
+
+
+WIDE = [(3, 70, 60, 4, 80, 40), (2, 150, 70, 70, 64, 128), (5, 65, 64, 2, 17, 96)]   # 256 blocks of 32 columns and more
+
+
+@pytest.mark.parametrize("shape", WIDE)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_many_heads(gpu, shape, dtype):
+    """Grids large enough for two blocks of columns a workgroup, with odd widths and ragged rows."""
+    B, L, H, G, P, N = shape
+    i = inputs(*shape, dtype, seed=50 + L, h0=True)
+    lengths = torch.tensor([L, 0, L - 3, 1, 64][:B], dtype=torch.int32, device=DEV)
+    y, last = ss.delta_fwd(**i, lengths=lengths)
+    yb, _ = ss.delta_fwd(**i, lengths=lengths, out_dtype=BF16)
+    torch.cuda.synchronize()
+    yr, lr = ref.delta(**i, lengths=host(lengths).tolist())
+    close(y, yr, "y")
+    close(yb, yr, "bf16 y")
+    close(last, lr, "last_state")
+    dout, dlast = douts(B, L, H, P, N, dtype, L)
+    check_grads(*grads(i, dout, dlast, lengths=lengths))
+
+
+def test_graph_replays(gpu):
+    """Forward and gradients captured once, replayed over new inputs with eager calls between."""
+    shape = (2, 150, 4, 2, 64, 100)
+    B, L, H, G, P, N = shape
+    i = inputs(*shape, BF16, seed=60, h0=True)
+    dout, dlast = douts(B, L, H, P, N, BF16, 60)
+    need = ss.delta_workspace_bytes(B, L, H, P, G, N, ss.BF16, ss.F32)
+    needb = ss.delta_bwd_workspace_bytes(B, L, H, P, G, N)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    wsb = torch.empty(needb, dtype=torch.uint8, device=DEV)
+
+    def both():
+        y, last = ss.delta_fwd(**i, workspace=ws)
+        return {"y": y, "last": last, **ss.delta_bwd(**i, dout=dout, dlast_state=dlast, workspace=wsb)}
+
+    both()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both()
+    for r in range(4):
+        for n, x in inputs(*shape, BF16, seed=61 + r, h0=True).items():
+            i[n].copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        held = {n: x.clone() for n, x in got.items()}
+        want = both()
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(held[n], want[n]), (r, n)
+
+
+def test_fwd_workspace_refusal_and_leftovers(gpu):
+    """Whatever the workspace holds changes nothing; one that is too small is refused."""
+    i = inputs(1, 100, 2, 2, 32, 20, F32, seed=70)
+    need = ss.delta_workspace_bytes(1, 100, 2, 32, 2, 20, ss.F32)
+    assert need > 0 and ss.delta_workspace_bytes(1, 16, 2, 32, 2, 20, ss.F32) == 0
+    y, last = ss.delta_fwd(**i)
+    y2, last2 = ss.delta_fwd(**i, workspace=torch.full((need,), 255, dtype=torch.uint8, device=DEV))
+    torch.cuda.synchronize()
+    assert torch.equal(y, y2) and torch.equal(last, last2)
+    with pytest.raises(ss.SelscanError) as err:
+        ss.delta_fwd(**i, workspace=torch.empty(need - 256, dtype=torch.uint8, device=DEV))
+    assert err.value.status == ss.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_step_unaligned(gpu, dtype):
+    """q, k and v of a token off 16-byte boundaries (one element on) give what aligned ones give."""
+    i = inputs(3, 1, 4, 2, 64, 128, dtype, seed=71, h0=True)
+    a, b = i["h0"].clone(), i["h0"].clone()
+    tok = {n: x[:, 0].contiguous() for n, x in i.items() if n != "h0"}
+
+    def shifted(t):
+        v = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:].view(t.shape)
+        return v.copy_(t)
+
+    y = ss.delta_step(a, **tok)
+    ys = ss.delta_step(b, **{n: shifted(x) for n, x in tok.items()})
+    torch.cuda.synchronize()
+    h0 = i.pop("h0")
+    yr, lr = ref.delta(**i, h0=h0)
+    for got, state in ((y, a), (ys, b)):
+        close(got, yr[:, 0], "y")
+        close(state, lr, "state")
+
+
+def test_fwd_past_32_bits(gpu):
+    """Tensors and workspace past 2^32 bytes: the last tokens, continued from the state in front of them."""
+    L, H, tail = 300032, 64, 192
+    g = torch.Generator(device=DEV).manual_seed(72)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV, dtype=BF16)
+    q, k, v = rnd(1, L, 1, 128), rnd(1, L, 1, 128), rnd(1, L, H, 128)
+    k /= k.float().norm(dim=-1, keepdim=True)
+    gate = -torch.rand((1, L, H), generator=g, device=DEV) * 0.3
+    beta = torch.rand((1, L, H), generator=g, device=DEV)
+    assert v.numel() * 2 > 1 << 32
+    y, last = ss.delta_fwd(q, k, v, gate, beta)
+    head = tuple(t[:, :L - tail].contiguous() for t in (q, k, v, gate, beta))
+    state = ss.delta_fwd(*head)[1]
+    rest = tuple(t[:, L - tail:].contiguous() for t in (q, k, v, gate, beta))
+    yt, lt = ss.delta_fwd(*rest, h0=state)
+    torch.cuda.synchronize()
+    close(y[:, L - tail:], host(yt).double().numpy(), "last tokens")
+    close(last, host(lt).double().numpy(), "last_state")
+    yr, lr = ref.delta(*rest, h0=state)
+    close(yt, yr, "last tokens against the oracle")
+
+
+def test_bwd_past_32_bits(gpu):
+    """A workspace past 2^32 bytes: the last batch element's gradients equal those of its own call."""
+    B, L, H, P, N = 10, 8192, 16, 128, 128
+    assert ss.delta_bwd_workspace_bytes(B, L, H, P, H, N) > 1 << 32
+    g = torch.Generator(device=DEV).manual_seed(73)
+    rnd = lambda *s: torch.randn(s, generator=g, device=DEV, dtype=BF16)
+    q, k, v, dout = rnd(B, L, H, N), rnd(B, L, H, N), rnd(B, L, H, P), rnd(B, L, H, P)
+    k /= k.float().norm(dim=-1, keepdim=True)
+    gate = -torch.rand((B, L, H), generator=g, device=DEV) * 0.3
+    beta = torch.rand((B, L, H), generator=g, device=DEV)
+    got = ss.delta_bwd(q, k, v, gate, beta, dout)
+    want = ss.delta_bwd(*(t[B - 1:].contiguous() for t in (q, k, v, gate, beta, dout)))
+    torch.cuda.synchronize()
+    for n in want:
+        close(got[n][B - 1:], host(want[n]).double().numpy(), n)
