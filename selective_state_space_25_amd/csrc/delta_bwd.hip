@@ -35,29 +35,41 @@ namespace {
 using namespace dchunk;
 
 // ------------------------------------------------------------ the scan back
-// Waves share the work as in delta_scan.hip: wave w has dU, dR and dV of the
-// tokens 16 w .. 16 w + 15 and a quarter of D's rows.
+// Waves share the work as in delta_scan.hip: of the state waves, wave w has
+// dU, dR and dV of the tokens 16 w .. 16 w + 15 and a quarter of D's rows; the
+// helper wave beside it makes what does not wait for D, A^T dO of the next
+// chunk and Q^T (e^cum dO), which it hands over as C tiles, and stages K, Q,
+// the gates and dO, a chunk ahead.
+constexpr int kBackThreads = 512;
+
 template <typename Tin, typename Tdo, int NP, int CT>
 struct BackSmem {
     static constexpr int kRow = NP + 8;
-    uint16_t K[kPlanes<Tin>][kC][kRow];
+    static constexpr int kBufs = kPlanes<Tin> == 1 ? 2 : 1;   // K by chunk parity, where there is room
+    float gate[3][kC];                       // e^cum, e^(last - cum), beta
+    uint16_t K[kBufs][kPlanes<Tin>][kC][kRow];
     uint16_t Q[kPlanes<Tin>][kC][kRow];
     Operands<NP / 32, 3> D[CT];
     Operands<2, kPlanes<Tdo>> O[CT];         // dout
     Operands<2, 3> U[CT], R[CT], G[CT];      // dU; -beta e^cum dR; e^cum dO
+    Tiles X[CT];                             // A^T dO
+    Tiles H[CT][NP / 64];                    // Q^T (e^cum dO): tile i of wave w at [i][w]
 };
 
 template <typename Tin, typename Tdo, int NP, int CT>
-__global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_t nch, int npb) {
+__global__ __launch_bounds__(kBackThreads, 2) void delta_back_kernel(DeltaBwdArgs ba, int64_t nch, int npb) {
     constexpr int NK = kPlanes<Tin>, NO = kPlanes<Tdo>;
     constexpr int ES = (int)sizeof(Tin), EO = (int)sizeof(Tdo);
-    constexpr int kRow = BackSmem<Tin, Tdo, NP, CT>::kRow;
+    using Smem = BackSmem<Tin, Tdo, NP, CT>;
+    constexpr int kRow = Smem::kRow;
+    constexpr bool one = Smem::kBufs == 1;
     constexpr int KS = NP / 32, NT = NP / 64, NPC = NP / 32;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
-    auto& sm = *reinterpret_cast<BackSmem<Tin, Tdo, NP, CT>*>(smem_raw);
+    auto& sm = *reinterpret_cast<Smem*>(smem_raw);
     const DeltaArgs& a = ba.f;
-    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    const int tid = threadIdx.x & 255, lane = tid & 63, li = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const bool helper = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
     const int jx = blockIdx.x / 8;
     const int64_t bh = (int64_t)(jx / npb) * 8 + blockIdx.x % 8;
     if (bh >= a.batch * a.H) return;
@@ -67,91 +79,182 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
     const int mine = seq.n;
     const int N = a.N, P = (int)a.P, pad = ba.pad;
     const int p0 = (jx % npb) * 16 * CT + li;
-    const int sk = scalar((int)(a.G * a.qk_row * ES)), sv = scalar((int)(a.H * P * ES)), so = scalar((int)(a.H * P * EO));
+    const int sv = scalar((int)(a.H * P * ES));
+    char* dVg = scalar(static_cast<char*>(ba.dv) + b * a.L * sv + h * P * ES);
+    const char* Rg = scalar(ba.recs + bh * nch * GradRec::bytes);
+    const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto record = [&](int c) { return rows_buf(Rg + (int64_t)c * GradRec::bytes, c < 0 ? 0 : 1, 0, GradRec::bytes); };
+    int toff[2];
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks) toff[ks] = row_of_t(w, ks, lane);
+    // Inputs are asked for as soon as the chunk before has used their
+    // registers, a chunk's work ahead (before the first chunk: buffers of no
+    // rows)
+    bf16x8 fm[2][3];   // T^T for a state wave, A^T for a helper
+    auto fetch_m = [&](int c, int at) {
+        const auto rb = record(c);
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int x = 0; x < 3; ++x) fm[ks][x] = buf_op(rb, toff[ks] + at + x * kPlane);
+    };
+
+    if (!helper) {
+        f32x4 D[NT][CT];
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int n = 16 * (NT * w + i) + 4 * lg + q, p = p0 + 16 * ct;
+                    D[i][ct][q] = ba.dlast && p < P && n < N ? ba.dlast[(bh * P + p) * N + n] : 0.0f;
+                }
+        auto put_state = [&]() {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < NT; ++i) sm.D[ct].put_tile(NT * w + i, D[i][ct], lane);
+        };
+        int voff[CT];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            const int p = p0 + 16 * ct;
+            voff[ct] = p < P ? (16 * w + 4 * lg) * sv + p * ES : kOut;
+        }
+        fetch_m(mine - 1, GradRec::Tt);
+        put_state();
+        lds_barrier();
+        lds_barrier();
+        for (int c = mine - 1; c >= 0; --c) {
+            const uint16_t* K = &sm.K[one ? 0 : c & 1][0][0][0];
+            // dU for the wave's tokens
+            auto gate = [&](int i) { return *reinterpret_cast<const f32x4*>(sm.gate[i] + 16 * w + 4 * lg); };
+            const f32x4 gam = gate(0), tail = gate(1), beta = gate(2);
+            const float gl = sm.gate[0][kC - 1];
+            {
+                bf16x8 k[KS][NK];
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int x = 0; x < NK; ++x) k[ks][x] = ld8(K + (x * kC + 16 * w + li) * kRow + 32 * ks + 8 * lg);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    bf16x8 d[KS][3];
+                    f32x4 acc[KS];
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        sm.D[ct].get(ks, lane, d[ks]);
+                        acc[ks] = z4;
+                    }
+                    mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return d[m]; }, acc);
+                    sm.U[ct].put_tile(w, sum_of(acc) * tail + sm.X[ct].get(w, lane), lane);
+                    float* kd = ba.D + (bh * nch + c) * pad * NP + kept_tile<NP>(p0 - li + 16 * ct, NT * w, lane);
+#pragma unroll
+                    for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(kd + 256 * i) = D[i][ct];
+                }
+            }
+            lds_barrier();
+            // dR and dV for the wave's tokens (the last two waves' rows of
+            // T^T begin in the second k-step)
+            f32x4 r[CT];
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                bf16x8 y[2][3];
+                sm.U[ct].get(1, lane, y[1]);
+                if (w >= 2) {
+                    r[ct] = mm<3>(fm[1], y[1], z4);
+                } else {
+                    sm.U[ct].get(0, lane, y[0]);
+                    r[ct] = mm_pair(fm, y);
+                }
+                sm.R[ct].put_tile(w, -(r[ct] * beta * gam), lane);
+            }
+            fetch_m(c - 1, GradRec::Tt);
+            bf16x8 k[NT * 2][NK];
+#pragma unroll
+            for (int i = 0; i < NT * 2; ++i)
+#pragma unroll
+                for (int l = 0; l < NK; ++l)
+                    k[i][l] = ld_down(K + l * kC * kRow, kRow, 32 * (i & 1), 16 * (NT * w + i / 2), lane);
+            const auto vb = rows_buf(scalar(dVg + (int64_t)c * kC * sv), scalar(all.rows(c)), sv, P * ES);
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                float* kr = ba.dR + (bh * nch + c) * kC * pad + p0 + 16 * ct;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    kr[(16 * w + 4 * lg + q) * pad] = r[ct][q];
+                    buf_st(vb, voff[ct] + q * sv, beta[q] * r[ct][q], Tin(0));
+                }
+            }
+            lds_barrier();
+            // the wave's rows of the adjoint before the chunk
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) {
+                bf16x8 y[2][3];
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) sm.R[ct].get(ks, lane, y[ks]);
+                f32x4 acc[NT * 2];
+#pragma unroll
+                for (int i = 0; i < NT * 2; ++i) acc[i] = i & 1 ? sm.H[ct][i / 2].get(w, lane) : D[i / 2][ct] * gl;
+                mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return y[m & 1]; }, acc);
+#pragma unroll
+                for (int i = 0; i < NT; ++i) D[i][ct] = acc[2 * i] + acc[2 * i + 1];
+            }
+            put_state();
+            lds_barrier();
+        }
+        if (ba.dh0) {
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int i = 0; i < NT; ++i)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int n = 16 * (NT * w + i) + 4 * lg + q, p = p0 + 16 * ct;
+                        if (p < P && n < N) ba.dh0[(bh * P + p) * N + n] = D[i][ct][q];
+                    }
+        }
+        return;
+    }
+
+    // ---- helper waves
+    const int sk = scalar((int)(a.G * a.qk_row * ES)), so = scalar((int)(a.H * P * EO));
     const int64_t krow = b * a.L * sk + grp * a.qk_row * ES;
     const char* Kg = scalar(static_cast<const char*>(a.k) + krow);
     const char* Qg = scalar(static_cast<const char*>(a.q) + krow);
     const char* Og = scalar(static_cast<const char*>(ba.dout) + b * a.L * so + h * P * EO);
-    char* dVg = scalar(static_cast<char*>(ba.dv) + b * a.L * sv + h * P * ES);
-    const char* Rg = scalar(ba.recs + bh * nch * GradRec::bytes);
-
-    f32x4 D[NT][CT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int n = 16 * (NT * w + i) + 4 * lg + q, p = p0 + 16 * ct;
-                D[i][ct][q] = ba.dlast && p < P && n < N ? ba.dlast[(bh * P + p) * N + n] : 0.0f;
-            }
-    auto put_state = [&]() {
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct)
-#pragma unroll
-            for (int i = 0; i < NT; ++i) sm.D[ct].put_tile(NT * w + i, D[i][ct], lane);
-    };
-    int koff[NPC], roff[KS], toff[2], voff[CT], ooff[CT];
+    int koff[NPC], ooff[CT];
 #pragma unroll
     for (int i = 0; i < NPC; ++i) {
         const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
         koff[i] = n0 < a.NL ? r * sk + n0 * ES : kOut;
     }
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-        const int n = 32 * ks + 8 * lg;
-        roff[ks] = n < a.NL ? (16 * w + li) * sk + n * ES : kOut;
-    }
-#pragma unroll
-    for (int ks = 0; ks < 2; ++ks) toff[ks] = row_of_t(w, ks, lane);
-#pragma unroll
     for (int ct = 0; ct < CT; ++ct) {
         const int p = p0 + 16 * ct;
-        voff[ct] = p < P ? (16 * w + 4 * lg) * sv + p * ES : kOut;
         ooff[ct] = p < P ? (16 * w + 4 * lg) * so + p * EO : kOut;
     }
-
-    // Inputs are asked for as soon as the chunk before has used their
-    // registers, a chunk's work ahead (before the first chunk: buffers of no
-    // rows)
-    Raw8<Tin> fk[NPC], fq[NPC], fr[KS];
-    bf16x8 ft[2][3], fa[2][3];
+    Raw8<Tin> fk[NPC], fq[NPC];
     f32x4 fgate[3];
-    float fgl;
     Tdo fo[CT][4];
     auto rows = [&](const char* base, int stride, int c, int bytes) {
         return rows_buf(base + (int64_t)c * kC * stride, c < 0 ? 0 : seq.rows(c), stride, bytes);
     };
-    auto record = [&](int c) { return rows_buf(Rg + (int64_t)c * GradRec::bytes, c < 0 ? 0 : 1, 0, GradRec::bytes); };
     auto fetch_p = [&](const char* base, int c, Raw8<Tin> (&f)[NPC]) {
         const auto kb = rows(base, sk, c, a.NL * ES);
 #pragma unroll
         for (int i = 0; i < NPC; ++i) fetch8(kb, koff[i], f[i]);
     };
-    auto fetch_r = [&](int c) {
-        const auto kb = rows(Kg, sk, c, a.NL * ES);
+    auto fetch_o = [&](int c) {   // and the gates of the wave's tokens
+        const auto rb = record(c);
 #pragma unroll
-        for (int ks = 0; ks < KS; ++ks) fetch8(kb, roff[ks], fr[ks]);
-    };
-    auto fetch_o = [&](int c) {
+        for (int i = 0; i < 3; ++i) fgate[i] = buf_ld4(rb, GradRec::gam + (i * kC + 16 * w + 4 * lg) * 4);
         const auto ob = rows(Og, so, c, P * EO);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
             for (int q = 0; q < 4; ++q) fo[ct][q] = buf_raw<Tdo>(ob, ooff[ct] + q * so);
-    };
-    auto fetch_g = [&](int c) {
-        const auto rb = record(c);
-#pragma unroll
-        for (int i = 0; i < 3; ++i) fgate[i] = buf_ld4(rb, GradRec::gam + (i * kC + 16 * w + 4 * lg) * 4);
-        fgl = buf_raw<float>(rb, GradRec::gam + (kC - 1) * 4);
-    };
-    auto fetch_m = [&](int c, int at, bf16x8 (&f)[2][3]) {
-        const auto rb = record(c);
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-            for (int x = 0; x < 3; ++x) f[ks][x] = buf_op(rb, toff[ks] + at + x * kPlane);
     };
     auto stage_p = [&](uint16_t (*m)[kC][kRow], const Raw8<Tin> (&f)[NPC]) {
 #pragma unroll
@@ -160,162 +263,92 @@ __global__ __launch_bounds__(256) void delta_back_kernel(DeltaBwdArgs ba, int64_
             stage8(m[0][r], kC * kRow, n0, f[i]);
         }
     };
-    f32x4 o[CT];
-    auto put_o = [&]() {
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            o[ct] = widen(fo[ct]);
-            sm.O[ct].put_tile(w, o[ct], lane);
-        }
-    };
-
-    put_state();
-    if (mine > 0) {
-        const int c = mine - 1;
-        fetch_o(c);
-        fetch_r(c);
-        fetch_m(c, GradRec::At, fa);
-        fetch_g(c);
-        fetch_p(Kg, c, fk);
-        fetch_m(c, GradRec::Tt, ft);
-        fetch_p(Qg, c, fq);
-        put_o();
-        fetch_o(c - 1);
-    }
-    lds_barrier();
-    for (int c = mine - 1; c >= 0; --c) {
-        const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
-        // dU for the wave's tokens
-        f32x4 u[CT], x[CT];
-        {
-            bf16x8 k[KS][NK];
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks) to_operand(fr[ks], k[ks]);
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                bf16x8 d[KS][3];
-                f32x4 acc[KS];
-#pragma unroll
-                for (int ks = 0; ks < KS; ++ks) {
-                    sm.D[ct].get(ks, lane, d[ks]);
-                    acc[ks] = z4;
-                }
-                mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return d[m]; }, acc);
-                u[ct] = sum_of(acc);
-            }
-        }
-        fetch_r(c - 1);
-        {
-#pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                bf16x8 d[2][NO];
-                // (the last two waves' rows of A^T begin in the second k-step)
-                sm.O[ct].get(1, lane, d[1]);
-                if (w >= 2) {
-                    x[ct] = mm<3>(fa[1], d[1], z4);
-                } else {
-                    sm.O[ct].get(0, lane, d[0]);
-                    f32x4 acc[2] = {z4, z4};
-                    mm_turns<3, 3, NO>([&](int m) { return fa[m]; }, [&](int m) { return d[m]; }, acc);
-                    x[ct] = sum_of(acc);
-                }
-            }
-        }
-        fetch_m(c - 1, GradRec::At, fa);
-        const f32x4 gam = fgate[0], tail = fgate[1], beta = fgate[2];
-        const float gl = fgl;
-        fetch_g(c - 1);
-#pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            sm.U[ct].put_tile(w, u[ct] * tail + x[ct] * a.scale, lane);
-            sm.G[ct].put_tile(w, o[ct] * gam * a.scale, lane);
-            float* kd = ba.D + (bh * nch + c) * pad * NP + kept_tile<NP>(p0 - li + 16 * ct, NT * w, lane);
-#pragma unroll
-            for (int i = 0; i < NT; ++i) *reinterpret_cast<f32x4*>(kd + 256 * i) = D[i][ct];
-        }
-        stage_p(sm.K, fk);
+    auto stage_k = [&](int c) {
+        stage_p(sm.K[one ? 0 : c & 1], fk);
         fetch_p(Kg, c - 1, fk);
-        lds_barrier();
-        // dR and dV for the wave's tokens
-        f32x4 r[CT];
-        {
+    };
+    // all that a chunk needs in LDS but K; and the next one's on the way
+    auto stage = [&](int c) {
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) {
-                bf16x8 y[2][3];
-                sm.U[ct].get(1, lane, y[1]);
-                if (w >= 2) {
-                    r[ct] = mm<3>(ft[1], y[1], z4);
-                } else {
-                    sm.U[ct].get(0, lane, y[0]);
-                    f32x4 acc[2] = {z4, z4};
-                    mm_turns<3, 3, 3>([&](int m) { return ft[m]; }, [&](int m) { return y[m]; }, acc);
-                    r[ct] = sum_of(acc);
-                }
-                sm.R[ct].put_tile(w, -(r[ct] * beta * gam), lane);
-            }
+        for (int i = 0; i < 3; ++i)
+            if (li == 0) *reinterpret_cast<f32x4*>(sm.gate[i] + 16 * w + 4 * lg) = fgate[i];
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            const f32x4 o = widen(fo[ct]);
+            sm.O[ct].put_tile(w, o, lane);
+            sm.G[ct].put_tile(w, o * fgate[0] * a.scale, lane);
         }
-        fetch_m(c - 1, GradRec::Tt, ft);
+        fetch_o(c - 1);
         stage_p(sm.Q, fq);
         fetch_p(Qg, c - 1, fq);
-        const auto vb = rows_buf(scalar(dVg + (int64_t)c * kC * sv), scalar(all.rows(c)), sv, P * ES);
+    };
+    // A^T dO for the wave's tokens
+    auto put_x = [&](int c) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            float* kr = ba.dR + (bh * nch + c) * kC * pad + p0 + 16 * ct;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                kr[(16 * w + 4 * lg + q) * pad] = r[ct][q];
-                buf_st(vb, voff[ct] + q * sv, beta[q] * r[ct][q], Tin(0));
+            bf16x8 d[2][NO];
+            f32x4 x;
+            sm.O[ct].get(1, lane, d[1]);
+            if (w >= 2) {
+                x = mm<3>(fm[1], d[1], z4);
+            } else {
+                sm.O[ct].get(0, lane, d[0]);
+                f32x4 acc[2] = {z4, z4};
+                mm_turns<3, 3, NO>([&](int m) { return fm[m]; }, [&](int m) { return d[m]; }, acc);
+                x = sum_of(acc);
             }
+            sm.X[ct].put(w, x * a.scale, lane);
         }
+        fetch_m(c - 1, GradRec::At);
+    };
+
+    {
+        const int c = mine - 1;
+        fetch_o(c);
+        fetch_p(Qg, c, fq);
+        fetch_p(Kg, c, fk);
+        fetch_m(c, GradRec::At);
+        stage(c);
+        stage_k(c);
         lds_barrier();
-        // the wave's rows of the adjoint before the chunk
+        put_x(c);
+        lds_barrier();
+    }
+    for (int c = mine - 1; c >= 0; --c) {
+        // Q^T (e^cum dO), the wave's rows
         {
-            bf16x8 k[NT * 2][NK], q[NT * 2][NK];
+            bf16x8 q[NT * 2][NK];
 #pragma unroll
             for (int i = 0; i < NT * 2; ++i)
 #pragma unroll
-                for (int l = 0; l < NK; ++l) {
-                    k[i][l] = ld_down(&sm.K[l][0][0], kRow, 32 * (i & 1), 16 * (NT * w + i / 2), lane);
-                    q[i][l] = ld_down(&sm.Q[l][0][0], kRow, 32 * (i & 1), 16 * (NT * w + i / 2), lane);
-                }
+                for (int l = 0; l < NK; ++l) q[i][l] = ld_down(&sm.Q[l][0][0], kRow, 32 * (i & 1), 16 * (NT * w + i / 2), lane);
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
-                bf16x8 y[2][3], g[2][3];
+                bf16x8 g[2][3];
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    sm.R[ct].get(ks, lane, y[ks]);
-                    sm.G[ct].get(ks, lane, g[ks]);
-                }
+                for (int ks = 0; ks < 2; ++ks) sm.G[ct].get(ks, lane, g[ks]);
                 f32x4 acc[NT * 2];
 #pragma unroll
-                for (int i = 0; i < NT * 2; ++i) acc[i] = i & 1 ? z4 : D[i / 2][ct] * gl;
-                mm_turns<3, NK, 3>([&](int m) { return k[m]; }, [&](int m) { return y[m & 1]; }, acc);
+                for (int i = 0; i < NT * 2; ++i) acc[i] = z4;
                 mm_turns<3, NK, 3>([&](int m) { return q[m]; }, [&](int m) { return g[m & 1]; }, acc);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) D[i][ct] = acc[2 * i] + acc[2 * i + 1];
+                for (int i = 0; i < NT; ++i) sm.H[ct][i].put(w, acc[2 * i] + acc[2 * i + 1], lane);
             }
         }
-        put_state();
-        put_o();
-        fetch_o(c - 2);
+        lds_barrier();
+        stage(c - 1);
+        if constexpr (!one) stage_k(c - 1);
+        lds_barrier();
+        put_x(c - 1);
+        // (the state waves have K in registers since the barrier)
+        if constexpr (one) stage_k(c - 1);
         lds_barrier();
     }
 #pragma unroll
-    for (int ct = 0; ct < CT; ++ct) {
-        const int p = p0 + 16 * ct;
-        if (p >= P) continue;
-        for (int64_t t = (int64_t)mine * kC + 4 * w + lg; t < a.L; t += 16)
-            io::st(reinterpret_cast<Tin*>(dVg + t * sv) + p, 0.0f);
-        if (ba.dh0) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int n = 16 * (NT * w + i) + 4 * lg + q;
-                    if (n < N) ba.dh0[(bh * P + p) * N + n] = D[i][ct][q];
-                }
-        }
-    }
+    for (int ct = 0; ct < CT; ++ct)
+        if (p0 + 16 * ct < P)
+            for (int64_t t = (int64_t)mine * kC + 4 * w + lg; t < a.L; t += 16)
+                io::st(reinterpret_cast<Tin*>(dVg + t * sv) + p0 + 16 * ct, 0.0f);
 }
 
 // ------------------------------------------------- gradients inside a chunk
@@ -809,7 +842,7 @@ hipError_t launch_back(const DeltaBwdArgs& a, hipStream_t stream) {
     const int npb = a.pad / (16 * CT);
     const int64_t units = (f.batch * f.H + 7) / 8 * 8;
     KTime kt("delta_back", stream);
-    hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(256), bytes, stream, a, delta_chunks(f.L), npb);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(units * npb)), dim3(kBackThreads), bytes, stream, a, delta_chunks(f.L), npb);
     return hipGetLastError();
 }
 
@@ -822,8 +855,9 @@ hipError_t launch(const DeltaBwdArgs& a, hipStream_t stream) {
     e = launch_delta_keep(f, sizeof(Tin) == 2, a.recs, a.S, a.U, a.pad, stream);
     if (e != hipSuccess) return e;
     // Two column blocks to a workgroup where half as many still give each CU
-    // one, as in the scan (batch 4, 16 heads of 128 x 128, L 2048: 171 us
-    // against 194).  float32 inputs: one block takes all registers.
+    // one, as in the scan (batch 4, 16 heads of 128 x 128, L 2048, before the
+    // helper waves: 171 us against 194).  float32 inputs: two blocks' LDS
+    // would not fit.
     bool two = false;
     if constexpr (sizeof(Tin) == 2) {
         two = f.batch * f.H * (a.pad / 32) >= host::device_cus();
