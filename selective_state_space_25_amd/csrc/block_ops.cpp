@@ -29,8 +29,8 @@ selscan_status_t check_norm(const selscan_norm_shape_t* s) {
     if (!is_probability(s->p)) return set_error(SELSCAN_ERR_INVALID_ARG, "p must be in [0, 1]");
     if (mul_checked({s->rows, s->dim, 4}) < 0 || mul_checked({s->dim, 2048, 8}) < 0)
         return set_error(SELSCAN_ERR_INVALID_ARG, "tensor sizes overflow 64-bit byte counts");
-    if (s->rows > 0x7fffffff || s->dim > 0x7fffffff)
-        return set_error(SELSCAN_ERR_UNSUPPORTED, "layer norm supports rows and dim < 2^31");
+    if (s->rows > 0x7fffffff || s->dim > 0xfffffff)
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "layer norm supports rows < 2^31 and dim < 2^28");
     return SELSCAN_OK;
 }
 
@@ -63,7 +63,7 @@ selscan_status_t selscan_dropout(const selscan_dropout_shape_t* s, const void* x
         if (!is_dtype(s->dtype)) return set_error(SELSCAN_ERR_UNSUPPORTED, "dtype must be SELSCAN_F32 or SELSCAN_BF16");
         if (!is_probability(s->p)) return set_error(SELSCAN_ERR_INVALID_ARG, "p must be in [0, 1]");
         if (mul_checked({s->n, 4}) < 0) return set_error(SELSCAN_ERR_INVALID_ARG, "n overflows 64-bit byte counts");
-        if (s->n / 1024 >= 0x7fffffff) return set_error(SELSCAN_ERR_UNSUPPORTED, "too many elements for one launch");
+        if (s->n >> 45) return set_error(SELSCAN_ERR_UNSUPPORTED, "too many elements for one launch");
         if (!x || !y) return set_error(SELSCAN_ERR_INVALID_ARG, "x and y must be non-NULL");
         selscan_status_t st = device_check();
         if (st != SELSCAN_OK) return st;

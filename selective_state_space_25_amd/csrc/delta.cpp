@@ -31,9 +31,9 @@ selscan_status_t check_shape(const selscan_m2_shape_t* s) {
     // the chunked form's offsets inside 64 tokens are 32-bit
     if (s->nheads * s->headdim > (int64_t(1) << 22) || s->ngroups > (int64_t(1) << 15))
         return set_error(SELSCAN_ERR_UNSUPPORTED, "the gated delta rule supports nheads headdim <= 2^22 and ngroups <= 2^15");
-    // 16 rows of a state per workgroup of the token-by-token kernel, a chunk per workgroup of the chunked form
-    if (mul_checked({s->batch, s->nheads, s->headdim}) / 16 >= 0x7fffff00 ||
-        mul_checked({s->batch, s->nheads, selscan::delta_chunks(s->seqlen)}) >= 0x7fffff00)
+    // a launch has fewer than 2^32 threads: 512 to 16 rows of a head's state, 256 to a chunk
+    const int64_t heads = (s->batch * s->nheads + 7) / 8 * 8;
+    if (heads * ((s->headdim + 15) / 16) >= 1 << 23 || mul_checked({heads, selscan::delta_chunks(s->seqlen)}) >= 1 << 24)
         return set_error(SELSCAN_ERR_UNSUPPORTED, "too many (batch, head, channel) rows or chunks for one launch");
     return SELSCAN_OK;
 }

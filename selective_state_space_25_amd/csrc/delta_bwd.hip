@@ -24,7 +24,14 @@
 // dV (16 or 32 value columns a workgroup), the gradients that are local to a
 // chunk (all chunks at once), and, where heads share q and k, their sum over
 // the heads in a fixed order.  All products are fp32-grade except those that
-// go into a bf16 dq or dk alone.
+// go into a bf16 dq or dk alone, which keep plane pairs a + b < 2, an error
+// near 2^-16 of the term under the 2^-9 of the gradient's own rounding.
+//
+// Measured at batch 4, 16 heads of 128 x 128, L 2048, bf16: records 40 us,
+// kept scan 94, scan back 152 (0.39 GB, 2.6 TB/s: a chain of three products a
+// chunk, 4.7 us), gradients 252 (0.5 GB, 2 TB/s: the vector ALU, a quarter of
+// the time for splitting into planes, the matrix cores, 15 %, and LDS take
+// turns, with one workgroup to a CU).
 #include "delta_chunk.hpp"
 #include "host.hpp"
 

@@ -8,6 +8,11 @@
 //
 // where S.k, S.q and k.q are sums over the row's old state, reduced together
 // across the Q lanes that share a row: one reduction a token, not two.
+//
+// One token is bound by the state's bytes: batch 128, 16 heads of 128 x 128,
+// 270 MB read and written in 52 us alone (5.2 TB/s, what a copy reaches), 63
+// us behind other work.  A single small sequence (32 heads of 64 x 128) is
+// the launch: 9 us a call through a bound call.
 #include "io.hpp"
 #include "kernels.hpp"
 

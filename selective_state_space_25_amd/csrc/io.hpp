@@ -52,5 +52,13 @@ __device__ __forceinline__ void st8(uint16_t* p, const float* v) {
                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
+// Workgroups 0 .. n - 1 over two dimensions (a dimension holds fewer than
+// 2^32 threads): those past n are for the kernel to turn away.
+inline dim3 groups(int64_t n) {
+    const int64_t x = n < (1 << 20) ? n : 1 << 20;
+    return dim3((unsigned)x, (unsigned)((n + x - 1) / x));
+}
+__device__ __forceinline__ int64_t group_id() { return (int64_t)blockIdx.y * gridDim.x + blockIdx.x; }
+
 }  // namespace io
 }  // namespace selscan

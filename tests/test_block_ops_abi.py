@@ -115,3 +115,21 @@ def test_delta_bwd_null(missing):
     a = [FAKE] * 5 + [1.0, None, None, FAKE, None] + [FAKE] * 5 + [None, None]
     a[missing] = None
     assert ss.lib().selscan_delta_bwd(ctypes.byref(s), *a) == ss.ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw", [dict(batch=1 << 20, nheads=64, headdim=64), dict(seqlen=1 << 31),
+                                dict(nheads=1 << 15, headdim=256)])
+def test_delta_more_than_a_launch(kw):
+    """Shapes whose grids no launch holds are refused, not cut off."""
+    s = _delta(**kw)
+    r = ss.lib().selscan_delta_fwd(ctypes.byref(s), FAKE, FAKE, FAKE, FAKE, FAKE, 1.0, None, None, FAKE, None, None)
+    assert r == ss.ERR_UNSUPPORTED and ss.last_error()
+    assert ss.lib().selscan_delta_bwd_workspace_bytes(ctypes.byref(s)) == 0
+
+
+def test_norm_and_dropout_more_than_a_launch():
+    s = ss.NormShape(2, 1 << 28, 0, 0, 0, 1e-5, 0.0, 1, 0, None, 0)
+    assert ss.lib().selscan_layer_norm_fwd(ctypes.byref(s), FAKE, None, None, None, FAKE, None, None, None,
+                                           None) == ss.ERR_UNSUPPORTED
+    d = ss.DropoutShape(1 << 45, 0, 0.5, 1, 0)
+    assert ss.lib().selscan_dropout(ctypes.byref(d), FAKE, FAKE, None) == ss.ERR_UNSUPPORTED

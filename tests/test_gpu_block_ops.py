@@ -168,3 +168,31 @@ def test_layer_norm_longer_rows_and_many_rows(gpu, rows, dim):
         atol, rtol = _tol(t, gr[name])
         # (sums over the rows: their magnitudes add up where the result does not)
         check_close(host(g[name]).double().numpy(), gr[name], (atol * max(1.0, float(np.max(rr))), rtol), name)
+
+
+@pytest.mark.parametrize("rows,dim", [((1 << 24) + 3, 5), ((1 << 24) + 5, 16)])
+def test_layer_norm_more_rows_than_a_grid_dimension(gpu, rows, dim):
+    """Rows past 2^32 threads in one dimension of the grid: the last rows equal those of their own call."""
+    g = torch.Generator(device=DEV).manual_seed(5)
+    x = torch.randn((rows, dim), generator=g, device=DEV, dtype=torch.bfloat16)
+    dy = torch.randn((rows, dim), generator=g, device=DEV, dtype=torch.bfloat16)
+    y, s, mean, rstd = ss.layer_norm_fwd(x)
+    d = ss.layer_norm_bwd(dy, s, None, mean, rstd)
+    tail = slice(rows - 1000, rows)
+    yt, st, mt, rt = ss.layer_norm_fwd(x[tail].contiguous())
+    dt = ss.layer_norm_bwd(dy[tail].contiguous(), st, None, mt, rt)
+    torch.cuda.synchronize()
+    assert torch.equal(y[tail], yt) and torch.equal(mean[tail], mt) and torch.equal(rstd[tail], rt)
+    assert torch.equal(d["dx"][tail], dt["dx"])
+
+
+def test_dropout_past_32_bits(gpu):
+    """Elements past 2^34, a grid of more than 2^32 threads: the last ones' words by their own counters."""
+    n = (1 << 34) + 22
+    x = torch.ones(n, dtype=torch.bfloat16, device=DEV)
+    y = ss.dropout(x, 0.5, 9, 4, out=x)
+    got = host(y[n - 22:]).double().numpy()
+    first = n // 4 - 5
+    words = np.asarray([w for c in range(first, first + 6) for w in ref.philox((c & 0xFFFFFFFF, c >> 32, 4, 0), (9, 0))])
+    want = np.where(words >= (1 << 31), 2.0, 0.0)[(n - 22) - 4 * first:][:22]
+    assert np.array_equal(got, want)
