@@ -359,6 +359,9 @@ __global__ __launch_bounds__(kBackThreads, 2) void delta_back_kernel(DeltaBwdArg
 }
 
 // ------------------------------------------------- gradients inside a chunk
+// Eight waves: wave w has the 16 tokens of row block w % 4 and half w / 4 of
+// the key's columns; of its row block's pairs it has every other block.
+constexpr int kGradThreads = 512;
 constexpr int kPb = 32;            // value columns per step of the sums over p
 constexpr int kRowP = kPb + 8;
 constexpr int kRowX = kC + 8;
@@ -368,8 +371,7 @@ struct GradSmem {
     static constexpr int kRow = NP + 8;
     double cum[kC];
     double col[4][kC];             // per row block: column sums of Z
-    double up[kC], down[kC];       // rowsum Z + a; b
-    double sd[4];
+    double sd[8];
     float rv[kC];
     union {
         struct {                   // a step over 32 value columns
@@ -382,6 +384,11 @@ struct GradSmem {
             uint16_t X[LB][kC][kRowX], E[LB][kC][kRowX];
         } m;
     };
+    // A half's sums for token t, in the padding of its rows of X and E:
+    // rowsum Z + a; b; what dbeta gets beside dR.V.
+    __device__ __forceinline__ double* up(int t) { return reinterpret_cast<double*>(&m.X[0][t][kC]); }
+    __device__ __forceinline__ double* down(int t) { return reinterpret_cast<double*>(&m.X[1][t][kC]); }
+    __device__ __forceinline__ double* db(int t) { return reinterpret_cast<double*>(&m.E[0][t][kC]); }
 };
 
 // Four elements of a row as loaded, those past n zero (vec: in one piece).
@@ -414,33 +421,35 @@ __device__ __forceinline__ f32x4 widen(const Raw4<uint16_t>& r) {
 }
 __device__ __forceinline__ f32x4 widen(const Raw4<float>& r) { return r.v; }
 
-__device__ __forceinline__ void from_floats(const float (&e)[8], Raw8<uint16_t>& r) {   // (values that are bf16)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.w[i] = pack_bf16x2(e[2 * i], e[2 * i + 1]);
-}
-__device__ __forceinline__ void from_floats(const float (&e)[8], Raw8<float>& r) {
-    r.lo = f32x4{e[0], e[1], e[2], e[3]};
-    r.hi = f32x4{e[4], e[5], e[6], e[7]};
-}
-
 __device__ __forceinline__ double sum16(double v) {
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o, 64);
     return v;
 }
 
+// Into the planes of a staged row (plane stride ps elements).
+__device__ __forceinline__ void stage4(uint16_t* row, int ps, const Raw4<uint16_t>& r) {
+    *reinterpret_cast<uint2*>(row) = make_uint2(r.w[0], r.w[1]);
+}
+__device__ __forceinline__ void stage4(uint16_t* row, int ps, const Raw4<float>& r) {
+    uint2 p[3];
+    split4<3>(r.v, p);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) *reinterpret_cast<uint2*>(row + i * ps) = p[i];
+}
+
 template <typename Tin, typename Tdo, int NP>
-__global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_t nch) {
+__global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs ba, int64_t nch) {
     constexpr int NK = kPlanes<Tin>, NO = kPlanes<Tdo>;
     constexpr int LB = NK == 1 ? 2 : 3;      // plane pairs of what goes into dq and dk alone
     using Smem = GradSmem<Tin, Tdo, NP, LB>;
     constexpr int kRow = Smem::kRow;
-    constexpr int NB = NP / 16;
+    constexpr int NB = NP / 16, NH = NB / 2;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
     auto& sm = *reinterpret_cast<Smem*>(smem_raw);
     const DeltaArgs& a = ba.f;
-    const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, li = lane & 15, lg = lane >> 4;
-    const int tb = wave;                     // the wave's 16 tokens
+    const int tid = threadIdx.x, lane = tid & 63, li = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), tb = wave & 3, half = wave >> 2;
     const int64_t bh = blockIdx.x / nch, c = blockIdx.x - bh * nch;
     const int64_t b = bh / a.H, h = bh - b * a.H, grp = h / (a.H / a.G);
     const int64_t t0 = c * kC;
@@ -456,7 +465,7 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
         else io::st(reinterpret_cast<Tin*>(out) + ((b * a.L + t0 + r) * a.G + grp) * N + n, v);
     };
     if (live == 0) {
-        for (int i = tid; i < inside * N; i += 256) {
+        for (int i = tid; i < inside * N; i += kGradThreads) {
             put(ba.dq, ba.pq, i / N, i % N, 0.0f);
             put(ba.dk, ba.pk, i / N, i % N, 0.0f);
         }
@@ -470,16 +479,16 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     if (tid < kC) sm.cum[tid] = reinterpret_cast<const double*>(rec + GradRec::cum)[tid];
 
     // ---- sums over the value columns: dO S^T, dR S^T, U D^T for the wave's
-    // tokens, dO U^T and dR U^T for its row block, <S, D>, dR.V
+    // tokens and columns, dO U^T and dR U^T for its pairs, <S, D>, dR.V
     const f32x4 z4 = {0.0f, 0.0f, 0.0f, 0.0f};
     // (U D^T in two sums: D may be far larger than what of it reaches dg)
-    f32x4 q1[NB], k2[NB], k3[NB], k3r[NB], x1[4], x2[4];
+    f32x4 q1[NH], k2[NH], k3[NH], k3r[NH], x1[2], x2[2];
 #pragma unroll
-    for (int i = 0; i < NB; ++i) q1[i] = k2[i] = k3[i] = k3r[i] = z4;
+    for (int i = 0; i < NH; ++i) q1[i] = k2[i] = k3[i] = k3r[i] = z4;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x1[i] = x2[i] = z4;
+    for (int i = 0; i < 2; ++i) x1[i] = x2[i] = z4;
     double sd = 0.0;
-    float rv[2] = {0.0f, 0.0f};
+    float rv = 0.0f;
     const float* Sg = ba.S + (int64_t)blockIdx.x * pad * NP;
     const float* Dg = ba.D + (int64_t)blockIdx.x * pad * NP;
     const float* Ug = ba.U + (int64_t)blockIdx.x * kC * pad;
@@ -491,49 +500,41 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     const auto ob = rows_buf(scalar(static_cast<const char*>(ba.dout) + row0 * so + h * P * EO), scalar(live), so, P * EO);
     const auto vb = rows_buf(scalar(static_cast<const char*>(a.v) + row0 * sv + h * P * ES), scalar(live), sv, P * ES);
     // A step's inputs are fetched while the step before computes.
-    f32x4 fs[NP / 32], fd[NP / 32], fu[2], fr[2];
-    Raw4<Tin> fv[2];
-    Raw8<Tdo> fo;
+    f32x4 fs[NP / 64], fd[NP / 64], fu, fr;
+    Raw4<Tin> fv;
+    Raw4<Tdo> fo;
+    const int pr = tid >> 3, pe = 4 * (tid & 7);   // the thread's row and columns of a step's U, dR, V and dO
     auto fetch = [&](int pb) {
 #pragma unroll
-        for (int i = 0; i < NP / 32; ++i) {      // S and D: two column blocks' tiles in turn
-            const int id = wave + 4 * i;
+        for (int i = 0; i < NP / 64; ++i) {      // S and D: two column blocks' tiles in turn
+            const int id = wave + 8 * i;
             fs[i] = *reinterpret_cast<const f32x4*>(Sg + kept_tile<NP>(pb + 16 * (id / NB), id % NB, lane));
             fd[i] = *reinterpret_cast<const f32x4*>(Dg + kept_tile<NP>(pb + 16 * (id / NB), id % NB, lane));
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {            // U, dR and V: 64 rows of 32
-            const int id = tid + 256 * i, r = id >> 3, e0 = pb + 4 * (id & 7);
-            fu[i] = *reinterpret_cast<const f32x4*>(Ug + (int64_t)r * pad + e0);
-            fr[i] = *reinterpret_cast<const f32x4*>(Rg + (int64_t)r * pad + e0);
-            fetch4(vb, r * sv + e0 * ES, P - e0, ba.vec_p, fv[i]);
-        }
-        const int r = tid >> 2, e0 = pb + 8 * (tid & 3);
-        if (ba.vec_p) {
-            fetch8(ob, e0 < P ? r * so + e0 * EO : kOut, fo);
-        } else {
-            float e[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) e[i] = buf_ld<Tdo>(ob, e0 + i < P ? r * so + (e0 + i) * EO : kOut);
-            from_floats(e, fo);
-        }
+        const int e0 = pb + pe;
+        fu = *reinterpret_cast<const f32x4*>(Ug + (int64_t)pr * pad + e0);
+        fr = *reinterpret_cast<const f32x4*>(Rg + (int64_t)pr * pad + e0);
+        fetch4(vb, pr * sv + e0 * ES, P - e0, ba.vec_p, fv);
+        fetch4(ob, pr * so + e0 * EO, P - e0, ba.vec_p, fo);
     };
     // what follows the steps: K, Q, and A's rows of the wave's tokens
-    Raw8<Tin> fk[NP / 32], fq[NP / 32];
-    float am[4][4];
+    Raw8<Tin> fk[NP / 64], fq[NP / 64];
+    float am[2][4];
     auto fetch_kq = [&]() {
         const auto rb = rows_buf(scalar(rec), 1, 0, GradRec::bytes);
 #pragma unroll
-        for (int sb = 0; sb < 4; ++sb)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                am[sb][q] = buf_raw<float>(rb, sb <= tb ? GradRec::A + (block_at(tb, sb) * 256 + (4 * lg + q) * 16 + li) * 4 : kOut);
+            for (int q = 0; q < 4; ++q) {
+                const int sb = 2 * j + half;
+                am[j][q] = buf_raw<float>(rb, sb <= tb ? GradRec::A + (block_at(tb, sb) * 256 + (4 * lg + q) * 16 + li) * 4 : kOut);
+            }
         const int64_t at = row0 * sk + grp * a.qk_row * ES;
         const auto kb = rows_buf(scalar(static_cast<const char*>(a.k) + at), scalar(live), sk, a.NL * ES);
         const auto qb = rows_buf(scalar(static_cast<const char*>(a.q) + at), scalar(live), sk, a.NL * ES);
 #pragma unroll
-        for (int i = 0; i < NP / 32; ++i) {
-            const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+        for (int i = 0; i < NP / 64; ++i) {
+            const int id = tid + kGradThreads * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
             const int off = n0 < a.NL ? r * sk + n0 * ES : kOut;
             fetch8(kb, off, fk[i]);
             fetch8(qb, off, fq[i]);
@@ -543,8 +544,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     for (int pb = 0; pb < pad; pb += kPb) {
         lds_barrier();
 #pragma unroll
-        for (int i = 0; i < NP / 32; ++i) {
-            const int id = wave + 4 * i, r = 16 * (id / NB) + li, n = 16 * (id % NB) + 4 * lg;
+        for (int i = 0; i < NP / 64; ++i) {
+            const int id = wave + 8 * i, r = 16 * (id / NB) + li, n = 16 * (id % NB) + 4 * lg;
 #pragma unroll
             for (int e = 0; e < 4; ++e) sd = __builtin_fma((double)fs[i][e], (double)fd[i][e], sd);
             uint2 sp[3], dp[3];
@@ -556,25 +557,21 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 *reinterpret_cast<uint2*>(&sm.s.D[x][r][n]) = dp[x];
             }
         }
+        const f32x4 v = widen(fv);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int id = tid + 256 * i, r = id >> 3, e0 = 4 * (id & 7);
-            const f32x4 v = widen(fv[i]);
+        for (int e = 0; e < 4; ++e) rv = __builtin_fmaf(fr[e], v[e], rv);
+        uint2 up[3], dp[3];
+        split4<3>(fu, up);
+        split4<3>(fr, dp);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) rv[i] = __builtin_fmaf(fr[i][e], v[e], rv[i]);
-            uint2 up[3], dp[3];
-            split4<3>(fu[i], up);
-            split4<3>(fr[i], dp);
-#pragma unroll
-            for (int x = 0; x < 3; ++x) {
-                *reinterpret_cast<uint2*>(&sm.s.U[x][r][e0]) = up[x];
-                *reinterpret_cast<uint2*>(&sm.s.R[x][r][e0]) = dp[x];
-            }
+        for (int x = 0; x < 3; ++x) {
+            *reinterpret_cast<uint2*>(&sm.s.U[x][pr][pe]) = up[x];
+            *reinterpret_cast<uint2*>(&sm.s.R[x][pr][pe]) = dp[x];
         }
-        stage8(sm.s.O[0][tid >> 2], kC * kRowP, 8 * (tid & 3), fo);
+        stage4(&sm.s.O[0][pr][pe], kC * kRowP, fo);
         lds_barrier();
         if (pb + kPb < pad) fetch(pb + kPb);
-        else fetch_kq();
+        else if (NK == 1) fetch_kq();
         bf16x8 o[NO], r[3], u[3];
 #pragma unroll
         for (int x = 0; x < NO; ++x) o[x] = ld8(&sm.s.O[x][16 * tb + li][8 * lg]);
@@ -584,12 +581,12 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             u[x] = ld8(&sm.s.U[x][16 * tb + li][8 * lg]);
         }
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
+        for (int i = 0; i < NH; ++i) {
             bf16x8 s[3], d[3];
 #pragma unroll
             for (int x = 0; x < 3; ++x) {
-                s[x] = ld_down(&sm.s.S[x][0][0], kRow, 0, 16 * i, lane);
-                d[x] = ld_down(&sm.s.D[x][0][0], kRow, 0, 16 * i, lane);
+                s[x] = ld_down(&sm.s.S[x][0][0], kRow, 0, 16 * (half * NH + i), lane);
+                d[x] = ld_down(&sm.s.D[x][0][0], kRow, 0, 16 * (half * NH + i), lane);
             }
             // the planes' products in turn over the sums
 #pragma unroll
@@ -603,7 +600,8 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 }
         }
 #pragma unroll
-        for (int sb = 0; sb < 4; ++sb) {
+        for (int j = 0; j < 2; ++j) {
+            const int sb = 2 * j + half;
             if (sb > tb) continue;
             bf16x8 w[3];
 #pragma unroll
@@ -612,25 +610,23 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             for (int x = 2; x >= 0; --x)
 #pragma unroll
                 for (int y = 0; y <= x; ++y) {
-                    x2[sb] = mfma(r[y], w[x - y], x2[sb]);
-                    if (y < NO) x1[sb] = mfma(o[y], w[x - y], x1[sb]);
+                    x2[j] = mfma(r[y], w[x - y], x2[j]);
+                    if (y < NO) x1[j] = mfma(o[y], w[x - y], x1[j]);
                 }
         }
     }
+    if (NK != 1) fetch_kq();   // (fp32: no registers for them before)
     lds_barrier();
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) sd += __shfl_xor(sd, o, 64);
     if (lane == 0) sm.sd[wave] = sd;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int o = 1; o < 8; o <<= 1) rv[i] += __shfl_xor(rv[i], o, 64);
-        if ((tid & 7) == 0) sm.rv[(tid >> 3) + 32 * i] = rv[i];
-    }
+    for (int o = 1; o < 8; o <<= 1) rv += __shfl_xor(rv, o, 64);
+    if ((tid & 7) == 0) sm.rv[pr] = rv;
     // K and Q over what the steps used
 #pragma unroll
-    for (int i = 0; i < NP / 32; ++i) {
-        const int id = tid + 256 * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
+    for (int i = 0; i < NP / 64; ++i) {
+        const int id = tid + kGradThreads * i, r = id / (NP / 8), n0 = 8 * (id % (NP / 8));
         stage8(sm.m.K[0][r], kC * kRow, n0, fk[i]);
         stage8(sm.m.Q[0][r], kC * kRow, n0, fq[i]);
     }
@@ -642,10 +638,10 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     const f32x4 beta = *reinterpret_cast<const f32x4*>(rec + GradRec::beta + 4 * (16 * tb + 4 * lg));
     double aq[4] = {}, ak[4] = {}, bk[4] = {};
 #pragma unroll
-    for (int i = 0; i < NB; ++i)
+    for (int i = 0; i < NH; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const int r = 16 * tb + 4 * lg + q, n = 16 * i + li;
+            const int r = 16 * tb + 4 * lg + q, n = 16 * (half * NH + i) + li;
             float kv = 0.0f, qv = 0.0f;
 #pragma unroll
             for (int x = NK - 1; x >= 0; --x) {
@@ -662,9 +658,9 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     // ---- pairs: X, E and the sums of Z
     double row[4] = {}, rb[4] = {};
 #pragma unroll
-    for (int sb = 0; sb < 4; ++sb) {
+    for (int j = 0; j < 2; ++j) {
         float xv[4] = {}, ev[4] = {};
-        const int s = 16 * sb + li;
+        const int sb = 2 * j + half, s = 16 * sb + li;
         if (sb <= tb) {
             f32x4 kk = z4;
 #pragma unroll
@@ -684,11 +680,11 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
                 const int t = 16 * tb + 4 * lg + q;
                 const float g = s <= t ? exp_f32((float)(sm.cum[t] - cs)) : 0.0f;
                 const float gl = s < t ? g : 0.0f;
-                const float e0 = -x2[sb][q] * gl;             // E without beta
-                xv[q] = a.scale * x1[sb][q] * g;
+                const float e0 = -x2[j][q] * gl;             // E without beta
+                xv[q] = a.scale * x1[j][q] * g;
                 ev[q] = beta[q] * e0;
                 const double ekk = (double)e0 * kk[q];
-                const double zv = (s < t ? (double)a.scale * x1[sb][q] * am[sb][q] : 0.0) + beta[q] * ekk;
+                const double zv = (s < t ? (double)a.scale * x1[j][q] * am[j][q] : 0.0) + beta[q] * ekk;
                 rb[q] += ekk;
                 row[q] += zv;
                 cz += zv;
@@ -723,15 +719,14 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
         row[q] = sum16(row[q]);
         rb[q] = sum16(rb[q]);
         if (li == 0) {
-            sm.up[t] = row[q] + gam[q] * (a.scale * aq[q] - beta[q] * ak[q]);
-            sm.down[t] = tail[q] * bk[q];
-            if (t < inside)
-                ba.dbeta[(b * a.L + t0 + t) * a.H + h] = t < live ? (float)(sm.rv[t] - gam[q] * ak[q] + rb[q]) : 0.0f;
+            sm.up(t)[half] = row[q] + gam[q] * (a.scale * aq[q] - beta[q] * ak[q]);
+            sm.down(t)[half] = tail[q] * bk[q];
+            sm.db(t)[half] = rb[q] - gam[q] * ak[q];
         }
     }
     __syncthreads();
-    if (wave == 0) {   // dg: lane = token
-        double up = sm.up[lane], down = sm.down[lane];
+    if (wave == 0) {   // dg and dbeta: lane = token
+        double up = sm.up(lane)[0] + sm.up(lane)[1], down = sm.down(lane)[0] + sm.down(lane)[1];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (i >= lane / 16) up -= sm.col[i][lane];
@@ -742,10 +737,12 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             if (lane + o < 64) up += u;
             if (lane >= o) down += d;
         }
-        const double last = reinterpret_cast<const float*>(rec + GradRec::gam)[kC - 1] * ((sm.sd[0] + sm.sd[1]) + (sm.sd[2] + sm.sd[3]));
+        const double last = reinterpret_cast<const float*>(rec + GradRec::gam)[kC - 1] *
+                            (((sm.sd[0] + sm.sd[1]) + (sm.sd[2] + sm.sd[3])) + ((sm.sd[4] + sm.sd[5]) + (sm.sd[6] + sm.sd[7])));
         if (lane < inside) {
             // a decay that is zero has no gradient; the sums would leave their rounding
             const int64_t gi = (b * a.L + t0 + lane) * a.H + h;
+            ba.dbeta[gi] = lane < live ? (float)(sm.rv[lane] + (sm.db(lane)[0] + sm.db(lane)[1])) : 0.0f;
             ba.dg[gi] = lane < live && exp_f32(a.g[gi]) != 0.0f ? (float)(up + (down - own) + last) : 0.0f;
         }
     }
@@ -766,17 +763,18 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
             }
         }
 #pragma unroll
-        for (int i = 0; i < NB; ++i) {
+        for (int i = 0; i < NH; ++i) {
+            const int n0 = 16 * (half * NH + i);
             bf16x8 k[NK], q[NK];
 #pragma unroll
-            for (int p = 0; p < NK; ++p) k[p] = ld_down(&sm.m.K[p][0][0], kRow, 32 * ks, 16 * i, lane);
+            for (int p = 0; p < NK; ++p) k[p] = ld_down(&sm.m.K[p][0][0], kRow, 32 * ks, n0, lane);
             if (lo) {
                 q1[i] = mm<LB>(x, k, q1[i]);
                 k3[i] = mm<LB>(e, k, k3[i]);
             }
             if (hi) {
 #pragma unroll
-                for (int p = 0; p < NK; ++p) q[p] = ld_down(&sm.m.Q[p][0][0], kRow, 32 * ks, 16 * i, lane);
+                for (int p = 0; p < NK; ++p) q[p] = ld_down(&sm.m.Q[p][0][0], kRow, 32 * ks, n0, lane);
                 k3[i] = mm<LB>(et, k, k3[i]);
                 k3[i] = mm<LB>(xt, q, k3[i]);
             }
@@ -784,11 +782,12 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
     }
     // rows through LDS (over K and Q), out 32 bytes or more a lane
     lds_barrier();
-    float (&out)[16][NP + 4] = *reinterpret_cast<float (*)[16][NP + 4]>(&sm.m.K[0][0][0] + wave * (2 * 16 * (NP + 4)));
-    static_assert(4 * 16 * (NP + 4) * 4 <= (int)sizeof(sm.m.K) + (int)sizeof(sm.m.Q), "the waves' rows fit over K and Q");
-    auto put_rows = [&](const f32x4 (&v)[NB], void* to, float* part) {
+    constexpr int NW = NP / 2, nr = NW + 4;
+    float (&out)[16][nr] = *reinterpret_cast<float (*)[16][nr]>(&sm.m.K[0][0][0] + wave * (2 * 16 * nr));
+    static_assert(8 * 16 * nr * 4 <= (int)sizeof(sm.m.K) + (int)sizeof(sm.m.Q), "the waves' rows fit over K and Q");
+    auto put_rows = [&](const f32x4 (&v)[NH], void* to, float* part) {
 #pragma unroll
-        for (int i = 0; i < NB; ++i)
+        for (int i = 0; i < NH; ++i)
 #pragma unroll
             for (int q = 0; q < 4; ++q) out[4 * lg + q][16 * i + li] = v[i][q];
         wave_sync();
@@ -796,14 +795,14 @@ __global__ __launch_bounds__(256) void delta_grad_kernel(DeltaBwdArgs ba, int64_
         const bool wide = shared_qk ? N % 8 == 0 : ba.vec_g;
         auto each = [&](auto* first, int64_t stride) {   // row r at first + r stride
             if (wide) {
-                for (int id = lane; id < 2 * NP; id += 64) {
-                    const int r = id / (NP / 8), n = 8 * (id % (NP / 8));
-                    if (r < rows && n < N) io::st8(first + r * stride + n, &out[r][n]);
+                for (int id = lane; id < 2 * NW; id += 64) {
+                    const int r = id / (NW / 8), m = 8 * (id % (NW / 8)), n = half * NW + m;
+                    if (r < rows && n < N) io::st8(first + r * stride + n, &out[r][m]);
                 }
             } else {
-                for (int id = lane; id < 16 * NP; id += 64) {
-                    const int r = id / NP, n = id % NP;
-                    if (r < rows && n < N) io::st(first + r * stride + n, out[r][n]);
+                for (int id = lane; id < 16 * NW; id += 64) {
+                    const int r = id / NW, m = id % NW, n = half * NW + m;
+                    if (r < rows && n < N) io::st(first + r * stride + n, out[r][m]);
                 }
             }
         };
@@ -878,7 +877,7 @@ hipError_t launch(const DeltaBwdArgs& a, hipStream_t stream) {
         static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
         if ((e = lds(kern, bytes)) != hipSuccess) return e;
         KTime kt("delta_grad", stream);
-        hipLaunchKernelGGL(kern, dim3((unsigned)(f.batch * f.H * nch)), dim3(256), bytes, stream, a, nch);
+        hipLaunchKernelGGL(kern, dim3((unsigned)(f.batch * f.H * nch)), dim3(kGradThreads), bytes, stream, a, nch);
     }
     if (a.pq) {
         KTime kt("delta_group", stream);
