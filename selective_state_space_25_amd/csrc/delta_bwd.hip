@@ -421,9 +421,21 @@ __device__ __forceinline__ f32x4 widen(const Raw4<uint16_t>& r) {
 }
 __device__ __forceinline__ f32x4 widen(const Raw4<float>& r) { return r.v; }
 
+// The value of the lane that a data-parallel move names.
+template <int CTRL>
+__device__ __forceinline__ double moved(double v) {
+    const uint64_t w = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)w, CTRL, 0xf, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(w >> 32), CTRL, 0xf, 0xf, true);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+// Sum over 16 lanes, in every one of them: over pairs, pairs of pairs (lanes
+// exchanged within four), the halves of eight and of sixteen (mirrored).
 __device__ __forceinline__ double sum16(double v) {
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) v += __shfl_xor(v, o, 64);
+    v += moved<0xB1>(v);
+    v += moved<0x4E>(v);
+    v += moved<0x141>(v);
+    v += moved<0x140>(v);
     return v;
 }
 
