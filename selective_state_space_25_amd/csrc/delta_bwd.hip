@@ -628,9 +628,17 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs b
         }
     }
     if (NK != 1) fetch_kq();   // (fp32: no registers for them before)
+    // (asked for here, used after the next barrier)
+    const f32x4 gam = *reinterpret_cast<const f32x4*>(rec + GradRec::gam + 4 * (16 * tb + 4 * lg));
+    const f32x4 tail = *reinterpret_cast<const f32x4*>(rec + GradRec::tail + 4 * (16 * tb + 4 * lg));
+    const f32x4 beta = *reinterpret_cast<const f32x4*>(rec + GradRec::beta + 4 * (16 * tb + 4 * lg));
+    const int64_t gi = (b * a.L + t0 + lane) * a.H + h;
+    const float gown = wave == 0 && lane < inside ? a.g[gi] : 0.0f;
+    const float glast = reinterpret_cast<const float*>(rec + GradRec::gam)[kC - 1];
     lds_barrier();
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) sd += __shfl_xor(sd, o, 64);
+    sd = sum16(sd);
+    sd += __shfl_xor(sd, 16, 64);
+    sd += __shfl_xor(sd, 32, 64);
     if (lane == 0) sm.sd[wave] = sd;
 #pragma unroll
     for (int o = 1; o < 8; o <<= 1) rv += __shfl_xor(rv, o, 64);
@@ -645,9 +653,6 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs b
     __syncthreads();
 
     // ---- the dots with q and k; dQ and dK from the states
-    const f32x4 gam = *reinterpret_cast<const f32x4*>(rec + GradRec::gam + 4 * (16 * tb + 4 * lg));
-    const f32x4 tail = *reinterpret_cast<const f32x4*>(rec + GradRec::tail + 4 * (16 * tb + 4 * lg));
-    const f32x4 beta = *reinterpret_cast<const f32x4*>(rec + GradRec::beta + 4 * (16 * tb + 4 * lg));
     double aq[4] = {}, ak[4] = {}, bk[4] = {};
 #pragma unroll
     for (int i = 0; i < NH; ++i)
@@ -749,13 +754,12 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs b
             if (lane + o < 64) up += u;
             if (lane >= o) down += d;
         }
-        const double last = reinterpret_cast<const float*>(rec + GradRec::gam)[kC - 1] *
+        const double last = glast *
                             (((sm.sd[0] + sm.sd[1]) + (sm.sd[2] + sm.sd[3])) + ((sm.sd[4] + sm.sd[5]) + (sm.sd[6] + sm.sd[7])));
         if (lane < inside) {
             // a decay that is zero has no gradient; the sums would leave their rounding
-            const int64_t gi = (b * a.L + t0 + lane) * a.H + h;
             ba.dbeta[gi] = lane < live ? (float)(sm.rv[lane] + (sm.db(lane)[0] + sm.db(lane)[1])) : 0.0f;
-            ba.dg[gi] = lane < live && exp_f32(a.g[gi]) != 0.0f ? (float)(up + (down - own) + last) : 0.0f;
+            ba.dg[gi] = lane < live && exp_f32(gown) != 0.0f ? (float)(up + (down - own) + last) : 0.0f;
         }
     }
     // ---- dQ += X K;  dK += X^T Q + E K + E^T K
