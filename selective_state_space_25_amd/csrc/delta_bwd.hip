@@ -28,10 +28,12 @@
 // near 2^-16 of the term under the 2^-9 of the gradient's own rounding.
 //
 // Measured at batch 4, 16 heads of 128 x 128, L 2048, bf16: records 40 us,
-// kept scan 94, scan back 152 (0.39 GB, 2.6 TB/s: a chain of three products a
-// chunk, 4.7 us), gradients 252 (0.5 GB, 2 TB/s: the vector ALU, a quarter of
-// the time for splitting into planes, the matrix cores, 15 %, and LDS take
-// turns, with one workgroup to a CU).
+// kept scan 94, scan back 152-163 (0.39 GB, 2.5 TB/s: a chain of three products
+// a chunk, 4.9 us), gradients 218 (0.5 GB, 2.3 TB/s).  Of a workgroup's time in
+// the last, 60 % are the steps over the value columns, at the rate of their
+// loads, 20 % the pairs and fp64 dots, 8 % the products with X and E; a CU
+// holds one such workgroup, whose LDS (92 KB) leaves no room for another to
+// load meanwhile.
 #include "delta_chunk.hpp"
 #include "host.hpp"
 

@@ -99,13 +99,6 @@ struct Chunks {
     __device__ __forceinline__ int rows(int c) const { return c + 1 < n ? kC : c + 1 == n ? last : 0; }
 };
 
-template <typename T> __device__ __forceinline__ float buf_ld(__amdgpu_buffer_rsrc_t r, int off);
-template <> __device__ __forceinline__ float buf_ld<float>(__amdgpu_buffer_rsrc_t r, int off) {
-    return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-}
-template <> __device__ __forceinline__ float buf_ld<uint16_t>(__amdgpu_buffer_rsrc_t r, int off) {
-    return bf16_to_f32(__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0));
-}
 // One element as loaded; widen it when it is used, not before: widening
 // waits for the load.
 template <typename T> __device__ __forceinline__ T buf_raw(__amdgpu_buffer_rsrc_t r, int off);
@@ -156,13 +149,6 @@ __device__ __forceinline__ void to_operand(const Raw8<uint16_t>& r, bf16x8 (&p)[
 }
 __device__ __forceinline__ void to_operand(const Raw8<float>& r, bf16x8 (&p)[3]) { split8<3>(r.lo, r.hi, p); }
 
-// Tile k of the 10 lower tiles: row block tb, column block sb.
-__device__ __forceinline__ void lower_tile(int k, int& tb, int& sb) {
-    tb = k >= 6 ? 3 : k >= 3 ? 2 : k >= 1 ? 1 : 0;
-    sb = k - tb * (tb + 1) / 2;
-}
-
-__device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[1]) { return v[0]; }
 __device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[2]) { return v[0] + v[1]; }
 __device__ __forceinline__ f32x4 sum_of(const f32x4 (&v)[4]) { return (v[0] + v[1]) + (v[2] + v[3]); }
 
