@@ -24,7 +24,10 @@
 // 1.6 us a chunk (one wave to a column block: 1830 us; four that share its
 // products: 730 us); 256 heads of 64 x 128, L 4096, fp32 y: 418 us, 0.95 GB of
 // inputs, records and y.  The matrix cores are busy for 11 and 28 % of it.
-// T staged in LDS by the helpers was slower, a raised wave priority no faster.
+// A chunk's 3850 cycles in the first: K S 1150 and 220 at the barrier, T R
+// 730-1080 (by row block) and 200-600, K^T W 800 and 360.  T staged in LDS by
+// the helpers was slower; a raised wave priority, and Q S, staging and A U one
+// phase earlier, were no faster.
 //
 // Products are fp32-grade (split_mfma.hpp).  Where inputs and y are bf16, A
 // and U take two planes in A U, an error near 2^-17 of that term under the
