@@ -448,3 +448,18 @@ def test_bwd_past_32_bits(gpu):
     torch.cuda.synchronize()
     for n in want:
         close(got[n][B - 1:], host(want[n]).double().numpy(), n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("shape", [(2, 70, 4, 2, 64, 128), (1, 100, 2, 2, 24, 40)])
+def test_bwd_unaligned(gpu, dtype, shape):
+    """Every tensor one element off a 16-byte boundary."""
+    B, L, H, G, P, N = shape
+    i = inputs(*shape, dtype, seed=80, h0=True)
+    dout, dlast = douts(B, L, H, P, N, dtype, 80)
+
+    def shifted(t):
+        v = torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:].view(t.shape)
+        return v.copy_(t)
+
+    check_grads(*grads({n: shifted(x) for n, x in i.items()}, shifted(dout), shifted(dlast)))
