@@ -406,7 +406,7 @@ hipError_t launch(const DeltaArgs& a, const char* recs, float* keep_s, float* ke
     // 4096, f32 y: 423 us against 531; the scan of the gradients at batch 4,
     // 16 heads of 128 x 128, L 2048: 94 against 107), not where CUs would
     // idle (batch 1, 16 heads of 128 x 128, L 16384: 579 us against 397).
-    // float32 inputs: two blocks' LDS would leave room for one workgroup.
+    // float32 inputs: K's planes and two blocks do not fit a CU's LDS.
     if constexpr (sizeof(Tin) == 2) {
         const int64_t blocks = ((KEEP ? pad : a.P) + 31) / 32;
         if (a.P > 16 && a.batch * a.H * blocks >= host::device_cus())
