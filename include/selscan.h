@@ -380,8 +380,8 @@ selscan_status_t selscan_conv1d(const selscan_conv_shape_t* shape, const void* x
  * y of its chunk and head, and what follows.
  *
  * Workspace as for the other entry points, sized by
- * selscan_delta_workspace_bytes: per head and 64 tokens 27 KB (32 KB for fp32
- * y), and where N is no multiple of 8 padded copies of q and k (which are
+ * selscan_delta_workspace_bytes: per head and 64 tokens 32 KB, and where N is
+ * no multiple of 8 padded copies of q and k (which are
  * allocated on `stream` by the call itself where only their addresses are off
  * a 16-byte boundary).
  */

@@ -60,8 +60,7 @@ size_t pad_bytes(const selscan_m2_shape_t* s) {
 }
 
 size_t record_bytes(const selscan_m2_shape_t* s) {
-    return align256((size_t)(s->batch * s->nheads * selscan::delta_chunks(s->seqlen)) * 
-                    selscan::delta_record_bytes(selscan::delta_a_planes(s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16), false));
+    return align256((size_t)(s->batch * s->nheads * selscan::delta_chunks(s->seqlen)) * selscan::delta_record_bytes(false));
 }
 
 size_t fwd_bytes(const selscan_m2_shape_t* s) {
@@ -146,7 +145,7 @@ selscan_status_t selscan_delta_fwd(const selscan_m2_shape_t* s, const void* q, c
         char* recs = static_cast<char*>(ws.ptr);
         st = pad_rows(a, s, recs + record_bytes(s), pad, hs);
         hipError_t e = hipSuccess;
-        if (st == SELSCAN_OK) e = selscan::launch_delta_prep(a, in_bf16, selscan::delta_a_planes(in_bf16, out_bf16), false, recs, hs);
+        if (st == SELSCAN_OK) e = selscan::launch_delta_prep(a, in_bf16, false, recs, hs);
         if (st == SELSCAN_OK && e == hipSuccess) e = selscan::launch_delta_scan(a, in_bf16, out_bf16, recs, hs);
         pad.release();
         ws.release();

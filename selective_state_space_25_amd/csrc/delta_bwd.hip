@@ -874,7 +874,7 @@ template <typename Tin, typename Tdo, int NP>
 hipError_t launch(const DeltaBwdArgs& a, hipStream_t stream) {
     const DeltaArgs& f = a.f;
     const int64_t nch = delta_chunks(f.L);
-    hipError_t e = launch_delta_prep(f, sizeof(Tin) == 2, 3, true, a.recs, stream);
+    hipError_t e = launch_delta_prep(f, sizeof(Tin) == 2, true, a.recs, stream);
     if (e != hipSuccess) return e;
     e = launch_delta_keep(f, sizeof(Tin) == 2, a.recs, a.S, a.U, a.pad, stream);
     if (e != hipSuccess) return e;
@@ -917,7 +917,7 @@ struct Sizes {
 Sizes sizes(int64_t batch, int64_t L, int64_t H, int64_t G, int64_t P, int64_t N) {
     const size_t chunks = (size_t)(batch * H * delta_chunks(L)), pad = (size_t)(P + 31) / 32 * 32;
     auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
-    return {up(chunks * delta_record_bytes(3, true)), up(chunks * pad * (N <= 64 ? 64 : 128) * 4), up(chunks * kC * pad * 4),
+    return {up(chunks * delta_record_bytes(true)), up(chunks * pad * (N <= 64 ? 64 : 128) * 4), up(chunks * kC * pad * 4),
             H > G ? up((size_t)(batch * L * H * N) * 4) : 0};
 }
 

@@ -15,16 +15,16 @@ constexpr int kC = 64;             // tokens per chunk
 constexpr int kBlocks = 10;        // 16 x 16 blocks on and below a chunk matrix's diagonal
 
 // Record of one (batch, head, chunk), byte offsets.  T in three bf16 planes,
-// each 10 row-major 16 x 16 blocks (block (t, s) at t (t + 1) / 2 + s); A in
-// OL planes; then per token e^cum, e^(last - cum), beta (zero past the
-// sequence's end) and cum itself as doubles.  For the gradients A is fp32,
-// and T's and A's blocks follow in three planes, each block transposed.
+// each 10 row-major 16 x 16 blocks (block (t, s) at t (t + 1) / 2 + s); A the
+// same; then per token e^cum, e^(last - cum), beta (zero past the sequence's
+// end) and cum itself as doubles.  For the gradients A is fp32, and T's and
+// A's blocks follow in three planes, each block transposed.
 constexpr int kPlane = kBlocks * 512;
-template <int OL, bool GRAD>
+template <bool GRAD>
 struct Rec {
     static constexpr int T = 0;
     static constexpr int A = 3 * kPlane;
-    static constexpr int gam = A + (GRAD ? 2 : OL) * kPlane;   // (fp32 takes the place of two planes)
+    static constexpr int gam = A + (GRAD ? 2 : 3) * kPlane;   // (fp32 takes the place of two planes)
     static constexpr int tail = gam + 4 * kC;
     static constexpr int beta = tail + 4 * kC;
     static constexpr int cum = beta + 4 * kC;
@@ -32,7 +32,7 @@ struct Rec {
     static constexpr int At = Tt + 3 * kPlane;
     static constexpr int bytes = GRAD ? At + 3 * kPlane : Tt;
 };
-using GradRec = Rec<3, true>;
+using GradRec = Rec<true>;
 
 // A state kept for the gradients: the C tiles of its 16-column blocks one
 // after the other, as the lanes hold them (1 KB a tile).  Floats from the

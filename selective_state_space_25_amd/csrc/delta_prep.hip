@@ -17,8 +17,8 @@
 // of M it stays as exact as substitution when keys repeat.  T and A leave
 // already split into the planes that the scan multiplies with.
 //
-// What bounds it are the records (27 KB a chunk and head for a bf16 y, 32 KB
-// for fp32, 56 KB for gradients) and the inverse's chain of dependent steps:
+// What bounds it are the records (32 KB a chunk and head, 57.6 KB for the
+// gradients) and the inverse's chain of dependent steps:
 // 16 heads of 128, L 16384: 62 us, 110 MB of records and 134 MB of q and k,
 // 3.9 TB/s; 256 heads, L 4096, q and k shared by 32 of them: 165 us, 524 MB of
 // records, 3.2 TB/s.
@@ -28,7 +28,6 @@
 // decays between the tokens that follow.  g below -200 counts as -200, whose
 // exponential is zero in fp32 either way, so that a reset (-inf) stays finite.
 #include <algorithm>
-#include <type_traits>
 
 #include "delta_chunk.hpp"
 
@@ -72,11 +71,11 @@ __device__ __forceinline__ void st_block(float (&Y)[16][kRowB], f32x4 v, int li,
     for (int q = 0; q < 4; ++q) Y[4 * lg + q][li] = v[q];
 }
 
-// OL planes of A (Rec); GRAD: the gradients' record.
-template <typename Tin, int NP, int OL, bool GRAD>
+// GRAD: the gradients' record.
+template <typename Tin, int NP, bool GRAD>
 __global__ __launch_bounds__(64 * kUnits) void delta_prep_kernel(DeltaArgs a, char* recs, int64_t nch, int64_t units) {
     constexpr int NK = kPlanes<Tin>, ES = (int)sizeof(Tin);
-    using R = Rec<OL, GRAD>;
+    using R = Rec<GRAD>;
     __shared__ __attribute__((aligned(16))) PrepUnit sms[kUnits];
     PrepUnit& sm = sms[threadIdx.x >> 6];
     const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
@@ -180,21 +179,20 @@ __global__ __launch_bounds__(64 * kUnits) void delta_prep_kernel(DeltaArgs a, ch
             }
         }
     }
-    // the blocks in LDS to NPL planes, a lane eight columns of a row of a pair of blocks
+    // the blocks in LDS to planes, a lane eight columns of a row of a pair of blocks
     const int r8 = (lane & 31) >> 1, c8 = 8 * (lane & 1);
-    auto put_planes = [&](char* to, auto npl) {
-        constexpr int NPL = decltype(npl)::value;
+    auto put_planes = [&](char* to) {
 #pragma unroll
         for (int i = 0; i < kBlocks; i += 2) {
             const float* x = &sm.M[i + (lane >> 5)][r8][c8];
-            bf16x8 w[NPL];
-            split8<NPL>(*reinterpret_cast<const f32x4*>(x), *reinterpret_cast<const f32x4*>(x + 4), w);
+            bf16x8 w[3];
+            split8<3>(*reinterpret_cast<const f32x4*>(x), *reinterpret_cast<const f32x4*>(x + 4), w);
 #pragma unroll
-            for (int p = 0; p < NPL; ++p) *reinterpret_cast<bf16x8*>(to + p * kPlane + i * 512 + lane * 16) = w[p];
+            for (int p = 0; p < 3; ++p) *reinterpret_cast<bf16x8*>(to + p * kPlane + i * 512 + lane * 16) = w[p];
         }
     };
     wave_sync();
-    if constexpr (!GRAD) put_planes(rec + R::A, std::integral_constant<int, OL>{});
+    if constexpr (!GRAD) put_planes(rec + R::A);
     wave_sync();
 #pragma unroll
     for (int i = 0; i < kBlocks; ++i) st_block(sm.M[i], kk[i], li, lg);
@@ -247,7 +245,7 @@ __global__ __launch_bounds__(64 * kUnits) void delta_prep_kernel(DeltaArgs a, ch
         st_block(M(3, 1), -t31, li, lg);
     }
     wave_sync();
-    put_planes(rec + R::T, std::integral_constant<int, 3>{});
+    put_planes(rec + R::T);
     if constexpr (GRAD) {
 #pragma unroll
         for (int i = 0; i < kBlocks; i += 2) {   // row r8 of the transposed block: column r8 down
@@ -266,26 +264,23 @@ __global__ __launch_bounds__(64 * kUnits) void delta_prep_kernel(DeltaArgs a, ch
     }
 }
 
-template <typename Tin, int NP, int OL, bool GRAD>
+template <typename Tin, int NP, bool GRAD>
 hipError_t launch(const DeltaArgs& a, char* recs, hipStream_t stream) {
     const int64_t nch = delta_chunks(a.L), units = a.batch * a.H * nch;
     KTime kt("delta_prep", stream);
-    hipLaunchKernelGGL((delta_prep_kernel<Tin, NP, OL, GRAD>), dim3((unsigned)((units + kUnits - 1) / kUnits)),
+    hipLaunchKernelGGL((delta_prep_kernel<Tin, NP, GRAD>), dim3((unsigned)((units + kUnits - 1) / kUnits)),
                        dim3(64 * kUnits), 0, stream, a, recs, nch, units);
     return hipGetLastError();
 }
 
-template <typename Tin, int OL, bool GRAD>
+template <typename Tin, bool GRAD>
 hipError_t by_n(const DeltaArgs& a, char* recs, hipStream_t stream) {
-    return a.N <= 64 ? launch<Tin, 64, OL, GRAD>(a, recs, stream) : launch<Tin, 128, OL, GRAD>(a, recs, stream);
+    return a.N <= 64 ? launch<Tin, 64, GRAD>(a, recs, stream) : launch<Tin, 128, GRAD>(a, recs, stream);
 }
 
 template <typename Tin>
-hipError_t by_use(const DeltaArgs& a, int planes, bool grad, char* recs, hipStream_t stream) {
-    if (grad) return by_n<Tin, 3, true>(a, recs, stream);
-    if constexpr (sizeof(Tin) == 2)
-        if (planes == 2) return by_n<Tin, 2, false>(a, recs, stream);
-    return by_n<Tin, 3, false>(a, recs, stream);
+hipError_t by_use(const DeltaArgs& a, bool grad, char* recs, hipStream_t stream) {
+    return grad ? by_n<Tin, true>(a, recs, stream) : by_n<Tin, false>(a, recs, stream);
 }
 
 // Rows of N elements, one after the other, to rows of `to`, zeros past N.
@@ -302,9 +297,7 @@ __global__ __launch_bounds__(256) void delta_pad_kernel(const T* q, const T* k, 
 }  // namespace
 
 int64_t delta_chunks(int64_t L) { return (L + dchunk::kC - 1) / dchunk::kC; }
-size_t delta_record_bytes(int planes, bool grad) {
-    return grad ? dchunk::GradRec::bytes : planes == 2 ? dchunk::Rec<2, false>::bytes : dchunk::Rec<3, false>::bytes;
-}
+size_t delta_record_bytes(bool grad) { return grad ? dchunk::GradRec::bytes : dchunk::Rec<false>::bytes; }
 
 hipError_t launch_delta_pad(DeltaArgs& a, int in_bf16, void* rows, hipStream_t stream) {
     const int to = a.N <= 64 ? 64 : 128;
@@ -326,8 +319,8 @@ hipError_t launch_delta_pad(DeltaArgs& a, int in_bf16, void* rows, hipStream_t s
     return hipGetLastError();
 }
 
-hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, int planes, bool grad, char* recs, hipStream_t stream) {
-    return in_bf16 ? by_use<uint16_t>(a, planes, grad, recs, stream) : by_use<float>(a, planes, grad, recs, stream);
+hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, bool grad, char* recs, hipStream_t stream) {
+    return in_bf16 ? by_use<uint16_t>(a, grad, recs, stream) : by_use<float>(a, grad, recs, stream);
 }
 
 }  // namespace selscan

@@ -29,9 +29,8 @@
 // the helpers was slower; a raised wave priority, and Q S, staging and A U one
 // phase earlier, were no faster.
 //
-// Products are fp32-grade (split_mfma.hpp).  Where inputs and y are bf16, A
-// and U take two planes in A U, an error near 2^-17 of that term under the
-// 2^-9 of y's own rounding.
+// Products are fp32-grade (split_mfma.hpp) whatever y's type: a bf16 y is the
+// rounding of the fp32 one.
 #include "delta_chunk.hpp"
 #include "host.hpp"
 
@@ -43,8 +42,8 @@ using namespace dchunk;
 
 constexpr int kThreads = 512;
 
-// OL: planes of A and U in y; 0 = no y.
-template <typename Tin, int NP, int CT, int OL>
+// KEEP: no y, and U has no second reader.
+template <typename Tin, int NP, int CT, bool KEEP>
 struct ScanSmem {
     static constexpr int kRow = NP + 8;
     float gam[kC], tail[kC], beta[kC];
@@ -52,7 +51,7 @@ struct ScanSmem {
     uint16_t K[2][kPlanes<Tin>][kC][kRow];   // by chunk parity
     Operands<NP / 32, 3> S[CT];
     Operands<2, 3> R[CT], W[CT];             // R; e^(last - cum) U
-    Operands<2, OL ? OL : 1> U[CT];
+    Operands<2, KEEP ? 1 : 3> U[CT];
 };
 
 // KEEP: instead of y, the state entering each chunk (kept_tile) and U
@@ -61,17 +60,15 @@ struct ScanSmem {
 template <typename Tin, typename Tout, int NP, int CT, bool KEEP>
 __global__ __launch_bounds__(kThreads, CT == 1 && sizeof(Tin) == 2 && (KEEP || sizeof(Tout) == 2) ? 4 : 2)
 void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, float* keep_s, float* keep_u, int pad) {
-    constexpr int OL = KEEP ? 0 : delta_a_planes(sizeof(Tin) == 2, sizeof(Tout) == 2);
-    constexpr int OA = OL ? OL : 1;
-    constexpr int NK = kPlanes<Tin>;
+    constexpr int NK = kPlanes<Tin>, NU = KEEP ? 1 : 3;
     constexpr int ES = (int)sizeof(Tin), EO = (int)sizeof(Tout);
-    constexpr int kRow = ScanSmem<Tin, NP, CT, OL>::kRow;
+    constexpr int kRow = ScanSmem<Tin, NP, CT, KEEP>::kRow;
     constexpr int KS = NP / 32;              // k-steps over the key dimension
     constexpr int NT = NP / 64;              // state tiles per state wave
     constexpr int NPC = NP / 32;             // 8-element pieces of K per helper thread
-    using Rc = Rec<KEEP ? 3 : OA, KEEP>;
+    using Rc = Rec<KEEP>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
-    auto& sm = *reinterpret_cast<ScanSmem<Tin, NP, CT, OL>*>(smem_raw);
+    auto& sm = *reinterpret_cast<ScanSmem<Tin, NP, CT, KEEP>*>(smem_raw);
     const int tid = threadIdx.x & 255, lane = tid & 63, li = lane & 15, lg = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool helper = __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) != 0;
@@ -200,7 +197,7 @@ void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, floa
                         k[i][l] = ld_down(K + l * kC * kRow, kRow, 32 * (i & 1), 16 * (NT * w + i / 2), lane);
             };
             // before the barrier that it does not need, where registers allow
-            if constexpr (OL != 3) load_kt();
+            if constexpr (KEEP) load_kt();
             if constexpr (KEEP) {
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
@@ -211,7 +208,7 @@ void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, floa
             }
             lds_barrier();
             // the wave's rows of the next state
-            if constexpr (OL == 3) load_kt();
+            if constexpr (!KEEP) load_kt();
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 bf16x8 x[2][3];
@@ -261,7 +258,7 @@ void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, floa
         voff[ct] = p < P ? (16 * w + 4 * lg) * sv + p * ES : kOut;
     }
     Raw8<Tin> fk[NPC], fq[KS];
-    bf16x8 fa[2][OA];
+    bf16x8 fa[2][NU];
     f32x4 fgam;
     auto fetch_k = [&](int c) {
         const auto kb = chunk_rows(Kg, sk, c, a.NL * ES);
@@ -279,7 +276,7 @@ void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, floa
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-            for (int x = 0; x < OA; ++x) fa[ks][x] = buf_op(rb, toff[ks] + Rc::A + x * kPlane);
+            for (int x = 0; x < NU; ++x) fa[ks][x] = buf_op(rb, toff[ks] + Rc::A + x * kPlane);
     };
     f32x4 fgate;
     Tin fv[CT][4];
@@ -307,15 +304,12 @@ void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, floa
     auto finish_y = [&](int c, f32x4 (&y)[CT]) {
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
-            bf16x8 x[2][OA];
-            sm.U[ct].get(0, lane, x[0]);
-            if (w < 2) {
-                y[ct] = mm<3>(fa[0], x[0], y[ct]);
-            } else {
-                sm.U[ct].get(1, lane, x[1]);
-                f32x4 acc[2] = {y[ct], z4};
-                mm_turns<3, OA, OA>([&](int m) { return fa[m]; }, [&](int m) { return x[m]; }, acc);
-                y[ct] = sum_of(acc);
+            bf16x8 x[NU];
+            sm.U[ct].get(0, lane, x);
+            y[ct] = mm<3>(fa[0], x, y[ct]);
+            if (w >= 2) {
+                sm.U[ct].get(1, lane, x);
+                y[ct] = mm<3>(fa[1], x, y[ct]);
             }
         }
         fetch_a(c + 1);
@@ -385,7 +379,7 @@ void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, floa
 
 template <typename Tin, typename Tout, int NP, int CT, bool KEEP>
 hipError_t launch_ct(const DeltaArgs& a, const char* recs, float* keep_s, float* keep_u, int pad, hipStream_t stream) {
-    constexpr int bytes = (int)sizeof(ScanSmem<Tin, NP, CT, KEEP ? 0 : delta_a_planes(sizeof(Tin) == 2, sizeof(Tout) == 2)>);
+    constexpr int bytes = (int)sizeof(ScanSmem<Tin, NP, CT, KEEP>);
     static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
     const int npb = (int)(((KEEP ? pad : a.P) + 16 * CT - 1) / (16 * CT));
     const int64_t units = (a.batch * a.H + 7) / 8 * 8;

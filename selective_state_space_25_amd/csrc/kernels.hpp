@@ -224,11 +224,9 @@ hipError_t launch_delta_rec(const DeltaArgs& a, int in_bf16, int out_bf16, hipSt
 // k that are not made of aligned 16-byte pieces are copied first, padded to
 // 64 or 128 elements (2 batch L G of them in `rows`; a is set to the copies).
 int64_t delta_chunks(int64_t L);
-size_t delta_record_bytes(int planes, bool grad);
-// Planes of A: two where y is the rounding to bf16 of sums over bf16 inputs.
-constexpr int delta_a_planes(bool in_bf16, bool out_bf16) { return in_bf16 && out_bf16 ? 2 : 3; }
+size_t delta_record_bytes(bool grad);
 hipError_t launch_delta_pad(DeltaArgs& a, int in_bf16, void* rows, hipStream_t stream);
-hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, int planes, bool grad, char* recs, hipStream_t stream);
+hipError_t launch_delta_prep(const DeltaArgs& a, int in_bf16, bool grad, char* recs, hipStream_t stream);
 hipError_t launch_delta_scan(const DeltaArgs& a, int in_bf16, int out_bf16, const char* recs, hipStream_t stream);
 
 // Gradients of the gated delta rule; the arrays below dh0 are workspace
