@@ -23,9 +23,8 @@
 // and U (delta_scan.hip), the scan back over the chunks that makes D, dR and
 // dV (16 or 32 value columns a workgroup), the gradients that are local to a
 // chunk (all chunks at once), and, where heads share q and k, their sum over
-// the heads in a fixed order.  All products are fp32-grade except those that
-// go into a bf16 dq or dk alone, which keep plane pairs a + b < 2, an error
-// near 2^-16 of the term under the 2^-9 of the gradient's own rounding.
+// the heads in a fixed order.  All products are fp32-grade, whatever the
+// inputs' type: bf16 gradients are the fp32 ones rounded.
 //
 // Measured at batch 4, 16 heads of 128 x 128, L 2048, bf16: records 40 us,
 // kept scan 94, scan back 152-163 (0.39 GB, 2.5 TB/s: a chain of three products
@@ -368,7 +367,7 @@ constexpr int kPb = 32;            // value columns per step of the sums over p
 constexpr int kRowP = kPb + 8;
 constexpr int kRowX = kC + 8;
 
-template <typename Tin, typename Tdo, int NP, int LB>
+template <typename Tin, typename Tdo, int NP>
 struct GradSmem {
     static constexpr int kRow = NP + 8;
     double cum[kC];
@@ -383,7 +382,7 @@ struct GradSmem {
         } s;
         struct {                   // the chunk's pairs
             uint16_t K[kPlanes<Tin>][kC][kRow], Q[kPlanes<Tin>][kC][kRow];
-            uint16_t X[LB][kC][kRowX], E[LB][kC][kRowX];
+            uint16_t X[3][kC][kRowX], E[3][kC][kRowX];
         } m;
     };
     // A half's sums for token t, in the padding of its rows of X and E:
@@ -455,8 +454,7 @@ __device__ __forceinline__ void stage4(uint16_t* row, int ps, const Raw4<float>&
 template <typename Tin, typename Tdo, int NP>
 __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs ba, int64_t nch) {
     constexpr int NK = kPlanes<Tin>, NO = kPlanes<Tdo>;
-    constexpr int LB = NK == 1 ? 2 : 3;      // plane pairs of what goes into dq and dk alone
-    using Smem = GradSmem<Tin, Tdo, NP, LB>;
+    using Smem = GradSmem<Tin, Tdo, NP>;
     constexpr int kRow = Smem::kRow;
     constexpr int NB = NP / 16, NH = NB / 2;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
@@ -719,7 +717,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs b
                 const int t = 16 * tb + 4 * lg + q;
                 float x = xv[q], e = ev[q];
 #pragma unroll
-                for (int l = 0; l < LB; ++l) {
+                for (int l = 0; l < 3; ++l) {
                     const uint16_t xh = f32_to_bf16(x), eh = f32_to_bf16(e);
                     sm.m.X[l][t][s] = xh;
                     sm.m.E[l][t][s] = eh;
@@ -768,9 +766,9 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs b
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
         const bool lo = ks <= tb / 2, hi = ks >= tb / 2;   // rows of X and E; their columns
-        bf16x8 x[LB], e[LB], xt[LB], et[LB];
+        bf16x8 x[3], e[3], xt[3], et[3];
 #pragma unroll
-        for (int l = 0; l < LB; ++l) {
+        for (int l = 0; l < 3; ++l) {
             if (lo) {
                 x[l] = ld8(&sm.m.X[l][16 * tb + li][32 * ks + 8 * lg]);
                 e[l] = ld8(&sm.m.E[l][16 * tb + li][32 * ks + 8 * lg]);
@@ -787,14 +785,14 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs b
 #pragma unroll
             for (int p = 0; p < NK; ++p) k[p] = ld_down(&sm.m.K[p][0][0], kRow, 32 * ks, n0, lane);
             if (lo) {
-                q1[i] = mm<LB>(x, k, q1[i]);
-                k3[i] = mm<LB>(e, k, k3[i]);
+                q1[i] = mm<3>(x, k, q1[i]);
+                k3[i] = mm<3>(e, k, k3[i]);
             }
             if (hi) {
 #pragma unroll
                 for (int p = 0; p < NK; ++p) q[p] = ld_down(&sm.m.Q[p][0][0], kRow, 32 * ks, n0, lane);
-                k3[i] = mm<LB>(et, k, k3[i]);
-                k3[i] = mm<LB>(xt, q, k3[i]);
+                k3[i] = mm<3>(et, k, k3[i]);
+                k3[i] = mm<3>(xt, q, k3[i]);
             }
         }
     }
@@ -891,7 +889,7 @@ hipError_t launch(const DeltaBwdArgs& a, hipStream_t stream) {
     if (e != hipSuccess) return e;
     {
         const auto kern = &delta_grad_kernel<Tin, Tdo, NP>;
-        constexpr int bytes = (int)sizeof(GradSmem<Tin, Tdo, NP, kPlanes<Tin> == 1 ? 2 : 3>);
+        constexpr int bytes = (int)sizeof(GradSmem<Tin, Tdo, NP>);
         static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
         if ((e = lds(kern, bytes)) != hipSuccess) return e;
         KTime kt("delta_grad", stream);
