@@ -314,10 +314,12 @@ void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, floa
         }
         fetch_a(c + 1);
         const auto yb = rows_buf(Yg + (int64_t)c * kC * sy, all.rows(c), sy, P * EO);
+        // (past the end a select: a row of zeros times a state that is not finite is not zero)
+        const int live = seq.rows(c) - (16 * w + 4 * lg);
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) buf_st(yb, yoff[ct] + q * sy, a.scale * y[ct][q], Tout(0));
+            for (int q = 0; q < 4; ++q) buf_st(yb, yoff[ct] + q * sy, q < live ? a.scale * y[ct][q] : 0.0f, Tout(0));
     };
     fetch_k(0);
     fetch_v(0);

@@ -42,3 +42,46 @@ def test_bf16_gradients_are_the_fp32_ones_rounded(gpu, shape, dtype):
     torch.cuda.synchronize()
     for n in want:
         assert torch.equal(got[n], want[n].to(got[n].dtype)), n
+
+
+BAD = [("v", float("nan")), ("k", float("inf")), ("q", float("nan")), ("beta", float("inf")), ("g", float("nan")),
+       ("h0", float("inf"))]
+
+
+def spoilt(L, lengths, t, name, value, dtype, seed):
+    """Inputs of len(lengths) sequences with one value of sequence 0, head 0,
+    token t that is not finite (h0: the state that it starts from)."""
+    i = inputs(len(lengths), L, 2, 2, 40, 48, dtype, seed=seed, h0=True)
+    x = i[name]
+    x[(0, 0, 3, 5) if name == "h0" else (0, t, 0, 7)[:x.dim()]] = value
+    return i
+
+
+# (length, token): the end of the sequence inside the last chunk, inside the first, in the token-by-token form
+ENDS = [(150, 140, 130), (150, 40, 3), (14, 9, 2)]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L,n,t", ENDS)
+@pytest.mark.parametrize("name,value", BAD)
+def test_fwd_not_finite(gpu, dtype, L, n, t, name, value):
+    """A value that is not finite reaches its chunk and head and what follows:
+    not the chunks before, not other heads or sequences, and no token past
+    the end, whose y is zero."""
+    lengths = [n, L]
+    i = spoilt(L, lengths, t, name, value, dtype, 340)
+    for out in (F32, BF16):
+        y, last = ss.delta_fwd(**i, lengths=torch.tensor(lengths, dtype=torch.int32, device=DEV), out_dtype=out)
+        torch.cuda.synchronize()
+        assert not host(y[0, n:]).any()
+        with np.errstate(all="ignore"):
+            yr, lr = ref.delta(**i, lengths=lengths)
+        half = 2.0 ** -8 if out == BF16 else 0.0
+        tol = (5e-5 * float(np.sqrt(np.mean(np.square(yr[1])))), 5e-5 + half)
+        before = 0 if name == "h0" else t // 64 * 64
+        for part in ((slice(0, 1), slice(0, before), slice(0, 1)), (slice(0, 1), slice(0, n), slice(1, 2)),
+                     (slice(1, 2), slice(0, L), slice(0, 2))):
+            check_close(host(y[part]).double().numpy(), yr[part], tol, "y that it does not reach")
+        # what the definition leaves without a value has none here
+        assert not np.isfinite(host(y).double().numpy()[~np.isfinite(yr)]).any()
+        assert not np.isfinite(host(last).double().numpy()[~np.isfinite(lr)]).any()
