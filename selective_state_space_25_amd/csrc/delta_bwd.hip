@@ -186,13 +186,14 @@ __global__ __launch_bounds__(kBackThreads, 2) void delta_back_kernel(DeltaBwdArg
                 for (int l = 0; l < NK; ++l)
                     k[i][l] = ld_down(K + l * kC * kRow, kRow, 32 * (i & 1), 16 * (NT * w + i / 2), lane);
             const auto vb = rows_buf(scalar(dVg + (int64_t)c * kC * sv), scalar(all.rows(c)), sv, P * ES);
+            const int live = seq.rows(c) - (16 * w + 4 * lg);   // (past the end zero whatever the states hold)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) {
                 float* kr = ba.dR + (bh * nch + c) * kC * pad + p0 + 16 * ct;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     kr[(16 * w + 4 * lg + q) * pad] = r[ct][q];
-                    buf_st(vb, voff[ct] + q * sv, beta[q] * r[ct][q], Tin(0));
+                    buf_st(vb, voff[ct] + q * sv, q < live ? beta[q] * r[ct][q] : 0.0f, Tin(0));
                 }
             }
             lds_barrier();
@@ -796,7 +797,8 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs b
             }
         }
     }
-    // rows through LDS (over K and Q), out 32 bytes or more a lane
+    // rows through LDS (over K and Q), out 32 bytes or more a lane; past the
+    // sequence's end zeros, whatever the states hold
     lds_barrier();
     constexpr int NW = NP / 2, nr = NW + 4;
     float (&out)[16][nr] = *reinterpret_cast<float (*)[16][nr]>(&sm.m.K[0][0][0] + wave * (2 * 16 * nr));
@@ -805,7 +807,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs b
 #pragma unroll
         for (int i = 0; i < NH; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) out[4 * lg + q][16 * i + li] = v[i][q];
+            for (int q = 0; q < 4; ++q) out[4 * lg + q][16 * i + li] = 16 * tb + 4 * lg + q < live ? v[i][q] : 0.0f;
         wave_sync();
         const int rows = min(16, inside - 16 * tb);
         const bool wide = shared_qk ? N % 8 == 0 : ba.vec_g;

@@ -85,3 +85,35 @@ def test_fwd_not_finite(gpu, dtype, L, n, t, name, value):
         # what the definition leaves without a value has none here
         assert not np.isfinite(host(y).double().numpy()[~np.isfinite(yr)]).any()
         assert not np.isfinite(host(last).double().numpy()[~np.isfinite(lr)]).any()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("L,n,t", ENDS)
+@pytest.mark.parametrize("name,value", BAD + [("dout", float("nan")), ("dlast", float("-inf"))])
+def test_bwd_not_finite(gpu, dtype, L, n, t, name, value):
+    """Gradients past the end are zero whatever a live token holds, and those
+    of other heads and sequences are what they were."""
+    lengths = [n, L]
+    dout, dlast = douts(2, L, 2, 40, 48, dtype, 341)
+    if name in ("dout", "dlast"):
+        i = inputs(2, L, 2, 2, 40, 48, dtype, seed=341, h0=True)
+        if name == "dout":
+            dout[0, t, 0, 7] = value
+        else:
+            dlast[0, 0, 3, 5] = value
+    else:
+        i = spoilt(L, lengths, t, name, value, dtype, 341)
+    got = ss.delta_bwd(**i, dout=dout, dlast_state=dlast, lengths=torch.tensor(lengths, dtype=torch.int32, device=DEV))
+    torch.cuda.synchronize()
+    with np.errstate(all="ignore"):
+        want = ref.delta_bwd(**i, dout=dout, dlast=dlast, lengths=lengths)
+    for name, x in got.items():
+        x, w = host(x).double().numpy(), want[name]
+        half = 2.0 ** -8 if got[name].dtype == BF16 else 0.0
+        tol = (5e-5 * float(np.sqrt(np.mean(np.square(w[1])))), 5e-5 + half)
+        check_close(x[1], w[1], tol, name + " of another sequence")
+        if name == "dh0":
+            check_close(x[0, 1], w[0, 1], tol, "dh0 of another head")
+            continue
+        assert not x[0, n:].any(), name
+        check_close(x[0, :, 1], w[0, :, 1], tol, name + " of another head")
