@@ -91,8 +91,6 @@ selscan_status_t check_bwd_shape(const selscan_m2_shape_t* s) {
     if (mul_checked({s->batch, s->nheads, selscan::delta_chunks(s->seqlen), (s->headdim + 31) / 32 * 32, 128, 16}) < 0 ||
         mul_checked({s->batch, s->seqlen, s->nheads, s->dstate, 16}) < 0)
         return set_error(SELSCAN_ERR_INVALID_ARG, "workspace size overflows 64-bit byte counts");
-    if (s->batch * s->seqlen * s->ngroups * s->dstate / 256 >= 0x7fffff00)
-        return set_error(SELSCAN_ERR_UNSUPPORTED, "too many dq/dk elements for one launch");
     return SELSCAN_OK;
 }
 

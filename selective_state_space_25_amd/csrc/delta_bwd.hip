@@ -837,7 +837,7 @@ __global__ __launch_bounds__(kGradThreads) void delta_grad_kernel(DeltaBwdArgs b
 template <typename Tin>
 __global__ __launch_bounds__(256) void delta_group_kernel(DeltaBwdArgs ba) {
     const DeltaArgs& a = ba.f;
-    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;   // [batch * L, G, N]
+    const int64_t i = io::group_id() * 256 + threadIdx.x;   // [batch * L, G, N]
     const int64_t n = i % a.N, tg = i / a.N;
     if (tg >= a.batch * a.L * a.G) return;
     const int64_t r = a.H / a.G;
@@ -900,7 +900,7 @@ hipError_t launch(const DeltaBwdArgs& a, hipStream_t stream) {
     if (a.pq) {
         KTime kt("delta_group", stream);
         const int64_t n = f.batch * f.L * f.G * f.N;
-        hipLaunchKernelGGL((delta_group_kernel<Tin>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((delta_group_kernel<Tin>), io::groups((n + 255) / 256), dim3(256), 0, stream, a);
     }
     return hipGetLastError();
 }
