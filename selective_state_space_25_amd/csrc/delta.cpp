@@ -31,7 +31,8 @@ selscan_status_t check_shape(const selscan_m2_shape_t* s) {
     // the chunked form's offsets inside 64 tokens are 32-bit
     if (s->nheads * s->headdim > (int64_t(1) << 22) || s->ngroups > (int64_t(1) << 15))
         return set_error(SELSCAN_ERR_UNSUPPORTED, "the gated delta rule supports nheads headdim <= 2^22 and ngroups <= 2^15");
-    // a launch has fewer than 2^32 threads: 512 to 16 rows of a head's state, 256 to a chunk
+    // a launch has fewer than 2^32 threads: 512 to 16 rows of a head's state, 64
+    // to a chunk (whose limit is lower: 2^24 chunks' records are 512 GB)
     const int64_t heads = (s->batch * s->nheads + 7) / 8 * 8;
     if (heads * ((s->headdim + 15) / 16) >= 1 << 23 || mul_checked({heads, selscan::delta_chunks(s->seqlen)}) >= 1 << 24)
         return set_error(SELSCAN_ERR_UNSUPPORTED, "too many (batch, head, channel) rows or chunks for one launch");
@@ -91,6 +92,11 @@ selscan_status_t check_bwd_shape(const selscan_m2_shape_t* s) {
     if (mul_checked({s->batch, s->nheads, selscan::delta_chunks(s->seqlen), (s->headdim + 31) / 32 * 32, 128, 16}) < 0 ||
         mul_checked({s->batch, s->seqlen, s->nheads, s->dstate, 16}) < 0)
         return set_error(SELSCAN_ERR_INVALID_ARG, "workspace size overflows 64-bit byte counts");
+    // 512 threads to 16 of the rows of a head's state, which are padded to a
+    // multiple of 32 here, and 512 to a chunk
+    const int64_t heads = (s->batch * s->nheads + 7) / 8 * 8;
+    if (heads * ((s->headdim + 31) / 32 * 2) >= 1 << 23 || s->batch * s->nheads * selscan::delta_chunks(s->seqlen) >= 1 << 23)
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "too many (batch, head, channel) rows or chunks for one launch");
     return SELSCAN_OK;
 }
 
