@@ -127,7 +127,9 @@ class Recall(torch.nn.Module):
 
     @torch.no_grad()
     def decoder(self, states):
-        """A function from one token [batch, 2] to its logits, which updates the states in place."""
+        """A function from one token [batch, 2] to its logits, which updates
+        the states in place.  Call it on the stream that is current here: the
+        bound calls stay on it."""
         batch = states[0].shape[0]
         bound = []
         for block, state in zip(self.blocks, states):

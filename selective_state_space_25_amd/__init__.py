@@ -290,10 +290,11 @@ def step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, softplus=Tru
 class _BoundCall:
     """A C-ABI call with its arguments marshalled once: calling it enqueues
     the kernel again on the same buffers (whose contents the caller may
-    change in place between calls, as a decoding loop does)."""
+    change in place between calls, as a decoding loop does).  It holds the
+    tensors whose addresses it passes, so that their memory stays theirs."""
 
-    def __init__(self, fn, shape, args):
-        self._fn, self._shape, self._args = fn, shape, args
+    def __init__(self, fn, shape, args, tensors):
+        self._fn, self._shape, self._args, self._tensors = fn, shape, args, tensors
 
     def __call__(self):
         st = self._fn(ctypes.byref(self._shape), *self._args)
@@ -323,7 +324,7 @@ def bind_step(state, u, delta, A, B, C, D=None, z=None, delta_bias=None, softplu
             _ptr(C, "C", (batch, N), dt, dev), _ptr(D, "D", (dim,), torch.float32, dev),
             _ptr(z, "z", (batch, dim), dt, dev), _ptr(delta_bias, "delta_bias", (dim,), torch.float32, dev),
             int(bool(softplus)), _ptr(out, "out", (batch, dim), odt, dev), _stream_handle(dev))
-    return _BoundCall(lib().selscan_step, s, args), out
+    return _BoundCall(lib().selscan_step, s, args, (state, u, delta, A, B, C, D, z, delta_bias, out)), out
 
 
 def bind_mamba2_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softplus=True, out=None,
@@ -347,7 +348,7 @@ def bind_mamba2_step(state, x, dt, A, B, C, D=None, z=None, dt_bias=None, softpl
             _ptr(C, "C", (batch, G, N), dtp, dev), _ptr(D, "D", (H,), torch.float32, dev),
             _ptr(z, "z", (batch, H, P), dtp, dev), _ptr(dt_bias, "dt_bias", (H,), torch.float32, dev),
             int(bool(softplus)), _ptr(out, "out", (batch, H, P), odt, dev), _stream_handle(dev))
-    return _BoundCall(lib().selscan_mamba2_step, s, args), out
+    return _BoundCall(lib().selscan_mamba2_step, s, args, (state, x, dt, A, B, C, D, z, dt_bias, out)), out
 
 
 def bwd(u, delta, A, B, C, D=None, z=None, delta_bias=None, dout=None, softplus=True, h0=None,
@@ -680,7 +681,7 @@ def bind_delta_step(state, q, k, v, g, beta, scale=None, out=None, out_dtype=Non
     """selscan_delta_step with its arguments checked and marshalled once:
     returns (call, y); see bind_step."""
     s, args, out = _delta_step_args(state, q, k, v, g, beta, scale, out, out_dtype)
-    return _BoundCall(lib().selscan_delta_step, s, args), out
+    return _BoundCall(lib().selscan_delta_step, s, args, (state, q, k, v, g, beta, out)), out
 
 
 def dropout(x, p, seed, offset=0, out=None):
