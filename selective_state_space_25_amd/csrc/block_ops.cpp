@@ -43,7 +43,7 @@ void fill(selscan::NormArgs& a, const selscan_norm_shape_t* s) {
 }
 
 size_t norm_bwd_bytes(const selscan_norm_shape_t* s) {
-    return align256((size_t)selscan::norm_bwd_blocks(s->rows, s->dim) * 2 * (size_t)s->dim * 4);
+    return align256(selscan::norm_bwd_part_bytes(s->rows, s->dim));
 }
 
 selscan_status_t launched(hipError_t e) {

@@ -269,7 +269,7 @@ struct NormArgs {
     float* rstd;
     float* dweight;
     float* dbias;
-    float* part;              // gradients: [blocks, 2, dim] partial sums of dweight, dbias
+    float* part;              // gradients: [blocks, 2, dim] partial sums of dweight, dbias, and room to add them up
     int64_t rows, dim;
     int blocks;
     float eps, inv_dim;
@@ -280,6 +280,7 @@ struct NormArgs {
     int vec;                  // rows start on 16-byte boundaries, dim % 8 == 0
 };
 int norm_bwd_blocks(int64_t rows, int64_t dim);
+size_t norm_bwd_part_bytes(int64_t rows, int64_t dim);
 hipError_t launch_norm_fwd(const NormArgs& a, int in_bf16, int res_bf16, int out_bf16, hipStream_t stream);
 hipError_t launch_norm_bwd(const NormArgs& a, int in_bf16, int res_bf16, int out_bf16, hipStream_t stream);
 

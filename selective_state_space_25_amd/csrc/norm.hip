@@ -13,12 +13,17 @@
 // summed over (s - mean)^2, not taken as a difference of moments.  The
 // gradients' waves walk rows a fixed distance apart and keep their sums for
 // dweight and dbias in registers, one partial row a workgroup, which a second
-// kernel adds in a fixed order.
+// kernel adds in a fixed order.  A wave adds up 64 rows at most (there are
+// more workgroups where there are more rows), the second kernel in fp64: a
+// plain fp32 sum of all that a wave would get, thousands of short rows, is off
+// by 1e-4 where its roundings lean one way.
 //
 // Measured at 32768 rows of 2560, bf16 x and y, fp32 residual, dropout 0.1:
 // forward 204 us (1.0 GB, 4.9 TB/s), gradients 260 us (1.34 GB, 5.1 TB/s);
 // reading rows again took 760 and 642 us.  One row of 768 is the launch: 14 us
 // a call.
+#include <algorithm>
+
 #include "io.hpp"
 #include "kernels.hpp"
 #include "philox.hpp"
@@ -266,54 +271,73 @@ __global__ __launch_bounds__(kT) void norm_bwd_kernel(NormArgs a) {
     }
 }
 
+// A sum over rows that keeps what each addition rounds off (Kahan).
+struct RowSum {
+    float s = 0.0f, c = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float y = v - c, t = s + y;
+        c = (t - s) - y;
+        s = t;
+    }
+};
+
 // Partial sums of dweight and dbias: workgroup (x, y) takes 256 columns and
-// every gridDim.y-th row.
+// every gridDim.y-th row, however many those are.
 template <typename Tres, typename Tout>
 __global__ __launch_bounds__(kT) void norm_wgrad_kernel(NormArgs a) {
     const int64_t d = (int64_t)blockIdx.x * kT + threadIdx.x;
     if (d >= a.dim) return;
     const Tout* DY = reinterpret_cast<const Tout*>(a.x) + d;
     const Tres* S = reinterpret_cast<const Tres*>(a.res) + d;
-    float gw = 0.0f, gb = 0.0f;
-    for (int64_t r = blockIdx.y; r < a.rows; r += a.blocks) {
+    RowSum gw, gb;
+    for (int64_t r = blockIdx.y; r < a.rows; r += gridDim.y) {
         const float dy = io::ld(DY + r * a.dim);
-        gw += dy * ((io::ld(S + r * a.dim) - a.mean_in[r]) * a.rstd_in[r]);
-        gb += dy;
+        gw.add(dy * ((io::ld(S + r * a.dim) - a.mean_in[r]) * a.rstd_in[r]));
+        gb.add(dy);
     }
-    a.part[(2 * (int64_t)blockIdx.y) * a.dim + d] = gw;
-    a.part[(2 * (int64_t)blockIdx.y + 1) * a.dim + d] = gb;
+    a.part[(2 * (int64_t)blockIdx.y) * a.dim + d] = gw.s;
+    a.part[(2 * (int64_t)blockIdx.y + 1) * a.dim + d] = gb.s;
 }
 
-// Sums of the partial rows: 64 columns and 16 slices of the rows a workgroup.
-__global__ __launch_bounds__(1024) void norm_wsum_kernel(NormArgs a) {
-    __shared__ float sm[2][16][64];
+// Sums of n partial rows [n, 2, dim]: workgroup (x, y) takes 64 columns and
+// kSumRows of the rows, in 16 slices; the sums of y lie 2 dim y further on.
+constexpr int kSumRows = 1024;
+__global__ __launch_bounds__(1024) void norm_wsum_kernel(const float* part, int n, int64_t dim, float* dweight, float* dbias) {
+    __shared__ double sm[2][16][64];
     const int col = threadIdx.x & 63, sl = threadIdx.x >> 6;
     const int64_t d = (int64_t)blockIdx.x * 64 + col;
-    float gw = 0.0f, gb = 0.0f;
-    if (d < a.dim) {
+    const int end = min(n, (int)(blockIdx.y + 1) * kSumRows);
+    double gw = 0.0, gb = 0.0;
+    if (d < dim) {
 #pragma unroll 4
-        for (int b = sl; b < a.blocks; b += 16) {
-            gw += a.part[2 * (int64_t)b * a.dim + d];
-            gb += a.part[(2 * (int64_t)b + 1) * a.dim + d];
+        for (int b = (int)blockIdx.y * kSumRows + sl; b < end; b += 16) {
+            gw += part[2 * (int64_t)b * dim + d];
+            gb += part[(2 * (int64_t)b + 1) * dim + d];
         }
     }
     sm[0][sl][col] = gw;
     sm[1][sl][col] = gb;
     __syncthreads();
-    if (sl < 2 && d < a.dim) {
-        float v = 0.0f;
+    if (sl < 2 && d < dim) {
+        double v = 0.0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) v += sm[sl][i][col];
-        float* out = sl ? a.dbias : a.dweight;
-        if (out) out[d] = v;
+        float* out = sl ? dbias : dweight;
+        if (out) out[2 * (int64_t)blockIdx.y * dim + d] = (float)v;
     }
 }
+
+constexpr int kBlocks = 512;
+
+// Rows that a workgroup of the register kernels works on at a time: one wave
+// or four to a row.
+int rows_at_once(int64_t dim) { return dim / 8 <= 5 * 64 ? 4 : 1; }
 
 // Waves per row and pieces per lane of the register kernels; 0: neither fits.
 int reg_pieces(const NormArgs& a, int& waves) {
     if (!a.vec || a.dim > 8192) return 0;
     const int np = (int)(a.dim / 8);
-    waves = np <= 5 * 64 ? 1 : 4;
+    waves = 4 / rows_at_once(a.dim);
     return (np + 64 * waves - 1) / (64 * waves);
 }
 
@@ -356,6 +380,7 @@ template <typename Tin, typename Tres, typename Tout>
 hipError_t bwd(const NormArgs& a, hipStream_t stream) {
     int waves = 0;
     const bool sums = a.dweight || a.dbias;
+    int n = a.blocks;   // partial rows
     if (const int pieces = reg_pieces(a, waves)) {
         const hipError_t e = by_size<false, Tin, Tres, Tout>(a, waves, pieces, stream);
         if (e != hipSuccess || !sums) return e;
@@ -366,11 +391,21 @@ hipError_t bwd(const NormArgs& a, hipStream_t stream) {
         }
         if (!sums) return hipGetLastError();
         KTime kt("norm_wgrad", stream);
-        hipLaunchKernelGGL((norm_wgrad_kernel<Tres, Tout>), dim3((unsigned)((a.dim + kT - 1) / kT), a.blocks), dim3(kT), 0,
+        n = std::min(n, kBlocks);
+        hipLaunchKernelGGL((norm_wgrad_kernel<Tres, Tout>), dim3((unsigned)((a.dim + kT - 1) / kT), n), dim3(kT), 0,
                            stream, a);
     }
     KTime kt("norm_wsum", stream);
-    hipLaunchKernelGGL(norm_wsum_kernel, dim3((unsigned)((a.dim + 63) / 64)), dim3(1024), 0, stream, a);
+    const unsigned columns = (unsigned)((a.dim + 63) / 64);
+    const float* part = a.part;
+    if (n > kSumRows) {   // (n past kBlocks: sums of kSumRows first, behind the rows)
+        float* next = a.part + 2 * (int64_t)n * a.dim;
+        const int slices = (n + kSumRows - 1) / kSumRows;
+        hipLaunchKernelGGL(norm_wsum_kernel, dim3(columns, slices), dim3(1024), 0, stream, part, n, a.dim, next, next + a.dim);
+        part = next;
+        n = slices;
+    }
+    hipLaunchKernelGGL(norm_wsum_kernel, dim3(columns), dim3(1024), 0, stream, part, n, a.dim, a.dweight, a.dbias);
     return hipGetLastError();
 }
 
@@ -388,14 +423,21 @@ hipError_t by_type(const NormArgs& a, int in_bf16, int res_bf16, int out_bf16, h
 
 }  // namespace
 
-// Partial rows of dweight and dbias: enough workgroups for the whole GPU
-// (2 per unit for the register kernel, whose workgroup takes the row whole),
-// no more than there are rows.
+// Workgroups of the gradients' kernel, each with a partial row of dweight and
+// dbias: enough for the whole GPU (2 per unit for the register kernel, whose
+// workgroup takes the row whole), and for the register kernel's waves to add
+// up 64 rows at most; a quarter of the rows at most.
 int norm_bwd_blocks(int64_t rows, int64_t dim) {
-    int64_t n = 512;
+    int64_t n = kBlocks;
     if (dim > 8192) n = (2048 * kT + dim - 1) / dim;
+    else n = std::max(n, std::min((rows + 64 * rows_at_once(dim) - 1) / (64 * rows_at_once(dim)), (int64_t)1 << 23));
     if (n > (rows + 3) / 4) n = (rows + 3) / 4;
     return (int)(n < 1 ? 1 : n);
+}
+
+size_t norm_bwd_part_bytes(int64_t rows, int64_t dim) {
+    const int64_t n = norm_bwd_blocks(rows, dim);
+    return (size_t)(n + (n > kSumRows ? (n + kSumRows - 1) / kSumRows : 0)) * 2 * (size_t)dim * 4;
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, int in_bf16, int res_bf16, int out_bf16, hipStream_t stream) {
