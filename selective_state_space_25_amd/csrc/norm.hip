@@ -426,13 +426,12 @@ hipError_t by_type(const NormArgs& a, int in_bf16, int res_bf16, int out_bf16, h
 // Workgroups of the gradients' kernel, each with a partial row of dweight and
 // dbias: enough for the whole GPU (2 per unit for the register kernel, whose
 // workgroup takes the row whole), and for the register kernel's waves to add
-// up 64 rows at most; a quarter of the rows at most.
+// up 64 rows at most; no more than have rows to work on.
 int norm_bwd_blocks(int64_t rows, int64_t dim) {
     int64_t n = kBlocks;
     if (dim > 8192) n = (2048 * kT + dim - 1) / dim;
     else n = std::max(n, std::min((rows + 64 * rows_at_once(dim) - 1) / (64 * rows_at_once(dim)), (int64_t)1 << 23));
-    if (n > (rows + 3) / 4) n = (rows + 3) / 4;
-    return (int)(n < 1 ? 1 : n);
+    return (int)std::min(n, (rows + rows_at_once(dim) - 1) / rows_at_once(dim));
 }
 
 size_t norm_bwd_part_bytes(int64_t rows, int64_t dim) {
