@@ -40,3 +40,87 @@ def test_weight_gradients_of_many_rows(gpu, rows, dim):
     for n in want:
         off = ((got[n].double() - want[n]).abs() / mag[n]).max()
         assert float(off) <= 2.0 ** -19, (n, float(off))
+
+
+def shifted(t):
+    """The same values one element off a 16-byte boundary."""
+    v = torch.empty(t.numel() + 1, dtype=t.dtype, device=t.device)[1:].view(t.shape)
+    return v.copy_(t)
+
+
+def close(got, want, tol, what):
+    rms = max(float(np.sqrt(np.mean(np.square(want)))), 1.0)
+    check_close(host(got).double().numpy(), want, (tol * rms, tol + (2.0 ** -8 if got.dtype == BF16 else 0.0)), what)
+
+
+# fp32 sums over up to 2^13 values in a tree, a division and a square root; s
+# itself is rounded twice, which y carries times rstd (here about 1)
+TOL = 2.0 ** -18
+
+
+@pytest.mark.parametrize("rows,dim", [(5, 64), (3, 2560), (2, 4096), (1, 8)])
+@pytest.mark.parametrize("types", [(F32, F32, F32), (BF16, F32, BF16), (BF16, BF16, F32)])
+def test_off_a_16_byte_boundary(gpu, rows, dim, types):
+    """Widths that make whole 16-byte pieces, on tensors that do not start on one."""
+    tin, tres, tout = types
+    g = torch.Generator().manual_seed(91)
+    rnd = lambda dt: shifted(torch.randn((rows, dim), generator=g).to(dt).to(DEV))
+    x, r = rnd(tin), rnd(tres)
+    w, b = (shifted(torch.randn(dim, generator=g).to(DEV)) for _ in range(2))
+    kw = dict(p=0.25, seed=5, offset=1)
+    y, s, mean, rstd = ss.layer_norm_fwd(x, w, b, residual=r, out=shifted(torch.empty((rows, dim), dtype=tout, device=DEV)),
+                                         **kw)
+    yr, sr, mr, rr = ref.layer_norm(x, w, b, r, **kw)
+    for got, want, what in ((y, yr, "y"), (s, sr, "s"), (mean, mr, "mean"), (rstd, rr, "rstd")):
+        close(got, want, TOL, what)
+    dy, dr = rnd(tout), rnd(tres)
+    got = ss.layer_norm_bwd(dy, shifted(s), w, mean, rstd, dresidual=dr, x_dtype=tin, **kw)
+    want = ref.layer_norm_bwd(dy, s, w, mean, rstd, dr, **kw)
+    for n in want:
+        close(got[n], want[n], TOL * max(1.0, float(rr.max())), n)
+
+
+def raw(rows, dim, types, p=0.25, seed=5, offset=1):
+    code = {F32: ss.F32, BF16: ss.BF16}
+    return ss.NormShape(rows, dim, *(code[t] for t in types), 1e-5, p, seed, offset, None, 0)
+
+
+def call(fn, s, *tensors):
+    st = fn(ctypes.byref(s), *(None if t is None else t.data_ptr() for t in tensors),
+            torch.cuda.current_stream().cuda_stream)
+    assert st == ss.OK, ss.last_error()
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("rows,dim", [(7, 64), (3, 101), (2, 4096), (2, 9001)])
+@pytest.mark.parametrize("types", [(F32, F32, F32), (BF16, F32, BF16)])
+def test_buffers_used_twice_and_outputs_left_out(gpu, rows, dim, types):
+    """The C entry points: s over residual, dresidual over dresidual_out, and
+    every output that may be NULL left out, against the calls with all of
+    them in buffers of their own."""
+    tin, tres, tout = types
+    L = ss.lib()
+    g = torch.Generator().manual_seed(92)
+    rnd = lambda dt, *shape: torch.randn(shape or (rows, dim), generator=g).to(dt).to(DEV)
+    x, r, w, b = rnd(tin), rnd(tres), rnd(F32, dim), rnd(F32, dim)
+    y, s, mean, rstd = ss.layer_norm_fwd(x, w, b, residual=r, p=0.25, seed=5, offset=1, out_dtype=tout)
+    y2, r2 = torch.empty_like(y), r.clone()
+    call(L.selscan_layer_norm_fwd, raw(rows, dim, types), x, r2, w, b, y2, r2, None, None)
+    assert torch.equal(y2, y) and torch.equal(r2, s)
+    y2.zero_()
+    call(L.selscan_layer_norm_fwd, raw(rows, dim, types), x, r, w, b, y2, None, None, None)
+    assert torch.equal(y2, y)
+
+    dy, dr = rnd(tout), rnd(tres)
+    full = ss.layer_norm_bwd(dy, s, w, mean, rstd, dresidual=dr, p=0.25, seed=5, offset=1, x_dtype=tin)
+    new = {"dx": lambda: torch.full_like(x, 7.0), "dresidual": lambda: torch.full_like(r, 7.0),
+           "dweight": lambda: torch.full_like(w, 7.0), "dbias": lambda: torch.full_like(w, 7.0)}
+    names = list(new)
+    for keep in [[n] for n in names] + [["dx", "dresidual"], ["dweight", "dbias"]]:
+        out = {n: new[n]() for n in keep}
+        call(L.selscan_layer_norm_bwd, raw(rows, dim, types), dy, s, w, mean, rstd, dr, *(out.get(n) for n in names))
+        for n in keep:
+            assert torch.equal(out[n], full[n]), (keep, n)
+    dr2, dx = dr.clone(), new["dx"]()
+    call(L.selscan_layer_norm_bwd, raw(rows, dim, types), dy, s, w, mean, rstd, dr2, dx, dr2, None, None)
+    assert torch.equal(dr2, full["dresidual"]) and torch.equal(dx, full["dx"])
