@@ -558,6 +558,7 @@ def _ws_arg(workspace, need, device):
         if need == 0:
             return None, 0, None
         workspace = _torch().empty(need, dtype=_torch().uint8, device=device)
+    _ptr(workspace, "workspace", device=device)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
 
 
