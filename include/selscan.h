@@ -466,7 +466,7 @@ selscan_status_t selscan_dropout(const selscan_dropout_shape_t* shape, const voi
  *   x            [rows, dim]  in_dtype
  *   residual     [rows, dim]  res_dtype   NULL = 0
  *   weight, bias [dim]        fp32        NULL = 1 and 0
- *   y            [rows, dim]  out_dtype   (written)
+ *   y            [rows, dim]  out_dtype   (written); may be x where their types agree
  *   residual_out [rows, dim]  res_dtype   s (written; NULL = skip); may be residual
  *   mean, rstd   [rows]       fp32        (written; NULL = skip)
  * p, seed, offset as for selscan_dropout; p = 0 leaves x as it is.  The sums

@@ -711,7 +711,8 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, p=0.0, se
     offset: the dropout of x (see dropout).
     Returns (y, s, mean, rstd): y in x's dtype unless out_dtype or out says
     otherwise; s in residual's dtype (x's, or res_dtype, without one; x itself
-    when there is neither dropout nor residual); mean and rstd [...] float32.
+    when there is neither dropout nor residual, unless out is x's memory); mean
+    and rstd [...] float32.
     """
     torch = _torch()
     f32 = torch.float32
@@ -721,9 +722,12 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, p=0.0, se
     dim = shape[-1]
     odt = (out.dtype if out is not None else x.dtype) if out_dtype is None else out_dtype
     rdt = residual.dtype if residual is not None else (x.dtype if res_dtype is None else res_dtype)
+    keep_x = residual is None and p == 0.0 and rdt == x.dtype
     if out is None:
         out = torch.empty(shape, dtype=odt, device=dev)
-    s = x if residual is None and p == 0.0 and rdt == x.dtype else torch.empty(shape, dtype=rdt, device=dev)
+    elif keep_x and out.untyped_storage().data_ptr() == x.untyped_storage().data_ptr():
+        keep_x = False   # y may be written over x
+    s = x if keep_x else torch.empty(shape, dtype=rdt, device=dev)
     mean = torch.empty(shape[:-1], dtype=f32, device=dev)
     rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
     sh = NormShape(x.numel() // max(dim, 1), dim, _dtype_code(x), _dtype_code(s), _dtype_code(out), eps, p, seed,

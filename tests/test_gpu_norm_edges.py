@@ -124,3 +124,20 @@ def test_buffers_used_twice_and_outputs_left_out(gpu, rows, dim, types):
     dr2, dx = dr.clone(), new["dx"]()
     call(L.selscan_layer_norm_bwd, raw(rows, dim, types), dy, s, w, mean, rstd, dr2, dx, dr2, None, None)
     assert torch.equal(dr2, full["dresidual"]) and torch.equal(dx, full["dx"])
+
+
+@pytest.mark.parametrize("rows,dim", [(7, 64), (3, 101), (2, 4096), (2, 9001)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_y_over_x(gpu, rows, dim, dtype):
+    """y written over x: s, which is x where nothing is added to it, is then a tensor of its own."""
+    g = torch.Generator().manual_seed(93)
+    x = torch.randn((rows, dim), generator=g).to(dtype).to(DEV)
+    w = torch.randn(dim, generator=g).to(DEV)
+    want = ss.layer_norm_fwd(x, w)
+    assert want[1] is x
+    buf = x.clone()
+    got = ss.layer_norm_fwd(buf, w, out=buf)
+    torch.cuda.synchronize()
+    assert got[0] is buf and got[1].data_ptr() != buf.data_ptr()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
