@@ -685,6 +685,13 @@ def bind_delta_step(state, q, k, v, g, beta, scale=None, out=None, out_dtype=Non
     return _BoundCall(lib().selscan_delta_step, s, args, (state, q, k, v, g, beta, out)), out
 
 
+def _stream_of_words(seed, offset):
+    """seed and offset of a mask: ctypes would keep 64 bits of any integer."""
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError(f"seed and offset must be in [0, 2^64), got {seed} and {offset}")
+    return seed, offset
+
+
 def dropout(x, p, seed, offset=0, out=None):
     """Dropout with a mask that is a function of (seed, offset, element index)
     and is never stored: kept elements times 1 / (1 - p), the others zero.
@@ -696,7 +703,7 @@ def dropout(x, p, seed, offset=0, out=None):
         raise ValueError("selscan.dropout needs tensors on a GPU device")
     if out is None:
         out = _torch().empty_like(x)
-    s = DropoutShape(x.numel(), _dtype_code(x), p, seed, offset)
+    s = DropoutShape(x.numel(), _dtype_code(x), p, *_stream_of_words(seed, offset))
     _check(lib().selscan_dropout(ctypes.byref(s), _ptr(x, "x"), _ptr(out, "out", x.shape, x.dtype, dev),
                                  _stream_handle(dev)))
     return out
@@ -730,8 +737,8 @@ def layer_norm_fwd(x, weight=None, bias=None, residual=None, eps=1e-5, p=0.0, se
     s = x if keep_x else torch.empty(shape, dtype=rdt, device=dev)
     mean = torch.empty(shape[:-1], dtype=f32, device=dev)
     rstd = torch.empty(shape[:-1], dtype=f32, device=dev)
-    sh = NormShape(x.numel() // max(dim, 1), dim, _dtype_code(x), _dtype_code(s), _dtype_code(out), eps, p, seed,
-                   offset, None, 0)
+    sh = NormShape(x.numel() // max(dim, 1), dim, _dtype_code(x), _dtype_code(s), _dtype_code(out), eps, p,
+                   *_stream_of_words(seed, offset), None, 0)
     _check(lib().selscan_layer_norm_fwd(
         ctypes.byref(sh), _ptr(x, "x"), _ptr(residual, "residual", shape, rdt, dev),
         _ptr(weight, "weight", (dim,), f32, dev), _ptr(bias, "bias", (dim,), f32, dev),
@@ -763,8 +770,8 @@ def layer_norm_bwd(dy, s, weight=None, mean=None, rstd=None, dresidual=None, p=0
     dx = ds if p == 0.0 and xdt == s.dtype else torch.empty(shape, dtype=xdt, device=dev)
     dw = torch.empty((dim,), dtype=f32, device=dev)
     db = torch.empty((dim,), dtype=f32, device=dev)
-    sh = NormShape(dy.numel() // max(dim, 1), dim, _dtype_code(dx), _dtype_code(s), _dtype_code(dy), 0.0, p, seed,
-                   offset, None, 0)
+    sh = NormShape(dy.numel() // max(dim, 1), dim, _dtype_code(dx), _dtype_code(s), _dtype_code(dy), 0.0, p,
+                   *_stream_of_words(seed, offset), None, 0)
     L_ = lib()
     sh.workspace, sh.workspace_bytes, ws = _ws_arg(
         workspace, L_.selscan_layer_norm_bwd_workspace_bytes(ctypes.byref(sh)), dev)

@@ -141,3 +141,20 @@ def test_y_over_x(gpu, rows, dim, dtype):
     assert got[0] is buf and got[1].data_ptr() != buf.data_ptr()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("bad", [-1, 1 << 64, (1 << 64) + 5])
+def test_seeds_out_of_range(gpu, bad):
+    """64 bits of a larger seed would give another seed's mask."""
+    x = torch.ones((4, 16), device=DEV)
+    _, s, mean, rstd = ss.layer_norm_fwd(x)
+    for kw in (dict(seed=bad), dict(seed=1, offset=bad)):
+        with pytest.raises(ValueError, match="seed"):
+            ss.dropout(x, 0.5, **kw)
+        with pytest.raises(ValueError, match="seed"):
+            ss.layer_norm_fwd(x, p=0.5, **kw)
+        with pytest.raises(ValueError, match="seed"):
+            ss.layer_norm_bwd(x, s, None, mean, rstd, p=0.5, **kw)
+    top = (1 << 64) - 1
+    want = ref.dropout(x, 0.5, top, top)
+    assert np.array_equal(host(ss.dropout(x, 0.5, top, top)).double().numpy(), want)
