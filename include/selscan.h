@@ -375,7 +375,9 @@ selscan_status_t selscan_conv1d(const selscan_conv_shape_t* shape, const void* x
  *   last_state [B, H, P, N]  fp32       (written; NULL = skip); may not alias h0
  *
  * 1 <= N <= 128, H P <= 2^22, G <= 2^15 (UNSUPPORTED above), any L.  State,
- * decays and sums are fp32.  Past 16 tokens the sequence is worked on in
+ * decays and sums are fp32, and so are products in effect, whatever the types
+ * of inputs and outputs: what is written in bf16 is the fp32 result, rounded
+ * once.  Past 16 tokens the sequence is worked on in
  * chunks of 64, as matrix products: a NaN or infinity in a token reaches every
  * y of its chunk and head, and what follows.
  *

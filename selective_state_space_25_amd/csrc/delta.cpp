@@ -48,10 +48,11 @@ bool vec4(const selscan_m2_shape_t* s, const void* q, const void* k) {
 // within a chunk, where the token-by-token form's is proportional to the
 // length.  us, token by token / chunked, at bf16, 128 x 128 states:
 //              16 heads     128 heads      1024 heads
-//   L =  8    7.7 / 14.4   11.6 / 27.3    64.7 / 137.5
-//   L = 16   12.3 / 14.8   17.8 / 27.5   110.2 / 138.9
-//   L = 24   17.1 / 15.0   24.6 / 28.1   151.2 / 140.6
-//   L = 64   40.3 / 16.7   73.0 / 29.7   349.3 / 154.2
+//   L =  8    7.5 / 14.3   11.5 / 25.0    58.1 / 115.3
+//   L = 16   12.1 / 14.6   17.8 / 25.2    96.3 / 115.0
+//   L = 24   16.9 / 15.0   23.6 / 25.5   135.3 / 115.1
+//   L = 32   21.4 / 15.5   28.9 / 25.9   175.3 / 116.8
+//   L = 64   39.7 / 16.6   71.1 / 27.4   333.1 / 123.2
 constexpr int64_t kRecTokens = 16;
 
 // Padded copies of q and k, which rows that are not made of 16-byte pieces take.

@@ -26,13 +26,13 @@
 // the heads in a fixed order.  All products are fp32-grade, whatever the
 // inputs' type: bf16 gradients are the fp32 ones rounded.
 //
-// Measured at batch 4, 16 heads of 128 x 128, L 2048, bf16: records 40 us,
-// kept scan 94, scan back 152-163 (0.39 GB, 2.5 TB/s: a chain of three products
-// a chunk, 4.9 us), gradients 218 (0.5 GB, 2.3 TB/s).  Of a workgroup's time in
-// the last, 60 % are the steps over the value columns, at the rate of their
-// loads, 20 % the pairs and fp64 dots, 8 % the products with X and E; a CU
-// holds one such workgroup, whose LDS (92 KB) leaves no room for another to
-// load meanwhile.
+// Measured at batch 4, 16 heads of 128 x 128, L 2048, bf16: records 38 us,
+// kept scan 87, scan back 143 (0.39 GB, 2.7 TB/s: a chain of three products
+// a chunk, 4.5 us), gradients 201 (0.5 GB, 2.5 TB/s), 470 in all; fp32: 50,
+// 161, 252 and 248.  Of a workgroup's time in the last, 60 % are the steps over
+// the value columns, at the rate of their loads, 20 % the pairs and fp64 dots,
+// 10 % the products with X and E; a CU holds one such workgroup, whose LDS (93
+// KB) leaves no room for another to load meanwhile.
 #include "delta_chunk.hpp"
 #include "host.hpp"
 
@@ -879,9 +879,11 @@ hipError_t launch(const DeltaBwdArgs& a, hipStream_t stream) {
     e = launch_delta_keep(f, sizeof(Tin) == 2, a.recs, a.S, a.U, a.pad, stream);
     if (e != hipSuccess) return e;
     // Two column blocks to a workgroup where half as many still give each CU
-    // one, as in the scan (batch 4, 16 heads of 128 x 128, L 2048, before the
-    // helper waves: 171 us against 194).  float32 inputs: two blocks' LDS
-    // would not fit.
+    // one, as in the scan (batch 4, 16 heads of 128 x 128, L 2048: 146 us
+    // against 194).  P of 16 and less too: the padded columns, which the
+    // kernel after this one reads, cost a workgroup of their own otherwise
+    // (batch 16, 32 heads of 16 x 64, L 1024: 141 us against 149).  float32
+    // inputs: two blocks' LDS would not fit.
     bool two = false;
     if constexpr (sizeof(Tin) == 2) {
         two = f.batch * f.H * (a.pad / 32) >= host::device_cus();

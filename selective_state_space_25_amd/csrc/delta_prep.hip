@@ -19,9 +19,9 @@
 //
 // What bounds it are the records (32 KB a chunk and head, 57.6 KB for the
 // gradients) and the inverse's chain of dependent steps:
-// 16 heads of 128, L 16384: 62 us, 110 MB of records and 134 MB of q and k,
-// 3.9 TB/s; 256 heads, L 4096, q and k shared by 32 of them: 165 us, 524 MB of
-// records, 3.2 TB/s.
+// 16 heads of 128, L 16384: 64 us, 131 MB of records and 134 MB of q and k,
+// 4.1 TB/s; 256 heads, L 4096, q and k shared by 32 of them: 149 us, 524 MB of
+// records, 3.5 TB/s.
 //
 // cum is summed in fp64 and G's exponents are fp64 differences: after a
 // strong decay cum is large and its fp32 steps would be errors of the

@@ -20,11 +20,11 @@
 // chain: Y (Q S while the state waves make U, A U a chunk later), staging K,
 // needed both ways up, in LDS, and most of the loads, a chunk ahead.
 //
-// Measured: 16 heads of 128 x 128 (128 workgroups), L 16384, bf16: 413 us,
+// Measured: 16 heads of 128 x 128 (128 workgroups), L 16384, bf16: 419 us,
 // 1.6 us a chunk (one wave to a column block: 1830 us; four that share its
-// products: 730 us); 256 heads of 64 x 128, L 4096, fp32 y: 418 us, 0.95 GB of
-// inputs, records and y.  The matrix cores are busy for 11 and 28 % of it.
-// A chunk's 3850 cycles in the first: K S 1150 and 220 at the barrier, T R
+// products: 730 us); 256 heads of 64 x 128, L 4096, fp32 y: 360 us, 0.95 GB of
+// inputs, records and y (2.6 TB/s).  The matrix cores are busy for 11 and 28 %
+// of it.  A chunk's 3850 cycles in the first: K S 1150 and 220 at the barrier, T R
 // 730-1080 (by row block) and 200-600, K^T W 800 and 360.  T staged in LDS by
 // the helpers was slower; a raised wave priority, and Q S, staging and A U one
 // phase earlier, were no faster.
@@ -56,7 +56,9 @@ struct ScanSmem {
 
 // KEEP: instead of y, the state entering each chunk (kept_tile) and U
 // [chunk, 64, pad], which the gradients read (pad: P rounded up to 32, the
-// columns past P zero).
+// columns past P zero).  bf16 in and out with one column block, and KEEP: two
+// workgroups to a CU (registers for four waves a SIMD), which such grids, up
+// to twice the CUs, need to run at once.
 template <typename Tin, typename Tout, int NP, int CT, bool KEEP>
 __global__ __launch_bounds__(kThreads, CT == 1 && sizeof(Tin) == 2 && (KEEP || sizeof(Tout) == 2) ? 4 : 2)
 void delta_scan_kernel(DeltaArgs a, const char* recs, int64_t nch, int npb, float* keep_s, float* keep_u, int pad) {
@@ -399,9 +401,9 @@ hipError_t launch(const DeltaArgs& a, const char* recs, float* keep_s, float* ke
     // Two column blocks to a workgroup share K's staging, its operands and
     // the barriers, but a chunk takes longer: worth it where half as many
     // workgroups still give each CU one (batch 8, 32 heads of 64 x 128, L
-    // 4096, f32 y: 423 us against 531; the scan of the gradients at batch 4,
-    // 16 heads of 128 x 128, L 2048: 94 against 107), not where CUs would
-    // idle (batch 1, 16 heads of 128 x 128, L 16384: 579 us against 397).
+    // 4096, f32 y: 356 us against 486; the scan of the gradients at batch 4,
+    // 16 heads of 128 x 128, L 2048: 92 against 105), not where CUs would
+    // idle (batch 1, 16 heads of 128 x 128, L 16384: 614 us against 421).
     // float32 inputs: K's planes and two blocks do not fit a CU's LDS.
     if constexpr (sizeof(Tin) == 2) {
         const int64_t blocks = ((KEEP ? pad : a.P) + 31) / 32;

@@ -2,8 +2,9 @@
 // index (philox.hpp): element i is kept when word i % 4 at counter i / 4 is
 // at least floor(p 2^32), and is then multiplied by 1 / (1 - p).  Reads and
 // writes each element once; the mask exists in registers only.  Ten rounds
-// for four elements keep the vector ALU 73 % busy, so at bf16 it is near bound
-// by both: 4 x 8192 x 5120 elements, 0.67 GB, 143 us (4.7 TB/s).
+// for four elements keep the vector ALU 72 % busy, so at bf16 it is near bound
+// by both: 4 x 8192 x 5120 elements, 0.67 GB, 144 to 157 us by card (4.3 to
+// 4.7 TB/s).
 #include "io.hpp"
 #include "kernels.hpp"
 #include "philox.hpp"

@@ -18,10 +18,17 @@
 // plain fp32 sum of all that a wave would get, thousands of short rows, is off
 // by 1e-4 where its roundings lean one way.
 //
-// Measured at 32768 rows of 2560, bf16 x and y, fp32 residual, dropout 0.1:
-// forward 204 us (1.0 GB, 4.9 TB/s), gradients 260 us (1.34 GB, 5.1 TB/s);
-// reading rows again took 760 and 642 us.  One row of 768 is the launch: 14 us
-// a call.
+// Measured at 32768 rows, bf16 x and y, fp32 residual, dropout 0.1:
+//
+//   dim    forward                  gradients
+//   2560   207 us (4.9 TB/s)        263 us (5.1 TB/s)
+//   4096   300 us (5.4 TB/s)        417 us (5.2 TB/s)
+//   2557   763 us                   553 us (417, 128 for dweight and dbias, 8)
+//
+// The last reads rows again: scalar loads, three passes in either direction,
+// and in the forward one ten-round generator call for each element and pass
+// (vector ALU 74 % busy).  One row of 768 is the launch: 16 us a call, 6 of
+// them the kernel's.
 #include <algorithm>
 
 #include "io.hpp"
@@ -330,7 +337,15 @@ __global__ __launch_bounds__(1024) void norm_wsum_kernel(const float* part, int 
 constexpr int kBlocks = 512;
 
 // Rows that a workgroup of the register kernels works on at a time: one wave
-// or four to a row.
+// or four to a row.  Past five pieces a lane the gradients' sums no longer fit
+// a wave's registers beside the row.  us, one wave / four, 2^26 elements, bf16
+// x and y, fp32 residual:
+//
+//   dim     512          1024         2048         2560         2816
+//   fwd     143 / 207    142 / 145    149 / 137    155 / 145    156 / 144
+//   grad    200 / 344    192 / 218    196 / 213    206 / 253    295 / 241
+//
+// One rule serves both directions: it is the gradients', the longer of them.
 int rows_at_once(int64_t dim) { return dim / 8 <= 5 * 64 ? 4 : 1; }
 
 // Waves per row and pieces per lane of the register kernels; 0: neither fits.
