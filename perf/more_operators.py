@@ -20,7 +20,7 @@ Norm, over the groups of a row:
 
     s = x + residual, or x silu(gate);   rstd = (mean s^2 + eps)^(-1/2);   y = s rstd weight
 
-and in 8 bits (e4m3), for each block of a row, scale = max(max |y| / 448,
+and in 8 bits (e4m3), for each block of a group, scale = max(max |y| / 448,
 2^-126) and y / scale rounded.
 """
 import math
@@ -50,7 +50,7 @@ def _conv(op, batch, seqlen, heads, groups, headdim, dstate, width, dtype, out, 
 
 
 def _norm(op, rows, dim, groups, dtype, res, out, gate=False, block=0):
-    """res: "" without a residual; block: of the 8-bit output's scales, 0 a row."""
+    """res: "" without a residual; block: of the 8-bit output's scales, 0 a group."""
     return {"op": op, "rows": rows, "dim": dim, "groups": groups, "dtype": dtype, "res": res, "out": out,
             "gate": gate, "block": block}
 
@@ -366,9 +366,10 @@ def _plain_rms_fwd(st):
     if st["out"] is not E4M3:
         out["y"] = y.to(st["out"])
         return out
-    y = _in_blocks(y, st["block"])
-    out["scale"] = torch.clamp(y.abs().amax(-1) / TOP8, min=LEAST_SCALE)
-    out["y"] = (y / out["scale"][..., None]).reshape(R, -1)[:, :D].to(E4M3)
+    y = _in_blocks(y.reshape(R * st["groups"], -1), st["block"])
+    scale = torch.clamp(y.abs().amax(-1, keepdim=True) / TOP8, min=LEAST_SCALE)
+    out["scale"] = scale.reshape(R, -1)
+    out["y"] = (y / scale).reshape(R * st["groups"], -1)[:, :D // st["groups"]].reshape(R, D).to(E4M3)
     return out
 
 
@@ -462,7 +463,8 @@ def work(case):
             # dy, s (or x and the gate) in; dx, dresidual, the gate's gradient, dweight out
             each = eo + es + (2 * es + es if case["gate"] else 3 * er if er else es)
             return {"bytes": n * each + small + 4 * D, "flops": (22 if case["gate"] else 10) * n}
-        scales = 4 * R * (-(-D // case["block"]) if case["block"] else 1) if case["out"] == "e4m3" else 0
+        groups = case["groups"]
+        scales = 4 * R * groups * (-(-(D // groups) // case["block"]) if case["block"] else 1) if case["out"] == "e4m3" else 0
         return {"bytes": n * (es + eo + 2 * er + (es if case["gate"] else 0)) + small + scales,
                 "flops": (10 if case["gate"] else 5) * n}
     B, L, H, P, N, K = (case[k] for k in ("batch", "seqlen", "heads", "headdim", "dstate", "width"))
@@ -582,10 +584,11 @@ def _exact_rms(st):
         if st["residual"] is not None:
             out["s"] = s
         if st["out"] is E4M3:
-            block = st["block"] or D
-            scale = torch.stack([y[:, i:i + block].abs().amax(1) / TOP8 for i in range(0, D, block)], 1)
-            out["scale"] = torch.clamp(scale, min=LEAST_SCALE)
-            y = y / out["scale"].repeat_interleave(block, 1)[:, :D]
+            width = D // groups
+            spans = [(g + i, g + min(i + (st["block"] or width), width)) for g in range(0, D, width)
+                     for i in range(0, width, st["block"] or width)]
+            out["scale"] = torch.clamp(torch.stack([y[:, i:j].abs().amax(1) / TOP8 for i, j in spans], 1), min=LEAST_SCALE)
+            y = torch.cat([y[:, i:j] / out["scale"][:, k, None] for k, (i, j) in enumerate(spans)], 1)
         out["y"] = y
         return out
     r = st["rstd"].double().repeat_interleave(D // groups, 1)
