@@ -21,7 +21,8 @@
  *
  * Conventions shared by every entry point
  *  - All tensor pointers are DEVICE pointers owned by the caller, dense and
- *    row-major in the layouts given below.  The library keeps no pointer after
+ *    row-major in the layouts given below (but for rows whose strides a shape
+ *    names).  The library keeps no pointer after
  *    a call returns.
  *  - `stream` is a hipStream_t passed as void* (NULL = the null stream).  Work
  *    is enqueued on it and the call returns without synchronising.  Faults
@@ -54,7 +55,8 @@ typedef enum {
 
 typedef enum {
     SELSCAN_F32 = 0,   /* IEEE binary32 */
-    SELSCAN_BF16 = 1   /* bfloat16 (upper half of a binary32); stores round to nearest even */
+    SELSCAN_BF16 = 1,  /* bfloat16 (upper half of a binary32); stores round to nearest even */
+    SELSCAN_E4M3 = 2   /* 8 bits, OCP e4m3 without infinities: an output of selscan_rms_norm_fwd alone */
 } selscan_dtype_t;
 
 /*
@@ -517,6 +519,215 @@ selscan_status_t selscan_layer_norm_bwd(const selscan_norm_shape_t* shape, const
                                         const float* weight, const float* mean, const float* rstd,
                                         const void* dresidual_out, void* dx, void* dresidual,
                                         float* dweight, float* dbias, void* stream);
+
+/*
+ * Short causal convolution of token-major rows, as the mixers take it in front
+ * of their scan: width K in 2..4 (UNSUPPORTED otherwise; selscan_conv1d has
+ * longer ones), rows read where a projection left them, the tokens before the
+ * first from a state, padded batches.  Per batch element b and channel d:
+ *
+ *     pre_t = bias[d] + sum_{k<K} weight[d,k] x[b,t-(K-1)+k,d]
+ *     out_t = pre_t sigmoid(pre_t) when silu == 1, else pre_t
+ *
+ * shape: x has seqlen rows of dim elements, a row x_row and a batch element
+ * x_batch elements after the one before (0 and more; any address of an
+ * element).  split: the outputs' channels, in order (dim in all); split[1] =
+ * split[2] = 0 for one output.
+ *   x          [B, L, D]     in_dtype   strided as above
+ *   weight     [D, K]        fp32
+ *   bias       [D]           fp32       NULL = 0
+ *   lengths    [B]           int32      as for selscan_delta_fwd: tokens past
+ *                                       the end are not read, their out is zero
+ *   state      [B, K-1, D]   in_dtype   the K - 1 tokens before the first,
+ *                                       oldest first; NULL = zero
+ *   y0, y1, y2 [B, L, split[i]] out_dtype (written; NULL where split[i] is 0)
+ *   last_state [B, K-1, D]   in_dtype   the last K - 1 tokens inside the
+ *                                       sequence, of `state` and x (written;
+ *                                       NULL = skip); may not alias state
+ * Sums and the activation are fp32.  No workspace (the field is the
+ * gradients').
+ */
+typedef struct {
+    int64_t batch, seqlen, dim, width;
+    int64_t x_row, x_batch;
+    int64_t split[3];
+    int32_t in_dtype, out_dtype;
+    void* workspace;
+    size_t workspace_bytes;
+} selscan_short_conv_shape_t;
+
+selscan_status_t selscan_short_conv_fwd(const selscan_short_conv_shape_t* shape, const void* x, const float* weight,
+                                        const float* bias, int silu, const int32_t* lengths, const void* state,
+                                        void* y0, void* y1, void* y2, void* last_state, void* stream);
+
+/* Bytes of workspace selscan_short_conv_bwd needs (0 on a bad shape). */
+size_t selscan_short_conv_bwd_workspace_bytes(const selscan_short_conv_shape_t* shape);
+
+/*
+ * Gradients of selscan_short_conv_fwd; what the activation needs is made again
+ * from x.
+ *   x .. state           as for selscan_short_conv_fwd
+ *   dout0, dout1, dout2  [B, L, split[i]]  out_dtype   gradients of y0, y1, y2
+ *                                          (not read past a sequence's end)
+ *   dlast_state          [B, K-1, D]       in_dtype    gradient of last_state; NULL = 0
+ *   dx                   [B, L, D]         in_dtype    (written; dense; zero past the end)
+ *   dweight              [D, K]            fp32        (written; NULL = skip)
+ *   dbias                [D]               fp32        (written; NULL = skip)
+ *   dstate               [B, K-1, D]       in_dtype    (written; NULL = skip)
+ * Gradients must not alias inputs or each other.  Sums run in a fixed order:
+ * results are reproducible bit for bit.  Workspace as for the other entry
+ * points; none where dweight and dbias are NULL.
+ */
+selscan_status_t selscan_short_conv_bwd(const selscan_short_conv_shape_t* shape, const void* x, const float* weight,
+                                        const float* bias, int silu, const int32_t* lengths, const void* state,
+                                        const void* dout0, const void* dout1, const void* dout2,
+                                        const void* dlast_state, void* dx, float* dweight, float* dbias, void* dstate,
+                                        void* stream);
+
+/* One token: x [B, D] (batch elements x_batch apart; seqlen, x_row and split
+ * ignored), y [B, D] out_dtype; state [B, K-1, D] in_dtype moves on in place. */
+selscan_status_t selscan_short_conv_step(const selscan_short_conv_shape_t* shape, void* state, const void* x,
+                                         const float* weight, const float* bias, int silu, void* y, void* stream);
+
+/*
+ * Mamba-2 mixer between its projections, for prompts: the short convolution
+ * with silu over xbc = (x, B, C), softplus of dt + dt_bias, and the Mamba-2
+ * scan, in one call; the convolution's result is not rounded to 16 bits on the
+ * way.  With v = silu(conv(xbc)) (selscan_short_conv_fwd) and x, B, C its
+ * channels in that order:
+ *
+ *     Delta_t = softplus(dt_t + dt_bias[h])
+ *     S_t = exp(Delta_t A[h]) S_{t-1} + Delta_t x_t B_t^T,  S_{-1} = h0
+ *     y_t = S_t C_t + D[h] x_t
+ *
+ *   xbc         [B, L, H P + 2 G N]  in_dtype   rows xbc_row, batch elements
+ *                                               xbc_batch elements apart
+ *   dt          [B, L, H]            in_dtype   the same with dt_row, dt_batch
+ *   conv_weight [H P + 2 G N, K]     fp32       K in 2..4
+ *   conv_bias   [H P + 2 G N]        fp32       NULL = 0
+ *   A           [H]                  fp32       normally < 0
+ *   D, dt_bias  [H]                  fp32       NULL = 0
+ *   lengths     [B]                  int32      tokens of each batch element,
+ *                                               clamped to 0..L; NULL = L.
+ *                                               Tokens past the end are not
+ *                                               read, their y is zero, and the
+ *                                               states are those after the last
+ *                                               token inside
+ *   h0          [B, H, P, N]         fp32       NULL = zero
+ *   conv_state  [B, K-1, H P + 2 G N] in_dtype  NULL = zero
+ *   y           [B, L, H, P]         out_dtype  (written)
+ *   last_state  [B, H, P, N]         fp32       (written; NULL = skip); may not alias h0
+ *   last_conv_state                  in_dtype   as conv_state (written; NULL =
+ *                                               skip); may not alias it
+ *
+ * N in {16, 32, 64, 128}.  State, decays and sums are fp32, and so are products
+ * in effect.  The sequence is worked on in chunks of 64 tokens: a NaN or
+ * infinity in a token reaches every y of its chunk and head, and what follows.
+ * Workspace as for the other entry points.
+ */
+typedef struct {
+    int64_t batch, seqlen, nheads, headdim, ngroups, dstate, width;
+    int64_t xbc_row, xbc_batch, dt_row, dt_batch;
+    int32_t in_dtype, out_dtype;
+    void* workspace;
+    size_t workspace_bytes;
+} selscan_m2_conv_shape_t;
+
+size_t selscan_mamba2_conv_workspace_bytes(const selscan_m2_conv_shape_t* shape);
+
+selscan_status_t selscan_mamba2_conv_fwd(const selscan_m2_conv_shape_t* shape, const void* xbc, const void* dt,
+                                         const float* conv_weight, const float* conv_bias, const float* A,
+                                         const float* D, const float* dt_bias, const int32_t* lengths,
+                                         const float* h0, const void* conv_state, void* y, float* last_state,
+                                         void* last_conv_state, void* stream);
+
+/*
+ * The mixer for one token: xbc [B, H P + 2 G N] (batch elements xbc_batch
+ * apart), dt [B, H] (dt_batch apart), y [B, H, P]; state [B, H, P, N] fp32
+ * (16-byte aligned) and conv_state [B, K-1, H P + 2 G N] are updated in place.
+ * seqlen, xbc_row, dt_row and workspace are ignored.
+ */
+selscan_status_t selscan_mamba2_conv_step(const selscan_m2_conv_shape_t* shape, float* state, void* conv_state,
+                                          const void* xbc, const void* dt, const float* conv_weight,
+                                          const float* conv_bias, const float* A, const float* D,
+                                          const float* dt_bias, void* y, void* stream);
+
+/*
+ * RMS norm with the residual sum or the mixer's gate in front of it, and an
+ * output in 8 bits with scales.  For each row and group (groups of width = dim
+ * / groups elements; 1 = the row):
+ *
+ *     s    = x + residual                    or, with a gate, x gate sigmoid(gate)
+ *     rstd = 1 / sqrt(sum s^2 / width + eps)
+ *     y    = s rstd weight
+ *
+ * and where out_dtype is SELSCAN_E4M3, for each block of scale_block elements
+ * of a group (the last one may be shorter; 0: the group):
+ *
+ *     scale = max(max |y| / 448, 2^-126);  y8 = y / scale, rounded to nearest even
+ *
+ * (a NaN makes its block's scale NaN).
+ *   x            [rows, dim]  in_dtype
+ *   residual     [rows, dim]  res_dtype   NULL = 0
+ *   gate         [rows, dim]  in_dtype    rows gate_row elements apart; NULL =
+ *                                         none; not with a residual (UNSUPPORTED)
+ *   weight       [dim]        fp32        NULL = 1
+ *   y            [rows, dim]  out_dtype   (written); may be x where their types
+ *                                         agree
+ *   residual_out [rows, dim]  res_dtype   s (written; NULL = skip; not with a
+ *                                         gate); may be residual
+ *   rstd         [rows, groups] fp32      (written; NULL = skip)
+ *   scale        [rows, groups ceil(width / scale_block)]  fp32  (written with
+ *                                         E4M3, where it is required)
+ * scale_block: 0, 32, 64, 128, 256 or 512.  Sums are fp32 over s before it is
+ * rounded.  rows, dim, groups >= 1, dim % groups == 0.  Workspace is used by
+ * the gradients only.
+ */
+typedef struct {
+    int64_t rows, dim, groups, gate_row, scale_block;
+    int32_t in_dtype, res_dtype, out_dtype;
+    float eps;
+    void* workspace;
+    size_t workspace_bytes;
+} selscan_rms_shape_t;
+
+selscan_status_t selscan_rms_norm_fwd(const selscan_rms_shape_t* shape, const void* x, const void* residual,
+                                      const void* gate, const float* weight, void* y, void* residual_out, float* rstd,
+                                      float* scale, void* stream);
+
+/* Bytes of workspace selscan_rms_norm_bwd needs (0 on a bad shape). */
+size_t selscan_rms_norm_bwd_workspace_bytes(const selscan_rms_shape_t* shape);
+
+/*
+ * Gradients of selscan_rms_norm_fwd:
+ *
+ *     w  = dy weight;  xhat = s rstd
+ *     ds = rstd (w - xhat sum (w xhat) / width) + dresidual_out
+ *     without a gate  dx = ds, dresidual = ds;    with one (s made again from
+ *     x and gate)     dx = ds silu(gate), dgate = ds x silu'(gate)
+ *     dweight = sum_r dy xhat
+ *
+ *   dy            [rows, dim]  out_dtype   (FP32 or BF16: the gradient of an
+ *                                          8-bit y is that of its value)
+ *   s             [rows, dim]  res_dtype   as written to residual_out (x itself
+ *                                          without a residual); with a gate x,
+ *                                          and res_dtype is in_dtype
+ *   gate, weight               as in the forward call
+ *   rstd          [rows, groups] fp32
+ *   dresidual_out [rows, dim]  res_dtype   gradient of s from its other uses;
+ *                                          NULL = 0; not with a gate
+ *   dx            [rows, dim]  in_dtype    (written; NULL = skip)
+ *   dresidual     [rows, dim]  res_dtype   (written; NULL = skip); may be
+ *                                          dresidual_out; not with a gate
+ *   dgate         [rows, dim]  in_dtype    (written; NULL = skip); with a gate only
+ *   dweight       [dim]        fp32        (written; NULL = skip)
+ * Sums over rows run in a fixed order: results are reproducible bit for bit.
+ * Workspace as for the other entry points; none where dweight is NULL.
+ */
+selscan_status_t selscan_rms_norm_bwd(const selscan_rms_shape_t* shape, const void* dy, const void* s,
+                                      const void* gate, const float* weight, const float* rstd,
+                                      const void* dresidual_out, void* dx, void* dresidual, void* dgate,
+                                      float* dweight, void* stream);
 
 /* Message for the last failed call on this thread ("" after a success).
  * The string stays valid until the next call on the same thread. */

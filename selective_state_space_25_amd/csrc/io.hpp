@@ -52,6 +52,40 @@ __device__ __forceinline__ void st8(uint16_t* p, const float* v) {
                                               pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
 }
 
+// V consecutive elements wherever they start: as loaded, widened, stored.
+// Global memory takes 16-byte accesses at any element's address on this GPU
+// (only a whole piece has to be inside the tensor).
+template <typename T, int V> struct Piece {
+    typedef T Vec __attribute__((ext_vector_type(V)));
+    struct __attribute__((packed, may_alias, aligned(sizeof(T)))) Loose { Vec v; };
+    Vec v;
+    __device__ __forceinline__ void get(const T* p) { v = reinterpret_cast<const Loose*>(p)->v; }
+    __device__ __forceinline__ void zero() { v = Vec(0); }
+    __device__ __forceinline__ void widen(float* f) const {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (sizeof(T) == 2) f[i] = bf16_to_f32((uint16_t)v[i]);
+            else f[i] = v[i];
+        }
+    }
+    __device__ __forceinline__ void narrow(const float* f) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            if constexpr (sizeof(T) == 2) v[i] = f32_to_bf16(f[i]);
+            else v[i] = f[i];
+        }
+    }
+    __device__ __forceinline__ void put(T* p) const { reinterpret_cast<Loose*>(p)->v = v; }
+};
+template <typename T> struct Piece<T, 1> {
+    T v;
+    __device__ __forceinline__ void get(const T* p) { v = *p; }
+    __device__ __forceinline__ void zero() { v = T(0); }
+    __device__ __forceinline__ void widen(float* f) const { f[0] = ld(&v); }
+    __device__ __forceinline__ void narrow(const float* f) { st(&v, f[0]); }
+    __device__ __forceinline__ void put(T* p) const { *p = v; }
+};
+
 // Workgroups 0 .. n - 1 over two dimensions (a dimension holds fewer than
 // 2^32 threads): those past n are for the kernel to turn away.
 inline dim3 groups(int64_t n) {

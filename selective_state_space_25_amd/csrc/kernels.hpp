@@ -254,6 +254,86 @@ hipError_t launch_delta_keep(const DeltaArgs& a, int in_bf16, const char* recs, 
                              hipStream_t stream);
 hipError_t launch_delta_bwd(const DeltaBwdArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
 
+// Short causal convolution of token-major rows (x [batch, L, C], rows x_row
+// and batch elements x_batch elements apart; weight [C, K]; states [batch,
+// K - 1, C]).  y and dout are split into up to three dense tensors: channels
+// from 0, begin[1], begin[2] on (begin[i] = C: no more pieces).
+struct ShortConvArgs {
+    const void* x;
+    int64_t x_row, x_batch;
+    const float* weight;
+    const float* bias;        // NULL = 0
+    const int32_t* lengths;   // tokens of each batch element, or NULL
+    const void* state;        // NULL = zero
+    void* y[3];
+    void* last;               // the state after; one token: the state, in place
+    const void* dout[3];
+    const void* dlast;        // NULL = zero
+    void* dx;
+    void* dstate;             // NULL = skip
+    float *dweight, *dbias;   // NULL = skip
+    float* part;              // [batch run_blocks, K + 1, C] sums of the taps' and the bias' gradients
+    int64_t begin[3];
+    int64_t batch, L, C;
+    int K, silu;
+    int V, cols;              // short_conv_plan: channels a thread, columns a workgroup,
+    int64_t run, col_blocks, run_blocks;   // tokens a run, workgroups over the channels and over the tokens
+};
+void short_conv_plan(ShortConvArgs& a, bool bwd);
+hipError_t launch_short_conv_fwd(const ShortConvArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
+hipError_t launch_short_conv_bwd(const ShortConvArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
+hipError_t launch_short_conv_step(const ShortConvArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
+
+// Sums of the columns of n partial rows of n0 + n1 fp32: the first n0 to out0,
+// the others to out1 (NULL = skip).  `part` has column_sums_rows(n) rows.
+int64_t column_sums_rows(int64_t n);
+hipError_t launch_column_sums(float* part, int64_t n, int64_t n0, int64_t n1, float* out0, float* out1, hipStream_t stream);
+
+// Mamba-2 with the short convolution in front (xbc [batch, L, H P + 2 G N], dt
+// [batch, L, H], strided; y [batch, L, H, P] dense; states [batch, H, P, N]
+// fp32 and [batch, K - 1, H P + 2 G N]).
+struct M2ConvArgs {
+    ShortConvArgs conv;       // of xbc; y unused
+    const void* dt;
+    int64_t dt_row, dt_batch;
+    const float* A;
+    const float* D;           // NULL = 0
+    const float* dt_bias;     // NULL = 0
+    const float* h0;          // NULL = zero
+    void* y;
+    float* last;              // NULL = skip; one token: the state, in place
+    int64_t batch, L, H, P, G, N;
+};
+// Bytes of workspace of the sequence form.
+size_t m2_conv_bytes(const M2ConvArgs& a);
+hipError_t launch_m2_conv(const M2ConvArgs& a, int in_bf16, int out_bf16, void* ws, hipStream_t stream);
+hipError_t launch_m2_conv_step(const M2ConvArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
+
+// RMS norm of s = x + residual, or s = x silu(gate), over the groups of a row.
+struct RmsArgs {
+    const void* x;            // forward: x; gradients: dy
+    const void* res;          // forward: residual or NULL; gradients: s, or x where there is a gate
+    const void* gate;         // rows gate_row elements apart, or NULL
+    const float* weight;      // NULL = 1
+    const float* rstd_in;     // gradients: [rows, groups]
+    const void* dres_in;      // gradients: of s from its other uses, or NULL
+    void* y;                  // forward: y; gradients: dx
+    void* res_out;            // forward: s; gradients: dresidual
+    void* dgate;
+    float* rstd;
+    float* scale;             // forward in 8 bits: [rows, blocks of a row]
+    float* dweight;
+    float* part;              // gradients: [blocks, dim] partial sums of dweight, and room to add them up
+    int64_t rows, dim, gate_row, groups, width;   // width: of a group, dim / groups
+    int64_t block, row_blocks;   // elements to a scale, scales to a row
+    int blocks;               // gradients: workgroups to a group
+    float eps, inv_width;
+};
+size_t rms_bwd_part_bytes(int64_t rows, int64_t dim, int64_t groups);
+int rms_bwd_blocks(int64_t rows, int64_t width);
+hipError_t launch_rms_fwd(const RmsArgs& a, int in_bf16, int res_bf16, int out_dtype, hipStream_t stream);
+hipError_t launch_rms_bwd(const RmsArgs& a, int in_bf16, int res_bf16, int out_bf16, hipStream_t stream);
+
 // Layer norm with dropout and residual sum in front.
 struct NormArgs {
     const void* x;            // forward: x; gradients: dy

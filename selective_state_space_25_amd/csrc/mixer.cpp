@@ -1,0 +1,266 @@
+// mixer.cpp -- host side of the short convolution and of the Mamba-2 mixer
+// with it in front: argument checks, plans and workspace.
+#include <hip/hip_runtime.h>
+
+#include <string>
+
+#include "host.hpp"
+#include "kernels.hpp"
+#include "selscan.h"
+
+using namespace selscan::host;
+using selscan::set_error;
+
+namespace {
+
+constexpr int64_t kMostGroups = (int64_t)1 << 35;   // workgroups of a launch over two grid dimensions
+
+bool is_dtype(int32_t d) { return d == SELSCAN_F32 || d == SELSCAN_BF16; }
+
+selscan_status_t check_width(int64_t width) {
+    if (width < 1) return set_error(SELSCAN_ERR_INVALID_ARG, "width must be >= 1");
+    if (width < 2 || width > 4) return set_error(SELSCAN_ERR_UNSUPPORTED, "the short convolution supports width 2, 3, 4");
+    return SELSCAN_OK;
+}
+
+// Rows of `dim` elements, strided: the byte offset of the last one fits.
+bool strides_fit(int64_t batch, int64_t b_stride, int64_t rows, int64_t stride, int64_t dim) {
+    if (b_stride < 0 || stride < 0) return false;
+    const int64_t x = mul_checked({batch, b_stride}), y = mul_checked({rows, stride});
+    return x >= 0 && y >= 0 && x < INT64_MAX / 16 && y < INT64_MAX / 16 && dim < INT64_MAX / 16;
+}
+
+enum Use { kSequence, kGrad, kToken };
+
+void fill(selscan::ShortConvArgs& a, const selscan_short_conv_shape_t* s, Use use) {
+    a.batch = s->batch; a.L = use == kToken ? 1 : s->seqlen; a.C = s->dim; a.K = (int)s->width;
+    a.x_row = s->x_row; a.x_batch = s->x_batch;
+    a.begin[0] = 0;
+    a.begin[1] = use == kToken ? s->dim : s->split[0];
+    a.begin[2] = use == kToken ? s->dim : s->split[0] + s->split[1];
+    selscan::short_conv_plan(a, use == kGrad);
+}
+
+selscan_status_t check_conv(const selscan_short_conv_shape_t* s, Use use) {
+    if (!s) return set_error(SELSCAN_ERR_INVALID_ARG, "shape is NULL");
+    const int64_t L = use == kToken ? 1 : s->seqlen;
+    if (s->batch < 1 || L < 1 || s->dim < 1) return set_error(SELSCAN_ERR_INVALID_ARG, "batch, seqlen and dim must be >= 1");
+    selscan_status_t st = check_width(s->width);
+    if (st != SELSCAN_OK) return st;
+    if (!is_dtype(s->in_dtype) || !is_dtype(s->out_dtype))
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "dtypes must be SELSCAN_F32 or SELSCAN_BF16");
+    if (mul_checked({s->batch, L, s->dim, 4}) < 0 || mul_checked({s->batch, s->dim, 16}) < 0)
+        return set_error(SELSCAN_ERR_INVALID_ARG, "tensor sizes overflow 64-bit byte counts");
+    if (!strides_fit(s->batch, s->x_batch, L, use == kToken ? 0 : s->x_row, s->dim))
+        return set_error(SELSCAN_ERR_INVALID_ARG, "x_row and x_batch must be >= 0 and their offsets fit 64 bits");
+    if (use != kToken) {
+        if (s->split[0] < 1 || s->split[1] < 0 || s->split[2] < 0 || s->split[0] > s->dim || s->split[1] > s->dim ||
+            s->split[2] > s->dim || s->split[0] + s->split[1] + s->split[2] != s->dim)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "split must be channels of the outputs, dim in all, the first >= 1");
+        selscan::ShortConvArgs a{};
+        fill(a, s, use);
+        const int64_t blocks = mul_checked({a.batch, a.run_blocks, a.col_blocks});
+        if (blocks < 0 || blocks > kMostGroups ||
+            (use == kGrad && mul_checked({a.batch, a.run_blocks, s->width + 1, s->dim, 8}) < 0))
+            return set_error(SELSCAN_ERR_UNSUPPORTED, "too many elements for one launch");
+    }
+    if (s->dim > (int64_t)1 << 32 || s->batch > (int64_t)1 << 31 ||
+        mul_checked({s->batch, s->dim}) / 256 > kMostGroups)
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "the short convolution supports dim <= 2^32 and batch <= 2^31");
+    return SELSCAN_OK;
+}
+
+size_t conv_part_bytes(const selscan::ShortConvArgs& a) {
+    return align256((size_t)selscan::column_sums_rows(a.batch * a.run_blocks) * (size_t)((a.K + 1) * a.C) * 4);
+}
+
+selscan_status_t launched(hipError_t e) {
+    if (e != hipSuccess)
+        return set_error(SELSCAN_ERR_LAUNCH, std::string("kernel launch failed: ") + hipGetErrorString(e));
+    return set_error(SELSCAN_OK, "");
+}
+
+selscan_status_t check_mixer(const selscan_m2_conv_shape_t* s, bool token) {
+    if (!s) return set_error(SELSCAN_ERR_INVALID_ARG, "shape is NULL");
+    const int64_t L = token ? 1 : s->seqlen;
+    if (s->batch < 1 || L < 1 || s->nheads < 1 || s->headdim < 1 || s->ngroups < 1 || s->dstate < 1)
+        return set_error(SELSCAN_ERR_INVALID_ARG, "batch, seqlen, nheads, headdim, ngroups, dstate must be >= 1");
+    if (s->nheads % s->ngroups != 0) return set_error(SELSCAN_ERR_INVALID_ARG, "nheads must be a multiple of ngroups");
+    if (s->dstate != 16 && s->dstate != 32 && s->dstate != 64 && s->dstate != 128)
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "the Mamba-2 mixer supports dstate 16, 32, 64, 128");
+    selscan_status_t st = check_width(s->width);
+    if (st != SELSCAN_OK) return st;
+    if (!is_dtype(s->in_dtype) || !is_dtype(s->out_dtype))
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "dtypes must be SELSCAN_F32 or SELSCAN_BF16");
+    const int64_t hp = mul_checked({s->nheads, s->headdim}), gn = mul_checked({s->ngroups, s->dstate});
+    if (hp < 0 || gn < 0 || hp > INT64_MAX / 4 || gn > INT64_MAX / 8 || mul_checked({s->batch, L, hp + 2 * gn, 4}) < 0 ||
+        mul_checked({s->batch, hp, s->dstate, 4}) < 0 || mul_checked({s->batch, hp + 2 * gn, 16}) < 0)
+        return set_error(SELSCAN_ERR_INVALID_ARG, "tensor sizes overflow 64-bit byte counts");
+    if (!strides_fit(s->batch, s->xbc_batch, L, token ? 0 : s->xbc_row, hp + 2 * gn) ||
+        !strides_fit(s->batch, s->dt_batch, L, token ? 0 : s->dt_row, s->nheads))
+        return set_error(SELSCAN_ERR_INVALID_ARG, "strides must be >= 0 and their offsets fit 64 bits");
+    if (hp + 2 * gn > (int64_t)1 << 22 || mul_checked({s->batch, s->nheads, (s->headdim + 15) / 16}) > kMostGroups ||
+        s->batch > (int64_t)1 << 31)
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "the Mamba-2 mixer supports up to 2^22 channels of xbc, and rows of states for one launch");
+    return SELSCAN_OK;
+}
+
+void fill(selscan::M2ConvArgs& a, const selscan_m2_conv_shape_t* s, bool token) {
+    a.batch = s->batch; a.L = token ? 1 : s->seqlen; a.H = s->nheads; a.P = s->headdim; a.G = s->ngroups; a.N = s->dstate;
+    a.dt_row = s->dt_row; a.dt_batch = s->dt_batch;
+    a.conv.batch = a.batch; a.conv.L = a.L; a.conv.C = a.H * a.P + 2 * a.G * a.N; a.conv.K = (int)s->width;
+    a.conv.x_row = s->xbc_row; a.conv.x_batch = s->xbc_batch;
+    a.conv.silu = 1;
+    a.conv.begin[0] = 0;
+    a.conv.begin[1] = token ? a.conv.C : a.H * a.P;
+    a.conv.begin[2] = token ? a.conv.C : a.H * a.P + a.G * a.N;
+    selscan::short_conv_plan(a.conv, false);
+}
+
+}  // namespace
+
+extern "C" {
+
+selscan_status_t selscan_short_conv_fwd(const selscan_short_conv_shape_t* s, const void* x, const float* weight,
+                                        const float* bias, int silu, const int32_t* lengths, const void* state, void* y0,
+                                        void* y1, void* y2, void* last_state, void* stream) {
+    try {
+        selscan_status_t st = check_conv(s, kSequence);
+        if (st != SELSCAN_OK) return st;
+        if (!x || !weight || !y0 || (s->split[1] && !y1) || (s->split[2] && !y2))
+            return set_error(SELSCAN_ERR_INVALID_ARG, "x, weight and the outputs of split must be non-NULL");
+        if (silu != 0 && silu != 1) return set_error(SELSCAN_ERR_INVALID_ARG, "silu must be 0 or 1");
+        if (state && state == last_state) return set_error(SELSCAN_ERR_INVALID_ARG, "state and last_state must not alias");
+        st = device_check();
+        if (st != SELSCAN_OK) return st;
+        selscan::ShortConvArgs a{};
+        fill(a, s, kSequence);
+        a.x = x; a.weight = weight; a.bias = bias; a.silu = silu; a.lengths = lengths; a.state = state;
+        a.y[0] = y0; a.y[1] = y1; a.y[2] = y2; a.last = last_state;
+        return launched(selscan::launch_short_conv_fwd(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16,
+                                                       reinterpret_cast<hipStream_t>(stream)));
+    } catch (...) {
+        return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
+    }
+}
+
+size_t selscan_short_conv_bwd_workspace_bytes(const selscan_short_conv_shape_t* s) {
+    if (check_conv(s, kGrad) != SELSCAN_OK) return 0;
+    selscan::ShortConvArgs a{};
+    fill(a, s, kGrad);
+    return conv_part_bytes(a);
+}
+
+selscan_status_t selscan_short_conv_bwd(const selscan_short_conv_shape_t* s, const void* x, const float* weight,
+                                        const float* bias, int silu, const int32_t* lengths, const void* state,
+                                        const void* dout0, const void* dout1, const void* dout2, const void* dlast_state,
+                                        void* dx, float* dweight, float* dbias, void* dstate, void* stream) {
+    try {
+        selscan_status_t st = check_conv(s, kGrad);
+        if (st != SELSCAN_OK) return st;
+        if (!x || !weight || !dx || !dout0 || (s->split[1] && !dout1) || (s->split[2] && !dout2))
+            return set_error(SELSCAN_ERR_INVALID_ARG, "x, weight, dx and the gradients of split must be non-NULL");
+        if (silu != 0 && silu != 1) return set_error(SELSCAN_ERR_INVALID_ARG, "silu must be 0 or 1");
+        st = device_check();
+        if (st != SELSCAN_OK) return st;
+        hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+        selscan::ShortConvArgs a{};
+        fill(a, s, kGrad);
+        Scratch ws;
+        st = ws.get(s->workspace, s->workspace_bytes, dweight || dbias ? conv_part_bytes(a) : 0, hs);
+        if (st != SELSCAN_OK) return st;
+        a.x = x; a.weight = weight; a.bias = bias; a.silu = silu; a.lengths = lengths; a.state = state;
+        a.dout[0] = dout0; a.dout[1] = dout1; a.dout[2] = dout2; a.dlast = dlast_state;
+        a.dx = dx; a.dweight = dweight; a.dbias = dbias; a.dstate = dstate;
+        a.part = static_cast<float*>(ws.ptr);
+        const hipError_t e = selscan::launch_short_conv_bwd(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16, hs);
+        ws.release();
+        return launched(e);
+    } catch (...) {
+        return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
+    }
+}
+
+selscan_status_t selscan_short_conv_step(const selscan_short_conv_shape_t* s, void* state, const void* x,
+                                         const float* weight, const float* bias, int silu, void* y, void* stream) {
+    try {
+        selscan_status_t st = check_conv(s, kToken);
+        if (st != SELSCAN_OK) return st;
+        if (!state || !x || !weight || !y)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "state, x, weight and y must be non-NULL");
+        if (silu != 0 && silu != 1) return set_error(SELSCAN_ERR_INVALID_ARG, "silu must be 0 or 1");
+        st = device_check();
+        if (st != SELSCAN_OK) return st;
+        selscan::ShortConvArgs a{};
+        fill(a, s, kToken);
+        a.x = x; a.weight = weight; a.bias = bias; a.silu = silu; a.last = state; a.y[0] = y;
+        return launched(selscan::launch_short_conv_step(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16,
+                                                        reinterpret_cast<hipStream_t>(stream)));
+    } catch (...) {
+        return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
+    }
+}
+
+size_t selscan_mamba2_conv_workspace_bytes(const selscan_m2_conv_shape_t* s) {
+    if (check_mixer(s, false) != SELSCAN_OK) return 0;
+    selscan::M2ConvArgs a{};
+    fill(a, s, false);
+    return selscan::m2_conv_bytes(a);
+}
+
+selscan_status_t selscan_mamba2_conv_fwd(const selscan_m2_conv_shape_t* s, const void* xbc, const void* dt,
+                                         const float* conv_weight, const float* conv_bias, const float* A, const float* D,
+                                         const float* dt_bias, const int32_t* lengths, const float* h0,
+                                         const void* conv_state, void* y, float* last_state, void* last_conv_state,
+                                         void* stream) {
+    try {
+        selscan_status_t st = check_mixer(s, false);
+        if (st != SELSCAN_OK) return st;
+        if (!xbc || !dt || !conv_weight || !A || !y)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "xbc, dt, conv_weight, A and y must be non-NULL");
+        if (h0 && h0 == last_state) return set_error(SELSCAN_ERR_INVALID_ARG, "h0 and last_state must not alias");
+        if (conv_state && conv_state == last_conv_state)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "conv_state and last_conv_state must not alias");
+        st = device_check();
+        if (st != SELSCAN_OK) return st;
+        hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
+        selscan::M2ConvArgs a{};
+        fill(a, s, false);
+        Scratch ws;
+        st = ws.get(s->workspace, s->workspace_bytes, selscan::m2_conv_bytes(a), hs);
+        if (st != SELSCAN_OK) return st;
+        a.conv.x = xbc; a.conv.weight = conv_weight; a.conv.bias = conv_bias; a.conv.lengths = lengths;
+        a.conv.state = conv_state; a.conv.last = last_conv_state;
+        a.dt = dt; a.A = A; a.D = D; a.dt_bias = dt_bias; a.h0 = h0; a.y = y; a.last = last_state;
+        const hipError_t e = selscan::launch_m2_conv(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16, ws.ptr, hs);
+        ws.release();
+        return launched(e);
+    } catch (...) {
+        return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
+    }
+}
+
+selscan_status_t selscan_mamba2_conv_step(const selscan_m2_conv_shape_t* s, float* state, void* conv_state, const void* xbc,
+                                          const void* dt, const float* conv_weight, const float* conv_bias, const float* A,
+                                          const float* D, const float* dt_bias, void* y, void* stream) {
+    try {
+        selscan_status_t st = check_mixer(s, true);
+        if (st != SELSCAN_OK) return st;
+        if (!state || !conv_state || !xbc || !dt || !conv_weight || !A || !y)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "state, conv_state, xbc, dt, conv_weight, A and y must be non-NULL");
+        if (!aligned16(state)) return set_error(SELSCAN_ERR_INVALID_ARG, "state must be 16-byte aligned");
+        st = device_check();
+        if (st != SELSCAN_OK) return st;
+        selscan::M2ConvArgs a{};
+        fill(a, s, true);
+        a.conv.x = xbc; a.conv.weight = conv_weight; a.conv.bias = conv_bias;
+        a.conv.state = conv_state; a.conv.last = conv_state;
+        a.dt = dt; a.A = A; a.D = D; a.dt_bias = dt_bias; a.last = state; a.y = y;
+        return launched(selscan::launch_m2_conv_step(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16,
+                                                     reinterpret_cast<hipStream_t>(stream)));
+    } catch (...) {
+        return set_error(SELSCAN_ERR_LAUNCH, "unexpected host exception");
+    }
+}
+
+}  // extern "C"

@@ -1,0 +1,203 @@
+"""The Mamba-2 mixer on the GPU: prompts and single tokens against the fp64
+oracle.
+
+Bound, in roundings (2^-24) of the oracle's magnitudes (products of the
+convolution's terms' absolute values, decayed): 16 for each of x, B, C, a few
+for the step and its decay, and what sums over a sequence of L tokens add, at
+most 4 a token: 96 + 4 L.  A decay's exponent is off by roundings of itself,
+whose weight falls as fast as it grows.
+"""
+import pytest
+import torch
+
+import selective_state_space_25_amd as ss
+from mixer_close import close
+from oracle import mixer_ops as ops
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+DEV = "cuda:0"
+
+
+def rnd(gen, *shape, dtype=F32, scale=1.0):
+    return (scale * torch.randn(shape, generator=gen)).to(dtype).to(DEV)
+
+
+class Inputs:
+    def __init__(self, B, L, H, G, P, N, K, dtype, seed=1, states=True, bias=True):
+        gen = self.gen = torch.Generator().manual_seed(seed)
+        C, self.G, self.N = H * P + 2 * G * N, G, N
+        rows = rnd(gen, B, L, 3 + C + H, dtype=dtype)       # one projection's result
+        self.xbc, self.dt = rows[..., 3:3 + C], rows[..., 3 + C:]
+        self.w, self.b = rnd(gen, C, K, scale=K ** -0.5), rnd(gen, C, scale=0.3) if bias else None
+        self.A = -torch.exp(rnd(gen, H))
+        self.D = rnd(gen, H) if bias else None
+        self.dtb = rnd(gen, H) - 2 if bias else None
+        self.h0 = rnd(gen, B, H, P, N, scale=0.3) if states else None
+        self.cs = rnd(gen, B, K - 1, C, dtype=dtype) if states else None
+
+    def fwd(self, out=F32, lengths=None, **kw):
+        return ss.mamba2_conv_fwd(self.xbc, self.dt, self.w, self.b, self.A, self.D, self.dtb, ngroups=self.G, dstate=self.N,
+                                  lengths=None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV),
+                                  h0=self.h0, conv_state=self.cs, out_dtype=out, **kw)
+
+    def ref(self, lengths=None):
+        return ops.mixer(self.xbc, self.dt, self.w, self.b, self.A, self.D, self.dtb, self.G, self.N, lengths, self.h0, self.cs)
+
+
+SHAPES = [  # B, L, H, G, P, N, K
+    (1, 1, 2, 1, 64, 128, 4), (2, 15, 4, 2, 16, 16, 4), (1, 64, 2, 1, 64, 64, 4), (2, 65, 3, 1, 48, 128, 3), (1, 130, 4, 4, 80, 32, 2),
+    (3, 200, 2, 1, 64, 128, 4), (1, 333, 8, 2, 33, 64, 3), (2, 129, 2, 2, 128, 16, 4), (1, 100, 1, 1, 1, 128, 4)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("ragged", [False, True])
+def test_prompt(gpu, shape, dtype, out, ragged):
+    B, L = shape[:2]
+    i = Inputs(*shape, dtype, states=ragged, bias=shape[3] == 1)
+    lengths = ([L, 1, 0] if B > 2 else [L // 2, L + 7] if B > 1 else [L - 1])[:B] if ragged else None
+    y, S, cs = i.fwd(out, lengths)
+    torch.cuda.synchronize()
+    (ry, rS, rcs), (my, mS) = i.ref(lengths)
+    close(y, ry, my, 96 + 4 * L, "y")
+    close(S, rS, mS, 96 + 4 * L, "state")
+    assert torch.equal(cs.cpu().double(), rcs)
+
+
+@pytest.mark.parametrize("shape", [(1, 4, 32, 1, 64, 128, 4), (3, 4, 4, 2, 48, 64, 3), (65, 4, 8, 1, 64, 128, 4), (2, 4, 3, 3, 20, 16, 2),
+                                   (1, 4, 2, 1, 1, 32, 4), (9, 4, 16, 1, 100, 128, 4)])
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
+def test_tokens_continue_a_prompt(gpu, shape, dtype, out):
+    i = Inputs(*shape, dtype, bias=shape[3] != 3)
+    (ry, rS, rcs), (my, mS) = i.ref()
+    xbc, dt = i.xbc, i.dt
+    i.xbc, i.dt = xbc[:, :2], dt[:, :2]
+    _, S, cs = i.fwd()
+    for t in (2, 3):
+        y = ss.mamba2_conv_step(S, cs, xbc[:, t], dt[:, t], i.w, i.b, i.A, i.D, i.dtb, out_dtype=out)
+        torch.cuda.synchronize()
+        close(y, ry[:, t], my[:, t], 112, f"token {t}")
+    close(S, rS, mS, 112, "state")
+    assert torch.equal(cs.cpu().double(), rcs)
+    S2, cs2 = S.clone(), cs.clone()
+    call, y2 = ss.bind_mamba2_conv_step(S2, cs2, xbc[:, 0], dt[:, 0], i.w, i.b, i.A, i.D, i.dtb, out_dtype=out)
+    call()
+    y = ss.mamba2_conv_step(S, cs, xbc[:, 0], dt[:, 0], i.w, i.b, i.A, i.D, i.dtb, out_dtype=out)
+    assert torch.equal(y, y2) and torch.equal(S, S2) and torch.equal(cs, cs2)
+
+
+def test_prompt_in_two_parts(gpu):
+    shape = (2, 150, 2, 1, 64, 128, 4)
+    i = Inputs(*shape, BF16)
+    (ry, rS, rcs), (my, mS) = i.ref()
+    xbc, dt = i.xbc, i.dt
+    i.xbc, i.dt = xbc[:, :70], dt[:, :70]
+    y0, S, cs = i.fwd()
+    i.xbc, i.dt, i.h0, i.cs = xbc[:, 70:], dt[:, 70:], S, cs
+    y1, S, cs = i.fwd()
+    torch.cuda.synchronize()
+    close(torch.cat([y0, y1], 1), ry, my, 96 + 600, "y")
+    close(S, rS, mS, 96 + 600, "state")
+    assert torch.equal(cs.cpu().double(), rcs)
+
+
+@pytest.mark.parametrize("L,n", [(40, [13, 0]), (200, [70, 0])])
+def test_tokens_past_the_end_are_not_read(gpu, L, n):
+    i = Inputs(2, L, 2, 1, 64, 128, 4, BF16)
+    i.h0[1, 0, 0, 0] = float("inf")     # a state that is not finite, and no token: y is still zero
+    clean = i.fwd(F32, n)
+    for b in range(2):
+        i.xbc[b, n[b]:] = float("nan")
+        i.dt[b, n[b]:] = float("nan")
+    again = i.fwd(F32, n)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(clean, again))
+    assert not again[0][0, n[0]:].any() and not again[0][1].any() and torch.equal(again[1][1], i.h0[1])
+
+
+def test_nan_reaches_its_head_and_nothing_before_its_chunk(gpu):
+    i = Inputs(1, 300, 3, 1, 64, 128, 4, F32)
+    clean = i.fwd()[0]
+    i.xbc[0, 200, 70] = float("nan")      # head 1
+    y, S, _ = i.fwd()
+    torch.cuda.synchronize()
+    assert torch.equal(y[:, :192], clean[:, :192]) and torch.equal(y[:, :, [0, 2]], clean[:, :, [0, 2]])
+    assert y[0, 200, 1, 6].isnan() and S[0, 1, 6].isnan().all() and S[0, 0].isfinite().all()
+
+
+def test_extreme_steps(gpu):
+    """Decays of nearly one and of zero; steps of zero."""
+    i = Inputs(1, 150, 4, 1, 64, 64, 4, F32)
+    i.A = torch.tensor([-1e-8, -1e4, -1.0, 0.0], device=DEV)
+    i.dt = i.dt.clone()
+    i.dt[0, 40:60, 2] = -200.0             # softplus is zero
+    i.dt[0, 80:85, 2] = 60.0
+    y, S, _ = i.fwd()
+    torch.cuda.synchronize()
+    (ry, rS, _), (my, mS) = i.ref()
+    close(y, ry, my, 96 + 600, "y")
+    close(S, rS, mS, 96 + 600, "state")
+
+
+def test_same_bits_every_time_and_on_another_stream(gpu):
+    i = Inputs(2, 400, 4, 2, 64, 128, 4, BF16)
+    a = i.fwd()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b = i.fwd()
+    side.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("L", [10, 300])
+def test_graph_replays(gpu, L):
+    i = Inputs(2, L, 4, 1, 64, 128, 4, BF16)
+    S, cs = i.h0.clone(), i.cs.clone()
+    token = i.xbc[:, 0].clone(), i.dt[:, 0].clone()
+    step = lambda s, c: ss.mamba2_conv_step(s, c, *token, i.w, i.b, i.A, i.D, i.dtb)
+    i.fwd(), step(S.clone(), cs.clone())
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = i.fwd()
+        yt = step(S, cs)
+    S2, cs2 = S.clone(), cs.clone()
+    for _ in range(3):
+        i.xbc.copy_(rnd(i.gen, *i.xbc.shape, dtype=BF16))
+        token[0].copy_(i.xbc[:, 1])
+        graph.replay()
+        want, yw = i.fwd(), step(S2, cs2)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+        assert torch.equal(yt, yw) and torch.equal(S, S2) and torch.equal(cs, cs2)
+
+
+def test_workspace_of_the_caller(gpu):
+    i = Inputs(1, 200, 2, 1, 64, 128, 4, BF16)
+    need = ss.mamba2_conv_workspace_bytes(1, 200, 2, 64, 1, 128)
+    want = i.fwd()
+    ws = torch.full((need + 256,), 255, dtype=torch.uint8, device=DEV)
+    got = i.fwd(workspace=ws[:need])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got)) and (ws[need:] == 255).all()
+    if need:
+        with pytest.raises(ss.SelscanError):
+            i.fwd(workspace=ws[:need - 256])
+    with pytest.raises(ValueError):
+        i.fwd(workspace=torch.empty(need, dtype=torch.uint8))
+
+
+def test_refusals(gpu):
+    i = Inputs(1, 8, 2, 1, 64, 128, 4, BF16)
+    with pytest.raises(ValueError, match="channels"):
+        ss.mamba2_conv_fwd(i.xbc, i.dt, i.w, i.b, i.A, ngroups=1, dstate=200)
+    with pytest.raises(TypeError):
+        ss.mamba2_conv_fwd(i.xbc, i.dt.float(), i.w, i.b, i.A, ngroups=1, dstate=128)
+    with pytest.raises(ValueError, match="channels"):
+        ss.mamba2_conv_step(i.h0[:, :, :1], i.cs, i.xbc[:, 0], i.dt[:, 0], i.w, i.b, i.A[:1])
+    with pytest.raises(ss.SelscanError, match="alias"):
+        i.fwd(last_state=i.h0)
