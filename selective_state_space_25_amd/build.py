@@ -30,7 +30,7 @@ BUILD = os.path.join(ROOT, "_build")
 SOURCES = ["selscan.cpp", "timing.cpp", "m1_scan.hip", "m2_scan.hip", "m2_ssd.hip", "step.hip", "conv1d.hip", "m1_bwd.hip", "m2_bwd.hip", "noalloc.hip",
            "delta.cpp", "delta_rec.hip", "delta_prep.hip", "delta_scan.hip", "delta_bwd.hip",
            "block_ops.cpp", "norm.hip", "dropout.hip", "mixer.cpp", "short_conv.hip", "column_sums.hip", "m2_conv_step.hip",
-           "m2_conv_rec.hip", "rms.cpp", "rms_fwd.hip", "rms_bwd.hip"]
+           "m2_conv_rec.hip", "m2_prep.hip", "m2_chunk_scan.hip", "rms.cpp", "rms_fwd.hip", "rms_bwd.hip"]
 ARCH = os.environ.get("SELSCAN_ARCH", "gfx950")
 
 

@@ -1,0 +1,528 @@
+// m2_chunk_scan.hip -- the Mamba-2 mixer's scan over 64-token chunks.
+//
+// With S [N, P] the state entering a chunk, cum_t the running sum of D_t A
+// inside it, B and C from m2_prep.hip and x = silu(conv), a head's outputs and
+// next state are
+//
+//   Y  = e^cum (C S) + M X,   M[t, s] = G[t, s] e^(cum_t - cum_s) D_s  (s <= t), + D on the diagonal
+//   S' = e^last S + B^T (D e^(last - cum) X)
+//
+// A wave owns 16 CT value columns of a head and walks the chunks with its S in
+// accumulators, which are the operands of C S as they are: nothing of a head
+// crosses waves.  The waves of a workgroup share a group's C, B and G, which
+// go from memory into LDS without passing through registers, C while M X and
+// B^T X run, B and G while C S runs: two barriers a chunk.  x is convolved by
+// the lanes that multiply it, from the raw rows, and never written.
+//
+// A chunk's work does not depend on how many others are walked, so a sequence
+// is cut into segments: a first pass makes each segment's state from zero
+// (the B^T X product alone), m2_carry_kernel joins them, and the second pass
+// runs all segments at once from the states that enter them.
+//
+// Products are fp32-grade (split_mfma.hpp).  cum is summed in fp64 and kept as
+// two fp32 parts: after strong decays it is large, and the differences between
+// neighbours would carry its rounding.
+#include <algorithm>
+
+#include "host.hpp"
+#include "lds_rows.hpp"
+#include "m2_chunk.hpp"
+
+namespace selscan {
+
+namespace {
+
+using namespace m2chunk;
+using dchunk::buf_st;
+using dchunk::kOut;
+using dchunk::rows_buf;
+
+constexpr int kWaves = 8;
+
+// Per token of a wave's head: cum as hi + lo (log2), e^cum, D, D e^(last - cum).
+struct Gates {
+    float hi[kC], lo[kC], in[kC], step[kC], out[kC];
+};
+
+template <int NP>
+struct Smem {
+    unsigned char C[Rec<NP>::blocks][kBlock];   // (the state pass: B of every other chunk)
+    unsigned char B[Rec<NP>::blocks][kBlock];
+    unsigned char G[12][kBlock];
+    Gates gates[kWaves];
+};
+
+__device__ __forceinline__ uint32_t lds_at(const void* p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
+}
+
+// CT neighbouring elements as loaded.
+template <typename T, int CT> struct RawOf;
+template <> struct RawOf<uint16_t, 1> { typedef uint16_t type; };
+template <> struct RawOf<uint16_t, 2> { typedef uint32_t type; };
+template <> struct RawOf<float, 1> { typedef float type; };
+template <> struct RawOf<float, 2> { typedef float type __attribute__((ext_vector_type(2))); };
+template <typename T, int CT> using RawX = typename RawOf<T, CT>::type;
+
+template <typename T, int CT>
+__device__ __forceinline__ RawX<T, CT> buf_x(__amdgpu_buffer_rsrc_t r, int off) {
+    using RX = RawX<T, CT>;
+    if constexpr (CT * sizeof(T) == 2) return __builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0);
+    else if constexpr (CT * sizeof(T) == 4) return __builtin_bit_cast(RX, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+    else return __builtin_bit_cast(RX, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+}
+__device__ __forceinline__ void widen(uint16_t r, float (&v)[1]) { v[0] = bf16_to_f32(r); }
+__device__ __forceinline__ void widen(uint32_t r, float (&v)[2]) { v[0] = bf16lo(r); v[1] = bf16hi(r); }
+__device__ __forceinline__ void widen(float r, float (&v)[1]) { v[0] = r; }
+__device__ __forceinline__ void widen(RawX<float, 2> r, float (&v)[2]) { v[0] = r[0]; v[1] = r[1]; }
+
+// CT neighbouring results; `even`: no lane has only the first of two.
+template <int CT, typename T>
+__device__ __forceinline__ void store_y(__amdgpu_buffer_rsrc_t r, int off, const float (&v)[CT], int np, bool even, T) {
+    if constexpr (CT == 1) {
+        buf_st(r, off, v[0], T(0));
+    } else if (even) {
+        if constexpr (sizeof(T) == 2) {
+            __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(v[0], v[1]), r, off, 0, 0);
+        } else {
+            typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])}, r, off, 0, 0);
+        }
+    } else {
+        buf_st(r, off, v[0], T(0));
+        buf_st(r, np > 1 ? off + (int)sizeof(T) : kOut, v[1], T(0));
+    }
+}
+
+// `n` blocks from global memory into LDS, shared out over the workgroup's waves.
+__device__ __forceinline__ void copy_blocks(const char* from, const void* to, int n, int wave, int waves, int lane) {
+    const uint32_t slot = lds_at(to);
+    for (int i = wave; i < n; i += waves) rows::dma_at<0>(from + i * kBlock + lane * 16, __builtin_amdgcn_readfirstlane(slot + i * kBlock));
+}
+
+// Everything that this wave asked of memory is there, and the other waves' too.
+__device__ __forceinline__ void all_there() {
+    rows::wait_vm();
+    lds_barrier();
+}
+
+__device__ __forceinline__ bf16x8 op_at(const unsigned char (*blocks)[kBlock], int i, int lane) {
+    return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(&blocks[i][lane * 16]));
+}
+
+// STATE: the first pass, a segment's state from zero and the sum of its log2 decays.
+template <typename Tin, typename Tout, int K, int NP, int CT, bool STATE>
+__global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, Plan pl, const char* recs, float* seg_state,
+                                                                 float* seg_log) {
+    constexpr int KS = NP / 32, NT = NP / 16, ES = (int)sizeof(Tin), EO = (int)sizeof(Tout);
+    using R = Rec<NP>;
+    extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
+    auto& sm = *reinterpret_cast<Smem<NP>*>(smem_raw);
+    const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // the workgroups that share a segment's records on one XCD (workgroups go round the eight)
+    const int64_t id = io::group_id(), oct = id / (8 * pl.sets), in8 = id - oct * 8 * pl.sets;
+    const int64_t seg_id = oct * 8 + in8 % 8;
+    const int set = (int)(in8 / 8);
+    const int64_t bs = seg_id / a.G, grp = seg_id - bs * a.G, b = bs / pl.segs, seg = bs - b * pl.segs;
+    if (b >= a.batch) return;
+    const int64_t len = seq_len(a, b);
+    const int64_t nch = (len + kC - 1) / kC;
+    const int64_t c0 = seg * pl.per, c1 = min(c0 + pl.per, nch);
+    if (STATE && c1 >= nch) return;   // nothing follows this segment
+    const int unit = set * pl.waves + wave;
+    const bool live = unit < pl.units;
+    const int64_t h = grp * (a.H / a.G) + (live ? unit / pl.cols : 0);
+    const int p0 = (live ? unit % pl.cols : 0) * 16 * CT + CT * li;   // the lane's first column; the others behind it
+    const int np = live ? max(0, min(CT, (int)a.P - p0)) : 0;
+    Tout* Y = static_cast<Tout*>(a.y) + (b * a.L * a.H + h) * a.P;
+    const int64_t yrow = a.H * a.P;
+    if (!STATE && c0 >= nch && seg > 0) {   // past the end
+        for (int64_t t = c0 * kC + lg; t < min(a.L, (c0 + pl.per) * kC); t += 4)
+            for (int i = 0; i < np; ++i) io::st(Y + t * yrow + p0 + i, 0.0f);
+        return;
+    }
+    Gates& gt = sm.gates[wave];
+    const Tin* T = static_cast<const Tin*>(a.dt) + b * a.dt_batch + h;
+    const float A = a.A[h], dt_bias = a.dt_bias ? a.dt_bias[h] : 0.0f, skip = a.D ? a.D[h] : 0.0f;
+    const int64_t ch = h * a.P + p0, C = a.conv.C;
+    const char* X0 = scalar(reinterpret_cast<const char*>(static_cast<const Tin*>(a.conv.x) + b * a.conv.x_batch + h * a.P));
+    const Tin* XS = scalar(a.conv.state ? static_cast<const Tin*>(a.conv.state) + b * (K - 1) * C + h * a.P : nullptr);
+    float w[K][CT], bias[CT];
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+        bias[i] = i < np && a.conv.bias ? a.conv.bias[ch + i] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < K; ++k) w[k][i] = i < np ? a.conv.weight[(ch + i) * K + k] : 0.0f;
+    }
+    // state tile nt: rows n = 16 nt + 4 lg + q, column p0 + ct
+    f32x4 S[NT][CT];
+    const int64_t srow = (b * a.H + h) * a.P + p0;
+    const float* S0 = STATE ? nullptr
+                      : seg > 0 ? seg_state + ((seg_id / a.G) * a.H + h) * a.P * a.N + p0 * a.N
+                      : a.h0    ? a.h0 + srow * a.N
+                                : nullptr;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            S[i][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            const int n = 16 * i + 4 * lg;
+            if (S0 && ct < np && n < a.N) {
+                io::Piece<float, 4> r;
+                r.get(S0 + ct * a.N + n);
+                S[i][ct] = r.v;
+            }
+        }
+    char* Y0 = scalar(reinterpret_cast<char*>(Y));
+    const int yat = np > 0 ? p0 * EO : kOut;
+    const bool even = CT == 1 || (a.P & 1) == 0;
+    const char* rec0 = recs + (b * pl.chunks * a.G + grp) * R::bytes;
+    const int64_t rec_row = a.G * R::bytes;
+    auto fetch_dt = [&](int64_t c) {
+        const int64_t t = c * kC + lane;
+        return t < len ? io::ld(T + t * a.dt_row) : 0.0f;
+    };
+    // The lane's raw x of a k-step: tokens 32 ks + 8 lg - (K - 1) .. + 7 of its
+    // columns.  Past the end, and before the first token, the buffer gives zero.
+    using RX = RawX<Tin, CT>;
+    RX xr[K - 1 + 8];
+    const int xrow = scalar((int)(a.conv.x_row * ES)), xbytes = scalar((int)(a.P * ES + ES));   // (B's channels follow the last head's)
+    auto fetch_x = [&](int64_t c, int ks) {
+        const int64_t t0 = c * kC;
+        const int before = c > 0 ? K - 1 : 0;
+        const auto xb = rows_buf(X0 + (t0 - before) * xrow, scalar((int)min((int64_t)(kC + before), len - t0 + before)), xrow, xbytes);
+        const int at = np > 0 ? p0 * ES + (8 * lg + before - (K - 1)) * xrow : kOut;
+#pragma unroll
+        for (int j = 0; j < K - 1 + 8; ++j) xr[j] = buf_x<Tin, CT>(xb, at + (32 * ks + j) * xrow);
+        if (ks == 0 && c == 0 && XS && lg == 0 && np > 0) {   // (one column past the last: B's first)
+#pragma unroll
+            for (int j = 0; j < K - 1; ++j) {
+                io::Piece<Tin, CT> r;
+                r.get(XS + j * C + p0);
+                xr[j] = __builtin_bit_cast(RX, r);
+            }
+        }
+    };
+    auto convolve = [&](int64_t c, int ks, float (&x)[CT][8]) {
+        float r[K - 1 + 8][CT];
+#pragma unroll
+        for (int j = 0; j < K - 1 + 8; ++j) widen(xr[j], r[j]);
+        const int in = scalar((int)min((int64_t)kC, len - c * kC)) - (32 * ks + 8 * lg);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int i = 0; i < CT; ++i) {
+                float pre = bias[i];
+#pragma unroll
+                for (int k = 0; k < K; ++k) pre = __builtin_fmaf(w[k][i], r[j + k][i], pre);
+                x[i][j] = j < in ? silu_scaled(pre, 1.0f) : 0.0f;
+            }
+    };
+    float dtv = c0 < c1 ? fetch_dt(c0) : 0.0f, next_dt = 0.0f;
+    double log_sum = 0.0;
+    float decay = 1.0f;   // e^last of the chunk
+    // the chunk's gates, a token a lane
+    auto make_gates = [&](int64_t c) {
+        const bool in = c * kC + lane < len;
+        const float sp = in ? softplus_log2((dtv + dt_bias) * kLog2e) : 0.0f;
+        double cum = in ? (double)sp * (double)A : 0.0;
+        cum = cum < -1e6 ? -1e6 : cum;   // (a decay of zero either way; stays finite)
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const double up = __shfl_up(cum, o, 64);
+            cum += lane >= o ? up : 0.0;
+        }
+        const double last = __shfl(cum, 63, 64);
+        const float hi = (float)cum, step = sp * kLn2;
+        if constexpr (!STATE) {
+            gt.hi[lane] = hi;
+            gt.lo[lane] = (float)(cum - (double)hi);
+            gt.in[lane] = fast_exp2(hi);
+            gt.step[lane] = step;
+        }
+        gt.out[lane] = step * fast_exp2((float)(last - cum));
+        decay = fast_exp2((float)last);
+        log_sum += last;
+        dchunk::wave_sync();
+    };
+    auto decay_state = [&]() {
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) S[i][ct] *= decay;
+    };
+    // what a k-step's x adds to the next state
+    auto write = [&](const unsigned char (*Bs)[kBlock], int ks, const float (&x)[CT][8]) {
+        bf16x8 xp[CT][3];
+        const f32x4 g0 = *reinterpret_cast<const f32x4*>(&gt.out[32 * ks + 8 * lg]);
+        const f32x4 g1 = *reinterpret_cast<const f32x4*>(&gt.out[32 * ks + 8 * lg + 4]);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            f32x4 lo, hi;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                lo[q] = x[ct][q] * g0[q];
+                hi[q] = x[ct][4 + q] * g1[q];
+            }
+            split8<3>(lo, hi, xp[ct]);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; i += 2) {   // (two tiles' chains take turns)
+            bf16x8 bp[2][3];
+            f32x4 acc[2 * CT];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+#pragma unroll
+                for (int x3 = 0; x3 < 3; ++x3) bp[k][x3] = op_at(Bs, ((i + k) * 2 + ks) * 3 + x3, lane);
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) acc[k * CT + ct] = S[i + k][ct];
+            }
+            mm_turns<3, 3, 3>([&](int m) -> const bf16x8(&)[3] { return bp[m / CT]; },
+                              [&](int m) -> const bf16x8(&)[3] { return xp[m % CT]; }, acc);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) S[i + k][ct] = acc[k * CT + ct];
+        }
+    };
+
+    if constexpr (STATE) {
+        copy_blocks(rec0 + c0 * rec_row + R::B, sm.C, R::blocks, wave, pl.waves, lane);
+        for (int64_t c = c0; c < c1; ++c) {
+            if (live) fetch_x(c, 0);
+            if (c + 1 < c1) next_dt = fetch_dt(c + 1);
+            make_gates(c);
+            all_there();
+            const bool odd = (c - c0) & 1;
+            if (c + 1 < c1) copy_blocks(rec0 + (c + 1) * rec_row + R::B, odd ? sm.C : sm.B, R::blocks, wave, pl.waves, lane);
+            if (live) {
+                decay_state();
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    float x[CT][8];
+                    convolve(c, ks, x);
+                    if (ks == 0) fetch_x(c, 1);
+                    write(odd ? sm.B : sm.C, ks, x);
+                }
+            }
+            dtv = next_dt;
+        }
+        if (lane == 0 && live && unit % pl.cols == 0) seg_log[(seg_id / a.G) * a.H + h] = (float)log_sum;
+    } else {
+        if (c0 < c1) copy_blocks(rec0 + c0 * rec_row + R::C, sm.C, R::blocks, wave, pl.waves, lane);
+        for (int64_t c = c0; c < c1; ++c) {
+            const char* rec = rec0 + c * rec_row;
+            make_gates(c);
+            all_there();   // C; and every wave is done with the chunk before
+            copy_blocks(rec + R::B, sm.B, R::blocks + 12, wave, pl.waves, lane);   // and G, behind B in both
+            if (live && ES == 2) fetch_x(c, 0);
+            if (c + 1 < c1) next_dt = fetch_dt(c + 1);
+            f32x4 y[4][CT];
+#pragma unroll
+            for (int tt = 0; tt < 4; ++tt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) y[tt][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            if (live) {
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+                    bf16x8 sp[CT][3];
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) split8<3>(S[2 * ks][ct], S[2 * ks + 1][ct], sp[ct]);
+#pragma unroll
+                    for (int tt = 0; tt < 4; ++tt) {
+                        bf16x8 cp[3];
+#pragma unroll
+                        for (int x3 = 0; x3 < 3; ++x3) cp[x3] = op_at(sm.C, (ks * 4 + tt) * 3 + x3, lane);
+                        mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return cp; },
+                                          [&](int m) -> const bf16x8(&)[3] { return sp[m]; }, y[tt]);
+                    }
+                }
+#pragma unroll
+                for (int tt = 0; tt < 4; ++tt) {
+                    const f32x4 e = *reinterpret_cast<const f32x4*>(&gt.in[16 * tt + 4 * lg]);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) y[tt][ct] *= e;
+                }
+                if (ES == 4) fetch_x(c, 0);   // (twice the registers: not beside C S's operands, nor M's)
+            }
+            all_there();   // B and G; and every wave is done with C
+            if (c + 1 < c1) copy_blocks(rec + rec_row + R::C, sm.C, R::blocks, wave, pl.waves, lane);
+            if (live) {
+                decay_state();
+                const auto yb = rows_buf(Y0 + c * kC * yrow * EO, scalar((int)min((int64_t)kC, a.L - c * kC)), scalar((int)(yrow * EO)), scalar((int)(a.P * EO)));
+                const int in = scalar((int)min((int64_t)kC, len - c * kC)) - 4 * lg;
+                int y0 = yat + 4 * lg * (int)(yrow * EO);
+                asm volatile("" : "+v"(y0));   // (else its sums with every row are kept in registers throughout)
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    float x[CT][8];
+                    convolve(c, ks, x);
+                    if (ks == 0 && ES == 2) fetch_x(c, 1);
+                    bf16x8 xp[CT][3];
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        split8<3>(f32x4{x[ct][0], x[ct][1], x[ct][2], x[ct][3]}, f32x4{x[ct][4], x[ct][5], x[ct][6], x[ct][7]}, xp[ct]);
+                    const int s0 = 32 * ks + 8 * lg;
+#pragma unroll
+                    for (int tt = 2 * ks; tt < 4; ++tt) {
+                        const int t = 16 * tt + li;
+                        const float ht = gt.hi[t], lt = gt.lo[t];
+                        f32x4 m[2];
+                        const f32x4* G = reinterpret_cast<const f32x4*>(sm.G) + g_tile(tt, ks) * 128 + lane * 2;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const f32x4 hs = *reinterpret_cast<const f32x4*>(&gt.hi[s0 + 4 * e]);
+                            const f32x4 ls = *reinterpret_cast<const f32x4*>(&gt.lo[s0 + 4 * e]);
+                            const f32x4 ds = *reinterpret_cast<const f32x4*>(&gt.step[s0 + 4 * e]);
+                            m[e] = G[e];
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int d = t - (s0 + 4 * e + j);
+                                const float v = m[e][j] * (fast_exp2((ht - hs[j]) + (lt - ls[j])) * ds[j]);
+                                m[e][j] = d > 0 ? v : d == 0 ? v + skip : 0.0f;
+                            }
+                        }
+                        bf16x8 mp[3];
+                        split8<3>(m[0], m[1], mp);
+                        mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return mp; },
+                                          [&](int i) -> const bf16x8(&)[3] { return xp[i]; }, y[tt]);
+                        if (ks == tt / 2) {   // done with these rows
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                float v[CT];
+#pragma unroll
+                                for (int ct = 0; ct < CT; ++ct) v[ct] = 16 * tt + q < in ? y[tt][ct][q] : 0.0f;
+                                store_y<CT>(yb, y0 + (16 * tt + q) * (int)(yrow * EO), v, np, even, Tout(0));
+                            }
+                        }
+                    }
+                    if (ks == 0 && ES == 4) fetch_x(c, 1);
+                    write(sm.B, ks, x);
+                }
+            }
+            dtv = next_dt;
+        }
+        // the rest of the segment's tokens, past the end
+        for (int64_t t = c1 * kC + lg; t < min(a.L, (c0 + pl.per) * kC); t += 4)
+            for (int i = 0; i < np; ++i) io::st(Y + t * yrow + p0 + i, 0.0f);
+        if (c1 < nch || !a.last) return;
+    }
+    float* S1 = STATE ? seg_state + ((seg_id / a.G + 1) * a.H + h) * a.P * a.N + p0 * a.N : a.last + srow * a.N;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) {
+            const int n = 16 * i + 4 * lg;
+            if (ct < np && n < a.N) {
+                io::Piece<float, 4> r;
+                r.v = S[i][ct];
+                r.put(S1 + ct * a.N + n);
+            }
+        }
+}
+
+// The states that enter segments 1, 2, ..: slot s of seg_state holds what
+// segment s - 1 made from zero, and takes the state entering segment s.
+__global__ __launch_bounds__(256) void m2_carry_kernel(M2ConvArgs a, Plan pl, float* seg_state, const float* seg_log) {
+    const int64_t head = a.P * a.N, i = io::group_id() * 256 + threadIdx.x;
+    const int64_t bh = i / head, e = i - bh * head, b = bh / a.H, h = bh - b * a.H;
+    if (b >= a.batch) return;
+    const int64_t len = a.conv.lengths ? min((int64_t)max(a.conv.lengths[b], 0), a.L) : a.L;
+    const int64_t n = ((len + kC - 1) / kC + pl.per - 1) / pl.per;   // the sequence's segments
+    float s = a.h0 ? a.h0[i] : 0.0f;
+    for (int64_t g = 0; g + 1 < n; ++g) {
+        float* to = seg_state + ((b * pl.segs + g + 1) * a.H + h) * head + e;
+        s = __builtin_fmaf(fast_exp2(seg_log[(b * pl.segs + g) * a.H + h]), s, *to);
+        *to = s;
+    }
+}
+
+Plan plan_of(const M2ConvArgs& a) {
+    Plan p;
+    p.chunks = (a.L + kC - 1) / kC;
+    p.np = a.N <= 32 ? 32 : (int)a.N;
+    const int64_t heads = a.H / a.G;
+    // two column blocks a wave halve the reads of B and C from LDS; one where
+    // a group would not fill a workgroup's waves
+    p.ct = heads * ((a.P + 31) / 32) < kWaves ? 1 : 2;
+    p.cols = (int)((a.P + 16 * p.ct - 1) / (16 * p.ct));
+    p.units = (int)(heads * p.cols);
+    p.sets = (p.units + kWaves - 1) / kWaves;
+    p.waves = (p.units + p.sets - 1) / p.sets;
+    // segments: enough workgroups for the GPU, four chunks each at least
+    const int64_t groups = a.batch * a.G * p.sets;
+    const int64_t want = host::env_int("SELSCAN_M2_SEG_WGS", 512);
+    p.segs = std::max<int64_t>(1, std::min((want + groups - 1) / groups, p.chunks / host::env_int("SELSCAN_M2_SEG_MIN", 4)));
+    p.per = (p.chunks + p.segs - 1) / p.segs;
+    p.segs = (p.chunks + p.per - 1) / p.per;
+    return p;
+}
+
+size_t rec_bytes(const Plan& p) { return p.np == 32 ? Rec<32>::bytes : p.np == 64 ? Rec<64>::bytes : Rec<128>::bytes; }
+size_t all_rec_bytes(const M2ConvArgs& a, const Plan& p) { return host::align256((size_t)(a.batch * p.chunks * a.G) * rec_bytes(p)); }
+size_t seg_bytes(const M2ConvArgs& a, const Plan& p) {
+    return p.segs == 1 ? 0 : host::align256((size_t)(a.batch * p.segs * a.H) * (size_t)(a.P * a.N) * 4);
+}
+
+struct Run {
+    const M2ConvArgs& a;
+    const Plan& pl;
+    char* recs;
+    float *seg_state, *seg_log;
+    hipStream_t stream;
+
+    template <typename Tin, typename Tout, int K, int NP, int CT, bool STATE>
+    hipError_t pass() const {
+        constexpr int bytes = (int)sizeof(Smem<NP>);
+        static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
+        const auto kern = &m2_chunk_kernel<Tin, Tout, K, NP, CT, STATE>;
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e != hipSuccess) return e;
+        const int64_t segs = (a.batch * pl.segs * a.G + 7) / 8 * 8;
+        KTime kt(STATE ? "m2_chunk_state" : "m2_chunk_scan", stream);
+        hipLaunchKernelGGL(kern, io::groups(segs * pl.sets), dim3(64 * pl.waves), bytes, stream, a, pl, recs, seg_state, seg_log);
+        return hipGetLastError();
+    }
+    template <typename Tin, typename Tout, int K, int NP, int CT>
+    hipError_t run() const {
+        if (pl.segs > 1) {
+            hipError_t e = pass<Tin, float, K, NP, CT, true>();
+            if (e != hipSuccess) return e;
+            KTime kt("m2_carry", stream);
+            hipLaunchKernelGGL(m2_carry_kernel, io::groups((a.batch * a.H * a.P * a.N + 255) / 256), dim3(256), 0, stream, a, pl,
+                               seg_state, seg_log);
+        }
+        return pass<Tin, Tout, K, NP, CT, false>();
+    }
+    template <typename Tin, typename Tout, int K, int NP>
+    hipError_t by_ct() const { return pl.ct == 1 ? run<Tin, Tout, K, NP, 1>() : run<Tin, Tout, K, NP, 2>(); }
+    template <typename Tin, typename Tout, int K>
+    hipError_t by_np() const {
+        return pl.np == 32 ? by_ct<Tin, Tout, K, 32>() : pl.np == 64 ? by_ct<Tin, Tout, K, 64>() : by_ct<Tin, Tout, K, 128>();
+    }
+    template <typename Tin, typename Tout>
+    hipError_t by_k() const {
+        return a.conv.K == 2 ? by_np<Tin, Tout, 2>() : a.conv.K == 3 ? by_np<Tin, Tout, 3>() : by_np<Tin, Tout, 4>();
+    }
+};
+
+}  // namespace
+
+size_t m2_chunk_bytes(const M2ConvArgs& a) {
+    const Plan p = plan_of(a);
+    return all_rec_bytes(a, p) + seg_bytes(a, p) + (p.segs == 1 ? 0 : host::align256((size_t)(a.batch * p.segs * a.H) * 4));
+}
+
+hipError_t launch_m2_chunk(const M2ConvArgs& a, int in_bf16, int out_bf16, void* ws, hipStream_t stream) {
+    const Plan p = plan_of(a);
+    char* recs = static_cast<char*>(ws);
+    char* states = recs + all_rec_bytes(a, p);
+    const Run r{a, p, recs, reinterpret_cast<float*>(states), reinterpret_cast<float*>(states + seg_bytes(a, p)), stream};
+    const hipError_t e = launch_m2_prep(a, in_bf16, p.np, recs, p.chunks, stream);
+    if (e != hipSuccess) return e;
+    if (in_bf16) return out_bf16 ? r.by_k<uint16_t, uint16_t>() : r.by_k<uint16_t, float>();
+    return out_bf16 ? r.by_k<float, uint16_t>() : r.by_k<float, float>();
+}
+
+}  // namespace selscan

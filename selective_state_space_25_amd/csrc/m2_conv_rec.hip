@@ -86,9 +86,9 @@ hipError_t by_n(const M2ConvArgs& a, const float* X, const float* B, const float
 
 }  // namespace
 
-size_t m2_conv_bytes(const M2ConvArgs& a) { return ((size_t)(a.batch * a.L * a.conv.C) * 4 + 255) & ~size_t(255); }
+size_t m2_rec_bytes(const M2ConvArgs& a) { return ((size_t)(a.batch * a.L * a.conv.C) * 4 + 255) & ~size_t(255); }
 
-hipError_t launch_m2_conv(const M2ConvArgs& a, int in_bf16, int out_bf16, void* ws, hipStream_t stream) {
+hipError_t launch_m2_rec(const M2ConvArgs& a, int in_bf16, int out_bf16, void* ws, hipStream_t stream) {
     ShortConvArgs c = a.conv;
     const int64_t rows = a.batch * a.L;
     float* X = static_cast<float*>(ws);

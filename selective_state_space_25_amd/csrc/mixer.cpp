@@ -117,6 +117,13 @@ void fill(selscan::M2ConvArgs& a, const selscan_m2_conv_shape_t* s, bool token) 
     selscan::short_conv_plan(a.conv, false);
 }
 
+constexpr int64_t kRecTokens = 16;
+
+// The chunked form's offsets inside 64 tokens and the three before are 32-bit.
+bool chunked(const selscan::M2ConvArgs& a) { return a.L > kRecTokens && a.conv.x_row < ((int64_t)1 << 30) / (4 * 68); }
+
+size_t mixer_bytes(const selscan::M2ConvArgs& a) { return chunked(a) ? selscan::m2_chunk_bytes(a) : selscan::m2_rec_bytes(a); }
+
 }  // namespace
 
 extern "C" {
@@ -205,7 +212,7 @@ size_t selscan_mamba2_conv_workspace_bytes(const selscan_m2_conv_shape_t* s) {
     if (check_mixer(s, false) != SELSCAN_OK) return 0;
     selscan::M2ConvArgs a{};
     fill(a, s, false);
-    return selscan::m2_conv_bytes(a);
+    return mixer_bytes(a);
 }
 
 selscan_status_t selscan_mamba2_conv_fwd(const selscan_m2_conv_shape_t* s, const void* xbc, const void* dt,
@@ -227,12 +234,13 @@ selscan_status_t selscan_mamba2_conv_fwd(const selscan_m2_conv_shape_t* s, const
         selscan::M2ConvArgs a{};
         fill(a, s, false);
         Scratch ws;
-        st = ws.get(s->workspace, s->workspace_bytes, selscan::m2_conv_bytes(a), hs);
+        st = ws.get(s->workspace, s->workspace_bytes, mixer_bytes(a), hs);
         if (st != SELSCAN_OK) return st;
         a.conv.x = xbc; a.conv.weight = conv_weight; a.conv.bias = conv_bias; a.conv.lengths = lengths;
         a.conv.state = conv_state; a.conv.last = last_conv_state;
         a.dt = dt; a.A = A; a.D = D; a.dt_bias = dt_bias; a.h0 = h0; a.y = y; a.last = last_state;
-        const hipError_t e = selscan::launch_m2_conv(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16, ws.ptr, hs);
+        const auto launch = chunked(a) ? &selscan::launch_m2_chunk : &selscan::launch_m2_rec;
+        const hipError_t e = launch(a, s->in_dtype == SELSCAN_BF16, s->out_dtype == SELSCAN_BF16, ws.ptr, hs);
         ws.release();
         return launched(e);
     } catch (...) {
