@@ -22,16 +22,16 @@ constexpr int kBlock = 1024;   // bytes of an operand block: 16 bytes a lane
 //     4 g .. and 32 ks + 16 + 4 g .. (the order in which a state's C tiles hold n)
 //   B [NP / 16][2][3]: its transpose, rows n = 16 nt + i; lane 16 g + i has
 //     tokens 32 ks + 8 g ..
-//   G = C B^T on and below the diagonal, fp32: tiles (tt, ks) = (0, 0), (1, 0),
-//     (2, 0), (2, 1), (3, 0), (3, 1); lane 16 g + i of a tile has row 16 tt + i,
-//     columns 32 ks + 8 g .. (above the diagonal: anything)
+//   G [6][3] = C B^T on and below the diagonal, zero above: tiles (tt, ks) =
+//     (0, 0), (1, 0), (2, 0), (2, 1), (3, 0), (3, 1); lane 16 g + i has row 16
+//     tt + i, columns 32 ks + 8 g ..
 template <int NP>
 struct Rec {
     static constexpr int blocks = NP / 32 * 12;   // of C, and of B
     static constexpr int C = 0;
     static constexpr int B = blocks * kBlock;
     static constexpr int G = 2 * blocks * kBlock;
-    static constexpr int bytes = G + 12 * kBlock;
+    static constexpr int bytes = G + 18 * kBlock;
 };
 __device__ __forceinline__ constexpr int g_tile(int tt, int ks) { return tt < 2 ? tt : 2 * tt - 2 + ks; }
 

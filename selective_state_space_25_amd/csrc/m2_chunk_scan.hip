@@ -1,27 +1,36 @@
 // m2_chunk_scan.hip -- the Mamba-2 mixer's scan over 64-token chunks.
 //
 // With S [N, P] the state entering a chunk, cum_t the running sum of D_t A
-// inside it, B and C from m2_prep.hip and x = silu(conv), a head's outputs and
-// next state are
+// inside it, B, C and G = C B^T from m2_prep.hip and x = silu(conv), a head's
+// outputs and next state are
 //
-//   Y  = e^cum (C S) + M X,   M[t, s] = G[t, s] e^(cum_t - cum_s) D_s  (s <= t), + D on the diagonal
+//   Y  = e^cum (C S) + M X + D x,   M[t, s] = G[t, s] e^(cum_t - cum_s) D_s  (s <= t)
 //   S' = e^last S + B^T (D e^(last - cum) X)
+//
+// and with X' = e^(r - cum) D X, r half of last,
+//
+//   M X = e^(cum - r) (G X');   S' = e^(last - r) (e^r S + B^T X')
+//
+// so that one split of X' into planes serves both products and G's planes are
+// the group's, whatever the head.  Where a chunk's decays span more than 2^120
+// the powers of two would leave fp32's range: such a head's M is made element
+// by element.
 //
 // A wave owns 16 CT value columns of a head and walks the chunks with its S in
 // accumulators, which are the operands of C S as they are: nothing of a head
 // crosses waves.  The waves of a workgroup share a group's C, B and G, which
-// go from memory into LDS without passing through registers, C while M X and
-// B^T X run, B and G while C S runs: two barriers a chunk.  x is convolved by
+// go from memory into LDS without passing through registers, C while G X' and
+// B^T X' run, B and G while C S runs: two barriers a chunk.  x is convolved by
 // the lanes that multiply it, from the raw rows, and never written.
 //
 // A chunk's work does not depend on how many others are walked, so a sequence
 // is cut into segments: a first pass makes each segment's state from zero
-// (the B^T X product alone), m2_carry_kernel joins them, and the second pass
+// (the B^T X' product alone), m2_carry_kernel joins them, and the second pass
 // runs all segments at once from the states that enter them.
 //
-// Products are fp32-grade (split_mfma.hpp).  cum is summed in fp64 and kept as
-// two fp32 parts: after strong decays it is large, and the differences between
-// neighbours would carry its rounding.
+// Products are fp32-grade (split_mfma.hpp).  cum is summed in fp64, and its
+// exponentials take it as two fp32 parts: after strong decays it is large, and
+// its rounding to one would be an error of them all.
 #include <algorithm>
 
 #include "host.hpp"
@@ -39,18 +48,52 @@ using dchunk::rows_buf;
 
 constexpr int kWaves = 8;
 
-// Per token of a wave's head: cum as hi + lo (log2), e^cum, D, D e^(last - cum).
+// Most that a chunk's decays span (log2) for r's powers of two: x D of 2^-30
+// keeps its three planes, of 2^60 stays finite.
+constexpr double kSpan = 120.0;
+
+// Per token of a wave's head: e^cum, e^(cum - r), D e^(r - cum).  With decays
+// past kSpan f is 1, h is D, and cum stands in two parts (log2).
 struct Gates {
-    float hi[kC], lo[kC], in[kC], step[kC], out[kC];
+    float in[kC], f[kC], h[kC], hi[kC], lo[kC];
 };
 
-template <int NP>
+template <int NP, int CT>
 struct Smem {
     unsigned char C[Rec<NP>::blocks][kBlock];   // (the state pass: B of every other chunk)
     unsigned char B[Rec<NP>::blocks][kBlock];
-    unsigned char G[12][kBlock];
+    unsigned char G[18][kBlock];
     Gates gates[kWaves];
+    float x[kWaves][CT][16][32];                // a k-step's x, a column a row (16-byte pieces exchanged by column)
 };
+
+// Sum over the lanes up to this one, by data-parallel moves (a lane that has
+// none to take from adds zero).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_moved(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, true);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), CTRL, ROWS, 0xf, true);
+    return v + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+__device__ __forceinline__ double sum_to_lane(double v) {
+    v = add_moved<0x111, 0xf>(v);   // 1, 2, 4, 8 lanes up within 16
+    v = add_moved<0x112, 0xf>(v);
+    v = add_moved<0x114, 0xf>(v);
+    v = add_moved<0x118, 0xf>(v);
+    v = add_moved<0x142, 0xa>(v);   // lane 15 to the second 16, 47 to the fourth
+    return add_moved<0x143, 0xc>(v);   // lane 31 to the upper half
+}
+__device__ __forceinline__ double of_lane_63(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
+__device__ __forceinline__ float exp2_of(double d) {
+    const float hi = (float)d, e = fast_exp2(hi);
+    return __builtin_fmaf(e, (float)(d - (double)hi) * kLn2, e);
+}
 
 __device__ __forceinline__ uint32_t lds_at(const void* p) {
     return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void*)p;
@@ -76,21 +119,16 @@ __device__ __forceinline__ void widen(uint32_t r, float (&v)[2]) { v[0] = bf16lo
 __device__ __forceinline__ void widen(float r, float (&v)[1]) { v[0] = r; }
 __device__ __forceinline__ void widen(RawX<float, 2> r, float (&v)[2]) { v[0] = r[0]; v[1] = r[1]; }
 
-// CT neighbouring results; `even`: no lane has only the first of two.
+// CT neighbouring results.
 template <int CT, typename T>
-__device__ __forceinline__ void store_y(__amdgpu_buffer_rsrc_t r, int off, const float (&v)[CT], int np, bool even, T) {
+__device__ __forceinline__ void store_y(__amdgpu_buffer_rsrc_t r, int off, const float (&v)[CT], T) {
     if constexpr (CT == 1) {
         buf_st(r, off, v[0], T(0));
-    } else if (even) {
-        if constexpr (sizeof(T) == 2) {
-            __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(v[0], v[1]), r, off, 0, 0);
-        } else {
-            typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])}, r, off, 0, 0);
-        }
+    } else if constexpr (sizeof(T) == 2) {
+        __builtin_amdgcn_raw_buffer_store_b32(pack_bf16x2(v[0], v[1]), r, off, 0, 0);
     } else {
-        buf_st(r, off, v[0], T(0));
-        buf_st(r, np > 1 ? off + (int)sizeof(T) : kOut, v[1], T(0));
+        typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])}, r, off, 0, 0);
     }
 }
 
@@ -117,8 +155,16 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     constexpr int KS = NP / 32, NT = NP / 16, ES = (int)sizeof(Tin), EO = (int)sizeof(Tout);
     using R = Rec<NP>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
-    auto& sm = *reinterpret_cast<Smem<NP>*>(smem_raw);
-    const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+    auto& sm = *reinterpret_cast<Smem<NP, CT>*>(smem_raw);
+    int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+    // Anew for each chunk: whatever follows from the lane alone would be kept in
+    // registers throughout, and there are none left for it.
+    auto place = [&]() {
+        lane = threadIdx.x & 63;
+        asm volatile("" : "+v"(lane));
+        li = lane & 15;
+        lg = lane >> 4;
+    };
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     // the workgroups that share a segment's records on one XCD (workgroups go round the eight)
     const int64_t id = io::group_id(), oct = id / (8 * pl.sets), in8 = id - oct * 8 * pl.sets;
@@ -133,33 +179,34 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     const int unit = set * pl.waves + wave;
     const bool live = unit < pl.units;
     const int64_t h = grp * (a.H / a.G) + (live ? unit / pl.cols : 0);
-    const int p0 = (live ? unit % pl.cols : 0) * 16 * CT + CT * li;   // the lane's first column; the others behind it
-    const int np = live ? max(0, min(CT, (int)a.P - p0)) : 0;
+    const int p0 = (live ? unit % pl.cols : 0) * 16 * CT;   // the wave's first column; lane li has CT li and the one behind it
+    const bool mine = live && p0 + CT * li < a.P;           // (CT = 2: P is even)
     Tout* Y = static_cast<Tout*>(a.y) + (b * a.L * a.H + h) * a.P;
     const int64_t yrow = a.H * a.P;
     if (!STATE && c0 >= nch && seg > 0) {   // past the end
         for (int64_t t = c0 * kC + lg; t < min(a.L, (c0 + pl.per) * kC); t += 4)
-            for (int i = 0; i < np; ++i) io::st(Y + t * yrow + p0 + i, 0.0f);
+            if (mine)
+                for (int i = 0; i < CT; ++i) io::st(Y + t * yrow + p0 + CT * li + i, 0.0f);
         return;
     }
     Gates& gt = sm.gates[wave];
     const Tin* T = static_cast<const Tin*>(a.dt) + b * a.dt_batch + h;
     const float A = a.A[h], dt_bias = a.dt_bias ? a.dt_bias[h] : 0.0f, skip = a.D ? a.D[h] : 0.0f;
-    const int64_t ch = h * a.P + p0, C = a.conv.C;
+    const int64_t ch = h * a.P + p0 + CT * li, C = a.conv.C;
     const char* X0 = scalar(reinterpret_cast<const char*>(static_cast<const Tin*>(a.conv.x) + b * a.conv.x_batch + h * a.P));
     const Tin* XS = scalar(a.conv.state ? static_cast<const Tin*>(a.conv.state) + b * (K - 1) * C + h * a.P : nullptr);
     float w[K][CT], bias[CT];
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
-        bias[i] = i < np && a.conv.bias ? a.conv.bias[ch + i] : 0.0f;
+        bias[i] = mine && a.conv.bias ? a.conv.bias[ch + i] : 0.0f;
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k][i] = i < np ? a.conv.weight[(ch + i) * K + k] : 0.0f;
+        for (int k = 0; k < K; ++k) w[k][i] = mine ? a.conv.weight[(ch + i) * K + k] : 0.0f;
     }
     // state tile nt: rows n = 16 nt + 4 lg + q, column p0 + ct
     f32x4 S[NT][CT];
-    const int64_t srow = (b * a.H + h) * a.P + p0;
+    const int64_t srow = (b * a.H + h) * a.P + p0 + CT * li;
     const float* S0 = STATE ? nullptr
-                      : seg > 0 ? seg_state + ((seg_id / a.G) * a.H + h) * a.P * a.N + p0 * a.N
+                      : seg > 0 ? seg_state + (((seg_id / a.G) * a.H + h) * a.P + p0 + CT * li) * a.N
                       : a.h0    ? a.h0 + srow * a.N
                                 : nullptr;
 #pragma unroll
@@ -168,15 +215,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
         for (int ct = 0; ct < CT; ++ct) {
             S[i][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             const int n = 16 * i + 4 * lg;
-            if (S0 && ct < np && n < a.N) {
+            if (S0 && mine && n < a.N) {
                 io::Piece<float, 4> r;
                 r.get(S0 + ct * a.N + n);
                 S[i][ct] = r.v;
             }
         }
     char* Y0 = scalar(reinterpret_cast<char*>(Y));
-    const int yat = np > 0 ? p0 * EO : kOut;
-    const bool even = CT == 1 || (a.P & 1) == 0;
     const char* rec0 = recs + (b * pl.chunks * a.G + grp) * R::bytes;
     const int64_t rec_row = a.G * R::bytes;
     auto fetch_dt = [&](int64_t c) {
@@ -186,28 +231,28 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     // The lane's raw x of a k-step: tokens 32 ks + 8 lg - (K - 1) .. + 7 of its
     // columns.  Past the end, and before the first token, the buffer gives zero.
     using RX = RawX<Tin, CT>;
-    RX xr[K - 1 + 8];
-    const int xrow = scalar((int)(a.conv.x_row * ES)), xbytes = scalar((int)(a.P * ES + ES));   // (B's channels follow the last head's)
+    RX xr[STATE ? 2 : 1][K - 1 + 8];
+    const int xrow = scalar((int)(a.conv.x_row * ES)), xbytes = scalar((int)(a.P * ES));
     auto fetch_x = [&](int64_t c, int ks) {
         const int64_t t0 = c * kC;
         const int before = c > 0 ? K - 1 : 0;
         const auto xb = rows_buf(X0 + (t0 - before) * xrow, scalar((int)min((int64_t)(kC + before), len - t0 + before)), xrow, xbytes);
-        const int at = np > 0 ? p0 * ES + (8 * lg + before - (K - 1)) * xrow : kOut;
+        const int at = mine ? (p0 + CT * li) * ES + (8 * lg + before - (K - 1)) * xrow : kOut;
 #pragma unroll
-        for (int j = 0; j < K - 1 + 8; ++j) xr[j] = buf_x<Tin, CT>(xb, at + (32 * ks + j) * xrow);
-        if (ks == 0 && c == 0 && XS && lg == 0 && np > 0) {   // (one column past the last: B's first)
+        for (int j = 0; j < K - 1 + 8; ++j) xr[STATE ? ks : 0][j] = buf_x<Tin, CT>(xb, at + (32 * ks + j) * xrow);
+        if (ks == 0 && c == 0 && XS && lg == 0 && mine) {
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
                 io::Piece<Tin, CT> r;
-                r.get(XS + j * C + p0);
-                xr[j] = __builtin_bit_cast(RX, r);
+                r.get(XS + j * C + p0 + CT * li);
+                xr[0][j] = __builtin_bit_cast(RX, r);
             }
         }
     };
     auto convolve = [&](int64_t c, int ks, float (&x)[CT][8]) {
         float r[K - 1 + 8][CT];
 #pragma unroll
-        for (int j = 0; j < K - 1 + 8; ++j) widen(xr[j], r[j]);
+        for (int j = 0; j < K - 1 + 8; ++j) widen(xr[STATE ? ks : 0][j], r[j]);
         const int in = scalar((int)min((int64_t)kC, len - c * kC)) - (32 * ks + 8 * lg);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -221,54 +266,76 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     };
     float dtv = c0 < c1 ? fetch_dt(c0) : 0.0f, next_dt = 0.0f;
     double log_sum = 0.0;
-    float decay = 1.0f;   // e^last of the chunk
+    float front = 1.0f, tail = 1.0f, last_hi = 0.0f, last_lo = 0.0f;   // e^r, e^(last - r); past kSpan e^last, 1; last
+    bool narrow = true;                                                // the chunk's decays are within kSpan
     // the chunk's gates, a token a lane
     auto make_gates = [&](int64_t c) {
         const bool in = c * kC + lane < len;
         const float sp = in ? softplus_log2((dtv + dt_bias) * kLog2e) : 0.0f;
         double cum = in ? (double)sp * (double)A : 0.0;
         cum = cum < -1e6 ? -1e6 : cum;   // (a decay of zero either way; stays finite)
-#pragma unroll
-        for (int o = 1; o < 64; o <<= 1) {
-            const double up = __shfl_up(cum, o, 64);
-            cum += lane >= o ? up : 0.0;
-        }
-        const double last = __shfl(cum, 63, 64);
-        const float hi = (float)cum, step = sp * kLn2;
-        if constexpr (!STATE) {
+        cum = sum_to_lane(cum);
+        const double last = of_lane_63(cum), r = 0.5 * last;
+        const float step = sp * kLn2;
+        narrow = __builtin_amdgcn_readfirstlane(last >= -kSpan && last <= kSpan ? 1 : 0) != 0;
+        if constexpr (!STATE) gt.in[lane] = exp2_of(cum);
+        if (narrow) {
+            if constexpr (!STATE) gt.f[lane] = exp2_of(cum - r);
+            gt.h[lane] = step * exp2_of(r - cum);
+        } else {
+            const float hi = (float)cum;
+            gt.f[lane] = 1.0f;
+            gt.h[lane] = step;
             gt.hi[lane] = hi;
             gt.lo[lane] = (float)(cum - (double)hi);
-            gt.in[lane] = fast_exp2(hi);
-            gt.step[lane] = step;
+            last_hi = (float)last;
+            last_lo = (float)(last - (double)last_hi);
         }
-        gt.out[lane] = step * fast_exp2((float)(last - cum));
-        decay = fast_exp2((float)last);
+        front = exp2_of(narrow ? r : last);
+        tail = narrow ? front : 1.0f;
         log_sum += last;
         dchunk::wave_sync();
     };
-    auto decay_state = [&]() {
+    // X' of a k-step from its x
+    auto scaled = [&](int ks, const float (&x)[CT][8], bf16x8 (&xp)[CT][3]) {
+        const f32x4 h0 = *reinterpret_cast<const f32x4*>(&gt.h[32 * ks + 8 * lg]);
+        const f32x4 h1 = *reinterpret_cast<const f32x4*>(&gt.h[32 * ks + 8 * lg + 4]);
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+            split8<3>(f32x4{x[ct][0], x[ct][1], x[ct][2], x[ct][3]} * h0, f32x4{x[ct][4], x[ct][5], x[ct][6], x[ct][7]} * h1, xp[ct]);
+    };
+    // what decays past kSpan leave to do: the values of planes times e^(to - cum_s), s = the k-step's tokens up to `most`
+    auto decayed = [&](int ks, bf16x8 (&p)[3], float to_hi, float to_lo, int most) {
+        const int s0 = 32 * ks + 8 * lg;
+        f32x4 v[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const f32x4 hs = *reinterpret_cast<const f32x4*>(&gt.hi[s0 + 4 * e]);
+            const f32x4 ls = *reinterpret_cast<const f32x4*>(&gt.lo[s0 + 4 * e]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float g = ((float)p[0][4 * e + j] + (float)p[1][4 * e + j]) + (float)p[2][4 * e + j];
+                v[e][j] = s0 + 4 * e + j <= most ? g * fast_exp2((to_hi - hs[j]) + (to_lo - ls[j])) : 0.0f;
+            }
+        }
+        split8<3>(v[0], v[1], p);
+    };
+    auto scale_state = [&](float by) {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) S[i][ct] *= decay;
+            for (int ct = 0; ct < CT; ++ct) S[i][ct] *= by;
     };
-    // what a k-step's x adds to the next state
-    auto write = [&](const unsigned char (*Bs)[kBlock], int ks, const float (&x)[CT][8]) {
-        bf16x8 xp[CT][3];
-        const f32x4 g0 = *reinterpret_cast<const f32x4*>(&gt.out[32 * ks + 8 * lg]);
-        const f32x4 g1 = *reinterpret_cast<const f32x4*>(&gt.out[32 * ks + 8 * lg + 4]);
+    // S' = e^(last - r) (e^r S + B^T X'), a k-step at a time
+    auto next_state = [&](const unsigned char (*Bs)[kBlock], int ks, bf16x8 (&xp)[CT][3]) {
+        if (!narrow) {
 #pragma unroll
-        for (int ct = 0; ct < CT; ++ct) {
-            f32x4 lo, hi;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                lo[q] = x[ct][q] * g0[q];
-                hi[q] = x[ct][4 + q] * g1[q];
-            }
-            split8<3>(lo, hi, xp[ct]);
+            for (int ct = 0; ct < CT; ++ct) decayed(ks, xp[ct], last_hi, last_lo, kC);
         }
+        if (ks == 0) scale_state(front);
 #pragma unroll
         for (int i = 0; i < NT; i += 2) {   // (two tiles' chains take turns)
+            if constexpr (ES == 4) asm volatile("" ::: "memory");   // (no operands ahead: x takes the registers)
             bf16x8 bp[2][3];
             f32x4 acc[2 * CT];
 #pragma unroll
@@ -285,25 +352,31 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) S[i + k][ct] = acc[k * CT + ct];
         }
+        if (ks == 1) scale_state(tail);
     };
 
     if constexpr (STATE) {
         copy_blocks(rec0 + c0 * rec_row + R::B, sm.C, R::blocks, wave, pl.waves, lane);
+        if (live) {
+            fetch_x(c0, 0);
+            fetch_x(c0, 1);
+        }
         for (int64_t c = c0; c < c1; ++c) {
-            if (live) fetch_x(c, 0);
+            place();
             if (c + 1 < c1) next_dt = fetch_dt(c + 1);
             make_gates(c);
             all_there();
             const bool odd = (c - c0) & 1;
             if (c + 1 < c1) copy_blocks(rec0 + (c + 1) * rec_row + R::B, odd ? sm.C : sm.B, R::blocks, wave, pl.waves, lane);
             if (live) {
-                decay_state();
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     float x[CT][8];
                     convolve(c, ks, x);
-                    if (ks == 0) fetch_x(c, 1);
-                    write(odd ? sm.B : sm.C, ks, x);
+                    if (c + 1 < c1) fetch_x(c + 1, ks);
+                    bf16x8 xp[CT][3];
+                    scaled(ks, x, xp);
+                    next_state(odd ? sm.B : sm.C, ks, xp);
                 }
             }
             dtv = next_dt;
@@ -311,12 +384,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
         if (lane == 0 && live && unit % pl.cols == 0) seg_log[(seg_id / a.G) * a.H + h] = (float)log_sum;
     } else {
         if (c0 < c1) copy_blocks(rec0 + c0 * rec_row + R::C, sm.C, R::blocks, wave, pl.waves, lane);
+        if (live && ES == 2 && c0 < c1) fetch_x(c0, 0);
         for (int64_t c = c0; c < c1; ++c) {
             const char* rec = rec0 + c * rec_row;
+            place();
             make_gates(c);
             all_there();   // C; and every wave is done with the chunk before
-            copy_blocks(rec + R::B, sm.B, R::blocks + 12, wave, pl.waves, lane);   // and G, behind B in both
-            if (live && ES == 2) fetch_x(c, 0);
+            copy_blocks(rec + R::B, sm.B, R::blocks + 18, wave, pl.waves, lane);   // and G, behind B in both
             if (c + 1 < c1) next_dt = fetch_dt(c + 1);
             f32x4 y[4][CT];
 #pragma unroll
@@ -338,83 +412,83 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
                                           [&](int m) -> const bf16x8(&)[3] { return sp[m]; }, y[tt]);
                     }
                 }
-#pragma unroll
-                for (int tt = 0; tt < 4; ++tt) {
-                    const f32x4 e = *reinterpret_cast<const f32x4*>(&gt.in[16 * tt + 4 * lg]);
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) y[tt][ct] *= e;
-                }
-                if (ES == 4) fetch_x(c, 0);   // (twice the registers: not beside C S's operands, nor M's)
+                if (ES == 4) fetch_x(c, 0);   // (twice the registers: not beside the operands of C S, nor those of G X')
             }
             all_there();   // B and G; and every wave is done with C
             if (c + 1 < c1) copy_blocks(rec + rec_row + R::C, sm.C, R::blocks, wave, pl.waves, lane);
             if (live) {
-                decay_state();
                 const auto yb = rows_buf(Y0 + c * kC * yrow * EO, scalar((int)min((int64_t)kC, a.L - c * kC)), scalar((int)(yrow * EO)), scalar((int)(a.P * EO)));
                 const int in = scalar((int)min((int64_t)kC, len - c * kC)) - 4 * lg;
-                int y0 = yat + 4 * lg * (int)(yrow * EO);
-                asm volatile("" : "+v"(y0));   // (else its sums with every row are kept in registers throughout)
+                const int y0 = (mine ? (p0 + CT * li) * EO : kOut) + 4 * lg * (int)(yrow * EO);
+                float (&xs)[CT][16][32] = sm.x[wave];
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks) {
                     float x[CT][8];
                     convolve(c, ks, x);
-                    if (ks == 0 && ES == 2) fetch_x(c, 1);
+                    if (ES == 2 && (ks == 0 || c + 1 < c1)) fetch_x(c + ks, 1 - ks);
                     bf16x8 xp[CT][3];
+                    scaled(ks, x, xp);
+                    // x in the order of y
+                    dchunk::wave_sync();
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
-                        split8<3>(f32x4{x[ct][0], x[ct][1], x[ct][2], x[ct][3]}, f32x4{x[ct][4], x[ct][5], x[ct][6], x[ct][7]}, xp[ct]);
-                    const int s0 = 32 * ks + 8 * lg;
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            *reinterpret_cast<f32x4*>(&xs[ct][li][4 * ((2 * lg + e) ^ (li & 7))]) =
+                                f32x4{x[ct][4 * e], x[ct][4 * e + 1], x[ct][4 * e + 2], x[ct][4 * e + 3]};
+                    dchunk::wave_sync();
 #pragma unroll
                     for (int tt = 2 * ks; tt < 4; ++tt) {
-                        const int t = 16 * tt + li;
-                        const float ht = gt.hi[t], lt = gt.lo[t];
-                        f32x4 m[2];
-                        const f32x4* G = reinterpret_cast<const f32x4*>(sm.G) + g_tile(tt, ks) * 128 + lane * 2;
+                        bf16x8 gp[3];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const f32x4 hs = *reinterpret_cast<const f32x4*>(&gt.hi[s0 + 4 * e]);
-                            const f32x4 ls = *reinterpret_cast<const f32x4*>(&gt.lo[s0 + 4 * e]);
-                            const f32x4 ds = *reinterpret_cast<const f32x4*>(&gt.step[s0 + 4 * e]);
-                            m[e] = G[e];
+                        for (int x3 = 0; x3 < 3; ++x3) gp[x3] = op_at(sm.G, g_tile(tt, ks) * 3 + x3, lane);
+                        if (!narrow) decayed(ks, gp, gt.hi[16 * tt + li], gt.lo[16 * tt + li], 16 * tt + li);
+                        f32x4 acc[CT];
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int d = t - (s0 + 4 * e + j);
-                                const float v = m[e][j] * (fast_exp2((ht - hs[j]) + (lt - ls[j])) * ds[j]);
-                                m[e][j] = d > 0 ? v : d == 0 ? v + skip : 0.0f;
-                            }
+                        for (int ct = 0; ct < CT; ++ct) acc[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                        mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return gp; },
+                                          [&](int i) -> const bf16x8(&)[3] { return xp[i]; }, acc);
+                        const f32x4 f = *reinterpret_cast<const f32x4*>(&gt.f[16 * tt + 4 * lg]);
+                        if (ks == 0) {
+                            const f32x4 e = *reinterpret_cast<const f32x4*>(&gt.in[16 * tt + 4 * lg]);
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct) y[tt][ct] = y[tt][ct] * e + acc[ct] * f;
+                        } else {
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct) y[tt][ct] += acc[ct] * f;
                         }
-                        bf16x8 mp[3];
-                        split8<3>(m[0], m[1], mp);
-                        mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return mp; },
-                                          [&](int i) -> const bf16x8(&)[3] { return xp[i]; }, y[tt]);
                         if (ks == tt / 2) {   // done with these rows
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct)
+                                y[tt][ct] += *reinterpret_cast<const f32x4*>(&xs[ct][li][4 * ((4 * (tt & 1) + lg) ^ (li & 7))]) * skip;
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 float v[CT];
 #pragma unroll
                                 for (int ct = 0; ct < CT; ++ct) v[ct] = 16 * tt + q < in ? y[tt][ct][q] : 0.0f;
-                                store_y<CT>(yb, y0 + (16 * tt + q) * (int)(yrow * EO), v, np, even, Tout(0));
+                                store_y<CT>(yb, y0 + (16 * tt + q) * (int)(yrow * EO), v, Tout(0));
                             }
                         }
                     }
                     if (ks == 0 && ES == 4) fetch_x(c, 1);
-                    write(sm.B, ks, x);
+                    next_state(sm.B, ks, xp);
                 }
             }
             dtv = next_dt;
         }
         // the rest of the segment's tokens, past the end
         for (int64_t t = c1 * kC + lg; t < min(a.L, (c0 + pl.per) * kC); t += 4)
-            for (int i = 0; i < np; ++i) io::st(Y + t * yrow + p0 + i, 0.0f);
+            if (mine)
+                for (int i = 0; i < CT; ++i) io::st(Y + t * yrow + p0 + CT * li + i, 0.0f);
         if (c1 < nch || !a.last) return;
     }
-    float* S1 = STATE ? seg_state + ((seg_id / a.G + 1) * a.H + h) * a.P * a.N + p0 * a.N : a.last + srow * a.N;
+    float* S1 = STATE ? seg_state + (((seg_id / a.G + 1) * a.H + h) * a.P + p0 + CT * li) * a.N : a.last + srow * a.N;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int ct = 0; ct < CT; ++ct) {
             const int n = 16 * i + 4 * lg;
-            if (ct < np && n < a.N) {
+            if (mine && n < a.N) {
                 io::Piece<float, 4> r;
                 r.v = S[i][ct];
                 r.put(S1 + ct * a.N + n);
@@ -431,10 +505,19 @@ __global__ __launch_bounds__(256) void m2_carry_kernel(M2ConvArgs a, Plan pl, fl
     const int64_t len = a.conv.lengths ? min((int64_t)max(a.conv.lengths[b], 0), a.L) : a.L;
     const int64_t n = ((len + kC - 1) / kC + pl.per - 1) / pl.per;   // the sequence's segments
     float s = a.h0 ? a.h0[i] : 0.0f;
-    for (int64_t g = 0; g + 1 < n; ++g) {
+    constexpr int kAhead = 8;   // loads in flight
+    for (int64_t g = 0; g + 1 < n; g += kAhead) {
+        float u[kAhead], d[kAhead];
         float* to = seg_state + ((b * pl.segs + g + 1) * a.H + h) * head + e;
-        s = __builtin_fmaf(fast_exp2(seg_log[(b * pl.segs + g) * a.H + h]), s, *to);
-        *to = s;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (g + k + 1 < n) {
+                u[k] = to[k * a.H * head];
+                d[k] = fast_exp2(seg_log[(b * pl.segs + g + k) * a.H + h]);
+            }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (g + k + 1 < n) to[k * a.H * head] = s = __builtin_fmaf(d[k], s, u[k]);
     }
 }
 
@@ -444,8 +527,8 @@ Plan plan_of(const M2ConvArgs& a) {
     p.np = a.N <= 32 ? 32 : (int)a.N;
     const int64_t heads = a.H / a.G;
     // two column blocks a wave halve the reads of B and C from LDS; one where
-    // a group would not fill a workgroup's waves
-    p.ct = heads * ((a.P + 31) / 32) < kWaves ? 1 : 2;
+    // a group would not fill a workgroup's waves (or pairs of columns P)
+    p.ct = a.P % 2 || heads * ((a.P + 31) / 32) < kWaves ? 1 : 2;
     p.cols = (int)((a.P + 16 * p.ct - 1) / (16 * p.ct));
     p.units = (int)(heads * p.cols);
     p.sets = (p.units + kWaves - 1) / kWaves;
@@ -474,7 +557,7 @@ struct Run {
 
     template <typename Tin, typename Tout, int K, int NP, int CT, bool STATE>
     hipError_t pass() const {
-        constexpr int bytes = (int)sizeof(Smem<NP>);
+        constexpr int bytes = (int)sizeof(Smem<NP, CT>);
         static_assert(bytes <= 160 * 1024, "LDS of a workgroup");
         const auto kern = &m2_chunk_kernel<Tin, Tout, K, NP, CT, STATE>;
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);

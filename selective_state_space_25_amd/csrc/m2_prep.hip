@@ -3,9 +3,11 @@
 // Per (batch, 64-token chunk, group): the short convolution with silu of the
 // group's 2 N channels of B and C in fp32, split into three bf16 planes
 // (split_mfma.hpp) and laid out as the scan's operands (m2_chunk.hpp), and
-// G = C B^T, which the heads of the group share.  A thread has one channel and
-// walks its tokens with the last K - 1 inputs in registers; eight consecutive
-// tokens of it are an operand of B^T as they are, the others are turned in LDS.
+// G = C B^T on and below the diagonal, which the heads of the group share.  A
+// thread has two neighbouring channels and walks 16 tokens (N = 128; fewer
+// for smaller N) with the last K - 1 inputs in registers; eight consecutive
+// tokens of a channel are an operand of B^T as they are, the others are turned
+// in LDS.
 #include "m2_chunk.hpp"
 
 namespace selscan {
@@ -14,12 +16,13 @@ namespace {
 
 using namespace m2chunk;
 
-constexpr int kT = 256;
+constexpr int kT = 512;
 
 template <int NP>
 struct Smem {
     static constexpr int kRow = NP + 8;
     uint16_t p[2][3][kC][kRow];   // B, C; planes; tokens; n in operand order
+    __attribute__((aligned(16))) float g[8][16 * 36];
 };
 
 // Where n stands in its row: the operands' order within each 32.
@@ -29,7 +32,7 @@ template <typename Tin, int K, int NP>
 __global__ __launch_bounds__(kT) void m2_prep_kernel(M2ConvArgs a, char* recs, int64_t chunks) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
     auto& sm = *reinterpret_cast<Smem<NP>*>(smem_raw);
-    constexpr int kSlices = kT / (2 * NP), kTokens = kC / kSlices;   // of a thread
+    constexpr int kSlices = NP == 32 ? 8 : kT / NP, kTokens = kC / kSlices;   // of a thread's two channels
     const int tid = threadIdx.x;
     const int64_t id = io::group_id();
     const int64_t bc = id / a.G, g = id - bc * a.G, b = bc / chunks, c = bc - b * chunks;
@@ -51,81 +54,106 @@ __global__ __launch_bounds__(kT) void m2_prep_kernel(M2ConvArgs a, char* recs, i
     if (t0 >= len) return;
     char* rec = recs + id * Rec<NP>::bytes;
     {
-        const int ch = tid % (2 * NP), isC = ch >= NP, n = ch % NP, first = tid / (2 * NP) * kTokens;
-        const bool live = n < a.N;
+        const int ch = 2 * (tid % NP), isC = ch >= NP, n = ch % NP, first = tid / NP * kTokens;
+        const bool live = n < a.N && first < kC;
         const int64_t cc = a.H * a.P + (isC * a.G + g) * a.N + (live ? n : 0);
-        float w[K], bias = a.conv.bias ? a.conv.bias[cc] : 0.0f;
+        float w[K][2], bias[2];
 #pragma unroll
-        for (int k = 0; k < K; ++k) w[k] = a.conv.weight[cc * K + k];
-        auto input = [&](int64_t t) {
-            if (!live || t >= len) return 0.0f;
-            if (t >= 0) return io::ld(X + t * row + cc);
-            return S ? io::ld(S + (t + K - 1) * C + cc) : 0.0f;
+        for (int i = 0; i < 2; ++i) {
+            bias[i] = a.conv.bias ? a.conv.bias[cc + i] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < K; ++k) w[k][i] = a.conv.weight[(cc + i) * K + k];
+        }
+        auto input = [&](int64_t t, float (&v)[2]) {
+            io::Piece<Tin, 2> r;
+            r.zero();
+            if (live && t < len) {
+                if (t >= 0) r.get(X + t * row + cc);
+                else if (S) r.get(S + (t + K - 1) * C + cc);
+            }
+            r.widen(v);
         };
-        float xs[K - 1 + 8];
+        float xs[K - 1 + kTokens][2];
 #pragma unroll
-        for (int j = 0; j < K - 1; ++j) xs[j] = input(t0 + first - (K - 1) + j);
+        for (int j = 0; j < K - 1 + kTokens; ++j) input(t0 + first - (K - 1) + j, xs[j]);
         uint16_t* to = &sm.p[isC][0][0][place(n)];
-#pragma unroll 2
-        for (int t = first; t < first + kTokens; t += 8) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) xs[K - 1 + j] = input(t0 + t + j);
-            float v[8];
+        for (int t = 0; t < kTokens; t += 8) {
+            if (first >= kC) break;
+            u32x4 p[3][2];   // planes of the eight tokens' channel pairs
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                float pre = bias;
+                float v[2];
+                const bool in = live && t0 + first + t + j < len;
 #pragma unroll
-                for (int k = 0; k < K; ++k) pre = __builtin_fmaf(w[k], xs[j + k], pre);
-                v[j] = live && t0 + t + j < len ? silu_scaled(pre, 1.0f) : 0.0f;
-            }
-            u32x4 p[3];
+                for (int i = 0; i < 2; ++i) {
+                    float pre = bias[i];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split2<3>(v[2 * e], v[2 * e + 1], p, e);
+                    for (int k = 0; k < K; ++k) pre = __builtin_fmaf(w[k][i], xs[t + j + k][i], pre);
+                    v[i] = in ? silu_scaled(pre, 1.0f) : 0.0f;
+                }
+                u32x4 q[3];
+                split2<3>(v[0], v[1], q, 0);
 #pragma unroll
-            for (int x = 0; x < 3; ++x) {
-                if (!isC)
-                    *reinterpret_cast<u32x4*>(rec + Rec<NP>::B + (((n >> 4) * 2 + (t >> 5)) * 3 + x) * kBlock +
-                                              (((t >> 3) & 3) * 16 + (n & 15)) * 16) = p[x];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    to[(x * kC + t + 2 * e) * Smem<NP>::kRow] = (uint16_t)p[x][e];
-                    to[(x * kC + t + 2 * e + 1) * Smem<NP>::kRow] = (uint16_t)(p[x][e] >> 16);
+                for (int x = 0; x < 3; ++x) {
+                    p[x][j >> 2][j & 3] = q[x][0];
+                    *reinterpret_cast<uint32_t*>(to + (x * kC + first + t + j) * Smem<NP>::kRow) = q[x][0];
                 }
             }
+            if (isC) continue;
+            const int tok = first + t;
 #pragma unroll
-            for (int j = 0; j < K - 1; ++j) xs[j] = xs[8 + j];
+            for (int x = 0; x < 3; ++x)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {   // the eight tokens of one channel
+                    u32x4 o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = __builtin_amdgcn_perm(p[x][e >> 1][2 * (e & 1) + 1], p[x][e >> 1][2 * (e & 1)], i ? 0x07060302 : 0x05040100);
+                    *reinterpret_cast<u32x4*>(rec + Rec<NP>::B + (((n >> 4) * 2 + (tok >> 5)) * 3 + x) * kBlock +
+                                              (((tok >> 3) & 3) * 16 + (n & 15) + i) * 16) = o;
+                }
         }
     }
     __syncthreads();
-    const int lane = tid & 63, li = lane & 15, lg = lane >> 4, tt = __builtin_amdgcn_readfirstlane(tid >> 6);
-    f32x4 acc[4];
+    // G: a wave has the columns 32 ks .. of rows 16 tt ..
+    const int lane = tid & 63, li = lane & 15, lg = lane >> 4, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tt = wave >> 1, half = wave & 1;
+    f32x4 acc[2];
 #pragma unroll
-    for (int s = 0; s < 4; ++s) acc[s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < 2; ++s) acc[s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int ks = 0; ks < NP / 32; ++ks) {
-        bf16x8 cp[3];
+        bf16x8 cp[3], bp[2][3];
 #pragma unroll
         for (int x = 0; x < 3; ++x) {
             cp[x] = ld8(&sm.p[1][x][16 * tt + li][32 * ks + 8 * lg]);
-            *reinterpret_cast<bf16x8*>(rec + ((ks * 4 + tt) * 3 + x) * kBlock + lane * 16) = cp[x];
+            if (half == (ks & 1)) *reinterpret_cast<bf16x8*>(rec + ((ks * 4 + tt) * 3 + x) * kBlock + lane * 16) = cp[x];
         }
+        if (2 * half > tt) continue;   // (the store above is the other half's too)
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-            if (s <= tt) {
-                bf16x8 bp[3];
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int x = 0; x < 3; ++x) bp[x] = ld8(&sm.p[0][x][16 * s + li][32 * ks + 8 * lg]);
-                acc[s] = mm<3>(cp, bp, acc[s]);
-            }
+            for (int x = 0; x < 3; ++x) bp[s][x] = ld8(&sm.p[0][x][32 * half + 16 * s + li][32 * ks + 8 * lg]);
+        mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return cp; }, [&](int m) -> const bf16x8(&)[3] { return bp[m]; }, acc);
     }
-    float* G = reinterpret_cast<float*>(rec + Rec<NP>::G);
+    if (2 * half > tt) return;
+    // through LDS into operand order, zero above the diagonal
+    float* to = sm.g[wave];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-        if (s <= tt) {
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)   // row 16 tt + 4 lg + q, column 16 s + li
-                G[g_tile(tt, s >> 1) * 512 + (4 * lg + q + 16 * (2 * (s & 1) + (li >> 3))) * 8 + (li & 7)] = acc[s][q];
+        for (int q = 0; q < 4; ++q) {
+            const int t = 4 * lg + q, col = 16 * s + li;   // row 16 tt + t, column 32 half + col
+            to[t * 36 + col] = 32 * half + col <= 16 * tt + t ? acc[s][q] : 0.0f;
         }
+    dchunk::wave_sync();
+    const float* from = to + li * 36 + 8 * lg;
+    bf16x8 gp[3];
+    split8<3>(*reinterpret_cast<const f32x4*>(from), *reinterpret_cast<const f32x4*>(from + 4), gp);
+#pragma unroll
+    for (int x = 0; x < 3; ++x)
+        *reinterpret_cast<bf16x8*>(rec + Rec<NP>::G + (g_tile(tt, half) * 3 + x) * kBlock + lane * 16) = gp[x];
 }
 
 template <typename Tin, int K, int NP>
