@@ -7,14 +7,16 @@
 //   Y  = e^cum (C S) + M X + D x,   M[t, s] = G[t, s] e^(cum_t - cum_s) D_s  (s <= t)
 //   S' = e^last S + B^T (D e^(last - cum) X)
 //
-// and with X' = e^(r - cum) D X, r half of last,
+// and with X'_s = e^(r - cum_s) D_s x_s, r the middle of cum over the 32 tokens
+// (0 and 1: the halves) that s is in,
 //
-//   M X = e^(cum - r) (G X');   S' = e^(last - r) (e^r S + B^T X')
+//   M X = e^(cum - r0) (G X'0) + e^(cum - r1) (G X'1)
+//   S'  = e^(last - r1) (e^(r1 - r0) (e^r0 S + B^T X'0) + B^T X'1)
 //
 // so that one split of X' into planes serves both products and G's planes are
-// the group's, whatever the head.  Where a chunk's decays span more than 2^120
-// the powers of two would leave fp32's range: such a head's M is made element
-// by element.
+// the group's, whatever the head.  Where the decays of 32 tokens span more than
+// 2^120 the powers of two would leave fp32's range: such a chunk's M is made
+// element by element.
 //
 // A wave owns 16 CT value columns of a head and walks the chunks with its S in
 // accumulators, which are the operands of C S as they are: nothing of a head
@@ -46,16 +48,19 @@ using dchunk::buf_st;
 using dchunk::kOut;
 using dchunk::rows_buf;
 
+// (lambdas that are called more than once would be calls, with a stack)
+#define SELSCAN_INLINE __attribute__((always_inline))
+
 constexpr int kWaves = 8;
 
-// Most that a chunk's decays span (log2) for r's powers of two: x D of 2^-30
-// keeps its three planes, of 2^60 stays finite.
+// Most that the decays of 32 tokens span (log2) for r's powers of two: x D of
+// 2^-30 keeps its three planes, of 2^60 stays finite.
 constexpr double kSpan = 120.0;
 
-// Per token of a wave's head: e^cum, e^(cum - r), D e^(r - cum).  With decays
-// past kSpan f is 1, h is D, and cum stands in two parts (log2).
+// Per token of a wave's head: e^cum, e^(cum - r0), e^(cum - r1), D e^(r - cum).
+// With decays past kSpan f0 and f1 are cum in two parts (log2), h is D.
 struct Gates {
-    float in[kC], f[kC], h[kC], hi[kC], lo[kC];
+    float in[kC], f0[kC], f1[kC], h[kC];
 };
 
 template <int NP, int CT>
@@ -84,9 +89,10 @@ __device__ __forceinline__ double sum_to_lane(double v) {
     v = add_moved<0x142, 0xa>(v);   // lane 15 to the second 16, 47 to the fourth
     return add_moved<0x143, 0xc>(v);   // lane 31 to the upper half
 }
-__device__ __forceinline__ double of_lane_63(double v) {
+template <int LANE>
+__device__ __forceinline__ double of_lane(double v) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, 63), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), 63);
+    const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)u, LANE), hi = __builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), LANE);
     return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
 }
 
@@ -148,6 +154,23 @@ __device__ __forceinline__ bf16x8 op_at(const unsigned char (*blocks)[kBlock], i
     return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(&blocks[i][lane * 16]));
 }
 
+// Of the instructions before it, G times M matrix products, V vector
+// instructions behind each, whose time the products hide, and R LDS reads that
+// the next M need ahead of them.
+template <int G, int R, int M, int V>
+__device__ __forceinline__ void mix() {
+    __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+#pragma unroll
+    for (int g = 0; g < G; ++g) {
+        if (g + 1 < G) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+#pragma unroll
+        for (int i = 0; i < M; ++i) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+        }
+    }
+}
+
 // STATE: the first pass, a segment's state from zero and the sum of its log2 decays.
 template <typename Tin, typename Tout, int K, int NP, int CT, bool STATE>
 __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, Plan pl, const char* recs, float* seg_state,
@@ -159,7 +182,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
     // Anew for each chunk: whatever follows from the lane alone would be kept in
     // registers throughout, and there are none left for it.
-    auto place = [&]() {
+    auto place = [&]() SELSCAN_INLINE {
         lane = threadIdx.x & 63;
         asm volatile("" : "+v"(lane));
         li = lane & 15;
@@ -224,35 +247,35 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     char* Y0 = scalar(reinterpret_cast<char*>(Y));
     const char* rec0 = recs + (b * pl.chunks * a.G + grp) * R::bytes;
     const int64_t rec_row = a.G * R::bytes;
-    auto fetch_dt = [&](int64_t c) {
+    auto fetch_dt = [&](int64_t c) SELSCAN_INLINE {
         const int64_t t = c * kC + lane;
         return t < len ? io::ld(T + t * a.dt_row) : 0.0f;
     };
     // The lane's raw x of a k-step: tokens 32 ks + 8 lg - (K - 1) .. + 7 of its
     // columns.  Past the end, and before the first token, the buffer gives zero.
     using RX = RawX<Tin, CT>;
-    RX xr[STATE ? 2 : 1][K - 1 + 8];
+    RX xr[K - 1 + 8];
     const int xrow = scalar((int)(a.conv.x_row * ES)), xbytes = scalar((int)(a.P * ES));
-    auto fetch_x = [&](int64_t c, int ks) {
+    auto fetch_x = [&](int64_t c, int ks, bool later = true) SELSCAN_INLINE {   // later: chunk 0 it is not
         const int64_t t0 = c * kC;
-        const int before = c > 0 ? K - 1 : 0;
+        const int before = later ? K - 1 : 0;
         const auto xb = rows_buf(X0 + (t0 - before) * xrow, scalar((int)min((int64_t)(kC + before), len - t0 + before)), xrow, xbytes);
         const int at = mine ? (p0 + CT * li) * ES + (8 * lg + before - (K - 1)) * xrow : kOut;
 #pragma unroll
-        for (int j = 0; j < K - 1 + 8; ++j) xr[STATE ? ks : 0][j] = buf_x<Tin, CT>(xb, at + (32 * ks + j) * xrow);
-        if (ks == 0 && c == 0 && XS && lg == 0 && mine) {
+        for (int j = 0; j < K - 1 + 8; ++j) xr[j] = buf_x<Tin, CT>(xb, at + (32 * ks + j) * xrow);
+        if (!later && ks == 0 && XS && lg == 0 && mine) {
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
                 io::Piece<Tin, CT> r;
                 r.get(XS + j * C + p0 + CT * li);
-                xr[0][j] = __builtin_bit_cast(RX, r);
+                xr[j] = __builtin_bit_cast(RX, r);
             }
         }
     };
     auto convolve = [&](int64_t c, int ks, float (&x)[CT][8]) {
         float r[K - 1 + 8][CT];
 #pragma unroll
-        for (int j = 0; j < K - 1 + 8; ++j) widen(xr[STATE ? ks : 0][j], r[j]);
+        for (int j = 0; j < K - 1 + 8; ++j) widen(xr[j], r[j]);
         const int in = scalar((int)min((int64_t)kC, len - c * kC)) - (32 * ks + 8 * lg);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -264,36 +287,40 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
                 x[i][j] = j < in ? silu_scaled(pre, 1.0f) : 0.0f;
             }
     };
-    float dtv = c0 < c1 ? fetch_dt(c0) : 0.0f, next_dt = 0.0f;
-    double log_sum = 0.0;
-    float front = 1.0f, tail = 1.0f, last_hi = 0.0f, last_lo = 0.0f;   // e^r, e^(last - r); past kSpan e^last, 1; last
-    bool narrow = true;                                                // the chunk's decays are within kSpan
+    float dtv = c0 < c1 ? fetch_dt(c0) : 0.0f;
+    double chunk_log = 0.0;   // its log2 decay
+    // e^r0, e^(r1 - r0), e^(last - r1); past kSpan e^last, 1, 1, and last
+    float front = 1.0f, mid = 1.0f, tail = 1.0f, last_hi = 0.0f, last_lo = 0.0f;
+    bool narrow = true;   // the chunk's decays are within kSpan
     // the chunk's gates, a token a lane
-    auto make_gates = [&](int64_t c) {
+    auto make_gates = [&](int64_t c) SELSCAN_INLINE {
         const bool in = c * kC + lane < len;
         const float sp = in ? softplus_log2((dtv + dt_bias) * kLog2e) : 0.0f;
         double cum = in ? (double)sp * (double)A : 0.0;
-        cum = cum < -1e6 ? -1e6 : cum;   // (a decay of zero either way; stays finite)
-        cum = sum_to_lane(cum);
-        const double last = of_lane_63(cum), r = 0.5 * last;
+        cum = sum_to_lane(cum < -1e6 ? -1e6 : cum);   // (a decay of zero either way; stays finite)
+        const double half = of_lane<31>(cum), last = of_lane<63>(cum);
+        const double r0 = 0.5 * half, r1 = 0.5 * (half + last), r = lane < 32 ? r0 : r1;
         const float step = sp * kLn2;
-        narrow = __builtin_amdgcn_readfirstlane(last >= -kSpan && last <= kSpan ? 1 : 0) != 0;
+        narrow = half >= -kSpan && last - half >= -kSpan && half <= 100.0 && last <= 100.0;
         if constexpr (!STATE) gt.in[lane] = exp2_of(cum);
         if (narrow) {
-            if constexpr (!STATE) gt.f[lane] = exp2_of(cum - r);
+            if constexpr (!STATE) {
+                gt.f0[lane] = exp2_of(cum - r0);
+                gt.f1[lane] = exp2_of(cum - r1);
+            }
             gt.h[lane] = step * exp2_of(r - cum);
         } else {
             const float hi = (float)cum;
-            gt.f[lane] = 1.0f;
+            gt.f0[lane] = hi;
+            gt.f1[lane] = (float)(cum - (double)hi);
             gt.h[lane] = step;
-            gt.hi[lane] = hi;
-            gt.lo[lane] = (float)(cum - (double)hi);
             last_hi = (float)last;
             last_lo = (float)(last - (double)last_hi);
         }
-        front = exp2_of(narrow ? r : last);
-        tail = narrow ? front : 1.0f;
-        log_sum += last;
+        front = exp2_of(narrow ? r0 : last);
+        mid = exp2_of(narrow ? r1 - r0 : 0.0);
+        tail = exp2_of(narrow ? last - r1 : 0.0);
+        chunk_log = last;
         dchunk::wave_sync();
     };
     // X' of a k-step from its x
@@ -307,174 +334,213 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     // what decays past kSpan leave to do: the values of planes times e^(to - cum_s), s = the k-step's tokens up to `most`
     auto decayed = [&](int ks, bf16x8 (&p)[3], float to_hi, float to_lo, int most) {
         const int s0 = 32 * ks + 8 * lg;
+        asm volatile("" ::: "memory");   // (cum is read again each time: it has no registers to stay in)
         f32x4 v[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const f32x4 hs = *reinterpret_cast<const f32x4*>(&gt.hi[s0 + 4 * e]);
-            const f32x4 ls = *reinterpret_cast<const f32x4*>(&gt.lo[s0 + 4 * e]);
+            const f32x4 hs = *reinterpret_cast<const f32x4*>(&gt.f0[s0 + 4 * e]);
+            const f32x4 ls = *reinterpret_cast<const f32x4*>(&gt.f1[s0 + 4 * e]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 const float g = ((float)p[0][4 * e + j] + (float)p[1][4 * e + j]) + (float)p[2][4 * e + j];
-                v[e][j] = s0 + 4 * e + j <= most ? g * fast_exp2((to_hi - hs[j]) + (to_lo - ls[j])) : 0.0f;
+                const float d = (to_hi - hs[j]) + (to_lo - ls[j]);
+                v[e][j] = g * fast_exp2(s0 + 4 * e + j <= most ? d : -1e30f);   // (G above its diagonal is zero, not e^d)
             }
         }
         split8<3>(v[0], v[1], p);
     };
-    auto scale_state = [&](float by) {
+    auto decayed_x = [&](int ks, bf16x8 (&xp)[CT][3]) {
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct) decayed(ks, xp[ct], last_hi, last_lo, kC);
+    };
+    auto scale_state = [&](float by) SELSCAN_INLINE {
 #pragma unroll
         for (int i = 0; i < NT; ++i)
 #pragma unroll
             for (int ct = 0; ct < CT; ++ct) S[i][ct] *= by;
     };
-    // S' = e^(last - r) (e^r S + B^T X'), a k-step at a time
-    auto next_state = [&](const unsigned char (*Bs)[kBlock], int ks, bf16x8 (&xp)[CT][3]) {
-        if (!narrow) {
+    // S += B^T X' over a k-step
+    auto write = [&](const unsigned char (*Bs)[kBlock], int ks, const bf16x8 (&xp)[CT][3]) {
 #pragma unroll
-            for (int ct = 0; ct < CT; ++ct) decayed(ks, xp[ct], last_hi, last_lo, kC);
+        for (int i = 0; i < NT; ++i) {
+            bf16x8 bp[3];
+#pragma unroll
+            for (int x3 = 0; x3 < 3; ++x3) bp[x3] = op_at(Bs, (i * 2 + ks) * 3 + x3, lane);
+            mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return bp; },
+                              [&](int m) -> const bf16x8(&)[3] { return xp[m]; }, S[i]);
         }
-        if (ks == 0) scale_state(front);
-#pragma unroll
-        for (int i = 0; i < NT; i += 2) {   // (two tiles' chains take turns)
-            if constexpr (ES == 4) asm volatile("" ::: "memory");   // (no operands ahead: x takes the registers)
-            bf16x8 bp[2][3];
-            f32x4 acc[2 * CT];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-#pragma unroll
-                for (int x3 = 0; x3 < 3; ++x3) bp[k][x3] = op_at(Bs, ((i + k) * 2 + ks) * 3 + x3, lane);
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) acc[k * CT + ct] = S[i + k][ct];
-            }
-            mm_turns<3, 3, 3>([&](int m) -> const bf16x8(&)[3] { return bp[m / CT]; },
-                              [&](int m) -> const bf16x8(&)[3] { return xp[m % CT]; }, acc);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int ct = 0; ct < CT; ++ct) S[i + k][ct] = acc[k * CT + ct];
-        }
-        if (ks == 1) scale_state(tail);
     };
+    // beside each of its products: a k-step's x and X'
+    constexpr int kV = (100 * CT + 6 * CT * NT - 1) / (6 * CT * NT);
 
+    // A chunk's gates and its first raw x stand ready when it begins (the state
+    // pass: its first X'), made beside the chunk before's last products.
+    bf16x8 x0p[CT][3], x1p[CT][3];
+    float x[CT][8];
+    if (c0 < c1) {
+        if (live) fetch_x(c0, 0, c0 > 0);
+        make_gates(c0);
+        if (STATE && live) {
+            convolve(c0, 0, x);
+            fetch_x(c0, 1, c0 > 0);
+            scaled(0, x, x0p);
+        }
+        dtv = c0 + 1 < c1 ? fetch_dt(c0 + 1) : 0.0f;
+    }
     if constexpr (STATE) {
         copy_blocks(rec0 + c0 * rec_row + R::B, sm.C, R::blocks, wave, pl.waves, lane);
-        if (live) {
-            fetch_x(c0, 0);
-            fetch_x(c0, 1);
-        }
+        double seg_sum = 0.0;
         for (int64_t c = c0; c < c1; ++c) {
             place();
-            if (c + 1 < c1) next_dt = fetch_dt(c + 1);
-            make_gates(c);
+            seg_sum += chunk_log;
             all_there();
             const bool odd = (c - c0) & 1;
+            const unsigned char(*Bs)[kBlock] = odd ? sm.B : sm.C;
             if (c + 1 < c1) copy_blocks(rec0 + (c + 1) * rec_row + R::B, odd ? sm.C : sm.B, R::blocks, wave, pl.waves, lane);
+            if (live && !narrow) decayed_x(0, x0p);
+            scale_state(front);
             if (live) {
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    float x[CT][8];
-                    convolve(c, ks, x);
-                    if (c + 1 < c1) fetch_x(c + 1, ks);
-                    bf16x8 xp[CT][3];
-                    scaled(ks, x, xp);
-                    next_state(odd ? sm.B : sm.C, ks, xp);
-                }
+                convolve(c, 1, x);
+                fetch_x(c + 1, 0);
+                scaled(1, x, x1p);
+                write(Bs, 0, x0p);
+                mix<NT, 3, 6 * CT, kV>();
+                if (!narrow) decayed_x(1, x1p);
+                scale_state(mid);
             }
-            dtv = next_dt;
+            const float out = tail;
+            make_gates(c + 1);
+            if (live) {
+                convolve(c + 1, 0, x);
+                fetch_x(c + 1, 1);
+                scaled(0, x, x0p);
+                write(Bs, 1, x1p);
+                mix<NT, 3, 6 * CT, kV>();
+                scale_state(out);
+            }
+            dtv = c + 2 < c1 ? fetch_dt(c + 2) : 0.0f;
         }
-        if (lane == 0 && live && unit % pl.cols == 0) seg_log[(seg_id / a.G) * a.H + h] = (float)log_sum;
+        if (lane == 0 && live && unit % pl.cols == 0) seg_log[(seg_id / a.G) * a.H + h] = (float)seg_sum;
     } else {
         if (c0 < c1) copy_blocks(rec0 + c0 * rec_row + R::C, sm.C, R::blocks, wave, pl.waves, lane);
-        if (live && ES == 2 && c0 < c1) fetch_x(c0, 0);
+        float(&xs)[CT][16][32] = sm.x[wave];
+        // a k-step's x into the order of y
+        auto turn = [&]() SELSCAN_INLINE {
+            dchunk::wave_sync();
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    *reinterpret_cast<f32x4*>(&xs[ct][li][4 * ((2 * lg + e) ^ (li & 7))]) =
+                        f32x4{x[ct][4 * e], x[ct][4 * e + 1], x[ct][4 * e + 2], x[ct][4 * e + 3]};
+            dchunk::wave_sync();
+        };
         for (int64_t c = c0; c < c1; ++c) {
             const char* rec = rec0 + c * rec_row;
             place();
-            make_gates(c);
             all_there();   // C; and every wave is done with the chunk before
             copy_blocks(rec + R::B, sm.B, R::blocks + 18, wave, pl.waves, lane);   // and G, behind B in both
-            if (c + 1 < c1) next_dt = fetch_dt(c + 1);
             f32x4 y[4][CT];
 #pragma unroll
             for (int tt = 0; tt < 4; ++tt)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) y[tt][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             if (live) {
+                bf16x8 sp[2][CT][3];
+                auto split_state = [&](int ks) SELSCAN_INLINE {
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) split8<3>(S[2 * ks][ct], S[2 * ks + 1][ct], sp[ks & 1][ct]);
+                };
+                split_state(0);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    bf16x8 sp[CT][3];
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) split8<3>(S[2 * ks][ct], S[2 * ks + 1][ct], sp[ct]);
+                    if (ks + 1 < KS) split_state(ks + 1);
 #pragma unroll
                     for (int tt = 0; tt < 4; ++tt) {
                         bf16x8 cp[3];
 #pragma unroll
                         for (int x3 = 0; x3 < 3; ++x3) cp[x3] = op_at(sm.C, (ks * 4 + tt) * 3 + x3, lane);
                         mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return cp; },
-                                          [&](int m) -> const bf16x8(&)[3] { return sp[m]; }, y[tt]);
+                                          [&](int m) -> const bf16x8(&)[3] { return sp[ks & 1][m]; }, y[tt]);
                     }
+                    if (ks + 1 < KS) mix<4, 3, 6 * CT, 2>();
                 }
-                if (ES == 4) fetch_x(c, 0);   // (twice the registers: not beside the operands of C S, nor those of G X')
             }
             all_there();   // B and G; and every wave is done with C
             if (c + 1 < c1) copy_blocks(rec + rec_row + R::C, sm.C, R::blocks, wave, pl.waves, lane);
-            if (live) {
-                const auto yb = rows_buf(Y0 + c * kC * yrow * EO, scalar((int)min((int64_t)kC, a.L - c * kC)), scalar((int)(yrow * EO)), scalar((int)(a.P * EO)));
-                const int in = scalar((int)min((int64_t)kC, len - c * kC)) - 4 * lg;
-                const int y0 = (mine ? (p0 + CT * li) * EO : kOut) + 4 * lg * (int)(yrow * EO);
-                float (&xs)[CT][16][32] = sm.x[wave];
+            if (!live) continue;
+            const auto yb = rows_buf(Y0 + c * kC * yrow * EO, scalar((int)min((int64_t)kC, a.L - c * kC)), scalar((int)(yrow * EO)), scalar((int)(a.P * EO)));
+            const int in = scalar((int)min((int64_t)kC, len - c * kC)) - 4 * lg;
+            const int y0 = (mine ? (p0 + CT * li) * EO : kOut) + 4 * lg * (int)(yrow * EO);
+            // G X' of a k-step; with decays past kSpan M X
+            auto add_gx = [&](auto fast, int ks, const bf16x8 (&xp)[CT][3]) {
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    float x[CT][8];
-                    convolve(c, ks, x);
-                    if (ES == 2 && (ks == 0 || c + 1 < c1)) fetch_x(c + ks, 1 - ks);
-                    bf16x8 xp[CT][3];
-                    scaled(ks, x, xp);
-                    // x in the order of y
-                    dchunk::wave_sync();
+                for (int tt = 2 * ks; tt < 4; ++tt) {
+                    bf16x8 gp[3];
+#pragma unroll
+                    for (int x3 = 0; x3 < 3; ++x3) gp[x3] = op_at(sm.G, g_tile(tt, ks) * 3 + x3, lane);
+                    if constexpr (!decltype(fast)::value) decayed(ks, gp, gt.f0[16 * tt + li], gt.f1[16 * tt + li], 16 * tt + li);
+                    f32x4 acc[CT];
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) acc[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return gp; },
+                                      [&](int i) -> const bf16x8(&)[3] { return xp[i]; }, acc);
+                    f32x4 f = {1.0f, 1.0f, 1.0f, 1.0f};
+                    if constexpr (decltype(fast)::value) f = *reinterpret_cast<const f32x4*>(&(ks ? gt.f1 : gt.f0)[16 * tt + 4 * lg]);
+                    f32x4 e = {1.0f, 1.0f, 1.0f, 1.0f};
+                    if (ks == 0) e = *reinterpret_cast<const f32x4*>(&gt.in[16 * tt + 4 * lg]);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct) y[tt][ct] = ks == 0 ? y[tt][ct] * e + acc[ct] * f : y[tt][ct] + acc[ct] * f;
+                }
+            };
+            // the rows of a k-step's tokens
+            auto put_y = [&](int ks) SELSCAN_INLINE {
+#pragma unroll
+                for (int tt = 2 * ks; tt < 2 * ks + 2; ++tt) {
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
+                        y[tt][ct] += *reinterpret_cast<const f32x4*>(&xs[ct][li][4 * ((4 * (tt & 1) + lg) ^ (li & 7))]) * skip;
 #pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            *reinterpret_cast<f32x4*>(&xs[ct][li][4 * ((2 * lg + e) ^ (li & 7))]) =
-                                f32x4{x[ct][4 * e], x[ct][4 * e + 1], x[ct][4 * e + 2], x[ct][4 * e + 3]};
-                    dchunk::wave_sync();
+                    for (int q = 0; q < 4; ++q) {
+                        float v[CT];
 #pragma unroll
-                    for (int tt = 2 * ks; tt < 4; ++tt) {
-                        bf16x8 gp[3];
-#pragma unroll
-                        for (int x3 = 0; x3 < 3; ++x3) gp[x3] = op_at(sm.G, g_tile(tt, ks) * 3 + x3, lane);
-                        if (!narrow) decayed(ks, gp, gt.hi[16 * tt + li], gt.lo[16 * tt + li], 16 * tt + li);
-                        f32x4 acc[CT];
-#pragma unroll
-                        for (int ct = 0; ct < CT; ++ct) acc[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                        mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return gp; },
-                                          [&](int i) -> const bf16x8(&)[3] { return xp[i]; }, acc);
-                        const f32x4 f = *reinterpret_cast<const f32x4*>(&gt.f[16 * tt + 4 * lg]);
-                        if (ks == 0) {
-                            const f32x4 e = *reinterpret_cast<const f32x4*>(&gt.in[16 * tt + 4 * lg]);
-#pragma unroll
-                            for (int ct = 0; ct < CT; ++ct) y[tt][ct] = y[tt][ct] * e + acc[ct] * f;
-                        } else {
-#pragma unroll
-                            for (int ct = 0; ct < CT; ++ct) y[tt][ct] += acc[ct] * f;
-                        }
-                        if (ks == tt / 2) {   // done with these rows
-#pragma unroll
-                            for (int ct = 0; ct < CT; ++ct)
-                                y[tt][ct] += *reinterpret_cast<const f32x4*>(&xs[ct][li][4 * ((4 * (tt & 1) + lg) ^ (li & 7))]) * skip;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                float v[CT];
-#pragma unroll
-                                for (int ct = 0; ct < CT; ++ct) v[ct] = 16 * tt + q < in ? y[tt][ct][q] : 0.0f;
-                                store_y<CT>(yb, y0 + (16 * tt + q) * (int)(yrow * EO), v, Tout(0));
-                            }
-                        }
+                        for (int ct = 0; ct < CT; ++ct) v[ct] = 16 * tt + q < in ? y[tt][ct][q] : 0.0f;
+                        store_y<CT>(yb, y0 + (16 * tt + q) * (int)(yrow * EO), v, Tout(0));
                     }
-                    if (ks == 0 && ES == 4) fetch_x(c, 1);
-                    next_state(sm.B, ks, xp);
                 }
+            };
+            convolve(c, 0, x);
+            fetch_x(c, 1, c > 0);
+            turn();
+            scaled(0, x, x0p);
+            if (narrow) {
+                add_gx(std::true_type(), 0, x0p);
+            } else {
+                add_gx(std::false_type(), 0, x0p);
+                decayed_x(0, x0p);
             }
-            dtv = next_dt;
+            put_y(0);
+            scale_state(front);
+            convolve(c, 1, x);
+            fetch_x(c + 1, 0);
+            scaled(1, x, x1p);
+            write(sm.B, 0, x0p);
+            mix<NT, 3, 6 * CT, kV>();
+            turn();
+            if (narrow) {
+                add_gx(std::true_type(), 1, x1p);
+            } else {
+                add_gx(std::false_type(), 1, x1p);
+                decayed_x(1, x1p);
+            }
+            put_y(1);
+            scale_state(mid);
+            const float out = tail;
+            make_gates(c + 1);
+            write(sm.B, 1, x1p);
+            mix<NT, 3, 6 * CT, 1>();
+            scale_state(out);
+            dtv = c + 2 < c1 ? fetch_dt(c + 2) : 0.0f;
         }
         // the rest of the segment's tokens, past the end
         for (int64_t t = c1 * kC + lg; t < min(a.L, (c0 + pl.per) * kC); t += 4)
@@ -521,22 +587,26 @@ __global__ __launch_bounds__(256) void m2_carry_kernel(M2ConvArgs a, Plan pl, fl
     }
 }
 
-Plan plan_of(const M2ConvArgs& a) {
+Plan plan_of(const M2ConvArgs& a, int in_bf16, bool ragged) {
     Plan p;
     p.chunks = (a.L + kC - 1) / kC;
     p.np = a.N <= 32 ? 32 : (int)a.N;
     const int64_t heads = a.H / a.G;
     // two column blocks a wave halve the reads of B and C from LDS; one where
-    // a group would not fill a workgroup's waves (or pairs of columns P)
-    p.ct = a.P % 2 || heads * ((a.P + 31) / 32) < kWaves ? 1 : 2;
+    // a group would not fill a workgroup's waves, pairs of columns P, or (fp32,
+    // N = 128) two blocks a wave's registers
+    p.ct = a.P % 2 || heads * ((a.P + 31) / 32) < kWaves || (!in_bf16 && p.np == 128) ? 1 : 2;
     p.cols = (int)((a.P + 16 * p.ct - 1) / (16 * p.ct));
     p.units = (int)(heads * p.cols);
     p.sets = (p.units + kWaves - 1) / kWaves;
     p.waves = (p.units + p.sets - 1) / p.sets;
-    // segments: enough workgroups for the GPU, four chunks each at least
-    const int64_t groups = a.batch * a.G * p.sets;
-    const int64_t want = host::env_int("SELSCAN_M2_SEG_WGS", 512);
-    p.segs = std::max<int64_t>(1, std::min((want + groups - 1) / groups, p.chunks / host::env_int("SELSCAN_M2_SEG_MIN", 4)));
+    // Segments of two chunks and more: a workgroup for each compute unit, which
+    // holds one; four where sequences may end early and leave units without
+    // (batch 1, L 16384, 32 heads of 64 x 128: 241 us, with two workgroups a
+    // unit 269; lengths spread over 0 .. 4096, batch 8: 418 us with two, 365
+    // with four).
+    const int64_t groups = a.batch * a.G * p.sets, want = (int64_t)host::device_cus() * (ragged ? 4 : 1);
+    p.segs = std::max<int64_t>(1, std::min((want + groups - 1) / groups, p.chunks / 2));
     p.per = (p.chunks + p.segs - 1) / p.segs;
     p.segs = (p.chunks + p.per - 1) / p.per;
     return p;
@@ -579,7 +649,12 @@ struct Run {
         return pass<Tin, Tout, K, NP, CT, false>();
     }
     template <typename Tin, typename Tout, int K, int NP>
-    hipError_t by_ct() const { return pl.ct == 1 ? run<Tin, Tout, K, NP, 1>() : run<Tin, Tout, K, NP, 2>(); }
+    hipError_t two_blocks() const {
+        if constexpr (sizeof(Tin) == 2 || NP < 128) return run<Tin, Tout, K, NP, 2>();
+        else return hipErrorInvalidValue;
+    }
+    template <typename Tin, typename Tout, int K, int NP>
+    hipError_t by_ct() const { return pl.ct == 1 ? run<Tin, Tout, K, NP, 1>() : two_blocks<Tin, Tout, K, NP>(); }
     template <typename Tin, typename Tout, int K>
     hipError_t by_np() const {
         return pl.np == 32 ? by_ct<Tin, Tout, K, 32>() : pl.np == 64 ? by_ct<Tin, Tout, K, 64>() : by_ct<Tin, Tout, K, 128>();
@@ -592,13 +667,13 @@ struct Run {
 
 }  // namespace
 
-size_t m2_chunk_bytes(const M2ConvArgs& a) {
-    const Plan p = plan_of(a);
+size_t m2_chunk_bytes(const M2ConvArgs& a, int in_bf16) {
+    const Plan p = plan_of(a, in_bf16, true);   // (as many segments at least as without lengths)
     return all_rec_bytes(a, p) + seg_bytes(a, p) + (p.segs == 1 ? 0 : host::align256((size_t)(a.batch * p.segs * a.H) * 4));
 }
 
 hipError_t launch_m2_chunk(const M2ConvArgs& a, int in_bf16, int out_bf16, void* ws, hipStream_t stream) {
-    const Plan p = plan_of(a);
+    const Plan p = plan_of(a, in_bf16, a.conv.lengths != nullptr);
     char* recs = static_cast<char*>(ws);
     char* states = recs + all_rec_bytes(a, p);
     const Run r{a, p, recs, reinterpret_cast<float*>(states), reinterpret_cast<float*>(states + seg_bytes(a, p)), stream};

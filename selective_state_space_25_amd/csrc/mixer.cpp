@@ -122,7 +122,9 @@ constexpr int64_t kRecTokens = 16;
 // The chunked form's offsets inside 64 tokens and the three before are 32-bit.
 bool chunked(const selscan::M2ConvArgs& a) { return a.L > kRecTokens && a.conv.x_row < ((int64_t)1 << 30) / (4 * 68); }
 
-size_t mixer_bytes(const selscan::M2ConvArgs& a) { return chunked(a) ? selscan::m2_chunk_bytes(a) : selscan::m2_rec_bytes(a); }
+size_t mixer_bytes(const selscan::M2ConvArgs& a, int in_bf16) {
+    return chunked(a) ? selscan::m2_chunk_bytes(a, in_bf16) : selscan::m2_rec_bytes(a);
+}
 
 }  // namespace
 
@@ -212,7 +214,7 @@ size_t selscan_mamba2_conv_workspace_bytes(const selscan_m2_conv_shape_t* s) {
     if (check_mixer(s, false) != SELSCAN_OK) return 0;
     selscan::M2ConvArgs a{};
     fill(a, s, false);
-    return mixer_bytes(a);
+    return mixer_bytes(a, s->in_dtype == SELSCAN_BF16);
 }
 
 selscan_status_t selscan_mamba2_conv_fwd(const selscan_m2_conv_shape_t* s, const void* xbc, const void* dt,
@@ -234,7 +236,7 @@ selscan_status_t selscan_mamba2_conv_fwd(const selscan_m2_conv_shape_t* s, const
         selscan::M2ConvArgs a{};
         fill(a, s, false);
         Scratch ws;
-        st = ws.get(s->workspace, s->workspace_bytes, mixer_bytes(a), hs);
+        st = ws.get(s->workspace, s->workspace_bytes, mixer_bytes(a, s->in_dtype == SELSCAN_BF16), hs);
         if (st != SELSCAN_OK) return st;
         a.conv.x = xbc; a.conv.weight = conv_weight; a.conv.bias = conv_bias; a.conv.lengths = lengths;
         a.conv.state = conv_state; a.conv.last = last_conv_state;
