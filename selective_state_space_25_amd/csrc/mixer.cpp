@@ -2,6 +2,7 @@
 // with it in front: argument checks, plans and workspace.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <string>
 
 #include "host.hpp"
@@ -117,10 +118,21 @@ void fill(selscan::M2ConvArgs& a, const selscan_m2_conv_shape_t* s, bool token) 
     selscan::short_conv_plan(a.conv, false);
 }
 
-constexpr int64_t kRecTokens = 16;
+// Short sequences are walked token by token, in a time that goes with their
+// length; in chunks it hardly moves within one.  us, token by token / in
+// chunks, bf16, heads of 64 x 128:
+//              32 heads       256 heads      2048 heads
+//   L =  8    11.4           14.3           51.7
+//   L = 16    16.3 / 31.4    19.4 / 32.3    89.9 / 57.7
+//   L = 32      -  / 31.6      -  / 32.4      -  / 58.1
+// (0.65 us a token until the GPU is full, and with the states from there).
+constexpr int64_t kRecTokens = 32;
 
 // The chunked form's offsets inside 64 tokens and the three before are 32-bit.
-bool chunked(const selscan::M2ConvArgs& a) { return a.L > kRecTokens && a.conv.x_row < ((int64_t)1 << 30) / (4 * 68); }
+bool chunked(const selscan::M2ConvArgs& a) {
+    const int64_t fills = std::max<int64_t>(1, a.batch * a.H * a.P * a.N >> 21);
+    return a.L * fills > kRecTokens && a.conv.x_row < ((int64_t)1 << 30) / (4 * 68);
+}
 
 size_t mixer_bytes(const selscan::M2ConvArgs& a, int in_bf16) {
     return chunked(a) ? selscan::m2_chunk_bytes(a, in_bf16) : selscan::m2_rec_bytes(a);

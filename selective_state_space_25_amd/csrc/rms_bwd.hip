@@ -210,7 +210,7 @@ struct Bwd {
 
 template <typename Tin, typename Tres, typename Tout, bool GATE>
 hipError_t bwd(const RmsArgs& a, hipStream_t stream) {
-    const Layout l(a.width);
+    const Layout l(a.width, false);
     if (l.pieces) return by_layout(l, Bwd<Tin, Tres, Tout, GATE>{a, stream});
     if (a.y || a.res_out || a.dgate) {
         KTime kt("rms_bwd", stream);
@@ -237,7 +237,7 @@ hipError_t by_out(const RmsArgs& a, int out_bf16, hipStream_t st) {
 // Workgroups to a group of columns, each with a partial row of dweight: two a
 // compute unit, and 64 rows each in fp32 at most; no more than have rows.
 int rms_bwd_blocks(int64_t rows, int64_t width) {
-    const Layout l(width);
+    const Layout l(width, false);
     const int64_t once = l.at_once();
     const int64_t n = l.pieces ? std::max((int64_t)kBlocks, std::min((rows + 64 * once - 1) / (64 * once), (int64_t)1 << 23))
                                : std::max((int64_t)64, std::min((rows + 63) / 64, (int64_t)65535));

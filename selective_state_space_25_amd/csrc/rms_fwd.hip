@@ -103,13 +103,13 @@ __global__ __launch_bounds__(kT) void rms_fwd_kernel(RmsArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-        // (past the end zero, unless x silu(gate) of the zeros there is not: it is)
-#pragma unroll
+    #pragma unroll
         for (int i = 0; i < 8; ++i) sq = __builtin_fmaf(s[j][i], s[j][i], sq);
     }
     const float rstd = 1.0f / sqrtf(row_sum<LR>(sq, sm) * a.inv_width + a.eps);
     if (at == 0 && a.rstd) a.rstd[unit] = rstd;
     uint32_t top = 0;
+    const int block = (int)a.block, shift = __builtin_ctz(block | (1 << 30));
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
         const int d = 8 * (at + LR * j);
@@ -125,14 +125,14 @@ __global__ __launch_bounds__(kT) void rms_fwd_kernel(RmsArgs a) {
             uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) m = larger(m, magnitude(s[j][i]));
-            if (a.block) {
+            if (block) {
                 // a block is 4 to 64 lanes of a wave; narrower groups are one block
-                for (int o = (int)min(a.block / 8, (int64_t)LR) / 2; o >= 1; o >>= 1) m = larger(m, (uint32_t)__shfl_xor((int)m, o, 64));
+                for (int o = min(block / 8, LR) / 2; o >= 1; o >>= 1) m = larger(m, (uint32_t)__shfl_xor((int)m, o, 64));
                 const float sc = scale_of(m), inv = 1.0f / sc;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) s[j][i] *= inv;
                 if (d < row.width) {
-                    if (d % a.block == 0) row.scale[d / a.block] = sc;
+                    if ((d & (block - 1)) == 0) row.scale[d >> shift] = sc;
                     stp<false>(row.y + d, row.width - d, s[j]);
                 }
             } else {
@@ -230,7 +230,7 @@ struct Fwd {
 
 template <typename Tin, typename Tres, typename Tout>
 hipError_t fwd(const RmsArgs& a, hipStream_t stream) {
-    const Layout l(a.width);
+    const Layout l(a.width, true);
     if (l.pieces) return by_layout(l, Fwd<Tin, Tres, Tout>{a, stream});
     KTime kt("rms_fwd", stream);
     hipLaunchKernelGGL((rms_fwd_long_kernel<Tin, Tres, Tout>), io::groups(a.rows * a.groups), dim3(kT), 0, stream, a);

@@ -79,9 +79,9 @@ __device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.0f + fast_
 // Lanes a group takes and pieces a lane (0: the group is too long).
 struct Layout {
     int lanes, pieces;
-    explicit Layout(int64_t width) {
+    Layout(int64_t width, bool fwd) {
         const int64_t np = (width + 7) / 8;
-        lanes = np <= 8 ? 8 : np <= 16 ? 16 : np <= 32 ? 32 : np <= 5 * 64 ? 64 : 256;
+        lanes = np <= 8 ? 8 : np <= 16 ? 16 : np <= 32 ? 32 : np <= (fwd ? 128 : 320) ? 64 : 256;
         pieces = width > kLongest ? 0 : (int)((np + lanes - 1) / lanes);
     }
     int at_once() const { return pieces ? kT / lanes : 1; }   // groups a workgroup has at a time
@@ -93,7 +93,7 @@ hipError_t by_layout(const Layout& l, F f) {
     if (l.lanes == 8) return f.template run<8, 1>();
     if (l.lanes == 16) return f.template run<16, 1>();
     if (l.lanes == 32) return f.template run<32, 1>();
-    if (l.lanes == 256) return l.pieces == 2 ? f.template run<256, 2>() : l.pieces == 3 ? f.template run<256, 3>() : f.template run<256, 4>();
+    if (l.lanes == 256) return l.pieces == 1 ? f.template run<256, 1>() : l.pieces == 2 ? f.template run<256, 2>() : l.pieces == 3 ? f.template run<256, 3>() : f.template run<256, 4>();
     switch (l.pieces) {
         case 1: return f.template run<64, 1>();
         case 2: return f.template run<64, 2>();

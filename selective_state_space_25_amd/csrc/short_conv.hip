@@ -24,7 +24,7 @@ namespace selscan {
 namespace {
 
 constexpr int kT = 256;
-constexpr int kU = 4;   // tokens asked for at a time
+constexpr int kFwdU = 4, kBwdU = 4;   // tokens asked for at a time
 
 // A thread's place: V channels from c of batch element b, tokens t0 .. t1 - 1.
 struct Place {
@@ -85,6 +85,7 @@ __device__ __forceinline__ T* part_of(const ShortConvArgs& a, T* p0, T* p1, T* p
 
 template <typename Tin, typename Tout, int K, int V>
 __global__ __launch_bounds__(kT) void conv_fwd_kernel(ShortConvArgs a) {
+    constexpr int kU = kFwdU;
     const Place p(a, V);
     if (!p.live) return;
     const Tin* X = static_cast<const Tin*>(a.x) + p.b * a.x_batch + p.c;
@@ -150,6 +151,7 @@ __global__ __launch_bounds__(kT) void conv_fwd_kernel(ShortConvArgs a) {
 
 template <typename Tin, typename Tout, int K, int V>
 __global__ __launch_bounds__(kT) void conv_bwd_kernel(ShortConvArgs a) {
+    constexpr int kU = kBwdU;
     __shared__ float sums[(K + 1) * V][kT];
     const Place p(a, V);
     float dw[K + 1][V];   // of the taps, then of the bias
@@ -327,7 +329,7 @@ hipError_t launch_v(const ShortConvArgs& a, hipStream_t stream) {
 }
 
 // Channels a thread has at a time: whole pieces of the split only.
-constexpr int kFwdV = 8, kBwdV = 4;
+constexpr int kFwdV = 4, kBwdV = 2;
 
 template <Form F, typename Tin, typename Tout, int K>
 hipError_t by_v(const ShortConvArgs& a, hipStream_t stream) {
@@ -361,7 +363,7 @@ void short_conv_plan(ShortConvArgs& a, bool bwd) {
         if ((n + c - 1) / c * c < (n + a.cols - 1) / a.cols * a.cols) a.cols = c;
     a.col_blocks = (n + a.cols - 1) / a.cols;
     // long runs read fewer tokens twice; shorter ones where the GPU would not fill
-    a.run = bwd ? 64 : 32;
+    a.run = 32;
     while (a.run > 4 && a.batch * ((a.L + a.run - 1) / a.run) * a.col_blocks * a.cols < (int64_t)1 << 18) a.run /= 2;
     const int64_t runs = (a.L + a.run - 1) / a.run;
     a.run_blocks = (runs + kT / a.cols - 1) / (kT / a.cols);
