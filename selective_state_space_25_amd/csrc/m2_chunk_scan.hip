@@ -154,21 +154,19 @@ __device__ __forceinline__ bf16x8 op_at(const unsigned char (*blocks)[kBlock], i
     return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4*>(&blocks[i][lane * 16]));
 }
 
-// Of the instructions before it, G times M matrix products, V vector
-// instructions behind each, whose time the products hide, and R LDS reads that
-// the next M need ahead of them.
-template <int G, int R, int M, int V>
-__device__ __forceinline__ void mix() {
-    __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+// M products over one k-step, in turns: an MFMA that adds to the sum of the one
+// before waits out its latency, and the compiler, which may move anything else
+// between them, is kept from lining such up.
+template <int M, typename FA, typename FB, typename FC>
+__device__ __forceinline__ void in_turns(FA a, FB b, FC c) {
 #pragma unroll
-    for (int g = 0; g < G; ++g) {
-        if (g + 1 < G) __builtin_amdgcn_sched_group_barrier(0x100, R, 0);
+    for (int s = 2; s >= 0; --s)
 #pragma unroll
-        for (int i = 0; i < M; ++i) {
-            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-            __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+        for (int i = 0; i <= s; ++i) {
+#pragma unroll
+            for (int m = 0; m < M; ++m) c(m) = mfma(a(m)[i], b(m)[s - i], c(m));
+            __builtin_amdgcn_sched_barrier(0x496);   // (vector, scalar, memory and LDS instructions may pass)
         }
-    }
 }
 
 // STATE: the first pass, a segment's state from zero and the sum of its log2 decays.
@@ -362,17 +360,17 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     // S += B^T X' over a k-step
     auto write = [&](const unsigned char (*Bs)[kBlock], int ks, const bf16x8 (&xp)[CT][3]) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            bf16x8 bp[3];
+        for (int i = 0; i < NT; i += 2) {
+            bf16x8 bp[2][3];
 #pragma unroll
-            for (int x3 = 0; x3 < 3; ++x3) bp[x3] = op_at(Bs, (i * 2 + ks) * 3 + x3, lane);
-            mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return bp; },
-                              [&](int m) -> const bf16x8(&)[3] { return xp[m]; }, S[i]);
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int x3 = 0; x3 < 3; ++x3) bp[k][x3] = op_at(Bs, ((i + k) * 2 + ks) * 3 + x3, lane);
+            in_turns<2 * CT>([&](int m) -> const bf16x8(&)[3] { return bp[m / CT]; },
+                             [&](int m) -> const bf16x8(&)[3] { return xp[m % CT]; },
+                             [&](int m) -> f32x4& { return S[i + m / CT][m % CT]; });
         }
     };
-    // beside each of its products: a k-step's x and X'
-    constexpr int kV = (100 * CT + 6 * CT * NT - 1) / (6 * CT * NT);
-
     // A chunk's gates and its first raw x stand ready when it begins (the state
     // pass: its first X'), made beside the chunk before's last products.
     bf16x8 x0p[CT][3], x1p[CT][3];
@@ -404,7 +402,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
                 fetch_x(c + 1, 0);
                 scaled(1, x, x1p);
                 write(Bs, 0, x0p);
-                mix<NT, 3, 6 * CT, kV>();
                 if (!narrow) decayed_x(1, x1p);
                 scale_state(mid);
             }
@@ -415,7 +412,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
                 fetch_x(c + 1, 1);
                 scaled(0, x, x0p);
                 write(Bs, 1, x1p);
-                mix<NT, 3, 6 * CT, kV>();
                 scale_state(out);
             }
             dtv = c + 2 < c1 ? fetch_dt(c + 2) : 0.0f;
@@ -446,24 +442,22 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) y[tt][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
             if (live) {
-                bf16x8 sp[2][CT][3];
-                auto split_state = [&](int ks) SELSCAN_INLINE {
-#pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) split8<3>(S[2 * ks][ct], S[2 * ks + 1][ct], sp[ks & 1][ct]);
-                };
-                split_state(0);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    if (ks + 1 < KS) split_state(ks + 1);
+                    bf16x8 sp[CT][3];
 #pragma unroll
-                    for (int tt = 0; tt < 4; ++tt) {
-                        bf16x8 cp[3];
+                    for (int ct = 0; ct < CT; ++ct) split8<3>(S[2 * ks][ct], S[2 * ks + 1][ct], sp[ct]);
 #pragma unroll
-                        for (int x3 = 0; x3 < 3; ++x3) cp[x3] = op_at(sm.C, (ks * 4 + tt) * 3 + x3, lane);
-                        mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return cp; },
-                                          [&](int m) -> const bf16x8(&)[3] { return sp[ks & 1][m]; }, y[tt]);
+                    for (int tt = 0; tt < 4; tt += 2) {
+                        bf16x8 cp[2][3];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int x3 = 0; x3 < 3; ++x3) cp[k][x3] = op_at(sm.C, (ks * 4 + tt + k) * 3 + x3, lane);
+                        in_turns<2 * CT>([&](int m) -> const bf16x8(&)[3] { return cp[m / CT]; },
+                                         [&](int m) -> const bf16x8(&)[3] { return sp[m % CT]; },
+                                         [&](int m) -> f32x4& { return y[tt + m / CT][m % CT]; });
                     }
-                    if (ks + 1 < KS) mix<4, 3, 6 * CT, 2>();
                 }
             }
             all_there();   // B and G; and every wave is done with C
@@ -475,22 +469,32 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
             // G X' of a k-step; with decays past kSpan M X
             auto add_gx = [&](auto fast, int ks, const bf16x8 (&xp)[CT][3]) {
 #pragma unroll
-                for (int tt = 2 * ks; tt < 4; ++tt) {
-                    bf16x8 gp[3];
+                for (int tt = 2 * ks; tt < 4; tt += 2) {
+                    bf16x8 gp[2][3];
+                    f32x4 acc[2][CT];
 #pragma unroll
-                    for (int x3 = 0; x3 < 3; ++x3) gp[x3] = op_at(sm.G, g_tile(tt, ks) * 3 + x3, lane);
-                    if constexpr (!decltype(fast)::value) decayed(ks, gp, gt.f0[16 * tt + li], gt.f1[16 * tt + li], 16 * tt + li);
-                    f32x4 acc[CT];
+                    for (int k = 0; k < 2; ++k) {
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) acc[ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                    mm_turns<3, 3, 3>([&](int) -> const bf16x8(&)[3] { return gp; },
-                                      [&](int i) -> const bf16x8(&)[3] { return xp[i]; }, acc);
-                    f32x4 f = {1.0f, 1.0f, 1.0f, 1.0f};
-                    if constexpr (decltype(fast)::value) f = *reinterpret_cast<const f32x4*>(&(ks ? gt.f1 : gt.f0)[16 * tt + 4 * lg]);
-                    f32x4 e = {1.0f, 1.0f, 1.0f, 1.0f};
-                    if (ks == 0) e = *reinterpret_cast<const f32x4*>(&gt.in[16 * tt + 4 * lg]);
+                        for (int x3 = 0; x3 < 3; ++x3) gp[k][x3] = op_at(sm.G, g_tile(tt + k, ks) * 3 + x3, lane);
+                        const int t = 16 * (tt + k) + li;
+                        if constexpr (!decltype(fast)::value) decayed(ks, gp[k], gt.f0[t], gt.f1[t], t);
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) y[tt][ct] = ks == 0 ? y[tt][ct] * e + acc[ct] * f : y[tt][ct] + acc[ct] * f;
+                        for (int ct = 0; ct < CT; ++ct) acc[k][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                    }
+                    in_turns<2 * CT>([&](int m) -> const bf16x8(&)[3] { return gp[m / CT]; },
+                                     [&](int m) -> const bf16x8(&)[3] { return xp[m % CT]; },
+                                     [&](int m) -> f32x4& { return acc[m / CT][m % CT]; });
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        f32x4 f = {1.0f, 1.0f, 1.0f, 1.0f}, e = f;
+                        if constexpr (decltype(fast)::value) f = *reinterpret_cast<const f32x4*>(&(ks ? gt.f1 : gt.f0)[16 * (tt + k) + 4 * lg]);
+                        if (ks == 0) e = *reinterpret_cast<const f32x4*>(&gt.in[16 * (tt + k) + 4 * lg]);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) {
+                            f32x4& v = y[tt + k][ct];
+                            v = ks == 0 ? v * e + acc[k][ct] * f : v + acc[k][ct] * f;
+                        }
+                    }
                 }
             };
             // the rows of a k-step's tokens
@@ -525,7 +529,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
             fetch_x(c + 1, 0);
             scaled(1, x, x1p);
             write(sm.B, 0, x0p);
-            mix<NT, 3, 6 * CT, kV>();
             turn();
             if (narrow) {
                 add_gx(std::true_type(), 1, x1p);
@@ -538,7 +541,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
             const float out = tail;
             make_gates(c + 1);
             write(sm.B, 1, x1p);
-            mix<NT, 3, 6 * CT, 1>();
             scale_state(out);
             dtv = c + 2 < c1 ? fetch_dt(c + 2) : 0.0f;
         }
