@@ -201,3 +201,79 @@ def test_refusals(gpu):
         ss.mamba2_conv_step(i.h0[:, :, :1], i.cs, i.xbc[:, 0], i.dt[:, 0], i.w, i.b, i.A[:1])
     with pytest.raises(ss.SelscanError, match="alias"):
         i.fwd(last_state=i.h0)
+
+
+@pytest.mark.parametrize("P", [64, 33])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_strong_decays_beside_weak_ones(gpu, P, dtype):
+    """Heads whose decays within 32 tokens span more than fp32's powers of two,
+    heads on the border of it and others, in one workgroup, over segments."""
+    i = Inputs(2, 400, 8, 1, P, 128, 4, dtype)
+    i.A = torch.tensor([-0.01, -1e5, -30.0, -25.0, -20.0, -500.0, -1.0, -60.0], device=DEV)
+    i.dtb = torch.full((8,), -2.0, device=DEV)
+    i.dt = (0.1 * i.dt).to(dtype)
+    (ry, rS, rcs), (my, mS) = i.ref()
+    y, S, cs = i.fwd()
+    torch.cuda.synchronize()
+    close(y, ry, my, 96 + 1600, "y")
+    close(S, rS, mS, 96 + 1600, "state")
+
+
+@pytest.mark.parametrize("L", [60, 300])
+def test_growing_states(gpu, L):
+    """A positive A: the state grows by up to e^0.25 a token."""
+    i = Inputs(1, L, 4, 1, 64, 64, 4, F32)
+    i.A = torch.tensor([0.5, 1.0, 2.0, -1.0], device=DEV)
+    i.dtb = torch.full((4,), -2.0, device=DEV)
+    i.dt = 0.1 * i.dt
+    (ry, rS, _), (my, mS) = i.ref()
+    y, S, _ = i.fwd()
+    torch.cuda.synchronize()
+    close(y, ry, my, 96 + 4 * L, "y")
+    close(S, rS, mS, 96 + 4 * L, "state")
+
+
+def test_many_groups_and_heads(gpu):
+    """A group to each head, more units than a workgroup's waves, and unaligned states."""
+    for shape in [(1, 140, 6, 6, 48, 32, 3), (1, 140, 20, 2, 64, 16, 4), (2, 140, 9, 1, 80, 64, 2)]:
+        i = Inputs(*shape, BF16)
+        room = torch.empty(i.h0.numel() + 1, device=DEV)
+        h0 = room[1:].view(i.h0.shape)          # 4 bytes off a 16-byte boundary
+        h0.copy_(i.h0)
+        i.h0 = h0
+        (ry, rS, rcs), (my, mS) = i.ref()
+        y, S, cs = i.fwd(BF16)
+        torch.cuda.synchronize()
+        close(y, ry, my, 96 + 560, "y")
+        close(S, rS, mS, 96 + 560, "state")
+        assert torch.equal(cs.cpu().double(), rcs)
+
+
+def test_two_streams_at_once(gpu):
+    """Two prompts on two streams, each with workspaces of its own."""
+    a, b = Inputs(1, 500, 4, 1, 64, 128, 4, BF16, seed=1), Inputs(1, 500, 4, 1, 64, 128, 4, BF16, seed=2)
+    want = a.fwd(), b.fwd()
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        with torch.cuda.stream(sa):
+            x = a.fwd()
+        with torch.cuda.stream(sb):
+            y = b.fwd()
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(x, want[0])) and all(torch.equal(p, q) for p, q in zip(y, want[1]))
+
+
+def test_rows_too_far_apart_for_a_chunk(gpu):
+    """Rows of xbc 2^23 elements apart: walked token by token."""
+    i = Inputs(1, 70, 1, 1, 16, 16, 2, BF16)
+    C = i.xbc.shape[2]
+    big = torch.empty(70 << 23, dtype=BF16, device=DEV)
+    far = big.as_strided((1, 70, C), (0, 1 << 23, 1))
+    far.copy_(i.xbc)
+    i.xbc = far
+    (ry, rS, rcs), (my, mS) = i.ref()
+    y, S, cs = i.fwd()
+    torch.cuda.synchronize()
+    close(y, ry, my, 96 + 280, "y")
+    close(S, rS, mS, 96 + 280, "state")
