@@ -41,8 +41,11 @@ __global__ __launch_bounds__(kT) void m2_conv_rec_kernel(M2ConvArgs a, const flo
         float bv[E], cv[E];
 #pragma unroll
         for (int e = 0; e < E; e += 4) {
-            io::ld4(Bp + t * a.G * N + e, bv + e);
-            io::ld4(Cp + t * a.G * N + e, cv + e);
+            io::Piece<float, 4> pb, pc;   // (not on 16 bytes where H P is odd)
+            pb.get(Bp + t * a.G * N + e);
+            pc.get(Cp + t * a.G * N + e);
+            pb.widen(bv + e);
+            pc.widen(cv + e);
         }
         const float x = Xp[t * a.H * a.P];
         const float w = softplus_log2((io::ld(T + t * a.dt_row) + bias) * kLog2e);

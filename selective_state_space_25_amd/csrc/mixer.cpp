@@ -16,6 +16,10 @@ namespace {
 
 constexpr int64_t kMostGroups = (int64_t)1 << 35;   // workgroups of a launch over two grid dimensions
 
+// What the sums of partial rows take in one launch: (width + 1) dim columns at
+// 16 threads each, fewer than 2^32, and 65535 times 1024 rows.
+constexpr int64_t kMostSumCols = (int64_t)1 << 24, kMostSumRows = (int64_t)1 << 25;
+
 bool is_dtype(int32_t d) { return d == SELSCAN_F32 || d == SELSCAN_BF16; }
 
 selscan_status_t check_width(int64_t width) {
@@ -64,6 +68,8 @@ selscan_status_t check_conv(const selscan_short_conv_shape_t* s, Use use) {
         if (blocks < 0 || blocks > kMostGroups ||
             (use == kGrad && mul_checked({a.batch, a.run_blocks, s->width + 1, s->dim, 8}) < 0))
             return set_error(SELSCAN_ERR_UNSUPPORTED, "too many elements for one launch");
+        if (use == kGrad && (s->dim > kMostSumCols || a.batch * a.run_blocks > kMostSumRows))
+            return set_error(SELSCAN_ERR_UNSUPPORTED, "the short convolution's gradients support dim <= 2^24 and up to 2^25 blocks of rows");
     }
     if (s->dim > (int64_t)1 << 32 || s->batch > (int64_t)1 << 31 ||
         mul_checked({s->batch, s->dim}) / 256 > kMostGroups)
@@ -103,6 +109,15 @@ selscan_status_t check_mixer(const selscan_m2_conv_shape_t* s, bool token) {
     if (hp + 2 * gn > (int64_t)1 << 22 || mul_checked({s->batch, s->nheads, (s->headdim + 15) / 16}) > kMostGroups ||
         s->batch > (int64_t)1 << 31)
         return set_error(SELSCAN_ERR_UNSUPPORTED, "the Mamba-2 mixer supports up to 2^22 channels of xbc, and rows of states for one launch");
+    if (!token) {
+        // a record of a chunk's B and C is at most 2^17 bytes, and a GPU's
+        // compute units ask for fewer than 2^12 segments of a sequence
+        const int64_t chunks = (L + 63) / 64;
+        const int64_t recs = mul_checked({s->batch, chunks, s->ngroups, (int64_t)1 << 17});
+        if (recs < 0 || recs >> 17 > kMostGroups || mul_checked({s->batch, hp, s->dstate, 4, 4096}) < 0 ||
+            mul_checked({s->batch, hp, s->dstate}) / 256 > kMostGroups)
+            return set_error(SELSCAN_ERR_UNSUPPORTED, "too many chunks or states for one launch");
+    }
     return SELSCAN_OK;
 }
 

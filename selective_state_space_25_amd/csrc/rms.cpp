@@ -27,8 +27,8 @@ selscan_status_t check(const selscan_rms_shape_t* s, bool grad) {
     if (s->gate_row < 0) return set_error(SELSCAN_ERR_INVALID_ARG, "gate_row must be >= 0");
     if (mul_checked({s->rows, s->dim, 4}) < 0 || mul_checked({s->rows, s->gate_row, 4}) < 0)
         return set_error(SELSCAN_ERR_INVALID_ARG, "tensor sizes overflow 64-bit byte counts");
-    if (s->rows > 0x7fffffff || s->dim > 0xfffffff || s->groups > 65535)
-        return set_error(SELSCAN_ERR_UNSUPPORTED, "the RMS norm supports rows < 2^31, dim < 2^28 and groups < 2^16");
+    if (s->rows > 0x7fffffff || s->dim > 0x7ffffff || s->groups > 65535)
+        return set_error(SELSCAN_ERR_UNSUPPORTED, "the RMS norm supports rows < 2^31, dim < 2^27 and groups < 2^16");
     if (s->rows * s->groups > (int64_t)1 << 35) return set_error(SELSCAN_ERR_UNSUPPORTED, "too many groups for one launch");
     return SELSCAN_OK;
 }

@@ -68,6 +68,16 @@ def test_conv_too_many_elements_for_a_launch():
     assert conv_step(conv(batch=1 << 40, x_batch=0)) in (BAD, NO)
 
 
+def test_conv_gradients_past_the_sums_launch():
+    """(width + 1) dim columns, and partial rows, that one launch adds up."""
+    size = lambda s: ss.lib().selscan_short_conv_bwd_workspace_bytes(ctypes.byref(s))
+    for kw in [dict(dim=(1 << 24) + 4, split=((1 << 24), 2, 2)), dict(batch=1 << 27, x_batch=0, dim=1, split=(1, 0, 0)),
+               dict(seqlen=1 << 40, x_batch=0, x_row=0, dim=1, split=(1, 0, 0))]:
+        s = conv(**kw)
+        assert conv_bwd(s) == NO and size(s) == 0
+    assert size(conv(dim=1 << 24, split=((1 << 24) - 4, 2, 2))) > 0
+
+
 def mixer(**kw):
     base = dict(batch=2, seqlen=8, nheads=4, headdim=8, ngroups=2, dstate=16, width=4, xbc_row=96, xbc_batch=768, dt_row=4,
                 dt_batch=32, in_dtype=ss.BF16, out_dtype=ss.F32)
@@ -105,6 +115,17 @@ def test_mixer_step_bad_shape(field, value, status):
     assert mixer_step(mixer(**{field: value})) == status and ss.last_error()
 
 
+def test_mixer_past_a_launch():
+    """Chunks, segments' states and their bytes that no launch holds."""
+    for kw in [dict(seqlen=1 << 43, xbc_row=0, dt_row=0, xbc_batch=0, dt_batch=0),
+               dict(seqlen=1 << 51, xbc_row=0, dt_row=0, xbc_batch=0, dt_batch=0),
+               dict(batch=1 << 31, seqlen=4096, xbc_batch=0, dt_batch=0, ngroups=4)]:
+        s = mixer(**kw)
+        assert mixer_fwd(s) in (BAD, NO) and ss.lib().selscan_mamba2_conv_workspace_bytes(ctypes.byref(s)) == 0
+    s = mixer(batch=1 << 20, seqlen=4096)
+    assert ss.lib().selscan_mamba2_conv_workspace_bytes(ctypes.byref(s)) > 0
+
+
 def test_mixer_null_alias_and_alignment():
     s = mixer()
     assert mixer_fwd(None) == mixer_step(None) == BAD
@@ -137,7 +158,8 @@ def rms_bwd(s, dy=FAKE, x=FAKE, gate=None, rstd=FAKE, dr=None, dx=FAKE, dres=Non
 @pytest.mark.parametrize("field,value,status", [
     ("rows", 0, BAD), ("dim", 0, BAD), ("groups", 0, BAD), ("groups", 5, BAD), ("gate_row", -1, BAD), ("scale_block", 16, NO),
     ("scale_block", 96, NO), ("scale_block", 1024, NO), ("scale_block", -32, NO), ("in_dtype", 2, NO), ("res_dtype", 2, NO),
-    ("out_dtype", 3, NO), ("eps", -1.0, BAD), ("eps", float("nan"), BAD), ("rows", 1 << 31, NO), ("rows", 1 << 62, BAD)])
+    ("out_dtype", 3, NO), ("eps", -1.0, BAD), ("eps", float("nan"), BAD), ("rows", 1 << 31, NO), ("rows", 1 << 62, BAD),
+    ("dim", 1 << 27, NO)])
 def test_rms_bad_shape(field, value, status):
     s = rms(**{field: value})
     assert rms_fwd(s) == status and ss.last_error()
