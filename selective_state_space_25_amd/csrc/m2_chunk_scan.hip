@@ -250,7 +250,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
         return t < len ? io::ld(T + t * a.dt_row) : 0.0f;
     };
     // The lane's raw x of a k-step: tokens 32 ks + 8 lg - (K - 1) .. + 7 of its
-    // columns.  Past the end, and before the first token, the buffer gives zero.
+    // columns.  Past the end the buffer gives zero.
     using RX = RawX<Tin, CT>;
     RX xr[K - 1 + 8];
     const int xrow = scalar((int)(a.conv.x_row * ES)), xbytes = scalar((int)(a.P * ES));
@@ -261,11 +261,12 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
         const int at = mine ? (p0 + CT * li) * ES + (8 * lg + before - (K - 1)) * xrow : kOut;
 #pragma unroll
         for (int j = 0; j < K - 1 + 8; ++j) xr[j] = buf_x<Tin, CT>(xb, at + (32 * ks + j) * xrow);
-        if (!later && ks == 0 && XS && lg == 0 && mine) {
+        if (!later && ks == 0 && lg == 0) {   // (rows that overlap reach back into the buffer, so not left to it)
 #pragma unroll
             for (int j = 0; j < K - 1; ++j) {
                 io::Piece<Tin, CT> r;
-                r.get(XS + j * C + p0 + CT * li);
+                r.zero();
+                if (XS && mine) r.get(XS + j * C + p0 + CT * li);
                 xr[j] = __builtin_bit_cast(RX, r);
             }
         }

@@ -277,3 +277,21 @@ def test_rows_too_far_apart_for_a_chunk(gpu):
     torch.cuda.synchronize()
     close(y, ry, my, 96 + 280, "y")
     close(S, rS, mS, 96 + 280, "state")
+
+
+@pytest.mark.parametrize("L", [20, 130])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_rows_that_overlap(gpu, L, dtype):
+    """One row for every token (an expanded tensor), and rows one element
+    apart: what lies before the first token is still zero, not the buffer's."""
+    i = Inputs(2, L, 4, 1, 64, 64, 4, dtype)
+    i.cs = None
+    C, room = i.xbc.shape[2], i.xbc.reshape(-1)
+    for xbc in (room[:C].expand(2, L, C), room.as_strided((2, L, C), (7, 1, 1))):
+        i.xbc = xbc
+        (ry, rS, rcs), (my, mS) = i.ref()
+        y, S, cs = i.fwd()
+        torch.cuda.synchronize()
+        close(y, ry, my, 96 + 4 * L, "y")
+        close(S, rS, mS, 96 + 4 * L, "state")
+        assert torch.equal(cs.cpu().double(), rcs)
