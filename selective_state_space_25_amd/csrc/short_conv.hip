@@ -16,6 +16,11 @@
 // does.  The gradients' recompute pre from x.  dw and dbias: fp32 over one
 // run, the workgroup's runs added up through LDS, one partial row a workgroup,
 // and those in fp64 by column_sums.hip in a fixed order.
+//
+// 8 x 4096 x 2304, width 4, split in three, bf16: 66 us for 0.30 GB, 4.6 TB/s;
+// gradients with dout in fp32 140 us for 0.60 GB, 4.3 TB/s (vector ALU 73 %
+// busy: the activation and its slope again, 2 K multiplications an element).
+// One token is a launch: 1.9 us at 1 x 2304, 5.5 at 128 x 2304.
 #include "io.hpp"
 #include "kernels.hpp"
 
@@ -328,7 +333,9 @@ hipError_t launch_v(const ShortConvArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Channels a thread has at a time: whole pieces of the split only.
+// Channels a thread has at a time: whole pieces of the split only.  Twice as
+// many take 73 us at the sizes above (fewer waves to hide loads behind), and
+// 150 for the gradients.
 constexpr int kFwdV = 4, kBwdV = 2;
 
 template <Form F, typename Tin, typename Tout, int K>
@@ -363,6 +370,7 @@ void short_conv_plan(ShortConvArgs& a, bool bwd) {
         if ((n + c - 1) / c * c < (n + a.cols - 1) / a.cols * a.cols) a.cols = c;
     a.col_blocks = (n + a.cols - 1) / a.cols;
     // long runs read fewer tokens twice; shorter ones where the GPU would not fill
+    // (a wave to each SIMD is 2^16 threads; loads need a few waves)
     a.run = 32;
     while (a.run > 4 && a.batch * ((a.L + a.run - 1) / a.run) * a.col_blocks * a.cols < (int64_t)1 << 18) a.run /= 2;
     const int64_t runs = (a.L + a.run - 1) / a.run;
