@@ -310,7 +310,7 @@ size_t m2_rec_bytes(const M2ConvArgs& a);
 hipError_t launch_m2_rec(const M2ConvArgs& a, int in_bf16, int out_bf16, void* ws, hipStream_t stream);
 size_t m2_chunk_bytes(const M2ConvArgs& a, int in_bf16);
 hipError_t launch_m2_chunk(const M2ConvArgs& a, int in_bf16, int out_bf16, void* ws, hipStream_t stream);
-hipError_t launch_m2_prep(const M2ConvArgs& a, int in_bf16, int np, char* recs, int64_t chunks, hipStream_t stream);
+hipError_t launch_m2_prep(const M2ConvArgs& a, int in_bf16, int out_bf16, int np, char* recs, int64_t chunks, hipStream_t stream);
 hipError_t launch_m2_conv_step(const M2ConvArgs& a, int in_bf16, int out_bf16, hipStream_t stream);
 
 // RMS norm of s = x + residual, or s = x silu(gate), over the groups of a row.

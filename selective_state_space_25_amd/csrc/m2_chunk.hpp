@@ -41,11 +41,39 @@ __device__ __forceinline__ int64_t seq_len(const M2ConvArgs& a, int64_t b) {
 
 // How the scan is divided: `units` of 16 ct value columns of a head share a
 // group's records; `waves` of them are a workgroup, `sets` workgroups a group.
-// A sequence's chunks are walked in `segs` segments of `per` chunks at once.
+// A sequence's chunks are walked in segments at once, `all` for all sequences:
+// `segs` of `per` chunks to a sequence, or (segs = 0) about `want` in all, cut
+// from the sequences' lengths on the device.
 struct Plan {
     int64_t chunks;
-    int64_t segs, per;
+    int64_t all, segs, per, want;
     int ct, cols, units, waves, sets, np;
+};
+
+// Where the segments lie.  Cut on the device: a lane has the sequence of its
+// number (a batch of 64 and fewer), at least one segment each, of two chunks
+// and more: T chunks in E sequences make T / per + E / 2 segments on average,
+// and T / per + batch at most.
+struct Cut {
+    int per, first, n;   // the lane's sequence: its first segment, its segments
+    __device__ __forceinline__ Cut(const M2ConvArgs& a, const Plan& pl) {
+        const int lane = threadIdx.x & 63;
+        const bool live = lane < a.batch;
+        const int chunks = live ? (int)((min((int64_t)max(a.conv.lengths[live ? lane : 0], 0), a.L) + kC - 1) / kC) : 0;
+        int all = chunks;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) all += __shfl_xor(all, o, 64);
+        const int want = (int)pl.want, fit = max(want - __popcll(__ballot(chunks > 0)) / 2, want / 2);
+        per = max(2, (all + fit - 1) / fit);
+        n = live ? max(1, (chunks + per - 1) / per) : 0;
+        int upto = n;
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) {
+            const int v = __shfl_up(upto, o, 64);
+            if (lane >= o) upto += v;
+        }
+        first = upto - n;
+    }
 };
 
 }  // namespace m2chunk

@@ -198,11 +198,24 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     const int64_t id = io::group_id(), oct = id / (8 * pl.sets), in8 = id - oct * 8 * pl.sets;
     const int64_t seg_id = oct * 8 + in8 % 8;
     const int set = (int)(in8 / 8);
-    const int64_t bs = seg_id / a.G, grp = seg_id - bs * a.G, b = bs / pl.segs, seg = bs - b * pl.segs;
-    if (b >= a.batch) return;
+    const int64_t bs = seg_id / a.G, grp = seg_id - bs * a.G;
+    if (bs >= pl.all) return;
+    int64_t b, seg, per;
+    if (pl.segs) {
+        b = bs / pl.segs;
+        seg = bs - b * pl.segs;
+        per = pl.per;
+    } else {
+        const Cut cut(a, pl);
+        const int of = __popcll(__ballot(cut.n > 0 && cut.first <= bs)) - 1;
+        b = of;
+        seg = bs - __builtin_amdgcn_readlane(cut.first, of);
+        per = scalar(cut.per);
+        if (seg >= __builtin_amdgcn_readlane(cut.n, of)) return;
+    }
     const int64_t len = seq_len(a, b);
     const int64_t nch = (len + kC - 1) / kC;
-    const int64_t c0 = seg * pl.per, c1 = min(c0 + pl.per, nch);
+    const int64_t c0 = seg * per, c1 = min(c0 + per, nch);
     if (STATE && c1 >= nch) return;   // nothing follows this segment
     const int unit = set * pl.waves + wave;
     const bool live = unit < pl.units;
@@ -211,12 +224,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     const bool mine = live && p0 + CT * li < a.P;           // (CT = 2: P is even)
     Tout* Y = static_cast<Tout*>(a.y) + (b * a.L * a.H + h) * a.P;
     const int64_t yrow = a.H * a.P;
-    if (!STATE && c0 >= nch && seg > 0) {   // past the end
-        for (int64_t t = c0 * kC + lg; t < min(a.L, (c0 + pl.per) * kC); t += 4)
-            if (mine)
-                for (int i = 0; i < CT; ++i) io::st(Y + t * yrow + p0 + CT * li + i, 0.0f);
-        return;
-    }
+    if (c0 >= nch && c0 > 0) return;   // past the end
     Gates& gt = sm.gates[wave];
     const Tin* T = static_cast<const Tin*>(a.dt) + b * a.dt_batch + h;
     const float A = a.A[h], dt_bias = a.dt_bias ? a.dt_bias[h] : 0.0f, skip = a.D ? a.D[h] : 0.0f;
@@ -234,7 +242,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
     f32x4 S[NT][CT];
     const int64_t srow = (b * a.H + h) * a.P + p0 + CT * li;
     const float* S0 = STATE ? nullptr
-                      : seg > 0 ? seg_state + (((seg_id / a.G) * a.H + h) * a.P + p0 + CT * li) * a.N
+                      : c0 > 0  ? seg_state + (((seg_id / a.G) * a.H + h) * a.P + p0 + CT * li) * a.N
                       : a.h0    ? a.h0 + srow * a.N
                                 : nullptr;
 #pragma unroll
@@ -552,10 +560,6 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
             scale_state(out);
             dtv = c + 2 < c1 ? fetch_dt(c + 2) : 0.0f;
         }
-        // the rest of the segment's tokens, past the end
-        for (int64_t t = c1 * kC + lg; t < min(a.L, (c0 + pl.per) * kC); t += 4)
-            if (mine)
-                for (int i = 0; i < CT; ++i) io::st(Y + t * yrow + p0 + CT * li + i, 0.0f);
         if (c1 < nch || !a.last) return;
     }
     float* S1 = STATE ? seg_state + (((seg_id / a.G + 1) * a.H + h) * a.P + p0 + CT * li) * a.N : a.last + srow * a.N;
@@ -573,27 +577,39 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
 }
 
 // The states that enter segments 1, 2, ..: slot s of seg_state holds what
-// segment s - 1 made from zero, and takes the state entering segment s.
+// segment s - 1 made from zero, and takes the state entering segment s.  Four
+// elements a thread.
 __global__ __launch_bounds__(256) void m2_carry_kernel(M2ConvArgs a, Plan pl, float* seg_state, const float* seg_log) {
-    const int64_t head = a.P * a.N, i = io::group_id() * 256 + threadIdx.x;
+    const int64_t head = a.P * a.N, i = (io::group_id() * 256 + threadIdx.x) * 4;
     const int64_t bh = i / head, e = i - bh * head, b = bh / a.H, h = bh - b * a.H;
+    int cut_n = 0, cut_first = 0;
+    if (!pl.segs) {   // (all lanes)
+        const Cut cut(a, pl);
+        cut_n = __shfl(cut.n, (int)b & 63, 64);
+        cut_first = __shfl(cut.first, (int)b & 63, 64);
+    }
     if (b >= a.batch) return;
     const int64_t len = a.conv.lengths ? min((int64_t)max(a.conv.lengths[b], 0), a.L) : a.L;
-    const int64_t n = ((len + kC - 1) / kC + pl.per - 1) / pl.per;   // the sequence's segments
-    float s = a.h0 ? a.h0[i] : 0.0f;
+    const int64_t n = pl.segs ? ((len + kC - 1) / kC + pl.per - 1) / pl.per : cut_n;   // the sequence's segments
+    const int64_t s0 = pl.segs ? b * pl.segs : cut_first;
+    io::Piece<float, 4> first;
+    first.zero();
+    if (a.h0) first.get(a.h0 + i);
+    f32x4 s = first.v;
     constexpr int kAhead = 8;   // loads in flight
     for (int64_t g = 0; g + 1 < n; g += kAhead) {
-        float u[kAhead], d[kAhead];
-        float* to = seg_state + ((b * pl.segs + g + 1) * a.H + h) * head + e;
+        f32x4 u[kAhead];
+        float d[kAhead];
+        float* to = seg_state + ((s0 + g + 1) * a.H + h) * head + e;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (g + k + 1 < n) {
-                u[k] = to[k * a.H * head];
-                d[k] = fast_exp2(seg_log[(b * pl.segs + g + k) * a.H + h]);
+                u[k] = *reinterpret_cast<const f32x4*>(to + k * a.H * head);
+                d[k] = fast_exp2(seg_log[(s0 + g + k) * a.H + h]);
             }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
-            if (g + k + 1 < n) to[k * a.H * head] = s = __builtin_fmaf(d[k], s, u[k]);
+            if (g + k + 1 < n) *reinterpret_cast<f32x4*>(to + k * a.H * head) = s = s * d[k] + u[k];
     }
 }
 
@@ -612,21 +628,31 @@ Plan plan_of(const M2ConvArgs& a, int in_bf16, bool ragged) {
     p.sets = (p.units + kWaves - 1) / kWaves;
     p.waves = (p.units + p.sets - 1) / p.sets;
     // Segments of two chunks and more: a workgroup for each compute unit, which
-    // holds one; four where sequences may end early and leave units without
-    // (batch 1, L 16384, 32 heads of 64 x 128: 241 us, with two workgroups a
-    // unit 269; lengths spread over 0 .. 4096, batch 8: 418 us with two, 365
-    // with four).
-    const int64_t groups = a.batch * a.G * p.sets, want = (int64_t)host::device_cus() * (ragged ? 4 : 1);
-    p.segs = std::max<int64_t>(1, std::min((want + groups - 1) / groups, p.chunks / 2));
+    // holds one (batch 1, L 16384, 32 heads of 64 x 128: 241 us, with two
+    // workgroups a unit 269).  Where sequences may end early the device cuts as
+    // many from the tokens that are there, and four a sequence where that is
+    // more, in whole rounds of workgroups (RAGGEDFIG); past 64 sequences, which
+    // one lane each could not cut, segments are of one length, four workgroups
+    // a unit.
+    const int64_t cus = host::device_cus(), groups = a.batch * a.G * p.sets;
+    p.want = std::max<int64_t>(1, cus / (a.G * p.sets));
+    p.want *= std::max<int64_t>(1, (4 * a.batch + p.want - 1) / p.want);
+    if (ragged && a.batch <= 64 && a.batch * p.chunks < (int64_t)1 << 30) {
+        p.segs = p.per = 0;
+        p.all = std::min(p.want + a.batch, a.batch * ((p.chunks + 1) / 2));
+        return p;
+    }
+    p.segs = std::max<int64_t>(1, std::min((cus * (ragged ? 4 : 1) + groups - 1) / groups, p.chunks / 2));
     p.per = (p.chunks + p.segs - 1) / p.segs;
     p.segs = (p.chunks + p.per - 1) / p.per;
+    p.all = a.batch * p.segs;
     return p;
 }
 
 size_t rec_bytes(const Plan& p) { return p.np == 32 ? Rec<32>::bytes : p.np == 64 ? Rec<64>::bytes : Rec<128>::bytes; }
 size_t all_rec_bytes(const M2ConvArgs& a, const Plan& p) { return host::align256((size_t)(a.batch * p.chunks * a.G) * rec_bytes(p)); }
 size_t seg_bytes(const M2ConvArgs& a, const Plan& p) {
-    return p.segs == 1 ? 0 : host::align256((size_t)(a.batch * p.segs * a.H) * (size_t)(a.P * a.N) * 4);
+    return p.all == a.batch ? 0 : host::align256((size_t)(p.all * a.H) * (size_t)(a.P * a.N) * 4);
 }
 
 struct Run {
@@ -643,18 +669,18 @@ struct Run {
         const auto kern = &m2_chunk_kernel<Tin, Tout, K, NP, CT, STATE>;
         const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
         if (e != hipSuccess) return e;
-        const int64_t segs = (a.batch * pl.segs * a.G + 7) / 8 * 8;
+        const int64_t segs = (pl.all * a.G + 7) / 8 * 8;
         KTime kt(STATE ? "m2_chunk_state" : "m2_chunk_scan", stream);
         hipLaunchKernelGGL(kern, io::groups(segs * pl.sets), dim3(64 * pl.waves), bytes, stream, a, pl, recs, seg_state, seg_log);
         return hipGetLastError();
     }
     template <typename Tin, typename Tout, int K, int NP, int CT>
     hipError_t run() const {
-        if (pl.segs > 1) {
+        if (pl.all > a.batch) {
             hipError_t e = pass<Tin, float, K, NP, CT, true>();
             if (e != hipSuccess) return e;
             KTime kt("m2_carry", stream);
-            hipLaunchKernelGGL(m2_carry_kernel, io::groups((a.batch * a.H * a.P * a.N + 255) / 256), dim3(256), 0, stream, a, pl,
+            hipLaunchKernelGGL(m2_carry_kernel, io::groups((a.batch * a.H * a.P * a.N / 4 + 255) / 256), dim3(256), 0, stream, a, pl,
                                seg_state, seg_log);
         }
         return pass<Tin, Tout, K, NP, CT, false>();
@@ -679,8 +705,9 @@ struct Run {
 }  // namespace
 
 size_t m2_chunk_bytes(const M2ConvArgs& a, int in_bf16) {
-    const Plan p = plan_of(a, in_bf16, true);   // (as many segments at least as without lengths)
-    return all_rec_bytes(a, p) + seg_bytes(a, p) + (p.segs == 1 ? 0 : host::align256((size_t)(a.batch * p.segs * a.H) * 4));
+    Plan p = plan_of(a, in_bf16, true);
+    p.all = std::max(p.all, plan_of(a, in_bf16, false).all);   // (with lengths and without)
+    return all_rec_bytes(a, p) + seg_bytes(a, p) + (p.all == a.batch ? 0 : host::align256((size_t)(p.all * a.H) * 4));
 }
 
 hipError_t launch_m2_chunk(const M2ConvArgs& a, int in_bf16, int out_bf16, void* ws, hipStream_t stream) {
@@ -688,7 +715,7 @@ hipError_t launch_m2_chunk(const M2ConvArgs& a, int in_bf16, int out_bf16, void*
     char* recs = static_cast<char*>(ws);
     char* states = recs + all_rec_bytes(a, p);
     const Run r{a, p, recs, reinterpret_cast<float*>(states), reinterpret_cast<float*>(states + seg_bytes(a, p)), stream};
-    const hipError_t e = launch_m2_prep(a, in_bf16, p.np, recs, p.chunks, stream);
+    const hipError_t e = launch_m2_prep(a, in_bf16, out_bf16, p.np, recs, p.chunks, stream);
     if (e != hipSuccess) return e;
     if (in_bf16) return out_bf16 ? r.by_k<uint16_t, uint16_t>() : r.by_k<uint16_t, float>();
     return out_bf16 ? r.by_k<float, uint16_t>() : r.by_k<float, float>();

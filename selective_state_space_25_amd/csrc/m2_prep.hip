@@ -33,7 +33,7 @@ struct Smem {
 __device__ __forceinline__ int place(int n) { return (n & ~31) + 8 * ((n & 15) >> 2) + 4 * ((n & 31) >> 4) + (n & 3); }
 
 template <typename Tin, int K, int NP>
-__global__ __launch_bounds__(kT) void m2_prep_kernel(M2ConvArgs a, char* recs, int64_t chunks) {
+__global__ __launch_bounds__(kT) void m2_prep_kernel(M2ConvArgs a, int y_bytes, char* recs, int64_t chunks) {
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
     auto& sm = *reinterpret_cast<Smem<NP>*>(smem_raw);
     constexpr int kSlices = NP == 32 ? 8 : kT / NP, kTokens = kC / kSlices;   // of a thread's two channels
@@ -55,7 +55,21 @@ __global__ __launch_bounds__(kT) void m2_prep_kernel(M2ConvArgs a, char* recs, i
             static_cast<Tin*>(a.conv.last)[b * (K - 1) * C + e] = v;
         }
     }
-    if (t0 >= len) return;
+    if (t0 >= len) {
+        // past the end: the group's y are zero
+        const int64_t n = a.H / a.G * a.P * y_bytes / 2, pieces = (n + 7) / 8, rows = min((int64_t)kC, a.L - t0);
+        uint16_t* Y = static_cast<uint16_t*>(a.y) + ((b * a.L + t0) * a.G + g) * n;
+        io::Piece<uint16_t, 8> none;
+        none.zero();
+        for (int64_t e = tid; e < rows * pieces; e += kT) {
+            const int64_t t = e / pieces, d = 8 * (e - t * pieces);
+            uint16_t* to = Y + t * a.G * n + d;
+            if (d + 8 <= n) none.put(to);
+            else
+                for (int i = 0; i < n - d; ++i) to[i] = 0;
+        }
+        return;
+    }
     char* rec = recs + id * Rec<NP>::bytes;
     {
         const int ch = 2 * (tid % NP), isC = ch >= NP, n = ch % NP, first = tid / NP * kTokens;
@@ -161,32 +175,33 @@ __global__ __launch_bounds__(kT) void m2_prep_kernel(M2ConvArgs a, char* recs, i
 }
 
 template <typename Tin, int K, int NP>
-hipError_t launch(const M2ConvArgs& a, char* recs, int64_t chunks, hipStream_t stream) {
+hipError_t launch(const M2ConvArgs& a, int y_bytes, char* recs, int64_t chunks, hipStream_t stream) {
     constexpr int bytes = (int)sizeof(Smem<NP>);
     const auto kern = &m2_prep_kernel<Tin, K, NP>;
     const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != hipSuccess) return e;
     KTime kt("m2_prep", stream);
-    hipLaunchKernelGGL(kern, io::groups(a.batch * chunks * a.G), dim3(kT), bytes, stream, a, recs, chunks);
+    hipLaunchKernelGGL(kern, io::groups(a.batch * chunks * a.G), dim3(kT), bytes, stream, a, y_bytes, recs, chunks);
     return hipGetLastError();
 }
 
 template <typename Tin, int K>
-hipError_t by_np(const M2ConvArgs& a, int np, char* recs, int64_t chunks, hipStream_t st) {
-    return np == 32 ? launch<Tin, K, 32>(a, recs, chunks, st) : np == 64 ? launch<Tin, K, 64>(a, recs, chunks, st)
-                                                                        : launch<Tin, K, 128>(a, recs, chunks, st);
+hipError_t by_np(const M2ConvArgs& a, int y_bytes, int np, char* recs, int64_t chunks, hipStream_t st) {
+    return np == 32 ? launch<Tin, K, 32>(a, y_bytes, recs, chunks, st) : np == 64 ? launch<Tin, K, 64>(a, y_bytes, recs, chunks, st)
+                                                                        : launch<Tin, K, 128>(a, y_bytes, recs, chunks, st);
 }
 
 template <typename Tin>
-hipError_t by_k(const M2ConvArgs& a, int np, char* recs, int64_t chunks, hipStream_t st) {
-    return a.conv.K == 2 ? by_np<Tin, 2>(a, np, recs, chunks, st) : a.conv.K == 3 ? by_np<Tin, 3>(a, np, recs, chunks, st)
-                                                                                 : by_np<Tin, 4>(a, np, recs, chunks, st);
+hipError_t by_k(const M2ConvArgs& a, int y_bytes, int np, char* recs, int64_t chunks, hipStream_t st) {
+    return a.conv.K == 2 ? by_np<Tin, 2>(a, y_bytes, np, recs, chunks, st) : a.conv.K == 3 ? by_np<Tin, 3>(a, y_bytes, np, recs, chunks, st)
+                                                                                 : by_np<Tin, 4>(a, y_bytes, np, recs, chunks, st);
 }
 
 }  // namespace
 
-hipError_t launch_m2_prep(const M2ConvArgs& a, int in_bf16, int np, char* recs, int64_t chunks, hipStream_t stream) {
-    return in_bf16 ? by_k<uint16_t>(a, np, recs, chunks, stream) : by_k<float>(a, np, recs, chunks, stream);
+hipError_t launch_m2_prep(const M2ConvArgs& a, int in_bf16, int out_bf16, int np, char* recs, int64_t chunks, hipStream_t stream) {
+    const int y_bytes = out_bf16 ? 2 : 4;
+    return in_bf16 ? by_k<uint16_t>(a, y_bytes, np, recs, chunks, stream) : by_k<float>(a, y_bytes, np, recs, chunks, stream);
 }
 
 }  // namespace selscan

@@ -37,10 +37,10 @@ class Inputs:
         self.h0 = rnd(gen, B, H, P, N, scale=0.3) if states else None
         self.cs = rnd(gen, B, K - 1, C, dtype=dtype) if states else None
 
-    def fwd(self, out=F32, lengths=None, **kw):
+    def fwd(self, out=F32, lengths=None, into=None, **kw):
         return ss.mamba2_conv_fwd(self.xbc, self.dt, self.w, self.b, self.A, self.D, self.dtb, ngroups=self.G, dstate=self.N,
                                   lengths=None if lengths is None else torch.tensor(lengths, dtype=torch.int32, device=DEV),
-                                  h0=self.h0, conv_state=self.cs, out_dtype=out, **kw)
+                                  h0=self.h0, conv_state=self.cs, out=into, out_dtype=out, **kw)
 
     def ref(self, lengths=None):
         return ops.mixer(self.xbc, self.dt, self.w, self.b, self.A, self.D, self.dtb, self.G, self.N, lengths, self.h0, self.cs)
@@ -295,3 +295,33 @@ def test_rows_that_overlap(gpu, L, dtype):
         close(y, ry, my, 96 + 4 * L, "y")
         close(S, rS, mS, 96 + 4 * L, "state")
         assert torch.equal(cs.cpu().double(), rcs)
+
+
+@pytest.mark.parametrize("lengths", [[0, 700, 1, 130, 64, 699, 65, 0, 128], [700] * 9, [0] * 9, [1, 0, 0, 0, 0, 0, 0, 0, 700]])
+@pytest.mark.parametrize("dtype,out", [(BF16, BF16), (F32, F32)])
+def test_segments_of_ragged_prompts(gpu, lengths, dtype, out):
+    """Sequences cut into segments by their lengths, empty ones between."""
+    i = Inputs(9, 700, 4, 2, 24, 32, 4, dtype)
+    (ry, rS, rcs), (my, mS) = i.ref(lengths)
+    room = torch.full((9, 700, 4, 24), float("nan"), dtype=out, device=DEV)
+    y, S, cs = i.fwd(out, lengths, room)
+    torch.cuda.synchronize()
+    close(y, ry, my, 96 + 2800, "y")
+    close(S, rS, mS, 96 + 2800, "state")
+    assert torch.equal(cs.cpu().double(), rcs)
+    for b, n in enumerate(lengths):
+        assert not y[b, n:].any()
+
+
+@pytest.mark.parametrize("batch", [64, 65, 70])
+@pytest.mark.parametrize("odd", [False, True])
+def test_many_ragged_prompts(gpu, batch, odd):
+    """As many sequences as lanes, and more; y's rows off 16 bytes."""
+    i = Inputs(batch, 200, 2, 1, 15 if odd else 16, 16, 3, BF16)
+    lengths = [(37 * b) % 203 for b in range(batch)]
+    (ry, rS, rcs), (my, mS) = i.ref(lengths)
+    y, S, cs = i.fwd(BF16, lengths, torch.full((batch, 200, 2, 15 if odd else 16), float("nan"), dtype=BF16, device=DEV))
+    torch.cuda.synchronize()
+    close(y, ry, my, 96 + 800, "y")
+    close(S, rS, mS, 96 + 800, "state")
+    assert torch.equal(cs.cpu().double(), rcs)
