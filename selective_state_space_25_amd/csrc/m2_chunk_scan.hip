@@ -28,7 +28,9 @@
 // A chunk's work does not depend on how many others are walked, so a sequence
 // is cut into segments: a first pass makes each segment's state from zero
 // (the B^T X' product alone), m2_carry_kernel joins them, and the second pass
-// runs all segments at once from the states that enter them.
+// runs all segments at once from the states that enter them.  In a padded batch
+// the device cuts the segments (m2_chunk.hpp), since the host does not know the
+// lengths.
 //
 // 1 x 16384, 32 heads of 64 x 128 in one group, bf16: 128 us, and 71 for the
 // state pass and 17 for the carry between them.  Six MFMAs a product make this
@@ -629,15 +631,17 @@ Plan plan_of(const M2ConvArgs& a, int in_bf16, bool ragged) {
     p.waves = (p.units + p.sets - 1) / p.sets;
     // Segments of two chunks and more: a workgroup for each compute unit, which
     // holds one (batch 1, L 16384, 32 heads of 64 x 128: 241 us, with two
-    // workgroups a unit 269).  Where sequences may end early the device cuts as
-    // many from the tokens that are there, and four a sequence where that is
-    // more, in whole rounds of workgroups (RAGGEDFIG); past 64 sequences, which
-    // one lane each could not cut, segments are of one length, four workgroups
-    // a unit.
+    // workgroups a unit 269).  Where sequences may end early and the shortest
+    // segments would be more than that, the device cuts them from the tokens
+    // that are there, four a sequence at least, in whole rounds of workgroups
+    // (batch 8, lengths spread over 0 .. 4096: 275 us; segments of one length,
+    // four workgroups a unit, 349).  Its cut costs 0.5 us a launch (batch 3 of
+    // up to 333 tokens: 38 us, without 35), and a lane a sequence does no more
+    // than 64: those have one length, and four workgroups a unit.
     const int64_t cus = host::device_cus(), groups = a.batch * a.G * p.sets;
     p.want = std::max<int64_t>(1, cus / (a.G * p.sets));
     p.want *= std::max<int64_t>(1, (4 * a.batch + p.want - 1) / p.want);
-    if (ragged && a.batch <= 64 && a.batch * p.chunks < (int64_t)1 << 30) {
+    if (ragged && a.batch <= 64 && groups * ((p.chunks + 1) / 2) > cus && a.batch * p.chunks < (int64_t)1 << 30) {
         p.segs = p.per = 0;
         p.all = std::min(p.want + a.batch, a.batch * ((p.chunks + 1) / 2));
         return p;

@@ -301,9 +301,9 @@ def test_rows_that_overlap(gpu, L, dtype):
 @pytest.mark.parametrize("dtype,out", [(BF16, BF16), (F32, F32)])
 def test_segments_of_ragged_prompts(gpu, lengths, dtype, out):
     """Sequences cut into segments by their lengths, empty ones between."""
-    i = Inputs(9, 700, 4, 2, 24, 32, 4, dtype)
+    i = Inputs(9, 700, 12, 6, 24, 32, 4, dtype)
     (ry, rS, rcs), (my, mS) = i.ref(lengths)
-    room = torch.full((9, 700, 4, 24), float("nan"), dtype=out, device=DEV)
+    room = torch.full((9, 700, 12, 24), float("nan"), dtype=out, device=DEV)
     y, S, cs = i.fwd(out, lengths, room)
     torch.cuda.synchronize()
     close(y, ry, my, 96 + 2800, "y")
@@ -317,10 +317,10 @@ def test_segments_of_ragged_prompts(gpu, lengths, dtype, out):
 @pytest.mark.parametrize("odd", [False, True])
 def test_many_ragged_prompts(gpu, batch, odd):
     """As many sequences as lanes, and more; y's rows off 16 bytes."""
-    i = Inputs(batch, 200, 2, 1, 15 if odd else 16, 16, 3, BF16)
+    i = Inputs(batch, 200, 4, 4, 15 if odd else 16, 16, 3, BF16)
     lengths = [(37 * b) % 203 for b in range(batch)]
     (ry, rS, rcs), (my, mS) = i.ref(lengths)
-    y, S, cs = i.fwd(BF16, lengths, torch.full((batch, 200, 2, 15 if odd else 16), float("nan"), dtype=BF16, device=DEV))
+    y, S, cs = i.fwd(BF16, lengths, torch.full((batch, 200, 4, 15 if odd else 16), float("nan"), dtype=BF16, device=DEV))
     torch.cuda.synchronize()
     close(y, ry, my, 96 + 800, "y")
     close(S, rS, mS, 96 + 800, "state")
