@@ -544,8 +544,8 @@ selscan_status_t selscan_layer_norm_bwd(const selscan_norm_shape_t* shape, const
  *   last_state [B, K-1, D]   in_dtype   the last K - 1 tokens inside the
  *                                       sequence, of `state` and x (written;
  *                                       NULL = skip); may not alias state
- * Sums and the activation are fp32.  No workspace (the field is the
- * gradients').
+ * Sums and the activation are fp32.  Outputs must not overlap inputs or each
+ * other.  No workspace (the field is the gradients').
  */
 typedef struct {
     int64_t batch, seqlen, dim, width;
@@ -620,6 +620,7 @@ selscan_status_t selscan_short_conv_step(const selscan_short_conv_shape_t* shape
  *   last_conv_state                  in_dtype   as conv_state (written; NULL =
  *                                               skip); may not alias it
  *
+ * Outputs must not overlap inputs or each other.
  * N in {16, 32, 64, 128}.  State, decays and sums are fp32, and so are products
  * in effect.  The sequence is worked on in chunks of 64 tokens (up to 32 tokens
  * one by one, where the heads do not fill the GPU): a NaN or infinity in a token

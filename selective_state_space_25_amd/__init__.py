@@ -1050,6 +1050,8 @@ def mamba2_conv_fwd(xbc, dt, conv_weight, conv_bias, A, D=None, dt_bias=None, *,
 def _mamba2_conv_step_args(state, conv_state, xbc, dt, conv_weight, conv_bias, A, D, dt_bias, out, out_dtype, what):
     torch = _torch()
     f32 = torch.float32
+    if not isinstance(state, torch.Tensor):
+        raise TypeError("state must be a torch.Tensor")
     dev, dtp = xbc.device, xbc.dtype
     _current(dev, what)
     batch, C = xbc.shape

@@ -167,6 +167,7 @@ selscan_status_t selscan_short_conv_fwd(const selscan_short_conv_shape_t* s, con
             return set_error(SELSCAN_ERR_INVALID_ARG, "x, weight and the outputs of split must be non-NULL");
         if (silu != 0 && silu != 1) return set_error(SELSCAN_ERR_INVALID_ARG, "silu must be 0 or 1");
         if (state && state == last_state) return set_error(SELSCAN_ERR_INVALID_ARG, "state and last_state must not alias");
+        if (x == y0 || x == y1 || x == y2) return set_error(SELSCAN_ERR_INVALID_ARG, "the outputs must not alias x");
         st = device_check();
         if (st != SELSCAN_OK) return st;
         selscan::ShortConvArgs a{};
@@ -196,6 +197,8 @@ selscan_status_t selscan_short_conv_bwd(const selscan_short_conv_shape_t* s, con
         if (st != SELSCAN_OK) return st;
         if (!x || !weight || !dx || !dout0 || (s->split[1] && !dout1) || (s->split[2] && !dout2))
             return set_error(SELSCAN_ERR_INVALID_ARG, "x, weight, dx and the gradients of split must be non-NULL");
+        if (dx == x || dx == dout0 || dx == dout1 || dx == dout2)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "dx must not alias x or the gradients of split");
         if (silu != 0 && silu != 1) return set_error(SELSCAN_ERR_INVALID_ARG, "silu must be 0 or 1");
         st = device_check();
         if (st != SELSCAN_OK) return st;
@@ -257,6 +260,7 @@ selscan_status_t selscan_mamba2_conv_fwd(const selscan_m2_conv_shape_t* s, const
         if (h0 && h0 == last_state) return set_error(SELSCAN_ERR_INVALID_ARG, "h0 and last_state must not alias");
         if (conv_state && conv_state == last_conv_state)
             return set_error(SELSCAN_ERR_INVALID_ARG, "conv_state and last_conv_state must not alias");
+        if (y == xbc || y == dt) return set_error(SELSCAN_ERR_INVALID_ARG, "y must not alias xbc or dt");
         st = device_check();
         if (st != SELSCAN_OK) return st;
         hipStream_t hs = reinterpret_cast<hipStream_t>(stream);

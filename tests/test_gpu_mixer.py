@@ -325,3 +325,23 @@ def test_many_ragged_prompts(gpu, batch, odd):
     close(y, ry, my, 96 + 800, "y")
     close(S, rS, mS, 96 + 800, "state")
     assert torch.equal(cs.cpu().double(), rcs)
+
+
+def test_graph_of_changing_lengths(gpu):
+    """A captured padded batch follows the lengths that stand on the device at
+    each replay; eager calls between the replays share no workspace with it."""
+    i = Inputs(9, 700, 12, 6, 24, 32, 4, BF16)
+    lengths = torch.tensor([700] * 9, dtype=torch.int32, device=DEV)
+    call = lambda n: ss.mamba2_conv_fwd(i.xbc, i.dt, i.w, i.b, i.A, i.D, i.dtb, ngroups=6, dstate=32, lengths=n, h0=i.h0,
+                                        conv_state=i.cs)
+    call(lengths)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = call(lengths)
+    for new in ([0] * 9, [700, 3, 0, 64, 65, 128, 699, 1, 400], [700] * 9, [5] * 9):
+        lengths.copy_(torch.tensor(new, dtype=torch.int32))
+        graph.replay()
+        want = call(torch.tensor(new, dtype=torch.int32, device=DEV))
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(held, want)), new

@@ -196,3 +196,16 @@ def test_rms_workspace_holds_a_row_for_each_workgroup(rows, dim, groups):
     """At least one partial row and no more than one for each row, with the room for their sums."""
     n = ss.lib().selscan_rms_norm_bwd_workspace_bytes(ctypes.byref(rms(rows=rows, dim=dim, groups=groups)))
     assert 4 * dim <= n <= 4 * dim * (rows + rows // 512 + 2) + 256
+
+
+def test_outputs_over_inputs():
+    """The convolution reads tokens that other threads' outputs would be written over."""
+    s = conv()
+    for i in range(3):
+        y = tuple(FAKE if j == i else 2 * FAKE for j in range(3))
+        assert conv_fwd(s, y=y) == BAD and "alias" in ss.last_error()
+        assert conv_bwd(s, dy=y, x=3 * FAKE) == BAD and "alias" in ss.last_error()
+    assert conv_bwd(s, dy=(2 * FAKE,) * 3) == BAD and "alias" in ss.last_error()
+    m = mixer()
+    assert mixer_fwd(m, (FAKE, 2 * FAKE, FAKE, FAKE, FAKE)) == BAD and "alias" in ss.last_error()
+    assert mixer_fwd(m, (2 * FAKE, FAKE, FAKE, FAKE, FAKE)) == BAD and "alias" in ss.last_error()
