@@ -4,7 +4,9 @@ oracle.
 Bound, in roundings (2^-24) of the oracle's magnitudes (products of the
 convolution's terms' absolute values, decayed): 16 for each of x, B, C, a few
 for the step and its decay, and what sums over a sequence of L tokens add, at
-most 4 a token: 96 + 4 L.  A decay's exponent is off by roundings of itself,
+most 4 a token: 96 + 4 L.  Where y is bf16 its products take two bf16 planes a
+side: a side's third plane is at most 2^-16 of it, and so is the product of the
+second ones of the sides', 3 x 2^-16 = 768 roundings a term in all.  A decay's exponent is off by roundings of itself,
 whose weight falls as fast as it grows.
 """
 import pytest
@@ -22,6 +24,10 @@ DEV = "cuda:0"
 
 def rnd(gen, *shape, dtype=F32, scale=1.0):
     return (scale * torch.randn(shape, generator=gen)).to(dtype).to(DEV)
+
+
+def planes(y):
+    return 768 if y.dtype is BF16 else 0
 
 
 class Inputs:
@@ -61,7 +67,7 @@ def test_prompt(gpu, shape, dtype, out, ragged):
     y, S, cs = i.fwd(out, lengths)
     torch.cuda.synchronize()
     (ry, rS, rcs), (my, mS) = i.ref(lengths)
-    close(y, ry, my, 96 + 4 * L, "y")
+    close(y, ry, my, 96 + 4 * L + planes(y), "y")
     close(S, rS, mS, 96 + 4 * L, "state")
     assert torch.equal(cs.cpu().double(), rcs)
 
@@ -137,7 +143,7 @@ def test_extreme_steps(gpu):
     y, S, _ = i.fwd()
     torch.cuda.synchronize()
     (ry, rS, _), (my, mS) = i.ref()
-    close(y, ry, my, 96 + 600, "y")
+    close(y, ry, my, 96 + 600 + planes(y), "y")
     close(S, rS, mS, 96 + 600, "state")
 
 
@@ -215,7 +221,7 @@ def test_strong_decays_beside_weak_ones(gpu, P, dtype):
     (ry, rS, rcs), (my, mS) = i.ref()
     y, S, cs = i.fwd()
     torch.cuda.synchronize()
-    close(y, ry, my, 96 + 1600, "y")
+    close(y, ry, my, 96 + 1600 + planes(y), "y")
     close(S, rS, mS, 96 + 1600, "state")
 
 
@@ -229,7 +235,7 @@ def test_growing_states(gpu, L):
     (ry, rS, _), (my, mS) = i.ref()
     y, S, _ = i.fwd()
     torch.cuda.synchronize()
-    close(y, ry, my, 96 + 4 * L, "y")
+    close(y, ry, my, 96 + 4 * L + planes(y), "y")
     close(S, rS, mS, 96 + 4 * L, "state")
 
 
@@ -244,7 +250,7 @@ def test_many_groups_and_heads(gpu):
         (ry, rS, rcs), (my, mS) = i.ref()
         y, S, cs = i.fwd(BF16)
         torch.cuda.synchronize()
-        close(y, ry, my, 96 + 560, "y")
+        close(y, ry, my, 96 + 560 + planes(y), "y")
         close(S, rS, mS, 96 + 560, "state")
         assert torch.equal(cs.cpu().double(), rcs)
 
@@ -275,7 +281,7 @@ def test_rows_too_far_apart_for_a_chunk(gpu):
     (ry, rS, rcs), (my, mS) = i.ref()
     y, S, cs = i.fwd()
     torch.cuda.synchronize()
-    close(y, ry, my, 96 + 280, "y")
+    close(y, ry, my, 96 + 280 + planes(y), "y")
     close(S, rS, mS, 96 + 280, "state")
 
 
@@ -292,7 +298,7 @@ def test_rows_that_overlap(gpu, L, dtype):
         (ry, rS, rcs), (my, mS) = i.ref()
         y, S, cs = i.fwd()
         torch.cuda.synchronize()
-        close(y, ry, my, 96 + 4 * L, "y")
+        close(y, ry, my, 96 + 4 * L + planes(y), "y")
         close(S, rS, mS, 96 + 4 * L, "state")
         assert torch.equal(cs.cpu().double(), rcs)
 
@@ -306,7 +312,7 @@ def test_segments_of_ragged_prompts(gpu, lengths, dtype, out):
     room = torch.full((9, 700, 12, 24), float("nan"), dtype=out, device=DEV)
     y, S, cs = i.fwd(out, lengths, room)
     torch.cuda.synchronize()
-    close(y, ry, my, 96 + 2800, "y")
+    close(y, ry, my, 96 + 2800 + planes(y), "y")
     close(S, rS, mS, 96 + 2800, "state")
     assert torch.equal(cs.cpu().double(), rcs)
     for b, n in enumerate(lengths):
@@ -322,7 +328,7 @@ def test_many_ragged_prompts(gpu, batch, odd):
     (ry, rS, rcs), (my, mS) = i.ref(lengths)
     y, S, cs = i.fwd(BF16, lengths, torch.full((batch, 200, 4, 15 if odd else 16), float("nan"), dtype=BF16, device=DEV))
     torch.cuda.synchronize()
-    close(y, ry, my, 96 + 800, "y")
+    close(y, ry, my, 96 + 800 + planes(y), "y")
     close(S, rS, mS, 96 + 800, "state")
     assert torch.equal(cs.cpu().double(), rcs)
 
