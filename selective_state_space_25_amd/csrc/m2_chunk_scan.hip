@@ -642,9 +642,10 @@ Plan plan_of(const M2ConvArgs& a, int in_bf16, bool ragged) {
     // segments would be more than that, the device cuts them from the tokens
     // that are there, four a sequence at least, in whole rounds of workgroups
     // (batch 8, lengths spread over 0 .. 4096: 249 us; segments of one length,
-    // four workgroups a unit, took 349 where the cut took 275).  Its cut costs 0.5 us a launch (batch 3 of
-    // up to 333 tokens: 38 us, without 35), and a lane a sequence does no more
-    // than 64: those have one length, and four workgroups a unit.
+    // four workgroups a unit, took 349 where the cut took 275).  Its cut costs
+    // 0.5 us a launch (batch 3 of up to 333 tokens: 38 us, without 35), and a
+    // lane a sequence does no more than 64: those have one length, and four
+    // workgroups a unit.
     const int64_t cus = host::device_cus(), groups = a.batch * a.G * p.sets;
     p.want = std::max<int64_t>(1, cus / (a.G * p.sets));
     p.want *= std::max<int64_t>(1, (4 * a.batch + p.want - 1) / p.want);
