@@ -670,7 +670,9 @@ selscan_status_t selscan_mamba2_conv_step(const selscan_m2_conv_shape_t* shape, 
  *
  *     scale = max(max |y| / 448, 2^-126);  y8 = y / scale, rounded to nearest even
  *
- * (a NaN makes its block's scale NaN).
+ * of the fp32 y and the fp32 quotient: y's own roundings (a few of 2^-24) take a
+ * y / scale next to a tie of two e4m3 values to either of them.  A NaN makes its
+ * block's scale NaN.
  *   x            [rows, dim]  in_dtype
  *   residual     [rows, dim]  res_dtype   NULL = 0
  *   gate         [rows, dim]  in_dtype    rows gate_row elements apart; NULL =

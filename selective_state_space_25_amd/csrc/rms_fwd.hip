@@ -3,8 +3,8 @@
 //   s = x + residual, or x silu(gate);  rstd = 1 / sqrt(sum s^2 / width + eps);  y = s rstd weight
 //
 // over the groups of a row (one group: the row), y in fp32, bf16 or, with a
-// scale for each block of a group, e4m3: scale = max(max |y| / 448, 2^-126), y
-// / scale rounded to nearest even.  A stream bound by memory: a group stays in
+// scale for each block of a group, e4m3: scale = max(max |y| / 448, 2^-126), the
+// fp32 quotient y / scale rounded to nearest even.  A stream bound by memory: a group stays in
 // registers between its sum and its output, in 8-element pieces over 8 to 64
 // lanes of a wave (up to 2560 elements, sums without a barrier) or the 256 of
 // a workgroup (to 8192), so every element is read once and written once; the
@@ -13,7 +13,7 @@
 // a piece.  Longer groups are read again for each step.
 //
 // 32768 x 2560, bf16 with an fp32 residual: 183 us for 1.01 GB, 5.5 TB/s.
-// 16384 x 5120 with a gate, e4m3 in blocks of 128: 97 us for 0.42 GB, 4.3 TB/s,
+// 16384 x 5120 with a gate, e4m3 in blocks of 128: 100 us for 0.42 GB, 4.2 TB/s,
 // vector ALU 74 % busy (silu, the blocks' maxima, conversions).  One row of 768
 // is the launch: 2.9 us.
 #include "rms_rows.hpp"
@@ -33,6 +33,25 @@ __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > 
 __device__ __forceinline__ float scale_of(uint32_t m) {
     const float s = __uint_as_float(m) / kTop8;
     return s < kLeastScale ? kLeastScale : s;   // (NaN stays)
+}
+
+// v / scale, rounded as a division is: a product with the rounded reciprocal is
+// off in one of four quotients, and next to a tie of e4m3 that costs a whole
+// step.  One correction from the exact remainder makes it the division's
+// (P. Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990) where nothing leaves fp32's range; scales outside 2^-80 ..
+// 2^100 (NaN among them) are divided by.
+__device__ __forceinline__ void over_scale(float (&v)[8], float scale, float inv) {
+    if (scale >= 0x1p-80f && scale <= 0x1p100f) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q = v[i] * inv;
+            v[i] = __builtin_fmaf(__builtin_fmaf(-q, scale, v[i]), inv, q);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] /= scale;
+    }
 }
 
 // One group of one row.
@@ -133,9 +152,8 @@ __global__ __launch_bounds__(kT) void rms_fwd_kernel(RmsArgs a) {
             if (block) {
                 // a block is 4 to 64 lanes of a wave; narrower groups are one block
                 for (int o = min(block / 8, LR) / 2; o >= 1; o >>= 1) m = larger(m, (uint32_t)__shfl_xor((int)m, o, 64));
-                const float sc = scale_of(m), inv = 1.0f / sc;
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[j][i] *= inv;
+                const float sc = scale_of(m);
+                over_scale(s[j], sc, 1.0f / sc);
                 if (d < row.width) {
                     if ((d & (block - 1)) == 0) row.scale[d >> shift] = sc;
                     stp<false>(row.y + d, row.width - d, s[j]);
@@ -153,8 +171,7 @@ __global__ __launch_bounds__(kT) void rms_fwd_kernel(RmsArgs a) {
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
             const int d = 8 * (at + LR * j);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[j][i] *= inv;
+            over_scale(s[j], sc, inv);
             if (d < row.width) stp<false>(row.y + d, row.width - d, s[j]);
         }
     }
@@ -177,7 +194,7 @@ __global__ __launch_bounds__(kT) void rms_fwd_long_kernel(RmsArgs a) {
     }
     const float rstd = 1.0f / sqrtf(row_sum<256>(sq, sm) * a.inv_width + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[unit] = rstd;
-    float inv = 1.0f;
+    float sc = 1.0f, inv = 1.0f;
     if constexpr (k8) {
         if (!a.block) {
             uint32_t m = 0;
@@ -187,7 +204,7 @@ __global__ __launch_bounds__(kT) void rms_fwd_long_kernel(RmsArgs a) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) m = larger(m, magnitude(v[i]));
             }
-            const float sc = scale_of(over_row<256>(m, sm8, larger));
+            sc = scale_of(over_row<256>(m, sm8, larger));
             inv = 1.0f / sc;
             if (threadIdx.x == 0) row.scale[0] = sc;
         }
@@ -208,12 +225,11 @@ __global__ __launch_bounds__(kT) void rms_fwd_long_kernel(RmsArgs a) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) m = larger(m, magnitude(v[i]));
                 for (int o = (int)(a.block / 16); o >= 1; o >>= 1) m = larger(m, (uint32_t)__shfl_xor((int)m, o, 64));
-                const float sc = scale_of(m);
+                sc = scale_of(m);
                 inv = 1.0f / sc;
                 if (live && d % a.block == 0) row.scale[d / a.block] = sc;
             }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] *= inv;
+            over_scale(v, sc, inv);
         }
         if (live) stp<false>(row.y + d, row.width - d, v);
     }
