@@ -32,14 +32,14 @@
 // the device cuts the segments (m2_chunk.hpp), since the host does not know the
 // lengths.
 //
-// 1 x 16384, 32 heads of 64 x 128 in one group, bf16: 108 us, and 72 for the
-// state pass and 17 for the carry between them.  Six MFMAs a product, three
-// where it makes y in bf16, are 0.14 TFLOP, 100 us of a library product's rate
-// (1378 TFLOP/s); the matrix cores are busy a third of the time, the vector ALU
-// (convolution, splits, decays) half, and a compute unit's one workgroup, two waves a SIMD,
+// 1 x 16384, 32 heads of 64 x 128 in one group, bf16: 128 us, and 71 for the
+// state pass and 17 for the carry between them.  Six MFMAs a product make this
+// 0.17 TFLOP, 126 us of a library product's rate (1378 TFLOP/s), the state pass
+// a fifth of it; the matrix cores are busy 40 %, the vector ALU (convolution,
+// splits, decays) 47 %, and a compute unit's one workgroup, two waves a SIMD,
 // overlaps them as far as its two barriers a chunk let it.
 //
-// Products are fp32-grade (split_mfma.hpp), those of a bf16 y 16 bits.  cum is summed in fp64, and its
+// Products are fp32-grade (split_mfma.hpp).  cum is summed in fp64, and its
 // exponentials take it as two fp32 parts: after strong decays it is large, and
 // its rounding to one would be an error of them all.
 #include <algorithm>
@@ -166,10 +166,10 @@ __device__ __forceinline__ bf16x8 op_at(const unsigned char (*blocks)[kBlock], i
 // M products over one k-step, in turns: an MFMA that adds to the sum of the one
 // before waits out its latency, and the compiler, which may move anything else
 // between them, is kept from lining such up.
-template <int M, int PL, typename FA, typename FB, typename FC>
+template <int M, typename FA, typename FB, typename FC>
 __device__ __forceinline__ void in_turns(FA a, FB b, FC c) {
 #pragma unroll
-    for (int s = PL - 1; s >= 0; --s)
+    for (int s = 2; s >= 0; --s)
 #pragma unroll
         for (int i = 0; i <= s; ++i) {
 #pragma unroll
@@ -183,13 +183,6 @@ template <typename Tin, typename Tout, int K, int NP, int CT, bool STATE>
 __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, Plan pl, const char* recs, float* seg_state,
                                                                  float* seg_log) {
     constexpr int KS = NP / 32, NT = NP / 16, ES = (int)sizeof(Tin), EO = (int)sizeof(Tout);
-    // Planes of the products that make y alone, C S and G X': two where y is
-    // rounded to bf16.  Each term is then off by 3 x 2^-16 of itself at most
-    // (2^-16 from either side's third plane and from the product of the second
-    // ones), 1 / 85 of y's own rounding where terms do not cancel.
-    // (1 x 16384 as above: 108 us, with three planes 128; the state and the
-    // products that make it have three whatever y is.)
-    constexpr int PY = sizeof(Tout) == 2 ? 2 : 3;
     using R = Rec<NP>;
     extern __shared__ __attribute__((aligned(16))) unsigned char smem_raw[];
     auto& sm = *reinterpret_cast<Smem<NP, CT>*>(smem_raw);
@@ -391,7 +384,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
             for (int k = 0; k < 2; ++k)
 #pragma unroll
                 for (int x3 = 0; x3 < 3; ++x3) bp[k][x3] = op_at(Bs, ((i + k) * 2 + ks) * 3 + x3, lane);
-            in_turns<2 * CT, 3>([&](int m) -> const bf16x8(&)[3] { return bp[m / CT]; },
+            in_turns<2 * CT>([&](int m) -> const bf16x8(&)[3] { return bp[m / CT]; },
                              [&](int m) -> const bf16x8(&)[3] { return xp[m % CT]; },
                              [&](int m) -> f32x4& { return S[i + m / CT][m % CT]; });
         }
@@ -469,19 +462,19 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
             if (live) {
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
-                    bf16x8 sp[CT][PY];
+                    bf16x8 sp[CT][3];
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct) split8<PY>(S[2 * ks][ct], S[2 * ks + 1][ct], sp[ct]);
+                    for (int ct = 0; ct < CT; ++ct) split8<3>(S[2 * ks][ct], S[2 * ks + 1][ct], sp[ct]);
 #pragma unroll
                     for (int tt = 0; tt < 4; tt += 2) {
-                        bf16x8 cp[2][PY];
+                        bf16x8 cp[2][3];
 #pragma unroll
                         for (int k = 0; k < 2; ++k)
 #pragma unroll
-                            for (int x3 = 0; x3 < PY; ++x3) cp[k][x3] = op_at(sm.C, (ks * 4 + tt + k) * 3 + x3, lane);
-                        in_turns<2 * CT, PY>([&](int m) -> const bf16x8(&)[PY] { return cp[m / CT]; },
-                                             [&](int m) -> const bf16x8(&)[PY] { return sp[m % CT]; },
-                                             [&](int m) -> f32x4& { return y[tt + m / CT][m % CT]; });
+                            for (int x3 = 0; x3 < 3; ++x3) cp[k][x3] = op_at(sm.C, (ks * 4 + tt + k) * 3 + x3, lane);
+                        in_turns<2 * CT>([&](int m) -> const bf16x8(&)[3] { return cp[m / CT]; },
+                                         [&](int m) -> const bf16x8(&)[3] { return sp[m % CT]; },
+                                         [&](int m) -> f32x4& { return y[tt + m / CT][m % CT]; });
                     }
                 }
             }
@@ -506,9 +499,9 @@ __global__ __launch_bounds__(64 * kWaves, 2) void m2_chunk_kernel(M2ConvArgs a, 
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct) acc[k][ct] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                     }
-                    in_turns<2 * CT, PY>([&](int m) -> const bf16x8(&)[3] { return gp[m / CT]; },
-                                         [&](int m) -> const bf16x8(&)[3] { return xp[m % CT]; },
-                                         [&](int m) -> f32x4& { return acc[m / CT][m % CT]; });
+                    in_turns<2 * CT>([&](int m) -> const bf16x8(&)[3] { return gp[m / CT]; },
+                                     [&](int m) -> const bf16x8(&)[3] { return xp[m % CT]; },
+                                     [&](int m) -> f32x4& { return acc[m / CT][m % CT]; });
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         f32x4 f = {1.0f, 1.0f, 1.0f, 1.0f}, e = f;
@@ -641,11 +634,10 @@ Plan plan_of(const M2ConvArgs& a, int in_bf16, bool ragged) {
     // workgroups a unit 269).  Where sequences may end early and the shortest
     // segments would be more than that, the device cuts them from the tokens
     // that are there, four a sequence at least, in whole rounds of workgroups
-    // (batch 8, lengths spread over 0 .. 4096: 249 us; segments of one length,
-    // four workgroups a unit, took 349 where the cut took 275).  Its cut costs
-    // 0.5 us a launch (batch 3 of up to 333 tokens: 38 us, without 35), and a
-    // lane a sequence does no more than 64: those have one length, and four
-    // workgroups a unit.
+    // (batch 8, lengths spread over 0 .. 4096: 269 us; segments of one length,
+    // four workgroups a unit, took 349 where the cut took 275).  Its cut costs 0.5 us a launch (batch 3 of
+    // up to 333 tokens: 38 us, without 35), and a lane a sequence does no more
+    // than 64: those have one length, and four workgroups a unit.
     const int64_t cus = host::device_cus(), groups = a.batch * a.G * p.sets;
     p.want = std::max<int64_t>(1, cus / (a.G * p.sets));
     p.want *= std::max<int64_t>(1, (4 * a.batch + p.want - 1) / p.want);
