@@ -648,7 +648,8 @@ selscan_status_t selscan_mamba2_conv_fwd(const selscan_m2_conv_shape_t* shape, c
  * The mixer for one token: xbc [B, H P + 2 G N] (batch elements xbc_batch
  * apart), dt [B, H] (dt_batch apart), y [B, H, P]; state [B, H, P, N] fp32
  * (16-byte aligned) and conv_state [B, K-1, H P + 2 G N] are updated in place.
- * seqlen, xbc_row, dt_row and workspace are ignored.
+ * y, state and conv_state must not overlap xbc, dt or each other
+ * (INVALID_ARG).  seqlen, xbc_row, dt_row and workspace are ignored.
  */
 selscan_status_t selscan_mamba2_conv_step(const selscan_m2_conv_shape_t* shape, float* state, void* conv_state,
                                           const void* xbc, const void* dt, const float* conv_weight,

@@ -56,6 +56,18 @@ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Whether one of the n bytes at p is one of those of `rows` rows at q, m bytes
+// each and `stride` bytes apart.
+inline bool overlap(const void* p, int64_t n, const void* q, int64_t m, int64_t rows = 1, int64_t stride = 0) {
+    const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    uint64_t r = 0;   // the first row that ends behind p
+    if (b + (uint64_t)m <= a) {
+        if (stride <= 0) return false;
+        r = (a - b - (uint64_t)m) / (uint64_t)stride + 1;
+    }
+    return r < (uint64_t)rows && b + r * (uint64_t)stride < a + (uint64_t)n;
+}
+
 // The current device must be a gfx950.  The architecture check runs once per
 // device (cached like device_cus()); later calls only read the current device.
 inline selscan_status_t device_check() {

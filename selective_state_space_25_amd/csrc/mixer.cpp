@@ -21,6 +21,7 @@ constexpr int64_t kMostGroups = (int64_t)1 << 35;   // workgroups of a launch ov
 constexpr int64_t kMostSumCols = (int64_t)1 << 24, kMostSumRows = (int64_t)1 << 25;
 
 bool is_dtype(int32_t d) { return d == SELSCAN_F32 || d == SELSCAN_BF16; }
+int64_t bytes_of(int32_t dtype) { return dtype == SELSCAN_F32 ? 4 : 2; }
 
 selscan_status_t check_width(int64_t width) {
     if (width < 1) return set_error(SELSCAN_ERR_INVALID_ARG, "width must be >= 1");
@@ -290,6 +291,18 @@ selscan_status_t selscan_mamba2_conv_step(const selscan_m2_conv_shape_t* s, floa
         if (!state || !conv_state || !xbc || !dt || !conv_weight || !A || !y)
             return set_error(SELSCAN_ERR_INVALID_ARG, "state, conv_state, xbc, dt, conv_weight, A and y must be non-NULL");
         if (!aligned16(state)) return set_error(SELSCAN_ERR_INVALID_ARG, "state must be 16-byte aligned");
+        // y is written while other workgroups read dt and the channels of B and C,
+        // and a launch behind that reads all of xbc
+        const int64_t hp = s->nheads * s->headdim, C = hp + 2 * s->ngroups * s->dstate;
+        const int64_t es = bytes_of(s->in_dtype), ny = s->batch * hp * bytes_of(s->out_dtype);
+        const int64_t ns = s->batch * hp * s->dstate * 4, nc = s->batch * (s->width - 1) * C * es;
+        const auto inputs = [&](const void* p, int64_t n) {
+            return overlap(p, n, xbc, C * es, s->batch, s->xbc_batch * es) ||
+                   overlap(p, n, dt, s->nheads * es, s->batch, s->dt_batch * es);
+        };
+        if (inputs(y, ny) || inputs(state, ns) || inputs(conv_state, nc) || overlap(y, ny, state, ns) ||
+            overlap(y, ny, conv_state, nc) || overlap(state, ns, conv_state, nc))
+            return set_error(SELSCAN_ERR_INVALID_ARG, "y, state and conv_state must not alias xbc, dt or each other");
         st = device_check();
         if (st != SELSCAN_OK) return st;
         selscan::M2ConvArgs a{};
