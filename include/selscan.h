@@ -585,7 +585,9 @@ selscan_status_t selscan_short_conv_bwd(const selscan_short_conv_shape_t* shape,
                                         void* stream);
 
 /* One token: x [B, D] (batch elements x_batch apart; seqlen, x_row and split
- * ignored), y [B, D] out_dtype; state [B, K-1, D] in_dtype moves on in place. */
+ * ignored), y [B, D] out_dtype; state [B, K-1, D] in_dtype moves on in place.
+ * y may be x where their types agree and x is dense; otherwise y and state must
+ * not overlap x or each other (INVALID_ARG). */
 selscan_status_t selscan_short_conv_step(const selscan_short_conv_shape_t* shape, void* state, const void* x,
                                          const float* weight, const float* bias, int silu, void* y, void* stream);
 

@@ -976,7 +976,8 @@ def _short_conv_step_args(state, x, weight, bias, silu, out, out_dtype, what):
 def short_conv_step(state, x, weight, bias=None, silu=True, out=None, out_dtype=None):
     """One token of the short convolution (decoding): x [batch, dim], its rows
     strided; state [batch, K - 1, dim] in x's dtype moves on in place.  Returns
-    y [batch, dim] in x's dtype unless out_dtype or out says otherwise."""
+    y [batch, dim] in x's dtype unless out_dtype or out says otherwise; out may
+    be x itself where it is contiguous, and no other memory of x or state."""
     if state is None:
         raise TypeError("state must be a torch.Tensor")
     s, args, out = _short_conv_step_args(state, x, weight, bias, silu, out, out_dtype, "short_conv_step")
@@ -1078,7 +1079,7 @@ def mamba2_conv_step(state, conv_state, xbc, dt, conv_weight, conv_bias, A, D=No
     dt [batch, H], rows strided; state [batch, H, P, N] float32 and conv_state
     [batch, K - 1, H P + 2 G N] are updated in place; the rest as for
     mamba2_conv_fwd.  Returns y [batch, H, P] (float32 unless out_dtype or out
-    says otherwise)."""
+    says otherwise); out must not overlap xbc, dt or the states."""
     s, args, out = _mamba2_conv_step_args(state, conv_state, xbc, dt, conv_weight, conv_bias, A, D, dt_bias, out, out_dtype,
                                           "mamba2_conv_step")
     _check(lib().selscan_mamba2_conv_step(ctypes.byref(s), *args))

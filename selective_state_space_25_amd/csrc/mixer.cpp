@@ -229,6 +229,13 @@ selscan_status_t selscan_short_conv_step(const selscan_short_conv_shape_t* s, vo
         if (!state || !x || !weight || !y)
             return set_error(SELSCAN_ERR_INVALID_ARG, "state, x, weight and y must be non-NULL");
         if (silu != 0 && silu != 1) return set_error(SELSCAN_ERR_INVALID_ARG, "silu must be 0 or 1");
+        // (a thread reads its channels of a row before it writes them)
+        const int64_t es = bytes_of(s->in_dtype), ny = s->batch * s->dim * bytes_of(s->out_dtype);
+        const int64_t ns = s->batch * (s->width - 1) * s->dim * es;
+        const bool in_place = y == x && s->in_dtype == s->out_dtype && (s->batch == 1 || s->x_batch == s->dim);
+        if ((!in_place && overlap(y, ny, x, s->dim * es, s->batch, s->x_batch * es)) || overlap(y, ny, state, ns) ||
+            overlap(state, ns, x, s->dim * es, s->batch, s->x_batch * es))
+            return set_error(SELSCAN_ERR_INVALID_ARG, "y must not alias x (but be x, of its type and dense) or state, nor state x");
         st = device_check();
         if (st != SELSCAN_OK) return st;
         selscan::ShortConvArgs a{};
