@@ -680,13 +680,14 @@ selscan_status_t selscan_mamba2_conv_step(const selscan_m2_conv_shape_t* shape, 
  *   gate         [rows, dim]  in_dtype    rows gate_row elements apart; NULL =
  *                                         none; not with a residual (UNSUPPORTED)
  *   weight       [dim]        fp32        NULL = 1
- *   y            [rows, dim]  out_dtype   (written); may be x where their types
- *                                         agree
+ *   y            [rows, dim]  out_dtype   (written)
  *   residual_out [rows, dim]  res_dtype   s (written; NULL = skip; not with a
- *                                         gate); may be residual
+ *                                         gate)
  *   rstd         [rows, groups] fp32      (written; NULL = skip)
  *   scale        [rows, groups ceil(width / scale_block)]  fp32  (written with
  *                                         E4M3, where it is required)
+ * y and residual_out may each be an input of the same type (y over x, s over
+ * residual), rows where that has them; other overlaps are INVALID_ARG.
  * scale_block: 0, 32, 64, 128, 256 or 512.  Sums are fp32 over s before it is
  * rounded.  rows, dim, groups >= 1, dim % groups == 0.  Workspace is used by
  * the gradients only.
@@ -725,10 +726,12 @@ size_t selscan_rms_norm_bwd_workspace_bytes(const selscan_rms_shape_t* shape);
  *   dresidual_out [rows, dim]  res_dtype   gradient of s from its other uses;
  *                                          NULL = 0; not with a gate
  *   dx            [rows, dim]  in_dtype    (written; NULL = skip)
- *   dresidual     [rows, dim]  res_dtype   (written; NULL = skip); may be
- *                                          dresidual_out; not with a gate
+ *   dresidual     [rows, dim]  res_dtype   (written; NULL = skip); not with a gate
  *   dgate         [rows, dim]  in_dtype    (written; NULL = skip); with a gate only
  *   dweight       [dim]        fp32        (written; NULL = skip)
+ * dx, dresidual and dgate may each be an input of the same type, rows where that
+ * has them (dresidual over dresidual_out); not dy, s or gate where dweight of
+ * groups longer than 8192 is asked for.  Other overlaps are INVALID_ARG.
  * Sums over rows run in a fixed order: results are reproducible bit for bit.
  * Workspace as for the other entry points; none where dweight is NULL.
  */

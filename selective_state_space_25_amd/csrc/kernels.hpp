@@ -335,6 +335,7 @@ struct RmsArgs {
 };
 size_t rms_bwd_part_bytes(int64_t rows, int64_t dim, int64_t groups);
 int rms_bwd_blocks(int64_t rows, int64_t width);
+bool rms_reads_again(int64_t width);   // dweight by a kernel of its own, behind the other gradients
 hipError_t launch_rms_fwd(const RmsArgs& a, int in_bf16, int res_bf16, int out_dtype, hipStream_t stream);
 hipError_t launch_rms_bwd(const RmsArgs& a, int in_bf16, int res_bf16, int out_bf16, hipStream_t stream);
 

@@ -33,6 +33,25 @@ selscan_status_t check(const selscan_rms_shape_t* s, bool grad) {
     return SELSCAN_OK;
 }
 
+int64_t bytes_of(int32_t dtype) { return dtype == SELSCAN_F32 ? 4 : dtype == SELSCAN_BF16 ? 2 : 1; }
+
+// Whether `rows` rows of dim elements at p (dense) overlap those at q (`row`
+// elements apart) other than element by element: the kernels read an element
+// before they write in its place, and no others.
+struct Tensor {
+    const void* p;
+    int32_t dtype;
+    int64_t row;
+};
+bool in_place(const selscan_rms_shape_t* s, const Tensor& out, const Tensor& in) {
+    return out.p == in.p && out.dtype == in.dtype && (in.row == s->dim || s->rows == 1);
+}
+bool clash(const selscan_rms_shape_t* s, const Tensor& out, const Tensor& in, bool may_be = true) {
+    const int64_t eo = bytes_of(out.dtype), ei = bytes_of(in.dtype);
+    return out.p && in.p && !(may_be && in_place(s, out, in)) &&
+           overlap(out.p, s->rows * s->dim * eo, in.p, s->dim * ei, s->rows, in.row * ei);
+}
+
 void fill(selscan::RmsArgs& a, const selscan_rms_shape_t* s) {
     a.rows = s->rows; a.dim = s->dim; a.groups = s->groups; a.gate_row = s->gate_row;
     a.width = s->dim / s->groups;
@@ -65,6 +84,13 @@ selscan_status_t selscan_rms_norm_fwd(const selscan_rms_shape_t* s, const void* 
             return set_error(SELSCAN_ERR_UNSUPPORTED, "a gate takes neither residual nor residual_out");
         if (s->out_dtype == SELSCAN_E4M3 && !scale)
             return set_error(SELSCAN_ERR_INVALID_ARG, "scale must be non-NULL where y is in 8 bits");
+        const Tensor outs[] = {{y, s->out_dtype, s->dim}, {residual_out, s->res_dtype, s->dim}};
+        const Tensor ins[] = {{x, s->in_dtype, s->dim}, {residual, s->res_dtype, s->dim}, {gate, s->in_dtype, s->gate_row}};
+        bool bad = clash(s, outs[0], outs[1], false);
+        for (const Tensor& o : outs)
+            for (const Tensor& i : ins) bad = bad || clash(s, o, i);
+        if (bad)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "y and residual_out must not alias each other, nor inputs but in the place and type of one");
         st = device_check();
         if (st != SELSCAN_OK) return st;
         selscan::RmsArgs a{};
@@ -97,6 +123,18 @@ selscan_status_t selscan_rms_norm_bwd(const selscan_rms_shape_t* s, const void* 
         if (gate && s->res_dtype != s->in_dtype)
             return set_error(SELSCAN_ERR_UNSUPPORTED, "with a gate, s is x: res_dtype must be in_dtype");
         if (!gate && dgate) return set_error(SELSCAN_ERR_INVALID_ARG, "dgate needs gate");
+        const Tensor outs[] = {{dx, s->in_dtype, s->dim}, {dresidual, s->res_dtype, s->dim}, {dgate, s->in_dtype, s->dim}};
+        const Tensor ins[] = {{dy, s->out_dtype, s->dim}, {sum, s->res_dtype, s->dim}, {gate, s->in_dtype, s->gate_row}};
+        // long groups: dweight is made from dy, s and gate when the gradients are there
+        const bool again = dweight && selscan::rms_reads_again(s->dim / s->groups);
+        bool bad = clash(s, outs[0], outs[1], false) || clash(s, outs[0], outs[2], false);
+        for (const Tensor& o : outs) {
+            bad = bad || clash(s, o, {dresidual_out, s->res_dtype, s->dim});
+            for (const Tensor& i : ins) bad = bad || clash(s, o, i, !again);
+        }
+        if (bad)
+            return set_error(SELSCAN_ERR_INVALID_ARG, "gradients must not alias each other, nor inputs but in the place and type of one "
+                                                      "(dy, s and gate: not with dweight of groups past 8192)");
         st = device_check();
         if (st != SELSCAN_OK) return st;
         hipStream_t hs = reinterpret_cast<hipStream_t>(stream);

@@ -247,6 +247,8 @@ int rms_bwd_blocks(int64_t rows, int64_t width) {
     return (int)std::min(n, (rows + once - 1) / once);
 }
 
+bool rms_reads_again(int64_t width) { return !Layout(width, false).pieces; }
+
 size_t rms_bwd_part_bytes(int64_t rows, int64_t dim, int64_t groups) {
     return (size_t)column_sums_rows(rms_bwd_blocks(rows, dim / groups)) * (size_t)dim * 4;
 }
