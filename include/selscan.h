@@ -689,7 +689,7 @@ selscan_status_t selscan_mamba2_conv_step(const selscan_m2_conv_shape_t* shape, 
  * y and residual_out may each be an input of the same type (y over x, s over
  * residual), rows where that has them; other overlaps are INVALID_ARG.
  * scale_block: 0, 32, 64, 128, 256 or 512.  Sums are fp32 over s before it is
- * rounded.  rows, dim, groups >= 1, dim % groups == 0.  Workspace is used by
+ * rounded, fp64 over the pieces of groups longer than 8192.  rows, dim, groups >= 1, dim % groups == 0.  Workspace is used by
  * the gradients only.
  */
 typedef struct {

@@ -162,19 +162,21 @@ __global__ __launch_bounds__(kT) void rms_bwd_kernel(RmsArgs a) {
     }
 }
 
-// Groups longer than the registers: read twice, and dweight by columns.
+// Groups longer than the registers: read twice (sums as in the forward), and
+// dweight by columns.
 template <typename Tin, typename Tres, typename Tout, bool GATE>
 __global__ __launch_bounds__(kT) void rms_bwd_long_kernel(RmsArgs a) {
     __shared__ float sm[4];
     const int64_t unit = io::group_id(), r = unit / a.groups;
     if (r >= a.rows) return;
     const Row<Tin, Tres, Tout, GATE> row(a, r, unit - r * a.groups);
-    float y[8], x[8], z[GATE ? 8 : 1], c = 0.0f;
+    float y[8], x[8], z[GATE ? 8 : 1];
+    double sum = 0.0;
     for (int d = 8 * (int)threadIdx.x; d < row.width; d += 8 * kT) {
         row.template load<false>(d, y, x, z);
-        c += row.template dot<false>(d, y, x, z, nullptr);
+        sum += row.template dot<false>(d, y, x, z, nullptr);
     }
-    c = row_sum<256>(c, sm) * a.inv_width;
+    const float c = row_sum<256>((float)sum, sm) * a.inv_width;
     for (int d = 8 * (int)threadIdx.x; d < row.width; d += 8 * kT) {
         row.template load<false>(d, y, x, z);
         row.template dot<false>(d, y, x, z, nullptr);

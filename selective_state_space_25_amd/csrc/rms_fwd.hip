@@ -177,7 +177,9 @@ __global__ __launch_bounds__(kT) void rms_fwd_kernel(RmsArgs a) {
     }
 }
 
-// Groups longer than the registers: read again for each step, 2048 elements at a time.
+// Groups longer than the registers: read again for each step, 2048 elements at
+// a time.  A lane's sum over those is fp64: in fp32 its error grows with the
+// length, as fast as that where the terms are alike.
 template <typename Tin, typename Tres, typename Tout>
 __global__ __launch_bounds__(kT) void rms_fwd_long_kernel(RmsArgs a) {
     __shared__ float sm[4];
@@ -186,13 +188,16 @@ __global__ __launch_bounds__(kT) void rms_fwd_long_kernel(RmsArgs a) {
     const int64_t unit = io::group_id();
     if (unit >= a.rows * a.groups) return;
     const Row<Tin, Tres, Tout> row(a, unit);
-    float v[8], sq = 0.0f;
+    float v[8];
+    double sq = 0.0;
     for (int d = 8 * (int)threadIdx.x; d < row.width; d += 8 * kT) {
+        float p = 0.0f;
         row.template sum<false>(d, v);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sq = __builtin_fmaf(v[i], v[i], sq);
+        for (int i = 0; i < 8; ++i) p = __builtin_fmaf(v[i], v[i], p);
+        sq += p;
     }
-    const float rstd = 1.0f / sqrtf(row_sum<256>(sq, sm) * a.inv_width + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum<256>((float)sq, sm) * a.inv_width + a.eps);
     if (threadIdx.x == 0 && a.rstd) a.rstd[unit] = rstd;
     float sc = 1.0f, inv = 1.0f;
     if constexpr (k8) {
