@@ -625,7 +625,7 @@ selscan_status_t selscan_short_conv_step(const selscan_short_conv_shape_t* shape
  * Outputs must not overlap inputs or each other.
  * N in {16, 32, 64, 128}.  State, decays and sums are fp32, and so are products
  * in effect.  The sequence is worked on in chunks of 64 tokens (up to 32 tokens
- * one by one, where the heads do not fill the GPU): a NaN or infinity in a token
+ * one by one, fewer where the heads fill the GPU, 7 at least): a NaN or infinity in a token
  * reaches every y of its chunk and head, and what follows, and so does a Delta x
  * past 2^60.  Rows may overlap (a row stride of 0 repeats one).  Workspace as
  * for the other entry points.

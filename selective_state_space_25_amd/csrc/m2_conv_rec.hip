@@ -5,9 +5,11 @@
 // from the convolution's results in fp32 (short_conv.hip, in the workspace).  A
 // workgroup has some rows of one head's state in registers, 8 (N >= 64) or 4
 // states a lane, and walks the sequence; a row's lanes add y up by shuffles.
-// Time goes with the length, whatever the number of heads: for short
-// sequences (0.65 us a token; what both forms take at which lengths stands at
-// kRecTokens in mixer.cpp).
+// For short sequences: time goes with the length, 0.6 us a token (a chain of
+// loads, exponentials and updates) as long as a compute unit has one or two
+// workgroups, up to 256 heads of 64 x 128, and with the heads from there (2048:
+// 9 us a token).  What both forms take at which lengths stands at kRecTokens in
+// mixer.cpp.
 #include "io.hpp"
 #include "kernels.hpp"
 

@@ -135,19 +135,28 @@ void fill(selscan::M2ConvArgs& a, const selscan_m2_conv_shape_t* s, bool token) 
 }
 
 // Short sequences are walked token by token, in a time that goes with their
-// length; in chunks it hardly moves within one.  us, token by token / in
-// chunks, bf16, heads of 64 x 128:
-//              32 heads       256 heads      2048 heads
-//   L =  8    11.4           14.3           51.7
-//   L = 16    16.3 / 31.4    19.4 / 32.3    89.9 / 57.7
-//   L = 32      -  / 31.6      -  / 32.4      -  / 58.1
-// (0.65 us a token until the GPU is full, and with the states from there).
-constexpr int64_t kRecTokens = 32;
+// length; in chunks it hardly moves within one.  us, token by token / in chunks,
+// bf16, heads of 64 x 128, from a state of zero and from h0 (whose states are
+// read too):
+//              32 heads       256 heads      512 heads      2048 heads     4096 heads
+//   L =  4     8.5 / 30.0    11.1 / 31.0    14.7 / 32.3    32.7 /  55.8    55.2 /  93.7
+//     h0       8.9 / 33.4    13.7 / 34.3    21.9 / 37.2    58.6 /  64.7   111.9 / 117.3
+//   L =  8    10.6 / 29.9    13.4 / 30.9    20.0 / 32.1    51.2 /  55.8    90.5 /  94.1
+//     h0      11.0 / 33.4    16.2 / 34.3    26.9 / 37.3    76.6 /  64.9   150.3 / 118.1
+//   L = 16    15.0 / 30.1    18.1 / 31.0    30.1 / 32.2    87.5 /  56.2   160.8 /  94.4
+//     h0      15.3 / 33.6    21.0 / 34.5    36.9 / 37.5   112.9 /  65.0   226.6 / 120.9
+//   L = 32    22.4 / 30.2    27.8 / 31.3    52.9 / 32.5   159.1 /  56.7   296.4 /  95.4
+//     h0      22.8 / 33.8    30.7 / 34.9    59.3 / 37.5   184.8 /  65.5   370.2 / 125.9
+// The two meet at 38 tokens (256 heads, 2^21 elements of state), 16 (512), and
+// from 2048 heads on, where both go with the states, at 9 from zero and 5 from
+// h0, whatever the number.  (fp32's chunks take less up to 512 heads, 24 to 30
+// us, and more from there; heads of 64 x 16 as many as 32 meet at 33.)
+constexpr int64_t kRecTokens = 32, kRecTokensFull = 7;
 
 // The chunked form's offsets inside 64 tokens and the three before are 32-bit.
 bool chunked(const selscan::M2ConvArgs& a) {
     const int64_t fills = std::max<int64_t>(1, a.batch * a.H * a.P * a.N >> 21);
-    return a.L * fills > kRecTokens && a.conv.x_row < ((int64_t)1 << 30) / (4 * 68);
+    return a.L > std::max(kRecTokens / fills, kRecTokensFull) && a.conv.x_row < ((int64_t)1 << 30) / (4 * 68);
 }
 
 size_t mixer_bytes(const selscan::M2ConvArgs& a, int in_bf16) {
