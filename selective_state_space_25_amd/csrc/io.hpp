@@ -76,7 +76,6 @@ template <typename T, int V> struct Piece {
         }
     }
     __device__ __forceinline__ void put(T* p) const { reinterpret_cast<Loose*>(p)->v = v; }
-    __device__ __forceinline__ void first(T x) { v[0] = x; }
 };
 template <typename T> struct Piece<T, 1> {
     T v;
@@ -85,7 +84,6 @@ template <typename T> struct Piece<T, 1> {
     __device__ __forceinline__ void widen(float* f) const { f[0] = ld(&v); }
     __device__ __forceinline__ void narrow(const float* f) { st(&v, f[0]); }
     __device__ __forceinline__ void put(T* p) const { *p = v; }
-    __device__ __forceinline__ void first(T x) { v = x; }
 };
 
 // Workgroups 0 .. n - 1 over two dimensions (a dimension holds fewer than
