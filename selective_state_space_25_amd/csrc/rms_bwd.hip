@@ -27,6 +27,16 @@ using namespace rms;
 
 constexpr int kBlocks = 512;
 
+// Groups of up to 2560 elements stay in one wave: three or four streams of
+// loads a group are enough without a barrier.  us, one wave / four, 84
+// million elements in bf16:
+//                          1280         2048         2560
+//   with fp32 residual   265 / 272    251 / 282    253 / 336
+//   with a gate          210 / 252    253 / 248    230 / 292
+// (past that a wave's registers do not hold a group and its sums: 5120 over four
+// waves 272 and 216.)
+constexpr int kWavePieces = 320;
+
 // One group of one row.  GATE: res is x, in Tin.
 template <typename Tin, typename Tres, typename Tout, bool GATE>
 struct Row {
@@ -215,8 +225,8 @@ struct Bwd {
 
 template <typename Tin, typename Tres, typename Tout, bool GATE>
 hipError_t bwd(const RmsArgs& a, hipStream_t stream) {
-    const Layout l(a.width, false);
-    if (l.pieces) return by_layout(l, Bwd<Tin, Tres, Tout, GATE>{a, stream});
+    const Layout l(a.width, kWavePieces);
+    if (l.pieces) return by_layout<5, 5>(l, Bwd<Tin, Tres, Tout, GATE>{a, stream});
     if (a.y || a.res_out || a.dgate) {
         KTime kt("rms_bwd", stream);
         hipLaunchKernelGGL((rms_bwd_long_kernel<Tin, Tres, Tout, GATE>), io::groups(a.rows * a.groups), dim3(kT), 0, stream, a);
@@ -242,14 +252,14 @@ hipError_t by_out(const RmsArgs& a, int out_bf16, hipStream_t st) {
 // Workgroups to a group of columns, each with a partial row of dweight: two a
 // compute unit, and 64 rows each in fp32 at most; no more than have rows.
 int rms_bwd_blocks(int64_t rows, int64_t width) {
-    const Layout l(width, false);
+    const Layout l(width, kWavePieces);
     const int64_t once = l.at_once();
     const int64_t n = l.pieces ? std::max((int64_t)kBlocks, std::min((rows + 64 * once - 1) / (64 * once), (int64_t)1 << 23))
                                : std::max((int64_t)64, std::min((rows + 63) / 64, (int64_t)65535));
     return (int)std::min(n, (rows + once - 1) / once);
 }
 
-bool rms_reads_again(int64_t width) { return !Layout(width, false).pieces; }
+bool rms_reads_again(int64_t width) { return !Layout(width, kWavePieces).pieces; }
 
 size_t rms_bwd_part_bytes(int64_t rows, int64_t dim, int64_t groups) {
     return (size_t)column_sums_rows(rms_bwd_blocks(rows, dim / groups)) * (size_t)dim * 4;

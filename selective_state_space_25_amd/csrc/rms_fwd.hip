@@ -4,13 +4,13 @@
 //
 // over the groups of a row (one group: the row), y in fp32, bf16 or, with a
 // scale for each block of a group, e4m3: scale = max(max |y| / 448, 2^-126), the
-// fp32 quotient y / scale rounded to nearest even.  A stream bound by memory: a group stays in
-// registers between its sum and its output, in 8-element pieces over 8 to 64
-// lanes of a wave (up to 2560 elements, sums without a barrier) or the 256 of
-// a workgroup (to 8192), so every element is read once and written once; the
-// 8-bit form costs a shuffle of a block's lanes and no second pass.  Narrow
-// groups share a wave.  Rows may start at any element's address and end inside
-// a piece.  Longer groups are read again for each step.
+// fp32 quotient y / scale rounded to nearest even.  A stream bound by memory: a
+// group stays in registers between its sum and its output, in 8-element pieces
+// over 8 to 64 lanes of a wave (up to 1024 to 1536 elements, sums without a
+// barrier) or the 256 of a workgroup (to 8192), so every element is read once
+// and written once; the 8-bit form costs a shuffle of a block's lanes and no
+// second pass.  Narrow groups share a wave.  Rows may start at any element's
+// address and end inside a piece.  Longer groups are read again for each step.
 //
 // 32768 x 2560, bf16 with an fp32 residual: 183 us for 1.01 GB, 5.5 TB/s.
 // 16384 x 5120 with a gate, e4m3 in blocks of 128: 100 us for 0.42 GB, 4.2 TB/s,
@@ -254,10 +254,28 @@ struct Fwd {
     }
 };
 
+// Pieces of a group that stay in one wave: fewer where an element moves more
+// bytes.  us, one wave / four, 2^26 elements (bf16 unless it says fp32):
+//   bytes              1088         1280         1536         1664         2048         2560
+//   4  x, y           54 /  81     50 /  70     48 /  60     52 /  59     51 /  51     51 /  54
+//   5  gate, e4m3     96 / 132     86 / 115     75 /  95     93 /  94     80 /  78     90 /  91
+//   6  gate           82 / 111     78 /  98     77 /  85     83 /  84     84 /  74     84 /  82
+//   6  fp32 x         71 /  84     71 /  77     71 /  71     73 /  71     72 /  68     74 /  70
+//   8  residual, s   103 / 119    103 / 105    104 /  96    110 /  95    108 /  92    109 /  98
+//   8  fp32 x, y     101 / 101    103 / 101    102 /  97    104 /  98    105 /  94    107 /  98
+//   8  gate, fp32 y  111 / 125    111 / 113    110 / 106    117 / 106    116 / 100    118 / 109
+//   12 fp32 residual 155 / 145    159 / 147    158 / 143    164 / 143    167 / 140    167 / 147
+//   12 gate, fp32    146 / 142    149 / 143    150 / 139    152 / 140    152 / 138    157 / 142
+template <typename Tin, typename Tres, typename Tout>
+int wave_pieces(const RmsArgs& a) {
+    const int bytes = (int)sizeof(Tin) * (a.gate ? 2 : 1) + (int)sizeof(Tres) * ((a.res ? 1 : 0) + (a.res_out ? 1 : 0)) + (int)sizeof(Tout);
+    return bytes > 8 ? 128 : bytes == 8 ? 160 : 192;
+}
+
 template <typename Tin, typename Tres, typename Tout>
 hipError_t fwd(const RmsArgs& a, hipStream_t stream) {
-    const Layout l(a.width, true);
-    if (l.pieces) return by_layout(l, Fwd<Tin, Tres, Tout>{a, stream});
+    const Layout l(a.width, wave_pieces<Tin, Tres, Tout>(a));
+    if (l.pieces) return by_layout<3, 3>(l, Fwd<Tin, Tres, Tout>{a, stream});
     KTime kt("rms_fwd", stream);
     hipLaunchKernelGGL((rms_fwd_long_kernel<Tin, Tres, Tout>), io::groups(a.rows * a.groups), dim3(kT), 0, stream, a);
     return hipGetLastError();

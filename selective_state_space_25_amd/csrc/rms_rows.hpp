@@ -76,35 +76,38 @@ __device__ __forceinline__ float row_sum(float v, float* sm) {
 
 __device__ __forceinline__ float sigmoid(float z) { return fast_rcp(1.0f + fast_exp2(-z * kLog2e)); }
 
-// Lanes a group takes and pieces a lane (0: the group is too long).  Past 1024
-// elements the forward spreads a group over four waves, for more loads in
-// flight a group (32768 x 2560: 183 us, in one wave 206); the gradients stay in
-// one wave up to 2560, without barriers, with three streams of loads a group
-// (255 us, over four waves 337).
+// Lanes a group takes and pieces a lane (0: the group is too long).  A group of
+// up to `wave` pieces stays in one wave, a longer one takes the four of a
+// workgroup: more loads in flight a group, but barriers, and idle lanes where
+// its pieces are not a multiple of 256 by far.
 struct Layout {
     int lanes, pieces;
-    Layout(int64_t width, bool fwd) {
+    Layout(int64_t width, int wave) {
         const int64_t np = (width + 7) / 8;
-        lanes = np <= 8 ? 8 : np <= 16 ? 16 : np <= 32 ? 32 : np <= (fwd ? 128 : 320) ? 64 : 256;
+        lanes = np <= 8 ? 8 : np <= 16 ? 16 : np <= 32 ? 32 : np <= wave ? 64 : 256;
         pieces = width > kLongest ? 0 : (int)((np + lanes - 1) / lanes);
     }
     int at_once() const { return pieces ? kT / lanes : 1; }   // groups a workgroup has at a time
 };
 
-// f.template operator()<LR, NV>() of the layout.
-template <typename F>
+// f.template run<LR, NV>() of the layout, whose `wave` lies between 64 (LEAST -
+// 1) and 64 MOST pieces.
+template <int LEAST, int MOST, typename F>
 hipError_t by_layout(const Layout& l, F f) {
     if (l.lanes == 8) return f.template run<8, 1>();
     if (l.lanes == 16) return f.template run<16, 1>();
     if (l.lanes == 32) return f.template run<32, 1>();
-    if (l.lanes == 256) return l.pieces == 1 ? f.template run<256, 1>() : l.pieces == 2 ? f.template run<256, 2>() : l.pieces == 3 ? f.template run<256, 3>() : f.template run<256, 4>();
-    switch (l.pieces) {
-        case 1: return f.template run<64, 1>();
-        case 2: return f.template run<64, 2>();
-        case 3: return f.template run<64, 3>();
-        case 4: return f.template run<64, 4>();
-        default: return f.template run<64, 5>();
+    if (l.lanes == 256) {
+        if constexpr (LEAST <= 4) {
+            if (l.pieces == 1) return f.template run<256, 1>();
+        }
+        return l.pieces == 2 ? f.template run<256, 2>() : l.pieces == 3 ? f.template run<256, 3>() : f.template run<256, 4>();
     }
+    if constexpr (MOST >= 4) {
+        if (l.pieces == 4) return f.template run<64, 4>();
+        if (l.pieces == 5) return f.template run<64, 5>();
+    }
+    return l.pieces == 1 ? f.template run<64, 1>() : l.pieces == 2 ? f.template run<64, 2>() : f.template run<64, 3>();
 }
 
 }  // namespace rms
