@@ -32,12 +32,14 @@
 // the device cuts the segments (m2_chunk.hpp), since the host does not know the
 // lengths.
 //
-// 1 x 16384, 32 heads of 64 x 128 in one group, bf16: 128 us, and 71 for the
-// state pass and 17 for the carry between them.  Six MFMAs a product make this
-// 0.17 TFLOP, 126 us of a library product's rate (1378 TFLOP/s), the state pass
-// a fifth of it; the matrix cores are busy 40 %, the vector ALU (convolution,
-// splits, decays) 47 %, and a compute unit's one workgroup, two waves a SIMD,
-// overlaps them as far as its two barriers a chunk let it.
+// 1 x 16384, 32 heads of 64 x 128 in one group, bf16, of a call of 220 us: 117
+// us, 65 for the state pass, 17 for the carry between them and 21 for B and C
+// (y in fp32: 120 of 225; fp32 inputs, one column block a wave: 138 of 242).
+// Six MFMAs a product make this 0.17 TFLOP, 126 us of a library product's rate
+// (1378 TFLOP/s), the state pass a fifth of it; the scan's matrix cores are busy
+// 41 %, the vector ALU (convolution, splits, decays) 48 %, and a compute unit's
+// one workgroup, two waves a SIMD, overlaps them as far as its two barriers a
+// chunk let it.
 //
 // Products are fp32-grade (split_mfma.hpp).  cum is summed in fp64, and its
 // exponentials take it as two fp32 parts: after strong decays it is large, and
@@ -622,20 +624,20 @@ Plan plan_of(const M2ConvArgs& a, int in_bf16, bool ragged) {
     const int64_t heads = a.H / a.G;
     // two column blocks a wave halve the reads of B and C from LDS; one where
     // a group would not fill a workgroup's waves, pairs of columns P, or (fp32,
-    // N = 128) two blocks a wave's registers (1 x 16384 as above: 222 us a call
-    // with two, 235 with one)
+    // N = 128) two blocks a wave's registers (1 x 16384 as above: 219 us a call
+    // with two, 234 with one; 8 x 4096 ragged 268 and 309)
     p.ct = a.P % 2 || heads * ((a.P + 31) / 32) < kWaves || (!in_bf16 && p.np == 128) ? 1 : 2;
     p.cols = (int)((a.P + 16 * p.ct - 1) / (16 * p.ct));
     p.units = (int)(heads * p.cols);
     p.sets = (p.units + kWaves - 1) / kWaves;
     p.waves = (p.units + p.sets - 1) / p.sets;
     // Segments of two chunks and more: a workgroup for each compute unit, which
-    // holds one (batch 1, L 16384, 32 heads of 64 x 128: 241 us, with two
-    // workgroups a unit 269).  Where sequences may end early and the shortest
+    // holds one (batch 1, L 16384, 32 heads of 64 x 128: 219 us, with two
+    // workgroups a unit 247; 8 x 4096: 379 and 411).  Where sequences may end early and the shortest
     // segments would be more than that, the device cuts them from the tokens
     // that are there, four a sequence at least, in whole rounds of workgroups
-    // (batch 8, lengths spread over 0 .. 4096: 269 us; segments of one length,
-    // four workgroups a unit, took 349 where the cut took 275).  Its cut costs 0.5 us a launch (batch 3 of
+    // (batch 8, lengths spread over 0 .. 4096: 268 us; segments of one length,
+    // four workgroups a unit, 337).  Its cut costs 0.5 us a launch (batch 3 of
     // up to 333 tokens: 38 us, without 35), and a lane a sequence does no more
     // than 64: those have one length, and four workgroups a unit.
     const int64_t cus = host::device_cus(), groups = a.batch * a.G * p.sets;

@@ -13,8 +13,8 @@
 // bits.  The convolution's state is only read here: the workgroups of a group
 // share the channels of B and C, so a kernel behind this one moves it on.
 //
-// 32 heads of 64 x 128, bf16: batch 128 57 us for 0.27 GB of state read and
-// written, 4.8 TB/s, with the launch behind it 59.6; one sequence 4.5 and 1.9
+// 32 heads of 64 x 128, bf16: batch 128 56 us for 0.27 GB of state read and
+// written, 4.8 TB/s, with the launch behind it 59.5; one sequence 4.4 and 2.1
 // us, below what the two launches take the host (7.5).
 #include "io.hpp"
 #include "kernels.hpp"

@@ -11,7 +11,7 @@
 //
 // 1 x 16384, one group, N = 128: 21 us, 28 MB of records written.  A workgroup
 // a chunk is 256 of them, one a compute unit: its chain of loads, convolution,
-// splits and products is what takes the time (waves wait 54 % of it).
+// splits and products is what takes the time (waves wait 57 % of it).
 #include "m2_chunk.hpp"
 
 namespace selscan {

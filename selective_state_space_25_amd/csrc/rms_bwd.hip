@@ -13,8 +13,10 @@
 // where there are more rows), one partial row a workgroup, which
 // column_sums.hip adds in fp64: a fixed order.
 //
-// 32768 x 2560, bf16 with an fp32 residual: 251 us for 1.34 GB, 5.3 TB/s, and
-// 5 us for the partial rows.
+// 32768 x 2560, bf16 with an fp32 residual: 249 us for 1.34 GB, 5.4 TB/s, and
+// 5 us for the partial rows.  With a gate 225 us there and 211 at 16384 x 5120
+// for 0.84 GB, 3.7 and 4.0 TB/s: waves wait half their time and more for loads,
+// with fewer of them on a compute unit (registers).
 #include <algorithm>
 
 #include "rms_rows.hpp"

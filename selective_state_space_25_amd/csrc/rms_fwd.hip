@@ -12,10 +12,10 @@
 // second pass.  Narrow groups share a wave.  Rows may start at any element's
 // address and end inside a piece.  Longer groups are read again for each step.
 //
-// 32768 x 2560, bf16 with an fp32 residual: 183 us for 1.01 GB, 5.5 TB/s.
-// 16384 x 5120 with a gate, e4m3 in blocks of 128: 100 us for 0.42 GB, 4.2 TB/s,
-// vector ALU 74 % busy (silu, the blocks' maxima, conversions).  One row of 768
-// is the launch: 2.9 us.
+// 32768 x 2560, bf16 with an fp32 residual: 182 us for 1.01 GB, 5.5 TB/s.
+// 16384 x 5120 with a gate, e4m3 in blocks of 128: 102 us for 0.42 GB, 4.1 TB/s,
+// vector ALU 80 % busy (silu, the blocks' maxima, quotients, conversions).  One
+// row of 768 is the launch: 2.8 us.
 #include "rms_rows.hpp"
 
 namespace selscan {

@@ -17,10 +17,11 @@
 // run, the workgroup's runs added up through LDS, one partial row a workgroup,
 // and those in fp64 by column_sums.hip in a fixed order.
 //
-// 8 x 4096 x 2304, width 4, split in three, bf16: 66 us for 0.30 GB, 4.6 TB/s;
-// gradients with dout in fp32 140 us for 0.60 GB, 4.3 TB/s (vector ALU 73 %
-// busy: the activation and its slope again, 2 K multiplications an element).
-// One token is a launch: 1.9 us at 1 x 2304, 5.5 at 128 x 2304.
+// 8 x 4096 x 2304, width 4, split in three, bf16: 61 us for 0.30 GB, 5.0 TB/s
+// (fp32 123 for 0.60); gradients with dout in fp32 137 us for 0.60 GB, 4.4 TB/s
+// (vector ALU 73 % busy: the activation and its slope again, 2 K multiplications
+// an element; x in fp32 183 for 0.91).  One token is a launch: 2.1 us at 1 x
+// 2304, 5.1 at 128 x 2304.
 #include "io.hpp"
 #include "kernels.hpp"
 
@@ -333,9 +334,10 @@ hipError_t launch_v(const ShortConvArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
-// Channels a thread has at a time: whole pieces of the split only.  Twice as
-// many take 73 us at the sizes above (fewer waves to hide loads behind), and
-// 150 for the gradients.
+// Channels a thread has at a time: whole pieces of the split only, one where
+// those are not (2303 channels in bf16: 96 us where 2304 take 60, gradients 185
+// and 139).  Twice as many take 73 us at the sizes above (fewer waves to hide
+// loads behind), and 150 for the gradients.
 constexpr int kFwdV = 4, kBwdV = 2;
 
 template <Form F, typename Tin, typename Tout, int K>
