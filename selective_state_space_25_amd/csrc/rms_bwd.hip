@@ -35,8 +35,8 @@ constexpr int kBlocks = 512;
 //                          1280         2048         2560
 //   with fp32 residual   265 / 272    251 / 282    253 / 336
 //   with a gate          210 / 252    253 / 248    230 / 292
-// (past that a wave's registers do not hold a group and its sums: 5120 over four
-// waves 272 and 216.)
+// Longer ones take four: 333 and 301 just past it (2568, a third of the lanes
+// idle), 254 and 221 at 4096, 246 and 268 at 8192.
 constexpr int kWavePieces = 320;
 
 // One group of one row.  GATE: res is x, in Tin.
