@@ -255,7 +255,8 @@ struct Fwd {
 };
 
 // Pieces of a group that stay in one wave: fewer where an element moves more
-// bytes.  us, one wave / four, 2^26 elements (bf16 unless it says fp32):
+// bytes (a residual counts with its s, asked for or not: y has the same bits).
+// us, one wave / four, 2^26 elements (bf16 unless it says fp32):
 //   bytes              1088         1280         1536         1664         2048         2560
 //   4  x, y           54 /  81     50 /  70     48 /  60     52 /  59     51 /  51     51 /  54
 //   5  gate, e4m3     96 / 132     86 / 115     75 /  95     93 /  94     80 /  78     90 /  91
@@ -268,7 +269,7 @@ struct Fwd {
 //   12 gate, fp32    146 / 142    149 / 143    150 / 139    152 / 140    152 / 138    157 / 142
 template <typename Tin, typename Tres, typename Tout>
 int wave_pieces(const RmsArgs& a) {
-    const int bytes = (int)sizeof(Tin) * (a.gate ? 2 : 1) + (int)sizeof(Tres) * ((a.res ? 1 : 0) + (a.res_out ? 1 : 0)) + (int)sizeof(Tout);
+    const int bytes = (int)sizeof(Tin) * (a.gate ? 2 : 1) + (int)sizeof(Tres) * (a.res ? 2 : 0) + (int)sizeof(Tout);
     return bytes > 8 ? 128 : bytes == 8 ? 160 : 192;
 }
 

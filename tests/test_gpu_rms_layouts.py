@@ -1,6 +1,8 @@
 """RMS norm at the widths where a group goes over from one wave to the four of a
 workgroup: 1024, 1280 or 1536 elements by the bytes that an element moves, 2560
 for the gradients.  Bounds as for other widths: 48 and 128 roundings."""
+import ctypes
+
 import pytest
 import torch
 
@@ -53,3 +55,21 @@ def test_gradients(gpu, width, gated):
     ref, mag = ops.rms_bwd(dy, s, w, rstd, z)
     for k in g:
         close(g[k], ref[k], mag[k], 128, k)
+
+
+@pytest.mark.parametrize("width", [1032, 1200, 1280, 1400, 2560])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_the_same_bits_with_and_without_s(gpu, width, dtype):
+    """Whether s is asked for does not change y: over x (s in memory of its own) and without it."""
+    gen = torch.Generator().manual_seed(width)
+    x, r, w = rnd(gen, 40, width, dtype=dtype), rnd(gen, 40, width, dtype=dtype), rnd(gen, width)
+    xx = x.clone()
+    y = ss.rms_norm_fwd(x, w)[0]
+    assert torch.equal(ss.rms_norm_fwd(xx, w, out=xx)[0], y)
+    want, got = ss.rms_norm_fwd(x, w, r)[0], torch.empty_like(x)
+    code = ss.F32 if dtype is F32 else ss.BF16
+    sh = ss.RmsShape(40, width, 1, 0, 0, code, code, code, 1e-5, None, 0)
+    assert ss.lib().selscan_rms_norm_fwd(ctypes.byref(sh), x.data_ptr(), r.data_ptr(), None, w.data_ptr(), got.data_ptr(), None, None,
+                                         None, torch.cuda.current_stream().cuda_stream) == ss.OK
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
