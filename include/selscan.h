@@ -545,7 +545,7 @@ selscan_status_t selscan_layer_norm_bwd(const selscan_norm_shape_t* shape, const
  *                                       sequence, of `state` and x (written;
  *                                       NULL = skip); may not alias state
  * Sums and the activation are fp32.  Outputs must not overlap inputs or each
- * other.  No workspace (the field is the gradients').
+ * other (INVALID_ARG).  No workspace (the field is the gradients').
  */
 typedef struct {
     int64_t batch, seqlen, dim, width;
@@ -574,9 +574,9 @@ size_t selscan_short_conv_bwd_workspace_bytes(const selscan_short_conv_shape_t* 
  *   dweight              [D, K]            fp32        (written; NULL = skip)
  *   dbias                [D]               fp32        (written; NULL = skip)
  *   dstate               [B, K-1, D]       in_dtype    (written; NULL = skip)
- * Gradients must not alias inputs or each other.  Sums run in a fixed order:
- * results are reproducible bit for bit.  Workspace as for the other entry
- * points; none where dweight and dbias are NULL.
+ * Gradients must not overlap inputs or each other (INVALID_ARG).  Sums run in a
+ * fixed order: results are reproducible bit for bit.  Workspace as for the other
+ * entry points; none where dweight and dbias are NULL.
  */
 selscan_status_t selscan_short_conv_bwd(const selscan_short_conv_shape_t* shape, const void* x, const float* weight,
                                         const float* bias, int silu, const int32_t* lengths, const void* state,
@@ -622,7 +622,7 @@ selscan_status_t selscan_short_conv_step(const selscan_short_conv_shape_t* shape
  *   last_conv_state                  in_dtype   as conv_state (written; NULL =
  *                                               skip); may not alias it
  *
- * Outputs must not overlap inputs or each other.
+ * Outputs must not overlap inputs or each other (INVALID_ARG).
  * N in {16, 32, 64, 128}.  State, decays and sums are fp32, and so are products
  * in effect.  The sequence is worked on in chunks of 64 tokens (up to 32 tokens
  * one by one, fewer where the heads fill the GPU, 7 at least): a NaN or infinity in a token

@@ -10,6 +10,7 @@
 #include <initializer_list>
 #include <mutex>
 #include <string>
+#include <utility>
 
 #include "kernels.hpp"
 #include "selscan.h"
@@ -66,6 +67,24 @@ inline bool overlap(const void* p, int64_t n, const void* q, int64_t m, int64_t 
         r = (a - b - (uint64_t)m) / (uint64_t)stride + 1;
     }
     return r < (uint64_t)rows && b + r * (uint64_t)stride < a + (uint64_t)n;
+}
+
+// The same with `batches` such sets of rows, `b_stride` bytes apart, in either
+// order of the two strides; where rows run into each other, anything from the
+// first to the last byte counts.
+inline bool overlap(const void* p, int64_t n, const void* q, int64_t m, int64_t rows, int64_t stride, int64_t batches, int64_t b_stride) {
+    if (b_stride < (rows - 1) * stride + m) {
+        std::swap(rows, batches);
+        std::swap(stride, b_stride);
+    }
+    const int64_t set = (rows - 1) * stride + m;
+    if (b_stride < set) return overlap(p, n, q, (batches - 1) * b_stride + set);
+    const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    const uint64_t first = b + (uint64_t)set <= a ? (a - b - (uint64_t)set) / (uint64_t)b_stride + 1 : 0;   // the set that ends behind p
+    if (first >= (uint64_t)batches) return false;
+    const char* at = static_cast<const char*>(q) + first * (uint64_t)b_stride;
+    return overlap(p, n, at, m, rows, stride) ||
+           (first + 1 < (uint64_t)batches && b + (first + 1) * (uint64_t)b_stride < a + (uint64_t)n);
 }
 
 // The current device must be a gfx950.  The architecture check runs once per

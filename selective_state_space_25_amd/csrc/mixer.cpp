@@ -78,6 +78,29 @@ selscan_status_t check_conv(const selscan_short_conv_shape_t* s, Use use) {
     return SELSCAN_OK;
 }
 
+// Dense tensors by their bytes (p NULL: none), of which an output must overlap
+// neither another nor an input.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+bool apart(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        if (!o->p) continue;
+        for (const Span* i = o + 1; i != outs.end(); ++i)
+            if (i->p && overlap(o->p, o->bytes, i->p, i->bytes)) return false;
+        for (const Span& i : ins)
+            if (i.p && overlap(o->p, o->bytes, i.p, i.bytes)) return false;
+    }
+    return true;
+}
+// The outputs and rows that a projection left, [batch, rows] of them.
+bool apart(std::initializer_list<Span> outs, const void* q, int64_t bytes, int64_t rows, int64_t stride, int64_t batch, int64_t b_stride) {
+    for (const Span& o : outs)
+        if (o.p && overlap(o.p, o.bytes, q, bytes, rows, stride, batch, b_stride)) return false;
+    return true;
+}
+
 size_t conv_part_bytes(const selscan::ShortConvArgs& a) {
     return align256((size_t)selscan::column_sums_rows(a.batch * a.run_blocks) * (size_t)((a.K + 1) * a.C) * 4);
 }
@@ -176,8 +199,12 @@ selscan_status_t selscan_short_conv_fwd(const selscan_short_conv_shape_t* s, con
         if (!x || !weight || !y0 || (s->split[1] && !y1) || (s->split[2] && !y2))
             return set_error(SELSCAN_ERR_INVALID_ARG, "x, weight and the outputs of split must be non-NULL");
         if (silu != 0 && silu != 1) return set_error(SELSCAN_ERR_INVALID_ARG, "silu must be 0 or 1");
-        if (state && state == last_state) return set_error(SELSCAN_ERR_INVALID_ARG, "state and last_state must not alias");
-        if (x == y0 || x == y1 || x == y2) return set_error(SELSCAN_ERR_INVALID_ARG, "the outputs must not alias x");
+        const int64_t es = bytes_of(s->in_dtype), n = s->batch * s->seqlen * bytes_of(s->out_dtype);
+        const int64_t ns = s->batch * (s->width - 1) * s->dim * es;
+        const std::initializer_list<Span> outs = {{y0, n * s->split[0]}, {s->split[1] ? y1 : nullptr, n * s->split[1]},
+                                                  {s->split[2] ? y2 : nullptr, n * s->split[2]}, {last_state, ns}};
+        if (!apart(outs, {{state, ns}}) || !apart(outs, x, s->dim * es, s->seqlen, s->x_row * es, s->batch, s->x_batch * es))
+            return set_error(SELSCAN_ERR_INVALID_ARG, "the outputs and last_state must not alias x, state or each other");
         st = device_check();
         if (st != SELSCAN_OK) return st;
         selscan::ShortConvArgs a{};
@@ -207,9 +234,14 @@ selscan_status_t selscan_short_conv_bwd(const selscan_short_conv_shape_t* s, con
         if (st != SELSCAN_OK) return st;
         if (!x || !weight || !dx || !dout0 || (s->split[1] && !dout1) || (s->split[2] && !dout2))
             return set_error(SELSCAN_ERR_INVALID_ARG, "x, weight, dx and the gradients of split must be non-NULL");
-        if (dx == x || dx == dout0 || dx == dout1 || dx == dout2)
-            return set_error(SELSCAN_ERR_INVALID_ARG, "dx must not alias x or the gradients of split");
         if (silu != 0 && silu != 1) return set_error(SELSCAN_ERR_INVALID_ARG, "silu must be 0 or 1");
+        const int64_t es = bytes_of(s->in_dtype), n = s->batch * s->seqlen, ny = n * bytes_of(s->out_dtype);
+        const int64_t ns = s->batch * (s->width - 1) * s->dim * es;
+        const std::initializer_list<Span> outs = {{dx, n * s->dim * es}, {dweight, s->dim * s->width * 4}, {dbias, s->dim * 4}, {dstate, ns}};
+        if (!apart(outs, {{dout0, ny * s->split[0]}, {s->split[1] ? dout1 : nullptr, ny * s->split[1]},
+                          {s->split[2] ? dout2 : nullptr, ny * s->split[2]}, {state, ns}, {dlast_state, ns}}) ||
+            !apart(outs, x, s->dim * es, s->seqlen, s->x_row * es, s->batch, s->x_batch * es))
+            return set_error(SELSCAN_ERR_INVALID_ARG, "gradients must not alias inputs or each other");
         st = device_check();
         if (st != SELSCAN_OK) return st;
         hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
@@ -274,10 +306,13 @@ selscan_status_t selscan_mamba2_conv_fwd(const selscan_m2_conv_shape_t* s, const
         if (st != SELSCAN_OK) return st;
         if (!xbc || !dt || !conv_weight || !A || !y)
             return set_error(SELSCAN_ERR_INVALID_ARG, "xbc, dt, conv_weight, A and y must be non-NULL");
-        if (h0 && h0 == last_state) return set_error(SELSCAN_ERR_INVALID_ARG, "h0 and last_state must not alias");
-        if (conv_state && conv_state == last_conv_state)
-            return set_error(SELSCAN_ERR_INVALID_ARG, "conv_state and last_conv_state must not alias");
-        if (y == xbc || y == dt) return set_error(SELSCAN_ERR_INVALID_ARG, "y must not alias xbc or dt");
+        const int64_t hp = s->nheads * s->headdim, C = hp + 2 * s->ngroups * s->dstate, es = bytes_of(s->in_dtype);
+        const int64_t ns = s->batch * hp * s->dstate * 4, nc = s->batch * (s->width - 1) * C * es;
+        const std::initializer_list<Span> outs = {{y, s->batch * s->seqlen * hp * bytes_of(s->out_dtype)}, {last_state, ns}, {last_conv_state, nc}};
+        if (!apart(outs, {{h0, ns}, {conv_state, nc}}) ||
+            !apart(outs, xbc, C * es, s->seqlen, s->xbc_row * es, s->batch, s->xbc_batch * es) ||
+            !apart(outs, dt, s->nheads * es, s->seqlen, s->dt_row * es, s->batch, s->dt_batch * es))
+            return set_error(SELSCAN_ERR_INVALID_ARG, "y, last_state and last_conv_state must not alias inputs or each other");
         st = device_check();
         if (st != SELSCAN_OK) return st;
         hipStream_t hs = reinterpret_cast<hipStream_t>(stream);
